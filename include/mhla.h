@@ -123,7 +123,8 @@ mhla_status mhla_forward_causal(const void* q, const void* k, const void* v, con
 typedef enum {
   MHLA_PHI_ELU1 = 0, /* phi(x) = ELU(x) + 1 (the default everywhere)   [LA §二] */
   MHLA_PHI_RELU = 1, /* phi(x) = max(x, 0)                              [LA §二] */
-  MHLA_PHI_EXP = 2   /* phi(x) = exp(x)                                 [LA §二] */
+  MHLA_PHI_EXP = 2,  /* phi(x) = exp(x)                                 [LA §二] */
+  MHLA_PHI_IDENTITY = 3 /* phi(x) = x: the retention_* entries only     [LA §七] */
 } mhla_feature;
 
 typedef struct {
@@ -288,6 +289,101 @@ mhla_status mhla_backward(const void* q, const void* k, const void* v, const flo
  * MHLA_PATH_TCGEN05 for the tensor-core token passes, MHLA_PATH_SIMT
  * otherwise, MHLA_PATH_NONE for invalid or unsupported sizes. */
 mhla_path mhla_backward_path(int B, int H, int N, int d, int block_size, mhla_dtype dt);
+
+/* ---------------------------------------------------------------- retention
+ * Linear attention with a decay for each head ([LA] §七, RetNet):
+ *   S_t = gamma_h S_{t-1} + phi(k_t) v_t^T,   y_t = scale * phi(q_t) S_t
+ * (update, then read, as everywhere in this library; no normaliser and no eps).
+ * Prompts and training run in chunks, single tokens recurrently; the state S
+ * [d][d] fp32 (S[c][e] = sum gamma^(t-s) phi(k_s)_c v_se) carries a sequence
+ * from one call to the next.
+ *
+ * Conventions of the retention_* entries:
+ *   - Token tensors are [B, H, N, d] with any strides: an mhla_strides holds
+ *     the element strides of b, h and n (d contiguous); NULL means dense
+ *     row-major.  Strides are >= 0 and, like the pointers, multiples of 16
+ *     bytes; an input may have stride 0 (a head shared by several), an output
+ *     may not overlap itself.  So token-major tensors and slices of a fused
+ *     projection are taken as they are.
+ *   - cu_seqlens: NULL, or device int32 [B + 1]: then the tensors are
+ *     [1, H, N, d] (the b strides are not used) and sequence i is the rows
+ *     cu_seqlens[i] .. cu_seqlens[i + 1] - 1, of any lengths, empty ones among
+ *     them.  Rows of no sequence are not written.  The offsets are not
+ *     inspected by the host: non-decreasing values in [0, N] are the caller's
+ *     contract, anything else is clamped to it and touches no other memory.
+ *   - gamma: device fp32 [H], each in [0, 1] (the caller's contract).
+ *   - states: [n_slots, H, d, d] fp32.  slots: device int32 [B], the slot of
+ *     each sequence or row, or NULL (sequence i uses slot i).  A sequence whose
+ *     slot is outside [0, n_slots), or is the slot of a sequence before it, has
+ *     none: see the entries.
+ *   - Not-a-number or infinite values of a token reach its own sequence only;
+ *     in retention_forward and retention_backward they may reach all 128
+ *     tokens of the chunk that they are in, also those before them. */
+
+/* Element strides of a [B, H, N, d] tensor. */
+typedef struct {
+  long long b, h, n;
+} mhla_strides;
+
+typedef struct {
+  int feature; /* an mhla_feature, applied to q and k (default MHLA_PHI_IDENTITY) */
+  float scale; /* finite (default 1) */
+} retention_options;
+
+/* Workspace bytes of retention_forward (backward = 0) or retention_backward
+ * (backward = 1) for B sequences of `tokens` tokens in all (dense: B N); 0 if
+ * the sizes are invalid.  Valid for both dtypes, dense and packed. */
+size_t retention_workspace_bytes(int B, int H, int tokens, int d, int backward);
+
+/* The outputs of whole prompts.
+ *   q, k, v : inputs;  y : output, overlapping no input
+ *   states  : NULL, or read (load_state = 1: a sequence starts from its slot's
+ *             state; 0: from zero) and written (the state after its last token).
+ *             A sequence without a slot starts from zero and its state is not
+ *             kept; one without tokens leaves its slot as it is.
+ *   opt     : NULL = the defaults
+ *   B*H*N = 0 returns MHLA_OK without a launch. */
+mhla_status retention_forward(const void* q, const mhla_strides* q_strides, const void* k,
+                              const mhla_strides* k_strides, const void* v, const mhla_strides* v_strides,
+                              const float* gamma, void* y, const mhla_strides* y_strides, int B, int H, int N, int d,
+                              const int* cu_seqlens, float* states, const int* slots, int n_slots, int load_state,
+                              mhla_dtype dt, const retention_options* opt, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* The gradients of q, k and v of retention_forward without states, for training:
+ *   G_t = gamma_h G_{t+1} + scale phi(q_t) dy_t^T
+ *   dq_t = phi'(q_t) * (scale S_t dy_t),  dk_t = phi'(k_t) * (G_t v_t),  dv_t = G_t^T phi(k_t)
+ * with phi' = 1 (identity), phi'(x) = 1 for x > 0 and exp(x) otherwise (ELU + 1),
+ * 1 for x > 0 and 0 otherwise (ReLU), exp(x) (exp).  gamma is a constant.
+ *   dy : input, dL/dY;  dq, dk, dv : outputs, written (not accumulated), of the
+ *   full shape also where an input is shared by stride 0; overlapping neither
+ *   an input nor each other.  Deterministic: every sum has a fixed order. */
+mhla_status retention_backward(const void* q, const mhla_strides* q_strides, const void* k,
+                               const mhla_strides* k_strides, const void* v, const mhla_strides* v_strides,
+                               const float* gamma, const void* dy, const mhla_strides* dy_strides, void* dq,
+                               const mhla_strides* dq_strides, void* dk, const mhla_strides* dk_strides, void* dv,
+                               const mhla_strides* dv_strides, int B, int H, int N, int d, const int* cu_seqlens,
+                               mhla_dtype dt, const retention_options* opt, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* One token for each of B rows: updates the rows' states and writes out.
+ *   q, k, v, out : [B, H, d]; of the strides b and h are used
+ *   A row without a slot is left out: neither its output nor a state is touched.
+ *   No workspace. */
+mhla_status retention_step(const void* q, const mhla_strides* q_strides, const void* k, const mhla_strides* k_strides,
+                           const void* v, const mhla_strides* v_strides, const float* gamma, float* states,
+                           const int* slots, int n_slots, void* out, const mhla_strides* out_strides, int B, int H,
+                           int d, mhla_dtype dt, const retention_options* opt, void* stream);
+
+/* states[dst[i]] = states[src[i]] for the n pairs, src[i] < 0: zeros.  Forks one
+ * state to many, moves states together, clears slots.  As if every source were
+ * read before any target is written, so slots may be sources and targets in
+ * any combination.  src, dst: device int32 [n], n <= 1024 (more:
+ * MHLA_ERR_UNSUPPORTED).  A pair whose src is >= n_slots or whose dst is outside
+ * [0, n_slots) does nothing; of several pairs with one target the last counts.
+ * No workspace. */
+mhla_status retention_copy_states(float* states, int n_slots, int H, int d, const int* src, const int* dst, int n,
+                                  void* stream);
 
 /* Workspace bytes for rala_forward; 0 if the sizes are invalid. */
 size_t rala_workspace_bytes(int B, int H, int N, int d, int cx);

@@ -30,5 +30,10 @@ from .binding import (  # noqa: F401
     new_workspace,
     rala_forward,
     rala_workspace_bytes,
+    retention_backward,
+    retention_copy_states,
+    retention_forward,
+    retention_step,
+    retention_workspace_bytes,
     status_string,
 )

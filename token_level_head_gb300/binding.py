@@ -47,6 +47,11 @@ _SIGNATURES = {
     "mhla_debug_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
     "mhla_backward_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "mhla_backward_path": (_i, [_i, _i, _i, _i, _i, _i]),
+    "retention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "retention_forward": (_i, [_vp] * 9 + [_i] * 4 + [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "retention_backward": (_i, [_vp] * 15 + [_i] * 4 + [_vp, _i, _vp, _vp, _sz, _vp]),
+    "retention_step": (_i, [_vp] * 9 + [_i, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
+    "retention_copy_states": (_i, [_vp, _i, _i, _i, _vp, _vp, _i, _vp]),
     "mhla_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
 }
 
@@ -362,6 +367,171 @@ def linattn_decode_steps(q, k, v, S, z, out, *, eps=1e-6, gamma=1.0, den_out=Non
                                          _stream(stream, dev))
     _check("linattn_decode_steps", st)
     return out
+
+
+class _Strides(ctypes.Structure):
+    """The C struct mhla_strides: element strides of b, h and n."""
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("n", ctypes.c_longlong)]
+
+
+class _RetentionOptions(ctypes.Structure):
+    """The C struct retention_options."""
+    _fields_ = [("feature", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+def _retention_options(feature, scale):
+    kinds = {**FEATURES, "identity": 3}
+    if feature not in kinds:
+        raise ValueError(f"feature: one of {sorted(kinds)}, got {feature!r}")
+    return ctypes.byref(_RetentionOptions(kinds[feature], float(scale)))
+
+
+def _strided(t, name):
+    """(pointer, strides) of a token tensor [B, H, N, d] or [B, H, d] with contiguous rows."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {t.stride(-1)}")
+    st = _Strides(t.stride(0), t.stride(1), t.stride(2) if t.dim() == 4 else 0)
+    return [_ptr(t), ctypes.byref(st)]
+
+
+def _retention_device(tokens, others):
+    """The one CUDA device of all tensors; ``others`` (not the token tensors) must be contiguous."""
+    q = tokens[0]
+    for t in tokens:
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if t.device != q.device:
+            raise ValueError(f"tensor on {t.device}, expected {q.device} (the device of q)")
+    others = [t for t in others if t is not None]
+    _need_cuda(*others)
+    for t in others:
+        if t.device != q.device:
+            raise ValueError(f"tensor on {t.device}, expected {q.device} (the device of q)")
+    return q.device
+
+
+def _retention_sizes(q, cu_seqlens):
+    """B (sequences), H, N (packed: all tokens), d of q [B, H, N, d]; packed: q [1, H, tokens, d]."""
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, H, N, d], got shape {tuple(q.shape)}")
+    B, H, N, d = q.shape
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError(f"q: expected [1, H, tokens, d] with cu_seqlens, got shape {tuple(q.shape)}")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError(f"cu_seqlens: expected [sequences + 1], got shape {tuple(cu_seqlens.shape)}")
+        _expect(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
+        B = cu_seqlens.numel() - 1
+    return B, H, N, d
+
+
+def _retention_states(states, slots, B, H, d):
+    if states is None:
+        if slots is not None:
+            raise ValueError("slots: given without states")
+        return 0
+    if states.dim() != 4:
+        raise ValueError(f"states: expected [slots, H, d, d], got shape {tuple(states.shape)}")
+    _expect(states, "states", (states.shape[0], H, d, d), torch.float32)
+    _expect(slots, "slots", (B,), torch.int32)
+    return states.shape[0]
+
+
+def retention_workspace_bytes(B: int, H: int, tokens: int, d: int, backward: bool = False) -> int:
+    return int(load().retention_workspace_bytes(B, H, tokens, d, 1 if backward else 0))
+
+
+def _retention_workspace(workspace, B, H, N, d, packed, backward, dev):
+    if workspace is None:
+        workspace = new_workspace(retention_workspace_bytes(B, H, N if packed else B * N, d, backward), dev)
+    return [_ptr(workspace), workspace.numel() * workspace.element_size()]
+
+
+def retention_forward(q, k, v, gamma, y, *, cu_seqlens=None, states=None, slots=None, load_state=False, scale=1.0,
+                      feature="identity", workspace=None, stream=None):
+    """Linear attention with a decay for each head, y_t = scale phi(q_t) S_t, S_t = gamma S_{t-1} +
+    phi(k_t) v_t^T, over whole prompts.  q/k/v/y [B, H, N, d] with any strides (rows contiguous),
+    gamma [H] fp32; packed sequences: q/k/v/y [1, H, tokens, d] and int32 ``cu_seqlens``
+    [sequences + 1].  ``states`` [slots, H, d, d] fp32 receives the final states (``slots``: the slot
+    of each sequence, int32); with ``load_state`` the sequences start from them."""
+    B, H, N, d = _retention_sizes(q, cu_seqlens)
+    for name, t in (("k", k), ("v", v), ("y", y)):
+        _expect(t, name, q.shape, q.dtype)
+    _expect(gamma, "gamma", (H,), torch.float32)
+    if load_state and states is None:
+        raise ValueError("load_state: needs states")
+    n_slots = _retention_states(states, slots, B, H, d)
+    opt = _retention_options(feature, scale)
+    dev = _retention_device([q, k, v, y], [gamma, cu_seqlens, states, slots, workspace])
+    with torch.cuda.device(dev):
+        st = load().retention_forward(*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), _ptr(gamma),
+                                      *_strided(y, "y"), B, H, N, d, _ptr(cu_seqlens), _ptr(states), _ptr(slots),
+                                      n_slots, int(bool(load_state)), _dtype(q), opt,
+                                      *_retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, False, dev),
+                                      _stream(stream, dev))
+    _check("retention_forward", st)
+    return y
+
+
+def retention_backward(q, k, v, gamma, dy, dq, dk, dv, *, cu_seqlens=None, scale=1.0, feature="identity",
+                       workspace=None, stream=None):
+    """Gradients of retention_forward (without states) from dy = dL/dY; dq, dk and dv are written.
+    Shapes as there; every tensor may have its own strides."""
+    B, H, N, d = _retention_sizes(q, cu_seqlens)
+    for name, t in (("k", k), ("v", v), ("dy", dy), ("dq", dq), ("dk", dk), ("dv", dv)):
+        _expect(t, name, q.shape, q.dtype)
+    _expect(gamma, "gamma", (H,), torch.float32)
+    opt = _retention_options(feature, scale)
+    dev = _retention_device([q, k, v, dy, dq, dk, dv], [gamma, cu_seqlens, workspace])
+    with torch.cuda.device(dev):
+        st = load().retention_backward(*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), _ptr(gamma),
+                                       *_strided(dy, "dy"), *_strided(dq, "dq"), *_strided(dk, "dk"),
+                                       *_strided(dv, "dv"), B, H, N, d, _ptr(cu_seqlens), _dtype(q), opt,
+                                       *_retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, True, dev),
+                                       _stream(stream, dev))
+    _check("retention_backward", st)
+    return dq, dk, dv
+
+
+def retention_step(q, k, v, gamma, states, out, *, slots=None, scale=1.0, feature="identity", stream=None):
+    """One token for every row: q/k/v/out [B, H, d] with any strides (rows contiguous), gamma [H] fp32,
+    states [slots, H, d, d] fp32 (updated); ``slots`` int32 [B], an entry outside the pool leaves its
+    row out."""
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [B, H, d], got shape {tuple(q.shape)}")
+    B, H, d = q.shape
+    for name, t in (("k", k), ("v", v), ("out", out)):
+        _expect(t, name, q.shape, q.dtype)
+    _expect(gamma, "gamma", (H,), torch.float32)
+    if states is None:
+        raise ValueError("states: required")
+    n_slots = _retention_states(states, slots, B, H, d)
+    opt = _retention_options(feature, scale)
+    dev = _retention_device([q, k, v, out], [gamma, states, slots])
+    with torch.cuda.device(dev):
+        st = load().retention_step(*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), _ptr(gamma), _ptr(states),
+                                   _ptr(slots), n_slots, *_strided(out, "out"), B, H, d, _dtype(q), opt,
+                                   _stream(stream, dev))
+    _check("retention_step", st)
+    return out
+
+
+def retention_copy_states(states, src, dst, *, stream=None):
+    """states[dst[i]] = states[src[i]] for all pairs at once (src < 0: zeros); states [slots, H, d, d]
+    fp32, src and dst int32 [n], n <= 1024."""
+    if states.dim() != 4 or states.shape[2] != states.shape[3]:
+        raise ValueError(f"states: expected [slots, H, d, d], got shape {tuple(states.shape)}")
+    _expect(states, "states", states.shape, torch.float32)
+    if src.dim() != 1:
+        raise ValueError(f"src: expected [n], got shape {tuple(src.shape)}")
+    for name, t in (("src", src), ("dst", dst)):
+        _expect(t, name, src.shape, torch.int32)
+    dev = _same_device(states, src, dst)
+    with torch.cuda.device(dev):
+        st = load().retention_copy_states(_ptr(states), states.shape[0], states.shape[1], states.shape[2], _ptr(src),
+                                          _ptr(dst), src.numel(), _stream(stream, dev))
+    _check("retention_copy_states", st)
+    return states
 
 
 def rala_forward(q, k, v, x, w, y, *, workspace=None, stream=None):

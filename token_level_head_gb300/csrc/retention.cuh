@@ -1,0 +1,117 @@
+// Device helpers shared by the retention kernels: decays, feature maps, segments, slots.
+#pragma once
+
+#include "common.cuh"
+#include "retention.h"
+
+namespace mhla {
+
+constexpr int kFeatIdentity = 3;  // beside the kinds of phi_k
+
+__device__ __forceinline__ float ret_phi(float x, int feature) {
+  return feature == kFeatIdentity ? x : phi_k(x, feature);
+}
+// phi'(x): 1 for the identity; ELU + 1: 1 for x > 0, e^x otherwise; ReLU: 1 for x > 0; exp: e^x
+__device__ __forceinline__ float ret_dphi(float x, int feature) {
+  if (feature == kFeatIdentity) return 1.f;
+  if (feature == 1) return x > 0.f ? 1.f : 0.f;
+  return feature == 0 && x > 0.f ? 1.f : expf(x);
+}
+
+// log2(gamma).  gamma - 1 is exact for gamma in [1/2, 2], so decays close to 1 keep their digits;
+// gamma = 0 gives -inf.
+__device__ __forceinline__ float decay_log2(float gamma) { return log1pf(gamma - 1.f) * 1.4426950408889634f; }
+
+// gamma^n for n >= 0 from lg = log2(gamma).  The relative error is about 2^-23 n |lg|, so below 2^-18
+// wherever the power itself is above 2^-32.  gamma^0 = 1 for every gamma, 0 among them.
+__device__ __forceinline__ float decay_pow(float lg, int n) { return n == 0 ? 1.f : exp2f(lg * (float)n); }
+
+struct Segment {
+  int seq;     // sequence, -1: no such segment
+  int seg;     // its number within the sequence
+  int nseg;    // segments of the sequence
+  int row0;    // first token row (within the sequence's batch entry when dense)
+  int len;     // tokens of the segment
+};
+
+// Tokens [lo, hi) of packed sequence i.  Offsets outside [0, T] or out of order are clamped, so that
+// whatever cu holds, no row outside the tensors is touched.
+__device__ __forceinline__ void packed_range(const RetArgs& a, int i, int* lo, int* hi) {
+  *lo = min(max(a.cu[i], 0), a.T);
+  *hi = min(max(a.cu[i + 1], *lo), a.T);
+}
+__device__ __forceinline__ int packed_segments(const RetArgs& a, int i) {
+  int lo, hi;
+  packed_range(a, i, &lo, &hi);
+  return (hi - lo + a.L - 1) / a.L;
+}
+
+// Segment number g of the call (whole block; scratch: 34 ints of shared memory).  An empty sequence has none.  Packed sequences'
+// segments are numbered sequence after sequence: thread t counts those of B / blockDim.x sequences,
+// a block-wide scan finds the thread whose range holds g.
+__device__ __forceinline__ Segment find_segment(const RetArgs& a, int g, int* scratch) {
+  Segment s;
+  if (a.cu == nullptr) {
+    s.nseg = (a.N + a.L - 1) / a.L;
+    s.seq = g / s.nseg;
+    s.seg = g - s.seq * s.nseg;
+    s.row0 = s.seg * a.L;
+    s.len = min(a.L, a.N - s.row0);
+    return s;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = (blockDim.x + 31) >> 5;
+  const int per = (a.B + blockDim.x - 1) / blockDim.x;
+  const int i0 = min(tid * per, a.B), i1 = min(i0 + per, a.B);
+  int n = 0;
+  for (int i = i0; i < i1; ++i) n += packed_segments(a, i);
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  if (tid == 0) scratch[32] = -1;
+  __syncthreads();
+  int first = inc - n;
+  for (int w = 0; w < nw && w < warp; ++w) first += scratch[w];
+  if (g >= first && g < first + n) {
+    for (int i = i0; i < i1; ++i) {
+      const int m = packed_segments(a, i);
+      if (g < first + m) {
+        scratch[32] = i;
+        scratch[33] = g - first;
+        break;
+      }
+      first += m;
+    }
+  }
+  __syncthreads();
+  s.seq = scratch[32];
+  s.seg = scratch[33];
+  __syncthreads();
+  if (s.seq < 0) return s;
+  int lo, hi;
+  packed_range(a, s.seq, &lo, &hi);
+  s.nseg = packed_segments(a, s.seq);
+  s.row0 = lo + s.seg * a.L;
+  s.len = max(0, min(a.L, hi - s.row0));
+  return s;
+}
+
+// Base of sequence seq, head h: packed sequences share batch entry 0.
+__device__ __forceinline__ long long ret_base(const RetArgs& a, const RetTensor& t, int seq, int h) {
+  return (a.cu == nullptr ? (long long)seq * t.sb : 0ll) + (long long)h * t.sh;
+}
+
+// The slot of sequence `seq`, -1 for none: out of range, or already taken by a sequence before it
+// (whole block; at most B compares).
+__device__ __forceinline__ int ret_slot(const int* slots, int n_slots, int seq) {
+  if (slots == nullptr) return seq < n_slots ? seq : -1;
+  const int s = slots[seq];
+  bool taken = false;
+  for (int i = threadIdx.x; i < seq; i += blockDim.x) taken |= slots[i] == s;
+  return __syncthreads_or(taken) || s < 0 || s >= n_slots ? -1 : s;
+}
+
+}  // namespace mhla

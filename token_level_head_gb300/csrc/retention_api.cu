@@ -1,0 +1,336 @@
+// C-ABI entry points of the retention operators: argument validation, the plan of the segments and
+// dispatch.  The operations are documented in include/mhla.h.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "retention.h"
+
+namespace mhla {
+namespace {
+
+bool valid_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+mhla_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA; }
+
+constexpr int kMaxPairs = 1024;
+
+// ---- token tensors
+struct Extent {  // of a tensor: B x H x N rows of d elements
+  long long b, h, n, d;
+  int es;
+};
+
+// Fills t; false if the pointer, the alignment or the strides are not valid.
+bool make_tensor(RetTensor* t, const void* p, const mhla_strides* st, const Extent& e) {
+  if (p == nullptr || !aligned(p, 16)) return false;
+  t->p = p;
+  t->sb = st ? st->b : e.h * e.n * e.d;
+  t->sh = st ? st->h : e.n * e.d;
+  t->sn = st ? st->n : e.d;
+  if (e.b <= 1) t->sb = 0;  // the stride of a single entry is not looked at
+  if (e.h <= 1) t->sh = 0;
+  if (e.n <= 1) t->sn = 0;
+  const long long q = 16 / e.es, most = 1ll << 38;  // 2^40 bytes
+  for (long long s : {t->sb, t->sh, t->sn})
+    if (s < 0 || s % q != 0 || s >= most) return false;
+  t->feature = MHLA_PHI_IDENTITY;
+  return true;
+}
+
+long long span(const RetTensor& t, const Extent& e) {
+  return (e.b - 1) * t.sb + (e.h - 1) * t.sh + (e.n - 1) * t.sn + e.d;
+}
+
+struct Dim {
+  long long stride, extent;
+};
+void sorted_dims(const RetTensor& t, const Extent& e, Dim* d) {
+  d[0] = {t.sb, e.b};
+  d[1] = {t.sh, e.h};
+  d[2] = {t.sn, e.n};
+  std::sort(d, d + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+}
+
+// No two rows of the tensor overlap (sufficient: each stride spans what is inside it).
+bool injective(const RetTensor& t, const Extent& e) {
+  Dim d[3];
+  sorted_dims(t, e, d);
+  long long inner = e.d;
+  for (const Dim& x : d) {
+    if (x.extent <= 1) continue;
+    if (x.stride < inner) return false;
+    inner = (x.extent - 1) * x.stride + inner;
+  }
+  return true;
+}
+
+// Is there a combination of index differences with |delta + sum| < width?  dims[0 .. n): strides
+// ascending, each spanning what is inside it, so only the two multiples around delta can be near.
+bool meet(long long delta, const Dim* dims, int n, long long width) {
+  while (n > 0 && dims[n - 1].extent <= 1) --n;
+  if (n == 0) return std::llabs(delta) < width;
+  const Dim& x = dims[n - 1];
+  const long long q = delta / x.stride;
+  for (long long c = q - 1; c <= q + 1; ++c)
+    if (std::llabs(c) < x.extent && meet(delta - c * x.stride, dims, n - 1, width)) return true;
+  return false;
+}
+
+// An output against another tensor: apart in memory, or interleaved with the same strides (slices of one
+// fused tensor) without a common element.
+bool disjoint(const RetTensor& o, const RetTensor& t, const Extent& e) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(o.p), b = reinterpret_cast<uintptr_t>(t.p);
+  if (a >= b + span(t, e) * e.es || b >= a + span(o, e) * e.es) return true;
+  if (o.sb != t.sb || o.sh != t.sh || o.sn != t.sn || !injective(o, e)) return false;
+  const long long diff = (long long)(b - a);
+  if (diff % e.es != 0) return false;
+  Dim d[3];
+  sorted_dims(o, e, d);
+  return !meet(diff / e.es, d, 3, e.d);
+}
+
+bool apart(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an == 0 || bn == 0 || a == nullptr || b == nullptr || x >= y + bn || y >= x + an;
+}
+
+bool options_ok(const retention_options* opt) {
+  return opt == nullptr ||
+         (opt->feature >= MHLA_PHI_ELU1 && opt->feature <= MHLA_PHI_IDENTITY && std::isfinite(opt->scale));
+}
+
+// ---- segments
+struct Plan {
+  int L, G;      // tokens of a segment, segments
+  size_t bytes;  // workspace
+  bool split;    // some sequence may have two segments
+};
+
+// tokens: in all.  Enough segments to fill the GPU a few times over, no more: each costs a state.
+Plan make_plan(int B, int H, long long tokens, int d, bool packed, bool backward) {
+  const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
+  const long long want = 608, rows = (long long)H * npass * (d > 64 ? 2 : 1);
+  const long long segs = std::max<long long>(1, (want + rows - 1) / rows);
+  long long L = std::max<long long>(128, (tokens + segs - 1) / segs);
+  L = std::min<long long>((L + 127) / 128 * 128, ((long long)N + 127) / 128 * 128);
+  Plan p;
+  p.L = (int)std::max<long long>(L, 128);
+  p.G = (int)(packed ? tokens / p.L + B : (long long)B * ((N + p.L - 1) / p.L));
+  p.split = N > p.L;
+  p.bytes = kWorkspacePrefix + (p.split ? (size_t)nsum * p.G * H * d * d * sizeof(float) : 0);
+  return p;
+}
+
+bool sizes_ok(int B, int H, int N, int d) { return B >= 0 && H >= 0 && N >= 0 && valid_d(d); }
+
+// What retention_forward and retention_backward have in common; *empty: nothing to do.
+mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, int H, int N, int d, const int* cu,
+                  mhla_dtype dt, const retention_options* opt, bool backward, void* ws, size_t ws_bytes, bool* empty) {
+  *empty = false;
+  if (!sizes_ok(B, H, N, d) || (dt != MHLA_F32 && dt != MHLA_BF16) || !options_ok(opt)) return MHLA_ERR_INVALID_ARG;
+  if (B == 0 || H == 0 || N == 0) {
+    *empty = true;
+    return MHLA_OK;
+  }
+  const long long tokens = cu ? N : (long long)B * N;
+  if (tokens > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
+  if (!gamma || !aligned(gamma, 4) || !aligned(cu, 4)) return MHLA_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256)) return MHLA_ERR_INVALID_ARG;
+  *plan = make_plan(B, H, tokens, d, cu != nullptr, backward);
+  if ((long long)plan->G * H > 0x7fffffffll || (long long)B * H > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
+  if (ws_bytes < plan->bytes) return MHLA_ERR_INVALID_ARG;
+  *e = {cu ? 1 : B, H, N, d, dt == MHLA_F32 ? 4 : 2};
+  *a = RetArgs{};
+  a->B = B;
+  a->H = H;
+  a->N = N;
+  a->T = (int)tokens;
+  a->d = d;
+  a->cu = cu;
+  a->gamma = gamma;
+  a->scale = opt ? opt->scale : 1.f;
+  a->L = plan->L;
+  a->G = plan->G;
+  a->seg = plan->split ? reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspacePrefix) : nullptr;
+  a->status = &static_cast<WorkspaceHeader*>(ws)->status;
+  return MHLA_OK;
+}
+
+RetTensor mapped(RetTensor t, int feature) {
+  t.feature = feature;
+  return t;
+}
+
+}  // namespace
+}  // namespace mhla
+
+using namespace mhla;
+
+extern "C" {
+
+size_t retention_workspace_bytes(int B, int H, int tokens, int d, int backward) {
+  if (!sizes_ok(B, H, tokens, d) || (backward != 0 && backward != 1)) return 0;
+  if (B == 0 || H == 0 || tokens == 0) return kWorkspacePrefix;
+  size_t n = make_plan(B, H, tokens, d, true, backward != 0).bytes;
+  if (tokens % B == 0) n = std::max(n, make_plan(B, H, tokens, d, false, backward != 0).bytes);
+  return n;
+}
+
+mhla_status retention_forward(const void* q, const mhla_strides* q_strides, const void* k,
+                              const mhla_strides* k_strides, const void* v, const mhla_strides* v_strides,
+                              const float* gamma, void* y, const mhla_strides* y_strides, int B, int H, int N, int d,
+                              const int* cu_seqlens, float* states, const int* slots, int n_slots, int load_state,
+                              mhla_dtype dt, const retention_options* opt, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (load_state != 0 && load_state != 1) return MHLA_ERR_INVALID_ARG;
+  if (states == nullptr ? (slots != nullptr || load_state != 0) : n_slots < 0) return MHLA_ERR_INVALID_ARG;
+  RetArgs a;
+  Plan plan;
+  Extent e;
+  bool empty;
+  const mhla_status st = begin(&a, &plan, &e, gamma, B, H, N, d, cu_seqlens, dt, opt, false, workspace,
+                               workspace_bytes, &empty);
+  if (st != MHLA_OK || empty) return st;
+  RetTensor tq, tk, tv, ty;
+  if (!make_tensor(&tq, q, q_strides, e) || !make_tensor(&tk, k, k_strides, e) || !make_tensor(&tv, v, v_strides, e) ||
+      !make_tensor(&ty, y, y_strides, e) || !injective(ty, e))
+    return MHLA_ERR_INVALID_ARG;
+  const size_t sb = (size_t)(states ? n_slots : 0) * H * d * d * sizeof(float);
+  if (!aligned(states, 16) || !aligned(slots, 4)) return MHLA_ERR_INVALID_ARG;
+  for (const RetTensor* t : {&tq, &tk, &tv, &ty}) {
+    const size_t n = (size_t)span(*t, e) * e.es;
+    if (t != &ty && !disjoint(ty, *t, e)) return MHLA_ERR_INVALID_ARG;
+    if (!apart(t->p, n, states, sb) || !apart(t->p, n, workspace, plan.bytes)) return MHLA_ERR_INVALID_ARG;
+  }
+  const size_t yb = (size_t)span(ty, e) * e.es, gb = (size_t)H * 4, cb = (size_t)(B + 1) * 4, lb = (size_t)B * 4;
+  if (!apart(states, sb, workspace, plan.bytes) || !apart(gamma, gb, y, yb) || !apart(gamma, gb, states, sb) ||
+      !apart(gamma, gb, workspace, plan.bytes) || !apart(cu_seqlens, cb, y, yb) || !apart(cu_seqlens, cb, states, sb) ||
+      !apart(cu_seqlens, cb, workspace, plan.bytes) || !apart(slots, lb, y, yb) || !apart(slots, lb, states, sb) ||
+      !apart(slots, lb, workspace, plan.bytes))
+    return MHLA_ERR_INVALID_ARG;
+  const int f = opt ? opt->feature : MHLA_PHI_IDENTITY;
+  a.npass = a.nsum = 1;
+  a.pass[0].a = mapped(tq, f);
+  a.pass[0].b = mapped(tk, f);
+  a.pass[0].c = tv;
+  a.pass[0].out = ty;
+  a.states = states;
+  a.slots = slots;
+  a.n_slots = n_slots;
+  a.load = load_state;
+  return from_cuda(simt_retention_launch(a, dt, static_cast<cudaStream_t>(stream)));
+}
+
+mhla_status retention_backward(const void* q, const mhla_strides* q_strides, const void* k,
+                               const mhla_strides* k_strides, const void* v, const mhla_strides* v_strides,
+                               const float* gamma, const void* dy, const mhla_strides* dy_strides, void* dq,
+                               const mhla_strides* dq_strides, void* dk, const mhla_strides* dk_strides, void* dv,
+                               const mhla_strides* dv_strides, int B, int H, int N, int d, const int* cu_seqlens,
+                               mhla_dtype dt, const retention_options* opt, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  RetArgs a;
+  Plan plan;
+  Extent e;
+  bool empty;
+  const mhla_status st = begin(&a, &plan, &e, gamma, B, H, N, d, cu_seqlens, dt, opt, true, workspace,
+                               workspace_bytes, &empty);
+  if (st != MHLA_OK || empty) return st;
+  RetTensor in[4], out[3];
+  const void* ip[4] = {q, k, v, dy};
+  void* op[3] = {dq, dk, dv};
+  const mhla_strides* is[4] = {q_strides, k_strides, v_strides, dy_strides};
+  const mhla_strides* os[3] = {dq_strides, dk_strides, dv_strides};
+  const size_t gb = (size_t)H * 4, cb = (size_t)(B + 1) * 4;
+  for (int i = 0; i < 4; ++i) {
+    if (!make_tensor(&in[i], ip[i], is[i], e)) return MHLA_ERR_INVALID_ARG;
+    if (!apart(ip[i], (size_t)span(in[i], e) * e.es, workspace, plan.bytes)) return MHLA_ERR_INVALID_ARG;
+  }
+  if (!apart(gamma, gb, workspace, plan.bytes) || !apart(cu_seqlens, cb, workspace, plan.bytes))
+    return MHLA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (!make_tensor(&out[i], op[i], os[i], e) || !injective(out[i], e)) return MHLA_ERR_INVALID_ARG;
+    const size_t n = (size_t)span(out[i], e) * e.es;
+    for (int j = 0; j < 4; ++j)
+      if (!disjoint(out[i], in[j], e)) return MHLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (!disjoint(out[i], out[j], e)) return MHLA_ERR_INVALID_ARG;
+    if (!apart(op[i], n, workspace, plan.bytes) || !apart(op[i], n, gamma, gb) || !apart(op[i], n, cu_seqlens, cb))
+      return MHLA_ERR_INVALID_ARG;
+  }
+  const int f = opt ? opt->feature : MHLA_PHI_IDENTITY;
+  const RetTensor fq = mapped(in[0], f), fk = mapped(in[1], f);
+  const bool deriv = f != MHLA_PHI_IDENTITY;
+  a.npass = 3;
+  a.nsum = 2;
+  RetPass& pq = a.pass[0];
+  pq.a = in[3];
+  pq.b = in[2];
+  pq.c = fk;
+  if (deriv) pq.x = fq;
+  pq.out = out[0];
+  RetPass& pk = a.pass[1];
+  pk.a = in[2];
+  pk.b = in[3];
+  pk.c = fq;
+  if (deriv) pk.x = fk;
+  pk.out = out[1];
+  pk.reverse = 1;
+  pk.sum = 1;
+  RetPass& pv = a.pass[2];  // its state, sum phi(q) dy^T, is the transpose of the one above
+  pv.a = fk;
+  pv.b = fq;
+  pv.c = in[3];
+  pv.out = out[2];
+  pv.reverse = 1;
+  pv.sum = 1;
+  pv.sum_t = 1;
+  return from_cuda(simt_retention_launch(a, dt, static_cast<cudaStream_t>(stream)));
+}
+
+mhla_status retention_step(const void* q, const mhla_strides* q_strides, const void* k, const mhla_strides* k_strides,
+                           const void* v, const mhla_strides* v_strides, const float* gamma, float* states,
+                           const int* slots, int n_slots, void* out, const mhla_strides* out_strides, int B, int H,
+                           int d, mhla_dtype dt, const retention_options* opt, void* stream) {
+  if (!sizes_ok(B, H, 1, d) || (dt != MHLA_F32 && dt != MHLA_BF16) || !options_ok(opt) || n_slots < 0)
+    return MHLA_ERR_INVALID_ARG;
+  if (B == 0 || H == 0) return MHLA_OK;
+  if ((long long)B * H > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
+  if (!gamma || !states || !aligned(gamma, 4) || !aligned(states, 16) || !aligned(slots, 4))
+    return MHLA_ERR_INVALID_ARG;
+  const Extent e{B, H, 1, d, dt == MHLA_F32 ? 4 : 2};
+  RetTensor tq, tk, tv, to;
+  if (!make_tensor(&tq, q, q_strides, e) || !make_tensor(&tk, k, k_strides, e) || !make_tensor(&tv, v, v_strides, e) ||
+      !make_tensor(&to, out, out_strides, e) || !injective(to, e))
+    return MHLA_ERR_INVALID_ARG;
+  const size_t sb = (size_t)n_slots * H * d * d * sizeof(float), ob = (size_t)span(to, e) * e.es;
+  for (const RetTensor* t : {&tq, &tk, &tv, &to}) {
+    if (t != &to && !disjoint(to, *t, e)) return MHLA_ERR_INVALID_ARG;
+    if (!apart(t->p, (size_t)span(*t, e) * e.es, states, sb)) return MHLA_ERR_INVALID_ARG;
+  }
+  if (!apart(gamma, (size_t)H * 4, states, sb) || !apart(slots, (size_t)B * 4, states, sb) ||
+      !apart(gamma, (size_t)H * 4, out, ob) || !apart(slots, (size_t)B * 4, out, ob))
+    return MHLA_ERR_INVALID_ARG;
+  const int f = opt ? opt->feature : MHLA_PHI_IDENTITY;
+  return from_cuda(retention_step_launch(B, H, d, dt, mapped(tq, f), mapped(tk, f), tv, to, gamma,
+                                         opt ? opt->scale : 1.f, states, slots, n_slots,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+mhla_status retention_copy_states(float* states, int n_slots, int H, int d, const int* src, const int* dst, int n,
+                                  void* stream) {
+  if (!sizes_ok(n_slots, H, 0, d) || n < 0) return MHLA_ERR_INVALID_ARG;
+  if (n_slots == 0 || H == 0 || n == 0) return MHLA_OK;
+  if (n > kMaxPairs) return MHLA_ERR_UNSUPPORTED;
+  if (!states || !src || !dst || !aligned(states, 16) || !aligned(src, 4) || !aligned(dst, 4))
+    return MHLA_ERR_INVALID_ARG;
+  const long long slot = (long long)H * d * d;
+  if (slot / 32 > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
+  const size_t sb = (size_t)n_slots * slot * sizeof(float);
+  if (!apart(states, sb, src, (size_t)n * 4) || !apart(states, sb, dst, (size_t)n * 4)) return MHLA_ERR_INVALID_ARG;
+  return from_cuda(retention_copy_launch(states, slot, n_slots, src, dst, n, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,505 @@
+// Retention passes on the SIMT cores (fp32 arithmetic), the scan over segments, the single-token step
+// and the copies between state slots.  The mathematics is in retention.h.
+#include <algorithm>
+
+#include "internal.h"
+#include "retention.cuh"
+
+namespace mhla {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTok = 64;  // tokens of a chunk
+
+// ================================================================ passes
+// A block takes one segment of one head and ES columns of c: per chunk of 64 tokens
+//   P = (A B^T) gamma^(t-s), masked;  out = P C + gamma^(i+1) A X;  X = gamma^len X + (B w)^T C,
+// w_s = gamma^(len-1-s), with X [D][ES] and the chunk's A, B, C and P in shared memory and 4 x 4 (X: up
+// to 8 x 4) register tiles.  With SUM only X is formed: the segment's own sum.
+template <int D>
+struct SimtTile {
+  static constexpr int ES = D < 64 ? D : 64;
+  static constexpr int LD = D + 4;           // row of A and B: lanes on neighbouring rows hit other banks
+  static constexpr int LP = kTok + 4;
+  static constexpr int NX = ES / 4, NY = kThreads / NX;
+  static constexpr int RO = kTok / NY;       // rows of out a thread holds
+  static constexpr int RS = D >= NY ? D / NY : 1;
+  static constexpr int kFloats = 2 * kTok * LD + kTok * ES + D * ES + kTok * LP + kTok;
+  static constexpr size_t kBytes = kFloats * sizeof(float);
+};
+
+template <typename T>
+__device__ __forceinline__ void load_row_piece(const T* p, float* f);
+template <>
+__device__ __forceinline__ void load_row_piece<float>(const float* p, float* f) {
+  const float4 u = *reinterpret_cast<const float4*>(p);
+  f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
+}
+template <>
+__device__ __forceinline__ void load_row_piece<__nv_bfloat16>(const __nv_bfloat16* p, float* f) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(u.x << 16);
+  f[1] = __uint_as_float(u.x & 0xffff0000u);
+  f[2] = __uint_as_float(u.y << 16);
+  f[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+
+// Rows 0 .. len - 1, columns c0 .. c0 + W - 1 of a tensor from row `row`, widened, phi applied; zeros behind.
+template <typename T, int W, int LDS>
+__device__ __forceinline__ void load_tile(float* dst, const RetTensor& t, long long base, int row, int len, int c0) {
+  const T* src = static_cast<const T*>(t.p) + base + (long long)row * t.sn + c0;
+  for (int i = threadIdx.x; i < kTok * (W / 4); i += kThreads) {
+    const int r = i / (W / 4), c = (i % (W / 4)) * 4;
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < len) {
+      load_row_piece<T>(src + (long long)r * t.sn + c, f);
+      if (t.feature != kFeatIdentity)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] = ret_phi(f[x], t.feature);
+    }
+    *reinterpret_cast<float4*>(dst + r * LDS + c) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+}
+
+template <typename T, int D, bool SUM>
+__global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_constant__ RetArgs a) {
+  using C = SimtTile<D>;
+  extern __shared__ float4 smem4[];
+  float* sA = reinterpret_cast<float*>(smem4);
+  float* sB = sA + kTok * C::LD;
+  float* sC = sB + kTok * C::LD;
+  float* sX = sC + kTok * C::ES;
+  float* sP = sX + D * C::ES;
+  float* sW = sP + kTok * C::LP;
+  __shared__ int scratch[34];
+  const int tid = threadIdx.x;
+  const int h = blockIdx.x % a.H, g = blockIdx.x / a.H;
+  int z = blockIdx.z;
+  if (SUM)  // the pass that makes set z
+    for (int i = 0; i < a.npass; ++i)
+      if (a.pass[i].sum == (int)blockIdx.z && !a.pass[i].sum_t) z = i;
+  const RetPass& p = a.pass[z];
+  const Segment sg = find_segment(a, g, scratch);
+  if (sg.seq < 0) return;
+  const int e0 = blockIdx.y * C::ES;
+  const float lg = decay_log2(a.gamma[h]);
+  const int tx = tid % C::NX, ty = tid / C::NX;
+  float* seg = a.seg == nullptr ? nullptr : a.seg + (((size_t)p.sum * a.G + g) * a.H + h) * (D * D);
+  if (SUM) {
+    // the last segment in the pass's direction enters no other
+    if (p.reverse ? sg.seg == 0 : sg.seg == sg.nseg - 1) return;
+    for (int i = tid; i < D * C::ES; i += kThreads) sX[i] = 0.f;
+  }
+  int slot = -1;
+  if (!SUM) {
+    const float* src = nullptr;
+    bool tr = false;
+    if (a.states != nullptr) slot = ret_slot(a.slots, a.n_slots, sg.seq);
+    if (sg.nseg > 1) {
+      src = seg;
+      tr = p.sum_t != 0;
+    } else if (a.load && slot >= 0) {
+      src = a.states + ((size_t)slot * a.H + h) * (D * D);
+    }
+    for (int i = tid; i < D * C::ES; i += kThreads) {
+      const int r = i / C::ES, e = e0 + i % C::ES;
+      sX[i] = src == nullptr ? 0.f : tr ? src[e * D + r] : src[r * D + e];
+    }
+  }
+  const long long ba = ret_base(a, p.a, sg.seq, h), bb = ret_base(a, p.b, sg.seq, h), bc = ret_base(a, p.c, sg.seq, h);
+  const int nch = (sg.len + kTok - 1) / kTok;
+  for (int it = 0; it < nch; ++it) {
+    const int ch = p.reverse ? nch - 1 - it : it;
+    const int row = sg.row0 + ch * kTok, len = min(kTok, sg.len - ch * kTok);
+    __syncthreads();
+    if (!SUM) load_tile<T, D, C::LD>(sA, p.a, ba, row, len, 0);
+    load_tile<T, D, C::LD>(sB, p.b, bb, row, len, 0);
+    load_tile<T, C::ES, C::ES>(sC, p.c, bc, row, len, e0);
+    if (tid < kTok) sW[tid] = tid < len ? decay_pow(lg, p.reverse ? tid : len - 1 - tid) : 0.f;
+    __syncthreads();
+    if (!SUM) {
+      // P: 4 rows t, 4 columns s = tp + 16 j
+      const int tp = tid & 15, tr = tid >> 4;
+      float acc[4][4] = {};
+      for (int c = 0; c < D; c += 4) {
+        float4 fa[4], fb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const float4*>(sA + (4 * tr + i) * C::LD + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fb[j] = *reinterpret_cast<const float4*>(sB + (tp + 16 * j) * C::LD + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[i][j] = fmaf(fa[i].x, fb[j].x, acc[i][j]);
+            acc[i][j] = fmaf(fa[i].y, fb[j].y, acc[i][j]);
+            acc[i][j] = fmaf(fa[i].z, fb[j].z, acc[i][j]);
+            acc[i][j] = fmaf(fa[i].w, fb[j].w, acc[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = 4 * tr + i, s = tp + 16 * j, n = p.reverse ? s - t : t - s;
+          sP[t * C::LP + s] = n >= 0 && s < len ? acc[i][j] * decay_pow(lg, n) : 0.f;
+        }
+      __syncthreads();
+      // out = P C + gamma^(i+1) A X
+      float in[C::RO][4] = {}, ac[C::RO][4] = {};
+      for (int s = 0; s < kTok; s += 4) {
+        float4 fp[C::RO];
+#pragma unroll
+        for (int i = 0; i < C::RO; ++i) fp[i] = *reinterpret_cast<const float4*>(sP + (C::RO * ty + i) * C::LP + s);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 v = *reinterpret_cast<const float4*>(sC + (s + u) * C::ES + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < C::RO; ++i) {
+            const float w = u == 0 ? fp[i].x : u == 1 ? fp[i].y : u == 2 ? fp[i].z : fp[i].w;
+            in[i][0] = fmaf(w, v.x, in[i][0]);
+            in[i][1] = fmaf(w, v.y, in[i][1]);
+            in[i][2] = fmaf(w, v.z, in[i][2]);
+            in[i][3] = fmaf(w, v.w, in[i][3]);
+          }
+        }
+      }
+      for (int c = 0; c < D; c += 4) {
+        float4 fa[C::RO];
+#pragma unroll
+        for (int i = 0; i < C::RO; ++i) fa[i] = *reinterpret_cast<const float4*>(sA + (C::RO * ty + i) * C::LD + c);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 v = *reinterpret_cast<const float4*>(sX + (c + u) * C::ES + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < C::RO; ++i) {
+            const float w = u == 0 ? fa[i].x : u == 1 ? fa[i].y : u == 2 ? fa[i].z : fa[i].w;
+            ac[i][0] = fmaf(w, v.x, ac[i][0]);
+            ac[i][1] = fmaf(w, v.y, ac[i][1]);
+            ac[i][2] = fmaf(w, v.z, ac[i][2]);
+            ac[i][3] = fmaf(w, v.w, ac[i][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < C::RO; ++i) {
+        const int t = C::RO * ty + i;
+        if (t >= len) continue;
+        const float w = decay_pow(lg, p.reverse ? len - t : t + 1);
+        float o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[x] = a.scale * fmaf(w, ac[i][x], in[i][x]);
+        if (p.x.p != nullptr) {
+          float fx[4];
+          load_row_piece<T>(static_cast<const T*>(p.x.p) + ret_base(a, p.x, sg.seq, h) + (long long)(row + t) * p.x.sn +
+                                e0 + 4 * tx, fx);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[x] *= ret_dphi(fx[x], p.x.feature);
+        }
+        T* dst = static_cast<T*>(const_cast<void*>(p.out.p)) + ret_base(a, p.out, sg.seq, h) +
+                 (long long)(row + t) * p.out.sn + e0 + 4 * tx;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) dst[x] = from_f<T>(o[x]);
+      }
+      __syncthreads();  // every A X has read X
+    }
+    // X = gamma^len X + (B w)^T C: rows RS ty .., columns 4 tx ..
+    if (C::RS * ty < D) {
+      float acc[C::RS][4];
+      const float w0 = decay_pow(lg, len);
+#pragma unroll
+      for (int i = 0; i < C::RS; ++i) {
+        const float4 u = *reinterpret_cast<const float4*>(sX + (C::RS * ty + i) * C::ES + 4 * tx);
+        acc[i][0] = w0 * u.x;
+        acc[i][1] = w0 * u.y;
+        acc[i][2] = w0 * u.z;
+        acc[i][3] = w0 * u.w;
+      }
+      for (int s = 0; s < len; ++s) {
+        const float w = sW[s];
+        float4 v = *reinterpret_cast<const float4*>(sC + s * C::ES + 4 * tx);
+        v.x *= w;
+        v.y *= w;
+        v.z *= w;
+        v.w *= w;
+#pragma unroll
+        for (int i = 0; i < C::RS; ++i) {
+          const float b = sB[s * C::LD + C::RS * ty + i];
+          acc[i][0] = fmaf(b, v.x, acc[i][0]);
+          acc[i][1] = fmaf(b, v.y, acc[i][1]);
+          acc[i][2] = fmaf(b, v.z, acc[i][2]);
+          acc[i][3] = fmaf(b, v.w, acc[i][3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < C::RS; ++i)
+        *reinterpret_cast<float4*>(sX + (C::RS * ty + i) * C::ES + 4 * tx) =
+            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    }
+  }
+  __syncthreads();
+  float* dst = SUM ? seg : slot >= 0 && sg.seg == sg.nseg - 1 ? a.states + ((size_t)slot * a.H + h) * (D * D) : nullptr;
+  if (dst != nullptr)
+    for (int i = tid; i < D * C::ES; i += kThreads) dst[(i / C::ES) * D + e0 + i % C::ES] = sX[i];
+}
+
+template <typename T, int D>
+cudaError_t launch_passes(const RetArgs& a, cudaStream_t st) {
+  using C = SimtTile<D>;
+  static SmemOptIn opt_sum, opt_out;
+  cudaError_t e = opt_sum.ensure((const void*)retention_simt_kernel<T, D, true>, (int)C::kBytes);
+  if (e == cudaSuccess) e = opt_out.ensure((const void*)retention_simt_kernel<T, D, false>, (int)C::kBytes);
+  if (e != cudaSuccess) return e;
+  dim3 grid((unsigned)(a.G * a.H), D / C::ES, a.nsum);
+  if (a.seg != nullptr) {
+    retention_simt_kernel<T, D, true><<<grid, kThreads, C::kBytes, st>>>(a);
+    note_launch();
+    e = retention_scan_launch(a, st);
+    if (e != cudaSuccess) return e;
+  }
+  grid.z = a.npass;
+  retention_simt_kernel<T, D, false><<<grid, kThreads, C::kBytes, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_passes_d(const RetArgs& a, cudaStream_t st) {
+  switch (a.d) {
+    case 16: return launch_passes<T, 16>(a, st);
+    case 32: return launch_passes<T, 32>(a, st);
+    case 64: return launch_passes<T, 64>(a, st);
+    default: return launch_passes<T, 128>(a, st);
+  }
+}
+
+// ================================================================ scan
+// One thread carries four elements of a head's state over its sequence's segments, in the pass's
+// direction: the slot of a segment holds the segment's own sum before, the state entering it after.
+__global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_constant__ RetArgs a) {
+  __shared__ int part[33];
+  const int h = blockIdx.x % a.H, seq = blockIdx.x / a.H, set = blockIdx.z;
+  int ps = 0;
+  for (int i = 0; i < a.npass; ++i)
+    if (a.pass[i].sum == set && !a.pass[i].sum_t) ps = i;
+  const bool reverse = a.pass[ps].reverse != 0;
+  int g0, nseg, len;
+  if (a.cu == nullptr) {
+    nseg = (a.N + a.L - 1) / a.L;
+    g0 = seq * nseg;
+    len = a.N;
+  } else {
+    int n = 0;
+    for (int i = threadIdx.x; i < seq; i += blockDim.x) n += packed_segments(a, i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+    __syncthreads();
+    g0 = 0;
+    for (int w = 0; w < kThreads / 32; ++w) g0 += part[w];
+    int lo, hi;
+    packed_range(a, seq, &lo, &hi);
+    nseg = packed_segments(a, seq);
+    len = hi - lo;
+  }
+  if (nseg < 2) return;  // (uniform over the block) the pass takes its state from the slot itself
+  nseg = min(nseg, a.G - g0);
+  const int slot = a.load && a.states != nullptr ? ret_slot(a.slots, a.n_slots, seq) : -1;
+  const int i4 = blockIdx.y * kThreads + threadIdx.x, n4 = a.d * a.d / 4;
+  if (i4 >= n4) return;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (slot >= 0) x = reinterpret_cast<const float4*>(a.states + ((size_t)slot * a.H + h) * a.d * a.d)[i4];
+  const float lg = decay_log2(a.gamma[h]);
+  const float wfull = decay_pow(lg, a.L);
+  float4* w = reinterpret_cast<float4*>(a.seg + (((size_t)set * a.G + g0) * a.H + h) * a.d * a.d) + i4;
+  const size_t step = (size_t)a.H * n4;
+  constexpr int kAhead = 8;  // loads in flight
+  for (int j0 = 0; j0 < nseg; j0 += kAhead) {
+    float4 u[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = j0 + j;
+      if (k < nseg - 1) u[j] = __ldcg(w + (size_t)(reverse ? nseg - 1 - k : k) * step);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = j0 + j;
+      if (k >= nseg) break;
+      const int sgm = reverse ? nseg - 1 - k : k;
+      w[(size_t)sgm * step] = x;
+      if (k == nseg - 1) break;
+      const float wl = sgm == nseg - 1 ? decay_pow(lg, len - sgm * a.L) : wfull;
+      x.x = fmaf(wl, x.x, u[j].x);
+      x.y = fmaf(wl, x.y, u[j].y);
+      x.z = fmaf(wl, x.z, u[j].z);
+      x.w = fmaf(wl, x.w, u[j].w);
+    }
+  }
+}
+
+// ================================================================ single-token step
+// S = gamma S + phi(k) v^T, out = scale phi(q) S.  A block takes ES columns of a (row, head) state: a
+// thread holds RPT float4 of it, all loads issued before the first use; the columns' sums over c go
+// through shuffles and shared memory.
+template <typename T, int D, int ES>
+__global__ void __launch_bounds__(kThreads) retention_step_kernel(int H, RetTensor q, RetTensor k, RetTensor v,
+                                                                  RetTensor out, const float* gamma, float scale,
+                                                                  float* states, const int* slots, int n_slots) {
+  constexpr int NG = ES / 4, RT = kThreads / NG, RPT = D >= RT ? D / RT : 1;
+  __shared__ float4 red[kThreads / 32][NG];
+  const int tid = threadIdx.x, cg = tid % NG, r0 = tid / NG;
+  const int h = blockIdx.x % H, b = blockIdx.x / H, e0 = blockIdx.y * ES + 4 * cg;
+  const int s0 = slots == nullptr ? b : slots[b];
+  const bool in = s0 >= 0 && s0 < n_slots;
+  float4* S = reinterpret_cast<float4*>(states + ((size_t)(in ? s0 : 0) * H + h) * (D * D) + e0);
+  const bool act = r0 * RPT < D;
+  float4 x[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i)
+    x[i] = in && act ? __ldcs(S + (size_t)(r0 + i * RT) * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float fv[4];
+  load_row_piece<T>(static_cast<const T*>(v.p) + b * v.sb + h * v.sh + e0, fv);
+  const T* qp = static_cast<const T*>(q.p) + b * q.sb + h * q.sh;
+  const T* kp = static_cast<const T*>(k.p) + b * k.sb + h * k.sh;
+  float fq[RPT], fk[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    fq[i] = act ? ret_phi(to_f(qp[r0 + i * RT]), q.feature) : 0.f;
+    fk[i] = act ? ret_phi(to_f(kp[r0 + i * RT]), k.feature) : 0.f;
+  }
+  const float gm = gamma[h];
+  if (ret_slot(slots, n_slots, b) < 0) return;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    x[i].x = fmaf(gm, x[i].x, fk[i] * fv[0]);
+    x[i].y = fmaf(gm, x[i].y, fk[i] * fv[1]);
+    x[i].z = fmaf(gm, x[i].z, fk[i] * fv[2]);
+    x[i].w = fmaf(gm, x[i].w, fk[i] * fv[3]);
+    if (act) __stcs(S + (size_t)(r0 + i * RT) * (D / 4), x[i]);
+    y.x = fmaf(fq[i], x[i].x, y.x);
+    y.y = fmaf(fq[i], x[i].y, y.y);
+    y.z = fmaf(fq[i], x[i].z, y.z);
+    y.w = fmaf(fq[i], x[i].w, y.w);
+  }
+#pragma unroll
+  for (int o = NG; o < 32; o <<= 1) {
+    y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
+    y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+    y.z += __shfl_xor_sync(0xffffffffu, y.z, o);
+    y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
+  }
+  if ((tid & 31) < NG) red[tid >> 5][cg] = y;
+  __syncthreads();
+  if (tid < NG) {
+    float4 s = red[0][tid];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) {
+      const float4 u = red[w][tid];
+      s.x += u.x;
+      s.y += u.y;
+      s.z += u.z;
+      s.w += u.w;
+    }
+    T* dst = static_cast<T*>(const_cast<void*>(out.p)) + b * out.sb + h * out.sh + e0;
+    dst[0] = from_f<T>(scale * s.x);
+    dst[1] = from_f<T>(scale * s.y);
+    dst[2] = from_f<T>(scale * s.z);
+    dst[3] = from_f<T>(scale * s.w);
+  }
+}
+
+template <typename T, int D, int ES>
+cudaError_t launch_step(int B, int H, const RetTensor& q, const RetTensor& k, const RetTensor& v, const RetTensor& out,
+                        const float* gamma, float scale, float* states, const int* slots, int n_slots,
+                        cudaStream_t st) {
+  retention_step_kernel<T, D, ES><<<dim3((unsigned)(B * H), D / ES), kThreads, 0, st>>>(H, q, k, v, out, gamma, scale,
+                                                                                       states, slots, n_slots);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_step_d(int B, int H, int d, const RetTensor& q, const RetTensor& k, const RetTensor& v,
+                          const RetTensor& out, const float* gamma, float scale, float* states, const int* slots,
+                          int n_slots, cudaStream_t st) {
+  switch (d) {
+    case 16: return launch_step<T, 16, 16>(B, H, q, k, v, out, gamma, scale, states, slots, n_slots, st);
+    case 32: return launch_step<T, 32, 32>(B, H, q, k, v, out, gamma, scale, states, slots, n_slots, st);
+    case 64: return launch_step<T, 64, 64>(B, H, q, k, v, out, gamma, scale, states, slots, n_slots, st);
+    default: return launch_step<T, 128, 32>(B, H, q, k, v, out, gamma, scale, states, slots, n_slots, st);
+  }
+}
+
+// ================================================================ state copies
+// A block takes R floats of every slot: it reads them from all sources into shared memory, then writes
+// all targets, so that a slot may be source and target of different pairs in any order.
+__global__ void __launch_bounds__(kThreads) retention_copy_kernel(float* states, long long slot_elems, int n_slots,
+                                                                  const int* src, const int* dst, int n, int R) {
+  extern __shared__ float4 smem4[];
+  float4* buf = smem4;
+  int* sdst = reinterpret_cast<int*>(smem4 + (size_t)n * (R / 4));
+  int* ssrc = sdst + n;
+  const long long e0 = (long long)blockIdx.x * R;
+  const int w4 = (int)min((long long)R, slot_elems - e0) / 4;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    sdst[i] = dst[i];
+    ssrc[i] = src[i];
+  }
+  __syncthreads();
+  // a pair out of range does nothing; of several with one target the last counts
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int d = sdst[i];
+    bool drop = d < 0 || d >= n_slots || ssrc[i] >= n_slots;
+    for (int j = i + 1; j < n && !drop; ++j) drop = sdst[j] == d && ssrc[j] < n_slots;
+    if (drop) ssrc[i] = n_slots;  // seen by the others as a pair that does nothing: its later twin still counts
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * (R / 4); i += kThreads) {
+    const int pr = i / (R / 4), c = i % (R / 4), s = ssrc[pr];
+    if (s < n_slots && c < w4)
+      buf[i] = s < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : __ldcg(reinterpret_cast<const float4*>(states + s * slot_elems + e0) + c);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * (R / 4); i += kThreads) {
+    const int pr = i / (R / 4), c = i % (R / 4);
+    if (ssrc[pr] < n_slots && c < w4) reinterpret_cast<float4*>(states + sdst[pr] * slot_elems + e0)[c] = buf[i];
+  }
+}
+
+}  // namespace
+
+cudaError_t simt_retention_launch(const RetArgs& a, mhla_dtype dt, cudaStream_t st) {
+  return dt == MHLA_F32 ? launch_passes_d<float>(a, st) : launch_passes_d<__nv_bfloat16>(a, st);
+}
+
+cudaError_t retention_scan_launch(const RetArgs& a, cudaStream_t st) {
+  const int n4 = a.d * a.d / 4;
+  retention_scan_kernel<<<dim3((unsigned)(a.B * a.H), (n4 + kThreads - 1) / kThreads, a.nsum), kThreads, 0, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t retention_step_launch(int B, int H, int d, mhla_dtype dt, const RetTensor& q, const RetTensor& k,
+                                  const RetTensor& v, const RetTensor& out, const float* gamma, float scale,
+                                  float* states, const int* slots, int n_slots, cudaStream_t st) {
+  return dt == MHLA_F32
+             ? launch_step_d<float>(B, H, d, q, k, v, out, gamma, scale, states, slots, n_slots, st)
+             : launch_step_d<__nv_bfloat16>(B, H, d, q, k, v, out, gamma, scale, states, slots, n_slots, st);
+}
+
+cudaError_t retention_copy_launch(float* states, long long slot_elems, int n_slots, const int* src, const int* dst,
+                                  int n, cudaStream_t st) {
+  const int R = n <= 256 ? 64 : 32;  // at most 1024 pairs: 136 KB
+  const size_t bytes = (size_t)n * (R * sizeof(float) + 2 * sizeof(int));
+  static SmemOptIn opt;
+  cudaError_t e = opt.ensure((const void*)retention_copy_kernel, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  retention_copy_kernel<<<(unsigned)((slot_elems + R - 1) / R), kThreads, bytes, st>>>(states, slot_elems, n_slots, src,
+                                                                                       dst, n, R);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace mhla
