@@ -302,8 +302,8 @@ mhla_path mhla_backward_path(int B, int H, int N, int d, int block_size, mhla_dt
  *   - Token tensors are [B, H, N, d] with any strides: an mhla_strides holds
  *     the element strides of b, h and n (d contiguous); NULL means dense
  *     row-major.  Strides are >= 0 and, like the pointers, multiples of 16
- *     bytes; an input may have stride 0 (a head shared by several), an output
- *     may not overlap itself.  So token-major tensors and slices of a fused
+ *     bytes; an input may have stride 0 in b and h (keys shared by several
+ *     heads), an output may not overlap itself.  So token-major tensors and slices of a fused
  *     projection are taken as they are.
  *   - cu_seqlens: NULL, or device int32 [B + 1]: then the tensors are
  *     [1, H, N, d] (the b strides are not used) and sequence i is the rows
@@ -458,8 +458,9 @@ unsigned long long mhla_launch_count(void);
 
 /* Diagnostic: sets the limit, in nanoseconds, of the bounded device-side
  * waits of the non-causal bf16 tensor-core kernels (every wait of the stream
- * path; the waits for the mixed summaries of the three-pass path) and of the
- * tensor-core passes of mhla_backward (every wait) for calls launched after it
+ * path; the waits for the mixed summaries of the three-pass path), of the
+ * tensor-core passes of mhla_backward and of those of retention_forward and
+ * retention_backward (every wait) for calls launched after it
  * (process
  * wide; 0 restores the default of 0.5 s).  With a limit too short for the
  * work in flight a call gives up: its output is incomplete, the kernel lets

@@ -488,3 +488,27 @@ def test_tensors_on_a_device_that_is_not_current():
     with torch.cuda.device(q.device):
         lib.retention_forward(q, k, v, gammas(2), y)
     check_forward(q, k, v, gammas(2), y, 1.0, "identity")
+
+
+def test_wait_limit_gives_up_then_the_next_call_is_right():
+    """With every device-side wait at its shortest the tensor-core passes give up and the status says so;
+    the same workspace serves the next call."""
+    H, N, d = 3, 4000, 64
+    q, k, v, dy = (rand((1, H, N, d), BF, i) for i in range(4))
+    g, y = torch.full((H,), 0.98, device="cuda"), torch.zeros(1, H, N, d, dtype=BF, device="cuda")
+    grads = [torch.zeros_like(q) for _ in range(3)]
+    ws = lib.new_workspace(lib.retention_workspace_bytes(1, H, N, d, backward=True), "cuda")
+    for call in (lambda: lib.retention_forward(q, k, v, g, y, workspace=ws),
+                 lambda: lib.retention_backward(q, k, v, g, dy, *grads, workspace=ws)):
+        binding.mhla_debug_set_wait_limit_ns(1)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            binding.mhla_debug_set_wait_limit_ns(0)
+        assert binding.mhla_query_status(ws) == binding.MHLA_ERR_TIMEOUT
+        assert binding.mhla_query_status(ws) == binding.MHLA_OK
+        call()
+        assert binding.mhla_query_status(ws) == binding.MHLA_OK
+    check_forward(q, k, v, g, y, 1.0, "identity")
+    check_backward(q, k, v, g, dy, grads, 1.0, "identity")

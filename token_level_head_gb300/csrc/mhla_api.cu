@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "retention.h"
 
 namespace mhla {
 
@@ -434,6 +435,7 @@ void mhla_debug_set_wait_limit_ns(unsigned long long ns) {
   tc_stream_set_wait_limit(ns);
   tc_mhla_set_wait_limit(ns);
   tc_backward_set_wait_limit(ns);
+  tc_retention_set_wait_limit(ns);
 }
 
 }  // extern "C"

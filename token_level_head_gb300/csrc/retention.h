@@ -51,8 +51,12 @@ struct RetArgs {
   unsigned* status;             // the workspace's status word
 };
 
-// ---- SIMT passes (fp32 arithmetic)
-cudaError_t simt_retention_launch(const RetArgs& a, mhla_dtype dt, cudaStream_t st);
+// ---- tensor-core passes (bf16)
+cudaError_t tc_retention_launch(const RetArgs& a, cudaStream_t st);
+// Limit of every bounded device-side wait of these (0 restores the default 0.5 s).
+void tc_retention_set_wait_limit(unsigned long long ns);
+// ---- SIMT passes (fp32)
+cudaError_t simt_retention_launch(const RetArgs& a, cudaStream_t st);
 // Turns the segments' own sums into the states entering them (both kernel families).
 cudaError_t retention_scan_launch(const RetArgs& a, cudaStream_t st);
 

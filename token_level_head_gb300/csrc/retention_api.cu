@@ -36,6 +36,7 @@ bool make_tensor(RetTensor* t, const void* p, const mhla_strides* st, const Exte
   const long long q = 16 / e.es, most = 1ll << 38;  // 2^40 bytes
   for (long long s : {t->sb, t->sh, t->sn})
     if (s < 0 || s % q != 0 || s >= most) return false;
+  if (t->sn == 0 && e.n > 1) return false;  // rows of their own, so that a tile can be loaded by TMA
   t->feature = MHLA_PHI_IDENTITY;
   return true;
 }
@@ -221,7 +222,8 @@ mhla_status retention_forward(const void* q, const mhla_strides* q_strides, cons
   a.slots = slots;
   a.n_slots = n_slots;
   a.load = load_state;
-  return from_cuda(simt_retention_launch(a, dt, static_cast<cudaStream_t>(stream)));
+  return from_cuda(dt == MHLA_BF16 ? tc_retention_launch(a, static_cast<cudaStream_t>(stream))
+                                   : simt_retention_launch(a, static_cast<cudaStream_t>(stream)));
 }
 
 mhla_status retention_backward(const void* q, const mhla_strides* q_strides, const void* k,
@@ -287,7 +289,8 @@ mhla_status retention_backward(const void* q, const mhla_strides* q_strides, con
   pv.reverse = 1;
   pv.sum = 1;
   pv.sum_t = 1;
-  return from_cuda(simt_retention_launch(a, dt, static_cast<cudaStream_t>(stream)));
+  return from_cuda(dt == MHLA_BF16 ? tc_retention_launch(a, static_cast<cudaStream_t>(stream))
+                                   : simt_retention_launch(a, static_cast<cudaStream_t>(stream)));
 }
 
 mhla_status retention_step(const void* q, const mhla_strides* q_strides, const void* k, const mhla_strides* k_strides,

@@ -1,4 +1,4 @@
-// Retention passes on the SIMT cores (fp32 arithmetic), the scan over segments, the single-token step
+// Retention passes of fp32 tensors on the SIMT cores, the scan over segments, the single-token step
 // and the copies between state slots.  The mathematics is in retention.h.
 #include <algorithm>
 
@@ -45,14 +45,14 @@ __device__ __forceinline__ void load_row_piece<__nv_bfloat16>(const __nv_bfloat1
 }
 
 // Rows 0 .. len - 1, columns c0 .. c0 + W - 1 of a tensor from row `row`, widened, phi applied; zeros behind.
-template <typename T, int W, int LDS>
+template <int W, int LDS>
 __device__ __forceinline__ void load_tile(float* dst, const RetTensor& t, long long base, int row, int len, int c0) {
-  const T* src = static_cast<const T*>(t.p) + base + (long long)row * t.sn + c0;
+  const float* src = static_cast<const float*>(t.p) + base + (long long)row * t.sn + c0;
   for (int i = threadIdx.x; i < kTok * (W / 4); i += kThreads) {
     const int r = i / (W / 4), c = (i % (W / 4)) * 4;
     float f[4] = {0.f, 0.f, 0.f, 0.f};
     if (r < len) {
-      load_row_piece<T>(src + (long long)r * t.sn + c, f);
+      load_row_piece<float>(src + (long long)r * t.sn + c, f);
       if (t.feature != kFeatIdentity)
 #pragma unroll
         for (int x = 0; x < 4; ++x) f[x] = ret_phi(f[x], t.feature);
@@ -61,7 +61,7 @@ __device__ __forceinline__ void load_tile(float* dst, const RetTensor& t, long l
   }
 }
 
-template <typename T, int D, bool SUM>
+template <int D, bool SUM>
 __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_constant__ RetArgs a) {
   using C = SimtTile<D>;
   extern __shared__ float4 smem4[];
@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
     const int ch = p.reverse ? nch - 1 - it : it;
     const int row = sg.row0 + ch * kTok, len = min(kTok, sg.len - ch * kTok);
     __syncthreads();
-    if (!SUM) load_tile<T, D, C::LD>(sA, p.a, ba, row, len, 0);
-    load_tile<T, D, C::LD>(sB, p.b, bb, row, len, 0);
-    load_tile<T, C::ES, C::ES>(sC, p.c, bc, row, len, e0);
+    if (!SUM) load_tile<D, C::LD>(sA, p.a, ba, row, len, 0);
+    load_tile<D, C::LD>(sB, p.b, bb, row, len, 0);
+    load_tile<C::ES, C::ES>(sC, p.c, bc, row, len, e0);
     if (tid < kTok) sW[tid] = tid < len ? decay_pow(lg, p.reverse ? tid : len - 1 - tid) : 0.f;
     __syncthreads();
     if (!SUM) {
@@ -191,15 +191,14 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
         for (int x = 0; x < 4; ++x) o[x] = a.scale * fmaf(w, ac[i][x], in[i][x]);
         if (p.x.p != nullptr) {
           float fx[4];
-          load_row_piece<T>(static_cast<const T*>(p.x.p) + ret_base(a, p.x, sg.seq, h) + (long long)(row + t) * p.x.sn +
+          load_row_piece<float>(static_cast<const float*>(p.x.p) + ret_base(a, p.x, sg.seq, h) + (long long)(row + t) * p.x.sn +
                                 e0 + 4 * tx, fx);
 #pragma unroll
           for (int x = 0; x < 4; ++x) o[x] *= ret_dphi(fx[x], p.x.feature);
         }
-        T* dst = static_cast<T*>(const_cast<void*>(p.out.p)) + ret_base(a, p.out, sg.seq, h) +
-                 (long long)(row + t) * p.out.sn + e0 + 4 * tx;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) dst[x] = from_f<T>(o[x]);
+        float* dst = static_cast<float*>(const_cast<void*>(p.out.p)) + ret_base(a, p.out, sg.seq, h) +
+                     (long long)(row + t) * p.out.sn + e0 + 4 * tx;
+        *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
       }
       __syncthreads();  // every A X has read X
     }
@@ -243,34 +242,24 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
     for (int i = tid; i < D * C::ES; i += kThreads) dst[(i / C::ES) * D + e0 + i % C::ES] = sX[i];
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_passes(const RetArgs& a, cudaStream_t st) {
   using C = SimtTile<D>;
   static SmemOptIn opt_sum, opt_out;
-  cudaError_t e = opt_sum.ensure((const void*)retention_simt_kernel<T, D, true>, (int)C::kBytes);
-  if (e == cudaSuccess) e = opt_out.ensure((const void*)retention_simt_kernel<T, D, false>, (int)C::kBytes);
+  cudaError_t e = opt_sum.ensure((const void*)retention_simt_kernel<D, true>, (int)C::kBytes);
+  if (e == cudaSuccess) e = opt_out.ensure((const void*)retention_simt_kernel<D, false>, (int)C::kBytes);
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)(a.G * a.H), D / C::ES, a.nsum);
   if (a.seg != nullptr) {
-    retention_simt_kernel<T, D, true><<<grid, kThreads, C::kBytes, st>>>(a);
+    retention_simt_kernel<D, true><<<grid, kThreads, C::kBytes, st>>>(a);
     note_launch();
     e = retention_scan_launch(a, st);
     if (e != cudaSuccess) return e;
   }
   grid.z = a.npass;
-  retention_simt_kernel<T, D, false><<<grid, kThreads, C::kBytes, st>>>(a);
+  retention_simt_kernel<D, false><<<grid, kThreads, C::kBytes, st>>>(a);
   note_launch();
   return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t launch_passes_d(const RetArgs& a, cudaStream_t st) {
-  switch (a.d) {
-    case 16: return launch_passes<T, 16>(a, st);
-    case 32: return launch_passes<T, 32>(a, st);
-    case 64: return launch_passes<T, 64>(a, st);
-    default: return launch_passes<T, 128>(a, st);
-  }
 }
 
 // ================================================================ scan
@@ -470,8 +459,13 @@ __global__ void __launch_bounds__(kThreads) retention_copy_kernel(float* states,
 
 }  // namespace
 
-cudaError_t simt_retention_launch(const RetArgs& a, mhla_dtype dt, cudaStream_t st) {
-  return dt == MHLA_F32 ? launch_passes_d<float>(a, st) : launch_passes_d<__nv_bfloat16>(a, st);
+cudaError_t simt_retention_launch(const RetArgs& a, cudaStream_t st) {
+  switch (a.d) {
+    case 16: return launch_passes<16>(a, st);
+    case 32: return launch_passes<32>(a, st);
+    case 64: return launch_passes<64>(a, st);
+    default: return launch_passes<128>(a, st);
+  }
 }
 
 cudaError_t retention_scan_launch(const RetArgs& a, cudaStream_t st) {
