@@ -11,9 +11,12 @@
 // inter is weighted by gamma^(len-i).
 //
 // What is rounded to bf16: the masked scores, the copy of X that the product reads (X itself stays
-// fp32), phi of operands with a feature map, and B w.  Where a call returns the final state in fp32, B w
-// is carried as a sum of two bf16 numbers (hi over the B tile, the remainder over the A tile), 2^-16 of
-// each term; where only bf16 outputs come of it, one is enough.
+// fp32) and phi of operands with a feature map.  B w is carried as a sum of bf16 numbers: of two (over
+// the B tile, the remainder over the A tile: 2^-16 of a term) where only bf16 outputs come of it, of
+// three (the last over the tile of X: 2^-24) where the call returns the final state in fp32.
+//
+// The roles' loops are kept short rather than unrolled: one warp a scheduler runs each of them, and with
+// whole rows unrolled the instruction fetch, not the arithmetic, set the pace (a chunk took 23,000 cycles).
 //
 // Roles (10 warps; D = 128: one CTA an SM, D = 64: two):
 //   warp 0     TMA producer: the A, B and C tiles of a chunk (2-stage ring)
@@ -62,12 +65,18 @@ struct Guard {
   unsigned long long limit;
 };
 __device__ __forceinline__ bool aborted(const Guard& g) { return *reinterpret_cast<volatile int*>(g.abort) != 0; }
+// The thread sleeps in the barrier's own wait; the clock is read only after about a microsecond of that.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* ab, unsigned long long limit) {
-  const uint64_t t0 = globaltimer_ns();
+  const uint32_t nap = limit < 1000 ? (uint32_t)limit : 1000u;
+  uint64_t t0 = 0;
   for (;;) {
-    if (mbar_try_wait_ns(bar, parity, 256)) return true;
+    if (mbar_try_wait_ns(bar, parity, nap)) return true;
     if (*reinterpret_cast<volatile int*>(ab) != 0) return false;
-    if (globaltimer_ns() - t0 > limit) break;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0)
+      t0 = now;
+    else if (now - t0 > limit)
+      break;
   }
   *reinterpret_cast<volatile int*>(ab) = 1;
   return false;
@@ -113,8 +122,8 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
 
 // phi over the d columns of row r of a tile in place, zeros for a row behind the sequence.
 template <int D>
-__device__ __forceinline__ void map_row(uint8_t* tile, int r, int len, int d, int feature) {
-#pragma unroll
+__device__ __noinline__ void map_row(uint8_t* tile, int r, int len, int d, int feature) {
+#pragma unroll 2
   for (int j = 0; j < D / 8; ++j) {
     uint4* p = piece(tile, kTok, r, j);
     if (r >= len) {
@@ -129,38 +138,48 @@ __device__ __forceinline__ void map_row(uint8_t* tile, int r, int len, int d, in
   }
 }
 
-// Row r of B times w, as bf16 over the B tile; with lo the remainder as bf16 there.  raw: the row in
-// global memory (d columns), where phi is applied to it anew in fp32 instead of reading the rounded
-// phi of the tile; null: the tile's values are taken.
+// f - bf16(f) in place, given bf16(f) packed.
+__device__ __forceinline__ void remainder8(float* f, uint4 h) {
+  float g[8];
+  unpack8(h, g);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) f[x] -= g[x];
+}
+
+// Row r of B times w as a sum of bf16 numbers: over the B tile, the remainder in lo, with lo2 the
+// remainder of that.  The row is read from raw (global memory, d columns) where given, else from the
+// tile; a feature map, if any, is applied to it in fp32.
 template <int D>
-__device__ __forceinline__ void weigh_row(uint8_t* hi, uint8_t* lo, int r, float w, const __nv_bfloat16* raw, int d,
-                                          int feature) {
+__device__ __forceinline__ void weigh_row(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, float w,
+                                          const __nv_bfloat16* raw, int d, int feature) {
+#pragma unroll 1
+  for (int j0 = 0; j0 < D / 8; j0 += 4) {
+    uint4 u[4];
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
-    uint4* p = piece(hi, kTok, r, j);
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (w != 0.f) {
-      if (raw == nullptr)
-        u = *p;
-      else if (8 * j < d)
-        u = *reinterpret_cast<const uint4*>(raw + 8 * j);
-    }
-    float f[8];
-    unpack8(u, f);
-    if (raw != nullptr) {
-#pragma unroll
-      for (int x = 0; x < 8; ++x) f[x] = w != 0.f && 8 * j < d ? ret_phi(f[x], feature) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      u[j] = *piece(hi, kTok, r, j0 + j);
+      if (raw != nullptr && 8 * (j0 + j) < d) u[j] = *reinterpret_cast<const uint4*>(raw + 8 * (j0 + j));
+      if (w == 0.f) u[j] = make_uint4(0, 0, 0, 0);  // rows behind the sequence, whatever they hold
     }
 #pragma unroll
-    for (int x = 0; x < 8; ++x) f[x] *= w;
-    const uint4 h = pack8(f);
-    *p = h;
-    if (lo != nullptr) {
-      float g[8];
-      unpack8(h, g);
+    for (int j = 0; j < 4; ++j) {
+      float f[8];
+      unpack8(u[j], f);
+      if (feature != kFeatIdentity && 8 * (j0 + j) < d) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) g[x] = f[x] - g[x];
-      *piece(lo, kTok, r, j) = pack8(g);
+        for (int x = 0; x < 8; ++x) f[x] = ret_phi(f[x], feature);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) f[x] *= w;
+      const uint4 h = pack8(f);
+      *piece(hi, kTok, r, j0 + j) = h;
+      remainder8(f, h);
+      const uint4 l = pack8(f);
+      *piece(lo, kTok, r, j0 + j) = l;
+      if (lo2 != nullptr) {
+        remainder8(f, l);
+        *piece(lo2, kTok, r, j0 + j) = pack8(f);
+      }
     }
   }
 }
@@ -189,7 +208,7 @@ struct PassTile {
   static constexpr int kOp = (D / 64) * kAtom;          // an operand's tile
   static constexpr int kStage = 3 * kOp;
   static constexpr int kOffX = kStages * kStage;        // bf16 X: D rows c, D columns e
-  static constexpr int kOffBars = kOffX + D * D * 2;
+  static constexpr int kOffBars = kOffX + kOp;          // (a tile's room: also the third part of B w)
   static constexpr uint32_t kCols = D == 128 ? 512 : 256;
   static constexpr uint32_t kColS = 0;                  // scores, P over their first half
   static constexpr uint32_t kColInter = 128, kColIntra = 128 + D;
@@ -213,13 +232,14 @@ struct PassBars {
   int abort;
   int issued;         // chunks whose loads the producer issued
   int scratch[34];
+  float decay[kTok];  // gamma^n
 };
 
 template <int D>
-constexpr size_t pass_smem() {
-  return 1024 + PassTile<D>::kOffBars + sizeof(PassBars);
+constexpr size_t pass_smem() {  // (the kernels' shared memory starts on 1024 bytes: no room to align it)
+  return PassTile<D>::kOffBars + sizeof(PassBars);
 }
-static_assert(pass_smem<128>() <= 232448 && pass_smem<64>() <= 232448 / 2 - 1024, "shared memory budget");
+static_assert(pass_smem<128>() <= 232448 && 2 * (pass_smem<64>() + 1024) <= 233472, "shared memory budget");
 
 // What the roles share.
 struct PassCtx {
@@ -229,9 +249,10 @@ struct PassCtx {
   uint32_t tmem;
   int z, h, seq, row0, len, n;   // pass, head, sequence, first row, tokens, chunks
   int nx;                        // chunks whose dX is needed
-  bool fixed;                    // some operand has a feature map
+  int reverse, terms;            // direction; bf16 numbers that B w is the sum of
+  bool mapped;                   // some operand has a feature map
   float lg;
-  __device__ __forceinline__ int chunk(const TcArgs& t, int i) const { return t.r.pass[z].reverse ? n - 1 - i : i; }
+  __device__ __forceinline__ int chunk(int i) const { return reverse ? n - 1 - i : i; }
   __device__ __forceinline__ int chunk_len(int ch) const { return min(kTok, len - ch * kTok); }
 };
 
@@ -240,7 +261,7 @@ __device__ __forceinline__ void pass_producer(const TcArgs& t, const PassCtx& c)
   using P = PassTile<D>;
   int i = 0;
   for (; i < c.n; ++i) {
-    const int s = i % kStages, row = c.row0 + c.chunk(t, i) * kTok;
+    const int s = i % kStages, row = c.row0 + c.chunk(i) * kTok;
     if (i >= kStages && !wait(&c.b->empty[s], ((i / kStages) - 1) & 1, c.g)) break;
     uint8_t* st = c.sm + s * P::kStage;
     mbar_arrive_expect_tx(&c.b->full[s], P::kStage);
@@ -252,17 +273,16 @@ __device__ __forceinline__ void pass_producer(const TcArgs& t, const PassCtx& c)
 }
 
 template <int D>
-__device__ __forceinline__ void pass_mma(const TcArgs& t, const PassCtx& c) {
+__device__ __forceinline__ void pass_mma(const PassCtx& c) {
   using P = PassTile<D>;
   PassBars* b = c.b;
-  const bool lo = t.r.states != nullptr;
   int maps = 0;
   for (int i = 0; i < c.n; ++i) {
     const int s = i % kStages;
     const uint32_t a0 = smem_u32(c.sm + s * P::kStage), b0 = a0 + P::kOp, c0 = b0 + P::kOp;
     if (!wait(&b->full[s], (i / kStages) & 1, c.g)) return;
     if (i > 0 && !wait(&b->o_full, (i - 1) & 1, c.g)) return;  // the scores go over P of the last chunk
-    if (c.fixed || c.chunk_len(c.chunk(t, i)) < kTok) {
+    if (c.mapped || c.chunk_len(c.chunk(i)) < kTok) {
       if (!wait(&b->mapped, maps & 1, c.g)) return;
       ++maps;
     }
@@ -301,7 +321,8 @@ __device__ __forceinline__ void pass_mma(const TcArgs& t, const PassCtx& c) {
       if (!wait(&b->w_full, i & 1, c.g)) return;
       tc_fence_after();
       mma_outer<D, D>(c.tmem + P::kColDX, b0, c0, false);
-      if (lo) mma_outer<D, D>(c.tmem + P::kColDX, a0, c0, true);
+      mma_outer<D, D>(c.tmem + P::kColDX, a0, c0, true);
+      if (c.terms > 2) mma_outer<D, D>(c.tmem + P::kColDX, smem_u32(c.sm + P::kOffX), c0, true);
       mma_commit(&b->dx_full);
     }
     mma_commit(&b->empty[s]);
@@ -314,35 +335,48 @@ __device__ __forceinline__ void pass_out(const TcArgs& t, const PassCtx& c, int 
   using P = PassTile<D>;
   PassBars* b = c.b;
   const RetPass& p = t.r.pass[c.z];
-  const int qd = warp & 3, row = 32 * qd + lane;
+  const int qd = warp & 3, row = 32 * qd + lane, d = t.r.d;
   const uint32_t tl = c.tmem + ((uint32_t)(32 * qd) << 16);
-  // gamma^|t-s| of a block of 32 columns off the diagonal = gamma^(rows to its near edge) * col[x]
-  float col[32];
-#pragma unroll
-  for (int x = 0; x < 32; ++x) col[x] = decay_pow(c.lg, p.reverse ? x : 31 - x);
+  const float scale = t.r.scale;
+  const bool wide = t.wide_out[c.z] != 0;
+  const long long sn = p.out.sn, xsn = p.x.sn;
+  const int xf = p.x.feature;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + ret_base(t.r, p.out, c.seq, c.h);
+  const __nv_bfloat16* xin = static_cast<const __nv_bfloat16*>(p.x.p);
+  if (xin != nullptr) xin += ret_base(t.r, p.x, c.seq, c.h);
+#pragma unroll 1
   for (int i = 0; i < c.n; ++i) {
-    const int ch = c.chunk(t, i), len = c.chunk_len(ch);
+    const int ch = c.chunk(i), len = c.chunk_len(ch);
     if (!wait_warp(&b->s_full, i & 1, c.g)) return;
     tc_fence_after();
     // block j of scores lies in columns 32 j .., its P in 16 j ..: never over scores still to be read
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < 4; ++j) {
       uint32_t w[16];
-      const bool diag = j == qd;
-      if (p.reverse ? j < qd : j > qd) {
+      if (c.reverse ? j < qd : j > qd) {
 #pragma unroll
         for (int x = 0; x < 16; ++x) w[x] = 0;
       } else {
         float v[32];
         tmem_ld16(tl + P::kColS + 32 * j, v);
         tmem_ld16(tl + P::kColS + 32 * j + 16, v + 16);
-        tmem_ld_wait();
-        const float r = diag ? 0.f : decay_pow(c.lg, p.reverse ? 32 * j - row : row - 32 * j - 31);
+        // gamma^|t-s|; on the diagonal block the entries of the wrong sign are read beside the table and dropped
+        const int n = row - 32 * j;
+        float f[32];
+        if (c.reverse) {
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const int n = p.reverse ? x - lane : lane - x;
-          const float f = diag ? decay_pow(c.lg, max(n, 0)) : r * col[x];
-          v[x] = (!diag || n >= 0) && 32 * j + x < len ? v[x] * f : 0.f;
+          for (int x = 0; x < 32; ++x) f[x] = b->decay[x - n];
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) f[x] = b->decay[n - x];
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) v[x] *= f[x];
+        if (j == qd) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (c.reverse ? x < lane : x > lane) v[x] = 0.f;
         }
 #pragma unroll
         for (int x = 0; x < 16; ++x) w[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
@@ -356,38 +390,34 @@ __device__ __forceinline__ void pass_out(const TcArgs& t, const PassCtx& c, int 
 
     const bool live = row < len;
     const long long at = (long long)(c.row0 + ch * kTok + row);
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + ret_base(t.r, p.out, c.seq, c.h) +
-                         at * p.out.sn;
-    const __nv_bfloat16* xp = static_cast<const __nv_bfloat16*>(p.x.p);
-    if (xp != nullptr) xp += ret_base(t.r, p.x, c.seq, c.h) + at * p.x.sn;
-    const float wi = t.r.scale * decay_pow(c.lg, p.reverse ? max(len - row, 0) : row + 1);
+    __nv_bfloat16* dst = out + at * sn;
+    const __nv_bfloat16* xp = xin == nullptr ? nullptr : xin + at * xsn;
+    const float wi = scale * decay_pow(c.lg, c.reverse ? max(len - row, 0) : row + 1);
     if (!wait_warp(&b->o_full, i & 1, c.g)) return;
     tc_fence_after();
-#pragma unroll
-    for (int g = 0; g < D / 16; ++g) {
-      if (16 * g >= t.r.d) break;
+#pragma unroll 1
+    for (int g = 0; g < d; g += 16) {
       float u[16], v[16];
-      tmem_ld16(tl + P::kColInter + 16 * g, u);
-      tmem_ld16(tl + P::kColIntra + 16 * g, v);
+      tmem_ld16(tl + P::kColInter + g, u);
+      tmem_ld16(tl + P::kColIntra + g, v);
       tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 16; ++x) v[x] = fmaf(wi, u[x], scale * v[x]);
       if (live) {
-#pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = fmaf(wi, u[x], t.r.scale * v[x]);
         if (xp != nullptr) {
-          float f[16];
-          unpack8(*reinterpret_cast<const uint4*>(xp + 16 * g), f);
-          unpack8(*reinterpret_cast<const uint4*>(xp + 16 * g + 8), f + 8);
+          unpack8(*reinterpret_cast<const uint4*>(xp + g), u);
+          unpack8(*reinterpret_cast<const uint4*>(xp + g + 8), u + 8);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] *= ret_dphi(f[x], p.x.feature);
+          for (int x = 0; x < 16; ++x) v[x] *= ret_dphi(u[x], xf);
         }
         const uint4 lo8 = pack8(v), hi8 = pack8(v + 8);
-        if (t.wide_out[c.z]) {  // one whole 32-byte sector a store
-          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * g), "r"(lo8.x), "r"(lo8.y),
+        if (wide) {  // one whole 32-byte sector a store
+          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + g), "r"(lo8.x), "r"(lo8.y),
                        "r"(lo8.z), "r"(lo8.w), "r"(hi8.x), "r"(hi8.y), "r"(hi8.z), "r"(hi8.w)
                        : "memory");
         } else {
-          *reinterpret_cast<uint4*>(dst + 16 * g) = lo8;
-          *reinterpret_cast<uint4*>(dst + 16 * g + 8) = hi8;
+          *reinterpret_cast<uint4*>(dst + g) = lo8;
+          *reinterpret_cast<uint4*>(dst + g + 8) = hi8;
         }
       }
       __syncwarp();  // the TMEM loads are the whole warp's
@@ -409,8 +439,9 @@ __device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, in
   const int qd = warp & 3, row = 32 * qd + lane, d = t.r.d;
   const int xr = D == 128 ? row : 16 * qd + lane;           // row of X
   const bool has = (D == 128 || lane < 16) && xr < d;
-  const bool lo = t.r.states != nullptr;
   const uint32_t tl = c.tmem + ((uint32_t)(32 * qd) << 16);
+  const int fa = p.a.feature, fb = p.b.feature, fc = p.c.feature;
+  const bool anew = c.terms > 2 && fb != kFeatIdentity;  // phi(b) in fp32 for the state
   uint8_t* xt = c.sm + P::kOffX;
   float X[D];
 #pragma unroll
@@ -438,14 +469,14 @@ __device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, in
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->x_full);
   };
-  auto map = [&](int i) -> bool {  // feature maps of chunk i, rows behind the sequence cleared in C
-    const int len = c.chunk_len(c.chunk(t, i));
-    if (!c.fixed && len == kTok) return true;
+  auto map = [&](int i) -> bool {  // feature maps of chunk i, rows behind the sequence cleared in B and C
+    const int len = c.chunk_len(c.chunk(i));
+    if (!c.mapped && len == kTok) return true;
     if (!wait_warp(&b->full[i % kStages], (i / kStages) & 1, c.g)) return false;
     uint8_t* st = c.sm + (i % kStages) * P::kStage;
-    if (p.a.feature != kFeatIdentity) map_row<D>(st, row, len, d, p.a.feature);
-    if (p.b.feature != kFeatIdentity) map_row<D>(st + P::kOp, row, len, d, p.b.feature);
-    map_row<D>(st + 2 * P::kOp, row, len, d, p.c.feature);
+    if (fa != kFeatIdentity) map_row<D>(st, row, kTok, d, fa);
+    if (fb != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, d, fb);
+    if (fc != kFeatIdentity || len < kTok) map_row<D>(st + 2 * P::kOp, row, len, d, fc);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->mapped);
@@ -453,17 +484,19 @@ __device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, in
   };
   if (!map(0)) return;
   publish();
+#pragma unroll 1
   for (int i = 0; i < c.nx; ++i) {
-    const int ch = c.chunk(t, i), len = c.chunk_len(ch);
+    const int ch = c.chunk(i), len = c.chunk_len(ch);
     uint8_t* st = c.sm + (i % kStages) * P::kStage;
     // B has been read by the scores, A (and the old X) by inter
     if (!wait_warp(&b->s_full, i & 1, c.g) || !wait_warp(&b->in_full, i & 1, c.g)) return;
-    const float w = row < len ? decay_pow(c.lg, p.reverse ? row : len - 1 - row) : 0.f;
+    const float w = row < len ? b->decay[c.reverse ? row : len - 1 - row] : 0.f;
     const __nv_bfloat16* raw = nullptr;
-    if (lo && p.b.feature != kFeatIdentity && row < len)
+    if (anew && row < len)
       raw = static_cast<const __nv_bfloat16*>(p.b.p) + ret_base(t.r, p.b, c.seq, c.h) +
             (long long)(c.row0 + ch * kTok + row) * p.b.sn;
-    weigh_row<D>(st + P::kOp, lo ? st : nullptr, row, w, raw, d, p.b.feature);
+    // (without fp32 states the tile's rounded phi is good enough)
+    weigh_row<D>(st + P::kOp, st, c.terms > 2 ? xt : nullptr, row, w, raw, d, anew ? fb : kFeatIdentity);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->w_full);
@@ -491,9 +524,9 @@ __device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, in
 template <int D>
 __global__ void __launch_bounds__(kThreads, PassTile<D>::kPerSm) retention_pass_kernel(const __grid_constant__ TcArgs t) {
   using P = PassTile<D>;
-  extern __shared__ uint8_t smraw[];
+  extern __shared__ __align__(1024) uint8_t smraw[];
   PassCtx c;
-  c.sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  c.sm = smraw;
   c.b = reinterpret_cast<PassBars*>(c.sm + P::kOffBars);
   PassBars* b = c.b;
   const RetArgs& r = t.r;
@@ -514,6 +547,11 @@ __global__ void __launch_bounds__(kThreads, PassTile<D>::kPerSm) retention_pass_
     b->abort = 0;
     b->issued = 0;
     fence_mbar_init();
+  }
+  c.lg = decay_log2(r.gamma[c.h]);
+  if (threadIdx.x >= kThreads - kTok) {
+    const int n = threadIdx.x - (kThreads - kTok);
+    b->decay[n] = decay_pow(c.lg, n);
   }
   if (warp == kWarpMma) {
     tmem_alloc(&b->tbase, P::kCols);
@@ -537,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, PassTile<D>::kPerSm) retention_pass_
   const size_t dd = (size_t)r.d * r.d;
   float* to = slot >= 0 && sg.seg == sg.nseg - 1 ? r.states + ((size_t)slot * r.H + c.h) * dd : nullptr;
   c.nx = to != nullptr ? c.n : c.n - 1;
-  c.fixed = p.a.feature != kFeatIdentity || p.b.feature != kFeatIdentity || p.c.feature != kFeatIdentity;
-  c.lg = decay_log2(r.gamma[c.h]);
+  c.reverse = p.reverse;
+  c.terms = r.states != nullptr ? 3 : 2;
+  c.mapped = p.a.feature != kFeatIdentity || p.b.feature != kFeatIdentity || p.c.feature != kFeatIdentity;
   const float* from = nullptr;
   if (sg.nseg > 1)
     from = r.seg + (((size_t)p.sum * r.G + g) * r.H + c.h) * dd;
@@ -550,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, PassTile<D>::kPerSm) retention_pass_
     __syncwarp();
   } else if (warp == kWarpMma) {
     if (lane == 0) {
-      pass_mma<D>(t, c);
+      pass_mma<D>(c);
       mma_commit(&b->fin);
     }
     __syncwarp();
@@ -578,8 +617,9 @@ __global__ void __launch_bounds__(kThreads, PassTile<D>::kPerSm) retention_pass_
 template <int D>
 struct SumTile {
   static constexpr int kOp = (D / 64) * kAtom;
-  static constexpr int kStage = 3 * kOp;                // B, C, the remainders of B w
-  static constexpr int kOffBars = kStages * kStage;
+  static constexpr int kStage = 2 * kOp;                // B, C
+  static constexpr int kOffLo = kStages * kStage;       // the second and third part of B w
+  static constexpr int kOffBars = kOffLo + 2 * kOp;
 };
 
 constexpr int kSumThreads = 192;                         // producer, MMA issuer, 4 warps for the rest
@@ -595,15 +635,15 @@ struct SumBars {
 
 template <int D>
 constexpr size_t sum_smem() {
-  return 1024 + SumTile<D>::kOffBars + sizeof(SumBars);
+  return SumTile<D>::kOffBars + sizeof(SumBars);
 }
-static_assert(sum_smem<128>() <= 232448 && sum_smem<64>() <= 232448 / 2 - 1024, "shared memory budget");
+static_assert(sum_smem<128>() <= 232448 && 2 * (sum_smem<64>() + 1024) <= 233472, "shared memory budget");
 
 template <int D>
 __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid_constant__ TcArgs t) {
   using P = SumTile<D>;
-  extern __shared__ uint8_t smraw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smraw[];
+  uint8_t* sm = smraw;
   SumBars* b = reinterpret_cast<SumBars*>(sm + P::kOffBars);
   const RetArgs& r = t.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -639,7 +679,8 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
   const Guard gd{&b->abort, t.wait_ns};
   const uint32_t tmem = b->tbase;
   const int n = (sg.len + kTok - 1) / kTok;
-  const bool lo = r.states != nullptr;
+  const int terms = r.states != nullptr ? 3 : 2;
+  uint8_t* lo = sm + P::kOffLo;
 
   if (warp == kWarpProd) {
     if (lane == 0) {
@@ -663,7 +704,8 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
         tc_fence_after();
         const uint32_t b0 = smem_u32(sm + s * P::kStage);
         mma_outer<D, D>(tmem, b0, b0 + P::kOp, i > 0);
-        if (lo) mma_outer<D, D>(tmem, b0 + 2 * P::kOp, b0 + P::kOp, true);
+        mma_outer<D, D>(tmem, smem_u32(lo), b0 + P::kOp, true);
+        if (terms > 2) mma_outer<D, D>(tmem, smem_u32(lo) + P::kOp, b0 + P::kOp, true);
         mma_commit(&b->empty[s]);
       }
       mma_commit(&b->fin);
@@ -678,12 +720,12 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
       ok = wait_warp(&b->full[s], (i / kStages) & 1, gd);
       if (!ok) break;
       uint8_t* st = sm + s * P::kStage;
+      // the remainders' tiles have been read by the MMAs of the chunk before
+      if (i > 0) ok = wait_warp(&b->empty[(i - 1) % kStages], ((i - 1) / kStages) & 1, gd);
+      if (!ok) break;
       if (p.c.feature != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, r.d, p.c.feature);
       const float w = row < len ? decay_pow(lg, p.reverse ? at : sg.len - 1 - at) : 0.f;
-      const __nv_bfloat16* raw = nullptr;
-      if (p.b.feature != kFeatIdentity && row < len)
-        raw = static_cast<const __nv_bfloat16*>(p.b.p) + ret_base(r, p.b, sg.seq, h) + (long long)(sg.row0 + at) * p.b.sn;
-      weigh_row<D>(st, lo ? st + 2 * P::kOp : nullptr, row, w, raw, r.d, p.b.feature);
+      weigh_row<D>(st, lo, terms > 2 ? lo + P::kOp : nullptr, row, w, nullptr, r.d, p.b.feature);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->ready[s]);
