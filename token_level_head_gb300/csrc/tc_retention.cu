@@ -13,16 +13,18 @@
 // What is rounded to bf16: the masked scores, the copy of X that the product reads (X itself stays
 // fp32) and phi of operands with a feature map.  B w is carried as a sum of bf16 numbers: of two (over
 // the B tile, the remainder over the A tile: 2^-16 of a term) where only bf16 outputs come of it, of
-// three (the last over the tile of X: 2^-24) where the call returns the final state in fp32.
+// three (the last over the tile of X: 2^-24) in the segment whose state is returned in fp32.
 //
 // The roles' loops are kept short rather than unrolled: one warp a scheduler runs each of them, and with
 // whole rows unrolled the instruction fetch, not the arithmetic, set the pace (a chunk took 23,000 cycles).
 //
-// Roles (10 warps; D = 128: one CTA an SM, D = 64: two):
+// Roles (D = 128: 18 warps and one CTA an SM, D = 64: 10 warps and two):
 //   warp 0     TMA producer: the A, B and C tiles of a chunk (2-stage ring)
 //   warp 1     MMA issuer
-//   warps 2-5  scores -> P, then out = scale (intra + gamma^(i+1) inter) to global memory
-//   warps 6-9  feature maps in place, B w over B, and X: registers, and its bf16 tile for the next chunk
+//   out warps  scores -> P, then out = scale (intra + gamma^(i+1) inter) to global memory
+//   X warps    feature maps in place, B w over B, and X: registers, and its bf16 tile for the next chunk
+// Four out and four X warps take a row each thread; with D = 128 there are twice as many and two threads
+// share a row, half of the columns each (X then takes 64 registers a thread, not 128).
 // All waits are bounded: on time-out the kernel sets the status word and winds down.
 //
 // A sequence of several segments needs the states that enter them: retention_sum_kernel forms each
@@ -44,8 +46,7 @@ using namespace tc;
 
 constexpr int kTok = 128;                    // tokens of a chunk
 constexpr int kAtom = kTok * 128;            // 16 KB: 128 rows x 64 bf16, 128-byte swizzle
-constexpr int kThreads = 320;
-constexpr int kWarpProd = 0, kWarpMma = 1, kWarpX = 6;
+constexpr int kWarpProd = 0, kWarpMma = 1, kWarpOut = 2;
 constexpr int kStages = 2;
 constexpr uint64_t kWaitLimitNs = 500000000ull;
 unsigned long long g_wait_ns = kWaitLimitNs;
@@ -63,26 +64,29 @@ struct TcArgs {
 struct Guard {
   int* abort;
   unsigned long long limit;
+  uint32_t nap;  // ns of one sleep
 };
+__device__ __forceinline__ Guard make_guard(int* abort, unsigned long long limit) {
+  return {abort, limit, limit < 1000 ? (uint32_t)limit : 1000u};
+}
 __device__ __forceinline__ bool aborted(const Guard& g) { return *reinterpret_cast<volatile int*>(g.abort) != 0; }
 // The thread sleeps in the barrier's own wait; the clock is read only after about a microsecond of that.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* ab, unsigned long long limit) {
-  const uint32_t nap = limit < 1000 ? (uint32_t)limit : 1000u;
+// (Inline: a call would save the caller's registers, and most waits do wait.)
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Guard& g) {
+  if (mbar_test(bar, parity)) return true;
   uint64_t t0 = 0;
+#pragma unroll 1
   for (;;) {
-    if (mbar_try_wait_ns(bar, parity, nap)) return true;
-    if (*reinterpret_cast<volatile int*>(ab) != 0) return false;
+    if (mbar_try_wait_ns(bar, parity, g.nap)) return true;
+    if (aborted(g)) return false;
     const uint64_t now = globaltimer_ns();
     if (t0 == 0)
       t0 = now;
-    else if (now - t0 > limit)
+    else if (now - t0 > g.limit)
       break;
   }
-  *reinterpret_cast<volatile int*>(ab) = 1;
+  *reinterpret_cast<volatile int*>(g.abort) = 1;
   return false;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Guard& g) {
-  return mbar_test(bar, parity) || wait_slow(bar, parity, g.abort, g.limit);
 }
 // The whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Guard& g) {
@@ -120,11 +124,12 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-// phi over the d columns of row r of a tile in place, zeros for a row behind the sequence.
+// phi over D of the columns, from 8 j0, of row r of a tile in place (those below d), zeros for a row behind
+// the sequence.
 template <int D>
-__device__ __noinline__ void map_row(uint8_t* tile, int r, int len, int d, int feature) {
+__device__ __noinline__ void map_row(uint8_t* tile, int r, int j0, int len, int d, int feature) {
 #pragma unroll 2
-  for (int j = 0; j < D / 8; ++j) {
+  for (int j = j0; j < j0 + D / 8; ++j) {
     uint4* p = piece(tile, kTok, r, j);
     if (r >= len) {
       *p = make_uint4(0, 0, 0, 0);
@@ -146,41 +151,54 @@ __device__ __forceinline__ void remainder8(float* f, uint4 h) {
   for (int x = 0; x < 8; ++x) f[x] -= g[x];
 }
 
-// Row r of B times w as a sum of bf16 numbers: over the B tile, the remainder in lo, with lo2 the
-// remainder of that.  The row is read from raw (global memory, d columns) where given, else from the
-// tile; a feature map, if any, is applied to it in fp32.
-template <int D>
-__device__ __forceinline__ void weigh_row(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, float w,
-                                          const __nv_bfloat16* raw, int d, int feature) {
+// f[0..8) as a sum of bf16 numbers at piece j of row r: over the B tile, the remainder in lo, with T = 3 the
+// remainder of that in lo2.
+template <int T>
+__device__ __forceinline__ void split8(float* f, uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int j) {
+  const uint4 h = pack8(f);
+  *piece(hi, kTok, r, j) = h;
+  remainder8(f, h);
+  const uint4 l = pack8(f);
+  *piece(lo, kTok, r, j) = l;
+  if (T > 2) {
+    remainder8(f, l);
+    *piece(lo2, kTok, r, j) = pack8(f);
+  }
+}
+
+// D columns, from 8 jb, of row r of B times w, split.  w = 0: zeros, whatever the tile holds.
+template <int D, int T>
+__device__ __forceinline__ void weigh_row(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w) {
 #pragma unroll 1
-  for (int j0 = 0; j0 < D / 8; j0 += 4) {
-    uint4 u[4];
+  for (int j0 = jb; j0 < jb + D / 8; j0 += 2) {
+    uint4 u[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u[j] = *piece(hi, kTok, r, j0 + j);
-      if (raw != nullptr && 8 * (j0 + j) < d) u[j] = *reinterpret_cast<const uint4*>(raw + 8 * (j0 + j));
-      if (w == 0.f) u[j] = make_uint4(0, 0, 0, 0);  // rows behind the sequence, whatever they hold
-    }
+    for (int j = 0; j < 2; ++j) u[j] = *piece(hi, kTok, r, j0 + j);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       float f[8];
-      unpack8(u[j], f);
-      if (feature != kFeatIdentity && 8 * (j0 + j) < d) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) f[x] = ret_phi(f[x], feature);
-      }
+      unpack8(w == 0.f ? make_uint4(0, 0, 0, 0) : u[j], f);
 #pragma unroll
       for (int x = 0; x < 8; ++x) f[x] *= w;
-      const uint4 h = pack8(f);
-      *piece(hi, kTok, r, j0 + j) = h;
-      remainder8(f, h);
-      const uint4 l = pack8(f);
-      *piece(lo, kTok, r, j0 + j) = l;
-      if (lo2 != nullptr) {
-        remainder8(f, l);
-        *piece(lo2, kTok, r, j0 + j) = pack8(f);
-      }
+      split8<T>(f, hi, lo, lo2, r, j0 + j);
     }
+  }
+}
+
+// The same of phi of the row, in fp32, over its d columns: of the row in global memory (raw) where the tile
+// holds the rounded phi already.
+template <int D, int T>
+__device__ __noinline__ void weigh_phi_row(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w,
+                                           const __nv_bfloat16* raw, int d, int feature) {
+#pragma unroll 1
+  for (int j = jb; j < jb + D / 8; ++j) {
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (w != 0.f && 8 * j < d) {
+      unpack8(raw != nullptr ? *reinterpret_cast<const uint4*>(raw + 8 * j) : *piece(hi, kTok, r, j), f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) f[x] = w * ret_phi(f[x], feature);
+    }
+    split8<T>(f, hi, lo, lo2, r, j);
   }
 }
 
@@ -195,11 +213,10 @@ __device__ __forceinline__ void mma_outer(uint32_t d, uint32_t a, uint32_t b, bo
 
 // TMA of one operand's chunk: D / 64 atoms.
 template <int D>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const TcArgs& t, int map, int row, int h, int seq,
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int row, int h, int seq,
                                           uint64_t* bar) {
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c)
-    tma_load_4d(dst + c * kAtom, &t.tm[map], 64 * c, row, t.by_h[map] ? h : 0, t.by_b[map] ? seq : 0, bar);
+  for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * kAtom, map, 64 * c, row, h, seq, bar);
 }
 
 // ================================================================ pass
@@ -214,25 +231,55 @@ struct PassTile {
   static constexpr uint32_t kColInter = 128, kColIntra = 128 + D;
   static constexpr uint32_t kColDX = D == 128 ? 384 : 64;  // D = 64: over the scores that P leaves free
   static constexpr int kPerSm = D == 128 ? 1 : 2;
+  static constexpr int kSplit = D / 64;                 // threads that share a row
+  static constexpr int kWarpX = kWarpOut + 4 * kSplit;
+  static constexpr int kThreads = 32 * (kWarpX + 4 * kSplit);
 };
+
+// What the roles share.  It is kept in shared memory and the roles are functions of their own, so that none
+// holds registers for another.
+struct PassCtx {
+  const CUtensorMap *ma, *mb, *mc;
+  int ha, hb, hc, ba, bb, bc;    // head and batch coordinates in the maps
+  int row0, len, n;              // first row, tokens, chunks
+  int nx;                        // chunks whose dX is needed
+  int reverse, terms;            // direction; bf16 numbers that B w is the sum of
+  int fa, fb, fc, fx;            // feature maps of A, B, C and x
+  int d, wide;
+  int from_t;
+  float lg, scale;
+  __nv_bfloat16* out;            // of the head; rows out_n apart
+  const __nv_bfloat16 *x, *b;    // of the head: x (null: none), B
+  long long out_n, x_n, b_n;
+  const float* from;             // state entering the segment, null: zero
+  float* to;                     // where the state after it goes, null: nowhere
+  unsigned long long wait_ns;
+  __device__ __forceinline__ bool mapped() const {
+    return fa != kFeatIdentity || fb != kFeatIdentity || fc != kFeatIdentity;
+  }
+};
+__device__ __forceinline__ int chunk_of(int i, int n, int reverse) { return reverse ? n - 1 - i : i; }
+__device__ __forceinline__ int chunk_len(int ch, int len) { return min(kTok, len - ch * kTok); }
 
 struct PassBars {
   uint64_t full[kStages], empty[kStages];
-  uint64_t mapped;    // feature maps applied / rows behind the sequence cleared (4 X warps)
+  uint64_t mapped;    // feature maps applied / rows behind the sequence cleared (X warps)
   uint64_t s_full;    // scores
   uint64_t in_full;   // inter
-  uint64_t p_full;    // P in TMEM (4 out warps)
-  uint64_t w_full;    // B w (4 X warps)
+  uint64_t read[4];   // D = 128: a quadrant's scores read by both its out warps
+  uint64_t p_full;    // P in TMEM (out warps)
+  uint64_t w_full;    // B w (X warps)
   uint64_t dx_full;   // dX
-  uint64_t x_full;    // the bf16 tile of X (4 X warps)
+  uint64_t x_full;    // the bf16 tile of X (X warps)
   uint64_t o_full;    // intra
-  uint64_t o_free;    // inter and intra read (4 out warps)
+  uint64_t o_free;    // inter and intra read (out warps)
   uint64_t fin;       // every MMA of the CTA has completed
   uint32_t tbase;
   int abort;
   int issued;         // chunks whose loads the producer issued
-  int scratch[34];
-  float decay[kTok];  // gamma^n
+  // gamma^n, 32 zeros beside it: forward [32 + n], reverse [kTok - 1 - n] (first the segment search's scratch)
+  float decay[kTok + 32];
+  PassCtx ctx;
 };
 
 template <int D>
@@ -241,186 +288,232 @@ constexpr size_t pass_smem() {  // (the kernels' shared memory starts on 1024 by
 }
 static_assert(pass_smem<128>() <= 232448 && 2 * (pass_smem<64>() + 1024) <= 233472, "shared memory budget");
 
-// What the roles share.
-struct PassCtx {
-  uint8_t* sm;
-  PassBars* b;
-  Guard g;
-  uint32_t tmem;
-  int z, h, seq, row0, len, n;   // pass, head, sequence, first row, tokens, chunks
-  int nx;                        // chunks whose dX is needed
-  int reverse, terms;            // direction; bf16 numbers that B w is the sum of
-  bool mapped;                   // some operand has a feature map
-  float lg;
-  __device__ __forceinline__ int chunk(int i) const { return reverse ? n - 1 - i : i; }
-  __device__ __forceinline__ int chunk_len(int ch) const { return min(kTok, len - ch * kTok); }
-};
-
 template <int D>
-__device__ __forceinline__ void pass_producer(const TcArgs& t, const PassCtx& c) {
+__device__ __noinline__ void pass_producer(uint8_t* sm, PassBars* b) {
   using P = PassTile<D>;
+  const PassCtx c = b->ctx;
+  const Guard gd = make_guard(&b->abort, c.wait_ns);
   int i = 0;
   for (; i < c.n; ++i) {
-    const int s = i % kStages, row = c.row0 + c.chunk(i) * kTok;
-    if (i >= kStages && !wait(&c.b->empty[s], ((i / kStages) - 1) & 1, c.g)) break;
-    uint8_t* st = c.sm + s * P::kStage;
-    mbar_arrive_expect_tx(&c.b->full[s], P::kStage);
-    load_tile<D>(st, t, t.ia[c.z], row, c.h, c.seq, &c.b->full[s]);
-    load_tile<D>(st + P::kOp, t, t.ib[c.z], row, c.h, c.seq, &c.b->full[s]);
-    load_tile<D>(st + 2 * P::kOp, t, t.ic[c.z], row, c.h, c.seq, &c.b->full[s]);
+    const int s = i % kStages, row = c.row0 + chunk_of(i, c.n, c.reverse) * kTok;
+    if (i >= kStages && !wait(&b->empty[s], ((i / kStages) - 1) & 1, gd)) break;
+    uint8_t* st = sm + s * P::kStage;
+    mbar_arrive_expect_tx(&b->full[s], P::kStage);
+    load_tile<D>(st, c.ma, row, c.ha, c.ba, &b->full[s]);
+    load_tile<D>(st + P::kOp, c.mb, row, c.hb, c.bb, &b->full[s]);
+    load_tile<D>(st + 2 * P::kOp, c.mc, row, c.hc, c.bc, &b->full[s]);
   }
-  c.b->issued = i;
+  b->issued = i;
 }
 
 template <int D>
-__device__ __forceinline__ void pass_mma(const PassCtx& c) {
+__device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
   using P = PassTile<D>;
-  PassBars* b = c.b;
+  const int n = b->ctx.n, nx = b->ctx.nx, len = b->ctx.len, reverse = b->ctx.reverse, terms = b->ctx.terms;
+  const bool mapped = b->ctx.mapped();
+  const uint32_t tmem = b->tbase, xt = smem_u32(sm + P::kOffX);
+  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
   int maps = 0;
-  for (int i = 0; i < c.n; ++i) {
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
     const int s = i % kStages;
-    const uint32_t a0 = smem_u32(c.sm + s * P::kStage), b0 = a0 + P::kOp, c0 = b0 + P::kOp;
-    if (!wait(&b->full[s], (i / kStages) & 1, c.g)) return;
-    if (i > 0 && !wait(&b->o_full, (i - 1) & 1, c.g)) return;  // the scores go over P of the last chunk
-    if (c.mapped || c.chunk_len(c.chunk(i)) < kTok) {
-      if (!wait(&b->mapped, maps & 1, c.g)) return;
+    const uint32_t a0 = smem_u32(sm + s * P::kStage), b0 = a0 + P::kOp, c0 = b0 + P::kOp;
+    if (!wait(&b->full[s], (i / kStages) & 1, gd)) return;
+    if (i > 0 && !wait(&b->o_full, (i - 1) & 1, gd)) return;  // the scores go over P of the last chunk
+    if (mapped || chunk_len(chunk_of(i, n, reverse), len) < kTok) {
+      if (!wait(&b->mapped, maps & 1, gd)) return;
       ++maps;
     }
     // D = 64: dX lies over the scores; X of this chunk is there once it has been read
-    if (D == 64 && !wait(&b->x_full, i & 1, c.g)) return;
+    if (D == 64 && !wait(&b->x_full, i & 1, gd)) return;
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = (k / 4) * kAtom + (k % 4) * 32;
-      mma_bf16(c.tmem + P::kColS, smem_desc(a0 + off, 16, 1024), smem_desc(b0 + off, 16, 1024),
+      mma_bf16(tmem + P::kColS, smem_desc(a0 + off, 16, 1024), smem_desc(b0 + off, 16, 1024),
                idesc_bf16_f32(128, 128, 0, 0), k > 0);
     }
     mma_commit(&b->s_full);
-    if (D != 64 && !wait(&b->x_full, i & 1, c.g)) return;
-    if (i > 0 && !wait(&b->o_free, (i - 1) & 1, c.g)) return;
+    if (D != 64 && !wait(&b->x_full, i & 1, gd)) return;
+    if (i > 0 && !wait(&b->o_free, (i - 1) & 1, gd)) return;
     tc_fence_after();
     {
-      const uint64_t dx = smem_desc(smem_u32(c.sm + P::kOffX), D * 128, 1024);
+      const uint64_t dx = smem_desc(xt, D * 128, 1024);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        mma_bf16(c.tmem + P::kColInter, smem_desc(a0 + (k / 4) * kAtom + (k % 4) * 32, 16, 1024),
-                 dx + k * (2048 >> 4), idesc_bf16_f32(128, D, 0, 1), k > 0);
+        mma_bf16(tmem + P::kColInter, smem_desc(a0 + (k / 4) * kAtom + (k % 4) * 32, 16, 1024), dx + k * (2048 >> 4),
+                 idesc_bf16_f32(128, D, 0, 1), k > 0);
     }
     mma_commit(&b->in_full);
-    if (!wait(&b->p_full, i & 1, c.g)) return;
+    if (!wait(&b->p_full, i & 1, gd)) return;
     tc_fence_after();
     {
       const uint64_t dc = smem_desc(c0, kAtom, 1024);
 #pragma unroll
       for (int k = 0; k < kTok / 16; ++k)
-        mma_bf16_ts(c.tmem + P::kColIntra, c.tmem + P::kColS + 8 * k, dc + k * (2048 >> 4),
-                    idesc_bf16_f32(128, D, 0, 1), k > 0);
+        mma_bf16_ts(tmem + P::kColIntra, tmem + P::kColS + 8 * k, dc + k * (2048 >> 4), idesc_bf16_f32(128, D, 0, 1),
+                    k > 0);
     }
     mma_commit(&b->o_full);
-    if (i < c.nx) {
-      if (!wait(&b->w_full, i & 1, c.g)) return;
+    if (i < nx) {
+      if (!wait(&b->w_full, i & 1, gd)) return;
       tc_fence_after();
-      mma_outer<D, D>(c.tmem + P::kColDX, b0, c0, false);
-      mma_outer<D, D>(c.tmem + P::kColDX, a0, c0, true);
-      if (c.terms > 2) mma_outer<D, D>(c.tmem + P::kColDX, smem_u32(c.sm + P::kOffX), c0, true);
+      mma_outer<D, D>(tmem + P::kColDX, b0, c0, false);
+      mma_outer<D, D>(tmem + P::kColDX, a0, c0, true);
+      if (terms > 2) mma_outer<D, D>(tmem + P::kColDX, xt, c0, true);
       mma_commit(&b->dx_full);
     }
     mma_commit(&b->empty[s]);
   }
 }
 
-// Warps 2-5, TMEM lane quadrant = warp % 4, one token row t a thread.
-template <int D>
-__device__ __forceinline__ void pass_out(const TcArgs& t, const PassCtx& c, int warp, int lane) {
-  using P = PassTile<D>;
-  PassBars* b = c.b;
-  const RetPass& p = t.r.pass[c.z];
-  const int qd = warp & 3, row = 32 * qd + lane, d = t.r.d;
-  const uint32_t tl = c.tmem + ((uint32_t)(32 * qd) << 16);
-  const float scale = t.r.scale;
-  const bool wide = t.wide_out[c.z] != 0;
-  const long long sn = p.out.sn, xsn = p.x.sn;
-  const int xf = p.x.feature;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + ret_base(t.r, p.out, c.seq, c.h);
-  const __nv_bfloat16* xin = static_cast<const __nv_bfloat16*>(p.x.p);
-  if (xin != nullptr) xin += ret_base(t.r, p.x, c.seq, c.h);
-#pragma unroll 1
-  for (int i = 0; i < c.n; ++i) {
-    const int ch = c.chunk(i), len = c.chunk_len(ch);
-    if (!wait_warp(&b->s_full, i & 1, c.g)) return;
-    tc_fence_after();
-    // block j of scores lies in columns 32 j .., its P in 16 j ..: never over scores still to be read
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      uint32_t w[16];
-      if (c.reverse ? j < qd : j > qd) {
+// Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  Split: the two warps of a quadrant take
+// every other block of 32 scores and a half of the output columns each.
+// 16 columns of a row: one whole 32-byte sector in one store where rows are aligned to that.
+__device__ __forceinline__ void store16(__nv_bfloat16* dst, uint4 a, uint4 b, bool live, bool wide) {
+  const int w = live && wide, n = live && !wide;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %9, 0;\n\t"
+      "setp.ne.b32 q, %10, 0;\n\t"
+      "@p st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+      "@q st.global.v4.b32 [%0], {%1,%2,%3,%4};\n\t"
+      "@q st.global.v4.b32 [%0 + 16], {%5,%6,%7,%8};\n\t}" ::"l"(dst),
+      "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w), "r"(w), "r"(n)
+      : "memory");
+}
+
+// 16 lanes x 64 columns: registers 4 g + {0, 1} are columns 8 g + 2 (l % 4) + {0, 1} of row l / 4, 4 g + {2, 3}
+// those of row l / 4 + 8.
+__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
 #pragma unroll
-        for (int x = 0; x < 16; ++x) w[x] = 0;
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The four lanes of a group of four hold pairs e[2 k], e[2 k + 1], k = 0 .. 3: lane q gets pair q of lane k as
+// its pair k.
+__device__ __forceinline__ void turn4(uint32_t* e, int lane) {
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & s) continue;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t &a = e[2 * k + w], &b = e[2 * (k | s) + w];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, s);
+        if (up)
+          a = got;
+        else
+          b = got;
+      }
+    }
+  }
+}
+
+template <int D, bool DERIV>
+__device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
+  using P = PassTile<D>;
+  constexpr int S = P::kSplit;
+  const int qd = warp & 3, row = 32 * qd + lane, half = S == 1 ? 0 : (warp - kWarpOut) >> 2;
+  const int n = b->ctx.n, all = b->ctx.len, reverse = b->ctx.reverse, row0 = b->ctx.row0, xf = b->ctx.fx;
+  const int d0 = half * 64, d1 = min(b->ctx.d, d0 + 64);
+  const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16);
+  const float scale = b->ctx.scale, scale1 = scale * exp2f(b->ctx.lg);  // scale gamma
+  const bool wide = b->ctx.wide != 0;
+  const long long sn = b->ctx.out_n, xsn = b->ctx.x_n;
+  __nv_bfloat16* out = b->ctx.out;
+  const __nv_bfloat16* xin = b->ctx.x;
+  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
+  const float* decay = b->decay + (reverse ? kTok - 1 : 32);  // [t - s]: its weight, 0 on the masked side
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
+    if (!wait_warp(&b->s_full, i & 1, gd)) return;
+    tc_fence_after();
+    // P of block j of the scores goes to columns 16 j .., over scores: they are written when all are read
+    uint32_t w[S == 1 ? 1 : 2][16];
+#pragma unroll(S == 1 ? 1 : 2)
+    for (int jj = 0; jj < 4 / S; ++jj) {
+      const int j = S * jj + half;
+      uint32_t* wj = w[S == 1 ? 0 : jj];
+      if (reverse ? j < qd : j > qd) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) wj[x] = 0;
       } else {
         float v[32];
         tmem_ld16(tl + P::kColS + 32 * j, v);
         tmem_ld16(tl + P::kColS + 32 * j + 16, v + 16);
-        // gamma^|t-s|; on the diagonal block the entries of the wrong sign are read beside the table and dropped
-        const int n = row - 32 * j;
-        float f[32];
-        if (c.reverse) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) f[x] = b->decay[x - n];
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) f[x] = b->decay[n - x];
-        }
+        const float* f = decay + (row - 32 * j);
         tmem_ld_wait();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) v[x] *= f[x];
-        if (j == qd) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (c.reverse ? x < lane : x > lane) v[x] = 0.f;
+        for (int x = 0; x < 32; ++x) {
+          const float fx = f[-x];
+          v[x] = fx != 0.f ? v[x] * fx : 0.f;  // (zero stays zero beside an infinite score)
         }
 #pragma unroll
-        for (int x = 0; x < 16; ++x) w[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
+        for (int x = 0; x < 16; ++x) wj[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
       }
-      tmem_st16u(tl + P::kColS + 16 * j, w);
+      if (S == 1) tmem_st16u(tl + P::kColS + 16 * j, wj);  // in the order of j: behind the scores read so far
+    }
+    if (S == 2) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->read[qd]);
+      if (!wait_warp(&b->read[qd], i & 1, gd)) return;  // the other warp of the quadrant has read its scores
+      tc_fence_after();
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) tmem_st16u(tl + P::kColS + 16 * (S * jj + half), w[S == 1 ? 0 : jj]);
     }
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->p_full);
 
-    const bool live = row < len;
-    const long long at = (long long)(c.row0 + ch * kTok + row);
-    __nv_bfloat16* dst = out + at * sn;
-    const __nv_bfloat16* xp = xin == nullptr ? nullptr : xin + at * xsn;
-    const float wi = scale * decay_pow(c.lg, c.reverse ? max(len - row, 0) : row + 1);
-    if (!wait_warp(&b->o_full, i & 1, c.g)) return;
+    if (!wait_warp(&b->o_full, i & 1, gd)) return;
     tc_fence_after();
+    // 16 rows at a time: lane l holds columns 8 g + 2 (l % 4) + {0, 1} of rows l / 4 and l / 4 + 8; the four
+    // lanes of a row turn their pairs round, so that each has 16 columns in a row and they store 128 bytes
 #pragma unroll 1
-    for (int g = 0; g < d; g += 16) {
-      float u[16], v[16];
-      tmem_ld16(tl + P::kColInter + g, u);
-      tmem_ld16(tl + P::kColIntra + g, v);
+    for (int hh = 0; hh < 2; ++hh) {
+      float u[32], v[32];
+      const uint32_t tr = tl + ((uint32_t)(16 * hh) << 16);
+      tmem_ld16x64(tr + P::kColInter + d0, u);
+      tmem_ld16x64(tr + P::kColIntra + d0, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int x = 0; x < 16; ++x) v[x] = fmaf(wi, u[x], scale * v[x]);
-      if (live) {
-        if (xp != nullptr) {
-          unpack8(*reinterpret_cast<const uint4*>(xp + g), u);
-          unpack8(*reinterpret_cast<const uint4*>(xp + g + 8), u + 8);
+      for (int k = 0; k < 2; ++k) {
+        const int rw = 32 * qd + 16 * hh + 8 * k + (lane >> 2);
+        const bool live = rw < len;
+        const float wi = live ? scale1 * b->decay[reverse ? kTok - len + rw : 32 + rw] : 0.f;
+        const long long at = (long long)(row0 + ch * kTok + rw);
+        uint32_t e[8];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] *= ret_dphi(u[x], xf);
+        for (int g = 0; g < 8; ++g) {
+          float x0 = fmaf(wi, u[4 * g + 2 * k], scale * v[4 * g + 2 * k]);
+          float x1 = fmaf(wi, u[4 * g + 2 * k + 1], scale * v[4 * g + 2 * k + 1]);
+          if (DERIV && live && d0 + 8 * g < d1) {
+            const uint32_t xx = *reinterpret_cast<const uint32_t*>(xin + at * xsn + d0 + 8 * g + 2 * (lane & 3));
+            x0 *= ret_dphi(__uint_as_float(xx << 16), xf);
+            x1 *= ret_dphi(__uint_as_float(xx & 0xffff0000u), xf);
+          }
+          e[g] = pack_bf16(x0, x1);
         }
-        const uint4 lo8 = pack8(v), hi8 = pack8(v + 8);
-        if (wide) {  // one whole 32-byte sector a store
-          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + g), "r"(lo8.x), "r"(lo8.y),
-                       "r"(lo8.z), "r"(lo8.w), "r"(hi8.x), "r"(hi8.y), "r"(hi8.z), "r"(hi8.w)
-                       : "memory");
-        } else {
-          *reinterpret_cast<uint4*>(dst + g) = lo8;
-          *reinterpret_cast<uint4*>(dst + g + 8) = hi8;
-        }
+        turn4(e, lane);
+        const int col = d0 + 16 * (lane & 3);
+        store16(out + at * sn + col, make_uint4(e[0], e[2], e[4], e[6]), make_uint4(e[1], e[3], e[5], e[7]),
+                live && col < d1, wide);
       }
-      __syncwarp();  // the TMEM loads are the whole warp's
     }
     tc_fence_before();
     __syncwarp();
@@ -428,31 +521,35 @@ __device__ __forceinline__ void pass_out(const TcArgs& t, const PassCtx& c, int 
   }
 }
 
-// Warps 6-9.  B w and the feature maps: one token row a thread.  X: TMEM lane quadrant = warp % 4, row c
-// of X a lane (D = 64: M = 64 puts 16 rows into the first lanes of each quadrant).
+// X warps.  B w and the feature maps: token row = 32 (warp % 4) + lane.  X: TMEM lane quadrant = warp % 4,
+// row c of X a lane (D = 64: M = 64 puts 16 rows into the first lanes of each quadrant).  Columns 64 half ..
 template <int D>
-__device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, int warp, int lane, const float* from,
-                                           bool from_t, float* to) {
+__device__ __noinline__ void pass_state(uint8_t* sm, PassBars* b, int warp, int lane) {
   using P = PassTile<D>;
-  PassBars* b = c.b;
-  const RetPass& p = t.r.pass[c.z];
-  const int qd = warp & 3, row = 32 * qd + lane, d = t.r.d;
+  const int qd = warp & 3, row = 32 * qd + lane, half = P::kSplit == 1 ? 0 : (warp - P::kWarpX) >> 2;
+  const int d0 = half * 64, j0 = half * 8;
+  const int d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
+  const int terms = b->ctx.terms, fa = b->ctx.fa, fb = b->ctx.fb, fc = b->ctx.fc;
+  const bool mapped = b->ctx.mapped(), anew = terms > 2 && fb != kFeatIdentity;  // phi(b) in fp32 for the state
+  const float lg = b->ctx.lg;
+  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
   const int xr = D == 128 ? row : 16 * qd + lane;           // row of X
   const bool has = (D == 128 || lane < 16) && xr < d;
-  const uint32_t tl = c.tmem + ((uint32_t)(32 * qd) << 16);
-  const int fa = p.a.feature, fb = p.b.feature, fc = p.c.feature;
-  const bool anew = c.terms > 2 && fb != kFeatIdentity;  // phi(b) in fp32 for the state
-  uint8_t* xt = c.sm + P::kOffX;
-  float X[D];
+  const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16);
+  uint8_t* xt = sm + P::kOffX;
+  const float* from = b->ctx.from;
+  const bool from_t = b->ctx.from_t != 0;
+  float X[64];
 #pragma unroll
-  for (int e = 0; e < D; e += 4) {
+  for (int e = 0; e < 64; e += 4) {
     float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (from != nullptr && has && e < d) {
+    if (from != nullptr && has && d0 + e < d) {
+      const int c0 = d0 + e;
       if (from_t)
-        u = make_float4(__ldcg(from + e * d + xr), __ldcg(from + (e + 1) * d + xr), __ldcg(from + (e + 2) * d + xr),
-                        __ldcg(from + (e + 3) * d + xr));
+        u = make_float4(__ldcg(from + c0 * d + xr), __ldcg(from + (c0 + 1) * d + xr), __ldcg(from + (c0 + 2) * d + xr),
+                        __ldcg(from + (c0 + 3) * d + xr));
       else
-        u = __ldcg(reinterpret_cast<const float4*>(from + xr * d + e));
+        u = __ldcg(reinterpret_cast<const float4*>(from + xr * d + c0));
     }
     X[e] = u.x;
     X[e + 1] = u.y;
@@ -462,7 +559,7 @@ __device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, in
   auto publish = [&] {
     if (D == 128 || lane < 16) {
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) *piece(xt, D, xr, j) = pack8(X + 8 * j);
+      for (int j = 0; j < 8; ++j) *piece(xt, D, xr, j0 + j) = pack8(X + 8 * j);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -470,13 +567,13 @@ __device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, in
     if (lane == 0) mbar_arrive(&b->x_full);
   };
   auto map = [&](int i) -> bool {  // feature maps of chunk i, rows behind the sequence cleared in B and C
-    const int len = c.chunk_len(c.chunk(i));
-    if (!c.mapped && len == kTok) return true;
-    if (!wait_warp(&b->full[i % kStages], (i / kStages) & 1, c.g)) return false;
-    uint8_t* st = c.sm + (i % kStages) * P::kStage;
-    if (fa != kFeatIdentity) map_row<D>(st, row, kTok, d, fa);
-    if (fb != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, d, fb);
-    if (fc != kFeatIdentity || len < kTok) map_row<D>(st + 2 * P::kOp, row, len, d, fc);
+    const int len = chunk_len(chunk_of(i, n, reverse), all);
+    if (!mapped && len == kTok) return true;
+    if (!wait_warp(&b->full[i % kStages], (i / kStages) & 1, gd)) return false;
+    uint8_t* st = sm + (i % kStages) * P::kStage;
+    if (fa != kFeatIdentity) map_row<64>(st, row, j0, kTok, d, fa);
+    if (fb != kFeatIdentity || len < kTok) map_row<64>(st + P::kOp, row, j0, len, d, fb);
+    if (fc != kFeatIdentity || len < kTok) map_row<64>(st + 2 * P::kOp, row, j0, len, d, fc);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->mapped);
@@ -485,132 +582,159 @@ __device__ __forceinline__ void pass_state(const TcArgs& t, const PassCtx& c, in
   if (!map(0)) return;
   publish();
 #pragma unroll 1
-  for (int i = 0; i < c.nx; ++i) {
-    const int ch = c.chunk(i), len = c.chunk_len(ch);
-    uint8_t* st = c.sm + (i % kStages) * P::kStage;
+  for (int i = 0; i < nx; ++i) {
+    const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
+    uint8_t* st = sm + (i % kStages) * P::kStage;
     // B has been read by the scores, A (and the old X) by inter
-    if (!wait_warp(&b->s_full, i & 1, c.g) || !wait_warp(&b->in_full, i & 1, c.g)) return;
-    const float w = row < len ? b->decay[c.reverse ? row : len - 1 - row] : 0.f;
-    const __nv_bfloat16* raw = nullptr;
-    if (anew && row < len)
-      raw = static_cast<const __nv_bfloat16*>(p.b.p) + ret_base(t.r, p.b, c.seq, c.h) +
-            (long long)(c.row0 + ch * kTok + row) * p.b.sn;
-    // (without fp32 states the tile's rounded phi is good enough)
-    weigh_row<D>(st + P::kOp, st, c.terms > 2 ? xt : nullptr, row, w, raw, d, anew ? fb : kFeatIdentity);
+    if (!wait_warp(&b->s_full, i & 1, gd) || !wait_warp(&b->in_full, i & 1, gd)) return;
+    const float w = row < len ? b->decay[reverse ? kTok - 1 - row : 32 + len - 1 - row] : 0.f;
+    if (anew) {
+      const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
+      weigh_phi_row<64, 3>(st + P::kOp, st, xt, row, j0, w, raw, d, fb);
+    } else if (terms > 2) {
+      weigh_row<64, 3>(st + P::kOp, st, xt, row, j0, w);
+    } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
+      weigh_row<64, 2>(st + P::kOp, st, xt, row, j0, w);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->w_full);
-    if (i + 1 < c.n && !map(i + 1)) return;
-    const float wl = decay_pow(c.lg, len);
-    if (!wait_warp(&b->dx_full, i & 1, c.g)) return;
+    if (i + 1 < n && !map(i + 1)) return;
+    const float wl = decay_pow(lg, len);
+    if (!wait_warp(&b->dx_full, i & 1, gd)) return;
     tc_fence_after();
 #pragma unroll
-    for (int g = 0; g < D / 16; ++g) {
+    for (int g = 0; g < 4; ++g) {
       float u[16];
-      tmem_ld16(tl + P::kColDX + 16 * g, u);
+      tmem_ld16(tl + P::kColDX + d0 + 16 * g, u);
       tmem_ld_wait();
 #pragma unroll
       for (int x = 0; x < 16; ++x) X[16 * g + x] = fmaf(wl, X[16 * g + x], u[x]);
     }
-    if (i + 1 < c.n) publish();
+    if (i + 1 < n) publish();
   }
+  float* to = b->ctx.to;
   if (to != nullptr && has) {
 #pragma unroll
-    for (int e = 0; e < D; e += 4)
-      if (e < d) *reinterpret_cast<float4*>(to + xr * d + e) = make_float4(X[e], X[e + 1], X[e + 2], X[e + 3]);
+    for (int e = 0; e < 64; e += 4)
+      if (d0 + e < d)
+        *reinterpret_cast<float4*>(to + xr * d + d0 + e) = make_float4(X[e], X[e + 1], X[e + 2], X[e + 3]);
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, PassTile<D>::kPerSm) retention_pass_kernel(const __grid_constant__ TcArgs t) {
+__global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) retention_pass_kernel(const __grid_constant__ TcArgs t) {
   using P = PassTile<D>;
-  extern __shared__ __align__(1024) uint8_t smraw[];
-  PassCtx c;
-  c.sm = smraw;
-  c.b = reinterpret_cast<PassBars*>(c.sm + P::kOffBars);
-  PassBars* b = c.b;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  PassBars* b = reinterpret_cast<PassBars*>(sm + P::kOffBars);
   const RetArgs& r = t.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  c.z = blockIdx.x % r.npass;  // a head's passes side by side: they read the same tensors
-  const int unit = blockIdx.x / r.npass, g = unit / r.H;
-  c.h = unit % r.H;
-  const Segment sg = find_segment(r, g, b->scratch);
+  const int z = blockIdx.x % r.npass;  // a head's passes side by side: they read the same tensors
+  const int unit = blockIdx.x / r.npass, g = unit / r.H, h = unit % r.H;
+  const Segment sg = find_segment(r, g, reinterpret_cast<int*>(b->decay));
   if (sg.seq < 0) return;
   const int slot = r.states != nullptr ? ret_slot(r.slots, r.n_slots, sg.seq) : -1;
+  const float lg = decay_log2(r.gamma[h]);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&b->full[s], 1);
       mbar_init(&b->empty[s], 1);
     }
     for (uint64_t* m : {&b->s_full, &b->in_full, &b->dx_full, &b->o_full, &b->fin}) mbar_init(m, 1);
-    for (uint64_t* m : {&b->mapped, &b->p_full, &b->w_full, &b->x_full, &b->o_free}) mbar_init(m, 4);
+    for (uint64_t* m : {&b->mapped, &b->p_full, &b->w_full, &b->x_full, &b->o_free}) mbar_init(m, 4 * P::kSplit);
+    for (int i = 0; i < 4; ++i) mbar_init(&b->read[i], 2);
     b->abort = 0;
     b->issued = 0;
     fence_mbar_init();
   }
-  c.lg = decay_log2(r.gamma[c.h]);
-  if (threadIdx.x >= kThreads - kTok) {
-    const int n = threadIdx.x - (kThreads - kTok);
-    b->decay[n] = decay_pow(c.lg, n);
+  if (threadIdx.x == 64) {
+    const RetPass& p = r.pass[z];
+    const int ia = t.ia[z], ib = t.ib[z], ic = t.ic[z];
+    const size_t dd = (size_t)r.d * r.d;
+    PassCtx& c = b->ctx;
+    c.ma = &t.tm[ia];
+    c.mb = &t.tm[ib];
+    c.mc = &t.tm[ic];
+    c.ha = t.by_h[ia] ? h : 0;
+    c.hb = t.by_h[ib] ? h : 0;
+    c.hc = t.by_h[ic] ? h : 0;
+    c.ba = t.by_b[ia] ? sg.seq : 0;
+    c.bb = t.by_b[ib] ? sg.seq : 0;
+    c.bc = t.by_b[ic] ? sg.seq : 0;
+    c.row0 = sg.row0;
+    c.len = sg.len;
+    c.n = (sg.len + kTok - 1) / kTok;
+    c.to = slot >= 0 && sg.seg == sg.nseg - 1 ? r.states + ((size_t)slot * r.H + h) * dd : nullptr;
+    c.nx = c.to != nullptr ? c.n : c.n - 1;
+    c.reverse = p.reverse;
+    c.terms = c.to != nullptr ? 3 : 2;
+    c.fa = p.a.feature;
+    c.fb = p.b.feature;
+    c.fc = p.c.feature;
+    c.fx = p.x.feature;
+    c.d = r.d;
+    c.wide = t.wide_out[z];
+    c.lg = lg;
+    c.scale = r.scale;
+    c.out = static_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + ret_base(r, p.out, sg.seq, h);
+    c.x = p.x.p == nullptr ? nullptr : static_cast<const __nv_bfloat16*>(p.x.p) + ret_base(r, p.x, sg.seq, h);
+    c.b = static_cast<const __nv_bfloat16*>(p.b.p) + ret_base(r, p.b, sg.seq, h);
+    c.out_n = p.out.sn;
+    c.x_n = p.x.sn;
+    c.b_n = p.b.sn;
+    c.from = sg.nseg > 1             ? r.seg + (((size_t)p.sum * r.G + g) * r.H + h) * dd
+             : r.load && slot >= 0 ? r.states + ((size_t)slot * r.H + h) * dd
+                                     : nullptr;
+    c.from_t = sg.nseg > 1 && p.sum_t;
+    c.wait_ns = t.wait_ns;
+  }
+  if (threadIdx.x >= P::kThreads - kTok - 32) {
+    const int i = threadIdx.x - (P::kThreads - kTok - 32), n = r.pass[z].reverse ? kTok - 1 - i : i - 32;
+    b->decay[i] = n >= 0 ? decay_pow(lg, n) : 0.f;
   }
   if (warp == kWarpMma) {
     tmem_alloc(&b->tbase, P::kCols);
     tmem_relinquish();
   }
   if (warp == kWarpProd && lane == 0) {
-    prefetch_tmap(&t.tm[t.ia[c.z]]);
-    prefetch_tmap(&t.tm[t.ib[c.z]]);
-    prefetch_tmap(&t.tm[t.ic[c.z]]);
+    prefetch_tmap(&t.tm[t.ia[z]]);
+    prefetch_tmap(&t.tm[t.ib[z]]);
+    prefetch_tmap(&t.tm[t.ic[z]]);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const RetPass& p = r.pass[c.z];
-  c.g = {&b->abort, t.wait_ns};
-  c.tmem = b->tbase;
-  c.seq = sg.seq;
-  c.row0 = sg.row0;
-  c.len = sg.len;
-  c.n = (sg.len + kTok - 1) / kTok;
-  const size_t dd = (size_t)r.d * r.d;
-  float* to = slot >= 0 && sg.seg == sg.nseg - 1 ? r.states + ((size_t)slot * r.H + c.h) * dd : nullptr;
-  c.nx = to != nullptr ? c.n : c.n - 1;
-  c.reverse = p.reverse;
-  c.terms = r.states != nullptr ? 3 : 2;
-  c.mapped = p.a.feature != kFeatIdentity || p.b.feature != kFeatIdentity || p.c.feature != kFeatIdentity;
-  const float* from = nullptr;
-  if (sg.nseg > 1)
-    from = r.seg + (((size_t)p.sum * r.G + g) * r.H + c.h) * dd;
-  else if (r.load && slot >= 0)
-    from = r.states + ((size_t)slot * r.H + c.h) * dd;
 
   if (warp == kWarpProd) {
-    if (lane == 0) pass_producer<D>(t, c);
+    if (lane == 0) pass_producer<D>(sm, b);
     __syncwarp();
   } else if (warp == kWarpMma) {
     if (lane == 0) {
-      pass_mma<D>(c);
+      pass_mma<D>(sm, b);
       mma_commit(&b->fin);
     }
     __syncwarp();
-  } else if (warp < kWarpX) {
-    pass_out<D>(t, c, warp, lane);
+  } else if (warp < P::kWarpX) {
+    if (b->ctx.x == nullptr)
+      pass_out<D, false>(b, warp, lane);
+    else
+      pass_out<D, true>(b, warp, lane);
   } else {
-    pass_state<D>(t, c, warp, lane, from, sg.nseg > 1 && p.sum_t, to);
+    pass_state<D>(sm, b, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) {
     drain(&b->fin, 0);
-    if (aborted(c.g)) {
+    if (b->abort) {
       for (int q = b->issued > kStages ? b->issued - kStages : 0; q < b->issued; ++q)
         drain(&b->full[q % kStages], (q / kStages) & 1);
       atomicOr(r.status, 1u);
     }
   }
   __syncthreads();
-  if (warp == kWarpMma) tmem_dealloc(c.tmem, P::kCols);
+  if (warp == kWarpMma) tmem_dealloc(b->tbase, P::kCols);
 }
 
 // ================================================================ segment sums
@@ -676,7 +800,7 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Guard gd{&b->abort, t.wait_ns};
+  const Guard gd = make_guard(&b->abort, t.wait_ns);
   const uint32_t tmem = b->tbase;
   const int n = (sg.len + kTok - 1) / kTok;
   const int terms = r.states != nullptr ? 3 : 2;
@@ -684,14 +808,16 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
 
   if (warp == kWarpProd) {
     if (lane == 0) {
+      const int ib = t.ib[z], ic = t.ic[z];
       int i = 0;
       for (; i < n; ++i) {
         const int s = i % kStages;
         if (i >= kStages && !wait(&b->empty[s], ((i / kStages) - 1) & 1, gd)) break;
         uint8_t* st = sm + s * P::kStage;
         mbar_arrive_expect_tx(&b->full[s], 2 * P::kOp);
-        load_tile<D>(st, t, t.ib[z], sg.row0 + i * kTok, h, sg.seq, &b->full[s]);
-        load_tile<D>(st + P::kOp, t, t.ic[z], sg.row0 + i * kTok, h, sg.seq, &b->full[s]);
+        load_tile<D>(st, &t.tm[ib], sg.row0 + i * kTok, t.by_h[ib] ? h : 0, t.by_b[ib] ? sg.seq : 0, &b->full[s]);
+        load_tile<D>(st + P::kOp, &t.tm[ic], sg.row0 + i * kTok, t.by_h[ic] ? h : 0, t.by_b[ic] ? sg.seq : 0,
+                     &b->full[s]);
       }
       b->issued = i;
     }
@@ -723,9 +849,14 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
       // the remainders' tiles have been read by the MMAs of the chunk before
       if (i > 0) ok = wait_warp(&b->empty[(i - 1) % kStages], ((i - 1) / kStages) & 1, gd);
       if (!ok) break;
-      if (p.c.feature != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, r.d, p.c.feature);
+      if (p.c.feature != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, 0, len, r.d, p.c.feature);
       const float w = row < len ? decay_pow(lg, p.reverse ? at : sg.len - 1 - at) : 0.f;
-      weigh_row<D>(st, lo, terms > 2 ? lo + P::kOp : nullptr, row, w, nullptr, r.d, p.b.feature);
+      if (p.b.feature != kFeatIdentity)
+        weigh_phi_row<D, 3>(st, lo, lo + P::kOp, row, 0, w, nullptr, r.d, p.b.feature);
+      else if (terms > 2)
+        weigh_row<D, 3>(st, lo, lo + P::kOp, row, 0, w);
+      else
+        weigh_row<D, 2>(st, lo, nullptr, row, 0, w);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->ready[s]);
@@ -827,7 +958,7 @@ cudaError_t launch(const TcArgs& t, cudaStream_t st) {
     e = retention_scan_launch(t.r, st);
     if (e != cudaSuccess) return e;
   }
-  retention_pass_kernel<D><<<units * t.r.npass, kThreads, pass_smem<D>(), st>>>(t);
+  retention_pass_kernel<D><<<units * t.r.npass, PassTile<D>::kThreads, pass_smem<D>(), st>>>(t);
   note_launch();
   return cudaGetLastError();
 }
