@@ -12,19 +12,24 @@
 //
 // What is rounded to bf16: the masked scores, the copy of X that the product reads (X itself stays
 // fp32) and phi of operands with a feature map.  B w is carried as a sum of bf16 numbers: of two (over
-// the B tile, the remainder over the A tile: 2^-16 of a term) where only bf16 outputs come of it, of
-// three (the last over the tile of X: 2^-24) in the segment whose state is returned in fp32.
+// the B tile and in a tile of its own: 2^-16 of a term) where only bf16 outputs come of it, of three (the
+// last over the tile of X: 2^-24) in the segment whose state is returned in fp32.
 //
-// The roles' loops are kept short rather than unrolled: one warp a scheduler runs each of them, and with
-// whole rows unrolled the instruction fetch, not the arithmetic, set the pace (a chunk took 23,000 cycles).
+// Roles (D = 128: 18 warps and one CTA an SM, D = 64: 14 warps and two):
+//   warp 0       TMA producer: the tiles of a chunk, B and C two chunks deep, A one
+//   warp 1       MMA issuer
+//   out warps    scores -> P, then out = scale (intra + gamma^(i+1) inter) to global memory (D = 128:
+//                eight warps, each with half of the scores and of the columns; D = 64: four)
+//   4 W warps    feature maps in place, B w
+//   4 X warps    X and its bf16 tile for the next chunk
+// A chunk's B w does not wait for the X that enters it, so the serial chain from one X to the next is
+// inter, intra, dX and the update.  What this costs is shared memory's bandwidth: with D = 128 a chunk's
+// products read 2.5 thousand cycles' worth of it (128 bytes a cycle; 128 x 128 x 16 from shared memory
+// takes 64 cycles, twice the tensor cores' time), TMA writes 0.8, B w 1.3, X and the scores' weights 0.6.
 //
-// Roles (D = 128: 18 warps and one CTA an SM, D = 64: 10 warps and two):
-//   warp 0     TMA producer: the A, B and C tiles of a chunk (2-stage ring)
-//   warp 1     MMA issuer
-//   out warps  scores -> P, then out = scale (intra + gamma^(i+1) inter) to global memory
-//   X warps    feature maps in place, B w over B, and X: registers, and its bf16 tile for the next chunk
-// Four out and four X warps take a row each thread; with D = 128 there are twice as many and two threads
-// share a row, half of the columns each (X then takes 64 registers a thread, not 128).
+// The roles' loops are kept short and free of branches: with whole rows unrolled the instruction fetch,
+// not the arithmetic, set the pace (23,000 cycles a chunk), and stores of one row a thread held up the
+// loads and stores of shared memory beside them (67 cycles each).
 // All waits are bounded: on time-out the kernel sets the status word and winds down.
 //
 // A sequence of several segments needs the states that enter them: retention_sum_kernel forms each
@@ -55,7 +60,6 @@ struct TcArgs {
   CUtensorMap tm[4];                         // q, k, v, dy as [B][H][N][d], box 64 x 128
   int by_b[4], by_h[4];                      // 0: shared by the batch / the heads
   int ia[kRetMaxPasses], ib[kRetMaxPasses], ic[kRetMaxPasses];  // tensor maps of a pass's operands
-  int wide_out[kRetMaxPasses];               // rows of out (and x) start on 32 bytes
   unsigned long long wait_ns;
   RetArgs r;
 };
@@ -223,17 +227,19 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 template <int D>
 struct PassTile {
   static constexpr int kOp = (D / 64) * kAtom;          // an operand's tile
-  static constexpr int kStage = 3 * kOp;
-  static constexpr int kOffX = kStages * kStage;        // bf16 X: D rows c, D columns e
-  static constexpr int kOffBars = kOffX + kOp;          // (a tile's room: also the third part of B w)
+  static constexpr int kOffA = 0, kOffBC = kOp;         // A; kStages x (B, C)
+  static constexpr int kOffLo = kOffBC + kStages * 2 * kOp;  // second part of B w
+  static constexpr int kOffX = kOffLo + kOp;            // bf16 X: D rows c, D columns e (third part of B w)
+  static constexpr int kOffBars = kOffX + kOp;
   static constexpr uint32_t kCols = D == 128 ? 512 : 256;
   static constexpr uint32_t kColS = 0;                  // scores, P over their first half
   static constexpr uint32_t kColInter = 128, kColIntra = 128 + D;
-  static constexpr uint32_t kColDX = D == 128 ? 384 : 64;  // D = 64: over the scores that P leaves free
+  // D = 128: X gamma^len, dX is added to it.  D = 64: dX alone, over the scores that P leaves free; X is in registers
+  static constexpr uint32_t kColDX = D == 128 ? 384 : 64;
   static constexpr int kPerSm = D == 128 ? 1 : 2;
-  static constexpr int kSplit = D / 64;                 // threads that share a row
-  static constexpr int kWarpX = kWarpOut + 4 * kSplit;
-  static constexpr int kThreads = 32 * (kWarpX + 4 * kSplit);
+  static constexpr int kSplit = D / 64;                 // out warps of a TMEM lane quadrant
+  static constexpr int kWarpW = kWarpOut + 4 * kSplit, kWarpX = kWarpW + 4;
+  static constexpr int kThreads = 32 * (kWarpX + 4);
 };
 
 // What the roles share.  It is kept in shared memory and the roles are functions of their own, so that none
@@ -245,9 +251,9 @@ struct PassCtx {
   int nx;                        // chunks whose dX is needed
   int reverse, terms;            // direction; bf16 numbers that B w is the sum of
   int fa, fb, fc, fx;            // feature maps of A, B, C and x
-  int d, wide;
+  int d;
   int from_t;
-  float lg, scale;
+  float lg;
   __nv_bfloat16* out;            // of the head; rows out_n apart
   const __nv_bfloat16 *x, *b;    // of the head: x (null: none), B
   long long out_n, x_n, b_n;
@@ -262,13 +268,14 @@ __device__ __forceinline__ int chunk_of(int i, int n, int reverse) { return reve
 __device__ __forceinline__ int chunk_len(int ch, int len) { return min(kTok, len - ch * kTok); }
 
 struct PassBars {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t mapped;    // feature maps applied / rows behind the sequence cleared (X warps)
+  uint64_t a_full;    // A (read for the last time by inter: in_full)
+  uint64_t full[kStages], empty[kStages];  // B, C
+  uint64_t mapped;    // feature maps applied / rows behind the sequence cleared (W warps)
   uint64_t s_full;    // scores
   uint64_t in_full;   // inter
   uint64_t read[4];   // D = 128: a quadrant's scores read by both its out warps
   uint64_t p_full;    // P in TMEM (out warps)
-  uint64_t w_full;    // B w (X warps)
+  uint64_t w_full;    // B w (W warps)
   uint64_t dx_full;   // dX
   uint64_t x_full;    // the bf16 tile of X (X warps)
   uint64_t o_full;    // intra
@@ -276,8 +283,8 @@ struct PassBars {
   uint64_t fin;       // every MMA of the CTA has completed
   uint32_t tbase;
   int abort;
-  int issued;         // chunks whose loads the producer issued
-  // gamma^n, 32 zeros beside it: forward [32 + n], reverse [kTok - 1 - n] (first the segment search's scratch)
+  int issued, issued_a;  // chunks whose B and C, whose A the producer asked for
+  // scale gamma^n, 32 zeros beside it: forward [32 + n], reverse [kTok - 1 - n] (first the segment search's scratch)
   float decay[kTok + 32];
   PassCtx ctx;
 };
@@ -293,17 +300,26 @@ __device__ __noinline__ void pass_producer(uint8_t* sm, PassBars* b) {
   using P = PassTile<D>;
   const PassCtx c = b->ctx;
   const Guard gd = make_guard(&b->abort, c.wait_ns);
-  int i = 0;
-  for (; i < c.n; ++i) {
-    const int s = i % kStages, row = c.row0 + chunk_of(i, c.n, c.reverse) * kTok;
-    if (i >= kStages && !wait(&b->empty[s], ((i / kStages) - 1) & 1, gd)) break;
-    uint8_t* st = sm + s * P::kStage;
-    mbar_arrive_expect_tx(&b->full[s], P::kStage);
-    load_tile<D>(st, c.ma, row, c.ha, c.ba, &b->full[s]);
-    load_tile<D>(st + P::kOp, c.mb, row, c.hb, c.bb, &b->full[s]);
-    load_tile<D>(st + 2 * P::kOp, c.mc, row, c.hc, c.bc, &b->full[s]);
+  auto row = [&](int i) { return c.row0 + chunk_of(i, c.n, c.reverse) * kTok; };
+  auto load_bc = [&](int i) {
+    const int s = i % kStages;
+    uint8_t* st = sm + P::kOffBC + s * 2 * P::kOp;
+    mbar_arrive_expect_tx(&b->full[s], 2 * P::kOp);
+    load_tile<D>(st, c.mb, row(i), c.hb, c.bb, &b->full[s]);
+    load_tile<D>(st + P::kOp, c.mc, row(i), c.hc, c.bc, &b->full[s]);
+    b->issued = i + 1;
+  };
+  load_bc(0);
+  for (int i = 0; i < c.n; ++i) {
+    if (i > 0 && !wait(&b->in_full, (i - 1) & 1, gd)) return;
+    mbar_arrive_expect_tx(&b->a_full, P::kOp);
+    load_tile<D>(sm + P::kOffA, c.ma, row(i), c.ha, c.ba, &b->a_full);
+    b->issued_a = i + 1;
+    if (i + 1 < c.n) {
+      if (i + 1 >= kStages && !wait(&b->empty[(i + 1) % kStages], ((i + 1) / kStages - 1) & 1, gd)) return;
+      load_bc(i + 1);
+    }
   }
-  b->issued = i;
 }
 
 template <int D>
@@ -311,14 +327,14 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
   using P = PassTile<D>;
   const int n = b->ctx.n, nx = b->ctx.nx, len = b->ctx.len, reverse = b->ctx.reverse, terms = b->ctx.terms;
   const bool mapped = b->ctx.mapped();
-  const uint32_t tmem = b->tbase, xt = smem_u32(sm + P::kOffX);
+  const uint32_t tmem = b->tbase, a0 = smem_u32(sm + P::kOffA), lo = smem_u32(sm + P::kOffLo), xt = smem_u32(sm + P::kOffX);
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
   int maps = 0;
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int s = i % kStages;
-    const uint32_t a0 = smem_u32(sm + s * P::kStage), b0 = a0 + P::kOp, c0 = b0 + P::kOp;
-    if (!wait(&b->full[s], (i / kStages) & 1, gd)) return;
+    const uint32_t b0 = smem_u32(sm + P::kOffBC + s * 2 * P::kOp), c0 = b0 + P::kOp;
+    if (!wait(&b->full[s], (i / kStages) & 1, gd) || !wait(&b->a_full, i & 1, gd)) return;
     if (i > 0 && !wait(&b->o_full, (i - 1) & 1, gd)) return;  // the scores go over P of the last chunk
     if (mapped || chunk_len(chunk_of(i, n, reverse), len) < kTok) {
       if (!wait(&b->mapped, maps & 1, gd)) return;
@@ -358,8 +374,8 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
     if (i < nx) {
       if (!wait(&b->w_full, i & 1, gd)) return;
       tc_fence_after();
-      mma_outer<D, D>(tmem + P::kColDX, b0, c0, false);
-      mma_outer<D, D>(tmem + P::kColDX, a0, c0, true);
+      mma_outer<D, D>(tmem + P::kColDX, b0, c0, D == 128);
+      mma_outer<D, D>(tmem + P::kColDX, lo, c0, true);
       if (terms > 2) mma_outer<D, D>(tmem + P::kColDX, xt, c0, true);
       mma_commit(&b->dx_full);
     }
@@ -369,38 +385,30 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
 
 // Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  Split: the two warps of a quadrant take
 // every other block of 32 scores and a half of the output columns each.
-// 16 columns of a row: one whole 32-byte sector in one store where rows are aligned to that.
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, uint4 a, uint4 b, bool live, bool wide) {
-  const int w = live && wide, n = live && !wide;
+// 16 lanes x 32 columns: registers 4 g + {0, 1} are columns 8 g + 2 (l % 4) + {0, 1} of row l / 4, 4 g + {2, 3}
+// those of row l / 4 + 8.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float* v) {
+  uint32_t r[16];
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %9, 0;\n\t"
-      "setp.ne.b32 q, %10, 0;\n\t"
-      "@p st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
-      "@q st.global.v4.b32 [%0], {%1,%2,%3,%4};\n\t"
-      "@q st.global.v4.b32 [%0 + 16], {%5,%6,%7,%8};\n\t}" ::"l"(dst),
-      "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w), "r"(w), "r"(n)
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// The reverse of tmem_ld16x32.
+__device__ __forceinline__ void tmem_st16x32(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
       : "memory");
 }
 
-// 16 lanes x 64 columns: registers 4 g + {0, 1} are columns 8 g + 2 (l % 4) + {0, 1} of row l / 4, 4 g + {2, 3}
-// those of row l / 4 + 8.
-__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// The four lanes of a group of four hold pairs e[2 k], e[2 k + 1], k = 0 .. 3: lane q gets pair q of lane k as
-// its pair k.
+// The four lanes of a group of four hold e[0 .. 3]: lane q gets element q of lane k as its element k.
 __device__ __forceinline__ void turn4(uint32_t* e, int lane) {
 #pragma unroll
   for (int s = 1; s <= 2; s <<= 1) {
@@ -408,15 +416,12 @@ __device__ __forceinline__ void turn4(uint32_t* e, int lane) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (k & s) continue;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint32_t &a = e[2 * k + w], &b = e[2 * (k | s) + w];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, s);
-        if (up)
-          a = got;
-        else
-          b = got;
-      }
+      uint32_t &a = e[k], &b = e[k | s];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, s);
+      if (up)
+        a = got;
+      else
+        b = got;
     }
   }
 }
@@ -429,8 +434,7 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
   const int n = b->ctx.n, all = b->ctx.len, reverse = b->ctx.reverse, row0 = b->ctx.row0, xf = b->ctx.fx;
   const int d0 = half * 64, d1 = min(b->ctx.d, d0 + 64);
   const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16);
-  const float scale = b->ctx.scale, scale1 = scale * exp2f(b->ctx.lg);  // scale gamma
-  const bool wide = b->ctx.wide != 0;
+  const float gamma = decay_pow(b->ctx.lg, 1);
   const long long sn = b->ctx.out_n, xsn = b->ctx.x_n;
   __nv_bfloat16* out = b->ctx.out;
   const __nv_bfloat16* xin = b->ctx.x;
@@ -459,7 +463,7 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
           const float fx = f[-x];
-          v[x] = fx != 0.f ? v[x] * fx : 0.f;  // (zero stays zero beside an infinite score)
+          v[x] = fx != 0.f ? v[x] * fx : 0.f;  // (a weight of zero beside an infinite score)
         }
 #pragma unroll
         for (int x = 0; x < 16; ++x) wj[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
@@ -482,37 +486,55 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
 
     if (!wait_warp(&b->o_full, i & 1, gd)) return;
     tc_fence_after();
-    // 16 rows at a time: lane l holds columns 8 g + 2 (l % 4) + {0, 1} of rows l / 4 and l / 4 + 8; the four
-    // lanes of a row turn their pairs round, so that each has 16 columns in a row and they store 128 bytes
+    // 16 rows and 32 columns at a time: lane l holds columns 8 g + 2 (l % 4) + {0, 1} of rows l / 4 and l / 4 + 8;
+    // the four lanes of a row turn their pairs round, so that each has 8 columns in a row and they store 64 bytes
 #pragma unroll 1
     for (int hh = 0; hh < 2; ++hh) {
-      float u[32], v[32];
-      const uint32_t tr = tl + ((uint32_t)(16 * hh) << 16);
-      tmem_ld16x64(tr + P::kColInter + d0, u);
-      tmem_ld16x64(tr + P::kColIntra + d0, v);
-      tmem_ld_wait();
+      float wi[2];
+      bool live[2];
+      __nv_bfloat16* dst[2];
+      const __nv_bfloat16* xp[2] = {nullptr, nullptr};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int rw = 32 * qd + 16 * hh + 8 * k + (lane >> 2);
-        const bool live = rw < len;
-        const float wi = live ? scale1 * b->decay[reverse ? kTok - len + rw : 32 + rw] : 0.f;
         const long long at = (long long)(row0 + ch * kTok + rw);
-        uint32_t e[8];
+        live[k] = rw < len;
+        wi[k] = live[k] ? gamma * b->decay[reverse ? kTok - len + rw : 32 + rw] : 0.f;
+        dst[k] = out + at * sn + d0 + 8 * (lane & 3);
+        if (DERIV) xp[k] = xin + at * xsn + d0 + 2 * (lane & 3);
+      }
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float x0 = fmaf(wi, u[4 * g + 2 * k], scale * v[4 * g + 2 * k]);
-          float x1 = fmaf(wi, u[4 * g + 2 * k + 1], scale * v[4 * g + 2 * k + 1]);
-          if (DERIV && live && d0 + 8 * g < d1) {
-            const uint32_t xx = *reinterpret_cast<const uint32_t*>(xin + at * xsn + d0 + 8 * g + 2 * (lane & 3));
-            x0 *= ret_dphi(__uint_as_float(xx << 16), xf);
-            x1 *= ret_dphi(__uint_as_float(xx & 0xffff0000u), xf);
-          }
-          e[g] = pack_bf16(x0, x1);
+      for (int cc = 0; cc < 64; cc += 32) {
+        float u[16], v[16];
+        const uint32_t tr = tl + ((uint32_t)(16 * hh) << 16) + d0 + cc;
+        tmem_ld16x32(tr + P::kColInter, u);
+        tmem_ld16x32(tr + P::kColIntra, v);
+        uint32_t xx[2][4];
+        if (DERIV) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              xx[k][g] = live[k] && d0 + cc + 8 * g < d1 ? *reinterpret_cast<const uint32_t*>(xp[k] + cc + 8 * g) : 0u;
         }
-        turn4(e, lane);
-        const int col = d0 + 16 * (lane & 3);
-        store16(out + at * sn + col, make_uint4(e[0], e[2], e[4], e[6]), make_uint4(e[1], e[3], e[5], e[7]),
-                live && col < d1, wide);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t e[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float x0 = fmaf(wi[k], u[4 * g + 2 * k], v[4 * g + 2 * k]);
+            float x1 = fmaf(wi[k], u[4 * g + 2 * k + 1], v[4 * g + 2 * k + 1]);
+            if (DERIV) {
+              x0 *= ret_dphi(__uint_as_float(xx[k][g] << 16), xf);
+              x1 *= ret_dphi(__uint_as_float(xx[k][g] & 0xffff0000u), xf);
+            }
+            e[g] = pack_bf16(x0, x1);
+          }
+          turn4(e, lane);
+          if (live[k] && d0 + cc + 8 * (lane & 3) < d1)
+            *reinterpret_cast<uint4*>(dst[k] + cc) = make_uint4(e[0], e[1], e[2], e[3]);
+        }
       }
     }
     tc_fence_before();
@@ -521,104 +543,149 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
   }
 }
 
-// X warps.  B w and the feature maps: token row = 32 (warp % 4) + lane.  X: TMEM lane quadrant = warp % 4,
-// row c of X a lane (D = 64: M = 64 puts 16 rows into the first lanes of each quadrant).  Columns 64 half ..
+// W warps, token row = 32 (warp % 4) + lane: the feature maps of a chunk and zeros behind the sequence (before
+// its scores), then B w (after them).
 template <int D>
-__device__ __noinline__ void pass_state(uint8_t* sm, PassBars* b, int warp, int lane) {
+__device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int lane) {
   using P = PassTile<D>;
-  const int qd = warp & 3, row = 32 * qd + lane, half = P::kSplit == 1 ? 0 : (warp - P::kWarpX) >> 2;
-  const int d0 = half * 64, j0 = half * 8;
+  const int row = 32 * (warp & 3) + lane;
   const int d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
   const int terms = b->ctx.terms, fa = b->ctx.fa, fb = b->ctx.fb, fc = b->ctx.fc;
-  const bool mapped = b->ctx.mapped(), anew = terms > 2 && fb != kFeatIdentity;  // phi(b) in fp32 for the state
+  const bool mapped = b->ctx.mapped();
   const float lg = b->ctx.lg;
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
-  const int xr = D == 128 ? row : 16 * qd + lane;           // row of X
-  const bool has = (D == 128 || lane < 16) && xr < d;
-  const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16);
-  uint8_t* xt = sm + P::kOffX;
-  const float* from = b->ctx.from;
-  const bool from_t = b->ctx.from_t != 0;
-  float X[64];
-#pragma unroll
-  for (int e = 0; e < 64; e += 4) {
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (from != nullptr && has && d0 + e < d) {
-      const int c0 = d0 + e;
-      if (from_t)
-        u = make_float4(__ldcg(from + c0 * d + xr), __ldcg(from + (c0 + 1) * d + xr), __ldcg(from + (c0 + 2) * d + xr),
-                        __ldcg(from + (c0 + 3) * d + xr));
-      else
-        u = __ldcg(reinterpret_cast<const float4*>(from + xr * d + c0));
+  uint8_t *at = sm + P::kOffA, *lo = sm + P::kOffLo, *lo2 = sm + P::kOffX;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int s = i % kStages, ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
+    uint8_t* bt = sm + P::kOffBC + s * 2 * P::kOp;
+    if (mapped || len < kTok) {
+      if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return;
+      if (fa != kFeatIdentity) map_row<D>(at, row, 0, kTok, d, fa);
+      if (fb != kFeatIdentity || len < kTok) map_row<D>(bt, row, 0, len, d, fb);
+      if (fc != kFeatIdentity || len < kTok) map_row<D>(bt + P::kOp, row, 0, len, d, fc);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->mapped);
     }
-    X[e] = u.x;
-    X[e + 1] = u.y;
-    X[e + 2] = u.z;
-    X[e + 3] = u.w;
+    if (i >= nx) return;
+    // B has been read by the scores, the second part by the last dX; the third part takes X's tile, once inter
+    // has read it
+    if (!wait_warp(&b->s_full, i & 1, gd) || (i > 0 && !wait_warp(&b->dx_full, (i - 1) & 1, gd)) ||
+        (terms > 2 && !wait_warp(&b->in_full, i & 1, gd)))
+      return;
+    const float w = row < len ? decay_pow(lg, reverse ? row : len - 1 - row) : 0.f;
+    if (terms > 2 && fb != kFeatIdentity) {  // phi(b) in fp32 for the state
+      const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
+      weigh_phi_row<D, 3>(bt, lo, lo2, row, 0, w, raw, d, fb);
+    } else if (terms > 2) {
+      weigh_row<D, 3>(bt, lo, lo2, row, 0, w);
+    } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
+      weigh_row<D, 2>(bt, lo, nullptr, row, 0, w);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b->w_full);
   }
-  auto publish = [&] {
-    if (D == 128 || lane < 16) {
+}
+
+// X warps.  TMEM lane quadrant = warp % 4: rows 32 quadrant .. of X, or with D = 64 (M = 64) 16 quadrant .. in its
+// first 16 lanes; 16 rows and 32 columns at a time, a lane's elements as in tmem_ld16x32.
+template <int D>
+__device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane) {
+  using P = PassTile<D>;
+  constexpr int kBlocks = D == 128 ? 8 : 2;                 // of 16 x 32 elements
+  const int qd = warp & 3, d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
+  const float lg = b->ctx.lg;
+  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
+  const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16) + P::kColDX;
+  uint8_t* xt = sm + P::kOffX;
+  float X[D == 128 ? 16 : 32];
+  // block k: rows r, r + 8, columns c0 + 8 g + {0, 1}
+  auto row_of = [&](int k) { return (D == 128 ? 32 * qd + 16 * (k / 4) : 16 * qd) + (lane >> 2); };
+  auto col_of = [&](int k) { return 32 * (k % (D / 32)); };
+  auto tmem_of = [&](int k) { return tl + ((uint32_t)(D == 128 ? 16 * (k / 4) : 0) << 16) + (uint32_t)col_of(k); };
+  auto tile = [&](int k, const float* v) {
+    const int r = row_of(k);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) *piece(xt, D, xr, j0 + j) = pack8(X + 8 * j);
+    for (int g = 0; g < 4; ++g) {
+      reinterpret_cast<uint32_t*>(piece(xt, D, r, col_of(k) / 8 + g))[lane & 3] = pack_bf16(v[4 * g], v[4 * g + 1]);
+      reinterpret_cast<uint32_t*>(piece(xt, D, r + 8, col_of(k) / 8 + g))[lane & 3] = pack_bf16(v[4 * g + 2], v[4 * g + 3]);
     }
+  };
+  auto publish = [&] {
+    if (D == 128) tmem_st_wait();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->x_full);
   };
-  auto map = [&](int i) -> bool {  // feature maps of chunk i, rows behind the sequence cleared in B and C
-    const int len = chunk_len(chunk_of(i, n, reverse), all);
-    if (!mapped && len == kTok) return true;
-    if (!wait_warp(&b->full[i % kStages], (i / kStages) & 1, gd)) return false;
-    uint8_t* st = sm + (i % kStages) * P::kStage;
-    if (fa != kFeatIdentity) map_row<64>(st, row, j0, kTok, d, fa);
-    if (fb != kFeatIdentity || len < kTok) map_row<64>(st + P::kOp, row, j0, len, d, fb);
-    if (fc != kFeatIdentity || len < kTok) map_row<64>(st + 2 * P::kOp, row, j0, len, d, fc);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&b->mapped);
-    return true;
-  };
-  if (!map(0)) return;
+  {
+    const float* from = b->ctx.from;
+    const bool from_t = b->ctx.from_t != 0;
+    const float wl = decay_pow(lg, chunk_len(chunk_of(0, n, reverse), all));
+#pragma unroll(D == 128 ? 1 : 2)
+    for (int k = 0; k < kBlocks; ++k) {
+      float* v = X + (D == 128 ? 0 : 16 * k);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const int r = row_of(k) + 8 * (m & 1), c = col_of(k) + 8 * (m >> 1) + 2 * (lane & 3);
+        float2 u = make_float2(0.f, 0.f);
+        if (from != nullptr && r < d && c < d) {
+          if (from_t)
+            u = make_float2(__ldcg(from + c * d + r), __ldcg(from + (c + 1) * d + r));
+          else
+            u = __ldcg(reinterpret_cast<const float2*>(from + r * d + c));
+        }
+        v[4 * (m >> 1) + 2 * (m & 1)] = u.x;
+        v[4 * (m >> 1) + 2 * (m & 1) + 1] = u.y;
+      }
+      tile(k, v);
+      if (D == 128) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] *= wl;
+        tmem_st16x32(tmem_of(k), v);
+      }
+    }
+  }
   publish();
 #pragma unroll 1
   for (int i = 0; i < nx; ++i) {
-    const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
-    uint8_t* st = sm + (i % kStages) * P::kStage;
-    // B has been read by the scores, A (and the old X) by inter
-    if (!wait_warp(&b->s_full, i & 1, gd) || !wait_warp(&b->in_full, i & 1, gd)) return;
-    const float w = row < len ? b->decay[reverse ? kTok - 1 - row : 32 + len - 1 - row] : 0.f;
-    if (anew) {
-      const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
-      weigh_phi_row<64, 3>(st + P::kOp, st, xt, row, j0, w, raw, d, fb);
-    } else if (terms > 2) {
-      weigh_row<64, 3>(st + P::kOp, st, xt, row, j0, w);
-    } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
-      weigh_row<64, 2>(st + P::kOp, st, xt, row, j0, w);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&b->w_full);
-    if (i + 1 < n && !map(i + 1)) return;
-    const float wl = decay_pow(lg, len);
-    if (!wait_warp(&b->dx_full, i & 1, gd)) return;
+    const bool more = i + 1 < n;
+    const float wl = decay_pow(lg, chunk_len(chunk_of(D == 128 && more ? i + 1 : i, n, reverse), all));
+    float* to = more ? nullptr : b->ctx.to;
+    // (inter has read the last tile)
+    if (!wait_warp(&b->in_full, i & 1, gd) || !wait_warp(&b->dx_full, i & 1, gd)) return;
     tc_fence_after();
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
+#pragma unroll(D == 128 ? 1 : 2)
+    for (int k = 0; k < kBlocks; ++k) {
       float u[16];
-      tmem_ld16(tl + P::kColDX + d0 + 16 * g, u);
+      float* v = D == 128 ? u : X + 16 * k;
+      tmem_ld16x32(tmem_of(k), u);
       tmem_ld_wait();
+      if (D != 128) {
 #pragma unroll
-      for (int x = 0; x < 16; ++x) X[16 * g + x] = fmaf(wl, X[16 * g + x], u[x]);
+        for (int x = 0; x < 16; ++x) v[x] = fmaf(wl, v[x], u[x]);
+      }
+      if (more) {
+        tile(k, v);
+        if (D == 128) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] *= wl;
+          tmem_st16x32(tmem_of(k), v);
+        }
+      } else if (to != nullptr) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int r = row_of(k) + 8 * (m & 1), c = col_of(k) + 8 * (m >> 1) + 2 * (lane & 3);
+          if (r < d && c < d)
+            *reinterpret_cast<float2*>(to + r * d + c) =
+                make_float2(v[4 * (m >> 1) + 2 * (m & 1)], v[4 * (m >> 1) + 2 * (m & 1) + 1]);
+        }
+        __syncwarp();
+      }
     }
-    if (i + 1 < n) publish();
-  }
-  float* to = b->ctx.to;
-  if (to != nullptr && has) {
-#pragma unroll
-    for (int e = 0; e < 64; e += 4)
-      if (d0 + e < d)
-        *reinterpret_cast<float4*>(to + xr * d + d0 + e) = make_float4(X[e], X[e + 1], X[e + 2], X[e + 3]);
+    if (more) publish();
   }
 }
 
@@ -640,11 +707,12 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
       mbar_init(&b->full[s], 1);
       mbar_init(&b->empty[s], 1);
     }
-    for (uint64_t* m : {&b->s_full, &b->in_full, &b->dx_full, &b->o_full, &b->fin}) mbar_init(m, 1);
-    for (uint64_t* m : {&b->mapped, &b->p_full, &b->w_full, &b->x_full, &b->o_free}) mbar_init(m, 4 * P::kSplit);
+    for (uint64_t* m : {&b->a_full, &b->s_full, &b->in_full, &b->dx_full, &b->o_full, &b->fin}) mbar_init(m, 1);
+    for (uint64_t* m : {&b->mapped, &b->w_full, &b->x_full}) mbar_init(m, 4);
+    for (uint64_t* m : {&b->p_full, &b->o_free}) mbar_init(m, 4 * P::kSplit);
     for (int i = 0; i < 4; ++i) mbar_init(&b->read[i], 2);
     b->abort = 0;
-    b->issued = 0;
+    b->issued = b->issued_a = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == 64) {
@@ -673,9 +741,7 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     c.fc = p.c.feature;
     c.fx = p.x.feature;
     c.d = r.d;
-    c.wide = t.wide_out[z];
     c.lg = lg;
-    c.scale = r.scale;
     c.out = static_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + ret_base(r, p.out, sg.seq, h);
     c.x = p.x.p == nullptr ? nullptr : static_cast<const __nv_bfloat16*>(p.x.p) + ret_base(r, p.x, sg.seq, h);
     c.b = static_cast<const __nv_bfloat16*>(p.b.p) + ret_base(r, p.b, sg.seq, h);
@@ -690,7 +756,7 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
   }
   if (threadIdx.x >= P::kThreads - kTok - 32) {
     const int i = threadIdx.x - (P::kThreads - kTok - 32), n = r.pass[z].reverse ? kTok - 1 - i : i - 32;
-    b->decay[i] = n >= 0 ? decay_pow(lg, n) : 0.f;
+    b->decay[i] = n >= 0 ? r.scale * decay_pow(lg, n) : 0.f;
   }
   if (warp == kWarpMma) {
     tmem_alloc(&b->tbase, P::kCols);
@@ -714,13 +780,15 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
       mma_commit(&b->fin);
     }
     __syncwarp();
-  } else if (warp < P::kWarpX) {
+  } else if (warp < P::kWarpW) {
     if (b->ctx.x == nullptr)
       pass_out<D, false>(b, warp, lane);
     else
       pass_out<D, true>(b, warp, lane);
+  } else if (warp < P::kWarpX) {
+    pass_weigh<D>(sm, b, warp, lane);
   } else {
-    pass_state<D>(sm, b, warp, lane);
+    pass_x<D>(sm, b, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -728,6 +796,7 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
   if (threadIdx.x == 0) {
     drain(&b->fin, 0);
     if (b->abort) {
+      if (b->issued_a > 0) drain(&b->a_full, (b->issued_a - 1) & 1);
       for (int q = b->issued > kStages ? b->issued - kStages : 0; q < b->issued; ++q)
         drain(&b->full[q % kStages], (q / kStages) & 1);
       atomicOr(r.status, 1u);
@@ -941,10 +1010,6 @@ int map_of(TcArgs* t, int* used, const RetTensor** seen, const RetTensor& x, boo
   return i;
 }
 
-bool wide_rows(const RetTensor& x) {
-  return (reinterpret_cast<uintptr_t>(x.p) & 31) == 0 && x.sb % 16 == 0 && x.sh % 16 == 0 && x.sn % 16 == 0;
-}
-
 template <int D>
 cudaError_t launch(const TcArgs& t, cudaStream_t st) {
   static SmemOptIn opt_pass, opt_sum;
@@ -978,7 +1043,6 @@ cudaError_t tc_retention_launch(const RetArgs& a, cudaStream_t st) {
     t.ia[i] = map_of(&t, &used, seen, a.pass[i].a, &ok);
     t.ib[i] = map_of(&t, &used, seen, a.pass[i].b, &ok);
     t.ic[i] = map_of(&t, &used, seen, a.pass[i].c, &ok);
-    t.wide_out[i] = wide_rows(a.pass[i].out);
   }
   if (!ok) return cudaErrorInvalidValue;
   return a.d == 128 ? launch<128>(t, st) : launch<64>(t, st);
