@@ -15,13 +15,13 @@
 // the B tile and in a tile of its own: 2^-16 of a term) where only bf16 outputs come of it, of three (the
 // last over the tile of X: 2^-24) in the segment whose state is returned in fp32.
 //
-// Roles (D = 128: 18 warps and one CTA an SM, D = 64: 14 warps and two):
+// Roles (D = 128: 22 warps and one CTA an SM, D = 64: 14 warps and two):
 //   warp 0       TMA producer: the tiles of a chunk, B and C two chunks deep, A one
 //   warp 1       MMA issuer
 //   out warps    scores -> P, then out = scale (intra + gamma^(i+1) inter) to global memory (D = 128:
 //                eight warps, each with half of the scores and of the columns; D = 64: four)
 //   4 W warps    feature maps in place, B w
-//   4 X warps    X and its bf16 tile for the next chunk
+//   X warps      X and its bf16 tile for the next chunk (D = 128: eight, D = 64: four)
 // A chunk's B w does not wait for the X that enters it, so the serial chain from one X to the next is
 // inter, intra, dX and the update.  What this costs is shared memory's bandwidth: with D = 128 a chunk's
 // products read 2.5 thousand cycles' worth of it (128 bytes a cycle; 128 x 128 x 16 from shared memory
@@ -128,12 +128,11 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-// phi over D of the columns, from 8 j0, of row r of a tile in place (those below d), zeros for a row behind
-// the sequence.
+// phi over the d columns of row r of a tile in place, zeros for a row behind the sequence.
 template <int D>
-__device__ __noinline__ void map_row(uint8_t* tile, int r, int j0, int len, int d, int feature) {
+__device__ __noinline__ void map_row(uint8_t* tile, int r, int len, int d, int feature) {
 #pragma unroll 2
-  for (int j = j0; j < j0 + D / 8; ++j) {
+  for (int j = 0; j < D / 8; ++j) {
     uint4* p = piece(tile, kTok, r, j);
     if (r >= len) {
       *p = make_uint4(0, 0, 0, 0);
@@ -155,54 +154,81 @@ __device__ __forceinline__ void remainder8(float* f, uint4 h) {
   for (int x = 0; x < 8; ++x) f[x] -= g[x];
 }
 
-// f[0..8) as a sum of bf16 numbers at piece j of row r: over the B tile, the remainder in lo, with T = 3 the
+// f[0..8) as a sum of three bf16 numbers at piece j of row r: over the B tile, the remainder in lo, the
 // remainder of that in lo2.
-template <int T>
 __device__ __forceinline__ void split8(float* f, uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int j) {
   const uint4 h = pack8(f);
   *piece(hi, kTok, r, j) = h;
   remainder8(f, h);
   const uint4 l = pack8(f);
   *piece(lo, kTok, r, j) = l;
-  if (T > 2) {
-    remainder8(f, l);
-    *piece(lo2, kTok, r, j) = pack8(f);
-  }
+  remainder8(f, l);
+  *piece(lo2, kTok, r, j) = pack8(f);
 }
 
-// D columns, from 8 jb, of row r of B times w, split.  w = 0: zeros, whatever the tile holds.
-template <int D, int T>
-__device__ __forceinline__ void weigh_row(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w) {
+// Row r (D columns) of B times w as a sum of three bf16 numbers.
+template <int D>
+__device__ __forceinline__ void weigh_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, float w) {
 #pragma unroll 1
-  for (int j0 = jb; j0 < jb + D / 8; j0 += 2) {
+  for (int j0 = 0; j0 < D / 8; j0 += 2) {
     uint4 u[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) u[j] = *piece(hi, kTok, r, j0 + j);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float f[8];
-      unpack8(w == 0.f ? make_uint4(0, 0, 0, 0) : u[j], f);
+      unpack8(u[j], f);
 #pragma unroll
       for (int x = 0; x < 8; ++x) f[x] *= w;
-      split8<T>(f, hi, lo, lo2, r, j0 + j);
+      split8(f, hi, lo, lo2, r, j0 + j);
     }
   }
 }
 
-// The same of phi of the row, in fp32, over its d columns: of the row in global memory (raw) where the tile
-// holds the rounded phi already.
-template <int D, int T>
-__device__ __noinline__ void weigh_phi_row(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w,
-                                           const __nv_bfloat16* raw, int d, int feature) {
+// Row r (D columns) of B times w as a sum of two bf16 numbers, in packed bf16 arithmetic: with w = wh + wl in
+// bf16, hi = round(b wh), b wh - hi is exact (16 bits less the first 8), lo = round(b wl + that).  A quarter of
+// the instructions of the same in fp32.
+template <int D>
+__device__ __forceinline__ void weigh_row2(uint8_t* hi, uint8_t* lo, int r, float w) {
+  const __nv_bfloat16 wh1 = __float2bfloat16_rn(w);
+  const __nv_bfloat162 wh = __bfloat162bfloat162(wh1);
+  const __nv_bfloat162 wl = __bfloat162bfloat162(__float2bfloat16_rn(w - __bfloat162float(wh1)));
 #pragma unroll 1
-  for (int j = jb; j < jb + D / 8; ++j) {
+  for (int j0 = 0; j0 < D / 8; j0 += 4) {
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = *piece(hi, kTok, r, j0 + j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t x[4] = {u[j].x, u[j].y, u[j].z, u[j].w}, h[4], l[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&x[m]);
+        const __nv_bfloat162 hv = __hmul2_rn(v, wh);
+        const __nv_bfloat162 lv = __hfma2(v, wl, __hfma2(v, wh, __hneg2(hv)));
+        h[m] = *reinterpret_cast<const uint32_t*>(&hv);
+        l[m] = *reinterpret_cast<const uint32_t*>(&lv);
+      }
+      *piece(hi, kTok, r, j0 + j) = make_uint4(h[0], h[1], h[2], h[3]);
+      *piece(lo, kTok, r, j0 + j) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
+}
+
+// weigh_row3 of phi of the row, in fp32, over its d columns: of the row in global memory (raw) where the tile
+// holds the rounded phi already.
+template <int D>
+__device__ __noinline__ void weigh_phi_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, float w,
+                                            const __nv_bfloat16* raw, int d, int feature) {
+#pragma unroll 1
+  for (int j = 0; j < D / 8; ++j) {
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (w != 0.f && 8 * j < d) {
       unpack8(raw != nullptr ? *reinterpret_cast<const uint4*>(raw + 8 * j) : *piece(hi, kTok, r, j), f);
 #pragma unroll
       for (int x = 0; x < 8; ++x) f[x] = w * ret_phi(f[x], feature);
     }
-    split8<T>(f, hi, lo, lo2, r, j);
+    split8(f, hi, lo, lo2, r, j);
   }
 }
 
@@ -213,6 +239,17 @@ __device__ __forceinline__ void mma_outer(uint32_t d, uint32_t a, uint32_t b, bo
 #pragma unroll
   for (int k = 0; k < kTok / 16; ++k)
     mma_bf16(d, da + k * (2048 >> 4), db + k * (2048 >> 4), idesc_bf16_f32(M, N, 1, 1), acc || k > 0);
+}
+
+// Prefetch of one operand's chunk into L2.
+template <int D>
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int row, int h, int seq) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(64 * c), "r"(row), "r"(h), "r"(seq)
+                 : "memory");
 }
 
 // TMA of one operand's chunk: D / 64 atoms.
@@ -239,7 +276,7 @@ struct PassTile {
   static constexpr int kPerSm = D == 128 ? 1 : 2;
   static constexpr int kSplit = D / 64;                 // out warps of a TMEM lane quadrant
   static constexpr int kWarpW = kWarpOut + 4 * kSplit, kWarpX = kWarpW + 4;
-  static constexpr int kThreads = 32 * (kWarpX + 4);
+  static constexpr int kThreads = 32 * (kWarpX + 4 * kSplit);
 };
 
 // What the roles share.  It is kept in shared memory and the roles are functions of their own, so that none
@@ -273,7 +310,6 @@ struct PassBars {
   uint64_t mapped;    // feature maps applied / rows behind the sequence cleared (W warps)
   uint64_t s_full;    // scores
   uint64_t in_full;   // inter
-  uint64_t read[4];   // D = 128: a quadrant's scores read by both its out warps
   uint64_t p_full;    // P in TMEM (out warps)
   uint64_t w_full;    // B w (W warps)
   uint64_t dx_full;   // dX
@@ -307,6 +343,7 @@ __device__ __noinline__ void pass_producer(uint8_t* sm, PassBars* b) {
     mbar_arrive_expect_tx(&b->full[s], 2 * P::kOp);
     load_tile<D>(st, c.mb, row(i), c.hb, c.bb, &b->full[s]);
     load_tile<D>(st + P::kOp, c.mc, row(i), c.hc, c.bc, &b->full[s]);
+    prefetch_tile<D>(c.ma, row(i), c.ha, c.ba);  // A has one tile: it is asked for when the last one has been read
     b->issued = i + 1;
   };
   load_bc(0);
@@ -367,8 +404,8 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
       const uint64_t dc = smem_desc(c0, kAtom, 1024);
 #pragma unroll
       for (int k = 0; k < kTok / 16; ++k)
-        mma_bf16_ts(tmem + P::kColIntra, tmem + P::kColS + 8 * k, dc + k * (2048 >> 4), idesc_bf16_f32(128, D, 0, 1),
-                    k > 0);
+        mma_bf16_ts(tmem + P::kColIntra, tmem + P::kColS + 8 * k + (D == 128 && k >= 4 ? 32 : 0), dc + k * (2048 >> 4),
+                    idesc_bf16_f32(128, D, 0, 1), k > 0);
     }
     mma_commit(&b->o_full);
     if (i < nx) {
@@ -384,7 +421,7 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
 }
 
 // Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  Split: the two warps of a quadrant take
-// every other block of 32 scores and a half of the output columns each.
+// half of the scores and of the output columns each.
 // 16 lanes x 32 columns: registers 4 g + {0, 1} are columns 8 g + 2 (l % 4) + {0, 1} of row l / 4, 4 g + {2, 3}
 // those of row l / 4 + 8.
 __device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float* v) {
@@ -445,39 +482,32 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
     const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
     if (!wait_warp(&b->s_full, i & 1, gd)) return;
     tc_fence_after();
-    // P of block j of the scores goes to columns 16 j .., over scores: they are written when all are read
-    uint32_t w[S == 1 ? 1 : 2][16];
-#pragma unroll(S == 1 ? 1 : 2)
-    for (int jj = 0; jj < 4 / S; ++jj) {
-      const int j = S * jj + half;
-      uint32_t* wj = w[S == 1 ? 0 : jj];
+    // P of block j of the scores (32 columns) goes over scores that this warp has read: to columns 16 j .., with
+    // two warps a quadrant those of tokens 64 .. to 64 + 16 (j - 2) ..
+#pragma unroll 1
+    for (int j = half * 2; j < half * 2 + 4 / S; ++j) {
+      const uint32_t dst = tl + P::kColS + 16 * j + half * 32;
       if (reverse ? j < qd : j > qd) {
+        uint32_t w[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) wj[x] = 0;
-      } else {
-        float v[32];
-        tmem_ld16(tl + P::kColS + 32 * j, v);
-        tmem_ld16(tl + P::kColS + 32 * j + 16, v + 16);
-        const float* f = decay + (row - 32 * j);
-        tmem_ld_wait();
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float fx = f[-x];
-          v[x] = fx != 0.f ? v[x] * fx : 0.f;  // (a weight of zero beside an infinite score)
-        }
-#pragma unroll
-        for (int x = 0; x < 16; ++x) wj[x] = pack_bf16(v[2 * x], v[2 * x + 1]);
+        for (int x = 0; x < 16; ++x) w[x] = 0;
+        tmem_st16u(dst, w);
+        continue;
       }
-      if (S == 1) tmem_st16u(tl + P::kColS + 16 * j, wj);  // in the order of j: behind the scores read so far
-    }
-    if (S == 2) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->read[qd]);
-      if (!wait_warp(&b->read[qd], i & 1, gd)) return;  // the other warp of the quadrant has read its scores
-      tc_fence_after();
+      const float* f = decay + (row - 32 * j);
+      // the masked columns x of the diagonal block (whose score may be infinite): forward above the lane, reverse below
+      const uint32_t keep = j != qd ? 0xffffffffu : reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+      float v[32];
+      tmem_ld16(tl + P::kColS + 32 * j, v);
+      tmem_ld16(tl + P::kColS + 32 * j + 16, v + 16);
+      tmem_ld_wait();
+      uint32_t w[16];
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj) tmem_st16u(tl + P::kColS + 16 * (S * jj + half), w[S == 1 ? 0 : jj]);
+      for (int x = 0; x < 16; ++x) {
+        const float p0 = v[2 * x] * f[-2 * x], p1 = v[2 * x + 1] * f[-2 * x - 1];
+        w[x] = pack_bf16((keep >> (2 * x)) & 1u ? p0 : 0.f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.f);
+      }
+      tmem_st16u(dst, w);
     }
     tmem_st_wait();
     tc_fence_before();
@@ -561,9 +591,9 @@ __device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int 
     uint8_t* bt = sm + P::kOffBC + s * 2 * P::kOp;
     if (mapped || len < kTok) {
       if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return;
-      if (fa != kFeatIdentity) map_row<D>(at, row, 0, kTok, d, fa);
-      if (fb != kFeatIdentity || len < kTok) map_row<D>(bt, row, 0, len, d, fb);
-      if (fc != kFeatIdentity || len < kTok) map_row<D>(bt + P::kOp, row, 0, len, d, fc);
+      if (fa != kFeatIdentity) map_row<D>(at, row, kTok, d, fa);
+      if (fb != kFeatIdentity || len < kTok) map_row<D>(bt, row, len, d, fb);
+      if (fc != kFeatIdentity || len < kTok) map_row<D>(bt + P::kOp, row, len, d, fc);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->mapped);
@@ -577,11 +607,11 @@ __device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int 
     const float w = row < len ? decay_pow(lg, reverse ? row : len - 1 - row) : 0.f;
     if (terms > 2 && fb != kFeatIdentity) {  // phi(b) in fp32 for the state
       const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
-      weigh_phi_row<D, 3>(bt, lo, lo2, row, 0, w, raw, d, fb);
+      weigh_phi_row3<D>(bt, lo, lo2, row, w, raw, d, fb);
     } else if (terms > 2) {
-      weigh_row<D, 3>(bt, lo, lo2, row, 0, w);
+      weigh_row3<D>(bt, lo, lo2, row, w);
     } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
-      weigh_row<D, 2>(bt, lo, nullptr, row, 0, w);
+      weigh_row2<D>(bt, lo, row, w);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -590,21 +620,22 @@ __device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int 
 }
 
 // X warps.  TMEM lane quadrant = warp % 4: rows 32 quadrant .. of X, or with D = 64 (M = 64) 16 quadrant .. in its
-// first 16 lanes; 16 rows and 32 columns at a time, a lane's elements as in tmem_ld16x32.
+// first 16 lanes; 16 rows and 32 columns at a time, a lane's elements as in tmem_ld16x32.  D = 128: the two warps
+// of a quadrant take half of the columns each.
 template <int D>
 __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane) {
   using P = PassTile<D>;
-  constexpr int kBlocks = D == 128 ? 8 : 2;                 // of 16 x 32 elements
-  const int qd = warp & 3, d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
+  constexpr int kBlocks = D == 128 ? 4 : 2;                 // of 16 x 32 elements
+  const int qd = warp & 3, half = D == 128 ? (warp - P::kWarpX) >> 2 : 0, d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
   const float lg = b->ctx.lg;
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
   const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16) + P::kColDX;
   uint8_t* xt = sm + P::kOffX;
   float X[D == 128 ? 16 : 32];
   // block k: rows r, r + 8, columns c0 + 8 g + {0, 1}
-  auto row_of = [&](int k) { return (D == 128 ? 32 * qd + 16 * (k / 4) : 16 * qd) + (lane >> 2); };
-  auto col_of = [&](int k) { return 32 * (k % (D / 32)); };
-  auto tmem_of = [&](int k) { return tl + ((uint32_t)(D == 128 ? 16 * (k / 4) : 0) << 16) + (uint32_t)col_of(k); };
+  auto row_of = [&](int k) { return (D == 128 ? 32 * qd + 16 * (k / 2) : 16 * qd) + (lane >> 2); };
+  auto col_of = [&](int k) { return 64 * half + 32 * (k % 2); };
+  auto tmem_of = [&](int k) { return tl + ((uint32_t)(D == 128 ? 16 * (k / 2) : 0) << 16) + (uint32_t)col_of(k); };
   auto tile = [&](int k, const float* v) {
     const int r = row_of(k);
 #pragma unroll
@@ -657,7 +688,7 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
     // (inter has read the last tile)
     if (!wait_warp(&b->in_full, i & 1, gd) || !wait_warp(&b->dx_full, i & 1, gd)) return;
     tc_fence_after();
-#pragma unroll(D == 128 ? 1 : 2)
+#pragma unroll 2
     for (int k = 0; k < kBlocks; ++k) {
       float u[16];
       float* v = D == 128 ? u : X + 16 * k;
@@ -708,9 +739,8 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
       mbar_init(&b->empty[s], 1);
     }
     for (uint64_t* m : {&b->a_full, &b->s_full, &b->in_full, &b->dx_full, &b->o_full, &b->fin}) mbar_init(m, 1);
-    for (uint64_t* m : {&b->mapped, &b->w_full, &b->x_full}) mbar_init(m, 4);
-    for (uint64_t* m : {&b->p_full, &b->o_free}) mbar_init(m, 4 * P::kSplit);
-    for (int i = 0; i < 4; ++i) mbar_init(&b->read[i], 2);
+    for (uint64_t* m : {&b->mapped, &b->w_full}) mbar_init(m, 4);
+    for (uint64_t* m : {&b->x_full, &b->p_full, &b->o_free}) mbar_init(m, 4 * P::kSplit);
     b->abort = 0;
     b->issued = b->issued_a = 0;
     fence_mbar_init();
@@ -918,14 +948,15 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
       // the remainders' tiles have been read by the MMAs of the chunk before
       if (i > 0) ok = wait_warp(&b->empty[(i - 1) % kStages], ((i - 1) / kStages) & 1, gd);
       if (!ok) break;
-      if (p.c.feature != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, 0, len, r.d, p.c.feature);
+      if (p.c.feature != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, r.d, p.c.feature);
+      if (len < kTok) map_row<D>(st, row, len, r.d, kFeatIdentity);
       const float w = row < len ? decay_pow(lg, p.reverse ? at : sg.len - 1 - at) : 0.f;
       if (p.b.feature != kFeatIdentity)
-        weigh_phi_row<D, 3>(st, lo, lo + P::kOp, row, 0, w, nullptr, r.d, p.b.feature);
+        weigh_phi_row3<D>(st, lo, lo + P::kOp, row, w, nullptr, r.d, p.b.feature);
       else if (terms > 2)
-        weigh_row<D, 3>(st, lo, lo + P::kOp, row, 0, w);
+        weigh_row3<D>(st, lo, lo + P::kOp, row, w);
       else
-        weigh_row<D, 2>(st, lo, nullptr, row, 0, w);
+        weigh_row2<D>(st, lo, row, w);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->ready[s]);
