@@ -317,8 +317,9 @@ mhla_path mhla_backward_path(int B, int H, int N, int d, int block_size, mhla_dt
  *     slot is outside [0, n_slots), or is the slot of a sequence before it, has
  *     none: see the entries.
  *   - Not-a-number or infinite values of a token reach its own sequence only;
- *     in retention_forward and retention_backward they may reach all 128
- *     tokens of the chunk that they are in, also those before them. */
+ *     in retention_forward and retention_backward they, and products
+ *     phi(q_t) . phi(k_s) that overflow, may reach all 128 tokens of the chunk
+ *     that they are in, also those before them. */
 
 /* Element strides of a [B, H, N, d] tensor. */
 typedef struct {

@@ -185,16 +185,16 @@ __device__ __forceinline__ void weigh_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo
   }
 }
 
-// Row r (D columns) of B times w as a sum of two bf16 numbers, in packed bf16 arithmetic: with w = wh + wl in
+// D columns, from 8 jb, of row r of B times w as a sum of two bf16 numbers, in packed bf16 arithmetic: with w = wh + wl in
 // bf16, hi = round(b wh), b wh - hi is exact (16 bits less the first 8), lo = round(b wl + that).  A quarter of
 // the instructions of the same in fp32.
 template <int D>
-__device__ __forceinline__ void weigh_row2(uint8_t* hi, uint8_t* lo, int r, float w) {
+__device__ __forceinline__ void weigh_row2(uint8_t* hi, uint8_t* lo, int r, int jb, float w) {
   const __nv_bfloat16 wh1 = __float2bfloat16_rn(w);
   const __nv_bfloat162 wh = __bfloat162bfloat162(wh1);
   const __nv_bfloat162 wl = __bfloat162bfloat162(__float2bfloat16_rn(w - __bfloat162float(wh1)));
 #pragma unroll 1
-  for (int j0 = 0; j0 < D / 8; j0 += 4) {
+  for (int j0 = jb; j0 < jb + D / 8; j0 += 4) {
     uint4 u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) u[j] = *piece(hi, kTok, r, j0 + j);
@@ -215,8 +215,8 @@ __device__ __forceinline__ void weigh_row2(uint8_t* hi, uint8_t* lo, int r, floa
   }
 }
 
-// weigh_row3 of phi of the row, in fp32, over its d columns: of the row in global memory (raw) where the tile
-// holds the rounded phi already.
+// weigh_row3 of phi of the row, in fp32, over its d columns: of the row in global memory (raw), the tile holds
+// the rounded phi already.
 template <int D>
 __device__ __noinline__ void weigh_phi_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, float w,
                                             const __nv_bfloat16* raw, int d, int feature) {
@@ -224,11 +224,29 @@ __device__ __noinline__ void weigh_phi_row3(uint8_t* hi, uint8_t* lo, uint8_t* l
   for (int j = 0; j < D / 8; ++j) {
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (w != 0.f && 8 * j < d) {
-      unpack8(raw != nullptr ? *reinterpret_cast<const uint4*>(raw + 8 * j) : *piece(hi, kTok, r, j), f);
+      unpack8(*reinterpret_cast<const uint4*>(raw + 8 * j), f);
 #pragma unroll
       for (int x = 0; x < 8; ++x) f[x] = w * ret_phi(f[x], feature);
     }
     split8(f, hi, lo, lo2, r, j);
+  }
+}
+
+// D columns, from 8 jb, of phi of row r of B times w as a sum of two bf16 numbers; w = 0: zeros.
+template <int D>
+__device__ __noinline__ void weigh_phi_row2(uint8_t* hi, uint8_t* lo, int r, int jb, float w, int d, int feature) {
+#pragma unroll 1
+  for (int j = jb; j < jb + D / 8; ++j) {
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (w != 0.f && 8 * j < d) {
+      unpack8(*piece(hi, kTok, r, j), f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) f[x] = w * ret_phi(f[x], feature);
+    }
+    const uint4 h = pack8(f);
+    *piece(hi, kTok, r, j) = h;
+    remainder8(f, h);
+    *piece(lo, kTok, r, j) = pack8(f);
   }
 }
 
@@ -422,6 +440,23 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
 
 // Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  Split: the two warps of a quadrant take
 // half of the scores and of the output columns each.
+// Two products / multiply-adds in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return r;
+}
+
 // 16 lanes x 32 columns: registers 4 g + {0, 1} are columns 8 g + 2 (l % 4) + {0, 1} of row l / 4, 4 g + {2, 3}
 // those of row l / 4 + 8.
 __device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float* v) {
@@ -495,8 +530,6 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
         continue;
       }
       const float* f = decay + (row - 32 * j);
-      // the masked columns x of the diagonal block (whose score may be infinite): forward above the lane, reverse below
-      const uint32_t keep = j != qd ? 0xffffffffu : reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
       float v[32];
       tmem_ld16(tl + P::kColS + 32 * j, v);
       tmem_ld16(tl + P::kColS + 32 * j + 16, v + 16);
@@ -504,8 +537,8 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
       uint32_t w[16];
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
-        const float p0 = v[2 * x] * f[-2 * x], p1 = v[2 * x + 1] * f[-2 * x - 1];
-        w[x] = pack_bf16((keep >> (2 * x)) & 1u ? p0 : 0.f, (keep >> (2 * x + 1)) & 1u ? p1 : 0.f);
+        const float2 p = mul2(make_float2(v[2 * x], v[2 * x + 1]), make_float2(f[-2 * x], f[-2 * x - 1]));
+        w[x] = pack_bf16(p.x, p.y);
       }
       tmem_st16u(dst, w);
     }
@@ -553,13 +586,13 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
           uint32_t e[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            float x0 = fmaf(wi[k], u[4 * g + 2 * k], v[4 * g + 2 * k]);
-            float x1 = fmaf(wi[k], u[4 * g + 2 * k + 1], v[4 * g + 2 * k + 1]);
+            float2 o = fma2(make_float2(wi[k], wi[k]), make_float2(u[4 * g + 2 * k], u[4 * g + 2 * k + 1]),
+                            make_float2(v[4 * g + 2 * k], v[4 * g + 2 * k + 1]));
             if (DERIV) {
-              x0 *= ret_dphi(__uint_as_float(xx[k][g] << 16), xf);
-              x1 *= ret_dphi(__uint_as_float(xx[k][g] & 0xffff0000u), xf);
+              o.x *= ret_dphi(__uint_as_float(xx[k][g] << 16), xf);
+              o.y *= ret_dphi(__uint_as_float(xx[k][g] & 0xffff0000u), xf);
             }
-            e[g] = pack_bf16(x0, x1);
+            e[g] = pack_bf16(o.x, o.y);
           }
           turn4(e, lane);
           if (live[k] && d0 + cc + 8 * (lane & 3) < d1)
@@ -611,7 +644,7 @@ __device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int 
     } else if (terms > 2) {
       weigh_row3<D>(bt, lo, lo2, row, w);
     } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
-      weigh_row2<D>(bt, lo, row, w);
+      weigh_row2<D>(bt, lo, row, 0, w);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -696,13 +729,16 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
       tmem_ld_wait();
       if (D != 128) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = fmaf(wl, v[x], u[x]);
+        for (int x = 0; x < 8; ++x)
+          reinterpret_cast<float2*>(v)[x] =
+              fma2(make_float2(wl, wl), reinterpret_cast<float2*>(v)[x], reinterpret_cast<float2*>(u)[x]);
       }
       if (more) {
         tile(k, v);
         if (D == 128) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] *= wl;
+          for (int x = 0; x < 8; ++x)
+            reinterpret_cast<float2*>(v)[x] = mul2(reinterpret_cast<float2*>(v)[x], make_float2(wl, wl));
           tmem_st16x32(tmem_of(k), v);
         }
       } else if (to != nullptr) {
@@ -837,18 +873,23 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
 }
 
 // ================================================================ segment sums
+// A segment's own sum of gamma^(distance to its end) b c^T: B w, with the distance counted to the segment's
+// end, is added up by the tensor cores over all its chunks.  B w is a sum of two bf16 numbers: the sums
+// reach a returned fp32 state only behind the last segment's decay.
 template <int D>
 struct SumTile {
+  static constexpr int kStages = 3;                     // chunks of B and C in flight
   static constexpr int kOp = (D / 64) * kAtom;
-  static constexpr int kStage = 2 * kOp;                // B, C
-  static constexpr int kOffLo = kStages * kStage;       // the second and third part of B w
-  static constexpr int kOffBars = kOffLo + 2 * kOp;
+  static constexpr int kOffLo = kStages * 2 * kOp;      // the second part of B w
+  static constexpr int kOffBars = kOffLo + kOp;
+  static constexpr int kSplit = D / 64;                 // threads that share a row of B
+  static constexpr int kThreads = 32 * (kWarpOut + 4 * kSplit);
+  static constexpr int kPerSm = D == 128 ? 1 : 2;
 };
 
-constexpr int kSumThreads = 192;                         // producer, MMA issuer, 4 warps for the rest
-
+template <int D>
 struct SumBars {
-  uint64_t full[kStages], empty[kStages], ready[kStages];
+  uint64_t full[SumTile<D>::kStages], empty[SumTile<D>::kStages], ready[SumTile<D>::kStages];
   uint64_t fin;
   uint32_t tbase;
   int abort;
@@ -858,16 +899,16 @@ struct SumBars {
 
 template <int D>
 constexpr size_t sum_smem() {
-  return SumTile<D>::kOffBars + sizeof(SumBars);
+  return SumTile<D>::kOffBars + sizeof(SumBars<D>);
 }
 static_assert(sum_smem<128>() <= 232448 && 2 * (sum_smem<64>() + 1024) <= 233472, "shared memory budget");
 
 template <int D>
-__global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid_constant__ TcArgs t) {
+__global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
+    retention_sum_kernel(const __grid_constant__ TcArgs t) {
   using P = SumTile<D>;
-  extern __shared__ __align__(1024) uint8_t smraw[];
-  uint8_t* sm = smraw;
-  SumBars* b = reinterpret_cast<SumBars*>(sm + P::kOffBars);
+  extern __shared__ __align__(1024) uint8_t sm[];
+  SumBars<D>* b = reinterpret_cast<SumBars<D>*>(sm + P::kOffBars);
   const RetArgs& r = t.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int set = blockIdx.x % r.nsum, unit = blockIdx.x / r.nsum, h = unit % r.H, g = unit / r.H;
@@ -878,10 +919,10 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
   const Segment sg = find_segment(r, g, b->scratch);
   if (sg.seq < 0 || (p.reverse ? sg.seg == 0 : sg.seg == sg.nseg - 1)) return;  // enters no other segment
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < P::kStages; ++s) {
       mbar_init(&b->full[s], 1);
       mbar_init(&b->empty[s], 1);
-      mbar_init(&b->ready[s], 4);
+      mbar_init(&b->ready[s], 4 * P::kSplit);
     }
     mbar_init(&b->fin, 1);
     b->abort = 0;
@@ -902,21 +943,21 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
   const Guard gd = make_guard(&b->abort, t.wait_ns);
   const uint32_t tmem = b->tbase;
   const int n = (sg.len + kTok - 1) / kTok;
-  const int terms = r.states != nullptr ? 3 : 2;
   uint8_t* lo = sm + P::kOffLo;
 
   if (warp == kWarpProd) {
     if (lane == 0) {
       const int ib = t.ib[z], ic = t.ic[z];
+      const int hb = t.by_h[ib] ? h : 0, sb = t.by_b[ib] ? sg.seq : 0, hc = t.by_h[ic] ? h : 0,
+                sc = t.by_b[ic] ? sg.seq : 0;
       int i = 0;
       for (; i < n; ++i) {
-        const int s = i % kStages;
-        if (i >= kStages && !wait(&b->empty[s], ((i / kStages) - 1) & 1, gd)) break;
-        uint8_t* st = sm + s * P::kStage;
+        const int s = i % P::kStages;
+        if (i >= P::kStages && !wait(&b->empty[s], ((i / P::kStages) - 1) & 1, gd)) break;
+        uint8_t* st = sm + s * 2 * P::kOp;
         mbar_arrive_expect_tx(&b->full[s], 2 * P::kOp);
-        load_tile<D>(st, &t.tm[ib], sg.row0 + i * kTok, t.by_h[ib] ? h : 0, t.by_b[ib] ? sg.seq : 0, &b->full[s]);
-        load_tile<D>(st + P::kOp, &t.tm[ic], sg.row0 + i * kTok, t.by_h[ic] ? h : 0, t.by_b[ic] ? sg.seq : 0,
-                     &b->full[s]);
+        load_tile<D>(st, &t.tm[ib], sg.row0 + i * kTok, hb, sb, &b->full[s]);
+        load_tile<D>(st + P::kOp, &t.tm[ic], sg.row0 + i * kTok, hc, sc, &b->full[s]);
       }
       b->issued = i;
     }
@@ -924,57 +965,58 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
   } else if (warp == kWarpMma) {
     if (lane == 0) {
       for (int i = 0; i < n; ++i) {
-        const int s = i % kStages;
-        if (!wait(&b->ready[s], (i / kStages) & 1, gd)) break;
+        const int s = i % P::kStages;
+        if (!wait(&b->ready[s], (i / P::kStages) & 1, gd)) break;
         tc_fence_after();
-        const uint32_t b0 = smem_u32(sm + s * P::kStage);
+        const uint32_t b0 = smem_u32(sm + s * 2 * P::kOp);
         mma_outer<D, D>(tmem, b0, b0 + P::kOp, i > 0);
         mma_outer<D, D>(tmem, smem_u32(lo), b0 + P::kOp, true);
-        if (terms > 2) mma_outer<D, D>(tmem, smem_u32(lo) + P::kOp, b0 + P::kOp, true);
         mma_commit(&b->empty[s]);
       }
       mma_commit(&b->fin);
     }
     __syncwarp();
   } else {
-    const int qd = warp & 3, row = 32 * qd + lane;
+    const int qd = warp & 3, row = 32 * qd + lane, half = (warp - kWarpOut) >> 2;
+    const int reverse = p.reverse, all = sg.len, d = r.d, fb = p.b.feature, fc = p.c.feature;
     const float lg = decay_log2(r.gamma[h]);
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int s = i % kStages, at = i * kTok + row, len = min(kTok, sg.len - i * kTok);
-      ok = wait_warp(&b->full[s], (i / kStages) & 1, gd);
+      const int s = i % P::kStages, at = i * kTok + row, len = min(kTok, all - i * kTok);
+      ok = wait_warp(&b->full[s], (i / P::kStages) & 1, gd);
+      // the second part's tile has been read by the MMAs of the chunk before
+      if (ok && i > 0) ok = wait_warp(&b->empty[(i - 1) % P::kStages], ((i - 1) / P::kStages) & 1, gd);
       if (!ok) break;
-      uint8_t* st = sm + s * P::kStage;
-      // the remainders' tiles have been read by the MMAs of the chunk before
-      if (i > 0) ok = wait_warp(&b->empty[(i - 1) % kStages], ((i - 1) / kStages) & 1, gd);
-      if (!ok) break;
-      if (p.c.feature != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, r.d, p.c.feature);
-      if (len < kTok) map_row<D>(st, row, len, r.d, kFeatIdentity);
-      const float w = row < len ? decay_pow(lg, p.reverse ? at : sg.len - 1 - at) : 0.f;
-      if (p.b.feature != kFeatIdentity)
-        weigh_phi_row3<D>(st, lo, lo + P::kOp, row, w, nullptr, r.d, p.b.feature);
-      else if (terms > 2)
-        weigh_row3<D>(st, lo, lo + P::kOp, row, w);
+      uint8_t* st = sm + s * 2 * P::kOp;
+      if (half == 0) {  // (the operands of a whole row: rarely)
+        if (fc != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, d, fc);
+      }
+      const float w = row < len ? decay_pow(lg, reverse ? at : all - 1 - at) : 0.f;
+      if (fb != kFeatIdentity || len < kTok)
+        weigh_phi_row2<64>(st, lo, row, 8 * half, w, d, fb);
       else
-        weigh_row2<D>(st, lo, row, w);
+        weigh_row2<64>(st, lo, row, 8 * half, w);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->ready[s]);
     }
     if (ok && wait_warp(&b->fin, 0, gd) && !aborted(gd)) {
       tc_fence_after();
-      const int xr = D == 128 ? row : 16 * qd + lane;
-      const bool has = (D == 128 || lane < 16) && xr < r.d;
-      float* dst = r.seg + (((size_t)set * r.G + g) * r.H + h) * r.d * r.d + (size_t)xr * r.d;
-#pragma unroll
-      for (int q = 0; q < D / 16; ++q) {
-        float u[16];
-        tmem_ld16(tmem + ((uint32_t)(32 * qd) << 16) + 16 * q, u);
+      float* dst = r.seg + (((size_t)set * r.G + g) * r.H + h) * d * d;
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {  // 16 rows x 32 columns
+        const int hh = D == 128 ? k / 2 : 0, c0 = 64 * half + 32 * (k % 2);
+        const int r0 = (D == 128 ? 32 * qd + 16 * hh : 16 * qd) + (lane >> 2);
+        float v[16];
+        tmem_ld16x32(tmem + ((uint32_t)(32 * qd + 16 * hh) << 16) + c0, v);
         tmem_ld_wait();
-        if (has && 16 * q < r.d) {
 #pragma unroll
-          for (int x = 0; x < 16; x += 4)
-            *reinterpret_cast<float4*>(dst + 16 * q + x) = make_float4(u[x], u[x + 1], u[x + 2], u[x + 3]);
+        for (int m = 0; m < 8; ++m) {
+          const int rr = r0 + 8 * (m & 1), cc = c0 + 8 * (m >> 1) + 2 * (lane & 3);
+          if (rr < d && cc < d)
+            *reinterpret_cast<float2*>(dst + rr * d + cc) =
+                make_float2(v[4 * (m >> 1) + 2 * (m & 1)], v[4 * (m >> 1) + 2 * (m & 1) + 1]);
         }
         __syncwarp();
       }
@@ -986,8 +1028,8 @@ __global__ void __launch_bounds__(kSumThreads) retention_sum_kernel(const __grid
   if (threadIdx.x == 0) {
     drain(&b->fin, 0);
     if (aborted(gd)) {
-      for (int q = b->issued > kStages ? b->issued - kStages : 0; q < b->issued; ++q)
-        drain(&b->full[q % kStages], (q / kStages) & 1);
+      for (int q = b->issued > P::kStages ? b->issued - P::kStages : 0; q < b->issued; ++q)
+        drain(&b->full[q % P::kStages], (q / P::kStages) & 1);
       atomicOr(r.status, 1u);
     }
   }
@@ -1049,7 +1091,7 @@ cudaError_t launch(const TcArgs& t, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const unsigned units = (unsigned)(t.r.G * t.r.H);
   if (t.r.seg != nullptr) {
-    retention_sum_kernel<D><<<units * t.r.nsum, kSumThreads, sum_smem<D>(), st>>>(t);
+    retention_sum_kernel<D><<<units * t.r.nsum, SumTile<D>::kThreads, sum_smem<D>(), st>>>(t);
     note_launch();
     e = retention_scan_launch(t.r, st);
     if (e != cudaSuccess) return e;
