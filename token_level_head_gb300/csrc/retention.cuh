@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "internal.h"
 #include "retention.h"
 
 namespace mhla {
@@ -25,6 +26,30 @@ __device__ __forceinline__ float decay_log2(float gamma) { return log1pf(gamma -
 // gamma^n for n >= 0 from lg = log2(gamma).  The relative error is about 2^-23 n |lg|, so below 2^-18
 // wherever the power itself is above 2^-32.  gamma^0 = 1 for every gamma, 0 among them.
 __device__ __forceinline__ float decay_pow(float lg, int n) { return n == 0 ? 1.f : exp2f(lg * (float)n); }
+
+// Programmatic dependent launch: a kernel of a call starts while the one before it drains; what it reads of
+// that one's results comes behind grid_dependency_wait().  The inputs do not: the first kernel of a call is
+// an ordinary launch.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename Args>
+cudaError_t launch_dependent(void (*kernel)(Args), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, bool dependent,
+                             const Args& args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = dependent ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args);
+  note_launch();
+  return e;
+}
 
 struct Segment {
   int seq;     // sequence, -1: no such segment

@@ -110,15 +110,45 @@ struct Plan {
   bool split;    // some sequence may have two segments
 };
 
-// tokens: in all.  Enough segments to fill the GPU a few times over, no more: each costs a state.
-Plan make_plan(int B, int H, long long tokens, int d, bool packed, bool backward) {
+// The length of a segment.  In units of a chunk's time in a pass, with `slots` blocks at once and segments of
+// n chunks, a call takes
+//   pass:  (rounds of blocks) (n + start)
+//   split: (rounds) (n + start) sum, then `fixed` for two more launches
+// where a round is slots blocks; packed sequences, of unknown lengths, take their work over slots and half a
+// block for the tail.  The costs are measured ones: a chunk takes 3.8 us at d = 128 and 5.4 us at d = 64
+// (two blocks an SM), a block 2.5 chunks to start, its sum pass 0.45 of the pass's time, two launches 8 us.
+// fp32 (SIMT, chunks of 64 tokens counted as two): 14 us.
+Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward) {
+  const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
-  const long long want = 608, rows = (long long)H * npass * (d > 64 ? 2 : 1);
-  const long long segs = std::max<long long>(1, (want + rows - 1) / rows);
-  long long L = std::max<long long>(128, (tokens + segs - 1) / segs);
-  L = std::min<long long>((L + 127) / 128 * 128, ((long long)N + 127) / 128 * 128);
+  const double slots = f32 ? 152.0 * (d == 128 ? 1 : d == 64 ? 2 : 4) : d == 128 ? 152.0 : 304.0;
+  const double chunk_us = f32 ? 14.0 : d == 128 ? 3.8 : 5.4;
+  const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, fixed = 8.0 / chunk_us;
+  const int cols = f32 && d == 128 ? 2 : 1;  // blocks that share a segment
+  const long long all = (tokens + 127) / 128, most = ((long long)N + 127) / 128;
+  double best = 1e300;
+  long long pick = most;
+  for (long long n = 1; n <= most; n = n < 64 ? n + 1 : n + n / 16) {
+    if (n + n / 16 > most && n > 64) n = most;
+    double cost;
+    if (packed) {
+      const double segs = (double)all / n + 0.5 * B, work = (double)all + 0.5 * B;
+      const double blocks = segs * H * cols;
+      auto time = [&](double per) { return (work * H * cols + blocks * start) * per / slots + 0.5 * (n + start); };
+      cost = time(npass) + (n < most ? sum * time(nsum) + fixed : 0.0);
+    } else {
+      const long long segs = (most + n - 1) / n;
+      const double blocks = (double)B * H * segs * cols;
+      cost = std::ceil(blocks * npass / slots) * (n + start);
+      if (segs > 1) cost += std::ceil((double)B * H * (segs - 1) * cols * nsum / slots) * (n + start) * sum + fixed;
+    }
+    if (cost < best) {
+      best = cost;
+      pick = n;
+    }
+  }
   Plan p;
-  p.L = (int)std::max<long long>(L, 128);
+  p.L = (int)std::max<long long>(std::min<long long>(pick, 1 << 23) * 128, 128);
   p.G = (int)(packed ? tokens / p.L + B : (long long)B * ((N + p.L - 1) / p.L));
   p.split = N > p.L;
   p.bytes = kWorkspacePrefix + (p.split ? (size_t)nsum * p.G * H * d * d * sizeof(float) : 0);
@@ -140,7 +170,7 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
   if (tokens > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
   if (!gamma || !aligned(gamma, 4) || !aligned(cu, 4)) return MHLA_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MHLA_ERR_INVALID_ARG;
-  *plan = make_plan(B, H, tokens, d, cu != nullptr, backward);
+  *plan = make_plan(B, H, tokens, d, dt, cu != nullptr, backward);
   if ((long long)plan->G * H > 0x7fffffffll || (long long)B * H > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
   if (ws_bytes < plan->bytes) return MHLA_ERR_INVALID_ARG;
   *e = {cu ? 1 : B, H, N, d, dt == MHLA_F32 ? 4 : 2};
@@ -175,8 +205,11 @@ extern "C" {
 size_t retention_workspace_bytes(int B, int H, int tokens, int d, int backward) {
   if (!sizes_ok(B, H, tokens, d) || (backward != 0 && backward != 1)) return 0;
   if (B == 0 || H == 0 || tokens == 0) return kWorkspacePrefix;
-  size_t n = make_plan(B, H, tokens, d, true, backward != 0).bytes;
-  if (tokens % B == 0) n = std::max(n, make_plan(B, H, tokens, d, false, backward != 0).bytes);
+  size_t n = 0;
+  for (mhla_dtype dt : {MHLA_F32, MHLA_BF16}) {
+    n = std::max(n, make_plan(B, H, tokens, d, dt, true, backward != 0).bytes);
+    if (tokens % B == 0) n = std::max(n, make_plan(B, H, tokens, d, dt, false, backward != 0).bytes);
+  }
   return n;
 }
 

@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   float* sW = sP + kTok * C::LP;
   __shared__ int scratch[34];
   const int tid = threadIdx.x;
+  launch_dependents();
   const int h = blockIdx.x % a.H, g = blockIdx.x / a.H;
   int z = blockIdx.z;
   if (SUM)  // the pass that makes set z
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
     const float* src = nullptr;
     bool tr = false;
     if (a.states != nullptr) slot = ret_slot(a.slots, a.n_slots, sg.seq);
+    grid_dependency_wait();  // the states entering the segments
     if (sg.nseg > 1) {
       src = seg;
       tr = p.sum_t != 0;
@@ -257,71 +259,74 @@ cudaError_t launch_passes(const RetArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   grid.z = a.npass;
-  retention_simt_kernel<D, false><<<grid, kThreads, C::kBytes, st>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(retention_simt_kernel<D, false>, grid, kThreads, C::kBytes, st, a.seg != nullptr, a);
 }
 
 // ================================================================ scan
-// One thread carries four elements of a head's state over its sequence's segments, in the pass's
-// direction: the slot of a segment holds the segment's own sum before, the state entering it after.
+// A thread carries V elements of a head's state over its sequence's segments, in the pass's direction: the
+// slot of a segment holds the segment's own sum before, the state entering it after.  V = 4 where there are
+// many heads (most packed sequences have one segment, and their blocks end at once), 1 where few.
+template <int V>
 __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_constant__ RetArgs a) {
-  __shared__ int part[33];
+  __shared__ int part[kThreads / 32];
+  launch_dependents();
   const int h = blockIdx.x % a.H, seq = blockIdx.x / a.H, set = blockIdx.z;
   int ps = 0;
   for (int i = 0; i < a.npass; ++i)
     if (a.pass[i].sum == set && !a.pass[i].sum_t) ps = i;
   const bool reverse = a.pass[ps].reverse != 0;
-  int g0, nseg, len;
+  int g0 = 0, nseg, len;
   if (a.cu == nullptr) {
     nseg = (a.N + a.L - 1) / a.L;
     g0 = seq * nseg;
     len = a.N;
   } else {
-    int n = 0;
-    for (int i = threadIdx.x; i < seq; i += blockDim.x) n += packed_segments(a, i);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
-    __syncthreads();
-    g0 = 0;
-    for (int w = 0; w < kThreads / 32; ++w) g0 += part[w];
     int lo, hi;
     packed_range(a, seq, &lo, &hi);
     nseg = packed_segments(a, seq);
     len = hi - lo;
+    if (nseg >= 2) {  // (uniform over the block)
+      int n = 0;
+      for (int i = threadIdx.x; i < seq; i += blockDim.x) n += packed_segments(a, i);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+      __syncthreads();
+      for (int w = 0; w < kThreads / 32; ++w) g0 += part[w];
+    }
   }
-  if (nseg < 2) return;  // (uniform over the block) the pass takes its state from the slot itself
+  const int slot = nseg >= 2 && a.load && a.states != nullptr ? ret_slot(a.slots, a.n_slots, seq) : -1;
+  grid_dependency_wait();  // the sums are there
+  if (nseg < 2) return;    // the pass takes its state from the slot itself
   nseg = min(nseg, a.G - g0);
-  const int slot = a.load && a.states != nullptr ? ret_slot(a.slots, a.n_slots, seq) : -1;
-  const int i4 = blockIdx.y * kThreads + threadIdx.x, n4 = a.d * a.d / 4;
-  if (i4 >= n4) return;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (slot >= 0) x = reinterpret_cast<const float4*>(a.states + ((size_t)slot * a.H + h) * a.d * a.d)[i4];
+  const int n = a.d * a.d, e = (blockIdx.y * kThreads + threadIdx.x) * V;
+  if (e >= n) return;
   const float lg = decay_log2(a.gamma[h]);
-  const float wfull = decay_pow(lg, a.L);
-  float4* w = reinterpret_cast<float4*>(a.seg + (((size_t)set * a.G + g0) * a.H + h) * a.d * a.d) + i4;
-  const size_t step = (size_t)a.H * n4;
-  constexpr int kAhead = 8;  // loads in flight
+  const float wfull = decay_pow(lg, a.L), wlast = decay_pow(lg, len - (nseg - 1) * a.L);
+  const size_t step = (size_t)a.H * n;
+  struct alignas(4 * V) Vec {
+    float v[V];
+  };
+  Vec x{};
+  if (slot >= 0) x = *reinterpret_cast<const Vec*>(a.states + ((size_t)slot * a.H + h) * n + e);
+  float* w = a.seg + (((size_t)set * a.G + g0) * a.H + h) * n + e;
+  constexpr int kAhead = 16 / V;  // loads in flight
   for (int j0 = 0; j0 < nseg; j0 += kAhead) {
-    float4 u[kAhead];
+    Vec u[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = j0 + j;
-      if (k < nseg - 1) u[j] = __ldcg(w + (size_t)(reverse ? nseg - 1 - k : k) * step);
+      u[j] = Vec{};
+      if (k < nseg - 1) u[j] = *reinterpret_cast<const Vec*>(w + (size_t)(reverse ? nseg - 1 - k : k) * step);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = j0 + j;
       if (k >= nseg) break;
       const int sgm = reverse ? nseg - 1 - k : k;
-      w[(size_t)sgm * step] = x;
-      if (k == nseg - 1) break;
-      const float wl = sgm == nseg - 1 ? decay_pow(lg, len - sgm * a.L) : wfull;
-      x.x = fmaf(wl, x.x, u[j].x);
-      x.y = fmaf(wl, x.y, u[j].y);
-      x.z = fmaf(wl, x.z, u[j].z);
-      x.w = fmaf(wl, x.w, u[j].w);
+      *reinterpret_cast<Vec*>(w + (size_t)sgm * step) = x;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x.v[i] = fmaf(sgm == nseg - 1 ? wlast : wfull, x.v[i], u[j].v[i]);
     }
   }
 }
@@ -469,10 +474,10 @@ cudaError_t simt_retention_launch(const RetArgs& a, cudaStream_t st) {
 }
 
 cudaError_t retention_scan_launch(const RetArgs& a, cudaStream_t st) {
-  const int n4 = a.d * a.d / 4;
-  retention_scan_kernel<<<dim3((unsigned)(a.B * a.H), (n4 + kThreads - 1) / kThreads, a.nsum), kThreads, 0, st>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  const int n = a.d * a.d, v = (long long)a.B * a.H * a.nsum >= 64 ? 4 : 1;
+  const dim3 grid((unsigned)(a.B * a.H), (n / v + kThreads - 1) / kThreads, a.nsum);
+  return v == 4 ? launch_dependent(retention_scan_kernel<4>, grid, kThreads, 0, st, true, a)
+                : launch_dependent(retention_scan_kernel<1>, grid, kThreads, 0, st, true, a);
 }
 
 cudaError_t retention_step_launch(int B, int H, int d, mhla_dtype dt, const RetTensor& q, const RetTensor& k,

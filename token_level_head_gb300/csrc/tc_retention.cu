@@ -252,7 +252,7 @@ __device__ __noinline__ void weigh_phi_row2(uint8_t* hi, uint8_t* lo, int r, int
 
 // MMAs of one product D[tmem] (+)= A^T-like operands, MN-major in both: A [K rows][M], B [K rows][N], K = 128.
 template <int M, int N>
-__device__ __forceinline__ void mma_outer(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+__device__ __forceinline__ void mma_outer(uint32_t d, uint32_t a, uint32_t b, bool acc = true) {
   const uint64_t da = smem_desc(a, kAtom, 1024), db = smem_desc(b, kAtom, 1024);
 #pragma unroll
   for (int k = 0; k < kTok / 16; ++k)
@@ -288,9 +288,9 @@ struct PassTile {
   static constexpr int kOffBars = kOffX + kOp;
   static constexpr uint32_t kCols = D == 128 ? 512 : 256;
   static constexpr uint32_t kColS = 0;                  // scores, P over their first half
-  static constexpr uint32_t kColInter = 128, kColIntra = 128 + D;
-  // D = 128: X gamma^len, dX is added to it.  D = 64: dX alone, over the scores that P leaves free; X is in registers
-  static constexpr uint32_t kColDX = D == 128 ? 384 : 64;
+  static constexpr uint32_t kColIntra = D == 128 ? 256 : 64;  // D = 64: over the scores that P leaves free
+  static constexpr uint32_t kColInter = 128;
+  static constexpr uint32_t kColX = D == 128 ? 384 : 192;     // X gamma^len, dX is added to it
   static constexpr int kPerSm = D == 128 ? 1 : 2;
   static constexpr int kSplit = D / 64;                 // out warps of a TMEM lane quadrant
   static constexpr int kWarpW = kWarpOut + 4 * kSplit, kWarpX = kWarpW + 4;
@@ -395,8 +395,7 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
       if (!wait(&b->mapped, maps & 1, gd)) return;
       ++maps;
     }
-    // D = 64: dX lies over the scores; X of this chunk is there once it has been read
-    if (D == 64 && !wait(&b->x_full, i & 1, gd)) return;
+    if (D == 64 && i > 0 && !wait(&b->o_free, (i - 1) & 1, gd)) return;  // (and over intra)
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
@@ -405,8 +404,8 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
                idesc_bf16_f32(128, 128, 0, 0), k > 0);
     }
     mma_commit(&b->s_full);
-    if (D != 64 && !wait(&b->x_full, i & 1, gd)) return;
-    if (i > 0 && !wait(&b->o_free, (i - 1) & 1, gd)) return;
+    if (!wait(&b->x_full, i & 1, gd)) return;
+    if (D != 64 && i > 0 && !wait(&b->o_free, (i - 1) & 1, gd)) return;
     tc_fence_after();
     {
       const uint64_t dx = smem_desc(xt, D * 128, 1024);
@@ -429,9 +428,9 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
     if (i < nx) {
       if (!wait(&b->w_full, i & 1, gd)) return;
       tc_fence_after();
-      mma_outer<D, D>(tmem + P::kColDX, b0, c0, D == 128);
-      mma_outer<D, D>(tmem + P::kColDX, lo, c0, true);
-      if (terms > 2) mma_outer<D, D>(tmem + P::kColDX, xt, c0, true);
+      mma_outer<D, D>(tmem + P::kColX, b0, c0);
+      mma_outer<D, D>(tmem + P::kColX, lo, c0);
+      if (terms > 2) mma_outer<D, D>(tmem + P::kColX, xt, c0);
       mma_commit(&b->dx_full);
     }
     mma_commit(&b->empty[s]);
@@ -662,9 +661,8 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
   const int qd = warp & 3, half = D == 128 ? (warp - P::kWarpX) >> 2 : 0, d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
   const float lg = b->ctx.lg;
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
-  const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16) + P::kColDX;
+  const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16) + P::kColX;
   uint8_t* xt = sm + P::kOffX;
-  float X[D == 128 ? 16 : 32];
   // block k: rows r, r + 8, columns c0 + 8 g + {0, 1}
   auto row_of = [&](int k) { return (D == 128 ? 32 * qd + 16 * (k / 2) : 16 * qd) + (lane >> 2); };
   auto col_of = [&](int k) { return 64 * half + 32 * (k % 2); };
@@ -677,20 +675,29 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
       reinterpret_cast<uint32_t*>(piece(xt, D, r + 8, col_of(k) / 8 + g))[lane & 3] = pack_bf16(v[4 * g + 2], v[4 * g + 3]);
     }
   };
+  // the tile for the next chunk, and X times its decay over that chunk for dX to be added to
+  auto keep = [&](int k, float* v, float wl) {
+    tile(k, v);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      reinterpret_cast<float2*>(v)[x] = mul2(reinterpret_cast<float2*>(v)[x], make_float2(wl, wl));
+    tmem_st16x32(tmem_of(k), v);
+  };
   auto publish = [&] {
-    if (D == 128) tmem_st_wait();
+    tmem_st_wait();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->x_full);
   };
   {
+    grid_dependency_wait();  // the states entering the segments
     const float* from = b->ctx.from;
     const bool from_t = b->ctx.from_t != 0;
     const float wl = decay_pow(lg, chunk_len(chunk_of(0, n, reverse), all));
-#pragma unroll(D == 128 ? 1 : 2)
+#pragma unroll 1
     for (int k = 0; k < kBlocks; ++k) {
-      float* v = X + (D == 128 ? 0 : 16 * k);
+      float v[16];
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         const int r = row_of(k) + 8 * (m & 1), c = col_of(k) + 8 * (m >> 1) + 2 * (lane & 3);
@@ -704,43 +711,26 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
         v[4 * (m >> 1) + 2 * (m & 1)] = u.x;
         v[4 * (m >> 1) + 2 * (m & 1) + 1] = u.y;
       }
-      tile(k, v);
-      if (D == 128) {
-#pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] *= wl;
-        tmem_st16x32(tmem_of(k), v);
-      }
+      __syncwarp();
+      keep(k, v, wl);
     }
   }
   publish();
 #pragma unroll 1
   for (int i = 0; i < nx; ++i) {
     const bool more = i + 1 < n;
-    const float wl = decay_pow(lg, chunk_len(chunk_of(D == 128 && more ? i + 1 : i, n, reverse), all));
+    const float wl = more ? decay_pow(lg, chunk_len(chunk_of(i + 1, n, reverse), all)) : 1.f;
     float* to = more ? nullptr : b->ctx.to;
     // (inter has read the last tile)
     if (!wait_warp(&b->in_full, i & 1, gd) || !wait_warp(&b->dx_full, i & 1, gd)) return;
     tc_fence_after();
 #pragma unroll 2
     for (int k = 0; k < kBlocks; ++k) {
-      float u[16];
-      float* v = D == 128 ? u : X + 16 * k;
-      tmem_ld16x32(tmem_of(k), u);
+      float v[16];
+      tmem_ld16x32(tmem_of(k), v);
       tmem_ld_wait();
-      if (D != 128) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          reinterpret_cast<float2*>(v)[x] =
-              fma2(make_float2(wl, wl), reinterpret_cast<float2*>(v)[x], reinterpret_cast<float2*>(u)[x]);
-      }
       if (more) {
-        tile(k, v);
-        if (D == 128) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            reinterpret_cast<float2*>(v)[x] = mul2(reinterpret_cast<float2*>(v)[x], make_float2(wl, wl));
-          tmem_st16x32(tmem_of(k), v);
-        }
+        keep(k, v, wl);
       } else if (to != nullptr) {
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
@@ -909,6 +899,7 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
   using P = SumTile<D>;
   extern __shared__ __align__(1024) uint8_t sm[];
   SumBars<D>* b = reinterpret_cast<SumBars<D>*>(sm + P::kOffBars);
+  launch_dependents();
   const RetArgs& r = t.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int set = blockIdx.x % r.nsum, unit = blockIdx.x / r.nsum, h = unit % r.H, g = unit / r.H;
@@ -1096,9 +1087,8 @@ cudaError_t launch(const TcArgs& t, cudaStream_t st) {
     e = retention_scan_launch(t.r, st);
     if (e != cudaSuccess) return e;
   }
-  retention_pass_kernel<D><<<units * t.r.npass, PassTile<D>::kThreads, pass_smem<D>(), st>>>(t);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(retention_pass_kernel<D>, dim3(units * t.r.npass), PassTile<D>::kThreads, pass_smem<D>(), st,
+                          t.r.seg != nullptr, t);
 }
 
 }  // namespace
