@@ -18,10 +18,10 @@
 // Roles (D = 128: 22 warps and one CTA an SM, D = 64: 14 warps and two):
 //   warp 0       TMA producer: the tiles of a chunk, B and C two chunks deep, A one
 //   warp 1       MMA issuer
-//   out warps    scores -> P, then out = scale (intra + gamma^(i+1) inter) to global memory (D = 128:
-//                eight warps, each with half of the scores and of the columns; D = 64: four)
+//   8 out warps  scores -> P, then out = scale (intra + gamma^(i+1) inter) to global memory: two for each
+//                quarter of the rows, with half of the scores and of the columns each
 //   4 W warps    feature maps in place, B w
-//   X warps      X and its bf16 tile for the next chunk (D = 128: eight, D = 64: four)
+//   X warps      X and its bf16 tile for the next chunk: eight (D = 128), or the W warps themselves (D = 64)
 // A chunk's B w does not wait for the X that enters it, so the serial chain from one X to the next is
 // inter, intra, dX and the update.  What this costs is shared memory's bandwidth: with D = 128 a chunk's
 // products read 2.5 thousand cycles' worth of it (128 bytes a cycle; 128 x 128 x 16 from shared memory
@@ -287,14 +287,17 @@ struct PassTile {
   static constexpr int kOffX = kOffLo + kOp;            // bf16 X: D rows c, D columns e (third part of B w)
   static constexpr int kOffBars = kOffX + kOp;
   static constexpr uint32_t kCols = D == 128 ? 512 : 256;
-  static constexpr uint32_t kColS = 0;                  // scores, P over their first half
-  static constexpr uint32_t kColIntra = D == 128 ? 256 : 64;  // D = 64: over the scores that P leaves free
+  // scores; P of tokens 0 .. 63 over their columns 0 .. 31, of tokens 64 .. 127 over 64 .. 95: each over scores
+  // that its own warp has read
+  static constexpr uint32_t kColS = 0;
+  // intra: D = 128 in columns of its own, D = 64 over the scores that P leaves free, 32 columns in two places
+  static constexpr uint32_t intra(uint32_t c) { return D == 128 ? 256 + c : 32 + c + (c & 32); }
   static constexpr uint32_t kColInter = 128;
   static constexpr uint32_t kColX = D == 128 ? 384 : 192;     // X gamma^len, dX is added to it
   static constexpr int kPerSm = D == 128 ? 1 : 2;
-  static constexpr int kSplit = D / 64;                 // out warps of a TMEM lane quadrant
-  static constexpr int kWarpW = kWarpOut + 4 * kSplit, kWarpX = kWarpW + 4;
-  static constexpr int kThreads = 32 * (kWarpX + 4 * kSplit);
+  static constexpr int kWarpW = kWarpOut + 8, kWarpX = D == 128 ? kWarpW + 4 : kWarpW;
+  static constexpr int kXWarps = D == 128 ? 8 : 4;
+  static constexpr int kThreads = 32 * (kWarpX + kXWarps);
 };
 
 // What the roles share.  It is kept in shared memory and the roles are functions of their own, so that none
@@ -419,10 +422,13 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
     tc_fence_after();
     {
       const uint64_t dc = smem_desc(c0, kAtom, 1024);
+      constexpr int kN = D == 128 ? 128 : 32;  // columns of intra in one place
 #pragma unroll
-      for (int k = 0; k < kTok / 16; ++k)
-        mma_bf16_ts(tmem + P::kColIntra, tmem + P::kColS + 8 * k + (D == 128 && k >= 4 ? 32 : 0), dc + k * (2048 >> 4),
-                    idesc_bf16_f32(128, D, 0, 1), k > 0);
+      for (int e = 0; e < D; e += kN)
+#pragma unroll
+        for (int k = 0; k < kTok / 16; ++k)
+          mma_bf16_ts(tmem + P::intra(e), tmem + P::kColS + 8 * k + (k >= 4 ? 32 : 0), dc + k * (2048 >> 4) + e * 2 / 16,
+                      idesc_bf16_f32(128, kN, 0, 1), k > 0);
     }
     mma_commit(&b->o_full);
     if (i < nx) {
@@ -437,7 +443,7 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
   }
 }
 
-// Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  Split: the two warps of a quadrant take
+// Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  The two warps of a quadrant take
 // half of the scores and of the output columns each.
 // Two products / multiply-adds in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -500,10 +506,9 @@ __device__ __forceinline__ void turn4(uint32_t* e, int lane) {
 template <int D, bool DERIV>
 __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
   using P = PassTile<D>;
-  constexpr int S = P::kSplit;
-  const int qd = warp & 3, row = 32 * qd + lane, half = S == 1 ? 0 : (warp - kWarpOut) >> 2;
+  const int qd = warp & 3, row = 32 * qd + lane, half = (warp - kWarpOut) >> 2;
   const int n = b->ctx.n, all = b->ctx.len, reverse = b->ctx.reverse, row0 = b->ctx.row0, xf = b->ctx.fx;
-  const int d0 = half * 64, d1 = min(b->ctx.d, d0 + 64);
+  const int d0 = half * (D / 2), d1 = min(b->ctx.d, d0 + D / 2);
   const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16);
   const float gamma = decay_pow(b->ctx.lg, 1);
   const long long sn = b->ctx.out_n, xsn = b->ctx.x_n;
@@ -516,10 +521,8 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
     const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
     if (!wait_warp(&b->s_full, i & 1, gd)) return;
     tc_fence_after();
-    // P of block j of the scores (32 columns) goes over scores that this warp has read: to columns 16 j .., with
-    // two warps a quadrant those of tokens 64 .. to 64 + 16 (j - 2) ..
 #pragma unroll 1
-    for (int j = half * 2; j < half * 2 + 4 / S; ++j) {
+    for (int j = 2 * half; j < 2 * half + 2; ++j) {  // 32 scores -> 16 columns of P
       const uint32_t dst = tl + P::kColS + 16 * j + half * 32;
       if (reverse ? j < qd : j > qd) {
         uint32_t w[16];
@@ -566,11 +569,11 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
         if (DERIV) xp[k] = xin + at * xsn + d0 + 2 * (lane & 3);
       }
 #pragma unroll
-      for (int cc = 0; cc < 64; cc += 32) {
+      for (int cc = 0; cc < D / 2; cc += 32) {
         float u[16], v[16];
-        const uint32_t tr = tl + ((uint32_t)(16 * hh) << 16) + d0 + cc;
-        tmem_ld16x32(tr + P::kColInter, u);
-        tmem_ld16x32(tr + P::kColIntra, v);
+        const uint32_t tr = tl + ((uint32_t)(16 * hh) << 16);
+        tmem_ld16x32(tr + P::kColInter + d0 + cc, u);
+        tmem_ld16x32(tr + P::intra(d0 + cc), v);
         uint32_t xx[2][4];
         if (DERIV) {
 #pragma unroll
@@ -605,37 +608,43 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
   }
 }
 
-// W warps, token row = 32 (warp % 4) + lane: the feature maps of a chunk and zeros behind the sequence (before
+// One W warp, token row = 32 (warp % 4) + lane: the feature maps of a chunk and zeros behind the sequence (before
 // its scores), then B w (after them).
 template <int D>
-__device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int lane) {
+struct Weigh {
   using P = PassTile<D>;
-  const int row = 32 * (warp & 3) + lane;
-  const int d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
-  const int terms = b->ctx.terms, fa = b->ctx.fa, fb = b->ctx.fb, fc = b->ctx.fc;
-  const bool mapped = b->ctx.mapped();
-  const float lg = b->ctx.lg;
-  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
-  uint8_t *at = sm + P::kOffA, *lo = sm + P::kOffLo, *lo2 = sm + P::kOffX;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const int s = i % kStages, ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
-    uint8_t* bt = sm + P::kOffBC + s * 2 * P::kOp;
-    if (mapped || len < kTok) {
-      if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return;
-      if (fa != kFeatIdentity) map_row<D>(at, row, kTok, d, fa);
-      if (fb != kFeatIdentity || len < kTok) map_row<D>(bt, row, len, d, fb);
-      if (fc != kFeatIdentity || len < kTok) map_row<D>(bt + P::kOp, row, len, d, fc);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->mapped);
-    }
-    if (i >= nx) return;
+  uint8_t* sm;
+  PassBars* b;
+  int lane, row, d, n, all, reverse, terms, fa, fb, fc;
+  bool mapped;
+  float lg;
+  Guard gd;
+  __device__ __forceinline__ Weigh(uint8_t* sm_, PassBars* b_, int warp, int lane_)
+      : sm(sm_), b(b_), lane(lane_), row(32 * (warp & 3) + lane_), d(b_->ctx.d), n(b_->ctx.n), all(b_->ctx.len),
+        reverse(b_->ctx.reverse), terms(b_->ctx.terms), fa(b_->ctx.fa), fb(b_->ctx.fb), fc(b_->ctx.fc),
+        mapped(b_->ctx.mapped()), lg(b_->ctx.lg), gd(make_guard(&b_->abort, b_->ctx.wait_ns)) {}
+
+  __device__ __forceinline__ bool map(int i) {
+    const int s = i % kStages, len = chunk_len(chunk_of(i, n, reverse), all);
+    if (!mapped && len == kTok) return true;
+    if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return false;
+    uint8_t *at = sm + P::kOffA, *bt = sm + P::kOffBC + s * 2 * P::kOp;
+    if (fa != kFeatIdentity) map_row<D>(at, row, kTok, d, fa);
+    if (fb != kFeatIdentity || len < kTok) map_row<D>(bt, row, len, d, fb);
+    if (fc != kFeatIdentity || len < kTok) map_row<D>(bt + P::kOp, row, len, d, fc);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b->mapped);
+    return true;
+  }
+  __device__ __forceinline__ bool weigh(int i) {
     // B has been read by the scores, the second part by the last dX; the third part takes X's tile, once inter
     // has read it
     if (!wait_warp(&b->s_full, i & 1, gd) || (i > 0 && !wait_warp(&b->dx_full, (i - 1) & 1, gd)) ||
         (terms > 2 && !wait_warp(&b->in_full, i & 1, gd)))
-      return;
+      return false;
+    const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
+    uint8_t *bt = sm + P::kOffBC + (i % kStages) * 2 * P::kOp, *lo = sm + P::kOffLo, *lo2 = sm + P::kOffX;
     const float w = row < len ? decay_pow(lg, reverse ? row : len - 1 - row) : 0.f;
     if (terms > 2 && fb != kFeatIdentity) {  // phi(b) in fp32 for the state
       const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
@@ -648,53 +657,63 @@ __device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int 
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->w_full);
+    return true;
   }
-}
+};
 
-// X warps.  TMEM lane quadrant = warp % 4: rows 32 quadrant .. of X, or with D = 64 (M = 64) 16 quadrant .. in its
-// first 16 lanes; 16 rows and 32 columns at a time, a lane's elements as in tmem_ld16x32.  D = 128: the two warps
-// of a quadrant take half of the columns each.
+// One X warp.  TMEM lane quadrant = warp % 4: rows 32 quadrant .. of X, or with D = 64 (M = 64) 16 quadrant .. in
+// its first 16 lanes; 16 rows and 32 columns at a time, a lane's elements as in tmem_ld16x32.  D = 128: the two
+// warps of a quadrant take half of the columns each.
 template <int D>
-__device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane) {
+struct Carry {
   using P = PassTile<D>;
-  constexpr int kBlocks = D == 128 ? 4 : 2;                 // of 16 x 32 elements
-  const int qd = warp & 3, half = D == 128 ? (warp - P::kWarpX) >> 2 : 0, d = b->ctx.d, n = b->ctx.n, nx = b->ctx.nx, all = b->ctx.len, reverse = b->ctx.reverse;
-  const float lg = b->ctx.lg;
-  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
-  const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16) + P::kColX;
-  uint8_t* xt = sm + P::kOffX;
-  // block k: rows r, r + 8, columns c0 + 8 g + {0, 1}
-  auto row_of = [&](int k) { return (D == 128 ? 32 * qd + 16 * (k / 2) : 16 * qd) + (lane >> 2); };
-  auto col_of = [&](int k) { return 64 * half + 32 * (k % 2); };
-  auto tmem_of = [&](int k) { return tl + ((uint32_t)(D == 128 ? 16 * (k / 2) : 0) << 16) + (uint32_t)col_of(k); };
-  auto tile = [&](int k, const float* v) {
+  static constexpr int kBlocks = D == 128 ? 4 : 2;          // of 16 x 32 elements
+  uint8_t* xt;
+  PassBars* b;
+  int lane, r0, c0, d, n, all, reverse;
+  uint32_t tl;
+  float lg;
+  Guard gd;
+  __device__ __forceinline__ Carry(uint8_t* sm, PassBars* b_, int warp, int lane_)
+      : xt(sm + P::kOffX), b(b_), lane(lane_), r0((D == 128 ? 32 : 16) * (warp & 3) + (lane_ >> 2)),
+        c0(64 * ((warp - P::kWarpX) >> 2)), d(b_->ctx.d), n(b_->ctx.n), all(b_->ctx.len), reverse(b_->ctx.reverse),
+        tl(b_->tbase + ((uint32_t)(32 * (warp & 3)) << 16) + P::kColX), lg(b_->ctx.lg),
+        gd(make_guard(&b_->abort, b_->ctx.wait_ns)) {}
+
+  // block k: rows r, r + 8, columns c + 8 g + {0, 1}
+  __device__ __forceinline__ int row_of(int k) const { return r0 + 16 * (k >> 1); }
+  __device__ __forceinline__ int col_of(int k) const { return c0 + 32 * (k & 1); }
+  __device__ __forceinline__ uint32_t tmem_of(int k) const {
+    return tl + ((uint32_t)(16 * (k >> 1)) << 16) + (uint32_t)col_of(k);
+  }
+  // decay of X over chunk i
+  __device__ __forceinline__ float over(int i) const { return decay_pow(lg, chunk_len(chunk_of(i, n, reverse), all)); }
+  // the tile for the next chunk, and X times its decay over that chunk for dX to be added to
+  __device__ __forceinline__ void keep(int k, float* v, float wl) {
     const int r = row_of(k);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      reinterpret_cast<uint32_t*>(piece(xt, D, r, col_of(k) / 8 + g))[lane & 3] = pack_bf16(v[4 * g], v[4 * g + 1]);
-      reinterpret_cast<uint32_t*>(piece(xt, D, r + 8, col_of(k) / 8 + g))[lane & 3] = pack_bf16(v[4 * g + 2], v[4 * g + 3]);
+      uint32_t* p = reinterpret_cast<uint32_t*>(piece(xt, D, r, col_of(k) / 8 + g)) + (lane & 3);
+      p[0] = pack_bf16(v[4 * g], v[4 * g + 1]);
+      p[256] = pack_bf16(v[4 * g + 2], v[4 * g + 3]);  // 8 rows of 128 bytes on: the same swizzle
     }
-  };
-  // the tile for the next chunk, and X times its decay over that chunk for dX to be added to
-  auto keep = [&](int k, float* v, float wl) {
-    tile(k, v);
 #pragma unroll
     for (int x = 0; x < 8; ++x)
       reinterpret_cast<float2*>(v)[x] = mul2(reinterpret_cast<float2*>(v)[x], make_float2(wl, wl));
     tmem_st16x32(tmem_of(k), v);
-  };
-  auto publish = [&] {
+  }
+  __device__ __forceinline__ void publish() {
     tmem_st_wait();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->x_full);
-  };
-  {
+  }
+  __device__ __forceinline__ void start() {
     grid_dependency_wait();  // the states entering the segments
     const float* from = b->ctx.from;
     const bool from_t = b->ctx.from_t != 0;
-    const float wl = decay_pow(lg, chunk_len(chunk_of(0, n, reverse), all));
+    const float wl = over(0);
 #pragma unroll 1
     for (int k = 0; k < kBlocks; ++k) {
       float v[16];
@@ -714,15 +733,14 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
       __syncwarp();
       keep(k, v, wl);
     }
+    publish();
   }
-  publish();
-#pragma unroll 1
-  for (int i = 0; i < nx; ++i) {
+  __device__ __forceinline__ bool update(int i) {
     const bool more = i + 1 < n;
-    const float wl = more ? decay_pow(lg, chunk_len(chunk_of(i + 1, n, reverse), all)) : 1.f;
+    const float wl = more ? over(i + 1) : 1.f;
     float* to = more ? nullptr : b->ctx.to;
     // (inter has read the last tile)
-    if (!wait_warp(&b->in_full, i & 1, gd) || !wait_warp(&b->dx_full, i & 1, gd)) return;
+    if (!wait_warp(&b->in_full, i & 1, gd) || !wait_warp(&b->dx_full, i & 1, gd)) return false;
     tc_fence_after();
 #pragma unroll 2
     for (int k = 0; k < kBlocks; ++k) {
@@ -743,7 +761,40 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
       }
     }
     if (more) publish();
+    return true;
   }
+};
+
+template <int D>
+__device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int lane) {
+  Weigh<D> w(sm, b, warp, lane);
+  const int n = b->ctx.n, nx = b->ctx.nx;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i)
+    if (!w.map(i) || i >= nx || !w.weigh(i)) return;
+}
+
+template <int D>
+__device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane) {
+  Carry<D> x(sm, b, warp, lane);
+  const int nx = b->ctx.nx;
+  x.start();
+#pragma unroll 1
+  for (int i = 0; i < nx; ++i)
+    if (!x.update(i)) return;
+}
+
+// Both in the same warps.
+template <int D>
+__device__ __noinline__ void pass_weigh_x(uint8_t* sm, PassBars* b, int warp, int lane) {
+  Weigh<D> w(sm, b, warp, lane);
+  Carry<D> x(sm, b, warp, lane);
+  const int n = b->ctx.n, nx = b->ctx.nx;
+  if (!w.map(0)) return;
+  x.start();
+#pragma unroll 1
+  for (int i = 0; i < nx; ++i)
+    if (!w.weigh(i) || (i + 1 < n && !w.map(i + 1)) || !x.update(i)) return;
 }
 
 template <int D>
@@ -766,7 +817,8 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     }
     for (uint64_t* m : {&b->a_full, &b->s_full, &b->in_full, &b->dx_full, &b->o_full, &b->fin}) mbar_init(m, 1);
     for (uint64_t* m : {&b->mapped, &b->w_full}) mbar_init(m, 4);
-    for (uint64_t* m : {&b->x_full, &b->p_full, &b->o_free}) mbar_init(m, 4 * P::kSplit);
+    for (uint64_t* m : {&b->p_full, &b->o_free}) mbar_init(m, 8);
+    mbar_init(&b->x_full, P::kXWarps);
     b->abort = 0;
     b->issued = b->issued_a = 0;
     fence_mbar_init();
@@ -841,10 +893,13 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
       pass_out<D, false>(b, warp, lane);
     else
       pass_out<D, true>(b, warp, lane);
-  } else if (warp < P::kWarpX) {
-    pass_weigh<D>(sm, b, warp, lane);
+  } else if constexpr (D == 128) {
+    if (warp < P::kWarpX)
+      pass_weigh<D>(sm, b, warp, lane);
+    else
+      pass_x<D>(sm, b, warp, lane);
   } else {
-    pass_x<D>(sm, b, warp, lane);
+    pass_weigh_x<D>(sm, b, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
