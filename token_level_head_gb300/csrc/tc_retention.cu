@@ -84,7 +84,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Guard
     if (mbar_try_wait_ns(bar, parity, g.nap)) return true;
     if (aborted(g)) return false;
     const uint64_t now = globaltimer_ns();
-    if (t0 == 0)
+    if (t0 == 0 && g.limit >= 1000)  // (a limit below one sleep: give up now)
       t0 = now;
     else if (now - t0 > g.limit)
       break;
@@ -250,13 +250,47 @@ __device__ __noinline__ void weigh_phi_row2(uint8_t* hi, uint8_t* lo, int r, int
   }
 }
 
-// MMAs of one product D[tmem] (+)= A^T-like operands, MN-major in both: A [K rows][M], B [K rows][N], K = 128.
-template <int M, int N>
-__device__ __forceinline__ void mma_outer(uint32_t d, uint32_t a, uint32_t b, bool acc = true) {
-  const uint64_t da = smem_desc(a, kAtom, 1024), db = smem_desc(b, kAtom, 1024);
+// ---------------------------------------------------------------- products
+// Shared-memory descriptors are kept as their two words: only the start address, in the low one, changes.
+struct Desc {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc make_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  const uint64_t d = smem_desc(saddr, lbo_bytes, sbo_bytes);
+  return {(uint32_t)d, (uint32_t)(d >> 32)};
+}
+
+// One MMA, K = 16: A at `bytes_a` behind its descriptor's start, B at `bytes_b`; the constants are immediates, so
+// that the issuing thread spends a few instructions on each.
+template <uint32_t IDESC, bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, uint32_t bytes_a, Desc b, uint32_t bytes_b) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a.lo + (bytes_a >> 4)), "r"(a.hi), "r"(b.lo + (bytes_b >> 4)), "r"(b.hi), "r"(IDESC), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+template <uint32_t IDESC, bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t bytes_b) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b.lo + (bytes_b >> 4)), "r"(b.hi), "r"(IDESC), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+
+// D[tmem] (+)= A^T B, both operands MN-major: A [128 rows][M], B [128 rows][N].
+template <int M, int N, bool ACC>
+__device__ __forceinline__ void mma_outer(uint32_t d, Desc a, Desc b) {
+  constexpr uint32_t kId = idesc_bf16_f32(M, N, 1, 1);
+  mma_ss<kId, ACC>(d, a, 0, b, 0);
 #pragma unroll
-  for (int k = 0; k < kTok / 16; ++k)
-    mma_bf16(d, da + k * (2048 >> 4), db + k * (2048 >> 4), idesc_bf16_f32(M, N, 1, 1), acc || k > 0);
+  for (int k = 1; k < kTok / 16; ++k) mma_ss<kId, true>(d, a, k * 2048, b, k * 2048);
 }
 
 // Prefetch of one operand's chunk into L2.
@@ -380,66 +414,85 @@ __device__ __noinline__ void pass_producer(uint8_t* sm, PassBars* b) {
   }
 }
 
+// The whole warp waits, one lane issues (the same one each time: elect.sync is deterministic).  With the issue
+// under an election the operands stay in uniform registers: an MMA costs the issuing lane 14 cycles, not 45.
 template <int D>
 __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
   using P = PassTile<D>;
   const int n = b->ctx.n, nx = b->ctx.nx, len = b->ctx.len, reverse = b->ctx.reverse, terms = b->ctx.terms;
   const bool mapped = b->ctx.mapped();
-  const uint32_t tmem = b->tbase, a0 = smem_u32(sm + P::kOffA), lo = smem_u32(sm + P::kOffLo), xt = smem_u32(sm + P::kOffX);
+  const uint32_t tmem = b->tbase;
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
+  // K-major A and B for the scores; MN-major: X (rows c), B w, its other parts and C (rows = tokens)
+  const Desc qa = make_desc(smem_u32(sm + P::kOffA), 16, 1024), x = make_desc(smem_u32(sm + P::kOffX), D * 128, 1024);
+  const Desc bk0 = make_desc(smem_u32(sm + P::kOffBC), 16, 1024);
+  const Desc bm0 = make_desc(smem_u32(sm + P::kOffBC), kAtom, 1024);
+  const Desc lo = make_desc(smem_u32(sm + P::kOffLo), kAtom, 1024), lo2 = make_desc(smem_u32(sm + P::kOffX), kAtom, 1024);
   int maps = 0;
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int s = i % kStages;
-    const uint32_t b0 = smem_u32(sm + P::kOffBC + s * 2 * P::kOp), c0 = b0 + P::kOp;
-    if (!wait(&b->full[s], (i / kStages) & 1, gd) || !wait(&b->a_full, i & 1, gd)) return;
-    if (i > 0 && !wait(&b->o_full, (i - 1) & 1, gd)) return;  // the scores go over P of the last chunk
+    const uint32_t at = s * (2 * P::kOp >> 4);  // the stage
+    const Desc bk{bk0.lo + at, bk0.hi}, bm{bm0.lo + at, bm0.hi}, cm{bm0.lo + at + (P::kOp >> 4), bm0.hi};
+    if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return;
+    if (i > 0 && !wait_warp(&b->o_full, (i - 1) & 1, gd)) return;  // the scores go over P of the last chunk
     if (mapped || chunk_len(chunk_of(i, n, reverse), len) < kTok) {
-      if (!wait(&b->mapped, maps & 1, gd)) return;
+      if (!wait_warp(&b->mapped, maps & 1, gd)) return;
       ++maps;
     }
-    if (D == 64 && i > 0 && !wait(&b->o_free, (i - 1) & 1, gd)) return;  // (and over intra)
+    if (D == 64 && i > 0 && !wait_warp(&b->o_free, (i - 1) & 1, gd)) return;  // (and over intra)
     tc_fence_after();
+    __syncwarp();
+    if (elect_one()) {
+      constexpr uint32_t kId = idesc_bf16_f32(128, 128, 0, 0);
+      mma_ss<kId, false>(tmem + P::kColS, qa, 0, bk, 0);
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k / 4) * kAtom + (k % 4) * 32;
-      mma_bf16(tmem + P::kColS, smem_desc(a0 + off, 16, 1024), smem_desc(b0 + off, 16, 1024),
-               idesc_bf16_f32(128, 128, 0, 0), k > 0);
+      for (int k = 1; k < D / 16; ++k) {
+        const uint32_t off = (k / 4) * kAtom + (k % 4) * 32;
+        mma_ss<kId, true>(tmem + P::kColS, qa, off, bk, off);
+      }
+      mma_commit(&b->s_full);
     }
-    mma_commit(&b->s_full);
-    if (!wait(&b->x_full, i & 1, gd)) return;
-    if (D != 64 && i > 0 && !wait(&b->o_free, (i - 1) & 1, gd)) return;
+    if (!wait_warp(&b->x_full, i & 1, gd)) return;
+    if (D != 64 && i > 0 && !wait_warp(&b->o_free, (i - 1) & 1, gd)) return;
     tc_fence_after();
-    {
-      const uint64_t dx = smem_desc(xt, D * 128, 1024);
+    __syncwarp();
+    if (elect_one()) {
+      constexpr uint32_t kId = idesc_bf16_f32(128, D, 0, 1);
+      mma_ss<kId, false>(tmem + P::kColInter, qa, 0, x, 0);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_bf16(tmem + P::kColInter, smem_desc(a0 + (k / 4) * kAtom + (k % 4) * 32, 16, 1024), dx + k * (2048 >> 4),
-                 idesc_bf16_f32(128, D, 0, 1), k > 0);
+      for (int k = 1; k < D / 16; ++k)
+        mma_ss<kId, true>(tmem + P::kColInter, qa, (k / 4) * kAtom + (k % 4) * 32, x, k * 2048);
+      mma_commit(&b->in_full);
     }
-    mma_commit(&b->in_full);
-    if (!wait(&b->p_full, i & 1, gd)) return;
+    if (!wait_warp(&b->p_full, i & 1, gd)) return;
     tc_fence_after();
-    {
-      const uint64_t dc = smem_desc(c0, kAtom, 1024);
+    __syncwarp();
+    if (elect_one()) {
       constexpr int kN = D == 128 ? 128 : 32;  // columns of intra in one place
+      constexpr uint32_t kId = idesc_bf16_f32(128, kN, 0, 1);
 #pragma unroll
-      for (int e = 0; e < D; e += kN)
+      for (int e = 0; e < D; e += kN) {
+        mma_ts<kId, false>(tmem + P::intra(e), tmem + P::kColS, cm, 2 * e);
 #pragma unroll
-        for (int k = 0; k < kTok / 16; ++k)
-          mma_bf16_ts(tmem + P::intra(e), tmem + P::kColS + 8 * k + (k >= 4 ? 32 : 0), dc + k * (2048 >> 4) + e * 2 / 16,
-                      idesc_bf16_f32(128, kN, 0, 1), k > 0);
+        for (int k = 1; k < kTok / 16; ++k)
+          mma_ts<kId, true>(tmem + P::intra(e), tmem + P::kColS + 8 * k + (k >= 4 ? 32 : 0), cm, k * 2048 + 2 * e);
+      }
+      mma_commit(&b->o_full);
+      if (i >= nx) mma_commit(&b->empty[s]);
     }
-    mma_commit(&b->o_full);
     if (i < nx) {
-      if (!wait(&b->w_full, i & 1, gd)) return;
+      if (!wait_warp(&b->w_full, i & 1, gd)) return;
       tc_fence_after();
-      mma_outer<D, D>(tmem + P::kColX, b0, c0);
-      mma_outer<D, D>(tmem + P::kColX, lo, c0);
-      if (terms > 2) mma_outer<D, D>(tmem + P::kColX, xt, c0);
-      mma_commit(&b->dx_full);
+      __syncwarp();
+      if (elect_one()) {
+        mma_outer<D, D, true>(tmem + P::kColX, bm, cm);
+        mma_outer<D, D, true>(tmem + P::kColX, lo, cm);
+        if (terms > 2) mma_outer<D, D, true>(tmem + P::kColX, lo2, cm);
+        mma_commit(&b->dx_full);
+        mma_commit(&b->empty[s]);
+      }
     }
-    mma_commit(&b->empty[s]);
   }
 }
 
@@ -883,10 +936,9 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     if (lane == 0) pass_producer<D>(sm, b);
     __syncwarp();
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      pass_mma<D>(sm, b);
-      mma_commit(&b->fin);
-    }
+    pass_mma<D>(sm, b);
+    __syncwarp();
+    if (elect_one()) mma_commit(&b->fin);
     __syncwarp();
   } else if (warp < P::kWarpW) {
     if (b->ctx.x == nullptr)
@@ -1009,18 +1061,26 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      for (int i = 0; i < n; ++i) {
-        const int s = i % P::kStages;
-        if (!wait(&b->ready[s], (i / P::kStages) & 1, gd)) break;
-        tc_fence_after();
-        const uint32_t b0 = smem_u32(sm + s * 2 * P::kOp);
-        mma_outer<D, D>(tmem, b0, b0 + P::kOp, i > 0);
-        mma_outer<D, D>(tmem, smem_u32(lo), b0 + P::kOp, true);
+    const Desc b0 = make_desc(smem_u32(sm), kAtom, 1024), dlo = make_desc(smem_u32(lo), kAtom, 1024);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int s = i % P::kStages;
+      if (!wait_warp(&b->ready[s], (i / P::kStages) & 1, gd)) break;
+      tc_fence_after();
+      const Desc bm{b0.lo + s * (2 * P::kOp >> 4), b0.hi}, cm{bm.lo + (P::kOp >> 4), b0.hi};
+      __syncwarp();
+      if (elect_one()) {
+        if (i == 0)
+          mma_outer<D, D, false>(tmem, bm, cm);
+        else
+          mma_outer<D, D, true>(tmem, bm, cm);
+        mma_outer<D, D, true>(tmem, dlo, cm);
         mma_commit(&b->empty[s]);
       }
-      mma_commit(&b->fin);
+      __syncwarp();
     }
+    __syncwarp();
+    if (elect_one()) mma_commit(&b->fin);
     __syncwarp();
   } else {
     const int qd = warp & 3, row = 32 * qd + lane, half = (warp - kWarpOut) >> 2;
