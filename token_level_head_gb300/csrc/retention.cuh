@@ -55,8 +55,17 @@ struct Segment {
   int seq;     // sequence, -1: no such segment
   int seg;     // its number within the sequence
   int nseg;    // segments of the sequence
+  int g0;      // segments of the sequences before it: this one's number is g0 + seg
   int row0;    // first token row (within the sequence's batch entry when dense)
   int len;     // tokens of the segment
+  int all;     // tokens of the sequence
+};
+
+// Which segments a kernel's blocks go over.
+enum SegmentKind {
+  SEG_ALL = 0,    // every segment
+  SEG_INNER = 1,  // nseg - 1 of each sequence: those that enter another one (numbered from 0)
+  SEG_SPLIT = 2   // one for each sequence of two segments or more
 };
 
 // Tokens [lo, hi) of packed sequence i.  Offsets outside [0, T] or out of order are clamped, so that
@@ -71,57 +80,92 @@ __device__ __forceinline__ int packed_segments(const RetArgs& a, int i) {
   return (hi - lo + a.L - 1) / a.L;
 }
 
-// Segment number g of the call (whole block; scratch: 34 ints of shared memory).  An empty sequence has none.  Packed sequences'
-// segments are numbered sequence after sequence: thread t counts those of B / blockDim.x sequences,
-// a block-wide scan finds the thread whose range holds g.
-__device__ __forceinline__ Segment find_segment(const RetArgs& a, int g, int* scratch) {
+__device__ __forceinline__ int segments_of_kind(int nseg, SegmentKind kind) {
+  return kind == SEG_ALL ? nseg : kind == SEG_INNER ? max(nseg - 1, 0) : nseg >= 2 ? 1 : 0;
+}
+
+// Number k of the call's segments of a kind (whole block; scratch: 68 ints of shared memory).  Packed sequences'
+// segments are numbered sequence after sequence: thread t counts those of B / blockDim.x sequences, a block-wide scan
+// finds the thread whose range holds k.  An empty sequence has none.
+__device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, SegmentKind kind, int* scratch) {
   Segment s;
+  int lo = 0;
   if (a.cu == nullptr) {
     s.nseg = (a.N + a.L - 1) / a.L;
-    s.seq = g / s.nseg;
-    s.seg = g - s.seq * s.nseg;
-    s.row0 = s.seg * a.L;
-    s.len = min(a.L, a.N - s.row0);
-    return s;
-  }
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = (blockDim.x + 31) >> 5;
-  const int per = (a.B + blockDim.x - 1) / blockDim.x;
-  const int i0 = min(tid * per, a.B), i1 = min(i0 + per, a.B);
-  int n = 0;
-  for (int i = i0; i < i1; ++i) n += packed_segments(a, i);
-  int inc = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 31) scratch[warp] = inc;
-  if (tid == 0) scratch[32] = -1;
-  __syncthreads();
-  int first = inc - n;
-  for (int w = 0; w < nw && w < warp; ++w) first += scratch[w];
-  if (g >= first && g < first + n) {
+    const int per = segments_of_kind(s.nseg, kind);
+    s.seq = per > 0 && k < a.B * per ? k / per : -1;
+    if (s.seq < 0) return s;
+    s.seg = k - s.seq * per;
+    s.g0 = s.seq * s.nseg;
+    s.all = a.N;
+  } else {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + blockDim.x - 1) / blockDim.x;
+    const int i0 = min(tid * per, a.B), i1 = min(i0 + per, a.B);
+    int n = 0, m = 0;  // of the kind, in all
     for (int i = i0; i < i1; ++i) {
-      const int m = packed_segments(a, i);
-      if (g < first + m) {
-        scratch[32] = i;
-        scratch[33] = g - first;
-        break;
+      const int q = packed_segments(a, i);
+      n += segments_of_kind(q, kind);
+      m += q;
+    }
+    int in = n, im = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, in, o), v = __shfl_up_sync(0xffffffffu, im, o);
+      if (lane >= o) {
+        in += u;
+        im += v;
       }
-      first += m;
+    }
+    if (lane == 31) {
+      scratch[warp] = in;
+      scratch[32 + warp] = im;
+    }
+    if (tid == 0) scratch[64] = -1;
+    __syncthreads();
+    int first = in - n, g0 = im - m;
+    for (int w = 0; w < warp; ++w) {
+      first += scratch[w];
+      g0 += scratch[32 + w];
+    }
+    if (k >= first && k < first + n) {
+      for (int i = i0; i < i1; ++i) {
+        const int q = packed_segments(a, i), c = segments_of_kind(q, kind);
+        if (k < first + c) {
+          scratch[64] = i;
+          scratch[65] = k - first;
+          scratch[66] = g0;
+          break;
+        }
+        first += c;
+        g0 += q;
+      }
+    }
+    __syncthreads();
+    s.seq = scratch[64];
+    s.seg = scratch[65];
+    s.g0 = scratch[66];
+    __syncthreads();
+    if (s.seq < 0) return s;
+    int hi;
+    packed_range(a, s.seq, &lo, &hi);
+    s.nseg = packed_segments(a, s.seq);
+    s.all = hi - lo;
+    if (s.g0 + s.nseg > a.G) {  // (offsets out of order may claim more segments than the workspace has)
+      s.seq = -1;
+      return s;
     }
   }
-  __syncthreads();
-  s.seq = scratch[32];
-  s.seg = scratch[33];
-  __syncthreads();
-  if (s.seq < 0) return s;
-  int lo, hi;
-  packed_range(a, s.seq, &lo, &hi);
-  s.nseg = packed_segments(a, s.seq);
   s.row0 = lo + s.seg * a.L;
-  s.len = max(0, min(a.L, hi - s.row0));
+  s.len = max(0, min(a.L, s.all - s.seg * a.L));
   return s;
+}
+// The segment of an inner one (SEG_INNER) in a pass's direction: forward all but the last, reverse all but the first.
+__device__ __forceinline__ void inner_segment(const RetArgs& a, Segment& s, int reverse) {
+  if (reverse == 0) return;
+  s.seg += 1;
+  s.row0 += a.L;
+  s.len = max(0, min(a.L, s.all - s.seg * a.L));
 }
 
 // Base of sequence seq, head h: packed sequences share batch entry 0.
@@ -137,6 +181,15 @@ __device__ __forceinline__ int ret_slot(const int* slots, int n_slots, int seq) 
   bool taken = false;
   for (int i = threadIdx.x; i < seq; i += blockDim.x) taken |= slots[i] == s;
   return __syncthreads_or(taken) || s < 0 || s >= n_slots ? -1 : s;
+}
+
+// The state entering a segment of head h (null: zero); slot: the sequence's state slot, -1 for none.  The states in
+// the workspace are there behind grid_dependency_wait().
+__device__ __forceinline__ const float* entering_state(const RetArgs& a, const RetPass& p, const Segment& sg, int h,
+                                                       int slot) {
+  const size_t dd = (size_t)a.d * a.d;
+  if (sg.nseg > 1) return a.seg + (((size_t)p.sum * a.G + sg.g0 + sg.seg) * a.H + h) * dd;
+  return a.load && slot >= 0 ? a.states + ((size_t)slot * a.H + h) * dd : nullptr;
 }
 
 }  // namespace mhla

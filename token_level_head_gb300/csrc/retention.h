@@ -46,7 +46,8 @@ struct RetArgs {
   const int* slots;             // [B] or null (sequence i uses slot i)
   int n_slots, load;
   int L;                        // tokens of a segment (a multiple of 128)
-  int G;                        // segments in all (packed: at most)
+  int G;                        // segments in all; of those, segments that enter another one; sequences of two
+  int inner, split;             // segments or more (packed: at most)
   float* seg;                   // [nsum][G][H][d][d] segment states; null when no sequence has two segments
   unsigned* status;             // the workspace's status word
 };

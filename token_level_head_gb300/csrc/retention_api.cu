@@ -106,51 +106,58 @@ bool options_ok(const retention_options* opt) {
 // ---- segments
 struct Plan {
   int L, G;      // tokens of a segment, segments
+  int inner, splits;  // segments that enter another one, sequences of two or more
   size_t bytes;  // workspace
   bool split;    // some sequence may have two segments
 };
 
-// The length of a segment.  In units of a chunk's time in a pass, with `slots` blocks at once and segments of
-// n chunks, a call takes
-//   pass:  (rounds of blocks) (n + start)
-//   split: (rounds) (n + start) sum, then `fixed` for two more launches
-// where a round is slots blocks; packed sequences, of unknown lengths, take their work over slots and half a
-// block for the tail.  The costs are measured ones: a chunk takes 3.8 us at d = 128 and 5.4 us at d = 64
-// (two blocks an SM), a block 2.5 chunks to start, its sum pass 0.45 of the pass's time, two launches 8 us.
-// fp32 (SIMT, chunks of 64 tokens counted as two): 14 us.
+// The length of a segment: the n chunks of 128 tokens for which a call is estimated to take least, in units of a
+// chunk's time in a pass:
+//   pass   (rounds of blocks) (n + start)
+//   split  (rounds) (n + start) sum  +  a state for each segment, written and read by the sums' kernel, the scan and
+//          the pass  +  two more launches
+// where a round is `slots` blocks.  Packed sequences, of unknown lengths, take their work over the slots and half a
+// block for the tail; four times the mean counts as their longest.  The costs are measured ones: a chunk takes 3.3 us
+// at d = 128 and 3.8 us at d = 64 (two blocks an SM), a block 2.5 chunks to start, the sum of a chunk 0.45 of its
+// pass, a segment's state 2 chunks, two launches 8 us; fp32 (SIMT; 128 tokens) 14 us a chunk.
 Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward) {
   const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
   const double slots = f32 ? 152.0 * (d == 128 ? 1 : d == 64 ? 2 : 4) : d == 128 ? 152.0 : 304.0;
-  const double chunk_us = f32 ? 14.0 : d == 128 ? 3.8 : 5.4;
-  const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, fixed = 8.0 / chunk_us;
+  const double fixed = 8.0 / (f32 ? 14.0 : d == 128 ? 3.3 : 3.8);
+  const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.5 : 2.0;
   const int cols = f32 && d == 128 ? 2 : 1;  // blocks that share a segment
   const long long all = (tokens + 127) / 128, most = ((long long)N + 127) / 128;
+  const double longest = packed ? std::min<double>((double)most, 4.0 * all / B) : (double)most;
   double best = 1e300;
   long long pick = most;
   for (long long n = 1; n <= most; n = n < 64 ? n + 1 : n + n / 16) {
-    if (n + n / 16 > most && n > 64) n = most;
     double cost;
     if (packed) {
-      const double segs = (double)all / n + 0.5 * B, work = (double)all + 0.5 * B;
-      const double blocks = segs * H * cols;
-      auto time = [&](double per) { return (work * H * cols + blocks * start) * per / slots + 0.5 * (n + start); };
-      cost = time(npass) + (n < most ? sum * time(nsum) + fixed : 0.0);
+      const double more = n < longest ? (double)all / n : 0.0;  // segments beyond one a sequence
+      const double work = ((double)all + 0.5 * B) * H * cols, blocks = ((double)B + more) * H * cols;
+      cost = (work + blocks * start) * npass / slots + 0.5 * (std::min<double>(n, longest) + start);
+      if (n < most) cost += fixed + (more > 0 ? (work + blocks * start) * nsum * sum / slots + more * H * nsum * state / slots : 0);
     } else {
       const long long segs = (most + n - 1) / n;
       const double blocks = (double)B * H * segs * cols;
       cost = std::ceil(blocks * npass / slots) * (n + start);
-      if (segs > 1) cost += std::ceil((double)B * H * (segs - 1) * cols * nsum / slots) * (n + start) * sum + fixed;
+      if (segs > 1)
+        cost += std::ceil((double)B * H * (segs - 1) * cols * nsum / slots) * (n + start) * sum + fixed +
+                (double)B * H * segs * nsum * state / slots;
     }
     if (cost < best) {
       best = cost;
       pick = n;
     }
   }
+  if (packed && pick >= longest) pick = std::max<long long>(32, (long long)longest);  // (a longer one would run alone)
   Plan p;
   p.L = (int)std::max<long long>(std::min<long long>(pick, 1 << 23) * 128, 128);
   p.G = (int)(packed ? tokens / p.L + B : (long long)B * ((N + p.L - 1) / p.L));
   p.split = N > p.L;
+  p.inner = packed ? (int)(tokens / p.L) : p.G - B;  // (an inner segment is a full one)
+  p.splits = packed ? std::min(B, p.inner) : B;
   p.bytes = kWorkspacePrefix + (p.split ? (size_t)nsum * p.G * H * d * d * sizeof(float) : 0);
   return p;
 }
@@ -171,7 +178,7 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
   if (!gamma || !aligned(gamma, 4) || !aligned(cu, 4)) return MHLA_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MHLA_ERR_INVALID_ARG;
   *plan = make_plan(B, H, tokens, d, dt, cu != nullptr, backward);
-  if ((long long)plan->G * H > 0x7fffffffll || (long long)B * H > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
+  if ((long long)plan->G * H > 0x7fffffffll / 3 || (long long)B * H > 0x7fffffffll / 3) return MHLA_ERR_UNSUPPORTED;
   if (ws_bytes < plan->bytes) return MHLA_ERR_INVALID_ARG;
   *e = {cu ? 1 : B, H, N, d, dt == MHLA_F32 ? 4 : 2};
   *a = RetArgs{};
@@ -185,6 +192,8 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
   a->scale = opt ? opt->scale : 1.f;
   a->L = plan->L;
   a->G = plan->G;
+  a->inner = plan->inner;
+  a->split = plan->splits;
   a->seg = plan->split ? reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspacePrefix) : nullptr;
   a->status = &static_cast<WorkspaceHeader*>(ws)->status;
   return MHLA_OK;

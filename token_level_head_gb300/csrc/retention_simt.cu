@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   float* sX = sC + kTok * C::ES;
   float* sP = sX + D * C::ES;
   float* sW = sP + kTok * C::LP;
-  __shared__ int scratch[34];
+  __shared__ int scratch[68];
   const int tid = threadIdx.x;
   launch_dependents();
   const int h = blockIdx.x % a.H, g = blockIdx.x / a.H;
@@ -80,32 +80,24 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
     for (int i = 0; i < a.npass; ++i)
       if (a.pass[i].sum == (int)blockIdx.z && !a.pass[i].sum_t) z = i;
   const RetPass& p = a.pass[z];
-  const Segment sg = find_segment(a, g, scratch);
+  Segment sg = find_segment(a, g, SUM ? SEG_INNER : SEG_ALL, scratch);
   if (sg.seq < 0) return;
+  if (SUM) inner_segment(a, sg, p.reverse);
   const int e0 = blockIdx.y * C::ES;
   const float lg = decay_log2(a.gamma[h]);
   const int tx = tid % C::NX, ty = tid / C::NX;
-  float* seg = a.seg == nullptr ? nullptr : a.seg + (((size_t)p.sum * a.G + g) * a.H + h) * (D * D);
-  if (SUM) {
-    // the last segment in the pass's direction enters no other
-    if (p.reverse ? sg.seg == 0 : sg.seg == sg.nseg - 1) return;
+  float* seg = a.seg == nullptr ? nullptr : a.seg + (((size_t)p.sum * a.G + sg.g0 + sg.seg) * a.H + h) * (D * D);
+  if (SUM)
     for (int i = tid; i < D * C::ES; i += kThreads) sX[i] = 0.f;
-  }
   int slot = -1;
   if (!SUM) {
-    const float* src = nullptr;
-    bool tr = false;
     if (a.states != nullptr) slot = ret_slot(a.slots, a.n_slots, sg.seq);
-    grid_dependency_wait();  // the states entering the segments
-    if (sg.nseg > 1) {
-      src = seg;
-      tr = p.sum_t != 0;
-    } else if (a.load && slot >= 0) {
-      src = a.states + ((size_t)slot * a.H + h) * (D * D);
-    }
+    const float* src = entering_state(a, p, sg, h, slot);
+    const bool tr = sg.nseg > 1 && p.sum_t;
+    grid_dependency_wait();
     for (int i = tid; i < D * C::ES; i += kThreads) {
       const int r = i / C::ES, e = e0 + i % C::ES;
-      sX[i] = src == nullptr ? 0.f : tr ? src[e * D + r] : src[r * D + e];
+      sX[i] = src == nullptr ? 0.f : __ldcg(src + (tr ? e * D + r : r * D + e));
     }
   }
   const long long ba = ret_base(a, p.a, sg.seq, h), bb = ret_base(a, p.b, sg.seq, h), bc = ret_base(a, p.c, sg.seq, h);
@@ -251,82 +243,75 @@ cudaError_t launch_passes(const RetArgs& a, cudaStream_t st) {
   cudaError_t e = opt_sum.ensure((const void*)retention_simt_kernel<D, true>, (int)C::kBytes);
   if (e == cudaSuccess) e = opt_out.ensure((const void*)retention_simt_kernel<D, false>, (int)C::kBytes);
   if (e != cudaSuccess) return e;
-  dim3 grid((unsigned)(a.G * a.H), D / C::ES, a.nsum);
+  dim3 grid((unsigned)((long long)a.inner * a.H), D / C::ES, a.nsum);
   if (a.seg != nullptr) {
     retention_simt_kernel<D, true><<<grid, kThreads, C::kBytes, st>>>(a);
     note_launch();
     e = retention_scan_launch(a, st);
     if (e != cudaSuccess) return e;
   }
+  grid.x = (unsigned)((long long)a.G * a.H);
   grid.z = a.npass;
   return launch_dependent(retention_simt_kernel<D, false>, grid, kThreads, C::kBytes, st, a.seg != nullptr, a);
 }
 
 // ================================================================ scan
-// A thread carries V elements of a head's state over its sequence's segments, in the pass's direction: the
-// slot of a segment holds the segment's own sum before, the state entering it after.  V = 4 where there are
-// many heads (most packed sequences have one segment, and their blocks end at once), 1 where few.
-template <int V>
+// A thread carries E groups of V elements of a head's state over its sequence's segments, in the pass's direction:
+// the slot of a segment holds the segment's own sum before, the state entering it after.  V = E = 4 where there are
+// many heads (most packed sequences have one segment, and their blocks end at once), single elements where few.
+template <int V, int E>
 __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_constant__ RetArgs a) {
-  __shared__ int part[kThreads / 32];
+  __shared__ int scratch[68];
   launch_dependents();
-  const int h = blockIdx.x % a.H, seq = blockIdx.x / a.H, set = blockIdx.z;
+  const int h = blockIdx.x % a.H, set = blockIdx.z;
   int ps = 0;
   for (int i = 0; i < a.npass; ++i)
     if (a.pass[i].sum == set && !a.pass[i].sum_t) ps = i;
   const bool reverse = a.pass[ps].reverse != 0;
-  int g0 = 0, nseg, len;
-  if (a.cu == nullptr) {
-    nseg = (a.N + a.L - 1) / a.L;
-    g0 = seq * nseg;
-    len = a.N;
-  } else {
-    int lo, hi;
-    packed_range(a, seq, &lo, &hi);
-    nseg = packed_segments(a, seq);
-    len = hi - lo;
-    if (nseg >= 2) {  // (uniform over the block)
-      int n = 0;
-      for (int i = threadIdx.x; i < seq; i += blockDim.x) n += packed_segments(a, i);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
-      __syncthreads();
-      for (int w = 0; w < kThreads / 32; ++w) g0 += part[w];
-    }
-  }
-  const int slot = nseg >= 2 && a.load && a.states != nullptr ? ret_slot(a.slots, a.n_slots, seq) : -1;
+  const Segment sg = find_segment(a, blockIdx.x / a.H, SEG_SPLIT, scratch);
+  const int slot = sg.seq >= 0 && a.load && a.states != nullptr ? ret_slot(a.slots, a.n_slots, sg.seq) : -1;
   grid_dependency_wait();  // the sums are there
-  if (nseg < 2) return;    // the pass takes its state from the slot itself
-  nseg = min(nseg, a.G - g0);
-  const int n = a.d * a.d, e = (blockIdx.y * kThreads + threadIdx.x) * V;
-  if (e >= n) return;
+  if (sg.seq < 0) return;
+  const int nseg = sg.nseg, g0 = sg.g0, len = sg.all;
+  const int n = a.d * a.d, e0 = (blockIdx.y * E * kThreads + threadIdx.x) * V;
   const float lg = decay_log2(a.gamma[h]);
   const float wfull = decay_pow(lg, a.L), wlast = decay_pow(lg, len - (nseg - 1) * a.L);
   const size_t step = (size_t)a.H * n;
   struct alignas(4 * V) Vec {
     float v[V];
   };
-  Vec x{};
-  if (slot >= 0) x = *reinterpret_cast<const Vec*>(a.states + ((size_t)slot * a.H + h) * n + e);
-  float* w = a.seg + (((size_t)set * a.G + g0) * a.H + h) * n + e;
-  constexpr int kAhead = 16 / V;  // loads in flight
+  Vec x[E] = {};
+  if (slot >= 0)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (e0 + i * kThreads * V < n)
+        x[i] = *reinterpret_cast<const Vec*>(a.states + ((size_t)slot * a.H + h) * n + e0 + i * kThreads * V);
+  float* w = a.seg + (((size_t)set * a.G + g0) * a.H + h) * n + e0;
+  constexpr int kAhead = E == 1 ? 16 : 2;  // segments loaded ahead
   for (int j0 = 0; j0 < nseg; j0 += kAhead) {
-    Vec u[kAhead];
+    Vec u[kAhead][E];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = j0 + j;
-      u[j] = Vec{};
-      if (k < nseg - 1) u[j] = *reinterpret_cast<const Vec*>(w + (size_t)(reverse ? nseg - 1 - k : k) * step);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        u[j][i] = Vec{};
+        if (k < nseg - 1 && e0 + i * kThreads * V < n)
+          u[j][i] = *reinterpret_cast<const Vec*>(w + (size_t)(reverse ? nseg - 1 - k : k) * step + i * kThreads * V);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = j0 + j;
       if (k >= nseg) break;
       const int sgm = reverse ? nseg - 1 - k : k;
-      *reinterpret_cast<Vec*>(w + (size_t)sgm * step) = x;
+      const float wl = sgm == nseg - 1 ? wlast : wfull;
 #pragma unroll
-      for (int i = 0; i < V; ++i) x.v[i] = fmaf(sgm == nseg - 1 ? wlast : wfull, x.v[i], u[j].v[i]);
+      for (int i = 0; i < E; ++i) {
+        if (e0 + i * kThreads * V < n) *reinterpret_cast<Vec*>(w + (size_t)sgm * step + i * kThreads * V) = x[i];
+#pragma unroll
+        for (int q = 0; q < V; ++q) x[i].v[q] = fmaf(wl, x[i].v[q], u[j][i].v[q]);
+      }
     }
   }
 }
@@ -474,10 +459,10 @@ cudaError_t simt_retention_launch(const RetArgs& a, cudaStream_t st) {
 }
 
 cudaError_t retention_scan_launch(const RetArgs& a, cudaStream_t st) {
-  const int n = a.d * a.d, v = (long long)a.B * a.H * a.nsum >= 64 ? 4 : 1;
-  const dim3 grid((unsigned)(a.B * a.H), (n / v + kThreads - 1) / kThreads, a.nsum);
-  return v == 4 ? launch_dependent(retention_scan_kernel<4>, grid, kThreads, 0, st, true, a)
-                : launch_dependent(retention_scan_kernel<1>, grid, kThreads, 0, st, true, a);
+  const int n = a.d * a.d, per = (long long)a.split * a.H * a.nsum >= 64 ? 16 : 1;  // elements of a thread
+  const dim3 grid((unsigned)((long long)a.split * a.H), (n + per * kThreads - 1) / (per * kThreads), a.nsum);
+  return per == 16 ? launch_dependent(retention_scan_kernel<4, 4>, grid, kThreads, 0, st, true, a)
+                   : launch_dependent(retention_scan_kernel<1, 1>, grid, kThreads, 0, st, true, a);
 }
 
 cudaError_t retention_step_launch(int B, int H, int d, mhla_dtype dt, const RetTensor& q, const RetTensor& k,

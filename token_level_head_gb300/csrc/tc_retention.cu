@@ -68,23 +68,21 @@ struct TcArgs {
 struct Guard {
   int* abort;
   unsigned long long limit;
-  uint32_t nap;  // ns of one sleep
 };
-__device__ __forceinline__ Guard make_guard(int* abort, unsigned long long limit) {
-  return {abort, limit, limit < 1000 ? (uint32_t)limit : 1000u};
-}
+__device__ __forceinline__ Guard make_guard(int* abort, unsigned long long limit) { return {abort, limit}; }
 __device__ __forceinline__ bool aborted(const Guard& g) { return *reinterpret_cast<volatile int*>(g.abort) != 0; }
-// The thread sleeps in the barrier's own wait; the clock is read only after about a microsecond of that.
-// (Inline: a call would save the caller's registers, and most waits do wait.)
+constexpr uint32_t kNapNs = 1000;
+// The thread sleeps in the barrier's own wait; the clock is read only after about a microsecond of that, and a limit
+// below one sleep gives up at once.  (Inline: a call would save the caller's registers, and most waits do wait.)
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Guard& g) {
   if (mbar_test(bar, parity)) return true;
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (;;) {
-    if (mbar_try_wait_ns(bar, parity, g.nap)) return true;
+  while (g.limit >= kNapNs) {
+    if (mbar_try_wait_ns(bar, parity, kNapNs)) return true;
     if (aborted(g)) return false;
     const uint64_t now = globaltimer_ns();
-    if (t0 == 0 && g.limit >= 1000)  // (a limit below one sleep: give up now)
+    if (t0 == 0)
       t0 = now;
     else if (now - t0 > g.limit)
       break;
@@ -344,12 +342,12 @@ struct PassCtx {
   int reverse, terms;            // direction; bf16 numbers that B w is the sum of
   int fa, fb, fc, fx;            // feature maps of A, B, C and x
   int d;
-  int from_t;
   float lg;
   __nv_bfloat16* out;            // of the head; rows out_n apart
   const __nv_bfloat16 *x, *b;    // of the head: x (null: none), B
   long long out_n, x_n, b_n;
   const float* from;             // state entering the segment, null: zero
+  int from_t, from_ws;           // it is transposed; it is in the workspace
   float* to;                     // where the state after it goes, null: nowhere
   unsigned long long wait_ns;
   __device__ __forceinline__ bool mapped() const {
@@ -386,30 +384,37 @@ constexpr size_t pass_smem() {  // (the kernels' shared memory starts on 1024 by
 }
 static_assert(pass_smem<128>() <= 232448 && 2 * (pass_smem<64>() + 1024) <= 233472, "shared memory budget");
 
+// The loads of chunk i's B and C, and of its A (one thread).
+template <int D>
+__device__ __forceinline__ void load_bc(uint8_t* sm, PassBars* b, const PassCtx& c, int i) {
+  using P = PassTile<D>;
+  const int s = i % kStages, row = c.row0 + chunk_of(i, c.n, c.reverse) * kTok;
+  uint8_t* st = sm + P::kOffBC + s * 2 * P::kOp;
+  mbar_arrive_expect_tx(&b->full[s], 2 * P::kOp);
+  load_tile<D>(st, c.mb, row, c.hb, c.bb, &b->full[s]);
+  load_tile<D>(st + P::kOp, c.mc, row, c.hc, c.bc, &b->full[s]);
+  b->issued = i + 1;
+}
+template <int D>
+__device__ __forceinline__ void load_a(uint8_t* sm, PassBars* b, const PassCtx& c, int i) {
+  mbar_arrive_expect_tx(&b->a_full, PassTile<D>::kOp);
+  load_tile<D>(sm + PassTile<D>::kOffA, c.ma, c.row0 + chunk_of(i, c.n, c.reverse) * kTok, c.ha, c.ba, &b->a_full);
+  b->issued_a = i + 1;
+}
+
+// (The block's start has loaded chunk 0 and B and C of chunk 1.)  A has one tile: it is asked for when the last one
+// has been read, and brought to L2 before.
 template <int D>
 __device__ __noinline__ void pass_producer(uint8_t* sm, PassBars* b) {
-  using P = PassTile<D>;
   const PassCtx c = b->ctx;
   const Guard gd = make_guard(&b->abort, c.wait_ns);
-  auto row = [&](int i) { return c.row0 + chunk_of(i, c.n, c.reverse) * kTok; };
-  auto load_bc = [&](int i) {
-    const int s = i % kStages;
-    uint8_t* st = sm + P::kOffBC + s * 2 * P::kOp;
-    mbar_arrive_expect_tx(&b->full[s], 2 * P::kOp);
-    load_tile<D>(st, c.mb, row(i), c.hb, c.bb, &b->full[s]);
-    load_tile<D>(st + P::kOp, c.mc, row(i), c.hc, c.bc, &b->full[s]);
-    prefetch_tile<D>(c.ma, row(i), c.ha, c.ba);  // A has one tile: it is asked for when the last one has been read
-    b->issued = i + 1;
-  };
-  load_bc(0);
-  for (int i = 0; i < c.n; ++i) {
-    if (i > 0 && !wait(&b->in_full, (i - 1) & 1, gd)) return;
-    mbar_arrive_expect_tx(&b->a_full, P::kOp);
-    load_tile<D>(sm + P::kOffA, c.ma, row(i), c.ha, c.ba, &b->a_full);
-    b->issued_a = i + 1;
+  for (int i = 1; i < c.n; ++i) {
+    prefetch_tile<D>(c.ma, c.row0 + chunk_of(i, c.n, c.reverse) * kTok, c.ha, c.ba);
+    if (!wait(&b->in_full, (i - 1) & 1, gd)) return;
+    load_a<D>(sm, b, c, i);
     if (i + 1 < c.n) {
-      if (i + 1 >= kStages && !wait(&b->empty[(i + 1) % kStages], ((i + 1) / kStages - 1) & 1, gd)) return;
-      load_bc(i + 1);
+      if (!wait(&b->empty[(i + 1) % kStages], ((i + 1) / kStages - 1) & 1, gd)) return;
+      load_bc<D>(sm, b, c, i + 1);
     }
   }
 }
@@ -661,55 +666,71 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
   }
 }
 
-// One W warp, token row = 32 (warp % 4) + lane: the feature maps of a chunk and zeros behind the sequence (before
-// its scores), then B w (after them).
+// W warps, token row = 32 (warp % 4) + lane: the feature maps of chunk i and zeros behind the sequence, before its
+// scores.  (Functions of their own where they are rare: their registers would spill those of the loops.)
+template <int D>
+__device__ __noinline__ bool map_chunk(uint8_t* sm, PassBars* b, int row, int i, int len) {
+  using P = PassTile<D>;
+  const int s = i % kStages, d = b->ctx.d, fa = b->ctx.fa, fb = b->ctx.fb, fc = b->ctx.fc;
+  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
+  if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return false;
+  uint8_t *at = sm + P::kOffA, *bt = sm + P::kOffBC + s * 2 * P::kOp;
+  if (fa != kFeatIdentity) map_row<D>(at, row, kTok, d, fa);
+  if (fb != kFeatIdentity || len < kTok) map_row<D>(bt, row, len, d, fb);
+  if (fc != kFeatIdentity || len < kTok) map_row<D>(bt + P::kOp, row, len, d, fc);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((row & 31) == 0) mbar_arrive(&b->mapped);
+  return true;
+}
+
+// B w of chunk i in three parts, the third one over X's tile, once inter has read it.
+template <int D>
+__device__ __noinline__ bool weigh_chunk3(uint8_t* sm, PassBars* b, int row, int i, int ch, float w) {
+  using P = PassTile<D>;
+  const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
+  if (!wait_warp(&b->in_full, i & 1, gd)) return false;
+  uint8_t *bt = sm + P::kOffBC + (i % kStages) * 2 * P::kOp, *lo = sm + P::kOffLo, *lo2 = sm + P::kOffX;
+  if (b->ctx.fb != kFeatIdentity) {  // phi(b) in fp32 for the state
+    const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
+    weigh_phi_row3<D>(bt, lo, lo2, row, w, raw, b->ctx.d, b->ctx.fb);
+  } else {
+    weigh_row3<D>(bt, lo, lo2, row, w);
+  }
+  return true;
+}
+
+// One W warp: what precedes a chunk's scores (map), then B w (weigh).
 template <int D>
 struct Weigh {
   using P = PassTile<D>;
   uint8_t* sm;
   PassBars* b;
-  int lane, row, d, n, all, reverse, terms, fa, fb, fc;
+  int row, n, all, reverse;
   bool mapped;
   float lg;
   Guard gd;
-  __device__ __forceinline__ Weigh(uint8_t* sm_, PassBars* b_, int warp, int lane_)
-      : sm(sm_), b(b_), lane(lane_), row(32 * (warp & 3) + lane_), d(b_->ctx.d), n(b_->ctx.n), all(b_->ctx.len),
-        reverse(b_->ctx.reverse), terms(b_->ctx.terms), fa(b_->ctx.fa), fb(b_->ctx.fb), fc(b_->ctx.fc),
+  __device__ __forceinline__ Weigh(uint8_t* sm_, PassBars* b_, int warp, int lane)
+      : sm(sm_), b(b_), row(32 * (warp & 3) + lane), n(b_->ctx.n), all(b_->ctx.len), reverse(b_->ctx.reverse),
         mapped(b_->ctx.mapped()), lg(b_->ctx.lg), gd(make_guard(&b_->abort, b_->ctx.wait_ns)) {}
 
   __device__ __forceinline__ bool map(int i) {
-    const int s = i % kStages, len = chunk_len(chunk_of(i, n, reverse), all);
-    if (!mapped && len == kTok) return true;
-    if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return false;
-    uint8_t *at = sm + P::kOffA, *bt = sm + P::kOffBC + s * 2 * P::kOp;
-    if (fa != kFeatIdentity) map_row<D>(at, row, kTok, d, fa);
-    if (fb != kFeatIdentity || len < kTok) map_row<D>(bt, row, len, d, fb);
-    if (fc != kFeatIdentity || len < kTok) map_row<D>(bt + P::kOp, row, len, d, fc);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&b->mapped);
-    return true;
+    const int len = chunk_len(chunk_of(i, n, reverse), all);
+    return (!mapped && len == kTok) || map_chunk<D>(sm, b, row, i, len);
   }
   __device__ __forceinline__ bool weigh(int i) {
-    // B has been read by the scores, the second part by the last dX; the third part takes X's tile, once inter
-    // has read it
-    if (!wait_warp(&b->s_full, i & 1, gd) || (i > 0 && !wait_warp(&b->dx_full, (i - 1) & 1, gd)) ||
-        (terms > 2 && !wait_warp(&b->in_full, i & 1, gd)))
-      return false;
+    // B has been read by the scores, the second part's tile by the last dX
+    if (!wait_warp(&b->s_full, i & 1, gd) || (i > 0 && !wait_warp(&b->dx_full, (i - 1) & 1, gd))) return false;
     const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
-    uint8_t *bt = sm + P::kOffBC + (i % kStages) * 2 * P::kOp, *lo = sm + P::kOffLo, *lo2 = sm + P::kOffX;
     const float w = row < len ? decay_pow(lg, reverse ? row : len - 1 - row) : 0.f;
-    if (terms > 2 && fb != kFeatIdentity) {  // phi(b) in fp32 for the state
-      const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
-      weigh_phi_row3<D>(bt, lo, lo2, row, w, raw, d, fb);
-    } else if (terms > 2) {
-      weigh_row3<D>(bt, lo, lo2, row, w);
+    if (b->ctx.terms > 2) {
+      if (!weigh_chunk3<D>(sm, b, row, i, ch, w)) return false;
     } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
-      weigh_row2<D>(bt, lo, row, 0, w);
+      weigh_row2<D>(sm + P::kOffBC + (i % kStages) * 2 * P::kOp, sm + P::kOffLo, row, 0, w);
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&b->w_full);
+    if ((row & 31) == 0) mbar_arrive(&b->w_full);
     return true;
   }
 };
@@ -762,32 +783,6 @@ struct Carry {
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->x_full);
   }
-  __device__ __forceinline__ void start() {
-    grid_dependency_wait();  // the states entering the segments
-    const float* from = b->ctx.from;
-    const bool from_t = b->ctx.from_t != 0;
-    const float wl = over(0);
-#pragma unroll 1
-    for (int k = 0; k < kBlocks; ++k) {
-      float v[16];
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const int r = row_of(k) + 8 * (m & 1), c = col_of(k) + 8 * (m >> 1) + 2 * (lane & 3);
-        float2 u = make_float2(0.f, 0.f);
-        if (from != nullptr && r < d && c < d) {
-          if (from_t)
-            u = make_float2(__ldcg(from + c * d + r), __ldcg(from + (c + 1) * d + r));
-          else
-            u = __ldcg(reinterpret_cast<const float2*>(from + r * d + c));
-        }
-        v[4 * (m >> 1) + 2 * (m & 1)] = u.x;
-        v[4 * (m >> 1) + 2 * (m & 1) + 1] = u.y;
-      }
-      __syncwarp();
-      keep(k, v, wl);
-    }
-    publish();
-  }
   __device__ __forceinline__ bool update(int i) {
     const bool more = i + 1 < n;
     const float wl = more ? over(i + 1) : 1.f;
@@ -818,6 +813,34 @@ struct Carry {
   }
 };
 
+// The state entering the segment: into X and its tile.  (A function of its own, once a block: its registers would
+// spill those of the loops.)
+template <int D>
+__device__ __noinline__ void carry_start(uint8_t* sm, PassBars* b, int warp, int lane) {
+  Carry<D> x(sm, b, warp, lane);
+  const int d = b->ctx.d;
+  const float* from = b->ctx.from;
+  const bool from_t = b->ctx.from_t != 0;
+  const float wl = x.over(0);
+  if (b->ctx.from_ws) grid_dependency_wait();
+#pragma unroll 2
+  for (int k = 0; k < Carry<D>::kBlocks; ++k) {
+    float2 v[8];  // (loads without branches between them)
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const int r = x.row_of(k) + 8 * (m & 1), c = x.col_of(k) + 8 * (m >> 1) + 2 * (lane & 3);
+      const bool in = from != nullptr && r < d && c < d;
+      v[m] = make_float2(0.f, 0.f);
+      if (in && !from_t) v[m] = __ldcg(reinterpret_cast<const float2*>(from + r * d + c));
+      if (in && from_t) v[m].x = __ldcg(from + c * d + r);
+      if (in && from_t) v[m].y = __ldcg(from + (c + 1) * d + r);
+    }
+    __syncwarp();
+    x.keep(k, reinterpret_cast<float*>(v), wl);
+  }
+  x.publish();
+}
+
 template <int D>
 __device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int lane) {
   Weigh<D> w(sm, b, warp, lane);
@@ -829,9 +852,9 @@ __device__ __noinline__ void pass_weigh(uint8_t* sm, PassBars* b, int warp, int 
 
 template <int D>
 __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane) {
+  carry_start<D>(sm, b, warp, lane);
   Carry<D> x(sm, b, warp, lane);
   const int nx = b->ctx.nx;
-  x.start();
 #pragma unroll 1
   for (int i = 0; i < nx; ++i)
     if (!x.update(i)) return;
@@ -841,10 +864,10 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
 template <int D>
 __device__ __noinline__ void pass_weigh_x(uint8_t* sm, PassBars* b, int warp, int lane) {
   Weigh<D> w(sm, b, warp, lane);
-  Carry<D> x(sm, b, warp, lane);
   const int n = b->ctx.n, nx = b->ctx.nx;
+  carry_start<D>(sm, b, warp, lane);
   if (!w.map(0)) return;
-  x.start();
+  Carry<D> x(sm, b, warp, lane);
 #pragma unroll 1
   for (int i = 0; i < nx; ++i)
     if (!w.weigh(i) || (i + 1 < n && !w.map(i + 1)) || !x.update(i)) return;
@@ -859,11 +882,10 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int z = blockIdx.x % r.npass;  // a head's passes side by side: they read the same tensors
   const int unit = blockIdx.x / r.npass, g = unit / r.H, h = unit % r.H;
-  const Segment sg = find_segment(r, g, reinterpret_cast<int*>(b->decay));
+  const Segment sg = find_segment(r, g, SEG_ALL, reinterpret_cast<int*>(b->decay));
   if (sg.seq < 0) return;
-  const int slot = r.states != nullptr ? ret_slot(r.slots, r.n_slots, sg.seq) : -1;
-  const float lg = decay_log2(r.gamma[h]);
-  if (threadIdx.x == 0) {
+  const RetPass& p = r.pass[z];
+  if (threadIdx.x == 0) {  // the barriers, what the producer needs, and the first loads
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&b->full[s], 1);
       mbar_init(&b->empty[s], 1);
@@ -875,11 +897,8 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     b->abort = 0;
     b->issued = b->issued_a = 0;
     fence_mbar_init();
-  }
-  if (threadIdx.x == 64) {
-    const RetPass& p = r.pass[z];
+    fence_proxy_async_smem();
     const int ia = t.ia[z], ib = t.ib[z], ic = t.ic[z];
-    const size_t dd = (size_t)r.d * r.d;
     PassCtx& c = b->ctx;
     c.ma = &t.tm[ia];
     c.mb = &t.tm[ib];
@@ -891,11 +910,26 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     c.bb = t.by_b[ib] ? sg.seq : 0;
     c.bc = t.by_b[ic] ? sg.seq : 0;
     c.row0 = sg.row0;
-    c.len = sg.len;
     c.n = (sg.len + kTok - 1) / kTok;
-    c.to = slot >= 0 && sg.seg == sg.nseg - 1 ? r.states + ((size_t)slot * r.H + h) * dd : nullptr;
-    c.nx = c.to != nullptr ? c.n : c.n - 1;
     c.reverse = p.reverse;
+    c.wait_ns = t.wait_ns;
+    load_bc<D>(sm, b, c, 0);
+    load_a<D>(sm, b, c, 0);
+    if (c.n > 1) load_bc<D>(sm, b, c, 1);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&b->tbase, P::kCols);
+    tmem_relinquish();
+  }
+  const int slot = r.states != nullptr ? ret_slot(r.slots, r.n_slots, sg.seq) : -1;
+  const float lg = decay_log2(r.gamma[h]);
+  if (threadIdx.x == 64) {
+    const size_t dd = (size_t)r.d * r.d;
+    PassCtx& c = b->ctx;
+    const int n = (sg.len + kTok - 1) / kTok;
+    c.len = sg.len;
+    c.to = slot >= 0 && sg.seg == sg.nseg - 1 ? r.states + ((size_t)slot * r.H + h) * dd : nullptr;
+    c.nx = c.to != nullptr ? n : n - 1;
     c.terms = c.to != nullptr ? 3 : 2;
     c.fa = p.a.feature;
     c.fb = p.b.feature;
@@ -909,24 +943,13 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     c.out_n = p.out.sn;
     c.x_n = p.x.sn;
     c.b_n = p.b.sn;
-    c.from = sg.nseg > 1             ? r.seg + (((size_t)p.sum * r.G + g) * r.H + h) * dd
-             : r.load && slot >= 0 ? r.states + ((size_t)slot * r.H + h) * dd
-                                     : nullptr;
+    c.from = entering_state(r, p, sg, h, slot);
     c.from_t = sg.nseg > 1 && p.sum_t;
-    c.wait_ns = t.wait_ns;
+    c.from_ws = sg.nseg > 1;
   }
   if (threadIdx.x >= P::kThreads - kTok - 32) {
-    const int i = threadIdx.x - (P::kThreads - kTok - 32), n = r.pass[z].reverse ? kTok - 1 - i : i - 32;
+    const int i = threadIdx.x - (P::kThreads - kTok - 32), n = p.reverse ? kTok - 1 - i : i - 32;
     b->decay[i] = n >= 0 ? r.scale * decay_pow(lg, n) : 0.f;
-  }
-  if (warp == kWarpMma) {
-    tmem_alloc(&b->tbase, P::kCols);
-    tmem_relinquish();
-  }
-  if (warp == kWarpProd && lane == 0) {
-    prefetch_tmap(&t.tm[t.ia[z]]);
-    prefetch_tmap(&t.tm[t.ib[z]]);
-    prefetch_tmap(&t.tm[t.ic[z]]);
   }
   tc_fence_before();
   __syncthreads();
@@ -967,6 +990,7 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
   }
   __syncthreads();
   if (warp == kWarpMma) tmem_dealloc(b->tbase, P::kCols);
+  grid_dependency_wait();  // (a kernel does not end before those it may overlap)
 }
 
 // ================================================================ segment sums
@@ -991,7 +1015,7 @@ struct SumBars {
   uint32_t tbase;
   int abort;
   int issued;
-  int scratch[34];
+  int scratch[68];
 };
 
 template <int D>
@@ -1009,13 +1033,14 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
   launch_dependents();
   const RetArgs& r = t.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int set = blockIdx.x % r.nsum, unit = blockIdx.x / r.nsum, h = unit % r.H, g = unit / r.H;
+  const int set = blockIdx.x % r.nsum, unit = blockIdx.x / r.nsum, h = unit % r.H;
   int z = 0;
   for (int i = 0; i < r.npass; ++i)
     if (r.pass[i].sum == set && !r.pass[i].sum_t) z = i;
   const RetPass& p = r.pass[z];
-  const Segment sg = find_segment(r, g, b->scratch);
-  if (sg.seq < 0 || (p.reverse ? sg.seg == 0 : sg.seg == sg.nseg - 1)) return;  // enters no other segment
+  Segment sg = find_segment(r, unit / r.H, SEG_INNER, b->scratch);
+  if (sg.seq < 0) return;
+  inner_segment(r, sg, p.reverse);
   if (threadIdx.x == 0) {
     for (int s = 0; s < P::kStages; ++s) {
       mbar_init(&b->full[s], 1);
@@ -1109,7 +1134,7 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
     }
     if (ok && wait_warp(&b->fin, 0, gd) && !aborted(gd)) {
       tc_fence_after();
-      float* dst = r.seg + (((size_t)set * r.G + g) * r.H + h) * d * d;
+      float* dst = r.seg + (((size_t)set * r.G + sg.g0 + sg.seg) * r.H + h) * d * d;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {  // 16 rows x 32 columns
         const int hh = D == 128 ? k / 2 : 0, c0 = 64 * half + 32 * (k % 2);
@@ -1195,14 +1220,13 @@ cudaError_t launch(const TcArgs& t, cudaStream_t st) {
   cudaError_t e = opt_pass.ensure((const void*)retention_pass_kernel<D>, (int)pass_smem<D>());
   if (e == cudaSuccess) e = opt_sum.ensure((const void*)retention_sum_kernel<D>, (int)sum_smem<D>());
   if (e != cudaSuccess) return e;
-  const unsigned units = (unsigned)(t.r.G * t.r.H);
   if (t.r.seg != nullptr) {
-    retention_sum_kernel<D><<<units * t.r.nsum, SumTile<D>::kThreads, sum_smem<D>(), st>>>(t);
+    retention_sum_kernel<D><<<(unsigned)(t.r.inner * t.r.H * t.r.nsum), SumTile<D>::kThreads, sum_smem<D>(), st>>>(t);
     note_launch();
     e = retention_scan_launch(t.r, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_dependent(retention_pass_kernel<D>, dim3(units * t.r.npass), PassTile<D>::kThreads, pass_smem<D>(), st,
+  return launch_dependent(retention_pass_kernel<D>, dim3((unsigned)(t.r.G * t.r.H * t.r.npass)), PassTile<D>::kThreads, pass_smem<D>(), st,
                           t.r.seg != nullptr, t);
 }
 
