@@ -84,12 +84,59 @@ __device__ __forceinline__ int segments_of_kind(int nseg, SegmentKind kind) {
   return kind == SEG_ALL ? nseg : kind == SEG_INNER ? max(nseg - 1, 0) : nseg >= 2 ? 1 : 0;
 }
 
-// Number k of the call's segments of a kind (whole block; scratch: 68 ints of shared memory).  Packed sequences'
+constexpr int kOrdered = 64;  // packed sequences up to so many are taken longest first
+
+// Number k of the call's segments, of at most kOrdered packed sequences taken in the order of their lengths, the
+// longest first: blocks start in the order of their numbers, and a long sequence started last would run alone (24
+// sequences, one of 4001 tokens among 20,000, d = 128: 177 us as they come, 145 us in order).
+__device__ __forceinline__ Segment find_ordered(const RetArgs& a, int k, int* scratch) {
+  const int tid = threadIdx.x;
+  int lo, hi;
+  if (tid < a.B) {
+    packed_range(a, tid, &lo, &hi);
+    scratch[tid] = hi - lo;
+  }
+  __syncthreads();
+  if (tid < a.B) {
+    const int mine = hi - lo;
+    int at = 0;
+    for (int i = 0; i < a.B; ++i) at += scratch[i] > mine || (scratch[i] == mine && i < tid);
+    scratch[kOrdered + at] = tid;
+  }
+  __syncthreads();
+  Segment s;
+  s.seq = -1;
+  int g0 = 0;
+  for (int i = 0; i < a.B; ++i) {  // (every thread; the lengths are in shared memory)
+    const int q = scratch[kOrdered + i], m = (scratch[q] + a.L - 1) / a.L;
+    if (k < m) {
+      s.seq = q;
+      s.seg = k;
+      s.nseg = m;
+      break;
+    }
+    k -= m;
+  }
+  if (s.seq >= 0)
+    for (int i = 0; i < s.seq; ++i) g0 += (scratch[i] + a.L - 1) / a.L;
+  __syncthreads();
+  if (s.seq < 0) return s;
+  packed_range(a, s.seq, &lo, &hi);
+  s.g0 = g0;
+  s.all = hi - lo;
+  s.row0 = lo + s.seg * a.L;
+  s.len = min(a.L, s.all - s.seg * a.L);
+  if (s.g0 + s.nseg > a.G) s.seq = -1;  // (offsets out of order, as below)
+  return s;
+}
+
+// Number k of the call's segments of a kind (whole block; scratch: 2 kOrdered ints of shared memory).  Packed sequences'
 // segments are numbered sequence after sequence: thread t counts those of B / blockDim.x sequences, a block-wide scan
 // finds the thread whose range holds k.  An empty sequence has none.
 __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, SegmentKind kind, int* scratch) {
   Segment s;
   int lo = 0;
+  if (a.cu != nullptr && kind == SEG_ALL && a.B <= kOrdered) return find_ordered(a, k, scratch);
   if (a.cu == nullptr) {
     s.nseg = (a.N + a.L - 1) / a.L;
     const int per = segments_of_kind(s.nseg, kind);

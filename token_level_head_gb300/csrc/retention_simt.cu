@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   float* sX = sC + kTok * C::ES;
   float* sP = sX + D * C::ES;
   float* sW = sP + kTok * C::LP;
-  __shared__ int scratch[68];
+  __shared__ int scratch[2 * kOrdered];
   const int tid = threadIdx.x;
   launch_dependents();
   const int h = blockIdx.x % a.H, g = blockIdx.x / a.H;
@@ -261,7 +261,7 @@ cudaError_t launch_passes(const RetArgs& a, cudaStream_t st) {
 // many heads (most packed sequences have one segment, and their blocks end at once), single elements where few.
 template <int V, int E>
 __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_constant__ RetArgs a) {
-  __shared__ int scratch[68];
+  __shared__ int scratch[2 * kOrdered];
   launch_dependents();
   const int h = blockIdx.x % a.H, set = blockIdx.z;
   int ps = 0;

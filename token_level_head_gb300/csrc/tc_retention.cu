@@ -1015,7 +1015,7 @@ struct SumBars {
   uint32_t tbase;
   int abort;
   int issued;
-  int scratch[68];
+  int scratch[2 * kOrdered];
 };
 
 template <int D>
