@@ -10,6 +10,7 @@ missing or CUDA is unavailable the call fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -379,35 +380,84 @@ class _RetentionOptions(ctypes.Structure):
     _fields_ = [("feature", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+_RETENTION_FEATURES = {**FEATURES, "identity": 3}
+
+
+# The retention entries are called for single tokens, where the host's time counts: the small C structs
+# (plain values, never written) are kept for the values seen last, pointers go as integers.
+@functools.lru_cache(maxsize=256)
 def _retention_options(feature, scale):
-    kinds = {**FEATURES, "identity": 3}
-    if feature not in kinds:
-        raise ValueError(f"feature: one of {sorted(kinds)}, got {feature!r}")
-    return ctypes.byref(_RetentionOptions(kinds[feature], float(scale)))
+    if feature not in _RETENTION_FEATURES:
+        raise ValueError(f"feature: one of {sorted(_RETENTION_FEATURES)}, got {feature!r}")
+    return ctypes.byref(_RetentionOptions(_RETENTION_FEATURES[feature], scale))
+
+
+@functools.lru_cache(maxsize=1024)
+def _c_strides(b, h, n):
+    return ctypes.byref(_Strides(b, h, n))
 
 
 def _strided(t, name):
     """(pointer, strides) of a token tensor [B, H, N, d] or [B, H, d] with contiguous rows."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {t.stride(-1)}")
-    st = _Strides(t.stride(0), t.stride(1), t.stride(2) if t.dim() == 4 else 0)
-    return [_ptr(t), ctypes.byref(st)]
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {st[-1]}")
+    return t.data_ptr(), _c_strides(st[0], st[1], st[2] if len(st) == 4 else 0)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _expect_like(q, *named):
+    """Every (name, tensor) of q's shape and dtype."""
+    shape, dtype = q.shape, q.dtype
+    for name, t in named:
+        if t.shape != shape or t.dtype != dtype:
+            _expect(t, name, shape, dtype)
 
 
 def _retention_device(tokens, others):
     """The one CUDA device of all tensors; ``others`` (not the token tensors) must be contiguous."""
-    q = tokens[0]
+    dev = tokens[0].device
     for t in tokens:
         if not t.is_cuda:
             raise ValueError("tensors must be CUDA tensors")
-        if t.device != q.device:
-            raise ValueError(f"tensor on {t.device}, expected {q.device} (the device of q)")
-    others = [t for t in others if t is not None]
-    _need_cuda(*others)
+        if t.device != dev:
+            raise ValueError(f"tensor on {t.device}, expected {dev} (the device of q)")
     for t in others:
-        if t.device != q.device:
-            raise ValueError(f"tensor on {t.device}, expected {q.device} (the device of q)")
-    return q.device
+        if t is not None:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("tensors must be contiguous CUDA tensors")
+            if t.device != dev:
+                raise ValueError(f"tensor on {t.device}, expected {dev} (the device of q)")
+    return dev
+
+
+# the current stream's handle without a Stream object around it, where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _retention_call(name, dev, args, stream):
+    """Calls entry ``name`` with ``dev`` current and the stream last."""
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:
+        handle = _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != MHLA_OK:
+        raise MhlaError(name, st)
+
+
+def _expect_fast(t, name, shape, dtype):
+    """_expect, quicker where it holds."""
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        _expect(t, name, shape, dtype)
 
 
 def _retention_sizes(q, cu_seqlens):
@@ -420,7 +470,7 @@ def _retention_sizes(q, cu_seqlens):
             raise ValueError(f"q: expected [1, H, tokens, d] with cu_seqlens, got shape {tuple(q.shape)}")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError(f"cu_seqlens: expected [sequences + 1], got shape {tuple(cu_seqlens.shape)}")
-        _expect(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
+        _expect_fast(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
         B = cu_seqlens.numel() - 1
     return B, H, N, d
 
@@ -430,11 +480,12 @@ def _retention_states(states, slots, B, H, d):
         if slots is not None:
             raise ValueError("slots: given without states")
         return 0
-    if states.dim() != 4:
-        raise ValueError(f"states: expected [slots, H, d, d], got shape {tuple(states.shape)}")
-    _expect(states, "states", (states.shape[0], H, d, d), torch.float32)
-    _expect(slots, "slots", (B,), torch.int32)
-    return states.shape[0]
+    shape = states.shape
+    if len(shape) != 4:
+        raise ValueError(f"states: expected [slots, H, d, d], got shape {tuple(shape)}")
+    _expect_fast(states, "states", (shape[0], H, d, d), torch.float32)
+    _expect_fast(slots, "slots", (B,), torch.int32)
+    return shape[0]
 
 
 def retention_workspace_bytes(B: int, H: int, tokens: int, d: int, backward: bool = False) -> int:
@@ -442,9 +493,10 @@ def retention_workspace_bytes(B: int, H: int, tokens: int, d: int, backward: boo
 
 
 def _retention_workspace(workspace, B, H, N, d, packed, backward, dev):
+    """The caller's workspace or, where there is none, a new one (a tensor: it has to outlive the call)."""
     if workspace is None:
         workspace = new_workspace(retention_workspace_bytes(B, H, N if packed else B * N, d, backward), dev)
-    return [_ptr(workspace), workspace.numel() * workspace.element_size()]
+    return workspace
 
 
 def retention_forward(q, k, v, gamma, y, *, cu_seqlens=None, states=None, slots=None, load_state=False, scale=1.0,
@@ -455,21 +507,18 @@ def retention_forward(q, k, v, gamma, y, *, cu_seqlens=None, states=None, slots=
     [sequences + 1].  ``states`` [slots, H, d, d] fp32 receives the final states (``slots``: the slot
     of each sequence, int32); with ``load_state`` the sequences start from them."""
     B, H, N, d = _retention_sizes(q, cu_seqlens)
-    for name, t in (("k", k), ("v", v), ("y", y)):
-        _expect(t, name, q.shape, q.dtype)
-    _expect(gamma, "gamma", (H,), torch.float32)
+    _expect_like(q, ("k", k), ("v", v), ("y", y))
+    _expect_fast(gamma, "gamma", (H,), torch.float32)
     if load_state and states is None:
         raise ValueError("load_state: needs states")
     n_slots = _retention_states(states, slots, B, H, d)
-    opt = _retention_options(feature, scale)
-    dev = _retention_device([q, k, v, y], [gamma, cu_seqlens, states, slots, workspace])
-    with torch.cuda.device(dev):
-        st = load().retention_forward(*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), _ptr(gamma),
-                                      *_strided(y, "y"), B, H, N, d, _ptr(cu_seqlens), _ptr(states), _ptr(slots),
-                                      n_slots, int(bool(load_state)), _dtype(q), opt,
-                                      *_retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, False, dev),
-                                      _stream(stream, dev))
-    _check("retention_forward", st)
+    opt = _retention_options(feature, float(scale))
+    dev = _retention_device((q, k, v, y), (gamma, cu_seqlens, states, slots, workspace))
+    ws = _retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, False, dev)
+    _retention_call("retention_forward", dev,
+                    (*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), gamma.data_ptr(), *_strided(y, "y"),
+                     B, H, N, d, _address(cu_seqlens), _address(states), _address(slots), n_slots,
+                     1 if load_state else 0, _dtype(q), opt, ws.data_ptr(), ws.nbytes), stream)
     return y
 
 
@@ -478,18 +527,15 @@ def retention_backward(q, k, v, gamma, dy, dq, dk, dv, *, cu_seqlens=None, scale
     """Gradients of retention_forward (without states) from dy = dL/dY; dq, dk and dv are written.
     Shapes as there; every tensor may have its own strides."""
     B, H, N, d = _retention_sizes(q, cu_seqlens)
-    for name, t in (("k", k), ("v", v), ("dy", dy), ("dq", dq), ("dk", dk), ("dv", dv)):
-        _expect(t, name, q.shape, q.dtype)
-    _expect(gamma, "gamma", (H,), torch.float32)
-    opt = _retention_options(feature, scale)
-    dev = _retention_device([q, k, v, dy, dq, dk, dv], [gamma, cu_seqlens, workspace])
-    with torch.cuda.device(dev):
-        st = load().retention_backward(*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), _ptr(gamma),
-                                       *_strided(dy, "dy"), *_strided(dq, "dq"), *_strided(dk, "dk"),
-                                       *_strided(dv, "dv"), B, H, N, d, _ptr(cu_seqlens), _dtype(q), opt,
-                                       *_retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, True, dev),
-                                       _stream(stream, dev))
-    _check("retention_backward", st)
+    _expect_like(q, ("k", k), ("v", v), ("dy", dy), ("dq", dq), ("dk", dk), ("dv", dv))
+    _expect_fast(gamma, "gamma", (H,), torch.float32)
+    opt = _retention_options(feature, float(scale))
+    dev = _retention_device((q, k, v, dy, dq, dk, dv), (gamma, cu_seqlens, workspace))
+    ws = _retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, True, dev)
+    _retention_call("retention_backward", dev,
+                    (*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), gamma.data_ptr(), *_strided(dy, "dy"),
+                     *_strided(dq, "dq"), *_strided(dk, "dk"), *_strided(dv, "dv"), B, H, N, d, _address(cu_seqlens),
+                     _dtype(q), opt, ws.data_ptr(), ws.nbytes), stream)
     return dq, dk, dv
 
 
@@ -500,19 +546,16 @@ def retention_step(q, k, v, gamma, states, out, *, slots=None, scale=1.0, featur
     if q.dim() != 3:
         raise ValueError(f"q: expected [B, H, d], got shape {tuple(q.shape)}")
     B, H, d = q.shape
-    for name, t in (("k", k), ("v", v), ("out", out)):
-        _expect(t, name, q.shape, q.dtype)
-    _expect(gamma, "gamma", (H,), torch.float32)
+    _expect_like(q, ("k", k), ("v", v), ("out", out))
+    _expect_fast(gamma, "gamma", (H,), torch.float32)
     if states is None:
         raise ValueError("states: required")
     n_slots = _retention_states(states, slots, B, H, d)
-    opt = _retention_options(feature, scale)
-    dev = _retention_device([q, k, v, out], [gamma, states, slots])
-    with torch.cuda.device(dev):
-        st = load().retention_step(*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), _ptr(gamma), _ptr(states),
-                                   _ptr(slots), n_slots, *_strided(out, "out"), B, H, d, _dtype(q), opt,
-                                   _stream(stream, dev))
-    _check("retention_step", st)
+    opt = _retention_options(feature, float(scale))
+    dev = _retention_device((q, k, v, out), (gamma, states, slots))
+    _retention_call("retention_step", dev,
+                    (*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), gamma.data_ptr(), states.data_ptr(),
+                     _address(slots), n_slots, *_strided(out, "out"), B, H, d, _dtype(q), opt), stream)
     return out
 
 
@@ -521,16 +564,15 @@ def retention_copy_states(states, src, dst, *, stream=None):
     fp32, src and dst int32 [n], n <= 1024."""
     if states.dim() != 4 or states.shape[2] != states.shape[3]:
         raise ValueError(f"states: expected [slots, H, d, d], got shape {tuple(states.shape)}")
-    _expect(states, "states", states.shape, torch.float32)
+    _expect_fast(states, "states", states.shape, torch.float32)
     if src.dim() != 1:
         raise ValueError(f"src: expected [n], got shape {tuple(src.shape)}")
     for name, t in (("src", src), ("dst", dst)):
-        _expect(t, name, src.shape, torch.int32)
-    dev = _same_device(states, src, dst)
-    with torch.cuda.device(dev):
-        st = load().retention_copy_states(_ptr(states), states.shape[0], states.shape[1], states.shape[2], _ptr(src),
-                                          _ptr(dst), src.numel(), _stream(stream, dev))
-    _check("retention_copy_states", st)
+        _expect_fast(t, name, src.shape, torch.int32)
+    dev = _retention_device((states,), (states, src, dst))
+    _retention_call("retention_copy_states", dev,
+                    (states.data_ptr(), states.shape[0], states.shape[1], states.shape[2], src.data_ptr(),
+                     dst.data_ptr(), src.shape[0]), stream)
     return states
 
 
