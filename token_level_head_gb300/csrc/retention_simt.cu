@@ -317,49 +317,56 @@ __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_c
 }
 
 // ================================================================ single-token step
-// S = gamma S + phi(k) v^T, out = scale phi(q) S.  A block takes ES columns of a (row, head) state: a
-// thread holds RPT float4 of it, all loads issued before the first use; the columns' sums over c go
-// through shuffles and shared memory.
+// S = gamma S + phi(k) v^T, out = scale phi(q) S.  A block takes ES columns of a (row, head) state; a thread RPT
+// neighbouring rows of four columns, all its loads issued before the first use; the columns' sums over c go through
+// shuffles and shared memory.  Bound by the state's traffic (8 d^2 bytes a head).
+template <typename T, int N>
+__device__ __forceinline__ void load_values(const T* p, float* f) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) load_row_piece<T>(p + i, f + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_f(p[i]);
+  }
+}
+
 template <typename T, int D, int ES>
-__global__ void __launch_bounds__(kThreads) retention_step_kernel(int H, RetTensor q, RetTensor k, RetTensor v,
-                                                                  RetTensor out, const float* gamma, float scale,
-                                                                  float* states, const int* slots, int n_slots) {
+__global__ void __launch_bounds__(kThreads, 6) retention_step_kernel(int H, RetTensor q, RetTensor k, RetTensor v,
+                                                                     RetTensor out, const float* gamma, float scale,
+                                                                     float* states, const int* slots, int n_slots) {
   constexpr int NG = ES / 4, RT = kThreads / NG, RPT = D >= RT ? D / RT : 1;
   __shared__ float4 red[kThreads / 32][NG];
-  const int tid = threadIdx.x, cg = tid % NG, r0 = tid / NG;
+  const int tid = threadIdx.x, cg = tid % NG, r0 = (tid / NG) * RPT;
   const int h = blockIdx.x % H, b = blockIdx.x / H, e0 = blockIdx.y * ES + 4 * cg;
   const int s0 = slots == nullptr ? b : slots[b];
   const bool in = s0 >= 0 && s0 < n_slots;
-  float4* S = reinterpret_cast<float4*>(states + ((size_t)(in ? s0 : 0) * H + h) * (D * D) + e0);
-  const bool act = r0 * RPT < D;
+  const bool act = r0 < D;
+  float4* S = reinterpret_cast<float4*>(states + ((size_t)(in ? s0 : 0) * H + h) * (D * D) + (act ? r0 : 0) * D + e0);
   float4 x[RPT];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i)
-    x[i] = in && act ? __ldcs(S + (size_t)(r0 + i * RT) * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-  float fv[4];
+  for (int i = 0; i < RPT; ++i) x[i] = in && act ? __ldcs(S + i * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float fv[4], fq[RPT], fk[RPT];
   load_row_piece<T>(static_cast<const T*>(v.p) + b * v.sb + h * v.sh + e0, fv);
-  const T* qp = static_cast<const T*>(q.p) + b * q.sb + h * q.sh;
-  const T* kp = static_cast<const T*>(k.p) + b * k.sb + h * k.sh;
-  float fq[RPT], fk[RPT];
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    fq[i] = act ? ret_phi(to_f(qp[r0 + i * RT]), q.feature) : 0.f;
-    fk[i] = act ? ret_phi(to_f(kp[r0 + i * RT]), k.feature) : 0.f;
-  }
+  load_values<T, RPT>(static_cast<const T*>(q.p) + b * q.sb + h * q.sh + (act ? r0 : 0), fq);
+  load_values<T, RPT>(static_cast<const T*>(k.p) + b * k.sb + h * k.sh + (act ? r0 : 0), fk);
   const float gm = gamma[h];
   if (ret_slot(slots, n_slots, b) < 0) return;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
-    x[i].x = fmaf(gm, x[i].x, fk[i] * fv[0]);
-    x[i].y = fmaf(gm, x[i].y, fk[i] * fv[1]);
-    x[i].z = fmaf(gm, x[i].z, fk[i] * fv[2]);
-    x[i].w = fmaf(gm, x[i].w, fk[i] * fv[3]);
-    if (act) __stcs(S + (size_t)(r0 + i * RT) * (D / 4), x[i]);
-    y.x = fmaf(fq[i], x[i].x, y.x);
-    y.y = fmaf(fq[i], x[i].y, y.y);
-    y.z = fmaf(fq[i], x[i].z, y.z);
-    y.w = fmaf(fq[i], x[i].w, y.w);
+    const float kk = ret_phi(fk[i], k.feature), qq = act ? ret_phi(fq[i], q.feature) : 0.f;
+    x[i].x = fmaf(gm, x[i].x, kk * fv[0]);
+    x[i].y = fmaf(gm, x[i].y, kk * fv[1]);
+    x[i].z = fmaf(gm, x[i].z, kk * fv[2]);
+    x[i].w = fmaf(gm, x[i].w, kk * fv[3]);
+    if (act) __stcs(S + i * (D / 4), x[i]);
+    if (act) {
+      y.x = fmaf(qq, x[i].x, y.x);
+      y.y = fmaf(qq, x[i].y, y.y);
+      y.z = fmaf(qq, x[i].z, y.z);
+      y.w = fmaf(qq, x[i].w, y.w);
+    }
   }
 #pragma unroll
   for (int o = NG; o < 32; o <<= 1) {
@@ -370,21 +377,12 @@ __global__ void __launch_bounds__(kThreads) retention_step_kernel(int H, RetTens
   }
   if ((tid & 31) < NG) red[tid >> 5][cg] = y;
   __syncthreads();
-  if (tid < NG) {
-    float4 s = red[0][tid];
+  if (tid < ES) {  // a column a thread
+    const float* f = reinterpret_cast<const float*>(red) + tid;
+    float s = 0.f;
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) {
-      const float4 u = red[w][tid];
-      s.x += u.x;
-      s.y += u.y;
-      s.z += u.z;
-      s.w += u.w;
-    }
-    T* dst = static_cast<T*>(const_cast<void*>(out.p)) + b * out.sb + h * out.sh + e0;
-    dst[0] = from_f<T>(scale * s.x);
-    dst[1] = from_f<T>(scale * s.y);
-    dst[2] = from_f<T>(scale * s.z);
-    dst[3] = from_f<T>(scale * s.w);
+    for (int w = 0; w < kThreads / 32; ++w) s += f[w * ES];
+    static_cast<T*>(const_cast<void*>(out.p))[b * out.sb + h * out.sh + blockIdx.y * ES + tid] = from_f<T>(scale * s);
   }
 }
 
@@ -411,39 +409,59 @@ cudaError_t launch_step_d(int B, int H, int d, const RetTensor& q, const RetTens
 }
 
 // ================================================================ state copies
-// A block takes R floats of every slot: it reads them from all sources into shared memory, then writes
-// all targets, so that a slot may be source and target of different pairs in any order.
+// A block takes R floats of every slot: it reads them from all sources into shared memory, then writes all targets,
+// so that a slot may be source and target of different pairs in any order.  A source of several pairs is read once.
+// Bound by the traffic; asynchronous copies keep a block's whole part in flight.
+constexpr int kCopyBytes = 100 * 1024;  // of shared memory a block, so that two are on an SM: one reads, one writes
+
+__device__ __forceinline__ void copy_async16(void* smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
+               : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads) retention_copy_kernel(float* states, long long slot_elems, int n_slots,
-                                                                  const int* src, const int* dst, int n, int R) {
-  extern __shared__ float4 smem4[];
-  float4* buf = smem4;
-  int* sdst = reinterpret_cast<int*>(smem4 + (size_t)n * (R / 4));
-  int* ssrc = sdst + n;
-  const long long e0 = (long long)blockIdx.x * R;
-  const int w4 = (int)min((long long)R, slot_elems - e0) / 4;
+                                                                  const int* src, const int* dst, int n, int log_r4) {
+  extern __shared__ float4 buf[];
+  const int r4 = 1 << log_r4;  // float4 of a part
+  int* sdst = reinterpret_cast<int*>(buf + ((size_t)n << log_r4));
+  int* ssrc = sdst + n;   // source; -1: zeros; n_slots: the pair does nothing
+  int* lead = ssrc + n;   // the first pair of the same source, whose part of buf both use
+  const long long e0 = (long long)blockIdx.x << (log_r4 + 2);
+  const int w4 = (int)min((long long)r4, (slot_elems - e0) / 4);
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    sdst[i] = dst[i];
-    ssrc[i] = src[i];
+    const int s = src[i], d = dst[i];
+    sdst[i] = d;
+    ssrc[i] = d < 0 || d >= n_slots || s >= n_slots ? n_slots : max(s, -1);
   }
   __syncthreads();
-  // a pair out of range does nothing; of several with one target the last counts
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int d = sdst[i];
-    bool drop = d < 0 || d >= n_slots || ssrc[i] >= n_slots;
-    for (int j = i + 1; j < n && !drop; ++j) drop = sdst[j] == d && ssrc[j] < n_slots;
-    if (drop) ssrc[i] = n_slots;  // seen by the others as a pair that does nothing: its later twin still counts
+    const int d = sdst[i], s = ssrc[i];
+    int l = i, m = s == n_slots ? -1 : i;
+    for (int j = 0; j < i; ++j)
+      if (ssrc[j] == s) {
+        l = j;
+        break;
+      }
+    for (int j = i + 1; j < n && m >= 0; ++j)
+      if (sdst[j] == d && ssrc[j] != n_slots) m = -1;  // of several pairs with one target the last counts
+    lead[i] = m < 0 ? -1 - l : l;                      // negative: nothing to write (but others may use its part)
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n * (R / 4); i += kThreads) {
-    const int pr = i / (R / 4), c = i % (R / 4), s = ssrc[pr];
-    if (s < n_slots && c < w4)
-      buf[i] = s < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                     : __ldcg(reinterpret_cast<const float4*>(states + s * slot_elems + e0) + c);
+  for (int i = threadIdx.x; i < n << log_r4; i += kThreads) {
+    const int pr = i >> log_r4, c = i & (r4 - 1), s = ssrc[pr], l = lead[pr];
+    if ((l == pr || l == -1 - pr) && s < n_slots && c < w4) {
+      if (s < 0)
+        buf[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+        copy_async16(buf + i, states + s * slot_elems + e0 + 4 * c);
+    }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  for (int i = threadIdx.x; i < n * (R / 4); i += kThreads) {
-    const int pr = i / (R / 4), c = i % (R / 4);
-    if (ssrc[pr] < n_slots && c < w4) reinterpret_cast<float4*>(states + sdst[pr] * slot_elems + e0)[c] = buf[i];
+  for (int i = threadIdx.x; i < n << log_r4; i += kThreads) {
+    const int pr = i >> log_r4, c = i & (r4 - 1), l = lead[pr];
+    if (l >= 0 && c < w4)
+      __stcs(reinterpret_cast<float4*>(states + sdst[pr] * slot_elems + e0) + c, buf[((size_t)l << log_r4) + c]);
   }
 }
 
@@ -475,13 +493,17 @@ cudaError_t retention_step_launch(int B, int H, int d, mhla_dtype dt, const RetT
 
 cudaError_t retention_copy_launch(float* states, long long slot_elems, int n_slots, const int* src, const int* dst,
                                   int n, cudaStream_t st) {
-  const int R = n <= 256 ? 64 : 32;  // at most 1024 pairs: 136 KB
-  const size_t bytes = (size_t)n * (R * sizeof(float) + 2 * sizeof(int));
+  // parts of 128 bytes to 4 KB: as much shared memory as two blocks an SM allow, but a few parts for every SM
+  int log_r4 = 3;
+  while (log_r4 < 8 && ((size_t)n << (log_r4 + 1)) * 16 <= (size_t)kCopyBytes && (slot_elems >> (log_r4 + 3)) >= 608)
+    ++log_r4;
+  const size_t bytes = ((size_t)n << log_r4) * 16 + (size_t)n * 3 * sizeof(int);
   static SmemOptIn opt;
   cudaError_t e = opt.ensure((const void*)retention_copy_kernel, 227 * 1024);
   if (e != cudaSuccess) return e;
-  retention_copy_kernel<<<(unsigned)((slot_elems + R - 1) / R), kThreads, bytes, st>>>(states, slot_elems, n_slots, src,
-                                                                                       dst, n, R);
+  const long long r = 4ll << log_r4;
+  retention_copy_kernel<<<(unsigned)((slot_elems + r - 1) / r), kThreads, bytes, st>>>(states, slot_elems, n_slots, src,
+                                                                                       dst, n, log_r4);
   note_launch();
   return cudaGetLastError();
 }
