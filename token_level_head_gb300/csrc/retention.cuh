@@ -19,6 +19,23 @@ __device__ __forceinline__ float ret_dphi(float x, int feature) {
   return feature == 0 && x > 0.f ? 1.f : expf(x);
 }
 
+// Two products / multiply-adds in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return r;
+}
+
 // log2(gamma).  gamma - 1 is exact for gamma in [1/2, 2], so decays close to 1 keep their digits;
 // gamma = 0 gives -inf.
 __device__ __forceinline__ float decay_log2(float gamma) { return log1pf(gamma - 1.f) * 1.4426950408889634f; }

@@ -1,6 +1,7 @@
 // Retention passes of fp32 tensors on the SIMT cores, the scan over segments, the single-token step
 // and the copies between state slots.  The mathematics is in retention.h.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "retention.cuh"
@@ -14,8 +15,10 @@ constexpr int kTok = 64;  // tokens of a chunk
 // ================================================================ passes
 // A block takes one segment of one head and ES columns of c: per chunk of 64 tokens
 //   P = (A B^T) gamma^(t-s), masked;  out = P C + gamma^(i+1) A X;  X = gamma^len X + (B w)^T C,
-// w_s = gamma^(len-1-s), with X [D][ES] and the chunk's A, B, C and P in shared memory and 4 x 4 (X: up
-// to 8 x 4) register tiles.  With SUM only X is formed: the segment's own sum.
+// w_s = gamma^(len-1-s), with X [D][ES] and the chunk's A, B, C and P in shared memory and 4 x 4 (X: up to 8 x 4)
+// register tiles; the masked half of the first two products is left out by blocks of 4 rows.  With SUM only X is
+// formed: the segment's own sum.  Bound by fp32 FMA issue and the latency of shared memory: the multiply-adds go in
+// pairs, the next chunk's rows are on their way in registers while this one is computed.
 template <int D>
 struct SimtTile {
   static constexpr int ES = D < 64 ? D : 64;
@@ -26,6 +29,7 @@ struct SimtTile {
   static constexpr int RS = D >= NY ? D / NY : 1;
   static constexpr int kFloats = 2 * kTok * LD + kTok * ES + D * ES + kTok * LP + kTok;
   static constexpr size_t kBytes = kFloats * sizeof(float);
+  static constexpr int kPerSm = D == 128 ? 1 : 2;
 };
 
 template <typename T>
@@ -44,25 +48,55 @@ __device__ __forceinline__ void load_row_piece<__nv_bfloat16>(const __nv_bfloat1
   f[3] = __uint_as_float(u.y & 0xffff0000u);
 }
 
-// Rows 0 .. len - 1, columns c0 .. c0 + W - 1 of a tensor from row `row`, widened, phi applied; zeros behind.
+// A chunk's rows of one operand, W columns from c0, on their way to shared memory: fetched into registers (zeros
+// behind the sequence), later stored with phi applied.
 template <int W, int LDS>
-__device__ __forceinline__ void load_tile(float* dst, const RetTensor& t, long long base, int row, int len, int c0) {
-  const float* src = static_cast<const float*>(t.p) + base + (long long)row * t.sn + c0;
-  for (int i = threadIdx.x; i < kTok * (W / 4); i += kThreads) {
-    const int r = i / (W / 4), c = (i % (W / 4)) * 4;
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < len) {
-      load_row_piece<float>(src + (long long)r * t.sn + c, f);
-      if (t.feature != kFeatIdentity)
+struct Fetch {
+  static constexpr int kN = kTok * (W / 4) / kThreads;
+  float4 v[kN];
+  __device__ __forceinline__ void load(const RetTensor& t, long long base, int row, int len, int c0) {
+    const float* src = static_cast<const float*>(t.p) + base + (long long)row * t.sn + c0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) f[x] = ret_phi(f[x], t.feature);
+    for (int i = 0; i < kN; ++i) {
+      const int at = threadIdx.x + i * kThreads, r = at / (W / 4), c = (at % (W / 4)) * 4;
+      v[i] = r < len ? *reinterpret_cast<const float4*>(src + (long long)r * t.sn + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    *reinterpret_cast<float4*>(dst + r * LDS + c) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+  __device__ __forceinline__ void store(float* dst, int feature, int len) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = threadIdx.x + i * kThreads, r = at / (W / 4), c = (at % (W / 4)) * 4;
+      if (feature != kFeatIdentity && r < len)
+        v[i] = make_float4(ret_phi(v[i].x, feature), ret_phi(v[i].y, feature), ret_phi(v[i].z, feature),
+                           ret_phi(v[i].w, feature));
+      *reinterpret_cast<float4*>(dst + r * LDS + c) = v[i];
+    }
+  }
+};
+
+// acc[i][0 .. 3] += sum over k of a[i][k] b[k][0 .. 3], k = 0 .. n - 1 (n a multiple of 4): rows of a LDA apart, of b LDB.
+template <int R, int LDA, int LDB>
+__device__ __forceinline__ void outer_rows(float2 (&acc)[R][2], const float* a, const float* b, int k0, int n) {
+#pragma unroll 2
+  for (int k = k0; k < n; k += 4) {
+    float4 fa[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) fa[i] = *reinterpret_cast<const float4*>(a + i * LDA + k);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float4 v = *reinterpret_cast<const float4*>(b + (k + u) * LDB);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float w = u == 0 ? fa[i].x : u == 1 ? fa[i].y : u == 2 ? fa[i].z : fa[i].w;
+        acc[i][0] = fma2(make_float2(w, w), make_float2(v.x, v.y), acc[i][0]);
+        acc[i][1] = fma2(make_float2(w, w), make_float2(v.z, v.w), acc[i][1]);
+      }
+    }
   }
 }
 
 template <int D, bool SUM>
-__global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_constant__ RetArgs a) {
+__global__ void __launch_bounds__(kThreads, SimtTile<D>::kPerSm) retention_simt_kernel(const __grid_constant__ RetArgs a) {
   using C = SimtTile<D>;
   extern __shared__ float4 smem4[];
   float* sA = reinterpret_cast<float*>(smem4);
@@ -82,107 +116,106 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
   const RetPass& p = a.pass[z];
   Segment sg = find_segment(a, g, SUM ? SEG_INNER : SEG_ALL, scratch);
   if (sg.seq < 0) return;
-  if (SUM) inner_segment(a, sg, p.reverse);
+  const int reverse = p.reverse;
+  if (SUM) inner_segment(a, sg, reverse);
   const int e0 = blockIdx.y * C::ES;
+  const long long ba = ret_base(a, p.a, sg.seq, h), bb = ret_base(a, p.b, sg.seq, h), bc = ret_base(a, p.c, sg.seq, h);
+  const int nch = (sg.len + kTok - 1) / kTok;
+  Fetch<D, C::LD> fA, fB;
+  Fetch<C::ES, C::ES> fC;
+  auto fetch = [&](int it) {
+    const int ch = reverse ? nch - 1 - it : it;
+    const int row = sg.row0 + ch * kTok, len = min(kTok, sg.len - ch * kTok);
+    if (!SUM) fA.load(p.a, ba, row, len, 0);
+    fB.load(p.b, bb, row, len, 0);
+    fC.load(p.c, bc, row, len, e0);
+  };
+  fetch(0);
   const float lg = decay_log2(a.gamma[h]);
   const int tx = tid % C::NX, ty = tid / C::NX;
   float* seg = a.seg == nullptr ? nullptr : a.seg + (((size_t)p.sum * a.G + sg.g0 + sg.seg) * a.H + h) * (D * D);
-  if (SUM)
-    for (int i = tid; i < D * C::ES; i += kThreads) sX[i] = 0.f;
   int slot = -1;
-  if (!SUM) {
-    if (a.states != nullptr) slot = ret_slot(a.slots, a.n_slots, sg.seq);
-    const float* src = entering_state(a, p, sg, h, slot);
-    const bool tr = sg.nseg > 1 && p.sum_t;
-    grid_dependency_wait();
+  if (!SUM && a.states != nullptr) slot = ret_slot(a.slots, a.n_slots, sg.seq);
+  {
+    const float* src = SUM ? nullptr : entering_state(a, p, sg, h, slot);
+    const bool tr = !SUM && sg.nseg > 1 && p.sum_t;
+    if (!SUM) grid_dependency_wait();
+#pragma unroll 8
     for (int i = tid; i < D * C::ES; i += kThreads) {
       const int r = i / C::ES, e = e0 + i % C::ES;
       sX[i] = src == nullptr ? 0.f : __ldcg(src + (tr ? e * D + r : r * D + e));
     }
   }
-  const long long ba = ret_base(a, p.a, sg.seq, h), bb = ret_base(a, p.b, sg.seq, h), bc = ret_base(a, p.c, sg.seq, h);
-  const int nch = (sg.len + kTok - 1) / kTok;
   for (int it = 0; it < nch; ++it) {
-    const int ch = p.reverse ? nch - 1 - it : it;
+    const int ch = reverse ? nch - 1 - it : it;
     const int row = sg.row0 + ch * kTok, len = min(kTok, sg.len - ch * kTok);
     __syncthreads();
-    if (!SUM) load_tile<D, C::LD>(sA, p.a, ba, row, len, 0);
-    load_tile<D, C::LD>(sB, p.b, bb, row, len, 0);
-    load_tile<C::ES, C::ES>(sC, p.c, bc, row, len, e0);
-    if (tid < kTok) sW[tid] = tid < len ? decay_pow(lg, p.reverse ? tid : len - 1 - tid) : 0.f;
+    if (!SUM) fA.store(sA, p.a.feature, len);
+    fB.store(sB, p.b.feature, len);
+    fC.store(sC, p.c.feature, len);
+    if (tid < kTok) sW[tid] = tid < len ? decay_pow(lg, reverse ? tid : len - 1 - tid) : 0.f;
     __syncthreads();
+    if (it + 1 < nch) fetch(it + 1);
     if (!SUM) {
-      // P: 4 rows t, 4 columns s = tp + 16 j
-      const int tp = tid & 15, tr = tid >> 4;
-      float acc[4][4] = {};
-      for (int c = 0; c < D; c += 4) {
-        float4 fa[4], fb[4];
+      // P: 4 rows t, 4 columns s = tp + 16 j; blocks wholly masked stay zero
+      const int tp = tid & 15, t0 = 4 * (tid >> 4);
+      float2 acc[4][4] = {};
+      auto scores = [&](auto lo, auto hi) {  // columns j = lo .. hi - 1
+#pragma unroll 2
+        for (int c = 0; c < D; c += 4) {
+          float4 fa[4], fb[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const float4*>(sA + (4 * tr + i) * C::LD + c);
+          for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const float4*>(sA + (t0 + i) * C::LD + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fb[j] = *reinterpret_cast<const float4*>(sB + (tp + 16 * j) * C::LD + c);
+          for (int j = lo(); j < hi(); ++j) fb[j] = *reinterpret_cast<const float4*>(sB + (tp + 16 * j) * C::LD + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int j = lo(); j < hi(); ++j)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[i][j] = fmaf(fa[i].x, fb[j].x, acc[i][j]);
-            acc[i][j] = fmaf(fa[i].y, fb[j].y, acc[i][j]);
-            acc[i][j] = fmaf(fa[i].z, fb[j].z, acc[i][j]);
-            acc[i][j] = fmaf(fa[i].w, fb[j].w, acc[i][j]);
-          }
+            for (int i = 0; i < 4; ++i) {
+              acc[i][j] = fma2(make_float2(fa[i].x, fa[i].y), make_float2(fb[j].x, fb[j].y), acc[i][j]);
+              acc[i][j] = fma2(make_float2(fa[i].z, fa[i].w), make_float2(fb[j].z, fb[j].w), acc[i][j]);
+            }
+        }
+      };
+      // a warp holds 8 rows, so these branches are its own: half of the columns, or all
+      using I0 = std::integral_constant<int, 0>;
+      using I2 = std::integral_constant<int, 2>;
+      using I4 = std::integral_constant<int, 4>;
+      if (t0 < kTok / 2) {
+        if (reverse)
+          scores(I0(), I4());
+        else
+          scores(I0(), I2());
+      } else {
+        if (reverse)
+          scores(I2(), I4());
+        else
+          scores(I0(), I4());
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int t = 4 * tr + i, s = tp + 16 * j, n = p.reverse ? s - t : t - s;
-          sP[t * C::LP + s] = n >= 0 && s < len ? acc[i][j] * decay_pow(lg, n) : 0.f;
+          const int t = t0 + i, s = tp + 16 * j, n = reverse ? s - t : t - s;
+          sP[t * C::LP + s] = n >= 0 && s < len ? (acc[i][j].x + acc[i][j].y) * decay_pow(lg, n) : 0.f;
         }
       __syncthreads();
       // out = P C + gamma^(i+1) A X
-      float in[C::RO][4] = {}, ac[C::RO][4] = {};
-      for (int s = 0; s < kTok; s += 4) {
-        float4 fp[C::RO];
-#pragma unroll
-        for (int i = 0; i < C::RO; ++i) fp[i] = *reinterpret_cast<const float4*>(sP + (C::RO * ty + i) * C::LP + s);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 v = *reinterpret_cast<const float4*>(sC + (s + u) * C::ES + 4 * tx);
-#pragma unroll
-          for (int i = 0; i < C::RO; ++i) {
-            const float w = u == 0 ? fp[i].x : u == 1 ? fp[i].y : u == 2 ? fp[i].z : fp[i].w;
-            in[i][0] = fmaf(w, v.x, in[i][0]);
-            in[i][1] = fmaf(w, v.y, in[i][1]);
-            in[i][2] = fmaf(w, v.z, in[i][2]);
-            in[i][3] = fmaf(w, v.w, in[i][3]);
-          }
-        }
-      }
-      for (int c = 0; c < D; c += 4) {
-        float4 fa[C::RO];
-#pragma unroll
-        for (int i = 0; i < C::RO; ++i) fa[i] = *reinterpret_cast<const float4*>(sA + (C::RO * ty + i) * C::LD + c);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 v = *reinterpret_cast<const float4*>(sX + (c + u) * C::ES + 4 * tx);
-#pragma unroll
-          for (int i = 0; i < C::RO; ++i) {
-            const float w = u == 0 ? fa[i].x : u == 1 ? fa[i].y : u == 2 ? fa[i].z : fa[i].w;
-            ac[i][0] = fmaf(w, v.x, ac[i][0]);
-            ac[i][1] = fmaf(w, v.y, ac[i][1]);
-            ac[i][2] = fmaf(w, v.z, ac[i][2]);
-            ac[i][3] = fmaf(w, v.w, ac[i][3]);
-          }
-        }
-      }
+      float2 in[C::RO][2] = {}, ac[C::RO][2] = {};
+      const int r0 = C::RO * ty, first = r0 & ~3, last = (r0 + C::RO + 3) & ~3;  // columns of P that are not all masked
+      outer_rows<C::RO, C::LP, C::ES>(in, sP + r0 * C::LP, sC + 4 * tx, reverse ? first : 0, reverse ? kTok : last);
+      outer_rows<C::RO, C::LD, C::ES>(ac, sA + r0 * C::LD, sX + 4 * tx, 0, D);
 #pragma unroll
       for (int i = 0; i < C::RO; ++i) {
-        const int t = C::RO * ty + i;
+        const int t = r0 + i;
         if (t >= len) continue;
-        const float w = decay_pow(lg, p.reverse ? len - t : t + 1);
+        const float w = decay_pow(lg, reverse ? len - t : t + 1);
         float o[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[x] = a.scale * fmaf(w, ac[i][x], in[i][x]);
+        for (int x = 0; x < 2; ++x) {
+          o[2 * x] = a.scale * fmaf(w, ac[i][x].x, in[i][x].x);
+          o[2 * x + 1] = a.scale * fmaf(w, ac[i][x].y, in[i][x].y);
+        }
         if (p.x.p != nullptr) {
           float fx[4];
           load_row_piece<float>(static_cast<const float*>(p.x.p) + ret_base(a, p.x, sg.seq, h) + (long long)(row + t) * p.x.sn +
@@ -198,41 +231,43 @@ __global__ void __launch_bounds__(kThreads) retention_simt_kernel(const __grid_c
     }
     // X = gamma^len X + (B w)^T C: rows RS ty .., columns 4 tx ..
     if (C::RS * ty < D) {
-      float acc[C::RS][4];
+      float2 acc[C::RS][2];
       const float w0 = decay_pow(lg, len);
 #pragma unroll
       for (int i = 0; i < C::RS; ++i) {
         const float4 u = *reinterpret_cast<const float4*>(sX + (C::RS * ty + i) * C::ES + 4 * tx);
-        acc[i][0] = w0 * u.x;
-        acc[i][1] = w0 * u.y;
-        acc[i][2] = w0 * u.z;
-        acc[i][3] = w0 * u.w;
+        acc[i][0] = make_float2(w0 * u.x, w0 * u.y);
+        acc[i][1] = make_float2(w0 * u.z, w0 * u.w);
       }
-      for (int s = 0; s < len; ++s) {
+#pragma unroll 4
+      for (int s = 0; s < kTok; ++s) {  // (rows behind the sequence are zeros)
         const float w = sW[s];
-        float4 v = *reinterpret_cast<const float4*>(sC + s * C::ES + 4 * tx);
-        v.x *= w;
-        v.y *= w;
-        v.z *= w;
-        v.w *= w;
+        const float4 v = *reinterpret_cast<const float4*>(sC + s * C::ES + 4 * tx);
+        const float2 v0 = mul2(make_float2(w, w), make_float2(v.x, v.y)), v1 = mul2(make_float2(w, w), make_float2(v.z, v.w));
+        float b[C::RS];
+        if constexpr (C::RS % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < C::RS; i += 4) load_row_piece<float>(sB + s * C::LD + C::RS * ty + i, b + i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::RS; ++i) b[i] = sB[s * C::LD + C::RS * ty + i];
+        }
 #pragma unroll
         for (int i = 0; i < C::RS; ++i) {
-          const float b = sB[s * C::LD + C::RS * ty + i];
-          acc[i][0] = fmaf(b, v.x, acc[i][0]);
-          acc[i][1] = fmaf(b, v.y, acc[i][1]);
-          acc[i][2] = fmaf(b, v.z, acc[i][2]);
-          acc[i][3] = fmaf(b, v.w, acc[i][3]);
+          acc[i][0] = fma2(make_float2(b[i], b[i]), v0, acc[i][0]);
+          acc[i][1] = fma2(make_float2(b[i], b[i]), v1, acc[i][1]);
         }
       }
 #pragma unroll
       for (int i = 0; i < C::RS; ++i)
         *reinterpret_cast<float4*>(sX + (C::RS * ty + i) * C::ES + 4 * tx) =
-            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
     }
   }
   __syncthreads();
   float* dst = SUM ? seg : slot >= 0 && sg.seg == sg.nseg - 1 ? a.states + ((size_t)slot * a.H + h) * (D * D) : nullptr;
   if (dst != nullptr)
+#pragma unroll 4
     for (int i = tid; i < D * C::ES; i += kThreads) dst[(i / C::ES) * D + e0 + i % C::ES] = sX[i];
 }
 
@@ -409,9 +444,11 @@ cudaError_t launch_step_d(int B, int H, int d, const RetTensor& q, const RetTens
 }
 
 // ================================================================ state copies
-// A block takes R floats of every slot: it reads them from all sources into shared memory, then writes all targets,
-// so that a slot may be source and target of different pairs in any order.  A source of several pairs is read once.
-// Bound by the traffic; asynchronous copies keep a block's whole part in flight.
+// A block takes a part of every slot at a time: it reads that part of all sources into shared memory, then writes all
+// targets, so that a slot may be source and target of different pairs in any order.  A source of several pairs is read
+// once.  Asynchronous copies keep a part in flight, and two blocks an SM take parts until none is left, one reading
+// while the other writes; the pairs are compared once a block (with a block a part that was half of the time: 160
+// moves of 1 MB took 119 us).
 constexpr int kCopyBytes = 100 * 1024;  // of shared memory a block, so that two are on an SM: one reads, one writes
 
 __device__ __forceinline__ void copy_async16(void* smem, const void* gmem) {
@@ -426,42 +463,47 @@ __global__ void __launch_bounds__(kThreads) retention_copy_kernel(float* states,
   int* sdst = reinterpret_cast<int*>(buf + ((size_t)n << log_r4));
   int* ssrc = sdst + n;   // source; -1: zeros; n_slots: the pair does nothing
   int* lead = ssrc + n;   // the first pair of the same source, whose part of buf both use
-  const long long e0 = (long long)blockIdx.x << (log_r4 + 2);
-  const int w4 = (int)min((long long)r4, (slot_elems - e0) / 4);
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const int s = src[i], d = dst[i];
     sdst[i] = d;
     ssrc[i] = d < 0 || d >= n_slots || s >= n_slots ? n_slots : max(s, -1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {  // a warp a pair
     const int d = sdst[i], s = ssrc[i];
-    int l = i, m = s == n_slots ? -1 : i;
-    for (int j = 0; j < i; ++j)
-      if (ssrc[j] == s) {
-        l = j;
-        break;
-      }
-    for (int j = i + 1; j < n && m >= 0; ++j)
-      if (sdst[j] == d && ssrc[j] != n_slots) m = -1;  // of several pairs with one target the last counts
-    lead[i] = m < 0 ? -1 - l : l;                      // negative: nothing to write (but others may use its part)
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n << log_r4; i += kThreads) {
-    const int pr = i >> log_r4, c = i & (r4 - 1), s = ssrc[pr], l = lead[pr];
-    if ((l == pr || l == -1 - pr) && s < n_slots && c < w4) {
-      if (s < 0)
-        buf[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      else
-        copy_async16(buf + i, states + s * slot_elems + e0 + 4 * c);
+    int l = i;
+    bool later = s == n_slots;
+    for (int j = threadIdx.x & 31; j < n; j += 32) {
+      const int sj = ssrc[j];
+      if (sj == s) l = min(l, j);
+      later |= j > i && sdst[j] == d && sj != n_slots;  // of several pairs with one target the last counts
     }
+    l = __reduce_min_sync(0xffffffffu, l);
+    later = __any_sync(0xffffffffu, later);
+    if ((threadIdx.x & 31) == 0) lead[i] = later ? -1 - l : l;  // negative: nothing to write, others may use its part
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  for (int i = threadIdx.x; i < n << log_r4; i += kThreads) {
-    const int pr = i >> log_r4, c = i & (r4 - 1), l = lead[pr];
-    if (l >= 0 && c < w4)
-      __stcs(reinterpret_cast<float4*>(states + sdst[pr] * slot_elems + e0) + c, buf[((size_t)l << log_r4) + c]);
+  const int parts = (int)((slot_elems + (4ll << log_r4) - 1) >> (log_r4 + 2));
+  for (int part = blockIdx.x; part < parts; part += gridDim.x) {
+    const long long e0 = (long long)part << (log_r4 + 2);
+    const int w4 = (int)min((long long)r4, (slot_elems - e0) / 4);
+    for (int i = threadIdx.x; i < n << log_r4; i += kThreads) {
+      const int pr = i >> log_r4, c = i & (r4 - 1), s = ssrc[pr], l = lead[pr];
+      if ((l == pr || l == -1 - pr) && s < n_slots && c < w4) {
+        if (s < 0)
+          buf[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        else
+          copy_async16(buf + i, states + s * slot_elems + e0 + 4 * c);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    for (int i = threadIdx.x; i < n << log_r4; i += kThreads) {
+      const int pr = i >> log_r4, c = i & (r4 - 1), l = lead[pr];
+      if (l >= 0 && c < w4)
+        __stcs(reinterpret_cast<float4*>(states + sdst[pr] * slot_elems + e0) + c, buf[((size_t)l << log_r4) + c]);
+    }
+    __syncthreads();
   }
 }
 
@@ -501,8 +543,8 @@ cudaError_t retention_copy_launch(float* states, long long slot_elems, int n_slo
   static SmemOptIn opt;
   cudaError_t e = opt.ensure((const void*)retention_copy_kernel, 227 * 1024);
   if (e != cudaSuccess) return e;
-  const long long r = 4ll << log_r4;
-  retention_copy_kernel<<<(unsigned)((slot_elems + r - 1) / r), kThreads, bytes, st>>>(states, slot_elems, n_slots, src,
+  const long long r = 4ll << log_r4, parts = (slot_elems + r - 1) / r;
+  retention_copy_kernel<<<(unsigned)std::min<long long>(parts, 152 * std::max<long long>(2, std::min<long long>(8, (long long)(200 * 1024 / bytes)))), kThreads, bytes, st>>>(states, slot_elems, n_slots, src,
                                                                                        dst, n, log_r4);
   note_launch();
   return cudaGetLastError();
