@@ -10,7 +10,11 @@ namespace mhla {
 constexpr int kFeatIdentity = 3;  // beside the kinds of phi_k
 
 __device__ __forceinline__ float ret_phi(float x, int feature) {
-  return feature == kFeatIdentity ? x : phi_k(x, feature);
+  if (feature == kFeatIdentity) return x;
+  if (feature == 1) return x > 0.f ? x : (x == x ? 0.f : x);  // (not-a-number stays)
+  // without a branch for the sign: neighbouring lanes differ in it
+  const float e = expf(feature == 0 && x > 0.f ? 0.f : x);
+  return feature == 0 && x > 0.f ? x + 1.f : e;
 }
 // phi'(x): 1 for the identity; ELU + 1: 1 for x > 0, e^x otherwise; ReLU: 1 for x > 0; exp: e^x
 __device__ __forceinline__ float ret_dphi(float x, int feature) {
