@@ -119,13 +119,15 @@ struct Plan {
 // where a round is `slots` blocks.  Packed sequences, of unknown lengths, take their work over the slots and half a
 // block for the tail; four times the mean counts as their longest.  The costs are measured ones: a chunk takes 3.3 us
 // at d = 128 and 3.8 us at d = 64 (two blocks an SM), a block 2.5 chunks to start, the sum of a chunk 0.45 of its
-// pass, a segment's state 2 chunks, two launches 8 us; fp32 (SIMT; 128 tokens) 14 us a chunk.
-Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward) {
+// pass, a segment's state 2 chunks, two launches 8 us; fp32 (SIMT; 128 tokens) 10 us a chunk.  A bf16 block that
+// returns a state (exact) takes 1.5 times as long: its segment, the last one, is better short.
+Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward, bool exact) {
   const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
   const double slots = f32 ? 152.0 * (d == 128 ? 1 : d == 64 ? 2 : 4) : d == 128 ? 152.0 : 304.0;
-  const double fixed = 8.0 / (f32 ? 14.0 : d == 128 ? 3.3 : 3.8);
+  const double fixed = 8.0 / (f32 ? 10.0 : d == 128 ? 3.3 : 3.8);
   const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.5 : 2.0;
+  const double last = exact && !f32 ? 1.5 : 1.0;
   const int cols = f32 && d == 128 ? 2 : 1;  // blocks that share a segment
   const long long all = (tokens + 127) / 128, most = ((long long)N + 127) / 128;
   const double longest = packed ? std::min<double>((double)most, 4.0 * all / B) : (double)most;
@@ -140,8 +142,8 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
       if (n < most) cost += fixed + (more > 0 ? (work + blocks * start) * nsum * sum / slots + more * H * nsum * state / slots : 0);
     } else {
       const long long segs = (most + n - 1) / n;
-      const double blocks = (double)B * H * segs * cols;
-      cost = std::ceil(blocks * npass / slots) * (n + start);
+      const double blocks = (double)B * H * segs * cols, end = last * (double)(most - (segs - 1) * n);
+      cost = std::ceil(blocks * npass / slots) * (std::max((double)std::min(n, most), end) + start);
       if (segs > 1)
         cost += std::ceil((double)B * H * (segs - 1) * cols * nsum / slots) * (n + start) * sum + fixed +
                 (double)B * H * segs * nsum * state / slots;
@@ -166,7 +168,8 @@ bool sizes_ok(int B, int H, int N, int d) { return B >= 0 && H >= 0 && N >= 0 &&
 
 // What retention_forward and retention_backward have in common; *empty: nothing to do.
 mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, int H, int N, int d, const int* cu,
-                  mhla_dtype dt, const retention_options* opt, bool backward, void* ws, size_t ws_bytes, bool* empty) {
+                  mhla_dtype dt, const retention_options* opt, bool backward, bool exact, void* ws, size_t ws_bytes,
+                  bool* empty) {
   *empty = false;
   if (!sizes_ok(B, H, N, d) || (dt != MHLA_F32 && dt != MHLA_BF16) || !options_ok(opt)) return MHLA_ERR_INVALID_ARG;
   if (B == 0 || H == 0 || N == 0) {
@@ -177,7 +180,7 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
   if (tokens > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
   if (!gamma || !aligned(gamma, 4) || !aligned(cu, 4)) return MHLA_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MHLA_ERR_INVALID_ARG;
-  *plan = make_plan(B, H, tokens, d, dt, cu != nullptr, backward);
+  *plan = make_plan(B, H, tokens, d, dt, cu != nullptr, backward, exact);
   if ((long long)plan->G * H > 0x7fffffffll / 3 || (long long)B * H > 0x7fffffffll / 3) return MHLA_ERR_UNSUPPORTED;
   if (ws_bytes < plan->bytes) return MHLA_ERR_INVALID_ARG;
   *e = {cu ? 1 : B, H, N, d, dt == MHLA_F32 ? 4 : 2};
@@ -215,10 +218,12 @@ size_t retention_workspace_bytes(int B, int H, int tokens, int d, int backward) 
   if (!sizes_ok(B, H, tokens, d) || (backward != 0 && backward != 1)) return 0;
   if (B == 0 || H == 0 || tokens == 0) return kWorkspacePrefix;
   size_t n = 0;
-  for (mhla_dtype dt : {MHLA_F32, MHLA_BF16}) {
-    n = std::max(n, make_plan(B, H, tokens, d, dt, true, backward != 0).bytes);
-    if (tokens % B == 0) n = std::max(n, make_plan(B, H, tokens, d, dt, false, backward != 0).bytes);
-  }
+  for (mhla_dtype dt : {MHLA_F32, MHLA_BF16})
+    for (bool exact : {false, true}) {
+      if (exact && backward) continue;
+      n = std::max(n, make_plan(B, H, tokens, d, dt, true, backward != 0, exact).bytes);
+      if (tokens % B == 0) n = std::max(n, make_plan(B, H, tokens, d, dt, false, backward != 0, exact).bytes);
+    }
   return n;
 }
 
@@ -234,8 +239,8 @@ mhla_status retention_forward(const void* q, const mhla_strides* q_strides, cons
   Plan plan;
   Extent e;
   bool empty;
-  const mhla_status st = begin(&a, &plan, &e, gamma, B, H, N, d, cu_seqlens, dt, opt, false, workspace,
-                               workspace_bytes, &empty);
+  const mhla_status st = begin(&a, &plan, &e, gamma, B, H, N, d, cu_seqlens, dt, opt, false, states != nullptr,
+                               workspace, workspace_bytes, &empty);
   if (st != MHLA_OK || empty) return st;
   RetTensor tq, tk, tv, ty;
   if (!make_tensor(&tq, q, q_strides, e) || !make_tensor(&tk, k, k_strides, e) || !make_tensor(&tv, v, v_strides, e) ||
@@ -279,7 +284,7 @@ mhla_status retention_backward(const void* q, const mhla_strides* q_strides, con
   Plan plan;
   Extent e;
   bool empty;
-  const mhla_status st = begin(&a, &plan, &e, gamma, B, H, N, d, cu_seqlens, dt, opt, true, workspace,
+  const mhla_status st = begin(&a, &plan, &e, gamma, B, H, N, d, cu_seqlens, dt, opt, true, false, workspace,
                                workspace_bytes, &empty);
   if (st != MHLA_OK || empty) return st;
   RetTensor in[4], out[3];

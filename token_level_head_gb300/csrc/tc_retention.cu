@@ -164,11 +164,11 @@ __device__ __forceinline__ void split8(float* f, uint8_t* hi, uint8_t* lo, uint8
   *piece(lo2, kTok, r, j) = pack8(f);
 }
 
-// Row r (D columns) of B times w as a sum of three bf16 numbers.
+// D columns, from 8 jb, of row r of B times w as a sum of three bf16 numbers.
 template <int D>
-__device__ __forceinline__ void weigh_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, float w) {
+__device__ __forceinline__ void weigh_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w) {
 #pragma unroll 1
-  for (int j0 = 0; j0 < D / 8; j0 += 2) {
+  for (int j0 = jb; j0 < jb + D / 8; j0 += 2) {
     uint4 u[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) u[j] = *piece(hi, kTok, r, j0 + j);
@@ -216,10 +216,10 @@ __device__ __forceinline__ void weigh_row2(uint8_t* hi, uint8_t* lo, int r, int 
 // weigh_row3 of phi of the row, in fp32, over its d columns: of the row in global memory (raw), the tile holds
 // the rounded phi already.
 template <int D>
-__device__ __noinline__ void weigh_phi_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, float w,
+__device__ __noinline__ void weigh_phi_row3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w,
                                             const __nv_bfloat16* raw, int d, int feature) {
 #pragma unroll 1
-  for (int j = 0; j < D / 8; ++j) {
+  for (int j = jb; j < jb + D / 8; ++j) {
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (w != 0.f && 8 * j < d) {
       unpack8(*reinterpret_cast<const uint4*>(raw + 8 * j), f);
@@ -282,13 +282,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t 
       : "memory");
 }
 
-// D[tmem] (+)= A^T B, both operands MN-major: A [128 rows][M], B [128 rows][N].
+// D[tmem] (+)= A^T B, both operands MN-major: A [128 rows][M], B [128 rows][N columns from `col`].
 template <int M, int N, bool ACC>
-__device__ __forceinline__ void mma_outer(uint32_t d, Desc a, Desc b) {
+__device__ __forceinline__ void mma_outer(uint32_t d, Desc a, Desc b, uint32_t col = 0) {
   constexpr uint32_t kId = idesc_bf16_f32(M, N, 1, 1);
-  mma_ss<kId, ACC>(d, a, 0, b, 0);
+  mma_ss<kId, ACC>(d, a, 0, b, 2 * col);
 #pragma unroll
-  for (int k = 1; k < kTok / 16; ++k) mma_ss<kId, true>(d, a, k * 2048, b, k * 2048);
+  for (int k = 1; k < kTok / 16; ++k) mma_ss<kId, true>(d, a, k * 2048, b, k * 2048 + 2 * col);
 }
 
 // Prefetch of one operand's chunk into L2.
@@ -326,6 +326,8 @@ struct PassTile {
   static constexpr uint32_t intra(uint32_t c) { return D == 128 ? 256 + c : 32 + c + (c & 32); }
   static constexpr uint32_t kColInter = 128;
   static constexpr uint32_t kColX = D == 128 ? 384 : 192;     // X gamma^len, dX is added to it
+  // dX by itself, where the state is returned: over P (D = 64: in its two places)
+  static constexpr uint32_t apart(uint32_t c) { return D == 128 ? c : c + (c & 32); }
   static constexpr int kPerSm = D == 128 ? 1 : 2;
   static constexpr int kWarpW = kWarpOut + 8, kWarpX = D == 128 ? kWarpW + 4 : kWarpW;
   static constexpr int kXWarps = D == 128 ? 8 : 4;
@@ -365,6 +367,7 @@ struct PassBars {
   uint64_t in_full;   // inter
   uint64_t p_full;    // P in TMEM (out warps)
   uint64_t w_full;    // B w (W warps)
+  uint64_t w2_full;   // D = 128, three parts: the X warps' columns of it
   uint64_t dx_full;   // dX
   uint64_t x_full;    // the bf16 tile of X (X warps)
   uint64_t o_full;    // intra
@@ -446,6 +449,7 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
       ++maps;
     }
     if (D == 64 && i > 0 && !wait_warp(&b->o_free, (i - 1) & 1, gd)) return;  // (and over intra)
+    if (terms > 2 && !wait_warp(&b->x_full, i & 1, gd)) return;               // (and over the last dX)
     tc_fence_after();
     __syncwarp();
     if (elect_one()) {
@@ -488,12 +492,25 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
     }
     if (i < nx) {
       if (!wait_warp(&b->w_full, i & 1, gd)) return;
+      if (terms > 2 && D == 128 && !wait_warp(&b->w2_full, i & 1, gd)) return;
+      if (terms > 2 && !wait_warp(&b->o_full, i & 1, gd)) return;  // P has been read
       tc_fence_after();
       __syncwarp();
       if (elect_one()) {
-        mma_outer<D, D, true>(tmem + P::kColX, bm, cm);
-        mma_outer<D, D, true>(tmem + P::kColX, lo, cm);
-        if (terms > 2) mma_outer<D, D, true>(tmem + P::kColX, lo2, cm);
+        if (terms > 2) {
+          // The accumulator rounds towards zero at each of these: dX is added up by itself and then, in fp32, to X.
+          // (On top of X the state of 4,000 tokens was off by 2^-19, so by 2^-21.)
+          constexpr int kN = D == 128 ? 128 : 32;
+#pragma unroll
+          for (int e = 0; e < D; e += kN) {
+            mma_outer<D, kN, false>(tmem + P::kColS + P::apart(e), bm, cm, e);
+            mma_outer<D, kN, true>(tmem + P::kColS + P::apart(e), lo, cm, e);
+            mma_outer<D, kN, true>(tmem + P::kColS + P::apart(e), lo2, cm, e);
+          }
+        } else {
+          mma_outer<D, D, true>(tmem + P::kColX, bm, cm);
+          mma_outer<D, D, true>(tmem + P::kColX, lo, cm);
+        }
         mma_commit(&b->dx_full);
         mma_commit(&b->empty[s]);
       }
@@ -667,19 +684,24 @@ __device__ __noinline__ bool map_chunk(uint8_t* sm, PassBars* b, int row, int i,
   return true;
 }
 
-// B w of chunk i in three parts, the third one over X's tile, once inter has read it.
-template <int D>
-__device__ __noinline__ bool weigh_chunk3(uint8_t* sm, PassBars* b, int row, int i, int ch, float w) {
+// C columns, from 8 jb, of row `row` of B w of chunk i in three parts, the third one over X's tile, once inter has
+// read it.  D = 128: the W warps take 64 columns, the X warps, which have nothing else to do then, the others.
+template <int D, int C>
+__device__ __noinline__ bool weigh_chunk3(uint8_t* sm, PassBars* b, int row, int jb, int i) {
   using P = PassTile<D>;
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
-  if (!wait_warp(&b->in_full, i & 1, gd)) return false;
+  if (!wait_warp(&b->s_full, i & 1, gd) || !wait_warp(&b->in_full, i & 1, gd)) return false;
+  const int ch = chunk_of(i, b->ctx.n, b->ctx.reverse), len = chunk_len(ch, b->ctx.len);
+  const float w = row < len ? decay_pow(b->ctx.lg, b->ctx.reverse ? row : len - 1 - row) : 0.f;
   uint8_t *bt = sm + P::kOffBC + (i % kStages) * 2 * P::kOp, *lo = sm + P::kOffLo, *lo2 = sm + P::kOffX;
   if (b->ctx.fb != kFeatIdentity) {  // phi(b) in fp32 for the state
     const __nv_bfloat16* raw = b->ctx.b + (long long)(b->ctx.row0 + ch * kTok + row) * b->ctx.b_n;
-    weigh_phi_row3<D>(bt, lo, lo2, row, w, raw, b->ctx.d, b->ctx.fb);
+    weigh_phi_row3<C>(bt, lo, lo2, row, jb, w, raw, b->ctx.d, b->ctx.fb);
   } else {
-    weigh_row3<D>(bt, lo, lo2, row, w);
+    weigh_row3<C>(bt, lo, lo2, row, jb, w);
   }
+  fence_proxy_async_smem();
+  __syncwarp();
   return true;
 }
 
@@ -704,15 +726,15 @@ struct Weigh {
   __device__ __forceinline__ bool weigh(int i) {
     // B has been read by the scores, the second part's tile by the last dX
     if (!wait_warp(&b->s_full, i & 1, gd) || (i > 0 && !wait_warp(&b->dx_full, (i - 1) & 1, gd))) return false;
-    const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
-    const float w = row < len ? decay_pow(lg, reverse ? row : len - 1 - row) : 0.f;
     if (b->ctx.terms > 2) {
-      if (!weigh_chunk3<D>(sm, b, row, i, ch, w)) return false;
+      if (!weigh_chunk3<D, 64>(sm, b, row, 0, i)) return false;
     } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
+      const int len = chunk_len(chunk_of(i, n, reverse), all);
+      const float w = row < len ? decay_pow(lg, reverse ? row : len - 1 - row) : 0.f;
       weigh_row2<D>(sm + P::kOffBC + (i % kStages) * 2 * P::kOp, sm + P::kOffLo, row, 0, w);
+      fence_proxy_async_smem();
+      __syncwarp();
     }
-    fence_proxy_async_smem();
-    __syncwarp();
     if ((row & 31) == 0) mbar_arrive(&b->w_full);
     return true;
   }
@@ -777,7 +799,15 @@ struct Carry {
     for (int k = 0; k < kBlocks; ++k) {
       float v[16];
       tmem_ld16x32(tmem_of(k), v);
-      tmem_ld_wait();
+      if (b->ctx.terms > 2) {
+        float u[16];
+        tmem_ld16x32(tl - P::kColX + P::kColS + ((uint32_t)(16 * (k >> 1)) << 16) + P::apart(col_of(k)), u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] += u[x];
+      } else {
+        tmem_ld_wait();
+      }
       if (more) {
         keep(k, v, wl);
       } else if (to != nullptr) {
@@ -838,9 +868,15 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
   carry_start<D>(sm, b, warp, lane);
   Carry<D> x(sm, b, warp, lane);
   const int nx = b->ctx.nx;
+  const bool help = b->ctx.terms > 2;
 #pragma unroll 1
-  for (int i = 0; i < nx; ++i)
+  for (int i = 0; i < nx; ++i) {
+    if (help) {
+      if (!weigh_chunk3<D, 32>(sm, b, 32 * (warp & 3) + lane, 8 + 4 * ((warp - PassTile<D>::kWarpX) >> 2), i)) return;
+      if (lane == 0) mbar_arrive(&b->w2_full);
+    }
     if (!x.update(i)) return;
+  }
 }
 
 // Both in the same warps.
@@ -877,6 +913,7 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     for (uint64_t* m : {&b->mapped, &b->w_full}) mbar_init(m, 4);
     for (uint64_t* m : {&b->p_full, &b->o_free}) mbar_init(m, 8);
     mbar_init(&b->x_full, P::kXWarps);
+    mbar_init(&b->w2_full, 8);
     b->abort = 0;
     b->issued = b->issued_a = 0;
     fence_mbar_init();
