@@ -120,14 +120,14 @@ struct Plan {
 // block for the tail; four times the mean counts as their longest.  The costs are measured ones: a chunk takes 3.3 us
 // at d = 128 and 3.8 us at d = 64 (two blocks an SM), a block 2.5 chunks to start, the sum of a chunk 0.45 of its
 // pass, a segment's state 2 chunks, two launches 8 us; fp32 (SIMT; 128 tokens) 10 us a chunk.  A bf16 block that
-// returns a state (exact) takes 1.5 times as long: its segment, the last one, is better short.
+// returns a state (exact) takes half as long again for about 8 chunks: its segment, the last one, is better short.
 Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward, bool exact) {
   const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
   const double slots = f32 ? 152.0 * (d == 128 ? 1 : d == 64 ? 2 : 4) : d == 128 ? 152.0 : 304.0;
   const double fixed = 8.0 / (f32 ? 10.0 : d == 128 ? 3.3 : 3.8);
   const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.5 : 2.0;
-  const double last = exact && !f32 ? 1.5 : 1.0;
+  const double slow = exact && !f32 ? 0.5 : 0.0;
   const int cols = f32 && d == 128 ? 2 : 1;  // blocks that share a segment
   const long long all = (tokens + 127) / 128, most = ((long long)N + 127) / 128;
   const double longest = packed ? std::min<double>((double)most, 4.0 * all / B) : (double)most;
@@ -142,7 +142,7 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
       if (n < most) cost += fixed + (more > 0 ? (work + blocks * start) * nsum * sum / slots + more * H * nsum * state / slots : 0);
     } else {
       const long long segs = (most + n - 1) / n;
-      const double blocks = (double)B * H * segs * cols, end = last * (double)(most - (segs - 1) * n);
+      const double blocks = (double)B * H * segs * cols, rest = (double)(most - (segs - 1) * n), end = rest + slow * std::min(rest, 8.0);
       cost = std::ceil(blocks * npass / slots) * (std::max((double)std::min(n, most), end) + start);
       if (segs > 1)
         cost += std::ceil((double)B * H * (segs - 1) * cols * nsum / slots) * (n + start) * sum + fixed +

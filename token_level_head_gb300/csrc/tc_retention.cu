@@ -12,8 +12,9 @@
 //
 // What is rounded to bf16: the masked scores, the copy of X that the product reads (X itself stays
 // fp32) and phi of operands with a feature map.  B w is carried as a sum of bf16 numbers: of two (over
-// the B tile and in a tile of its own: 2^-16 of a term) where only bf16 outputs come of it, of three (the
-// last over the tile of X: 2^-24) in the segment whose state is returned in fp32.
+// the B tile and in a tile of its own: 2^-16 of a term) where only bf16 outputs come of it or the decay
+// leaves less than 1/8 of it, of three (the last over the tile of X: 2^-24) in the chunks that make up a
+// state which is returned in fp32.
 //
 // Roles (D = 128: 22 warps and one CTA an SM, D = 64: 14 warps and two):
 //   warp 0       TMA producer: the tiles of a chunk, B and C two chunks deep, A one
@@ -341,7 +342,8 @@ struct PassCtx {
   int ha, hb, hc, ba, bb, bc;    // head and batch coordinates in the maps
   int row0, len, n;              // first row, tokens, chunks
   int nx;                        // chunks whose dX is needed
-  int reverse, terms;            // direction; bf16 numbers that B w is the sum of
+  int reverse;                   // direction
+  int exact;                     // first chunk whose B w is a sum of three bf16 numbers and whose dX is apart
   int fa, fb, fc, fx;            // feature maps of A, B, C and x
   int d;
   float lg;
@@ -427,7 +429,7 @@ __device__ __noinline__ void pass_producer(uint8_t* sm, PassBars* b) {
 template <int D>
 __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
   using P = PassTile<D>;
-  const int n = b->ctx.n, nx = b->ctx.nx, len = b->ctx.len, reverse = b->ctx.reverse, terms = b->ctx.terms;
+  const int n = b->ctx.n, nx = b->ctx.nx, len = b->ctx.len, reverse = b->ctx.reverse, exact = b->ctx.exact;
   const bool mapped = b->ctx.mapped();
   const uint32_t tmem = b->tbase;
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
@@ -449,7 +451,7 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
       ++maps;
     }
     if (D == 64 && i > 0 && !wait_warp(&b->o_free, (i - 1) & 1, gd)) return;  // (and over intra)
-    if (terms > 2 && !wait_warp(&b->x_full, i & 1, gd)) return;               // (and over the last dX)
+    if (i > exact && !wait_warp(&b->x_full, i & 1, gd)) return;               // (and over the last dX)
     tc_fence_after();
     __syncwarp();
     if (elect_one()) {
@@ -492,12 +494,12 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
     }
     if (i < nx) {
       if (!wait_warp(&b->w_full, i & 1, gd)) return;
-      if (terms > 2 && D == 128 && !wait_warp(&b->w2_full, i & 1, gd)) return;
-      if (terms > 2 && !wait_warp(&b->o_full, i & 1, gd)) return;  // P has been read
+      if (i >= exact && D == 128 && !wait_warp(&b->w2_full, (i - exact) & 1, gd)) return;
+      if (i >= exact && !wait_warp(&b->o_full, i & 1, gd)) return;  // P has been read
       tc_fence_after();
       __syncwarp();
       if (elect_one()) {
-        if (terms > 2) {
+        if (i >= exact) {
           // The accumulator rounds towards zero at each of these: dX is added up by itself and then, in fp32, to X.
           // (On top of X the state of 4,000 tokens was off by 2^-19, so by 2^-21.)
           constexpr int kN = D == 128 ? 128 : 32;
@@ -726,7 +728,7 @@ struct Weigh {
   __device__ __forceinline__ bool weigh(int i) {
     // B has been read by the scores, the second part's tile by the last dX
     if (!wait_warp(&b->s_full, i & 1, gd) || (i > 0 && !wait_warp(&b->dx_full, (i - 1) & 1, gd))) return false;
-    if (b->ctx.terms > 2) {
+    if (i >= b->ctx.exact) {
       if (!weigh_chunk3<D, 64>(sm, b, row, 0, i)) return false;
     } else {  // no fp32 state comes of it: the tile's rounded phi is good enough
       const int len = chunk_len(chunk_of(i, n, reverse), all);
@@ -799,7 +801,7 @@ struct Carry {
     for (int k = 0; k < kBlocks; ++k) {
       float v[16];
       tmem_ld16x32(tmem_of(k), v);
-      if (b->ctx.terms > 2) {
+      if (i >= b->ctx.exact) {
         float u[16];
         tmem_ld16x32(tl - P::kColX + P::kColS + ((uint32_t)(16 * (k >> 1)) << 16) + P::apart(col_of(k)), u);
         tmem_ld_wait();
@@ -868,10 +870,10 @@ __device__ __noinline__ void pass_x(uint8_t* sm, PassBars* b, int warp, int lane
   carry_start<D>(sm, b, warp, lane);
   Carry<D> x(sm, b, warp, lane);
   const int nx = b->ctx.nx;
-  const bool help = b->ctx.terms > 2;
+  const int exact = b->ctx.exact;
 #pragma unroll 1
   for (int i = 0; i < nx; ++i) {
-    if (help) {
+    if (i >= exact) {
       if (!weigh_chunk3<D, 32>(sm, b, 32 * (warp & 3) + lane, 8 + 4 * ((warp - PassTile<D>::kWarpX) >> 2), i)) return;
       if (lane == 0) mbar_arrive(&b->w2_full);
     }
@@ -950,11 +952,14 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
     c.len = sg.len;
     c.to = slot >= 0 && sg.seg == sg.nseg - 1 ? r.states + ((size_t)slot * r.H + h) * dd : nullptr;
     c.nx = c.to != nullptr ? n : n - 1;
-    c.terms = c.to != nullptr ? 3 : 2;
     c.fa = p.a.feature;
     c.fb = p.b.feature;
     c.fc = p.c.feature;
     c.fx = p.x.feature;
+    // the last chunks, whose terms the decay leaves more than 1/8 of (the last may be short); all, where the others
+    // would take the rounded phi
+    const float reach = lg == 0.f || c.fb != kFeatIdentity ? (float)n : fminf((float)n, 2.f + 3.f / (kTok * fabsf(lg)));
+    c.exact = c.to == nullptr ? n : n - (int)reach;
     c.d = r.d;
     c.lg = lg;
     c.out = static_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p)) + ret_base(r, p.out, sg.seq, h);
