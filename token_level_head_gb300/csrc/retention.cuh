@@ -76,7 +76,7 @@ struct Segment {
   int seq;     // sequence, -1: no such segment
   int seg;     // its number within the sequence
   int nseg;    // segments of the sequence
-  int g0;      // segments of the sequences before it: this one's number is g0 + seg
+  int w0;      // of a sequence of two segments or more: the workspace's first state of it
   int row0;    // first token row (within the sequence's batch entry when dense)
   int len;     // tokens of the segment
   int all;     // tokens of the sequence
@@ -112,7 +112,7 @@ constexpr int kOrdered = 64;  // packed sequences up to so many are taken longes
 // sequences, one of 4001 tokens among 20,000, d = 128: 177 us as they come, 145 us in order).
 __device__ __forceinline__ Segment find_ordered(const RetArgs& a, int k, int* scratch) {
   const int tid = threadIdx.x;
-  int lo, hi;
+  int lo = 0, hi = 0;
   if (tid < a.B) {
     packed_range(a, tid, &lo, &hi);
     scratch[tid] = hi - lo;
@@ -127,27 +127,66 @@ __device__ __forceinline__ Segment find_ordered(const RetArgs& a, int k, int* sc
   __syncthreads();
   Segment s;
   s.seq = -1;
-  int g0 = 0;
-  for (int i = 0; i < a.B; ++i) {  // (every thread; the lengths are in shared memory)
-    const int q = scratch[kOrdered + i], m = (scratch[q] + a.L - 1) / a.L;
-    if (k < m) {
-      s.seq = q;
-      s.seg = k;
-      s.nseg = m;
-      break;
+  if (tid < 32) {  // the first warp: places 2 lane, 2 lane + 1 of the order
+    int q[2], m[2], n = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      q[i] = 2 * tid + i < a.B ? scratch[kOrdered + 2 * tid + i] : 0;
+      m[i] = 2 * tid + i < a.B ? (scratch[q[i]] + a.L - 1) / a.L : 0;
+      n += m[i];
     }
-    k -= m;
+    int first = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, first, o);
+      if (tid >= o) first += u;
+    }
+    first -= n;
+    // states of the split sequences before sequence 2 tid, 2 tid + 1 (in their own order)
+    int w[2], v = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = 2 * tid + i < a.B ? (scratch[2 * tid + i] + a.L - 1) / a.L : 0;
+      w[i] = w[i] >= 2 ? w[i] : 0;
+      v += w[i];
+    }
+    int before = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, before, o);
+      if (tid >= o) before += u;
+    }
+    before -= v;
+    const bool one = k >= first && k < first + n;
+    const unsigned who = __ballot_sync(0xffffffffu, one);
+    if (who != 0) {
+      const int src = __ffs(who) - 1, hit = k - first >= m[0] ? 1 : 0;
+      s.seq = __shfl_sync(0xffffffffu, hit ? q[1] : q[0], src);
+      s.nseg = __shfl_sync(0xffffffffu, hit ? m[1] : m[0], src);
+      s.seg = __shfl_sync(0xffffffffu, k - first - (hit ? m[0] : 0), src);
+      const int even = __shfl_sync(0xffffffffu, before, s.seq >> 1), first_w = __shfl_sync(0xffffffffu, w[0], s.seq >> 1);
+      s.w0 = even + (s.seq & 1 ? first_w : 0);
+    }
+    __syncwarp();
+    if (tid == 0) {
+      scratch[kOrdered] = s.seq;
+      scratch[kOrdered + 1] = s.nseg;
+      scratch[kOrdered + 2] = s.seg;
+      scratch[kOrdered + 3] = s.w0;
+    }
   }
-  if (s.seq >= 0)
-    for (int i = 0; i < s.seq; ++i) g0 += (scratch[i] + a.L - 1) / a.L;
+  __syncthreads();
+  s.seq = scratch[kOrdered];
+  s.nseg = scratch[kOrdered + 1];
+  s.seg = scratch[kOrdered + 2];
+  s.w0 = scratch[kOrdered + 3];
   __syncthreads();
   if (s.seq < 0) return s;
   packed_range(a, s.seq, &lo, &hi);
-  s.g0 = g0;
   s.all = hi - lo;
   s.row0 = lo + s.seg * a.L;
   s.len = min(a.L, s.all - s.seg * a.L);
-  if (s.g0 + s.nseg > a.G) s.seq = -1;  // (offsets out of order, as below)
+  if (s.nseg >= 2 && s.w0 + s.nseg > a.W) s.seq = -1;  // (offsets out of order, as below)
   return s;
 }
 
@@ -164,17 +203,17 @@ __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, Segment
     s.seq = per > 0 && k < a.B * per ? k / per : -1;
     if (s.seq < 0) return s;
     s.seg = k - s.seq * per;
-    s.g0 = s.seq * s.nseg;
+    s.w0 = s.seq * s.nseg;
     s.all = a.N;
   } else {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.B + blockDim.x - 1) / blockDim.x;
     const int i0 = min(tid * per, a.B), i1 = min(i0 + per, a.B);
-    int n = 0, m = 0;  // of the kind, in all
+    int n = 0, m = 0;  // of the kind, of split sequences
     for (int i = i0; i < i1; ++i) {
       const int q = packed_segments(a, i);
       n += segments_of_kind(q, kind);
-      m += q;
+      m += q >= 2 ? q : 0;
     }
     int in = n, im = m;
 #pragma unroll
@@ -191,10 +230,10 @@ __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, Segment
     }
     if (tid == 0) scratch[64] = -1;
     __syncthreads();
-    int first = in - n, g0 = im - m;
+    int first = in - n, w0 = im - m;
     for (int w = 0; w < warp; ++w) {
       first += scratch[w];
-      g0 += scratch[32 + w];
+      w0 += scratch[32 + w];
     }
     if (k >= first && k < first + n) {
       for (int i = i0; i < i1; ++i) {
@@ -202,24 +241,24 @@ __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, Segment
         if (k < first + c) {
           scratch[64] = i;
           scratch[65] = k - first;
-          scratch[66] = g0;
+          scratch[66] = w0;
           break;
         }
         first += c;
-        g0 += q;
+        w0 += q >= 2 ? q : 0;
       }
     }
     __syncthreads();
     s.seq = scratch[64];
     s.seg = scratch[65];
-    s.g0 = scratch[66];
+    s.w0 = scratch[66];
     __syncthreads();
     if (s.seq < 0) return s;
     int hi;
     packed_range(a, s.seq, &lo, &hi);
     s.nseg = packed_segments(a, s.seq);
     s.all = hi - lo;
-    if (s.g0 + s.nseg > a.G) {  // (offsets out of order may claim more segments than the workspace has)
+    if (s.nseg >= 2 && s.w0 + s.nseg > a.W) {  // (offsets out of order may claim more than the workspace has)
       s.seq = -1;
       return s;
     }
@@ -256,7 +295,7 @@ __device__ __forceinline__ int ret_slot(const int* slots, int n_slots, int seq) 
 __device__ __forceinline__ const float* entering_state(const RetArgs& a, const RetPass& p, const Segment& sg, int h,
                                                        int slot) {
   const size_t dd = (size_t)a.d * a.d;
-  if (sg.nseg > 1) return a.seg + (((size_t)p.sum * a.G + sg.g0 + sg.seg) * a.H + h) * dd;
+  if (sg.nseg > 1) return a.seg + (((size_t)p.sum * a.W + sg.w0 + sg.seg) * a.H + h) * dd;
   return a.load && slot >= 0 ? a.states + ((size_t)slot * a.H + h) * dd : nullptr;
 }
 

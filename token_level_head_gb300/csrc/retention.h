@@ -48,7 +48,8 @@ struct RetArgs {
   int L;                        // tokens of a segment (a multiple of 128)
   int G;                        // segments in all; of those, segments that enter another one; sequences of two
   int inner, split;             // segments or more (packed: at most)
-  float* seg;                   // [nsum][G][H][d][d] segment states; null when no sequence has two segments
+  int W;                        // segments of such sequences (packed: at most)
+  float* seg;                   // [nsum][W][H][d][d] their states; null when no sequence has two segments
   unsigned* status;             // the workspace's status word
 };
 

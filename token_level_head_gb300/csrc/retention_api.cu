@@ -106,7 +106,7 @@ bool options_ok(const retention_options* opt) {
 // ---- segments
 struct Plan {
   int L, G;      // tokens of a segment, segments
-  int inner, splits;  // segments that enter another one, sequences of two or more
+  int inner, splits, W;  // segments that enter another one, sequences of two or more, segments of those
   size_t bytes;  // workspace
   bool split;    // some sequence may have two segments
 };
@@ -133,7 +133,7 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
   const double longest = packed ? std::min<double>((double)most, 4.0 * all / B) : (double)most;
   double best = 1e300;
   long long pick = most;
-  for (long long n = 1; n <= most; n = n < 64 ? n + 1 : n + n / 16) {
+  for (long long n = 1; n <= most; n = n < 64 ? n + 1 : n < most ? std::min(n + n / 16, most) : n + 1) {
     double cost;
     if (packed) {
       const double more = n < longest ? (double)all / n : 0.0;  // segments beyond one a sequence
@@ -160,7 +160,8 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
   p.split = N > p.L;
   p.inner = packed ? (int)(tokens / p.L) : p.G - B;  // (an inner segment is a full one)
   p.splits = packed ? std::min(B, p.inner) : B;
-  p.bytes = kWorkspacePrefix + (p.split ? (size_t)nsum * p.G * H * d * d * sizeof(float) : 0);
+  p.W = packed ? (int)std::min<long long>(p.G, 2ll * p.inner) : p.G;  // (nseg <= 2 (nseg - 1))
+  p.bytes = kWorkspacePrefix + (p.split ? (size_t)nsum * p.W * H * d * d * sizeof(float) : 0);
   return p;
 }
 
@@ -197,6 +198,7 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
   a->G = plan->G;
   a->inner = plan->inner;
   a->split = plan->splits;
+  a->W = plan->W;
   a->seg = plan->split ? reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspacePrefix) : nullptr;
   a->status = &static_cast<WorkspaceHeader*>(ws)->status;
   return MHLA_OK;

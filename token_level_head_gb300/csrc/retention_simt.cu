@@ -115,7 +115,10 @@ __global__ void __launch_bounds__(kThreads, SimtTile<D>::kPerSm) retention_simt_
       if (a.pass[i].sum == (int)blockIdx.z && !a.pass[i].sum_t) z = i;
   const RetPass& p = a.pass[z];
   Segment sg = find_segment(a, g, SUM ? SEG_INNER : SEG_ALL, scratch);
-  if (sg.seq < 0) return;
+  if (sg.seq < 0) {
+    grid_dependency_wait();  // (a kernel does not end before those it may overlap)
+    return;
+  }
   const int reverse = p.reverse;
   if (SUM) inner_segment(a, sg, reverse);
   const int e0 = blockIdx.y * C::ES;
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, SimtTile<D>::kPerSm) retention_simt_
   fetch(0);
   const float lg = decay_log2(a.gamma[h]);
   const int tx = tid % C::NX, ty = tid / C::NX;
-  float* seg = a.seg == nullptr ? nullptr : a.seg + (((size_t)p.sum * a.G + sg.g0 + sg.seg) * a.H + h) * (D * D);
+  float* seg = a.seg == nullptr ? nullptr : a.seg + (((size_t)p.sum * a.W + sg.w0 + sg.seg) * a.H + h) * (D * D);
   int slot = -1;
   if (!SUM && a.states != nullptr) slot = ret_slot(a.slots, a.n_slots, sg.seq);
   {
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_c
   const int slot = sg.seq >= 0 && a.load && a.states != nullptr ? ret_slot(a.slots, a.n_slots, sg.seq) : -1;
   grid_dependency_wait();  // the sums are there
   if (sg.seq < 0) return;
-  const int nseg = sg.nseg, g0 = sg.g0, len = sg.all;
+  const int nseg = sg.nseg, len = sg.all;
   const int n = a.d * a.d, e0 = (blockIdx.y * E * kThreads + threadIdx.x) * V;
   const float lg = decay_log2(a.gamma[h]);
   const float wfull = decay_pow(lg, a.L), wlast = decay_pow(lg, len - (nseg - 1) * a.L);
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_c
     for (int i = 0; i < E; ++i)
       if (e0 + i * kThreads * V < n)
         x[i] = *reinterpret_cast<const Vec*>(a.states + ((size_t)slot * a.H + h) * n + e0 + i * kThreads * V);
-  float* w = a.seg + (((size_t)set * a.G + g0) * a.H + h) * n + e0;
+  float* w = a.seg + (((size_t)set * a.W + sg.w0) * a.H + h) * n + e0;
   constexpr int kAhead = E == 1 ? 16 : 2;  // segments loaded ahead
   for (int j0 = 0; j0 < nseg; j0 += kAhead) {
     Vec u[kAhead][E];

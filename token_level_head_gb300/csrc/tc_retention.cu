@@ -837,7 +837,6 @@ __device__ __noinline__ void carry_start(uint8_t* sm, PassBars* b, int warp, int
   const float* from = b->ctx.from;
   const bool from_t = b->ctx.from_t != 0;
   const float wl = x.over(0);
-  if (b->ctx.from_ws) grid_dependency_wait();
 #pragma unroll 2
   for (int k = 0; k < Carry<D>::kBlocks; ++k) {
     float2 v[8];  // (loads without branches between them)
@@ -904,7 +903,10 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
   const int z = blockIdx.x % r.npass;  // a head's passes side by side: they read the same tensors
   const int unit = blockIdx.x / r.npass, g = unit / r.H, h = unit % r.H;
   const Segment sg = find_segment(r, g, SEG_ALL, reinterpret_cast<int*>(b->decay));
-  if (sg.seq < 0) return;
+  if (sg.seq < 0) {
+    grid_dependency_wait();  // (a kernel does not end before those it may overlap)
+    return;
+  }
   const RetPass& p = r.pass[z];
   if (threadIdx.x == 0) {  // the barriers, what the producer needs, and the first loads
     for (int s = 0; s < kStages; ++s) {
@@ -979,6 +981,7 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (b->ctx.from_ws) grid_dependency_wait();  // the state entering the segment; no wait with a limit before it
 
   if (warp == kWarpProd) {
     if (lane == 0) pass_producer<D>(sm, b);
@@ -1159,7 +1162,7 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
     }
     if (ok && wait_warp(&b->fin, 0, gd) && !aborted(gd)) {
       tc_fence_after();
-      float* dst = r.seg + (((size_t)set * r.G + sg.g0 + sg.seg) * r.H + h) * d * d;
+      float* dst = r.seg + (((size_t)set * r.W + sg.w0 + sg.seg) * r.H + h) * d * d;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {  // 16 rows x 32 columns
         const int hh = D == 128 ? k / 2 : 0, c0 = 64 * half + 32 * (k % 2);
