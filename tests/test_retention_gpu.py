@@ -512,3 +512,151 @@ def test_wait_limit_gives_up_then_the_next_call_is_right():
         assert binding.mhla_query_status(ws) == binding.MHLA_OK
     check_forward(q, k, v, g, y, 1.0, "identity")
     check_backward(q, k, v, g, dy, grads, 1.0, "identity")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("feature", ["elu1", "exp"])
+@pytest.mark.parametrize("d", [16, 32, 128])
+def test_features_with_states_of_every_width(d, feature, dtype):
+    """A feature map under a returned state, in every chunk and for every decay."""
+    B, H, N = 2, 5, 430
+    q, k, v = (0.5 * rand((B, H, N, d), dtype, i) for i in range(3))
+    g, y, st = gammas(H), torch.empty(B, H, N, d, dtype=dtype, device="cuda"), rand((B, H, d, d), F32, 4)
+    start = st.clone()
+    lib.retention_forward(q, k, v, g, y, states=st, load_state=True, feature=feature, scale=0.5)
+    check_forward(q, k, v, g, y, 0.5, feature, start=start, final=st)
+
+
+def many(n, longest, seed):
+    """Offsets of n sequences of 0 .. 40 tokens, one of them of `longest`."""
+    lens = torch.randint(0, 41, (n,), generator=torch.Generator().manual_seed(seed))
+    lens[n // 3] = longest
+    return [3] + (3 + lens.cumsum(0)).tolist()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n", [64, 65, 700])
+def test_many_packed_sequences(n, dtype):
+    """More sequences than are put in order, and more than a block has threads; one is cut into segments."""
+    H, d, cu = 2, 64, many(n, 9000, n)
+    T = cu[-1] + 5
+    q, k, v, dy, y = (rand((1, H, T, d), dtype, i, "bnhd") for i in range(5))
+    before, c = y.clone(), torch.tensor(cu, dtype=torch.int32, device="cuda")
+    g = torch.tensor([1.0, 0.75], device="cuda")
+    pool = rand((n, H, d, d), F32, 6)
+    start = pool.clone()
+    slots = torch.randperm(n, generator=torch.Generator().manual_seed(n)).int().cuda()
+    lib.retention_forward(q, k, v, g, y, cu_seqlens=c, states=pool, slots=slots, load_state=True, scale=0.3)
+    ids = slots.long()
+    check_forward(q, k, v, g, y, 0.3, "identity", cu, start[ids], pool[ids])
+    assert torch.equal(y[:, :, :3], before[:, :, :3]) and torch.equal(y[:, :, cu[-1]:], before[:, :, cu[-1]:])
+    grads = [torch.empty_like(q) for _ in range(3)]
+    lib.retention_backward(q, k, v, g, dy, *grads, cu_seqlens=c, scale=0.3)
+    check_backward(q, k, v, g, dy, grads, 0.3, "identity", cu)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [32, 128])
+def test_packed_sequences_in_segments_with_states(d, dtype):
+    """Split and whole sequences in one call, states taken and left in place, one slot out of range and one
+    asked for twice; the same again bit for bit."""
+    H, cu = 2, [0, 100, 7000, 7000, 12500, 12501, 17000]
+    T, n = cu[-1], len(cu) - 1
+    q, k, v = (rand((1, H, T, d), dtype, i) for i in range(3))
+    g, y = torch.tensor([1 - 2.0 ** -10, 1.0], device="cuda"), torch.empty(1, H, T, d, dtype=dtype, device="cuda")
+    pool = rand((8, H, d, d), F32, 6)
+    start = pool.clone()
+    slots = torch.tensor([5, 2, 0, 7, 8, 2], dtype=torch.int32, device="cuda")
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    lib.retention_forward(q, k, v, g, y, cu_seqlens=c, states=pool, slots=slots, load_state=True, scale=0.2)
+    zero = torch.zeros_like(start[0])
+    check_forward(q, k, v, g, y, 0.2, "identity", cu, [start[5], start[2], start[0], start[7], zero, zero])
+    check_forward(q[:, :, :12500], k[:, :, :12500], v[:, :, :12500], g, y, 0.2, "identity", cu[:5],
+                  [start[i] for i in (5, 2, 0, 7)], [pool[i] for i in (5, 2, 0, 7)])
+    assert torch.equal(pool[[0, 1, 3, 4, 6]], start[[0, 1, 3, 4, 6]])
+    again, pool2 = torch.empty_like(y), start.clone()
+    lib.retention_forward(q, k, v, g, again, cu_seqlens=c, states=pool2, slots=slots, load_state=True, scale=0.2)
+    assert torch.equal(y, again) and torch.equal(pool, pool2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [100, 6000])
+def test_more_sequences_than_slots(N, dtype):
+    """No slot numbers: sequences behind the pool start from zero and keep nothing."""
+    B, H, d = 3, 1, 64
+    q, k, v = (rand((B, H, N, d), dtype, i) for i in range(3))
+    pool, y = rand((2, H, d, d), F32, 3), torch.empty(B, H, N, d, dtype=dtype, device="cuda")
+    start, g = pool.clone(), torch.tensor([0.999], device="cuda")
+    lib.retention_forward(q, k, v, g, y, states=pool, load_state=True)
+    check_forward(q, k, v, g, y, 1.0, "identity", start=[start[0], start[1], torch.zeros_like(start[0])])
+    check_forward(q[:2], k[:2], v[:2], g, y, 1.0, "identity", start=start, final=pool)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_a_captured_token_loop(dtype):
+    """A copy, a prompt and tokens in one graph: slots and offsets are read when it is replayed."""
+    H, d, T = 3, 64, 300
+    g = gammas(H)
+    x = [rand((1, H, T, d), dtype, i) for i in range(3)]
+    t = [rand((2, H, 1, d), dtype, 10 + i)[:, :, 0] for i in range(3)]
+    pool, y = torch.zeros(6, H, d, d, device="cuda"), torch.zeros(1, H, T, d, dtype=dtype, device="cuda")
+    out = torch.zeros(2, H, d, dtype=dtype, device="cuda")
+    ints = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (2, 2, 2, 3)]
+    src, dst, slots, cu = ints
+    ws = lib.new_workspace(lib.retention_workspace_bytes(2, H, T, d), "cuda")
+
+    def calls():
+        lib.retention_copy_states(pool, src, dst)
+        lib.retention_forward(*x, g, y, cu_seqlens=cu, states=pool, slots=slots, load_state=True, workspace=ws)
+        lib.retention_step(*t, g, pool, out, slots=slots)
+
+    calls()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for values in ([[3, -1], [0, 1], [0, 1], [0, 130, 300]], [[1, 1], [5, 2], [5, 2], [7, 7, 260]], [[9, 2], [4, 2], [-1, 2], [0, 300, 300]]):
+        fill = rand((6, H, d, d), F32, 30)
+        for a, b in zip(ints, values):
+            a.copy_(torch.tensor(b, dtype=torch.int32))
+        results = []
+        for run in (calls, graph.replay):
+            pool.copy_(fill)
+            y.zero_()
+            out.zero_()
+            run()
+            results.append([z.clone() for z in (pool, y, out)])
+        assert all(torch.equal(a, b) for a, b in zip(*results))
+        assert results[0][0].abs().sum() > 0 and results[0][2].abs().sum() > 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_two_streams_at_once(dtype):
+    """Calls of every entry on two streams given by name, side by side, workspaces left to the calls."""
+    H, d, N = 3, 64, 5000
+    g = torch.tensor([0.9, 0.999, 1.0], device="cuda")
+    x = [[rand((1, H, N, d), dtype, 10 * s + i) for i in range(4)] for s in range(2)]
+    src, dst = (torch.tensor([i], dtype=torch.int32, device="cuda") for i in range(2))
+
+    def buffers():
+        return [torch.zeros_like(x[0][0]) for _ in range(4)] + [torch.zeros(2, H, d, d, device="cuda"),
+                                                               torch.zeros(1, H, d, dtype=dtype, device="cuda")]
+
+    def calls(s, o, stream):
+        q, k, v, dy = x[s]
+        lib.retention_forward(q, k, v, g, o[0], states=o[4], scale=0.1, stream=stream)
+        lib.retention_backward(q, k, v, g, dy, *o[1:4], scale=0.1, stream=stream)
+        lib.retention_copy_states(o[4], src, dst, stream=stream)
+        lib.retention_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], g, o[4], o[5], scale=0.1, stream=stream)
+
+    want, got = [buffers(), buffers()], [buffers(), buffers()]
+    for s in range(2):
+        calls(s, want[s], None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for s in range(2):
+            calls(s, got[s], streams[s])
+        torch.full((1 << 20,), 0xff, dtype=torch.uint8, device="cuda")  # memory of this stream, not of those
+    torch.cuda.synchronize()
+    for a, b in zip(got[0] + got[1], want[0] + want[1]):
+        assert torch.equal(a, b)

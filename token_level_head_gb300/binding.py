@@ -492,10 +492,13 @@ def retention_workspace_bytes(B: int, H: int, tokens: int, d: int, backward: boo
     return int(load().retention_workspace_bytes(B, H, tokens, d, 1 if backward else 0))
 
 
-def _retention_workspace(workspace, B, H, N, d, packed, backward, dev):
-    """The caller's workspace or, where there is none, a new one (a tensor: it has to outlive the call)."""
+def _retention_workspace(workspace, B, H, N, d, packed, backward, dev, stream):
+    """The caller's workspace or, where there is none, a new one: zeroed on the call's stream and of that
+    stream's memory, so that neither the zeros nor a later owner of the memory can meet the call's kernels."""
     if workspace is None:
-        workspace = new_workspace(retention_workspace_bytes(B, H, N if packed else B * N, d, backward), dev)
+        nbytes = retention_workspace_bytes(B, H, N if packed else B * N, d, backward)
+        with torch.cuda.stream(stream):
+            workspace = new_workspace(nbytes, dev)
     return workspace
 
 
@@ -514,7 +517,7 @@ def retention_forward(q, k, v, gamma, y, *, cu_seqlens=None, states=None, slots=
     n_slots = _retention_states(states, slots, B, H, d)
     opt = _retention_options(feature, float(scale))
     dev = _retention_device((q, k, v, y), (gamma, cu_seqlens, states, slots, workspace))
-    ws = _retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, False, dev)
+    ws = _retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, False, dev, stream)
     _retention_call("retention_forward", dev,
                     (*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), gamma.data_ptr(), *_strided(y, "y"),
                      B, H, N, d, _address(cu_seqlens), _address(states), _address(slots), n_slots,
@@ -531,7 +534,7 @@ def retention_backward(q, k, v, gamma, dy, dq, dk, dv, *, cu_seqlens=None, scale
     _expect_fast(gamma, "gamma", (H,), torch.float32)
     opt = _retention_options(feature, float(scale))
     dev = _retention_device((q, k, v, dy, dq, dk, dv), (gamma, cu_seqlens, workspace))
-    ws = _retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, True, dev)
+    ws = _retention_workspace(workspace, B, H, N, d, cu_seqlens is not None, True, dev, stream)
     _retention_call("retention_backward", dev,
                     (*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), gamma.data_ptr(), *_strided(dy, "dy"),
                      *_strided(dq, "dq"), *_strided(dk, "dk"), *_strided(dv, "dv"), B, H, N, d, _address(cu_seqlens),
