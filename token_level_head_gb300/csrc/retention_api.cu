@@ -117,15 +117,18 @@ struct Plan {
 //   split  (rounds) (n + start) sum  +  a state for each segment, written and read by the sums' kernel, the scan and
 //          the pass  +  two more launches
 // where a round is `slots` blocks.  Packed sequences, of unknown lengths, take their work over the slots and half a
-// block for the tail; four times the mean counts as their longest.  The costs are measured ones: a chunk takes 3.3 us
-// at d = 128 and 3.8 us at d = 64 (two blocks an SM), a block 2.5 chunks to start, the sum of a chunk 0.45 of its
-// pass, a segment's state 2 chunks, two launches 8 us; fp32 (SIMT; 128 tokens) 10 us a chunk.  A bf16 block that
+// block for the tail; four times the mean counts as their longest.  The costs are measured ones: a chunk takes 3.1 us
+// (d = 64: in each of two blocks an SM), a block 2.5 chunks to start, the sum of a chunk 0.45 of its
+// pass, a segment's state 2 chunks, two launches 8 us; fp32 (SIMT; 128 tokens) 10 us a chunk.  What it picks is within
+// 3 % of the best of a sweep of n for the long prompts and gradients tried (8 heads of 65,536 tokens: 159 us, others
+// 165 to 214; 64 heads of 8192: 101 us, others 106 to 130; 24 packed sequences of 20,011 tokens: 138 us, others 136 to
+// 171; gradients of 64 heads of 4096 tokens: 104 us, others 112 to 136).  A bf16 block that
 // returns a state (exact) takes half as long again for about 8 chunks: its segment, the last one, is better short.
 Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward, bool exact) {
   const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
   const double slots = f32 ? 152.0 * (d == 128 ? 1 : d == 64 ? 2 : 4) : d == 128 ? 152.0 : 304.0;
-  const double fixed = 8.0 / (f32 ? 10.0 : d == 128 ? 3.3 : 3.8);
+  const double fixed = 8.0 / (f32 ? 10.0 : 3.1);
   const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.5 : 2.0;
   const double slow = exact && !f32 ? 0.5 : 0.0;
   const int cols = f32 && d == 128 ? 2 : 1;  // blocks that share a segment

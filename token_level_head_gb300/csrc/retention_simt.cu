@@ -17,8 +17,9 @@ constexpr int kTok = 64;  // tokens of a chunk
 //   P = (A B^T) gamma^(t-s), masked;  out = P C + gamma^(i+1) A X;  X = gamma^len X + (B w)^T C,
 // w_s = gamma^(len-1-s), with X [D][ES] and the chunk's A, B, C and P in shared memory and 4 x 4 (X: up to 8 x 4)
 // register tiles; the masked half of the first two products is left out by blocks of 4 rows.  With SUM only X is
-// formed: the segment's own sum.  Bound by fp32 FMA issue and the latency of shared memory: the multiply-adds go in
-// pairs, the next chunk's rows are on their way in registers while this one is computed.
+// formed: the segment's own sum.  Bound by fp32 FMA issue and the latency of shared memory (12 heads of 4096 tokens, d = 64: 96 us, the pass 72 of
+// them; FMA units 30 % busy, 10 warps an SM on average): the multiply-adds go in pairs, the next chunk's rows are on
+// their way in registers while this one is computed.
 template <int D>
 struct SimtTile {
   static constexpr int ES = D < 64 ? D : 64;
@@ -296,7 +297,9 @@ cudaError_t launch_passes(const RetArgs& a, cudaStream_t st) {
 // ================================================================ scan
 // A thread carries E groups of V elements of a head's state over its sequence's segments, in the pass's direction:
 // the slot of a segment holds the segment's own sum before, the state entering it after.  V = E = 4 where there are
-// many heads (most packed sequences have one segment, and their blocks end at once), single elements where few.
+// many heads (most packed sequences have one segment, and their blocks end at once), single elements where few: calls
+// with 24 packed sequences x 16 heads 136 us, 151 with single elements, with 64 heads of 8192 tokens 101 and 103;
+// with 8 heads of 65,536 171 and 161, with 12 heads of 4096 fp32 103 and 99.  Bound by the loads' latency: 8 us.
 template <int V, int E>
 __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_constant__ RetArgs a) {
   __shared__ int scratch[2 * kOrdered];
@@ -357,7 +360,9 @@ __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_c
 // ================================================================ single-token step
 // S = gamma S + phi(k) v^T, out = scale phi(q) S.  A block takes ES columns of a (row, head) state; a thread RPT
 // neighbouring rows of four columns, all its loads issued before the first use; the columns' sums over c go through
-// shuffles and shared memory.  Bound by the state's traffic (8 d^2 bytes a head).
+// shuffles and shared memory.  At most 16 elements a thread, so that six blocks fit on an SM: d = 128 takes its columns
+// in four blocks.  Bound by the state's traffic (8 d^2 bytes a head): 256 x 16 heads, d = 64, 24.6 us = 5.5 TB/s, 82 %
+// of a copy's rate; a few rows by the launch: 4 us for 3 x 16 heads, d = 128.
 template <typename T, int N>
 __device__ __forceinline__ void load_values(const T* p, float* f) {
   if constexpr (N % 4 == 0) {
@@ -451,7 +456,7 @@ cudaError_t launch_step_d(int B, int H, int d, const RetTensor& q, const RetTens
 // targets, so that a slot may be source and target of different pairs in any order.  A source of several pairs is read
 // once.  Asynchronous copies keep a part in flight, and two blocks an SM take parts until none is left, one reading
 // while the other writes; the pairs are compared once a block (with a block a part that was half of the time: 160
-// moves of 1 MB took 119 us).
+// moves of 1 MB took 121 us, now 64: 325 MB at 5.1 TB/s, 75 % of a copy's rate).
 constexpr int kCopyBytes = 100 * 1024;  // of shared memory a block, so that two are on an SM: one reads, one writes
 
 __device__ __forceinline__ void copy_async16(void* smem, const void* gmem) {

@@ -23,10 +23,13 @@
 //                quarter of the rows, with half of the scores and of the columns each
 //   4 W warps    feature maps in place, B w
 //   X warps      X and its bf16 tile for the next chunk: eight (D = 128), or the W warps themselves (D = 64)
-// A chunk's B w does not wait for the X that enters it, so the serial chain from one X to the next is
-// inter, intra, dX and the update.  What this costs is shared memory's bandwidth: with D = 128 a chunk's
-// products read 2.5 thousand cycles' worth of it (128 bytes a cycle; 128 x 128 x 16 from shared memory
-// takes 64 cycles, twice the tensor cores' time), TMA writes 0.8, B w 1.3, X and the scores' weights 0.6.
+// What bounds it: chains of short steps, not a pipe.  With D = 128 a chunk takes about 6 thousand cycles an SM; its
+// products need 2.6 of the tensor cores (128 x 128 x 16: 64 cycles) and about 4.4 thousand of shared memory's bandwidth
+// (128 bytes a cycle: the products' operands 2.3, TMA 0.8, B w 0.8, X and the scores' weights 0.6).  Two chains run
+// beside each other: scores, P, intra, out (the out warps are busy nearly all of it), and dX, X, inter.  With D = 64
+// a chunk takes 4.5 thousand cycles in one CTA, 6 thousand in each of two on an SM; the instruction issue is at 34 %,
+// the tensor cores at 25 %, HBM at 45 %.  Measured for prompts: 8 heads of 65,536 tokens, d = 128, 97 us of the call's
+// 153 (1.07 GB in all: 61 % of HBM's rate in the pass); 4 x 16 heads of 8192 tokens, d = 64, 65 us of 96.
 //
 // The roles' loops are kept short and free of branches: with whole rows unrolled the instruction fetch,
 // not the arithmetic, set the pace (23,000 cycles a chunk), and stores of one row a thread held up the
@@ -438,24 +441,23 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
   const Desc bk0 = make_desc(smem_u32(sm + P::kOffBC), 16, 1024);
   const Desc bm0 = make_desc(smem_u32(sm + P::kOffBC), kAtom, 1024);
   const Desc lo = make_desc(smem_u32(sm + P::kOffLo), kAtom, 1024), lo2 = make_desc(smem_u32(sm + P::kOffX), kAtom, 1024);
-  int maps = 0;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const int s = i % kStages;
-    const uint32_t at = s * (2 * P::kOp >> 4);  // the stage
-    const Desc bk{bk0.lo + at, bk0.hi}, bm{bm0.lo + at, bm0.hi}, cm{bm0.lo + at + (P::kOp >> 4), bm0.hi};
-    if (!wait_warp(&b->full[s], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return;
-    if (i > 0 && !wait_warp(&b->o_full, (i - 1) & 1, gd)) return;  // the scores go over P of the last chunk
+  auto stage = [&](Desc d, int i) {  // of chunk i
+    d.lo += (i % kStages) * (2 * P::kOp >> 4);
+    return d;
+  };
+  const Desc cm0{bm0.lo + (P::kOp >> 4), bm0.hi};
+  int maps = 0;  // chunks whose operands the W warps have changed
+  auto scores = [&](int i) {
+    if (!wait_warp(&b->full[i % kStages], (i / kStages) & 1, gd) || !wait_warp(&b->a_full, i & 1, gd)) return false;
     if (mapped || chunk_len(chunk_of(i, n, reverse), len) < kTok) {
-      if (!wait_warp(&b->mapped, maps & 1, gd)) return;
+      if (!wait_warp(&b->mapped, maps & 1, gd)) return false;
       ++maps;
     }
-    if (D == 64 && i > 0 && !wait_warp(&b->o_free, (i - 1) & 1, gd)) return;  // (and over intra)
-    if (i > exact && !wait_warp(&b->x_full, i & 1, gd)) return;               // (and over the last dX)
     tc_fence_after();
     __syncwarp();
     if (elect_one()) {
       constexpr uint32_t kId = idesc_bf16_f32(128, 128, 0, 0);
+      const Desc bk = stage(bk0, i);
       mma_ss<kId, false>(tmem + P::kColS, qa, 0, bk, 0);
 #pragma unroll
       for (int k = 1; k < D / 16; ++k) {
@@ -464,6 +466,13 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
       }
       mma_commit(&b->s_full);
     }
+    return true;
+  };
+  if (!scores(0)) return;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int s = i % kStages;
+    const Desc cm = stage(cm0, i);
     if (!wait_warp(&b->x_full, i & 1, gd)) return;
     if (D != 64 && i > 0 && !wait_warp(&b->o_free, (i - 1) & 1, gd)) return;
     tc_fence_after();
@@ -492,16 +501,23 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
       mma_commit(&b->o_full);
       if (i >= nx) mma_commit(&b->empty[s]);
     }
+    const bool more = i + 1 < n, apart = i >= exact && i < nx;
+    // The next chunk's scores go over P, with D = 64 over intra too, so behind the intra (the out warps) of this one.
+    // D = 64: the longest chain is scores, P, intra, out; this chunk's dX comes behind the scores (gradients of 64 heads
+    // of 4096 tokens: 104 us, 107 the other way).  D = 128: it is dX, X, inter; dX comes first (8 heads of 65,536
+    // tokens: 156 us, 169 the other way).
+    // (w_full: the W warps have passed s_full, which may go on.)
+    if (i < nx && !wait_warp(&b->w_full, i & 1, gd)) return;
+    if (D == 64 && more && !apart && (!wait_warp(&b->o_free, i & 1, gd) || !scores(i + 1))) return;
     if (i < nx) {
-      if (!wait_warp(&b->w_full, i & 1, gd)) return;
-      if (i >= exact && D == 128 && !wait_warp(&b->w2_full, (i - exact) & 1, gd)) return;
-      if (i >= exact && !wait_warp(&b->o_full, i & 1, gd)) return;  // P has been read
+      if (apart && (!wait_warp(&b->o_full, i & 1, gd) || (D == 128 && !wait_warp(&b->w2_full, (i - exact) & 1, gd)))) return;
+      const Desc bm = stage(bm0, i);
       tc_fence_after();
       __syncwarp();
       if (elect_one()) {
-        if (i >= exact) {
-          // The accumulator rounds towards zero at each of these: dX is added up by itself and then, in fp32, to X.
-          // (On top of X the state of 4,000 tokens was off by 2^-19, so by 2^-21.)
+        if (apart) {
+          // The accumulator rounds towards zero at each of these: dX is added up by itself, over P, and then, in fp32,
+          // to X.  (On top of X the state of 4,000 tokens was off by 2^-19, so by 2^-21.)
           constexpr int kN = D == 128 ? 128 : 32;
 #pragma unroll
           for (int e = 0; e < D; e += kN) {
@@ -517,11 +533,14 @@ __device__ __noinline__ void pass_mma(uint8_t* sm, PassBars* b) {
         mma_commit(&b->empty[s]);
       }
     }
+    if (more && (D == 128 || apart)) {
+      if (!wait_warp(&b->o_full, i & 1, gd) || (D == 64 && !wait_warp(&b->o_free, i & 1, gd))) return;
+      if (apart && !wait_warp(&b->x_full, (i + 1) & 1, gd)) return;  // (dX has been read)
+      if (!scores(i + 1)) return;
+    }
   }
 }
 
-// Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  The two warps of a quadrant take
-// half of the scores and of the output columns each.
 // 16 lanes x 32 columns: registers 4 g + {0, 1} are columns 8 g + 2 (l % 4) + {0, 1} of row l / 4, 4 g + {2, 3}
 // those of row l / 4 + 8.
 __device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float* v) {
@@ -563,19 +582,23 @@ __device__ __forceinline__ void turn4(uint32_t* e, int lane) {
   }
 }
 
+// Out warps, TMEM lane quadrant = warp % 4, token row t = a lane.  The two warps of a quadrant take half of the scores
+// and of the output columns each.  What does not change is kept out of the loop: with D = 128 three instructions more
+// for each store cost 7 % of a call of 8 heads of 65,536 tokens (156 -> 167 us).
 template <int D, bool DERIV>
 __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
   using P = PassTile<D>;
   const int qd = warp & 3, row = 32 * qd + lane, half = (warp - kWarpOut) >> 2;
-  const int n = b->ctx.n, all = b->ctx.len, reverse = b->ctx.reverse, row0 = b->ctx.row0, xf = b->ctx.fx;
-  const int d0 = half * (D / 2), d1 = min(b->ctx.d, d0 + D / 2);
+  const int n = b->ctx.n, all = b->ctx.len, reverse = b->ctx.reverse;
+  const int d0 = half * (D / 2);
   const uint32_t tl = b->tbase + ((uint32_t)(32 * qd) << 16);
-  const float gamma = decay_pow(b->ctx.lg, 1);
-  const long long sn = b->ctx.out_n, xsn = b->ctx.x_n;
-  __nv_bfloat16* out = b->ctx.out;
-  const __nv_bfloat16* xin = b->ctx.x;
   const Guard gd = make_guard(&b->abort, b->ctx.wait_ns);
   const float* decay = b->decay + (reverse ? kTok - 1 : 32);  // [t - s]: its weight, 0 on the masked side
+  // out: this lane's rows rw, rw + 8, .. of a chunk, and the first of its columns once they are turned round
+  const int rw = 32 * qd + (lane >> 2);
+  long long sn8 = 8 * b->ctx.out_n;
+  __nv_bfloat16* out = b->ctx.out + (long long)(b->ctx.row0 + chunk_of(0, n, reverse) * kTok + rw) * b->ctx.out_n + d0 + 8 * (lane & 3);
+  const int room = min(b->ctx.d, d0 + D / 2) - d0 - 8 * (lane & 3);  // columns from there on
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int ch = chunk_of(i, n, reverse), len = chunk_len(ch, all);
@@ -611,23 +634,26 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
 
     if (!wait_warp(&b->o_full, i & 1, gd)) return;
     tc_fence_after();
-    // 16 rows and 32 columns at a time: lane l holds columns 8 g + 2 (l % 4) + {0, 1} of rows l / 4 and l / 4 + 8;
+    // 16 rows and 32 columns at a time: lane l holds columns 8 g + 2 (l % 4) + {0, 1} of rows l / 4 and l / 4 + 8
+    // D = 64: the next scores go over intra, so everything is read before anything is stored (gradients of 64 heads of
+    // 4096 tokens 115 -> 107 us); D = 128 has columns for both, and no registers to hold the rows (8 heads of 65,536
+    // tokens 165 -> 190 us)
+    constexpr bool kHold = D == 64 && !DERIV;
+    uint32_t e[kHold ? 2 : 1][2][4];
     // the four lanes of a row turn their pairs round, so that each has 8 columns in a row and they store 64 bytes
-#pragma unroll 1
+    auto store = [&](int hh, int cc, int k) {
+      uint32_t* p = e[kHold ? hh : 0][k];
+      turn4(p, lane);
+      if (rw + 16 * hh + 8 * k < len && (kHold ? d0 + 8 * (lane & 3) < b->ctx.d : cc < room))
+        *reinterpret_cast<uint4*>(out + (2 * hh + k) * sn8 + cc) = make_uint4(p[0], p[1], p[2], p[3]);
+    };
+    const float gamma = decay_pow(b->ctx.lg, 1);
+    const float* wt = b->decay + (reverse ? kTok - len + rw : 32 + rw);
+#pragma unroll(kHold ? 2 : 1)
     for (int hh = 0; hh < 2; ++hh) {
       float wi[2];
-      bool live[2];
-      __nv_bfloat16* dst[2];
-      const __nv_bfloat16* xp[2] = {nullptr, nullptr};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rw = 32 * qd + 16 * hh + 8 * k + (lane >> 2);
-        const long long at = (long long)(row0 + ch * kTok + rw);
-        live[k] = rw < len;
-        wi[k] = live[k] ? gamma * b->decay[reverse ? kTok - len + rw : 32 + rw] : 0.f;
-        dst[k] = out + at * sn + d0 + 8 * (lane & 3);
-        if (DERIV) xp[k] = xin + at * xsn + d0 + 2 * (lane & 3);
-      }
+      for (int k = 0; k < 2; ++k) wi[k] = rw + 16 * hh + 8 * k < len ? gamma * wt[16 * hh + 8 * k] : 0.f;
 #pragma unroll
       for (int cc = 0; cc < D / 2; cc += 32) {
         float u[16], v[16];
@@ -637,34 +663,43 @@ __device__ __noinline__ void pass_out(PassBars* b, int warp, int lane) {
         uint32_t xx[2][4];
         if (DERIV) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < 2; ++k) {
+            const int t = rw + 16 * hh + 8 * k;
+            const __nv_bfloat16* xp = b->ctx.x + (long long)(b->ctx.row0 + ch * kTok + t) * b->ctx.x_n + d0 + cc + 2 * (lane & 3);
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-              xx[k][g] = live[k] && d0 + cc + 8 * g < d1 ? *reinterpret_cast<const uint32_t*>(xp[k] + cc + 8 * g) : 0u;
+              xx[k][g] = t < len && d0 + cc + 8 * g < b->ctx.d ? *reinterpret_cast<const uint32_t*>(xp + 8 * g) : 0u;
+          }
         }
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t e[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             float2 o = fma2(make_float2(wi[k], wi[k]), make_float2(u[4 * g + 2 * k], u[4 * g + 2 * k + 1]),
                             make_float2(v[4 * g + 2 * k], v[4 * g + 2 * k + 1]));
             if (DERIV) {
-              o.x *= ret_dphi(__uint_as_float(xx[k][g] << 16), xf);
-              o.y *= ret_dphi(__uint_as_float(xx[k][g] & 0xffff0000u), xf);
+              o.x *= ret_dphi(__uint_as_float(xx[k][g] << 16), b->ctx.fx);
+              o.y *= ret_dphi(__uint_as_float(xx[k][g] & 0xffff0000u), b->ctx.fx);
             }
-            e[g] = pack_bf16(o.x, o.y);
+            e[kHold ? hh : 0][k][g] = pack_bf16(o.x, o.y);
           }
-          turn4(e, lane);
-          if (live[k] && d0 + cc + 8 * (lane & 3) < d1)
-            *reinterpret_cast<uint4*>(dst[k] + cc) = make_uint4(e[0], e[1], e[2], e[3]);
+          if (!kHold) store(hh, cc, k);
         }
       }
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b->o_free);
+    if (kHold) {
+      sn8 = 8 * b->ctx.out_n;
+      out = b->ctx.out + (long long)(b->ctx.row0 + ch * kTok + rw) * b->ctx.out_n + d0 + 8 * (lane & 3);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) store(hh, 0, k);
+    }
+    if (!kHold) out += reverse ? -16 * sn8 : 16 * sn8;
   }
 }
 
@@ -1024,14 +1059,18 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
 // ================================================================ segment sums
 // A segment's own sum of gamma^(distance to its end) b c^T: B w, with the distance counted to the segment's
 // end, is added up by the tensor cores over all its chunks.  B w is a sum of two bf16 numbers: the sums
-// reach a returned fp32 state only behind the last segment's decay.
+// reach a returned fp32 state only behind the last segment's decay.  Bound by HBM where the segments fill the SMs (8
+// heads of 65,536 tokens, d = 128: 43 us, 91 % of a copy's rate), else by a block's chain load, B w, products: 1.4 us
+// a chunk (64 heads of 8192 tokens, d = 64: 192 blocks, 25 us, 60 % of that rate).  A row of B is shared by D / 32
+// threads and the second part's product goes first, so that the next chunk's B w runs beside the first part's: 53
+// -> 43 us and 28 -> 25 us together.
 template <int D>
 struct SumTile {
   static constexpr int kStages = 3;                     // chunks of B and C in flight
   static constexpr int kOp = (D / 64) * kAtom;
   static constexpr int kOffLo = kStages * 2 * kOp;      // the second part of B w
   static constexpr int kOffBars = kOffLo + kOp;
-  static constexpr int kSplit = D / 64;                 // threads that share a row of B
+  static constexpr int kSplit = D / 32;                 // threads that share a row of B
   static constexpr int kThreads = 32 * (kWarpOut + 4 * kSplit);
   static constexpr int kPerSm = D == 128 ? 1 : 2;
 };
@@ -1039,6 +1078,7 @@ struct SumTile {
 template <int D>
 struct SumBars {
   uint64_t full[SumTile<D>::kStages], empty[SumTile<D>::kStages], ready[SumTile<D>::kStages];
+  uint64_t lo_free;  // the second part's tile has been read
   uint64_t fin;
   uint32_t tbase;
   int abort;
@@ -1075,6 +1115,7 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
       mbar_init(&b->empty[s], 1);
       mbar_init(&b->ready[s], 4 * P::kSplit);
     }
+    mbar_init(&b->lo_free, 1);
     mbar_init(&b->fin, 1);
     b->abort = 0;
     b->issued = 0;
@@ -1123,11 +1164,13 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
       const Desc bm{b0.lo + s * (2 * P::kOp >> 4), b0.hi}, cm{bm.lo + (P::kOp >> 4), b0.hi};
       __syncwarp();
       if (elect_one()) {
+        // the second part first: its tile has to be free for the next chunk
         if (i == 0)
-          mma_outer<D, D, false>(tmem, bm, cm);
+          mma_outer<D, D, false>(tmem, dlo, cm);
         else
-          mma_outer<D, D, true>(tmem, bm, cm);
-        mma_outer<D, D, true>(tmem, dlo, cm);
+          mma_outer<D, D, true>(tmem, dlo, cm);
+        mma_commit(&b->lo_free);
+        mma_outer<D, D, true>(tmem, bm, cm);
         mma_commit(&b->empty[s]);
       }
       __syncwarp();
@@ -1144,8 +1187,7 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
     for (int i = 0; i < n; ++i) {
       const int s = i % P::kStages, at = i * kTok + row, len = min(kTok, all - i * kTok);
       ok = wait_warp(&b->full[s], (i / P::kStages) & 1, gd);
-      // the second part's tile has been read by the MMAs of the chunk before
-      if (ok && i > 0) ok = wait_warp(&b->empty[(i - 1) % P::kStages], ((i - 1) / P::kStages) & 1, gd);
+      if (ok && i > 0) ok = wait_warp(&b->lo_free, (i - 1) & 1, gd);
       if (!ok) break;
       uint8_t* st = sm + s * 2 * P::kOp;
       if (half == 0) {  // (the operands of a whole row: rarely)
@@ -1153,9 +1195,9 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
       }
       const float w = row < len ? decay_pow(lg, reverse ? at : all - 1 - at) : 0.f;
       if (fb != kFeatIdentity || len < kTok)
-        weigh_phi_row2<64>(st, lo, row, 8 * half, w, d, fb);
+        weigh_phi_row2<32>(st, lo, row, 4 * half, w, d, fb);
       else
-        weigh_row2<64>(st, lo, row, 8 * half, w);
+        weigh_row2<32>(st, lo, row, 4 * half, w);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->ready[s]);
@@ -1164,8 +1206,8 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
       tc_fence_after();
       float* dst = r.seg + (((size_t)set * r.W + sg.w0 + sg.seg) * r.H + h) * d * d;
 #pragma unroll 1
-      for (int k = 0; k < D / 32; ++k) {  // 16 rows x 32 columns
-        const int hh = D == 128 ? k / 2 : 0, c0 = 64 * half + 32 * (k % 2);
+      for (int hh = 0; hh < D / 64; ++hh) {  // 16 rows x 32 columns
+        const int c0 = 32 * half;
         const int r0 = (D == 128 ? 32 * qd + 16 * hh : 16 * qd) + (lane >> 2);
         float v[16];
         tmem_ld16x32(tmem + ((uint32_t)(32 * qd + 16 * hh) << 16) + c0, v);
