@@ -393,8 +393,8 @@ def _retention_options(feature, scale):
 
 
 @functools.lru_cache(maxsize=1024)
-def _c_strides(b, h, n):
-    return ctypes.byref(_Strides(b, h, n))
+def _c_strides(st):
+    return ctypes.byref(_Strides(st[0], st[1], st[2] if len(st) == 4 else 0))
 
 
 def _strided(t, name):
@@ -402,7 +402,7 @@ def _strided(t, name):
     st = t.stride()
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {st[-1]}")
-    return t.data_ptr(), _c_strides(st[0], st[1], st[2] if len(st) == 4 else 0)
+    return t.data_ptr(), _c_strides(st)
 
 
 def _address(t):
@@ -419,23 +419,23 @@ def _expect_like(q, *named):
 
 def _retention_device(tokens, others):
     """The one CUDA device of all tensors; ``others`` (not the token tensors) must be contiguous."""
-    dev = tokens[0].device
+    index = tokens[0].get_device()  # -1: not a CUDA tensor
     for t in tokens:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if t.device != dev:
-            raise ValueError(f"tensor on {t.device}, expected {dev} (the device of q)")
+        if t.get_device() != index or index < 0:
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA tensors")
+            raise ValueError(f"tensor on {t.device}, expected {tokens[0].device} (the device of q)")
     for t in others:
-        if t is not None:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError("tensors must be contiguous CUDA tensors")
-            if t.device != dev:
-                raise ValueError(f"tensor on {t.device}, expected {dev} (the device of q)")
-    return dev
+            raise ValueError(f"tensor on {t.device}, expected {tokens[0].device} (the device of q)")
+    return tokens[0].device
 
 
 # the current stream's handle without a Stream object around it, where this torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _retention_call(name, dev, args, stream):
@@ -445,7 +445,7 @@ def _retention_call(name, dev, args, stream):
     else:
         handle = _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):

@@ -29,7 +29,7 @@
 // beside each other: scores, P, intra, out (the out warps are busy nearly all of it), and dX, X, inter.  With D = 64
 // a chunk takes 4.5 thousand cycles in one CTA, 6 thousand in each of two on an SM; the instruction issue is at 34 %,
 // the tensor cores at 25 %, HBM at 45 %.  Measured for prompts: 8 heads of 65,536 tokens, d = 128, 97 us of the call's
-// 153 (1.07 GB in all: 61 % of HBM's rate in the pass); 4 x 16 heads of 8192 tokens, d = 64, 65 us of 96.
+// 153 (537 MB at 5.5 TB/s); 4 x 16 heads of 8192 tokens, d = 64, 65 us of 96 (268 MB at 4.1 TB/s).
 //
 // The roles' loops are kept short and free of branches: with whole rows unrolled the instruction fetch,
 // not the arithmetic, set the pace (23,000 cycles a chunk), and stores of one row a thread held up the
