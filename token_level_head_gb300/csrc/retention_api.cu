@@ -117,21 +117,27 @@ struct Plan {
 //   split  (rounds) (n + start) sum  +  a state for each segment, written and read by the sums' kernel, the scan and
 //          the pass  +  two more launches
 // where a round is `slots` blocks.  Packed sequences, of unknown lengths, take their work over the slots and half a
-// block for the tail; four times the mean counts as their longest.  The costs are measured ones: a chunk takes 3.1 us
-// (d = 64: in each of two blocks an SM), a block 2.5 chunks to start, the sum of a chunk 0.45 of its
-// pass, a segment's state 2 chunks, two launches 8 us; fp32 (SIMT; 128 tokens) 10 us a chunk.  What it picks is within
-// 3 % of the best of a sweep of n for the long prompts and gradients tried (8 heads of 65,536 tokens: 159 us, others
-// 165 to 214; 64 heads of 8192: 101 us, others 106 to 130; 24 packed sequences of 20,011 tokens: 138 us, others 136 to
-// 171; gradients of 64 heads of 4096 tokens: 104 us, others 112 to 136).  A bf16 block that
-// returns a state (exact) takes half as long again for about 8 chunks: its segment, the last one, is better short.
+// block for the tail; four times the mean counts as their longest.  The costs are measured ones.  bf16: a chunk takes
+// 3.1 us (d = 64: in each of two blocks an SM), a block 2.5 chunks to start, the sum of a chunk 0.45 of its pass, a
+// segment's state 2 chunks, two launches 8 us; a block that returns a state (exact) takes half as long again for about
+// 8 chunks: its segment, the last one, is better short.  fp32: a chunk takes 26 us (two blocks an SM, but d = 128; a
+// third one waits, one by itself takes 0.86 of that), a block 0.3 chunks to start, a sum 0.35.
+// What it picks is within 3 % of the best of a sweep of n: 8 heads of 65,536 tokens 159 us, others 165 to 214; 64 heads
+// of 8192 101 us, others 106 to 130; 24 packed sequences of 20,011 tokens 138 us, others 136 to 171; gradients of 64
+// heads of 4096 tokens 104 us, others 112 to 136; fp32: 12 heads of 4096 tokens 91 us for n = 1, 97 for 2, 128 for 3;
+// 24 heads of 6000 194, 183, 214, 175, 280 us for n = 1, 2, 3, 4, 8.
 Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward, bool exact) {
   const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
-  const double slots = f32 ? 152.0 * (d == 128 ? 1 : d == 64 ? 2 : 4) : d == 128 ? 152.0 : 304.0;
-  const double fixed = 8.0 / (f32 ? 10.0 : 3.1);
-  const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.5 : 2.0;
+  const double slots = d == 128 ? 152.0 : 304.0;
+  const double fixed = 8.0 / (f32 ? 26.0 : 3.1);
+  const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.2 : 2.0;
   const double slow = exact && !f32 ? 0.5 : 0.0;
   const int cols = f32 && d == 128 ? 2 : 1;  // blocks that share a segment
+  const auto rounds = [&](double blocks) {
+    if (!f32 || d == 128) return std::ceil(blocks / slots);
+    return blocks <= slots / 2 ? 0.86 : std::ceil(2 * blocks / slots) / 2;
+  };
   const long long all = (tokens + 127) / 128, most = ((long long)N + 127) / 128;
   const double longest = packed ? std::min<double>((double)most, 4.0 * all / B) : (double)most;
   double best = 1e300;
@@ -146,9 +152,9 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
     } else {
       const long long segs = (most + n - 1) / n;
       const double blocks = (double)B * H * segs * cols, rest = (double)(most - (segs - 1) * n), end = rest + slow * std::min(rest, 8.0);
-      cost = std::ceil(blocks * npass / slots) * (std::max((double)std::min(n, most), end) + start);
+      cost = rounds(blocks * npass) * (std::max((double)std::min(n, most), end) + start);
       if (segs > 1)
-        cost += std::ceil((double)B * H * (segs - 1) * cols * nsum / slots) * (n + start) * sum + fixed +
+        cost += rounds((double)B * H * (segs - 1) * cols * nsum) * (n + start) * sum + fixed +
                 (double)B * H * segs * nsum * state / slots;
     }
     if (cost < best) {

@@ -17,9 +17,10 @@ constexpr int kTok = 64;  // tokens of a chunk
 //   P = (A B^T) gamma^(t-s), masked;  out = P C + gamma^(i+1) A X;  X = gamma^len X + (B w)^T C,
 // w_s = gamma^(len-1-s), with X [D][ES] and the chunk's A, B, C and P in shared memory and 4 x 4 (X: up to 8 x 4)
 // register tiles; the masked half of the first two products is left out by blocks of 4 rows.  With SUM only X is
-// formed: the segment's own sum.  Bound by fp32 FMA issue and the latency of shared memory (12 heads of 4096 tokens, d = 64: 96 us, the pass 72 of
-// them; FMA units 30 % busy, 10 warps an SM on average): the multiply-adds go in pairs, the next chunk's rows are on
-// their way in registers while this one is computed.
+// formed: the segment's own sum.  Bound by shared memory: 8 loads of 16 bytes a lane, four cycles each, for 32 multiply-adds of pairs (12 heads of 4096
+// tokens, d = 64: 87 us; FMA units 30 % busy).  The multiply-adds go in pairs; the next chunk's rows are on their way in
+// registers while X is computed.  (C and X transposed, so that pairs lie side by side, cost more in their stores and
+// uneven loads than it saved: 124 us against 97.)
 template <int D>
 struct SimtTile {
   static constexpr int ES = D < 64 ? D : 64;
@@ -78,7 +79,7 @@ struct Fetch {
 // acc[i][0 .. 3] += sum over k of a[i][k] b[k][0 .. 3], k = 0 .. n - 1 (n a multiple of 4): rows of a LDA apart, of b LDB.
 template <int R, int LDA, int LDB>
 __device__ __forceinline__ void outer_rows(float2 (&acc)[R][2], const float* a, const float* b, int k0, int n) {
-#pragma unroll 2
+#pragma unroll 4
   for (int k = k0; k < n; k += 4) {
     float4 fa[R];
 #pragma unroll
@@ -159,13 +160,12 @@ __global__ void __launch_bounds__(kThreads, SimtTile<D>::kPerSm) retention_simt_
     fC.store(sC, p.c.feature, len);
     if (tid < kTok) sW[tid] = tid < len ? decay_pow(lg, reverse ? tid : len - 1 - tid) : 0.f;
     __syncthreads();
-    if (it + 1 < nch) fetch(it + 1);
     if (!SUM) {
       // P: 4 rows t, 4 columns s = tp + 16 j; blocks wholly masked stay zero
       const int tp = tid & 15, t0 = 4 * (tid >> 4);
       float2 acc[4][4] = {};
       auto scores = [&](auto lo, auto hi) {  // columns j = lo .. hi - 1
-#pragma unroll 2
+#pragma unroll 4
         for (int c = 0; c < D; c += 4) {
           float4 fa[4], fb[4];
 #pragma unroll
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, SimtTile<D>::kPerSm) retention_simt_
       }
       __syncthreads();  // every A X has read X
     }
+    if (it + 1 < nch) fetch(it + 1);
     // X = gamma^len X + (B w)^T C: rows RS ty .., columns 4 tx ..
     if (C::RS * ty < D) {
       float2 acc[C::RS][2];
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, SimtTile<D>::kPerSm) retention_simt_
         acc[i][0] = make_float2(w0 * u.x, w0 * u.y);
         acc[i][1] = make_float2(w0 * u.z, w0 * u.w);
       }
-#pragma unroll 4
+#pragma unroll 8
       for (int s = 0; s < kTok; ++s) {  // (rows behind the sequence are zeros)
         const float w = sW[s];
         const float4 v = *reinterpret_cast<const float4*>(sC + s * C::ES + 4 * tx);
