@@ -45,7 +45,7 @@ struct RetArgs {
   float* states;                // [n_slots][H][d][d] or null: the forward's state in (load) and out
   const int* slots;             // [B] or null (sequence i uses slot i)
   int n_slots, load;
-  int L;                        // tokens of a segment (a multiple of 128)
+  int L;                        // tokens of a segment (a multiple of 128; fp32: of 64)
   int G;                        // segments in all; of those, segments that enter another one; sequences of two
   int inner, split;             // segments or more (packed: at most)
   int W;                        // segments of such sequences (packed: at most)

@@ -111,8 +111,8 @@ struct Plan {
   bool split;    // some sequence may have two segments
 };
 
-// The length of a segment: the n chunks of 128 tokens for which a call is estimated to take least, in units of a
-// chunk's time in a pass:
+// The length of a segment: the n chunks of 128 tokens (fp32: halves count) for which a call is estimated to take least, in
+// units of a chunk's time in a pass:
 //   pass   (rounds of blocks) (n + start)
 //   split  (rounds) (n + start) sum  +  a state for each segment, written and read by the sums' kernel, the scan and
 //          the pass  +  two more launches
@@ -122,14 +122,16 @@ struct Plan {
 // segment's state 2 chunks, two launches 8 us; a block that returns a state (exact) takes half as long again for about
 // 8 chunks: its segment, the last one, is better short.  fp32: a chunk takes 26 us (two blocks an SM, but d = 128; a
 // third one waits, one by itself takes 0.86 of that), a block 0.3 chunks to start, a sum 0.35.
-// What it picks is within 3 % of the best of a sweep of n: 8 heads of 65,536 tokens 159 us, others 165 to 214; 64 heads
+// What it picks is within 5 % of the best of a sweep of n: 8 heads of 65,536 tokens 159 us, others 165 to 214; 64 heads
 // of 8192 101 us, others 106 to 130; 24 packed sequences of 20,011 tokens 138 us, others 136 to 171; gradients of 64
-// heads of 4096 tokens 104 us, others 112 to 136; fp32: 12 heads of 4096 tokens 91 us for n = 1, 97 for 2, 128 for 3;
-// 24 heads of 6000 194, 183, 214, 175, 280 us for n = 1, 2, 3, 4, 8.
+// heads of 4096 tokens 104 us, others 112 to 136; fp32, in units of 64 tokens: 12 heads of 4096 tokens 87, 91,
+// 81 us for 1, 2, 3; 24 heads of 6000 210, 185, 183, 177 us for 1, 3, 4 (picked), 8; gradients of 8 heads of 500 tokens
+// 34 us for 1, 54 for 2.
 Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward, bool exact) {
   const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
-  const double slots = d == 128 ? 152.0 : 304.0;
+  const int unit = f32 ? 64 : 128;  // tokens that a length is counted in below
+  const double slots = d == 128 ? 152.0 : 304.0, chunk = unit / 128.0;
   const double fixed = 8.0 / (f32 ? 26.0 : 3.1);
   const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.2 : 2.0;
   const double slow = exact && !f32 ? 0.5 : 0.0;
@@ -138,7 +140,7 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
     if (!f32 || d == 128) return std::ceil(blocks / slots);
     return blocks <= slots / 2 ? 0.86 : std::ceil(2 * blocks / slots) / 2;
   };
-  const long long all = (tokens + 127) / 128, most = ((long long)N + 127) / 128;
+  const long long all = (tokens + unit - 1) / unit, most = ((long long)N + unit - 1) / unit;
   const double longest = packed ? std::min<double>((double)most, 4.0 * all / B) : (double)most;
   double best = 1e300;
   long long pick = most;
@@ -146,15 +148,15 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
     double cost;
     if (packed) {
       const double more = n < longest ? (double)all / n : 0.0;  // segments beyond one a sequence
-      const double work = ((double)all + 0.5 * B) * H * cols, blocks = ((double)B + more) * H * cols;
-      cost = (work + blocks * start) * npass / slots + 0.5 * (std::min<double>(n, longest) + start);
+      const double work = (all * chunk + 0.5 * B) * H * cols, blocks = ((double)B + more) * H * cols;
+      cost = (work + blocks * start) * npass / slots + 0.5 * (std::min<double>(n, longest) * chunk + start);
       if (n < most) cost += fixed + (more > 0 ? (work + blocks * start) * nsum * sum / slots + more * H * nsum * state / slots : 0);
     } else {
       const long long segs = (most + n - 1) / n;
-      const double blocks = (double)B * H * segs * cols, rest = (double)(most - (segs - 1) * n), end = rest + slow * std::min(rest, 8.0);
-      cost = rounds(blocks * npass) * (std::max((double)std::min(n, most), end) + start);
+      const double blocks = (double)B * H * segs * cols, rest = (most - (segs - 1) * n) * chunk, end = rest + slow * std::min(rest, 8.0);
+      cost = rounds(blocks * npass) * (std::max(std::min(n, most) * chunk, end) + start);
       if (segs > 1)
-        cost += rounds((double)B * H * (segs - 1) * cols * nsum) * (n + start) * sum + fixed +
+        cost += rounds((double)B * H * (segs - 1) * cols * nsum) * (n * chunk + start) * sum + fixed +
                 (double)B * H * segs * nsum * state / slots;
     }
     if (cost < best) {
@@ -162,9 +164,9 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
       pick = n;
     }
   }
-  if (packed && pick >= longest) pick = std::max<long long>(32, (long long)longest);  // (a longer one would run alone)
+  if (packed && pick >= longest) pick = std::max<long long>(4096 / unit, (long long)longest);  // (a longer one would run alone)
   Plan p;
-  p.L = (int)std::max<long long>(std::min<long long>(pick, 1 << 23) * 128, 128);
+  p.L = (int)std::max<long long>(std::min<long long>(pick, 1 << 23) * unit, unit);
   p.G = (int)(packed ? tokens / p.L + B : (long long)B * ((N + p.L - 1) / p.L));
   p.split = N > p.L;
   p.inner = packed ? (int)(tokens / p.L) : p.G - B;  // (an inner segment is a full one)
