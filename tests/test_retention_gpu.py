@@ -660,3 +660,18 @@ def test_two_streams_at_once(dtype):
     torch.cuda.synchronize()
     for a, b in zip(got[0] + got[1], want[0] + want[1]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("B,H,N,d,feature", [(4, 3, 1832, 32, "identity"), (1, 6, 3769, 64, "identity"),
+                                             (1, 4, 6000, 128, "elu1")])
+def test_states_of_long_sequences_keep_fp32(B, H, N, d, feature):
+    """Returned states of bf16 calls, over all decays: terms carry three bf16 parts, 2^-24, unless the decay
+    leaves at most 2^-2.75 of them: then two, 2^-17 of a term, so 2^-19.75 of the state; sums in fp32 stay
+    below 2^-20 of it (random signs): 2^-19 in all, relative to the states' norm."""
+    g = 1 - 2.0 ** -torch.linspace(5, 9, H)
+    q, k, v = (rand((B, H, N, d), BF, i) for i in range(3))
+    y, st = torch.empty_like(q), torch.zeros(B, H, d, d, device="cuda")
+    lib.retention_forward(q, k, v, g.cuda(), y, states=st, feature=feature, scale=0.2)
+    got = to_f64(st)
+    ref = np.stack([ro.retention(*(to_f64(t[b]) for t in (q, k, v)), to_f64(g), 0.2, feature)[1] for b in range(B)])
+    assert np.linalg.norm(got - ref) <= 2.0 ** -19 * np.linalg.norm(ref)

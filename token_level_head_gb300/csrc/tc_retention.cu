@@ -29,7 +29,7 @@
 // beside each other: scores, P, intra, out (the out warps are busy nearly all of it), and dX, X, inter.  With D = 64
 // a chunk takes 4.5 thousand cycles in one CTA, 6 thousand in each of two on an SM; the instruction issue is at 34 %,
 // the tensor cores at 25 %, HBM at 45 %.  Measured for prompts: 8 heads of 65,536 tokens, d = 128, 97 us of the call's
-// 153 (537 MB at 5.5 TB/s); 4 x 16 heads of 8192 tokens, d = 64, 65 us of 96 (268 MB at 4.1 TB/s).
+// 153 (537 MB at 5.5 TB/s); 4 x 16 heads of 8192 tokens, d = 64, 65 us of 101 (268 MB at 4.1 TB/s).
 //
 // The roles' loops are kept short and free of branches: with whole rows unrolled the instruction fetch,
 // not the arithmetic, set the pace (23,000 cycles a chunk), and stores of one row a thread held up the
@@ -1058,10 +1058,12 @@ __global__ void __launch_bounds__(PassTile<D>::kThreads, PassTile<D>::kPerSm) re
 
 // ================================================================ segment sums
 // A segment's own sum of gamma^(distance to its end) b c^T: B w, with the distance counted to the segment's
-// end, is added up by the tensor cores over all its chunks.  B w is a sum of two bf16 numbers: the sums
-// reach a returned fp32 state only behind the last segment's decay.  Bound by HBM where the segments fill the SMs (8
+// end, is added up by the tensor cores over all its chunks.  B w is a sum of two bf16 numbers; in a call that returns
+// states, of three where the decay up to the sequence's end leaves more than 2^-2.75, and those chunks' sums are added up in
+// fp32 (as in the pass; with two parts throughout, states of 2000 to 4000 tokens were off by 2e-6 to 3e-6).  Bound by HBM where the segments fill the SMs (8
 // heads of 65,536 tokens, d = 128: 43 us, 91 % of a copy's rate), else by a block's chain load, B w, products: 1.4 us
-// a chunk (64 heads of 8192 tokens, d = 64: 192 blocks, 25 us, 60 % of that rate).  A row of B is shared by D / 32
+// a chunk (64 heads of 8192 tokens, d = 64: 192 blocks, 25 us, 60 % of that rate; where states are
+// returned the chunks of three parts add 5 us).  A row of B is shared by D / 32
 // threads and the second part's product goes first, so that the next chunk's B w runs beside the first part's: 53
 // -> 43 us and 28 -> 25 us together.
 template <int D>
@@ -1072,7 +1074,8 @@ struct SumTile {
   static constexpr int kOffBars = kOffLo + kOp;
   static constexpr int kSplit = D / 32;                 // threads that share a row of B
   static constexpr int kThreads = 32 * (kWarpOut + 4 * kSplit);
-  static constexpr int kPerSm = D == 128 ? 1 : 2;
+  // blocks an SM by registers (shared memory allows one less): room for the next kernels' blocks
+  static constexpr int kPerSm = D == 128 ? 2 : 3;
 };
 
 template <int D>
@@ -1091,6 +1094,35 @@ constexpr size_t sum_smem() {
   return SumTile<D>::kOffBars + sizeof(SumBars<D>);
 }
 static_assert(sum_smem<128>() <= 232448 && 2 * (sum_smem<64>() + 1024) <= 233472, "shared memory budget");
+
+// 32 columns, from 8 jb, of row r of B w in three parts.  (This and the next are functions of their own, for the few chunks
+// that need them: with their registers no block of the scan fits beside this kernel's, which cost 6 to 11 us.)
+__device__ __noinline__ void sum_weigh3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w, bool part,
+                                        const RetTensor& b, long long at, int d) {
+  if (b.feature != kFeatIdentity || part)
+    weigh_phi_row3<32>(hi, lo, lo2, r, jb, w, static_cast<const __nv_bfloat16*>(b.p) + at, d, b.feature);
+  else
+    weigh_row3<32>(hi, lo, lo2, r, jb, w);
+}
+// Adds chunk i's own sum of three parts, in the columns D behind, to the segment's: a warp's 32 columns.
+template <int D>
+__device__ __noinline__ void sum_add(uint32_t at, int i) {
+  tc_fence_after();
+#pragma unroll 1
+  for (int hh = 0; hh < D / 64; ++hh, at += 16u << 16) {
+    float u[16], v[16];
+    tmem_ld16x32(at + D, v);
+    if (i > 0) {
+      tmem_ld16x32(at, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 16; ++x) v[x] += u[x];
+    }
+    tmem_ld_wait();
+    tmem_st16x32(at, v);
+  }
+  tmem_st_wait();
+}
 
 template <int D>
 __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
@@ -1122,7 +1154,7 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(&b->tbase, D);
+    tmem_alloc(&b->tbase, 2 * D);
     tmem_relinquish();
   }
   if (warp == kWarpProd && lane == 0) {
@@ -1136,6 +1168,16 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
   const uint32_t tmem = b->tbase;
   const int n = (sg.len + kTok - 1) / kTok;
   uint8_t* lo = sm + P::kOffLo;
+  const float lg = decay_log2(r.gamma[h]);
+  // the first chunk of three parts; the third part's tile takes the place of a stage
+  int three = n;
+  if (r.states != nullptr) {
+    const int rest = sg.all - sg.seg * r.L - sg.len;  // tokens behind the segment
+    const float reach = lg == 0.f ? 1e9f : fminf(1e9f, 2.75f / fabsf(lg));
+    three = n - min(n, (max(0, (int)reach - rest) + kTok - 1) / kTok);
+  }
+  const int stages = three < n ? P::kStages - 1 : P::kStages;
+  uint8_t* lo2 = sm + (P::kStages - 1) * 2 * P::kOp;
 
   if (warp == kWarpProd) {
     if (lane == 0) {
@@ -1144,8 +1186,8 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
                 sc = t.by_b[ic] ? sg.seq : 0;
       int i = 0;
       for (; i < n; ++i) {
-        const int s = i % P::kStages;
-        if (i >= P::kStages && !wait(&b->empty[s], ((i / P::kStages) - 1) & 1, gd)) break;
+        const int s = i % stages;
+        if (i >= stages && !wait(&b->empty[s], ((i / stages) - 1) & 1, gd)) break;
         uint8_t* st = sm + s * 2 * P::kOp;
         mbar_arrive_expect_tx(&b->full[s], 2 * P::kOp);
         load_tile<D>(st, &t.tm[ib], sg.row0 + i * kTok, hb, sb, &b->full[s]);
@@ -1156,21 +1198,29 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
     __syncwarp();
   } else if (warp == kWarpMma) {
     const Desc b0 = make_desc(smem_u32(sm), kAtom, 1024), dlo = make_desc(smem_u32(lo), kAtom, 1024);
+    const Desc dlo2 = make_desc(smem_u32(lo2), kAtom, 1024);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int s = i % P::kStages;
-      if (!wait_warp(&b->ready[s], (i / P::kStages) & 1, gd)) break;
+      const int s = i % stages;
+      if (!wait_warp(&b->ready[s], (i / stages) & 1, gd)) break;
       tc_fence_after();
       const Desc bm{b0.lo + s * (2 * P::kOp >> 4), b0.hi}, cm{bm.lo + (P::kOp >> 4), b0.hi};
       __syncwarp();
       if (elect_one()) {
-        // the second part first: its tile has to be free for the next chunk
-        if (i == 0)
-          mma_outer<D, D, false>(tmem, dlo, cm);
-        else
-          mma_outer<D, D, true>(tmem, dlo, cm);
-        mma_commit(&b->lo_free);
-        mma_outer<D, D, true>(tmem, bm, cm);
+        if (i >= three) {
+          mma_outer<D, D, false>(tmem + D, bm, cm);
+          mma_outer<D, D, true>(tmem + D, dlo, cm);
+          mma_outer<D, D, true>(tmem + D, dlo2, cm);
+          mma_commit(&b->lo_free);
+        } else {
+          // the second part first: its tile has to be free for the next chunk
+          if (i == 0)
+            mma_outer<D, D, false>(tmem, dlo, cm);
+          else
+            mma_outer<D, D, true>(tmem, dlo, cm);
+          mma_commit(&b->lo_free);
+          mma_outer<D, D, true>(tmem, bm, cm);
+        }
         mma_commit(&b->empty[s]);
       }
       __syncwarp();
@@ -1181,29 +1231,33 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
   } else {
     const int qd = warp & 3, row = 32 * qd + lane, half = (warp - kWarpOut) >> 2;
     const int reverse = p.reverse, all = sg.len, d = r.d, fb = p.b.feature, fc = p.c.feature;
-    const float lg = decay_log2(r.gamma[h]);
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int s = i % P::kStages, at = i * kTok + row, len = min(kTok, all - i * kTok);
-      ok = wait_warp(&b->full[s], (i / P::kStages) & 1, gd);
+      const int s = i % stages, at = i * kTok + row, len = min(kTok, all - i * kTok);
+      ok = wait_warp(&b->full[s], (i / stages) & 1, gd);
       if (ok && i > 0) ok = wait_warp(&b->lo_free, (i - 1) & 1, gd);
       if (!ok) break;
+      if (i > three) sum_add<D>(tmem + ((uint32_t)(32 * qd) << 16) + 32 * half, i - 1);
       uint8_t* st = sm + s * 2 * P::kOp;
       if (half == 0) {  // (the operands of a whole row: rarely)
         if (fc != kFeatIdentity || len < kTok) map_row<D>(st + P::kOp, row, len, d, fc);
       }
       const float w = row < len ? decay_pow(lg, reverse ? at : all - 1 - at) : 0.f;
-      if (fb != kFeatIdentity || len < kTok)
+      if (i >= three)
+        sum_weigh3(st, lo, lo2, row, 4 * half, w, len < kTok, p.b, ret_base(r, p.b, sg.seq, h) + (long long)(sg.row0 + at) * p.b.sn, d);
+      else if (fb != kFeatIdentity || len < kTok)
         weigh_phi_row2<32>(st, lo, row, 4 * half, w, d, fb);
       else
         weigh_row2<32>(st, lo, row, 4 * half, w);
       fence_proxy_async_smem();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->ready[s]);
     }
     if (ok && wait_warp(&b->fin, 0, gd) && !aborted(gd)) {
       tc_fence_after();
+      if (three < n) sum_add<D>(tmem + ((uint32_t)(32 * qd) << 16) + 32 * half, n - 1);
       float* dst = r.seg + (((size_t)set * r.W + sg.w0 + sg.seg) * r.H + h) * d * d;
 #pragma unroll 1
       for (int hh = 0; hh < D / 64; ++hh) {  // 16 rows x 32 columns
@@ -1229,13 +1283,13 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
   if (threadIdx.x == 0) {
     drain(&b->fin, 0);
     if (aborted(gd)) {
-      for (int q = b->issued > P::kStages ? b->issued - P::kStages : 0; q < b->issued; ++q)
-        drain(&b->full[q % P::kStages], (q / P::kStages) & 1);
+      for (int q = b->issued > stages ? b->issued - stages : 0; q < b->issued; ++q)
+        drain(&b->full[q % stages], (q / stages) & 1);
       atomicOr(r.status, 1u);
     }
   }
   __syncthreads();
-  if (warp == kWarpMma) tmem_dealloc(tmem, D);
+  if (warp == kWarpMma) tmem_dealloc(tmem, 2 * D);
 }
 
 // ================================================================ host
