@@ -311,6 +311,8 @@ mhla_path mhla_backward_path(int B, int H, int N, int d, int block_size, mhla_dt
  *     them.  Rows of no sequence are not written.  The offsets are not
  *     inspected by the host: non-decreasing values in [0, N] are the caller's
  *     contract, anything else is clamped to it and touches no other memory.
+ *   - A call takes up to 2^31 - 128 tokens (dense: B N); more:
+ *     MHLA_ERR_UNSUPPORTED, and no workspace size.
  *   - gamma: device fp32 [H], each in [0, 1] (the caller's contract).
  *   - states: [n_slots, H, d, d] fp32.  slots: device int32 [B], the slot of
  *     each sequence or row, or NULL (sequence i uses slot i).  A sequence whose

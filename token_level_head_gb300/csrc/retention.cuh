@@ -101,7 +101,7 @@ __device__ __forceinline__ void packed_range(const RetArgs& a, int i, int* lo, i
 __device__ __forceinline__ int packed_segments(const RetArgs& a, int i) {
   int lo, hi;
   packed_range(a, i, &lo, &hi);
-  return (hi - lo + a.L - 1) / a.L;
+  return ret_pieces(hi - lo, a.L);
 }
 
 __device__ __forceinline__ int segments_of_kind(int nseg, SegmentKind kind) {
@@ -135,7 +135,7 @@ __device__ __forceinline__ Segment find_ordered(const RetArgs& a, int k, int* sc
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       q[i] = 2 * tid + i < a.B ? scratch[kOrdered + 2 * tid + i] : 0;
-      m[i] = 2 * tid + i < a.B ? (scratch[q[i]] + a.L - 1) / a.L : 0;
+      m[i] = 2 * tid + i < a.B ? ret_pieces(scratch[q[i]], a.L) : 0;
       n += m[i];
     }
     int first = n;
@@ -149,7 +149,7 @@ __device__ __forceinline__ Segment find_ordered(const RetArgs& a, int k, int* sc
     int w[2], v = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      w[i] = 2 * tid + i < a.B ? (scratch[2 * tid + i] + a.L - 1) / a.L : 0;
+      w[i] = 2 * tid + i < a.B ? ret_pieces(scratch[2 * tid + i], a.L) : 0;
       w[i] = w[i] >= 2 ? w[i] : 0;
       v += w[i];
     }
@@ -201,7 +201,7 @@ __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, Segment
   int lo = 0;
   if (a.cu != nullptr && kind == SEG_ALL && a.B <= kOrdered) return find_ordered(a, k, scratch);
   if (a.cu == nullptr) {
-    s.nseg = (a.N + a.L - 1) / a.L;
+    s.nseg = ret_pieces(a.N, a.L);
     const int per = segments_of_kind(s.nseg, kind);
     s.seq = per > 0 && k < a.B * per ? k / per : -1;
     if (s.seq < 0) return s;

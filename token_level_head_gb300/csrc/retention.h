@@ -18,6 +18,11 @@
 namespace mhla {
 
 constexpr int kRetMaxPasses = 3;
+// Tokens of a call at most: a chunk's last row (128 tokens), in the sequence or behind it, has an int of its own.
+constexpr long long kRetMaxTokens = (1ll << 31) - 128;
+
+// Pieces of `size` tokens that `len` tokens take.  (len + size - 1 would pass 2^31 in the longest sequences.)
+__host__ __device__ __forceinline__ int ret_pieces(int len, int size) { return len > 0 ? (len - 1) / size + 1 : 0; }
 
 struct RetTensor {
   const void* p;                // element (0, 0, 0, 0) of [B, H, N, d], d contiguous

@@ -167,7 +167,7 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
   if (packed && pick >= longest) pick = std::max<long long>(4096 / unit, (long long)longest);  // (a longer one would run alone)
   Plan p;
   p.L = (int)std::max<long long>(std::min<long long>(pick, 1 << 23) * unit, unit);
-  p.G = (int)(packed ? tokens / p.L + B : (long long)B * ((N + p.L - 1) / p.L));
+  p.G = (int)(packed ? tokens / p.L + B : (long long)B * ret_pieces(N, p.L));
   p.split = N > p.L;
   p.inner = packed ? (int)(tokens / p.L) : p.G - B;  // (an inner segment is a full one)
   p.splits = packed ? std::min(B, p.inner) : B;
@@ -189,7 +189,7 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
     return MHLA_OK;
   }
   const long long tokens = cu ? N : (long long)B * N;
-  if (tokens > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
+  if (tokens > kRetMaxTokens) return MHLA_ERR_UNSUPPORTED;
   if (!gamma || !aligned(gamma, 4) || !aligned(cu, 4)) return MHLA_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MHLA_ERR_INVALID_ARG;
   *plan = make_plan(B, H, tokens, d, dt, cu != nullptr, backward, exact);
@@ -228,7 +228,7 @@ using namespace mhla;
 extern "C" {
 
 size_t retention_workspace_bytes(int B, int H, int tokens, int d, int backward) {
-  if (!sizes_ok(B, H, tokens, d) || (backward != 0 && backward != 1)) return 0;
+  if (!sizes_ok(B, H, tokens, d) || tokens > kRetMaxTokens || (backward != 0 && backward != 1)) return 0;
   if (B == 0 || H == 0 || tokens == 0) return kWorkspacePrefix;
   size_t n = 0;
   for (mhla_dtype dt : {MHLA_F32, MHLA_BF16})
