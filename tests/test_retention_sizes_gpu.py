@@ -44,3 +44,29 @@ def test_the_longest_sequence(packed):
     args = [to_f64(tail[0])] * 3 + [to_f64(g)]
     ref, mag = ro.retention(*args)[0], ro.retention(*args, magnitude=True)[0]
     assert (np.abs(to_f64(y[0, :, T - n:]) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.05 * 2.0 ** -8 * mag).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_offsets_that_claim_more_segments_than_an_int_holds(dtype):
+    """200,000 offsets 0, T, 0, T, ..: 100,000 sequences of all T tokens, 5 x 10^9 segments.  The first one has its
+    place in the workspace and comes out right; nothing around the workspace, and no row behind T, is written."""
+    T, d, n, pad = 200_000_001, 16, 300, 1 << 26
+    es = torch.finfo(dtype).bits // 8
+    if torch.cuda.mem_get_info()[0] < 3 * T * d * es:
+        pytest.skip("needs 40 GB of free device memory")
+    x, y = (torch.zeros(1, 1, T + 1, d, dtype=dtype, device="cuda") for _ in range(2))
+    y.fill_(7.0)
+    tail = torch.randn(1, 1, n, d, generator=torch.Generator().manual_seed(1)).to(dtype)
+    x[:, :, T - n:T] = tail.cuda()
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda").repeat(100_000)
+    size = lib.retention_workspace_bytes(cu.numel() - 1, 1, T + 1, d)
+    buf = torch.zeros(pad + size + pad, dtype=torch.uint8, device="cuda")
+    buf[:pad] = 77
+    buf[pad + size:] = 77
+    lib.retention_forward(x, x, x, torch.tensor([0.9], device="cuda"), y, cu_seqlens=cu, workspace=buf[pad:pad + size])
+    assert (buf[:pad] == 77).all() and (buf[pad + size:] == 77).all() and (y[:, :, T:] == 7).all()
+    assert (y[:, :, :T - n:997] == 0).all()
+    args = [to_f64(tail[0])] * 3 + [np.array([np.float64(np.float32(0.9))])]
+    ref, mag = ro.retention(*args)[0], ro.retention(*args, magnitude=True)[0]
+    u, more = (2.0 ** -8, 2.05 * 2.0 ** -8) if dtype == BF else (2.0 ** -24, 300 * 2.0 ** -24 + 2.0 ** -18)
+    assert (np.abs(to_f64(y[0, :, T - n:T]) - ref) <= u * np.abs(ref) + more * mag).all()

@@ -108,11 +108,18 @@ __device__ __forceinline__ int segments_of_kind(int nseg, SegmentKind kind) {
   return kind == SEG_ALL ? nseg : kind == SEG_INNER ? max(nseg - 1, 0) : nseg >= 2 ? 1 : 0;
 }
 
+// Sum of two counts of segments, capped: offsets out of order may claim 2^31 segments and more, and a place that
+// wrapped would lie outside the workspace.  Every number that counts (blocks of a grid, states of the workspace) is
+// below the cap: a call has at most 2^31 / 3.
+constexpr unsigned kMostSegments = 1u << 30;
+__device__ __forceinline__ int add_capped(int a, int b) { return (int)min((unsigned)a + (unsigned)b, kMostSegments - 1); }
+
 constexpr int kOrdered = 64;  // packed sequences up to so many are taken longest first
 
 // Number k of the call's segments, of at most kOrdered packed sequences taken in the order of their lengths, the
 // longest first: blocks start in the order of their numbers, and a long sequence started last would run alone (24
-// sequences, one of 4001 tokens among 20,000, d = 128: 177 us as they come, 145 us in order).
+// sequences, one of 4001 tokens among 20,000, d = 128: 177 us as they come, 145 us in order).  (The counts fit: 64
+// sequences of at most 2^31 - 128 tokens in segments of 64 or more are below 2^31 segments.)
 __device__ __forceinline__ Segment find_ordered(const RetArgs& a, int k, int* scratch) {
   const int tid = threadIdx.x;
   int lo = 0, hi = 0;
@@ -215,16 +222,16 @@ __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, Segment
     int n = 0, m = 0;  // of the kind, of split sequences
     for (int i = i0; i < i1; ++i) {
       const int q = packed_segments(a, i);
-      n += segments_of_kind(q, kind);
-      m += q >= 2 ? q : 0;
+      n = add_capped(n, segments_of_kind(q, kind));
+      m = add_capped(m, q >= 2 ? q : 0);
     }
     int in = n, im = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, in, o), v = __shfl_up_sync(0xffffffffu, im, o);
       if (lane >= o) {
-        in += u;
-        im += v;
+        in = add_capped(in, u);
+        im = add_capped(im, v);
       }
     }
     if (lane == 31) {
@@ -233,10 +240,12 @@ __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, Segment
     }
     if (tid == 0) scratch[64] = -1;
     __syncthreads();
-    int first = in - n, w0 = im - m;
+    // the sums before this thread (not in - n: capped sums have no difference)
+    int first = __shfl_up_sync(0xffffffffu, in, 1), w0 = __shfl_up_sync(0xffffffffu, im, 1);
+    if (lane == 0) first = w0 = 0;
     for (int w = 0; w < warp; ++w) {
-      first += scratch[w];
-      w0 += scratch[32 + w];
+      first = add_capped(first, scratch[w]);
+      w0 = add_capped(w0, scratch[32 + w]);
     }
     if (k >= first && k < first + n) {
       for (int i = i0; i < i1; ++i) {
@@ -247,8 +256,8 @@ __device__ __forceinline__ Segment find_segment(const RetArgs& a, int k, Segment
           scratch[66] = w0;
           break;
         }
-        first += c;
-        w0 += q >= 2 ? q : 0;
+        first = add_capped(first, c);
+        w0 = add_capped(w0, q >= 2 ? q : 0);
       }
     }
     __syncthreads();
