@@ -335,7 +335,7 @@ typedef struct {
 
 /* Workspace bytes of retention_forward (backward = 0) or retention_backward
  * (backward = 1) for B sequences of `tokens` tokens in all (dense: B N); 0 if
- * the sizes are invalid.  Valid for both dtypes, dense and packed. */
+ * the sizes are invalid or more than a call takes.  Valid for both dtypes, dense and packed. */
 size_t retention_workspace_bytes(int B, int H, int tokens, int d, int backward);
 
 /* The outputs of whole prompts.

@@ -1,5 +1,7 @@
 """Sizes at the ends of the retention entries' range (CPU: every call is refused before the library touches CUDA)."""
 
+import ctypes
+
 import pytest
 
 from token_level_head_gb300 import binding
@@ -45,3 +47,34 @@ def test_more_tokens_than_a_call_takes(lib):
             assert call(lib, 1, 1, MOST + 1, 16, cu) == UNSUPPORTED
             assert call(lib, 1, 1, MOST, 16, cu, wsb=64) == INVALID  # (the workspace)
         assert call(lib, 2, 1, 1 << 30, 16) == UNSUPPORTED
+
+
+def strides(*s):
+    return ctypes.byref(binding._Strides(*s))
+
+
+def test_sizes_that_no_memory_holds(lib):
+    """Products of sizes and strides past 2^63, where a wrapped span would look apart from everything."""
+    far = [0x10 * P, 0x20 * P, 0x30 * P, 0x40 * P, 0x50 * P]
+
+    def fwd(B, H, N, d, s=None, ys=None, n_slots=0, states=None, dt=BF16):
+        return lib.retention_forward(far[0], s, far[1], s, far[2], s, P, far[3], ys, B, H, N, d, None, states, None,
+                                     n_slots, 0, dt, None, far[4], 1 << 62, None)
+
+    wide = strides(1 << 36, 64, 64)                                        # (B - 1) x 2^36 = 2^64 and more
+    assert fwd((1 << 28) + 1, 1, 1, 64, s=wide, ys=wide) == INVALID
+    assert fwd(1, 1 << 29, (1 << 31) - 128, 128) in (INVALID, UNSUPPORTED)
+    assert fwd(1, 8, 4, 128, states=2 * P, n_slots=(1 << 31) - 1) == INVALID
+    s = strides(1 << 36, 64, 0)
+    assert lib.retention_step(far[0], s, far[1], s, far[2], s, P, far[4], None, 4, far[3], s, (1 << 28) + 1, 1, 64,
+                              BF16, None, None) == INVALID
+    assert lib.retention_step(far[0], None, far[1], None, far[2], None, P, far[4], None, (1 << 31) - 1, far[3], None,
+                              2, 4, 128, BF16, None, None) == INVALID
+    assert lib.retention_copy_states(P, (1 << 31) - 1, 1 << 10, 128, far[3], far[4], 3, None) == INVALID
+
+
+def test_no_workspace_size_for_calls_that_are_refused(lib):
+    w = binding.retention_workspace_bytes
+    for B, H, N in [((1 << 31) - 1, 1 << 20, 1000), (1 << 20, 1 << 20, 1 << 30), (1 << 30, 2, 1 << 30)]:
+        assert w(B, H, N, 128) == 0 and w(B, H, N, 128, backward=True) == 0
+        assert forward(lib, B, H, N, 128, cu=2 * P, wsb=1 << 62) == UNSUPPORTED

@@ -23,10 +23,21 @@ struct Extent {  // of a tensor: B x H x N rows of d elements
   int es;
 };
 
-// Fills t; false if the pointer, the alignment or the strides are not valid.
+// Bytes of no GPU's memory, virtual addresses included: what spans more is no tensor, and its sizes are not
+// multiplied in 64 bits.
+constexpr long long kNoMemory = 1ll << 48;
+using Wide = __int128;
+
+Wide wide_span(const RetTensor& t, const Extent& e) {
+  return (Wide)(e.b - 1) * t.sb + (Wide)(e.h - 1) * t.sh + (Wide)(e.n - 1) * t.sn + e.d;
+}
+long long span(const RetTensor& t, const Extent& e) { return (long long)wide_span(t, e); }
+
+// Fills t; false if the pointer, the alignment, the strides or the size are not valid.
 bool make_tensor(RetTensor* t, const void* p, const mhla_strides* st, const Extent& e) {
   if (p == nullptr || !aligned(p, 16)) return false;
   t->p = p;
+  if (st == nullptr && (Wide)e.b * e.h * e.n * e.d * e.es > kNoMemory) return false;
   t->sb = st ? st->b : e.h * e.n * e.d;
   t->sh = st ? st->h : e.n * e.d;
   t->sn = st ? st->n : e.d;
@@ -37,12 +48,16 @@ bool make_tensor(RetTensor* t, const void* p, const mhla_strides* st, const Exte
   for (long long s : {t->sb, t->sh, t->sn})
     if (s < 0 || s % q != 0 || s >= most) return false;
   if (t->sn == 0 && e.n > 1) return false;  // rows of their own, so that a tile can be loaded by TMA
+  if (wide_span(*t, e) * e.es > kNoMemory) return false;
   t->feature = MHLA_PHI_IDENTITY;
   return true;
 }
 
-long long span(const RetTensor& t, const Extent& e) {
-  return (e.b - 1) * t.sb + (e.h - 1) * t.sh + (e.n - 1) * t.sn + e.d;
+// Bytes of a pool of states; false if no memory holds it.
+bool pool_bytes(size_t* bytes, long long n_slots, int H, int d) {
+  const Wide n = (Wide)n_slots * H * d * d * sizeof(float);
+  *bytes = (size_t)n;
+  return n <= kNoMemory;
 }
 
 struct Dim {
@@ -105,10 +120,12 @@ bool options_ok(const retention_options* opt) {
 
 // ---- segments
 struct Plan {
-  int L, G;      // tokens of a segment, segments
-  int inner, splits, W;  // segments that enter another one, sequences of two or more, segments of those
+  int L;         // tokens of a segment
+  long long G;   // segments
+  long long inner, splits, W;  // segments that enter another one, sequences of two or more, segments of those
   size_t bytes;  // workspace
   bool split;    // some sequence may have two segments
+  bool fits;     // the grids' blocks can be numbered
 };
 
 // The length of a segment: the n chunks of 128 tokens (fp32: halves count) for which a call is estimated to take least, in
@@ -167,12 +184,13 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
   if (packed && pick >= longest) pick = std::max<long long>(4096 / unit, (long long)longest);  // (a longer one would run alone)
   Plan p;
   p.L = (int)std::max<long long>(std::min<long long>(pick, 1 << 23) * unit, unit);
-  p.G = (int)(packed ? tokens / p.L + B : (long long)B * ret_pieces(N, p.L));
+  p.G = packed ? tokens / p.L + B : (long long)B * ret_pieces(N, p.L);
   p.split = N > p.L;
-  p.inner = packed ? (int)(tokens / p.L) : p.G - B;  // (an inner segment is a full one)
-  p.splits = packed ? std::min(B, p.inner) : B;
-  p.W = packed ? (int)std::min<long long>(p.G, 2ll * p.inner) : p.G;  // (nseg <= 2 (nseg - 1))
-  p.bytes = kWorkspacePrefix + (p.split ? (size_t)nsum * p.W * H * d * d * sizeof(float) : 0);
+  p.inner = packed ? tokens / p.L : p.G - B;  // (an inner segment is a full one)
+  p.splits = packed ? std::min<long long>(B, p.inner) : B;
+  p.W = packed ? std::min(p.G, 2 * p.inner) : p.G;  // (nseg <= 2 (nseg - 1))
+  p.fits = p.G * H <= 0x7fffffffll / 3 && (long long)B * H <= 0x7fffffffll / 3;
+  p.bytes = kWorkspacePrefix + (p.split && p.fits ? (size_t)nsum * p.W * H * d * d * sizeof(float) : 0);
   return p;
 }
 
@@ -193,7 +211,7 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
   if (!gamma || !aligned(gamma, 4) || !aligned(cu, 4)) return MHLA_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MHLA_ERR_INVALID_ARG;
   *plan = make_plan(B, H, tokens, d, dt, cu != nullptr, backward, exact);
-  if ((long long)plan->G * H > 0x7fffffffll / 3 || (long long)B * H > 0x7fffffffll / 3) return MHLA_ERR_UNSUPPORTED;
+  if (!plan->fits) return MHLA_ERR_UNSUPPORTED;
   if (ws_bytes < plan->bytes) return MHLA_ERR_INVALID_ARG;
   *e = {cu ? 1 : B, H, N, d, dt == MHLA_F32 ? 4 : 2};
   *a = RetArgs{};
@@ -206,10 +224,10 @@ mhla_status begin(RetArgs* a, Plan* plan, Extent* e, const float* gamma, int B, 
   a->gamma = gamma;
   a->scale = opt ? opt->scale : 1.f;
   a->L = plan->L;
-  a->G = plan->G;
-  a->inner = plan->inner;
-  a->split = plan->splits;
-  a->W = plan->W;
+  a->G = (int)plan->G;
+  a->inner = (int)plan->inner;
+  a->split = (int)plan->splits;
+  a->W = (int)plan->W;
   a->seg = plan->split ? reinterpret_cast<float*>(static_cast<char*>(ws) + kWorkspacePrefix) : nullptr;
   a->status = &static_cast<WorkspaceHeader*>(ws)->status;
   return MHLA_OK;
@@ -234,8 +252,11 @@ size_t retention_workspace_bytes(int B, int H, int tokens, int d, int backward) 
   for (mhla_dtype dt : {MHLA_F32, MHLA_BF16})
     for (bool exact : {false, true}) {
       if (exact && backward) continue;
-      n = std::max(n, make_plan(B, H, tokens, d, dt, true, backward != 0, exact).bytes);
-      if (tokens % B == 0) n = std::max(n, make_plan(B, H, tokens, d, dt, false, backward != 0, exact).bytes);
+      for (bool packed : {true, false}) {
+        if (!packed && tokens % B != 0) continue;
+        const Plan p = make_plan(B, H, tokens, d, dt, packed, backward != 0, exact);
+        if (p.fits) n = std::max(n, p.bytes);
+      }
     }
   return n;
 }
@@ -259,8 +280,9 @@ mhla_status retention_forward(const void* q, const mhla_strides* q_strides, cons
   if (!make_tensor(&tq, q, q_strides, e) || !make_tensor(&tk, k, k_strides, e) || !make_tensor(&tv, v, v_strides, e) ||
       !make_tensor(&ty, y, y_strides, e) || !injective(ty, e))
     return MHLA_ERR_INVALID_ARG;
-  const size_t sb = (size_t)(states ? n_slots : 0) * H * d * d * sizeof(float);
-  if (!aligned(states, 16) || !aligned(slots, 4)) return MHLA_ERR_INVALID_ARG;
+  size_t sb;
+  if (!pool_bytes(&sb, states ? n_slots : 0, H, d) || !aligned(states, 16) || !aligned(slots, 4))
+    return MHLA_ERR_INVALID_ARG;
   for (const RetTensor* t : {&tq, &tk, &tv, &ty}) {
     const size_t n = (size_t)span(*t, e) * e.es;
     if (t != &ty && !disjoint(ty, *t, e)) return MHLA_ERR_INVALID_ARG;
@@ -368,7 +390,9 @@ mhla_status retention_step(const void* q, const mhla_strides* q_strides, const v
   if (!make_tensor(&tq, q, q_strides, e) || !make_tensor(&tk, k, k_strides, e) || !make_tensor(&tv, v, v_strides, e) ||
       !make_tensor(&to, out, out_strides, e) || !injective(to, e))
     return MHLA_ERR_INVALID_ARG;
-  const size_t sb = (size_t)n_slots * H * d * d * sizeof(float), ob = (size_t)span(to, e) * e.es;
+  const size_t ob = (size_t)span(to, e) * e.es;
+  size_t sb;
+  if (!pool_bytes(&sb, n_slots, H, d)) return MHLA_ERR_INVALID_ARG;
   for (const RetTensor* t : {&tq, &tk, &tv, &to}) {
     if (t != &to && !disjoint(to, *t, e)) return MHLA_ERR_INVALID_ARG;
     if (!apart(t->p, (size_t)span(*t, e) * e.es, states, sb)) return MHLA_ERR_INVALID_ARG;
@@ -391,8 +415,9 @@ mhla_status retention_copy_states(float* states, int n_slots, int H, int d, cons
     return MHLA_ERR_INVALID_ARG;
   const long long slot = (long long)H * d * d;
   if (slot / 32 > 0x7fffffffll) return MHLA_ERR_UNSUPPORTED;
-  const size_t sb = (size_t)n_slots * slot * sizeof(float);
-  if (!apart(states, sb, src, (size_t)n * 4) || !apart(states, sb, dst, (size_t)n * 4)) return MHLA_ERR_INVALID_ARG;
+  size_t sb;
+  if (!pool_bytes(&sb, n_slots, H, d) || !apart(states, sb, src, (size_t)n * 4) || !apart(states, sb, dst, (size_t)n * 4))
+    return MHLA_ERR_INVALID_ARG;
   return from_cuda(retention_copy_launch(states, slot, n_slots, src, dst, n, static_cast<cudaStream_t>(stream)));
 }
 
