@@ -3,6 +3,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from token_level_head_gb300 import binding
 from token_level_head_gb300.build import build_library
@@ -78,3 +79,36 @@ def test_no_workspace_size_for_calls_that_are_refused(lib):
     for B, H, N in [((1 << 31) - 1, 1 << 20, 1000), (1 << 20, 1 << 20, 1 << 30), (1 << 30, 2, 1 << 30)]:
         assert w(B, H, N, 128) == 0 and w(B, H, N, 128, backward=True) == 0
         assert forward(lib, B, H, N, 128, cu=2 * P, wsb=1 << 62) == UNSUPPORTED
+
+
+def test_sizes_past_an_int_are_not_cut():
+    """The binding refuses what the C entries' ints do not hold (expanded CPU tensors: nothing is allocated)."""
+    n = (1 << 32) + 8
+    w = binding.retention_workspace_bytes
+    assert w(1, 1, n, 16) == 0 and w(n, 1, 8, 16) == 0 and w(8, n, 8, 16, backward=True) == 0
+    g = torch.zeros(1)
+    x = torch.zeros(16).expand(1, 1, n, 16)
+    for call in (lambda: binding.retention_forward(x, x, x, g, x), lambda: binding.retention_backward(x, x, x, g, x, x, x, x)):
+        with pytest.raises(ValueError, match="N: 4294967304"):
+            call()
+    t = torch.zeros(16).expand(n, 1, 16)
+    pool = torch.zeros(16, 16).expand(n, 1, 16, 16)
+    with pytest.raises(ValueError, match="B: 4294967304"):
+        binding.retention_step(t, t, t, g, pool, t)
+    with pytest.raises(ValueError, match="slots: 4294967304"):
+        binding.retention_step(t[:2], t[:2], t[:2], g, pool, t[:2])
+    e = torch.as_strided(torch.zeros(1), (1, 1, 4, (1 << 32) + 64), (0, 0, 0, 0))
+    with pytest.raises(ValueError, match="d: 4294967360"):
+        binding.retention_forward(e, e, e, g, e)
+    with pytest.raises(ValueError, match="d: 4294967360"):
+        binding.retention_step(e[0], e[0], e[0], g, pool, e[0])
+    y = torch.zeros(16).expand(2, 1, 4, 16)
+    with pytest.raises(ValueError, match="slots: 4294967304"):
+        binding.retention_forward(y, y, y, g, y, states=pool)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="slots: 4294967304"):
+        binding.retention_copy_states(pool, i, i)
+    with pytest.raises(ValueError, match="n: 4294967304"):
+        binding.retention_copy_states(pool[:2], i.expand(n), i.expand(n))
+    with pytest.raises(ValueError, match="B: 4294967303"):
+        binding.retention_forward(x[:, :, :4], x[:, :, :4], x[:, :, :4], g, x[:, :, :4], cu_seqlens=i.expand(n))

@@ -460,6 +460,13 @@ def _expect_fast(t, name, shape, dtype):
         _expect(t, name, shape, dtype)
 
 
+def _fits_int(**sizes):
+    """ctypes would cut a size that the C entry's int does not hold."""
+    for name, n in sizes.items():
+        if n > 0x7fffffff:
+            raise ValueError(f"{name}: {n}, at most {0x7fffffff}")
+
+
 def _retention_sizes(q, cu_seqlens):
     """B (sequences), H, N (packed: all tokens), d of q [B, H, N, d]; packed: q [1, H, tokens, d]."""
     if q.dim() != 4:
@@ -472,6 +479,8 @@ def _retention_sizes(q, cu_seqlens):
             raise ValueError(f"cu_seqlens: expected [sequences + 1], got shape {tuple(cu_seqlens.shape)}")
         _expect_fast(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
         B = cu_seqlens.numel() - 1
+    if B > 0x7fffffff or H > 0x7fffffff or N > 0x7fffffff or d > 0x7fffffff:
+        _fits_int(B=B, H=H, N=N, d=d)
     return B, H, N, d
 
 
@@ -485,10 +494,14 @@ def _retention_states(states, slots, B, H, d):
         raise ValueError(f"states: expected [slots, H, d, d], got shape {tuple(shape)}")
     _expect_fast(states, "states", (shape[0], H, d, d), torch.float32)
     _expect_fast(slots, "slots", (B,), torch.int32)
+    if shape[0] > 0x7fffffff:
+        _fits_int(slots=shape[0])
     return shape[0]
 
 
 def retention_workspace_bytes(B: int, H: int, tokens: int, d: int, backward: bool = False) -> int:
+    if max(B, H, tokens, d) > 0x7fffffff:
+        return 0
     return int(load().retention_workspace_bytes(B, H, tokens, d, 1 if backward else 0))
 
 
@@ -549,6 +562,8 @@ def retention_step(q, k, v, gamma, states, out, *, slots=None, scale=1.0, featur
     if q.dim() != 3:
         raise ValueError(f"q: expected [B, H, d], got shape {tuple(q.shape)}")
     B, H, d = q.shape
+    if B > 0x7fffffff or H > 0x7fffffff or d > 0x7fffffff:
+        _fits_int(B=B, H=H, d=d)
     _expect_like(q, ("k", k), ("v", v), ("out", out))
     _expect_fast(gamma, "gamma", (H,), torch.float32)
     if states is None:
@@ -572,6 +587,7 @@ def retention_copy_states(states, src, dst, *, stream=None):
         raise ValueError(f"src: expected [n], got shape {tuple(src.shape)}")
     for name, t in (("src", src), ("dst", dst)):
         _expect_fast(t, name, src.shape, torch.int32)
+    _fits_int(slots=states.shape[0], H=states.shape[1], d=states.shape[2], n=src.shape[0])
     dev = _retention_device((states,), (states, src, dst))
     _retention_call("retention_copy_states", dev,
                     (states.data_ptr(), states.shape[0], states.shape[1], states.shape[2], src.data_ptr(),
