@@ -1095,11 +1095,13 @@ constexpr size_t sum_smem() {
 }
 static_assert(sum_smem<128>() <= 232448 && 2 * (sum_smem<64>() + 1024) <= 233472, "shared memory budget");
 
-// 32 columns, from 8 jb, of row r of B w in three parts.  (This and the next are functions of their own, for the few chunks
-// that need them: with their registers no block of the scan fits beside this kernel's, which cost 6 to 11 us.)
-__device__ __noinline__ void sum_weigh3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w, bool part,
+// 32 columns, from 8 jb, of row r of B w in three parts.  (Chunks of three parts are whole: states are returned by the
+// forward direction alone, whose inner segments have exactly L tokens, a multiple of a chunk's.)  (This and the next
+// are functions of their own, for the few chunks that need them: with their registers no block of the scan fits beside
+// this kernel's, which cost 6 to 11 us.)
+__device__ __noinline__ void sum_weigh3(uint8_t* hi, uint8_t* lo, uint8_t* lo2, int r, int jb, float w,
                                         const RetTensor& b, long long at, int d) {
-  if (b.feature != kFeatIdentity || part)
+  if (b.feature != kFeatIdentity)
     weigh_phi_row3<32>(hi, lo, lo2, r, jb, w, static_cast<const __nv_bfloat16*>(b.p) + at, d, b.feature);
   else
     weigh_row3<32>(hi, lo, lo2, r, jb, w);
@@ -1245,7 +1247,7 @@ __global__ void __launch_bounds__(SumTile<D>::kThreads, SumTile<D>::kPerSm)
       }
       const float w = row < len ? decay_pow(lg, reverse ? at : all - 1 - at) : 0.f;
       if (i >= three)
-        sum_weigh3(st, lo, lo2, row, 4 * half, w, len < kTok, p.b, ret_base(r, p.b, sg.seq, h) + (long long)(sg.row0 + at) * p.b.sn, d);
+        sum_weigh3(st, lo, lo2, row, 4 * half, w, p.b, ret_base(r, p.b, sg.seq, h) + (long long)(sg.row0 + at) * p.b.sn, d);
       else if (fb != kFeatIdentity || len < kTok)
         weigh_phi_row2<32>(st, lo, row, 4 * half, w, d, fb);
       else
