@@ -587,11 +587,13 @@ def retention_copy_states(states, src, dst, *, stream=None):
         raise ValueError(f"src: expected [n], got shape {tuple(src.shape)}")
     for name, t in (("src", src), ("dst", dst)):
         _expect_fast(t, name, src.shape, torch.int32)
-    _fits_int(slots=states.shape[0], H=states.shape[1], d=states.shape[2], n=src.shape[0])
+    slots, H, d, _ = states.shape
+    n = src.shape[0]
+    if slots > 0x7fffffff or H > 0x7fffffff or d > 0x7fffffff or n > 0x7fffffff:
+        _fits_int(slots=slots, H=H, d=d, n=n)
     dev = _retention_device((states,), (states, src, dst))
     _retention_call("retention_copy_states", dev,
-                    (states.data_ptr(), states.shape[0], states.shape[1], states.shape[2], src.data_ptr(),
-                     dst.data_ptr(), src.shape[0]), stream)
+                    (states.data_ptr(), slots, H, d, src.data_ptr(), dst.data_ptr(), n), stream)
     return states
 
 
