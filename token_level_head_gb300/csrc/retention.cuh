@@ -117,11 +117,13 @@ __device__ __forceinline__ int segments_of_kind(int nseg, SegmentKind kind) {
 constexpr unsigned kMostSegments = 1u << 30;
 __device__ __forceinline__ int add_capped(int a, int b) { return (int)min((unsigned)a + (unsigned)b, kMostSegments - 1); }
 
-constexpr int kOrdered = 64;  // packed sequences up to so many are taken longest first
+constexpr int kOrdered = 64;  // packed sequences up to so many are taken longest first: two a lane of one warp
 
 // Number k of the call's segments, of at most kOrdered packed sequences taken in the order of their lengths, the
-// longest first: blocks start in the order of their numbers, and a long sequence started last would run alone (24
-// sequences, one of 4001 tokens among 20,000, d = 128: 177 us as they come, 145 us in order).  (The counts fit: 64
+// longest first: blocks start in the order of their numbers, and a long sequence started last would run alone.  More
+// sequences are taken as they come.  On both sides of the limit, 64 sequences of 40,000 tokens, one of 4000 among them,
+// 16 heads, and the same with one of a single token more: prompts with d = 128 232 us, 285 with the long one first and 310
+// with it last; d = 64 126, 177 and 204; gradients 468, 492 and 512, d = 64 265, 337 and 362.  (The counts fit: 64
 // sequences of at most 2^31 - 128 tokens in segments of 64 or more are below 2^31 segments.)
 __device__ __forceinline__ Segment find_ordered(const RetArgs& a, int k, int* scratch) {
   const int tid = threadIdx.x;

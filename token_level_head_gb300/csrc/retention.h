@@ -18,6 +18,10 @@
 namespace mhla {
 
 constexpr int kRetMaxPasses = 3;
+// SMs of a GB300: what the segments' plan and the copies' grid count on.  A constant, so that a workspace's size
+// depends on the sizes alone and can be asked for without a device; with another count the results are the same
+// and the last round of blocks is filled less well.
+constexpr int kRetSms = 152;
 // Tokens of a call at most: a chunk's last row (128 tokens), in the sequence or behind it, has an int of its own.
 constexpr long long kRetMaxTokens = (1ll << 31) - 128;
 

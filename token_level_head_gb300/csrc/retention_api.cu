@@ -139,16 +139,24 @@ struct Plan {
 // segment's state 2 chunks, two launches 8 us; a block that returns a state (exact) takes half as long again for about
 // 8 chunks: its segment, the last one, is better short.  fp32: a chunk takes 26 us (two blocks an SM, but d = 128; a
 // third one waits, one by itself takes 0.86 of that), a block 0.3 chunks to start, a sum 0.35.
-// What it picks is within 5 % of the best of a sweep of n: 8 heads of 65,536 tokens 159 us, others 165 to 214; 64 heads
-// of 8192 101 us, others 106 to 130; 24 packed sequences of 20,011 tokens 138 us, others 136 to 171; gradients of 64
-// heads of 4096 tokens 104 us, others 112 to 136; fp32, in units of 64 tokens: 12 heads of 4096 tokens 87, 91,
-// 81 us for 1, 2, 3; 24 heads of 6000 210, 185, 183, 177 us for 1, 3, 4 (picked), 8; gradients of 8 heads of 500 tokens
-// 34 us for 1, 54 for 2.
+// What it picks is within 5 % of the best of a sweep of segment lengths (us of whole calls, the pick first): 8 heads of
+// 65,536 tokens 3584: 152, 3456: 168, 4096: 182, 2048: 207; 64 heads of 8192 2176: 101, 2304: 101, 2048: 106, 1024: 116, 4096:
+// 148; 24 packed sequences of 20,011 tokens 4096: 133, 2048: 152, 1024: 172; gradients of 64 heads of 4096 tokens 4096: 104,
+// 1408: 110, 1024: 127, 2048: 131; of 12 packed sequences of 16,384 tokens 5376: 162, 4096: 164, 2048: 204; fp32: 12 heads of
+// 4096 tokens 192: 80, 64: 86, 128: 88, 256: 96; 24 heads of 6000 320: 180, 512: 173, 192: 182, 64: 209; gradients of 8 heads of
+// 500 tokens 64: 31, 128: 49.
+// One length serves all packed sequences, of which the host knows the mean alone.  Where no cut is picked, sequences of up
+// to kUncut tokens or four times the mean are left whole and longer ones are cut at that length.  kUncut is a middle; with
+// 1024 / 4096 / 8192 in its place, 16 heads, d = 128: 60 sequences of 40,000 tokens, the longest 4000, 266 / 227 / 224 us,
+// the longest 16,000, 266 / 267 / 301; 24 of 20,011, the longest 6000, 159 / 155 / 183, 12,000, 148 / 170 / 303.  With few
+// heads short pieces would be better, and long ones with gradients: 4 heads, d = 64, 60 sequences of 20,011, the longest 12,000,
+// 57 / 130 / 218; gradients with 16 heads, d = 128, of 60 sequences of 40,000, the longest 8000, 508 / 503 / 450.
+constexpr int kUncut = 4096;
 Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed, bool backward, bool exact) {
   const bool f32 = dt == MHLA_F32;
   const int N = packed ? (int)tokens : (int)(tokens / B), npass = backward ? 3 : 1, nsum = backward ? 2 : 1;
   const int unit = f32 ? 64 : 128;  // tokens that a length is counted in below
-  const double slots = d == 128 ? 152.0 : 304.0, chunk = unit / 128.0;
+  const double slots = d == 128 ? kRetSms : 2.0 * kRetSms, chunk = unit / 128.0;
   const double fixed = 8.0 / (f32 ? 26.0 : 3.1);
   const double start = f32 ? 0.3 : 2.5, sum = f32 ? 0.35 : 0.45, state = f32 ? 0.2 : 2.0;
   const double slow = exact && !f32 ? 0.5 : 0.0;
@@ -181,7 +189,7 @@ Plan make_plan(int B, int H, long long tokens, int d, mhla_dtype dt, bool packed
       pick = n;
     }
   }
-  if (packed && pick >= longest) pick = std::max<long long>(4096 / unit, (long long)longest);  // (a longer one would run alone)
+  if (packed && pick >= longest) pick = std::max<long long>(kUncut / unit, (long long)longest);
   Plan p;
   p.L = (int)std::max<long long>(std::min<long long>(pick, 1 << 23) * unit, unit);
   p.G = packed ? tokens / p.L + B : (long long)B * ret_pieces(N, p.L);

@@ -298,9 +298,10 @@ cudaError_t launch_passes(const RetArgs& a, cudaStream_t st) {
 // ================================================================ scan
 // A thread carries E groups of V elements of a head's state over its sequence's segments, in the pass's direction:
 // the slot of a segment holds the segment's own sum before, the state entering it after.  V = E = 4 where there are
-// many heads (most packed sequences have one segment, and their blocks end at once), single elements where few: calls
-// with 24 packed sequences x 16 heads 136 us, 151 with single elements, with 64 heads of 8192 tokens 101 and 103;
-// with 8 heads of 65,536 171 and 161, with 12 heads of 4096 fp32 103 and 99.  Bound by the loads' latency: 8 us.
+// many heads (most packed sequences have one segment, and their blocks end at once), single elements where few.  Whole
+// calls, by fours and by ones: 24 packed sequences x 16 heads in segments of 2048 tokens 151 and 181 us, 64 heads of 8192
+// tokens 101 and 100; 8 heads of 65,536 165 and 152, gradients of 8 heads of 500 tokens fp32 32.8 and 30.7.  Bound by the
+// loads' latency: 8 us.
 template <int V, int E>
 __global__ void __launch_bounds__(kThreads) retention_scan_kernel(const __grid_constant__ RetArgs a) {
   __shared__ int scratch[2 * kOrdered];
@@ -546,15 +547,16 @@ cudaError_t retention_copy_launch(float* states, long long slot_elems, int n_slo
                                   int n, cudaStream_t st) {
   // parts of 128 bytes to 4 KB: as much shared memory as two blocks an SM allow, but a few parts for every SM
   int log_r4 = 3;
-  while (log_r4 < 8 && ((size_t)n << (log_r4 + 1)) * 16 <= (size_t)kCopyBytes && (slot_elems >> (log_r4 + 3)) >= 608)
+  while (log_r4 < 8 && ((size_t)n << (log_r4 + 1)) * 16 <= (size_t)kCopyBytes && (slot_elems >> (log_r4 + 3)) >= 4 * kRetSms)
     ++log_r4;
   const size_t bytes = ((size_t)n << log_r4) * 16 + (size_t)n * 3 * sizeof(int);
   static SmemOptIn opt;
   cudaError_t e = opt.ensure((const void*)retention_copy_kernel, 227 * 1024);
   if (e != cudaSuccess) return e;
   const long long r = 4ll << log_r4, parts = (slot_elems + r - 1) / r;
-  retention_copy_kernel<<<(unsigned)std::min<long long>(parts, 152 * std::max<long long>(2, std::min<long long>(8, (long long)(200 * 1024 / bytes)))), kThreads, bytes, st>>>(states, slot_elems, n_slots, src,
-                                                                                       dst, n, log_r4);
+  const long long per_sm = std::max<long long>(2, std::min<long long>(8, (long long)(200 * 1024 / bytes)));
+  retention_copy_kernel<<<(unsigned)std::min<long long>(parts, kRetSms * per_sm), kThreads, bytes, st>>>(
+      states, slot_elems, n_slots, src, dst, n, log_r4);
   note_launch();
   return cudaGetLastError();
 }

@@ -1,6 +1,6 @@
 // Retention passes on the sm_103a tensor cores (bf16).  The mathematics is in retention.h; a pass cuts
 // a segment into chunks of 128 tokens (len of them in the sequence) and carries X, the state entering
-// the chunk ([D][D], fp32 in registers):
+// the chunk ([D][D], fp32 in tensor memory):
 //   scores = A B^T                               M 128, N 128, K D
 //   P      = scores * gamma^(t-s), masked        bf16, written over the scores in TMEM
 //   inter  = A bf16(X)                           M 128, N D, K D
@@ -29,7 +29,15 @@
 // beside each other: scores, P, intra, out (the out warps are busy nearly all of it), and dX, X, inter.  With D = 64
 // a chunk takes 4.5 thousand cycles in one CTA, 6 thousand in each of two on an SM; the instruction issue is at 34 %,
 // the tensor cores at 25 %, HBM at 45 %.  Measured for prompts: 8 heads of 65,536 tokens, d = 128, 97 us of the call's
-// 153 (537 MB at 5.5 TB/s); 4 x 16 heads of 8192 tokens, d = 64, 65 us of 101 (268 MB at 4.1 TB/s).
+// 152 (537 MB at 5.5 TB/s); 4 x 16 heads of 8192 tokens, d = 64, 65 us of 101 (268 MB at 4.1 TB/s).  A block by itself, 16
+// heads, d = 64: a call of one whole chunk takes 5.5 us on the device without a state, 7.9 with one taken and left, 0.5 more
+// with slot numbers, and every further chunk 2.4 or 3.2; a chunk that is not whole 1.3 to 2 us more at the start (rows behind it are
+// cleared before the scores, behind the state's load).
+// Feature maps are far dearer: they are applied in the operands' tiles between the loads and the scores of every chunk, and
+// where a state is returned every chunk's B w has three parts, of phi taken again from global memory.  ELU + 1 against the
+// identity: 4 x 16 heads of 8192 tokens 344 us and 102, 8 heads of 65,536, d = 128, 659 and 154, gradients of 64 heads of 4096
+// tokens 412 and 103, of 12 packed sequences of 16,384 tokens, d = 128, 650 and 162.  Widths below 64 run as 64 with zero
+// columns: 91 us with d = 16, 93 with 32, 102 with 64.
 //
 // The roles' loops are kept short and free of branches: with whole rows unrolled the instruction fetch,
 // not the arithmetic, set the pace (23,000 cycles a chunk), and stores of one row a thread held up the
