@@ -70,3 +70,31 @@ def test_offsets_that_claim_more_segments_than_an_int_holds(dtype):
     ref, mag = ro.retention(*args)[0], ro.retention(*args, magnitude=True)[0]
     u, more = (2.0 ** -8, 2.05 * 2.0 ** -8) if dtype == BF else (2.0 ** -24, 300 * 2.0 ** -24 + 2.0 ** -18)
     assert (np.abs(to_f64(y[0, :, T - n:T]) - ref) <= u * np.abs(ref) + more * mag).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_states_past_32_bits(dtype):
+    """A pool of 2^31 elements and more: prompts, tokens and copies on its first and its last slots, against the same
+    calls on a small pool, bit for bit."""
+    H, d, n, N = 16, 128, 8200, 150
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GiB of free device memory")
+    far = torch.empty(n, H, d, d, device="cuda")
+    assert far.numel() > (1 << 31)
+    at = [n - 1, 0, 8192, n - 3]
+    near = torch.randn(4, H, d, d, generator=torch.Generator().manual_seed(1)).cuda()
+    for i, s in enumerate(at):
+        far[s] = near[i]
+    far[n - 2] = 7.0
+    q, k, v = (torch.randn(3, H, N, d, generator=torch.Generator().manual_seed(i)).to(dtype).cuda() for i in range(3))
+    g = (1 - 2.0 ** -torch.linspace(5, 9, H)).cuda()
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out = []
+    for pool, slots in ((far, at), (near, range(4))):
+        y, o, s = torch.empty_like(q), torch.empty(3, H, d, dtype=dtype, device="cuda"), list(slots)
+        lib.retention_forward(q, k, v, g, y, states=pool, slots=ints(*s[:3]), load_state=True, scale=0.1)
+        lib.retention_copy_states(pool, ints(s[0], s[1]), ints(s[3], s[0]))
+        lib.retention_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], g, pool, o, slots=ints(s[2], s[3], s[0]), scale=0.1)
+        out.append([y, o] + [pool[i].clone() for i in s])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert (far[n - 2] == 7).all()
