@@ -299,7 +299,8 @@ mhla_path mhla_backward_path(int B, int H, int N, int d, int block_size, mhla_dt
  * from one call to the next.
  *
  * Conventions of the retention_* entries:
- *   - Token tensors are [B, H, N, d] with any strides: an mhla_strides holds
+ *   - Token tensors are [B, H, N, d], d = 16, 32, 64 or 128 for keys and
+ *     values alike, with any strides: an mhla_strides holds
  *     the element strides of b, h and n (d contiguous); NULL means dense
  *     row-major.  Strides are >= 0 and, like the pointers, multiples of 16
  *     bytes; an input may have stride 0 in b and h (keys shared by several
@@ -356,6 +357,7 @@ mhla_status retention_forward(const void* q, const mhla_strides* q_strides, cons
 /* The gradients of q, k and v of retention_forward without states, for training:
  *   G_t = gamma_h G_{t+1} + scale phi(q_t) dy_t^T
  *   dq_t = phi'(q_t) * (scale S_t dy_t),  dk_t = phi'(k_t) * (G_t v_t),  dv_t = G_t^T phi(k_t)
+ * from a zero state before the first token and with none asked for behind the last,
  * with phi' = 1 (identity), phi'(x) = 1 for x > 0 and exp(x) otherwise (ELU + 1),
  * 1 for x > 0 and 0 otherwise (ReLU), exp(x) (exp).  gamma is a constant.
  *   dy : input, dL/dY;  dq, dk, dv : outputs, written (not accumulated), of the

@@ -521,7 +521,9 @@ def retention_forward(q, k, v, gamma, y, *, cu_seqlens=None, states=None, slots=
     phi(k_t) v_t^T, over whole prompts.  q/k/v/y [B, H, N, d] with any strides (rows contiguous),
     gamma [H] fp32; packed sequences: q/k/v/y [1, H, tokens, d] and int32 ``cu_seqlens``
     [sequences + 1].  ``states`` [slots, H, d, d] fp32 receives the final states (``slots``: the slot
-    of each sequence, int32); with ``load_state`` the sequences start from them."""
+    of each sequence, int32); with ``load_state`` the sequences start from them.  d is 16, 32, 64 or 128.
+    ``workspace``: of ``retention_workspace_bytes``; without one the call makes its own, and whether a device-side
+    wait gave up cannot be asked afterwards (``mhla_query_status`` reads the workspace)."""
     B, H, N, d = _retention_sizes(q, cu_seqlens)
     _expect_like(q, ("k", k), ("v", v), ("y", y))
     _expect_fast(gamma, "gamma", (H,), torch.float32)
@@ -541,7 +543,7 @@ def retention_forward(q, k, v, gamma, y, *, cu_seqlens=None, states=None, slots=
 def retention_backward(q, k, v, gamma, dy, dq, dk, dv, *, cu_seqlens=None, scale=1.0, feature="identity",
                        workspace=None, stream=None):
     """Gradients of retention_forward (without states) from dy = dL/dY; dq, dk and dv are written.
-    Shapes as there; every tensor may have its own strides."""
+    Shapes and workspace as there; every tensor may have its own strides."""
     B, H, N, d = _retention_sizes(q, cu_seqlens)
     _expect_like(q, ("k", k), ("v", v), ("dy", dy), ("dq", dq), ("dk", dk), ("dv", dv))
     _expect_fast(gamma, "gamma", (H,), torch.float32)
