@@ -18,7 +18,7 @@ constexpr int kTok = 64;  // tokens of a chunk
 // w_s = gamma^(len-1-s), with X [D][ES] and the chunk's A, B, C and P in shared memory and 4 x 4 (X: up to 8 x 4)
 // register tiles; the masked half of the first two products is left out by blocks of 4 rows.  With SUM only X is
 // formed: the segment's own sum.  Bound by shared memory: 8 loads of 16 bytes a lane, four cycles each, for 32 multiply-adds of pairs (12 heads of 4096
-// tokens, d = 64: 79 us; FMA units 30 % busy).  The multiply-adds go in pairs; the next chunk's rows are on their way in
+// tokens, d = 64: 80 us; FMA units 30 % busy).  The multiply-adds go in pairs; the next chunk's rows are on their way in
 // registers while X is computed.  (C and X transposed, so that pairs lie side by side, cost more in their stores and
 // uneven loads than it saved: 124 us against 97.)
 template <int D>
