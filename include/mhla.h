@@ -390,6 +390,71 @@ mhla_status retention_step(const void* q, const mhla_strides* q_strides, const v
 mhla_status retention_copy_states(float* states, int n_slots, int H, int d, const int* src, const int* dst, int n,
                                   void* stream);
 
+/* --------------------------------------------------------------- gated scan
+ * A recurrence with a gate of its own for every token and channel ([LA] §七, the
+ * gated update S_t = G_t * S_{t-1} + ..., for a state of one vector):
+ *   h_t = a_t h_{t-1} + b_t,   y_t = h_t      (elementwise over the D channels)
+ *   GATED_SCAN_SIGMOID: a = sigmoid(g),  b = (1 - a) x
+ *   GATED_SCAN_LOG    : a = exp(g),      b = x     (g <= 0 is the caller's contract)
+ *   GATED_SCAN_DECAY  : a = g,           b = x     (g in [0, 1] is the caller's contract)
+ * Conventions of the gated_scan_* entries:
+ *   - Token tensors are [B, N, D] (the step: [B, D]), D a multiple of 8 (bf16) or
+ *     4 (fp32), with any strides (the members b and n of mhla_strides; h is not
+ *     used) under the rules of the retention_* entries; an input may have stride
+ *     0 in b.  Outputs overlap neither inputs nor each other nor themselves.
+ *   - cu_seqlens as there: NULL, or device int32 [B + 1] with tensors [1, N, D].
+ *     Rows of no sequence are not written.
+ *   - At most 2^31 - 1024 tokens a sequence (packed: a call): MHLA_ERR_UNSUPPORTED.
+ *   - states: [n_slots, D] fp32, slots as there: a sequence whose slot is outside
+ *     [0, n_slots), or is the slot of a sequence before it, has none.
+ *   - h, the gradients and every sum are fp32.  Sums have a fixed order: equal
+ *     calls give equal bits.  No workspace and no device-side wait.
+ *   - Not-a-number or infinite values of a token reach later tokens (backward:
+ *     earlier ones too) of its own sequence and channel only. */
+typedef enum { GATED_SCAN_SIGMOID = 0, GATED_SCAN_LOG = 1, GATED_SCAN_DECAY = 2 } gated_scan_gate;
+
+/* Rows of D floats that gated_scan_forward keeps for gated_scan_backward: the
+ * state before every 64th token of the tensors' rows.  B, N: the first two sizes
+ * of the token tensors (packed: 1 and all tokens); 0 if they are invalid. */
+long long gated_scan_checkpoint_rows(int B, int N);
+
+/* The outputs of whole prompts.
+ *   states      : NULL, or read (load_state = 1: a sequence starts from its slot's
+ *                 state; 0: from zero) and written (the state after its last
+ *                 token).  A sequence without a slot starts from zero and its
+ *                 state is not kept; one without tokens leaves its slot as it is.
+ *   checkpoints : NULL, or [gated_scan_checkpoint_rows][D] fp32, written, for
+ *                 gated_scan_backward.
+ *   B*N*D = 0 returns MHLA_OK without a launch. */
+mhla_status gated_scan_forward(const void* x, const mhla_strides* x_strides, const void* g, const mhla_strides* g_strides,
+                               void* y, const mhla_strides* y_strides, int B, int N, int D, const int* cu_seqlens,
+                               float* states, const int* slots, int n_slots, int load_state, float* checkpoints,
+                               mhla_dtype dt, int gate, void* stream);
+
+/* The gradients of gated_scan_forward:
+ *   G_t = dy_t + a_{t+1} G_{t+1}  (the last token: dy_t + dh_last),  da_t = G_t h_{t-1}
+ *   SIGMOID: dx = (1 - a) G, dg = a (1 - a) G (h_{t-1} - x);  LOG: dx = G, dg = a da;
+ *   DECAY: dx = G, dg = da;   dh0 = a_1 G_1
+ *   checkpoints : those of the forward call with the same x, g and starts
+ *   h0          : [B, D] fp32, the states that the forward call started from, NULL: zero
+ *   dh_last     : [B, D] fp32, dL/d(last state), NULL: zero
+ *   dh0         : [B, D] fp32 or NULL: written, a sequence without tokens: dh_last
+ *   dx, dg      : written (not accumulated), of the full shape also where an input
+ *                 is shared by stride 0.
+ *   Rows of h0, dh_last and dh0 are the sequences in their order. */
+mhla_status gated_scan_backward(const void* x, const mhla_strides* x_strides, const void* g,
+                                const mhla_strides* g_strides, const void* dy, const mhla_strides* dy_strides,
+                                const float* checkpoints, void* dx, const mhla_strides* dx_strides, void* dg,
+                                const mhla_strides* dg_strides, int B, int N, int D, const int* cu_seqlens,
+                                const float* h0, const float* dh_last, float* dh0, mhla_dtype dt, int gate, void* stream);
+
+/* One token for each of B rows: updates the rows' states and writes out.  x, g,
+ * out: [B, D]; of the strides b is used.  A row without a slot is left out:
+ * neither its output nor a state is touched. */
+mhla_status gated_scan_step(const void* x, const mhla_strides* x_strides, const void* g, const mhla_strides* g_strides,
+                            float* states, const int* slots, int n_slots, void* out, const mhla_strides* out_strides,
+                            int B, int D, mhla_dtype dt, int gate, void* stream);
+
 /* Workspace bytes for rala_forward; 0 if the sizes are invalid. */
 size_t rala_workspace_bytes(int B, int H, int N, int d, int cx);
 

@@ -8,6 +8,10 @@ binding.  Build it with :func:`token_level_head_gb300.build.build_library`.
 from .binding import (  # noqa: F401
     EXPORTED,
     MhlaError,
+    gated_scan_backward,
+    gated_scan_checkpoint_rows,
+    gated_scan_forward,
+    gated_scan_step,
     linattn_decode_step,
     linattn_decode_steps,
     load,

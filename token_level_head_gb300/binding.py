@@ -53,6 +53,10 @@ _SIGNATURES = {
     "retention_backward": (_i, [_vp] * 15 + [_i] * 4 + [_vp, _i, _vp, _vp, _sz, _vp]),
     "retention_step": (_i, [_vp] * 9 + [_i, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
     "retention_copy_states": (_i, [_vp, _i, _i, _i, _vp, _vp, _i, _vp]),
+    "gated_scan_checkpoint_rows": (ctypes.c_longlong, [_i, _i]),
+    "gated_scan_forward": (_i, [_vp] * 6 + [_i] * 3 + [_vp, _vp, _vp, _i, _i, _vp, _i, _i, _vp]),
+    "gated_scan_backward": (_i, [_vp] * 11 + [_i] * 3 + [_vp] * 4 + [_i, _i, _vp]),
+    "gated_scan_step": (_i, [_vp] * 6 + [_i, _vp, _vp, _i, _i, _i, _i, _vp]),
     "mhla_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
 }
 
@@ -597,6 +601,128 @@ def retention_copy_states(states, src, dst, *, stream=None):
     _retention_call("retention_copy_states", dev,
                     (states.data_ptr(), slots, H, d, src.data_ptr(), dst.data_ptr(), n), stream)
     return states
+
+
+GATES = {"sigmoid": 0, "log": 1, "decay": 2}
+
+
+def _gate(gate):
+    try:
+        return GATES[gate]
+    except (KeyError, TypeError):
+        raise ValueError(f"gate: {gate!r}, one of {', '.join(GATES)}") from None
+
+
+@functools.lru_cache(maxsize=1024)
+def _c_scan_strides(st):
+    return ctypes.byref(_Strides(st[0], 0, st[1] if len(st) == 3 else 0))
+
+
+def _scan_strided(t, name):
+    """(pointer, strides) of a tensor [B, N, D] or [B, D] with contiguous rows."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {st[-1]}")
+    return t.data_ptr(), _c_scan_strides(st)
+
+
+def _scan_sizes(x, cu_seqlens):
+    """B (sequences), N (packed: all tokens), D of x [B, N, D]; packed: x [1, tokens, D]."""
+    if x.dim() != 3:
+        raise ValueError(f"x: expected [B, N, D], got shape {tuple(x.shape)}")
+    B, N, D = x.shape
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError(f"x: expected [1, tokens, D] with cu_seqlens, got shape {tuple(x.shape)}")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError(f"cu_seqlens: expected [sequences + 1], got shape {tuple(cu_seqlens.shape)}")
+        _expect_fast(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
+        B = cu_seqlens.numel() - 1
+    _fits_int(B=B, N=N, D=D)
+    return B, N, D
+
+
+def _scan_states(states, slots, B, D):
+    if states is None:
+        if slots is not None:
+            raise ValueError("slots: given without states")
+        return 0
+    if states.dim() != 2:
+        raise ValueError(f"states: expected [slots, D], got shape {tuple(states.shape)}")
+    _expect_fast(states, "states", (states.shape[0], D), torch.float32)
+    _expect_fast(slots, "slots", (B,), torch.int32)
+    _fits_int(slots=states.shape[0])
+    return states.shape[0]
+
+
+def gated_scan_checkpoint_rows(B: int, N: int) -> int:
+    """Rows of the fp32 [rows, D] tensor that gated_scan_forward keeps for gated_scan_backward; B, N: the first two
+    sizes of x."""
+    return 0 if max(B, N) > 0x7fffffff else int(load().gated_scan_checkpoint_rows(B, N))
+
+
+def _scan_checkpoints(checkpoints, x, D):
+    _expect_fast(checkpoints, "checkpoints", (gated_scan_checkpoint_rows(x.shape[0], x.shape[1]), D), torch.float32)
+
+
+def gated_scan_forward(x, g, y, *, gate="sigmoid", cu_seqlens=None, states=None, slots=None, load_state=False,
+                       checkpoints=None, stream=None):
+    """h_t = a_t h_{t-1} + b_t, y_t = h_t over whole prompts, with a gate of its own for every token and channel:
+    "sigmoid" a = sigmoid(g), b = (1 - a) x; "log" a = exp(g), b = x; "decay" a = g, b = x.  x/g/y [B, N, D] with any
+    strides (rows contiguous); packed sequences: [1, tokens, D] and int32 ``cu_seqlens`` [sequences + 1].  ``states``
+    [slots, D] fp32 receives the final states (``slots``: the slot of each sequence, int32); with ``load_state`` the
+    sequences start from them.  ``checkpoints`` (``gated_scan_checkpoint_rows``) is written for the backward pass."""
+    B, N, D = _scan_sizes(x, cu_seqlens)
+    _expect_like(x, ("g", g), ("y", y))
+    if load_state and states is None:
+        raise ValueError("load_state: needs states")
+    n_slots = _scan_states(states, slots, B, D)
+    if checkpoints is not None:
+        _scan_checkpoints(checkpoints, x, D)
+    dev = _retention_device((x, g, y), (cu_seqlens, states, slots, checkpoints))
+    _retention_call("gated_scan_forward", dev,
+                    (*_scan_strided(x, "x"), *_scan_strided(g, "g"), *_scan_strided(y, "y"), B, N, D,
+                     _address(cu_seqlens), _address(states), _address(slots), n_slots, 1 if load_state else 0,
+                     _address(checkpoints), _dtype(x), _gate(gate)), stream)
+    return y
+
+
+def gated_scan_backward(x, g, dy, checkpoints, dx, dg, *, gate="sigmoid", cu_seqlens=None, h0=None, dh_last=None,
+                        dh0=None, stream=None):
+    """Gradients of gated_scan_forward from dy = dL/dy and, where given, ``dh_last`` = dL/d(last states): dx and dg are
+    written, and ``dh0`` = dL/d(starts).  ``checkpoints``: of the forward call; ``h0``: the states that it started from
+    (load_state; None: zero).  h0, dh_last, dh0: fp32 [sequences, D]."""
+    B, N, D = _scan_sizes(x, cu_seqlens)
+    _expect_like(x, ("g", g), ("dy", dy), ("dx", dx), ("dg", dg))
+    if checkpoints is None:
+        raise ValueError("checkpoints: required")
+    _scan_checkpoints(checkpoints, x, D)
+    for name, t in (("h0", h0), ("dh_last", dh_last), ("dh0", dh0)):
+        _expect_fast(t, name, (B, D), torch.float32)
+    dev = _retention_device((x, g, dy, dx, dg), (cu_seqlens, checkpoints, h0, dh_last, dh0))
+    _retention_call("gated_scan_backward", dev,
+                    (*_scan_strided(x, "x"), *_scan_strided(g, "g"), *_scan_strided(dy, "dy"), checkpoints.data_ptr(),
+                     *_scan_strided(dx, "dx"), *_scan_strided(dg, "dg"), B, N, D, _address(cu_seqlens), _address(h0),
+                     _address(dh_last), _address(dh0), _dtype(x), _gate(gate)), stream)
+    return dx, dg
+
+
+def gated_scan_step(x, g, states, out, *, gate="sigmoid", slots=None, stream=None):
+    """One token for every row: x/g/out [B, D] with any strides (rows contiguous), states [slots, D] fp32 (updated);
+    ``slots`` int32 [B], an entry outside the pool leaves its row out."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [B, D], got shape {tuple(x.shape)}")
+    B, D = x.shape
+    _fits_int(B=B, D=D)
+    _expect_like(x, ("g", g), ("out", out))
+    if states is None:
+        raise ValueError("states: required")
+    n_slots = _scan_states(states, slots, B, D)
+    dev = _retention_device((x, g, out), (states, slots))
+    _retention_call("gated_scan_step", dev,
+                    (*_scan_strided(x, "x"), *_scan_strided(g, "g"), states.data_ptr(), _address(slots), n_slots,
+                     *_scan_strided(out, "out"), B, D, _dtype(x), _gate(gate)), stream)
+    return out
 
 
 def rala_forward(q, k, v, x, w, y, *, workspace=None, stream=None):
