@@ -6,11 +6,13 @@
 // through shared memory; then every thread knows the state before its rows and runs them once more.  The gradient
 // runs the same way from the end: c_t = a_t (dy_t + c_{t+1}), G_t = dy_t + c_{t+1}.
 //
-// Bound: memory (forward 3 tensors, backward 5; about 20 instructions a value).  A block takes a tile of kRows rows and
-// LW * 16 bytes of channels; tiles behind one another are taken by the blocks of a cluster (up to 16), which exchange
-// their (A, B) through distributed shared memory, and a cluster walks along the sequence.  So x and g are read once and
-// no memory, flag or wait is shared between clusters.
+// Bound: memory (forward 3 tensors, backward 5), next to it the instructions (at the memory's rate an SM has 32 a bf16
+// value and lane forwards, 53 backwards).  A block takes a tile of rows and LW lanes of channels; tiles behind one another
+// are taken by the blocks of a cluster, which exchange their (A, B) through distributed shared memory, and a cluster walks
+// along the sequence.  So x and g are read once and no memory, flag or wait is shared between clusters.
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "gated_scan.h"
 #include "retention.cuh"
@@ -21,63 +23,132 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
-constexpr int V = 4;  // channels of a thread
+constexpr int kMaxCluster = 8;
+constexpr int P = 1, V = 2 * P;  // channels of a thread: a pair, so that a warp of bf16 has a row of 128 bytes to itself
 
-// A thread's rows of a tile and the lanes that lie beside one another: 128 bytes of channels, 128 rows a block.
+// A thread's rows of a tile (32 values each of a and b in registers) and the lanes of 128 bytes of channels.
 template <typename T>
 struct Tile;
 template <>
 struct Tile<__nv_bfloat16> {
-  using Raw = uint2;
-  static constexpr int R = 8, LW = 16;
+  static constexpr int R = 16, WIDE = 32;
 };
 template <>
 struct Tile<float> {
-  using Raw = uint4;
-  static constexpr int R = 4, LW = 8;
+  static constexpr int R = 8, WIDE = 16;
 };
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
-  f[0] = __uint_as_float(u.x);
-  f[1] = __uint_as_float(u.y);
-  f[2] = __uint_as_float(u.z);
-  f[3] = __uint_as_float(u.w);
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
 }
-__device__ __forceinline__ void unpack(const uint2& u, float (&f)[4]) {
-  f[0] = __uint_as_float(u.x << 16);
-  f[1] = __uint_as_float(u.x & 0xffff0000u);
-  f[2] = __uint_as_float(u.y << 16);
-  f[3] = __uint_as_float(u.y & 0xffff0000u);
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// N pairs of channels as they lie in memory.
+template <typename T, int N>
+struct Io;
+template <>
+struct Io<float, 1> {
+  using Raw = uint2;
+};
+template <>
+struct Io<float, 2> {
+  using Raw = uint4;
+};
+template <>
+struct Io<__nv_bfloat16, 1> {
+  using Raw = unsigned;
+};
+template <>
+struct Io<__nv_bfloat16, 2> {
+  using Raw = uint2;
+};
+__device__ __forceinline__ float2 bf16_pair(unsigned u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
-__device__ __forceinline__ void store(float* p, const float (&f)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+template <typename T>
+__device__ __forceinline__ void unpack(unsigned u, float2 (&f)[1]) {
+  f[0] = bf16_pair(u);
 }
-__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[4]) {
-  __nv_bfloat162 r[2] = {__floats2bfloat162_rn(f[0], f[1]), __floats2bfloat162_rn(f[2], f[3])};
-  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r);
+template <typename T>
+__device__ __forceinline__ void unpack(const uint2& u, float2 (&f)[1]) {
+  f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
 }
-__device__ __forceinline__ void load_f(const float* p, float (&f)[4]) {
-  *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
+template <typename T>
+__device__ __forceinline__ void unpack(const uint2& u, float2 (&f)[2]) {
+  f[0] = bf16_pair(u.x);
+  f[1] = bf16_pair(u.y);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+// The next row's pointer, taken row by row: sixteen rows' pointers in registers would be spilled.
+template <typename T>
+__device__ __forceinline__ T* next_row(T* p, long long sn) {
+  p += sn;
+  asm volatile("" : "+l"(p));
+  return p;
 }
 
-// a and 1 - a of a gate.  sigmoid: from exp(-|g|), so that neither 1 + e overflows nor the smaller of the two is a
-// difference of nearly equal numbers; the larger is 1 - the smaller, rounded once (a long memory multiplies thousands of
-// gates near 1, and their errors).
-template <int GATE>
-__device__ __forceinline__ void gate_of(float g, float* a, float* rest) {
+__device__ __forceinline__ void store(float* p, const float2 (&f)[1]) { *reinterpret_cast<float2*>(p) = f[0]; }
+__device__ __forceinline__ void store(float* p, const float2 (&f)[2]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+}
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&f)[1]) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f[0].x, f[0].y);
+}
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&f)[2]) {
+  __nv_bfloat162 r[2] = {__floats2bfloat162_rn(f[0].x, f[0].y), __floats2bfloat162_rn(f[1].x, f[1].y)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(r);
+}
+__device__ __forceinline__ void load_f(const float* p, float2 (&f)[1]) { f[0] = *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void load_f(const float* p, float2 (&f)[2]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = make_float2(v.x, v.y);
+  f[1] = make_float2(v.z, v.w);
+}
+template <int N>
+__device__ __forceinline__ void fill(float2 (&f)[N], float v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = both(v);
+}
+
+// exp(x).  bf16 tensors: the hardware's base-2 exponential of x log2 e (log2 e = 1.4426950408889634), off by
+// |x| 2^-24 + 2^-22 at most, far below what a bf16 gate says; fp32: expf.  Not-a-number stays.
+template <typename T>
+__device__ __forceinline__ float exp_of(float x) {
+  if (sizeof(T) == 4) return expf(x);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+  return e;
+}
+
+// a and the factor of x of a gate.  sigmoid: from exp(-|g|), so that nothing overflows; of a and 1 - a the smaller is
+// e / (1 + e), the larger 1 - the smaller, rounded once (a long memory multiplies thousands of gates near 1, and their
+// errors).
+template <typename T, int GATE>
+__device__ __forceinline__ void gate_of(float2 g, float2* a, float2* rest) {
   if (GATE == GATED_SCAN_DECAY) {
     *a = g;
-    *rest = 1.f;
   } else if (GATE == GATED_SCAN_LOG) {
-    *a = expf(g);
-    *rest = 1.f;
+    *a = make_float2(exp_of<T>(g.x), exp_of<T>(g.y));
   } else {
-    const float e = expf(-fabsf(g));
-    const float s = __fdividef(e, 1.f + e), l = 1.f - s;
-    *a = g > 0.f ? l : s;
-    *rest = g > 0.f ? s : l;
+    const float2 e = make_float2(exp_of<T>(-fabsf(g.x)), exp_of<T>(-fabsf(g.y)));
+    const float2 d = add2(e, both(1.f));
+    const float2 s = mul2(e, make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y)));
+    const float2 l = fma2(s, both(-1.f), both(1.f));
+    *a = make_float2(g.x > 0.f ? l.x : s.x, g.y > 0.f ? l.y : s.y);
+    *rest = make_float2(g.x > 0.f ? s.x : l.x, g.y > 0.f ? s.y : l.y);
   }
+}
+template <int GATE>
+__device__ __forceinline__ float2 input_of(float2 x, float2 rest) {
+  return GATE == GATED_SCAN_SIGMOID ? mul2(rest, x) : x;
 }
 
 // ---- rows of a tile: which are tokens, and where sequences begin and end
@@ -149,100 +220,178 @@ template <bool PACKED>
 __device__ __forceinline__ float carry_on(float A, float B, float h) {
   return is_cut<PACKED>(A) ? B : fmaf(A, h, B);
 }
+template <bool PACKED>
+__device__ __forceinline__ float2 carry_on(float2 A, float2 B, float2 h) {
+  const float2 r = fma2(A, h, B);
+  return make_float2(is_cut<PACKED>(A.x) ? B.x : r.x, is_cut<PACKED>(A.y) ? B.y : r.y);
+}
 // A of a run with A, behind one with `before`.
 template <bool PACKED>
 __device__ __forceinline__ float join(float A, float before) {
   return is_cut<PACKED>(A) ? A : A * before;
 }
+template <bool PACKED>
+__device__ __forceinline__ float2 join(float2 A, float2 before) {
+  const float2 r = mul2(A, before);
+  return make_float2(is_cut<PACKED>(A.x) ? A.x : r.x, is_cut<PACKED>(A.y) ? A.y : r.y);
+}
 
 // ---- the scan of a block's tile over its threads
+template <bool REVERSE>
+__device__ __forceinline__ float2 shift(float2 v, int o) {
+  return make_float2(REVERSE ? __shfl_down_sync(0xffffffffu, v.x, o) : __shfl_up_sync(0xffffffffu, v.x, o),
+                     REVERSE ? __shfl_down_sync(0xffffffffu, v.y, o) : __shfl_up_sync(0xffffffffu, v.y, o));
+}
 // Row groups lie LW lanes apart.  (A, B) of the thread's rows becomes that of the row groups before it in the warp
 // (after it, if REVERSE), and (wA, wB), valid in the warp's last row group (first), that of the whole warp.
 template <int LW, bool REVERSE, bool PACKED>
-__device__ __forceinline__ void scan_warp(float (&A)[V], float (&B)[V], float (&wA)[V], float (&wB)[V], int lane) {
+__device__ __forceinline__ void scan_warp(float2 (&A)[P], float2 (&B)[P], float2 (&wA)[P], float2 (&wB)[P], int lane) {
+  if (LW == 32) {  // one row group
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      wA[i] = A[i];
+      wB[i] = B[i];
+      A[i] = both(1.f);
+      B[i] = both(0.f);
+    }
+    return;
+  }
   const int place = REVERSE ? 31 - lane : lane;
 #pragma unroll
-  for (int o = LW; o < 32; o <<= 1) {
+  for (int o = LW; o < 16; o <<= 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float ua = REVERSE ? __shfl_down_sync(0xffffffffu, A[v], o) : __shfl_up_sync(0xffffffffu, A[v], o);
-      const float ub = REVERSE ? __shfl_down_sync(0xffffffffu, B[v], o) : __shfl_up_sync(0xffffffffu, B[v], o);
+    for (int i = 0; i < P; ++i) {
+      const float2 ua = shift<REVERSE>(A[i], o), ub = shift<REVERSE>(B[i], o);
       if (place >= o) {
-        B[v] = carry_on<PACKED>(A[v], B[v], ub);
-        A[v] = join<PACKED>(A[v], ua);
+        B[i] = carry_on<PACKED>(A[i], B[i], ub);
+        A[i] = join<PACKED>(A[i], ua);
       }
     }
   }
+  // the step over half a warp: with two row groups it is the only one, and gives what lies before
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    wA[v] = A[v];
-    wB[v] = B[v];
-    const float ua = REVERSE ? __shfl_down_sync(0xffffffffu, A[v], LW) : __shfl_up_sync(0xffffffffu, A[v], LW);
-    const float ub = REVERSE ? __shfl_down_sync(0xffffffffu, B[v], LW) : __shfl_up_sync(0xffffffffu, B[v], LW);
-    A[v] = place >= LW ? ua : 1.f;
-    B[v] = place >= LW ? ub : 0.f;
+  for (int i = 0; i < P; ++i) {
+    const float2 ua = shift<REVERSE>(A[i], 16), ub = shift<REVERSE>(B[i], 16);
+    wA[i] = place >= 16 ? join<PACKED>(A[i], ua) : A[i];
+    wB[i] = place >= 16 ? carry_on<PACKED>(A[i], B[i], ub) : B[i];
+    const float2 pa = LW == 16 ? ua : shift<REVERSE>(wA[i], LW), pb = LW == 16 ? ub : shift<REVERSE>(wB[i], LW);
+    A[i] = place >= LW ? pa : both(1.f);
+    B[i] = place >= LW ? pb : both(0.f);
   }
 }
 
 template <int CW>
 struct ScanShared {
-  float2 warp[2][kWarps][CW];  // (A, B) of the warps, by the tile's parity
-  float2 block[2][kMaxCluster][CW];  // of the cluster's blocks, which write them here
-  float carry[2][CW];          // the state entering the block's tile
+  float wa[2][kWarps][CW], wb[2][kWarps][CW];            // A, B of the warps, by the tile's parity
+  float ba[2][kMaxCluster][CW], bb[2][kMaxCluster][CW];  // of the cluster's blocks, which write them here
+  float carry[2][CW];                                    // the state entering the block's tile
 };
 
 // The state entering the block's tile, for every channel, in s.carry[par] (whole block), and in `running` (threads
-// below CW: a channel each) that behind the cluster's tiles.  The warps' (A, B) are in s.warp[par].
+// below CW: a channel each) that behind the cluster's tiles.  The warps' A, B are in s.wa, s.wb[par].
 template <int CW, bool REVERSE, bool PACKED>
-__device__ __forceinline__ void exchange(ScanShared<CW>& s, int par, float* running, bool clustered) {
+__device__ __forceinline__ void exchange(ScanShared<CW>& s, int par, float* running, int n, int rank) {
   const int c = threadIdx.x;
-  if (!clustered) {
-    // the tile's entering state was written for this parity one tile ago; fold the next one meanwhile
+  if (n == 1) {
     if (c < CW) s.carry[par][c] = *running;
     __syncthreads();
     if (c < CW) {
       float h = *running;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 f = s.warp[par][REVERSE ? kWarps - 1 - w : w][c];
-        h = carry_on<PACKED>(f.x, f.y, h);
+      for (int i = 0; i < kWarps; ++i) {
+        const int w = REVERSE ? kWarps - 1 - i : i;
+        h = carry_on<PACKED>(s.wa[par][w][c], s.wb[par][w][c], h);
       }
       *running = h;
     }
     return;
   }
   cg::cluster_group cl = cg::this_cluster();
-  const int n = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   __syncthreads();
   if (c < CW) {
     float A = 1.f, B = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 f = s.warp[par][REVERSE ? kWarps - 1 - w : w][c];
-      B = carry_on<PACKED>(f.x, f.y, B);
-      A = join<PACKED>(f.x, A);
+    for (int i = 0; i < kWarps; ++i) {
+      const int w = REVERSE ? kWarps - 1 - i : i;
+      const float fa = s.wa[par][w][c];
+      B = carry_on<PACKED>(fa, s.wb[par][w][c], B);
+      A = join<PACKED>(fa, A);
     }
-    for (int i = 0; i < n; ++i) cl.map_shared_rank(&s.block[par][rank][0], i)[c] = make_float2(A, B);
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i)
+      if (i < n) {
+        cl.map_shared_rank(&s.ba[par][rank][0], i)[c] = A;
+        cl.map_shared_rank(&s.bb[par][rank][0], i)[c] = B;
+      }
   }
   cl.sync();
   if (c < CW) {
-    float h = *running;
-    for (int i = 0; i < n; ++i) {
-      if (i == rank) s.carry[par][c] = h;
-      const float2 f = s.block[par][i][c];
-      h = carry_on<PACKED>(f.x, f.y, h);
+    float h = *running, mine = h;
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) {
+      if (i == rank) mine = h;
+      if (i < n) h = carry_on<PACKED>(s.ba[par][i][c], s.bb[par][i][c], h);
     }
+    s.carry[par][c] = mine;
     *running = h;
   }
   __syncthreads();
 }
+// The state before the warp: over the warps from `from` on (backwards: down to it).
+template <int CW, bool REVERSE, bool PACKED>
+__device__ __forceinline__ void over_warps(const float (&wa)[kWarps][CW], const float (&wb)[kWarps][CW], int cl, int warp,
+                                           int from, float2 (&h)[P]) {
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const int w = REVERSE ? kWarps - 1 - i : i;
+    if (REVERSE ? w > warp : w >= from && w < warp) {
+      float2 A[P], B[P];
+      load_f(&wa[w][cl], A);
+      load_f(&wb[w][cl], B);
+#pragma unroll
+      for (int j = 0; j < P; ++j) h[j] = carry_on<PACKED>(A[j], B[j], h[j]);
+    }
+  }
+}
+
+// ---- tiles in shared memory
+// A tile's ROWS rows of CW channels of one tensor; row groups are 32 bytes further apart where several of them are read at
+// once, so that they lie in banks of their own.
+template <typename T, int LW>
+struct Stage {
+  static constexpr int CW = V * LW, kR = Tile<T>::R, ROWS = kThreads / LW * kR, PIECES = CW * (int)sizeof(T) / 16;
+  static constexpr int PAD = LW < Tile<T>::WIDE ? 32 / (int)sizeof(T) : 0;      // elements
+  static constexpr int ELEMS = ROWS * CW + ROWS / kR * PAD;
+  static __device__ __forceinline__ int at(int row) { return row * CW + row / kR * PAD; }
+  // The copy of rows [row0, row0 + ROWS) and channels from c0 on (D - c0 at most), asynchronously; zeros for rows outside
+  // [lo, hi) and channels behind D.
+  static __device__ __forceinline__ void fetch(T* to, const T* from, long long sn, long long row0, int lo, int hi, int c0,
+                                               int D) {
+    constexpr int N = ROWS * PIECES / kThreads, STEP = kThreads / PIECES;
+    const int piece = threadIdx.x % PIECES, r = threadIdx.x / PIECES;
+    const int c = piece * (16 / (int)sizeof(T));
+    const bool on = c0 + c < D;
+    const T* src = from + (on ? c0 + c : 0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long row = row0 + r + i * STEP;
+      const bool ok = on && row >= lo && row < hi;
+      const unsigned dst = (unsigned)__cvta_generic_to_shared(to + at(r + i * STEP) + c);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src + (ok ? row * sn : 0)), "r"(ok ? 16 : 0)
+                   : "memory");
+    }
+  }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // ---- forward
-template <typename T, int GATE, bool PACKED>
+template <typename T, int GATE, int LW, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
-  using Raw = typename Tile<T>::Raw;
-  constexpr int LW = Tile<T>::LW, kR = Tile<T>::R, CW = V * LW, ROWS = kThreads / LW * kR, GROUPS = 32 / LW;
-  __shared__ ScanShared<CW> s;
+  using Raw = typename Io<T, P>::Raw;
+  using St = Stage<T, LW>;
+  constexpr int kR = St::kR, CW = St::CW, ROWS = St::ROWS, GROUPS = 32 / LW;
+  __shared__ __align__(16) ScanShared<CW> s;
   __shared__ MarkRows<PACKED ? ROWS : 1> marks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % cluster), chain = (int)(blockIdx.x / cluster);
@@ -250,8 +399,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
   const int cl = (tid % LW) * V, c = c0 + cl;         // the thread's channels
   const int r0 = (warp * GROUPS + lane / LW) * kR;    // and rows of the tile
   const bool on = c < p.D;
-  const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb + c;
-  const T* g = static_cast<const T*>(p.g.p) + (long long)batch * p.g.sb + c;
+  const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb;
+  const T* g = static_cast<const T*>(p.g.p) + (long long)batch * p.g.sb;
   T* y = static_cast<T*>(const_cast<void*>(p.y.p)) + (long long)batch * p.y.sb + c;
   int lo = 0, hi = p.N;
   if (PACKED) {
@@ -260,112 +409,125 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
   }
   const int tiles = ret_pieces(p.N, ROWS), kept_rows = ret_pieces(p.N, kScanKept);
   float running = 0.f;
-  Raw nx[kR], ng[kR];
-  const auto fetch = [&](int t) {
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const long long row = (long long)t * ROWS + r0 + r;
-      const bool ok = on && t < tiles && row >= lo && row < hi;
-      nx[r] = ok ? *reinterpret_cast<const Raw*>(x + row * p.x.sn) : Raw{};
-      ng[r] = ok ? *reinterpret_cast<const Raw*>(g + row * p.g.sn) : Raw{};
+  extern __shared__ __align__(16) uint8_t raw[];
+  T* stage = reinterpret_cast<T*>(raw);  // [2][x, g]
+  const auto fetch = [&](int t, int buf) {
+    T* to = stage + buf * 2 * St::ELEMS;
+    if (t < tiles) {
+      St::fetch(to, x, p.x.sn, (long long)t * ROWS, lo, hi, c0, p.D);
+      St::fetch(to + St::ELEMS, g, p.g.sn, (long long)t * ROWS, lo, hi, c0, p.D);
     }
+    copies_commit();
   };
-  fetch(rank);
+  fetch(rank, 0);
   if (cluster > 1) cg::this_cluster().sync();  // every block runs: its shared memory may be written
   int par = 0;
   for (int t0 = 0; t0 < tiles; t0 += cluster, par ^= 1) {
     const int t = t0 + rank, row0 = (int)min((long long)t * ROWS, (long long)p.N);
-    if (PACKED) mark_rows(p, row0, marks);
+    copies_wait0();
+    if (PACKED)
+      mark_rows(p, row0, marks);
+    else
+      __syncthreads();  // (the tile is there, the other buffer has been read)
+    fetch(t + cluster, par ^ 1);
     const Marks m = marks_of<kR>(p, PACKED ? &marks : nullptr, row0, r0, lo, hi);
-    float a[kR][V], b[kR][V];
+    const unsigned first = m.first & m.live;
+    const T *sx = stage + par * 2 * St::ELEMS + St::at(r0) + cl, *sg = sx + St::ELEMS;
+    float2 a[kR][P], b[kR][P];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      float gv[V];
-      unpack(nx[r], b[r]);
-      unpack(ng[r], gv);
-      const bool live = m.live >> r & 1;
+      float2 gv[P], xv[P];
+      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
+      unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float rest;
-        gate_of<GATE>(gv[v], &a[r][v], &rest);
-        if (GATE == GATED_SCAN_SIGMOID) b[r][v] *= rest;
-        if (!live) {
-          a[r][v] = 1.f;
-          b[r][v] = 0.f;
-        }
+      for (int i = 0; i < P; ++i) {
+        float2 rest;
+        gate_of<T, GATE>(gv[i], &a[r][i], &rest);
+        b[r][i] = input_of<GATE>(xv[i], rest);
       }
     }
-    fetch(t + cluster);
-    if (m.first & m.live) {
+    if (m.live != (1u << kR) - 1) {
 #pragma unroll
       for (int r = 0; r < kR; ++r)
-        if ((m.first & m.live) >> r & 1) {
+        if (!(m.live >> r & 1)) {
+          fill(a[r], 1.f);
+          fill(b[r], 0.f);
+        }
+    }
+    if (first != 0) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+        if (first >> r & 1) {
           const int seq = PACKED ? marks.first[r0 + r] - 1 : batch;
           const int slot = p.load && on ? slot_of(p.slots, p.n_slots, seq) : -1;
-          float h[V];
+          float2 h[P];
           if (slot >= 0) load_f(p.states + (long long)slot * p.D + c, h);
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            if (slot >= 0) b[r][v] = fmaf(a[r][v], h[v], b[r][v]);
-            if (PACKED) a[r][v] = kCut;  // (dense: nothing comes before)
+          for (int i = 0; i < P; ++i) {
+            if (slot >= 0) b[r][i] = fma2(a[r][i], h[i], b[r][i]);
+            if (PACKED) a[r][i] = both(kCut);  // (dense: nothing comes before)
           }
         }
     }
-    float A[V], B[V], wA[V], wB[V];
+    float2 A[P], B[P], wA[P], wB[P];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      A[v] = a[0][v];
-      B[v] = b[0][v];
+    for (int i = 0; i < P; ++i) {
+      A[i] = a[0][i];
+      B[i] = b[0][i];
 #pragma unroll
       for (int r = 1; r < kR; ++r) {
-        B[v] = carry_on<PACKED>(a[r][v], b[r][v], B[v]);
-        A[v] = join<PACKED>(a[r][v], A[v]);
+        if (PACKED && (first >> r & 1)) {
+          B[i] = b[r][i];
+          A[i] = both(kCut);
+        } else {
+          B[i] = fma2(a[r][i], B[i], b[r][i]);
+          A[i] = mul2(A[i], a[r][i]);
+        }
       }
     }
     scan_warp<LW, false, PACKED>(A, B, wA, wB, lane);
     if (lane / LW == GROUPS - 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) s.warp[par][warp][cl + v] = make_float2(wA[v], wB[v]);
+      store(&s.wa[par][warp][cl], wA);
+      store(&s.wb[par][warp][cl], wB);
     }
-    exchange<CW, false, PACKED>(s, par, &running, cluster > 1);
-    float h[V];
+    exchange<CW, false, PACKED>(s, par, &running, cluster, rank);
+    float2 h[P];
+    load_f(&s.carry[par][cl], h);
+    over_warps<CW, false, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, h);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = s.carry[par][cl + v];
-      for (int w = 0; w < warp; ++w) {
-        const float2 f = s.warp[par][w][cl + v];
-        h[v] = carry_on<PACKED>(f.x, f.y, h[v]);
-      }
-      h[v] = carry_on<PACKED>(A[v], B[v], h[v]);
-    }
+    for (int i = 0; i < P; ++i) h[i] = carry_on<PACKED>(A[i], B[i], h[i]);
     const int row = row0 + r0;
     if (p.kept != nullptr && on && row < p.N && row % kScanKept == 0)
       store(p.kept + ((long long)batch * kept_rows + row / kScanKept) * p.D + c, h);
+    T* py = y + row * p.y.sn;
+    const bool whole = on && m.live == (1u << kR) - 1;
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = carry_on<PACKED>(a[r][v], b[r][v], h[v]);
-      if (on && m.live >> r & 1) {
-        store(y + (long long)(row + r) * p.y.sn, h);
-        if (p.states != nullptr && m.last >> r & 1) {
-          const int slot = slot_of(p.slots, p.n_slots, PACKED ? marks.last[r0 + r] - 1 : batch);
-          if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
-        }
+      for (int i = 0; i < P; ++i) h[i] = PACKED && (first >> r & 1) ? b[r][i] : fma2(a[r][i], h[i], b[r][i]);
+      if (whole || (on && m.live >> r & 1)) store(py, h);
+      py = next_row(py, p.y.sn);
+      if (p.states != nullptr && on && (m.last & m.live) >> r & 1) {
+        const int slot = slot_of(p.slots, p.n_slots, PACKED ? marks.last[r0 + r] - 1 : batch);
+        if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
       }
     }
   }
-  if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one reads its shared memory
+  if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one writes its shared memory
 }
 
 // ---- backward
-template <typename T, int GATE, bool PACKED>
+// A thread's rows three times: the runs of both directions; G from the last row on; h from the first row on, with what
+// goes out.  x, g and dy stay in registers as they came; the sigmoid is taken again in the third.
+template <typename T, int GATE, int LW, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
-  using Raw = typename Tile<T>::Raw;
-  constexpr int LW = Tile<T>::LW, kR = Tile<T>::R, CW = V * LW, ROWS = kThreads / LW * kR, GROUPS = 32 / LW;
+  using Raw = typename Io<T, P>::Raw;
+  using St = Stage<T, LW>;
+  constexpr int kR = St::kR, CW = St::CW, ROWS = St::ROWS, GROUPS = 32 / LW;
   constexpr int PER = kScanKept / (GROUPS * kR) > 1 ? kScanKept / (GROUPS * kR) : 1;  // warps of a kept state
-  static_assert((GROUPS * kR * PER) % kScanKept == 0, "a kept state at the first row of every PER warps");
-  __shared__ ScanShared<CW> s;
-  __shared__ float2 fwd[2][kWarps][CW];
+  static_assert((GROUPS * kR * PER) % kScanKept == 0 && kWarps % PER == 0, "a kept state at the first row of every PER warps");
+  __shared__ __align__(16) ScanShared<CW> s;
+  __shared__ __align__(16) float fwa[2][kWarps][CW], fwb[2][kWarps][CW];
   __shared__ MarkRows<PACKED ? ROWS : 1> marks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % cluster), chain = (int)(blockIdx.x / cluster);
@@ -373,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
   const int cl = (tid % LW) * V, c = c0 + cl;
   const int r0 = (warp * GROUPS + lane / LW) * kR;
   const bool on = c < p.D;
-  const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb + c;
-  const T* g = static_cast<const T*>(p.g.p) + (long long)batch * p.g.sb + c;
-  const T* dy = static_cast<const T*>(p.dy.p) + (long long)batch * p.dy.sb + c;
+  const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb;
+  const T* g = static_cast<const T*>(p.g.p) + (long long)batch * p.g.sb;
+  const T* dy = static_cast<const T*>(p.dy.p) + (long long)batch * p.dy.sb;
   T* dx = static_cast<T*>(const_cast<void*>(p.dx.p)) + (long long)batch * p.dx.sb + c;
   T* dg = static_cast<T*>(const_cast<void*>(p.dg.p)) + (long long)batch * p.dg.sb + c;
   int lo = 0, hi = p.N;
@@ -386,8 +548,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
     if (p.dh0 != nullptr && rank == 0)
       for (int i = tid / LW; i < p.B; i += kThreads / LW) {
         const int l = min(max(p.cu[i], 0), p.N);
-        if (on && p.cu[i + 1] <= l) {
-          float f[V] = {};
+        if (on && min(p.cu[i + 1], p.N) <= l) {
+          float2 f[P];
+          fill(f, 0.f);
           if (p.dh_last != nullptr) load_f(p.dh_last + (long long)i * p.D + c, f);
           store(p.dh0 + (long long)i * p.D + c, f);
         }
@@ -395,156 +558,152 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
   }
   const int tiles = ret_pieces(p.N, ROWS), kept_rows = ret_pieces(p.N, kScanKept);
   float running = 0.f;
+  extern __shared__ __align__(16) uint8_t raw[];
+  T* stage = reinterpret_cast<T*>(raw);  // [2][x, g, dy]
+  const auto fetch = [&](int t, int buf) {
+    T* to = stage + buf * 3 * St::ELEMS;
+    if (t >= 0) {
+      St::fetch(to, x, p.x.sn, (long long)t * ROWS, lo, hi, c0, p.D);
+      St::fetch(to + St::ELEMS, g, p.g.sn, (long long)t * ROWS, lo, hi, c0, p.D);
+      St::fetch(to + 2 * St::ELEMS, dy, p.dy.sn, (long long)t * ROWS, lo, hi, c0, p.D);
+    }
+    copies_commit();
+  };
+  fetch(tiles - 1 - rank, 0);
   if (cluster > 1) cg::this_cluster().sync();
   int par = 0;
   for (int t0 = 0; t0 < tiles; t0 += cluster, par ^= 1) {
     // tiles from the last one on; a cluster's last round may hold tiles before the first: without rows
     const int t = tiles - 1 - (t0 + rank);
     const int row0 = t >= 0 ? t * ROWS : p.N;
-    Raw qx[kR], qg[kR], qd[kR];
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const long long row = (long long)row0 + r0 + r;
-      const bool ok = on && row >= lo && row < hi;
-      qx[r] = ok ? *reinterpret_cast<const Raw*>(x + row * p.x.sn) : Raw{};
-      qg[r] = ok ? *reinterpret_cast<const Raw*>(g + row * p.g.sn) : Raw{};
-      qd[r] = ok ? *reinterpret_cast<const Raw*>(dy + row * p.dy.sn) : Raw{};
-    }
-    float hin[V] = {};
-    const int krow = row0 + warp / PER * PER * GROUPS * kR;
-    if (on && krow < p.N) load_f(p.kept + ((long long)batch * kept_rows + krow / kScanKept) * p.D + c, hin);
-    if (PACKED) mark_rows(p, row0, marks);
+    float2 h[P];
+    fill(h, 0.f);
+    const int from = warp / PER * PER, krow = row0 + from * GROUPS * kR;
+    if (on && krow < p.N) load_f(p.kept + ((long long)batch * kept_rows + krow / kScanKept) * p.D + c, h);
+    copies_wait0();
+    if (PACKED)
+      mark_rows(p, row0, marks);
+    else
+      __syncthreads();
+    fetch(t - cluster, par ^ 1);
+    const T *sx = stage + par * 3 * St::ELEMS + St::at(r0) + cl, *sg = sx + St::ELEMS, *sd = sg + St::ELEMS;
     const Marks m = marks_of<kR>(p, PACKED ? &marks : nullptr, row0, r0, lo, hi);
     const unsigned first = m.first & m.live, last = m.last & m.live;
     // the start of a sequence that begins in row r, the gradient behind one that ends there
-    const auto start = [&](int r, float (&f)[V]) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) f[v] = 0.f;
+    const auto start = [&](int r, float2 (&f)[P]) {
+      fill(f, 0.f);
       if (p.h0 != nullptr && on) load_f(p.h0 + (long long)(PACKED ? marks.first[r0 + r] - 1 : batch) * p.D + c, f);
     };
-    const auto end = [&](int r, float (&f)[V]) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) f[v] = 0.f;
+    const auto end = [&](int r, float2 (&f)[P]) {
+      fill(f, 0.f);
       if (p.dh_last != nullptr && on) load_f(p.dh_last + (long long)(PACKED ? marks.last[r0 + r] - 1 : batch) * p.D + c, f);
     };
-    const auto gates = [&](int r, float (&a)[V], float (&rest)[V], float (&xv)[V]) {
-      float gv[V];
-      unpack(qx[r], xv);
-      unpack(qg[r], gv);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gate_of<GATE>(gv[v], &a[v], &rest[v]);
-        if (!(m.live >> r & 1)) a[v] = 1.f;
-      }
-    };
     // the thread's rows: h -> fA h + fB forwards, c -> rA c + rB backwards
-    float fA[V], fB[V], rA[V], rB[V], wA[V], wB[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      fA[v] = rA[v] = 1.f;
-      fB[v] = rB[v] = 0.f;
-    }
+    float2 a[kR][P], fA[P], fB[P], rA[P], rB[P], wA[P], wB[P];
+    fill(fA, 1.f);
+    fill(rA, 1.f);
+    fill(fB, 0.f);
+    fill(rB, 0.f);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      float a[V], rest[V], xv[V], d[V];
-      gates(r, a, rest, xv);
-      unpack(qd[r], d);
-      float h[V], e[V];
-      if (first >> r & 1) start(r, h);
-      if (last >> r & 1) end(r, e);
+      float2 gv[P], xv[P], d[P];
+      unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
+      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
+      unpack<T>(*reinterpret_cast<const Raw*>(sd + r * CW), d);
+      if (first >> r & 1) {
+        start(r, fB);
+        if (PACKED) fill(fA, kCut);  // (dense: the state before the first row is zero)
+      }
+      if (last >> r & 1) {
+        float2 e[P];
+        end(r, e);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        // forwards: rows in order
-        if (first >> r & 1) {
-          fB[v] = h[v];
-          if (PACKED) fA[v] = kCut;  // (dense: the state before the first row is zero)
-        }
-        fB[v] = fmaf(a[v], fB[v], GATE == GATED_SCAN_SIGMOID ? rest[v] * xv[v] : xv[v]);
-        fA[v] *= a[v];
+        for (int i = 0; i < P; ++i) d[i] = add2(d[i], e[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        float2 rest;
+        gate_of<T, GATE>(gv[i], &a[r][i], &rest);
+        if (!(m.live >> r & 1)) a[r][i] = both(1.f);
+        fB[i] = fma2(a[r][i], fB[i], input_of<GATE>(xv[i], rest));
+        fA[i] = mul2(fA[i], a[r][i]);
         // backwards: row r acts before the rows so far, c -> rA (a (dy + c)) + rB
-        const float ad = last >> r & 1 ? a[v] * (d[v] + e[v]) : a[v] * d[v];
-        rB[v] = carry_on<PACKED>(rA[v], rB[v], ad);
-        rA[v] = join<PACKED>(rA[v], PACKED && (last >> r & 1) ? kCut : a[v]);
+        rB[i] = carry_on<PACKED>(rA[i], rB[i], mul2(a[r][i], d[i]));
+        rA[i] = join<PACKED>(rA[i], PACKED && (last >> r & 1) ? both(kCut) : a[r][i]);
       }
     }
     scan_warp<LW, false, PACKED>(fA, fB, wA, wB, lane);
     if (PER > 1 && lane / LW == GROUPS - 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) fwd[par][warp][cl + v] = make_float2(wA[v], wB[v]);
+      store(&fwa[par][warp][cl], wA);
+      store(&fwb[par][warp][cl], wB);
     }
     scan_warp<LW, true, PACKED>(rA, rB, wA, wB, lane);
     if (lane / LW == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) s.warp[par][warp][cl + v] = make_float2(wA[v], wB[v]);
+      store(&s.wa[par][warp][cl], wA);
+      store(&s.wb[par][warp][cl], wB);
     }
-    exchange<CW, true, PACKED>(s, par, &running, cluster > 1);
-    float k[V];
+    exchange<CW, true, PACKED>(s, par, &running, cluster, rank);
+    float2 k[P];
+    load_f(&s.carry[par][cl], k);
+    over_warps<CW, true, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, k);
+    if (PER > 1) over_warps<CW, false, PACKED>(fwa[par], fwb[par], cl, warp, from, h);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (PER > 1)
-        for (int w = warp / PER * PER; w < warp; ++w) {
-          const float2 f = fwd[par][w][cl + v];
-          hin[v] = carry_on<PACKED>(f.x, f.y, hin[v]);
-        }
-      hin[v] = carry_on<PACKED>(fA[v], fB[v], hin[v]);
-      k[v] = s.carry[par][cl + v];
-      for (int w = kWarps - 1; w > warp; --w) {
-        const float2 f = s.warp[par][w][cl + v];
-        k[v] = carry_on<PACKED>(f.x, f.y, k[v]);
-      }
-      k[v] = carry_on<PACKED>(rA[v], rB[v], k[v]);
+    for (int i = 0; i < P; ++i) {
+      k[i] = carry_on<PACKED>(rA[i], rB[i], k[i]);
+      h[i] = carry_on<PACKED>(fA[i], fB[i], h[i]);
     }
-    // h_{t-1} of every row, then the rows from the last one on
-    float before[kR][V];
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      float a[V], rest[V], xv[V];
-      gates(r, a, rest, xv);
-      if (first >> r & 1) start(r, hin);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        before[r][v] = hin[v];
-        hin[v] = fmaf(a[v], hin[v], GATE == GATED_SCAN_SIGMOID ? rest[v] * xv[v] : xv[v]);
-      }
-    }
+    float2 G[kR][P];
 #pragma unroll
     for (int r = kR - 1; r >= 0; --r) {
-      if (!(m.live >> r & 1)) continue;
-      float a[V], rest[V], xv[V], d[V], ox[V], og[V];
-      gates(r, a, rest, xv);
-      unpack(qd[r], d);
+      float2 d[P];
+      unpack<T>(*reinterpret_cast<const Raw*>(sd + r * CW), d);
       if (last >> r & 1) end(r, k);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float G = d[v] + k[v];
-        k[v] = a[v] * G;
-        if (GATE == GATED_SCAN_DECAY) {
-          ox[v] = G;
-          og[v] = G * before[r][v];
-        } else if (GATE == GATED_SCAN_LOG) {
-          ox[v] = G;
-          og[v] = k[v] * before[r][v];
+      for (int i = 0; i < P; ++i) {
+        G[r][i] = add2(d[i], k[i]);
+        k[i] = mul2(a[r][i], G[r][i]);
+      }
+      if (p.dh0 != nullptr && on && first >> r & 1)
+        store(p.dh0 + (long long)(PACKED ? marks.first[r0 + r] - 1 : batch) * p.D + c, k);
+    }
+    const long long row = (long long)row0 + r0;
+    T *px = dx + row * p.dx.sn, *pg = dg + row * p.dg.sn;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      float2 gv[P], xv[P], ox[P], og[P];
+      unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
+      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
+      if (first >> r & 1) start(r, h);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        float2 at = a[r][i], rest;
+        if (GATE == GATED_SCAN_SIGMOID) gate_of<T, GATE>(gv[i], &at, &rest);
+        if (GATE == GATED_SCAN_SIGMOID) {
+          ox[i] = mul2(rest, G[r][i]);
+          og[i] = mul2(mul2(at, ox[i]), fma2(xv[i], both(-1.f), h[i]));
         } else {
-          ox[v] = rest[v] * G;
-          og[v] = a[v] * ox[v] * (before[r][v] - xv[v]);
+          ox[i] = G[r][i];
+          og[i] = mul2(GATE == GATED_SCAN_LOG ? mul2(at, G[r][i]) : G[r][i], h[i]);
         }
+        h[i] = fma2(at, h[i], input_of<GATE>(xv[i], rest));
       }
-      if (on) {
-        const long long row = (long long)row0 + r0 + r;
-        store(dx + row * p.dx.sn, ox);
-        store(dg + row * p.dg.sn, og);
-        if (p.dh0 != nullptr && first >> r & 1)
-          store(p.dh0 + (long long)(PACKED ? marks.first[r0 + r] - 1 : batch) * p.D + c, k);
+      if (on && m.live >> r & 1) {
+        store(px, ox);
+        store(pg, og);
       }
+      px = next_row(px, p.dx.sn);
+      pg = next_row(pg, p.dg.sn);
     }
   }
   if (cluster > 1) cg::this_cluster().sync();
 }
 
 // ---- one token for every row: a block a row and a run of channels
+constexpr int kStepPairs = 2;
 template <typename T, int GATE>
 __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_constant__ ScanArgs p) {
-  using Raw = typename Tile<T>::Raw;
+  using Raw = typename Io<T, kStepPairs>::Raw;
+  constexpr int P = kStepPairs, V = 2 * P;
   const int runs = (p.D + 128 * V - 1) / (128 * V);
   const int b = (int)(blockIdx.x / runs), c = ((int)(blockIdx.x % runs) * 128 + threadIdx.x) * V;
   const bool on = c < p.D;
@@ -556,15 +715,15 @@ __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_const
   const int slot = ret_slot(p.slots, p.n_slots, b);
   if (!on || slot < 0) return;
   float* state = p.states + (long long)slot * p.D + c;
-  float h[V], xv[V], gv[V];
+  float2 h[P], xv[P], gv[P];
   load_f(state, h);
-  unpack(qx, xv);
-  unpack(qg, gv);
+  unpack<T>(qx, xv);
+  unpack<T>(qg, gv);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float a, rest;
-    gate_of<GATE>(gv[v], &a, &rest);
-    h[v] = fmaf(a, h[v], GATE == GATED_SCAN_SIGMOID ? rest * xv[v] : xv[v]);
+  for (int i = 0; i < P; ++i) {
+    float2 a, rest;
+    gate_of<T, GATE>(gv[i], &a, &rest);
+    h[i] = fma2(a, h[i], input_of<GATE>(xv[i], rest));
   }
   store(state, h);
   store(static_cast<T*>(const_cast<void*>(p.y.p)) + (long long)b * p.y.sb + c, h);
@@ -574,15 +733,15 @@ __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_const
 // Blocks of a cluster: as many as the SMs need (two blocks each) and the tiles give, a power of two.
 int cluster_of(long long chains, int tiles) {
   int n = 1;
-  while (n < kMaxCluster && chains * n < 2 * kRetSms && n < tiles) n *= 2;
+  while (n < kMaxCluster && chains * n < kRetSms && n < tiles) n *= 2;
   return n;
 }
 
-template <typename T, int GATE, bool PACKED>
+template <typename T, int GATE, int LW, bool PACKED>
 cudaError_t launch_scan(const ScanArgs& a, bool backward, cudaStream_t st) {
-  constexpr int CW = V * Tile<T>::LW, ROWS = kThreads / Tile<T>::LW * Tile<T>::R;
+  constexpr int CW = V * LW, ROWS = kThreads / LW * Tile<T>::R;
   void (*kernel)(ScanArgs, int) =
-      backward ? gated_scan_backward_kernel<T, GATE, PACKED> : gated_scan_forward_kernel<T, GATE, PACKED>;
+      backward ? gated_scan_backward_kernel<T, GATE, LW, PACKED> : gated_scan_forward_kernel<T, GATE, LW, PACKED>;
   const long long chains = (PACKED ? 1ll : a.B) * ((a.D + CW - 1) / CW);
   const int n = cluster_of(chains, ret_pieces(a.N, ROWS));
   if (chains * n > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -595,24 +754,26 @@ cudaError_t launch_scan(const ScanArgs& a, bool backward, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = n > 1 ? 1 : 0;
-  if (n > 8) {
-    static std::once_flag once[2][64];  // (an attribute of the kernel on each device)
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::call_once(once[backward][dev & 63], [&] {
-      e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    });
-    if (e != cudaSuccess) return e;
-  }
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, n);
+  static SmemOptIn opt[2];
+  const int smem = 2 * (backward ? 3 : 2) * Stage<T, LW>::ELEMS * (int)sizeof(T);
+  cudaError_t e = opt[backward].ensure((const void*)kernel, smem);
+  if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = smem;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, n);
   note_launch();
   return e;
 }
 
+// The lanes of a row: the most (128 bytes of channels) with which the chains, in clusters of eight, fill the SMs.
 template <typename T, int GATE>
 cudaError_t launch_gate(const ScanArgs& a, bool backward, cudaStream_t st) {
-  return a.cu != nullptr ? launch_scan<T, GATE, true>(a, backward, st) : launch_scan<T, GATE, false>(a, backward, st);
+  constexpr int WIDE = Tile<T>::WIDE;
+  const int cw = V * WIDE;
+  const long long chains = (a.cu ? 1ll : a.B) * ((a.D + cw - 1) / cw);
+  const bool narrow = chains * std::min(kMaxCluster, ret_pieces(a.N, kThreads / WIDE * Tile<T>::R)) < kRetSms;
+  if (a.cu != nullptr)
+    return narrow ? launch_scan<T, GATE, WIDE / 4, true>(a, backward, st) : launch_scan<T, GATE, WIDE, true>(a, backward, st);
+  return narrow ? launch_scan<T, GATE, WIDE / 4, false>(a, backward, st) : launch_scan<T, GATE, WIDE, false>(a, backward, st);
 }
 
 template <typename T>
@@ -626,7 +787,7 @@ cudaError_t launch_type(const ScanArgs& a, bool backward, cudaStream_t st) {
 
 template <typename T, int GATE>
 cudaError_t launch_step(const ScanArgs& a, cudaStream_t st) {
-  const int run = 128 * V;
+  const int run = 128 * 2 * kStepPairs;
   gated_scan_step_kernel<T, GATE><<<(unsigned)((long long)a.B * ((a.D + run - 1) / run)), 128, 0, st>>>(a);
   note_launch();
   return cudaGetLastError();
