@@ -22,8 +22,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the tiles,
+constexpr int kBlock = kThreads + 32;                  // and a warp that carries the state over the tiles (exchange)
+constexpr int kWideCluster = 4, kNarrowCluster = 8;    // blocks of a cluster at most, with 128 bytes of channels and with 32
 constexpr int P = 1, V = 2 * P;  // channels of a thread: a pair, so that a warp of bf16 has a row of 128 bytes to itself
 
 // A thread's rows of a tile (32 values each of a and b in registers) and the lanes of 128 bytes of channels.
@@ -118,33 +119,57 @@ __device__ __forceinline__ void fill(float2 (&f)[N], float v) {
   for (int i = 0; i < N; ++i) f[i] = both(v);
 }
 
+__device__ __forceinline__ float exp2_of(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
+}
 // exp(x).  bf16 tensors: the hardware's base-2 exponential of x log2 e (log2 e = 1.4426950408889634), off by
 // |x| 2^-24 + 2^-22 at most, far below what a bf16 gate says; fp32: expf.  Not-a-number stays.
 template <typename T>
 __device__ __forceinline__ float exp_of(float x) {
-  if (sizeof(T) == 4) return expf(x);
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
-  return e;
+  return sizeof(T) == 4 ? expf(x) : exp2_of(x * 1.4426950408889634f);
+}
+__device__ __forceinline__ float min_nan(float a, float b) {  // not-a-number stays
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp_of(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// a and the factor of x of a gate.  sigmoid: from exp(-|g|), so that nothing overflows; of a and 1 - a the smaller is
-// e / (1 + e), the larger 1 - the smaller, rounded once (a long memory multiplies thousands of gates near 1, and their
-// errors).
+struct Gate {
+  float2 a;     // the gate
+  float2 rest;  // sigmoid: 1 - a, the factor of x
+  float2 low;   // sigmoid: a once more, with all its digits also where it is small
+};
+// sigmoid, with e = exp(-g): 1 - a = e / (1 + e); a = 1 - (1 - a), so that gates near 1 are rounded once (a long memory
+// multiplies thousands of them, and their errors) and all are within 2^-24; low = 1 / (1 + e).  e stops at 2^126, where
+// e / (1 + e) is still a number.  Not-a-number stays.
 template <typename T, int GATE>
-__device__ __forceinline__ void gate_of(float2 g, float2* a, float2* rest) {
+__device__ __forceinline__ Gate gate_of(float2 g) {
+  Gate k;
   if (GATE == GATED_SCAN_DECAY) {
-    *a = g;
+    k.a = g;
   } else if (GATE == GATED_SCAN_LOG) {
-    *a = make_float2(exp_of<T>(g.x), exp_of<T>(g.y));
+    k.a = make_float2(exp_of<T>(g.x), exp_of<T>(g.y));
   } else {
-    const float2 e = make_float2(exp_of<T>(-fabsf(g.x)), exp_of<T>(-fabsf(g.y)));
+    float2 e;
+    if (sizeof(T) == 4) {
+      e = make_float2(expf(min_nan(-g.x, 87.f)), expf(min_nan(-g.y, 87.f)));
+    } else {
+      const float2 t = mul2(g, both(-1.4426950408889634f));
+      e = make_float2(exp2_of(min_nan(t.x, 126.f)), exp2_of(min_nan(t.y, 126.f)));
+    }
     const float2 d = add2(e, both(1.f));
-    const float2 s = mul2(e, make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y)));
-    const float2 l = fma2(s, both(-1.f), both(1.f));
-    *a = make_float2(g.x > 0.f ? l.x : s.x, g.y > 0.f ? l.y : s.y);
-    *rest = make_float2(g.x > 0.f ? s.x : l.x, g.y > 0.f ? s.y : l.y);
+    k.low = make_float2(rcp_of(d.x), rcp_of(d.y));
+    k.rest = mul2(e, k.low);
+    k.a = fma2(k.rest, both(-1.f), both(1.f));
   }
+  return k;
 }
 template <int GATE>
 __device__ __forceinline__ float2 input_of(float2 x, float2 rest) {
@@ -155,45 +180,65 @@ __device__ __forceinline__ float2 input_of(float2 x, float2 rest) {
 struct Marks {
   unsigned live, first, last;  // bit r: row r of the thread
 };
+__device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // the kThreads of the tiles
+static_assert(kThreads == 256, "the barrier's count");
 
-template <int ROWS>
+// Packed sequences: bits of the tile's rows row0 .. (the tiles' threads), a word for the kR rows of a thread.  Offsets
+// outside [0, N] are clamped; out of order they mark rows of the tile all the same and nothing else.
+template <int GROUPS>
 struct MarkRows {
-  int first[ROWS], last[ROWS];  // packed: 1 + the sequence whose first / last token the row is, 0: none
+  unsigned first[GROUPS], last[GROUPS];
 };
-
-// Packed sequences: marks of the tile's rows row0 .. row0 + ROWS - 1 (whole block).  Offsets outside [0, N] are clamped;
-// out of order they mark rows of the tile all the same and nothing else.
-template <int ROWS>
-__device__ __forceinline__ void mark_rows(const ScanArgs& p, int row0, MarkRows<ROWS>& m) {
-  __syncthreads();  // (the marks of the tile before have been read)
-  for (int i = threadIdx.x; i < ROWS; i += kThreads) m.first[i] = m.last[i] = 0;
-  __syncthreads();
+template <int kR, int GROUPS>
+__device__ __forceinline__ void mark_rows(const ScanArgs& p, int row0, MarkRows<GROUPS>& m) {
+  tile_sync();  // (the marks of the tile before have been read)
+  for (int i = threadIdx.x; i < GROUPS; i += kThreads) m.first[i] = m.last[i] = 0;
+  tile_sync();
   for (int i = threadIdx.x; i < p.B; i += kThreads) {
     const int lo = min(max(p.cu[i], 0), p.N), hi = min(max(p.cu[i + 1], lo), p.N);
     if (lo == hi) continue;
     const int f = lo - row0, l = hi - 1 - row0;
-    if (f >= 0 && f < ROWS) atomicMax(&m.first[f], i + 1);
-    if (l >= 0 && l < ROWS) atomicMax(&m.last[l], i + 1);
+    if (f >= 0 && f < GROUPS * kR) atomicOr(&m.first[f / kR], 1u << f % kR);
+    if (l >= 0 && l < GROUPS * kR) atomicOr(&m.last[l / kR], 1u << l % kR);
   }
-  __syncthreads();
+  tile_sync();
 }
-
-// The thread's rows r0 .. r0 + kR - 1, lo <= row < hi: tokens.
-template <int kR, int ROWS>
-__device__ __forceinline__ Marks marks_of(const ScanArgs& p, const MarkRows<ROWS>* m, int row0, int r0, int lo, int hi) {
-  Marks k{0, 0, 0};
-#pragma unroll
-  for (int r = 0; r < kR; ++r) {
-    const int row = row0 + r0 + r;
-    if (row >= lo && row < hi) k.live |= 1u << r;
-    if (m != nullptr) {
-      if (m->first[r0 + r] != 0) k.first |= 1u << r;
-      if (m->last[r0 + r] != 0) k.last |= 1u << r;
+// The sequence that a marked row is in: the last one whose offset is not behind the row.
+__device__ __noinline__ int sequence_of(const int* cu, int B, int row) {
+  int lo = 0, n = B;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int half = n / 2;
+    if (cu[lo + half] <= row) {
+      lo += half;
+      n -= half;
     } else {
-      if (row == 0) k.first |= 1u << r;
-      if (row == hi - 1) k.last |= 1u << r;
+      n = half;
     }
   }
+  return lo;
+}
+
+// The thread's kR rows from `row` on; rows in [lo, hi) are tokens.
+template <int kR>
+__device__ __forceinline__ unsigned live_rows(int row, int lo, int hi) {
+  constexpr unsigned all = (1u << kR) - 1;
+  const int skip = min(max(lo - row, 0), kR), n = min(max(hi - row, 0), kR);
+  return all >> (kR - n) & all << skip;
+}
+template <int kR>
+__device__ __forceinline__ Marks dense_marks(int row, int hi) {
+  Marks k;
+  k.live = live_rows<kR>(row, 0, hi);
+  k.first = row == 0 ? 1u : 0u;
+  k.last = hi > row && hi - row <= kR ? 1u << (hi - 1 - row) : 0u;
+  return k;
+}
+template <int kR, int GROUPS>
+__device__ __forceinline__ Marks packed_marks(const MarkRows<GROUPS>& m, int group, int row, int lo, int hi) {
+  Marks k;
+  k.live = live_rows<kR>(row, lo, hi);
+  k.first = m.first[group] & k.live;
+  k.last = m.last[group] & k.live;
   return k;
 }
 
@@ -280,62 +325,96 @@ __device__ __forceinline__ void scan_warp(float2 (&A)[P], float2 (&B)[P], float2
   }
 }
 
-template <int CW>
+template <typename T, int LW>
 struct ScanShared {
-  float wa[2][kWarps][CW], wb[2][kWarps][CW];            // A, B of the warps, by the tile's parity
-  float ba[2][kMaxCluster][CW], bb[2][kMaxCluster][CW];  // of the cluster's blocks, which write them here
-  float carry[2][CW];                                    // the state entering the block's tile
+  static constexpr int CW = V * LW, MOST = LW == Tile<T>::WIDE ? kWideCluster : kNarrowCluster;
+  float wa[2][kWarps][CW], wb[2][kWarps][CW];  // A, B of the warps, by the tile's parity
+  float ba[2][MOST][CW], bb[2][MOST][CW];      // of the cluster's blocks, which write them here
+  float carry[2][CW];                          // the state entering the block's tile
 };
 
-// The state entering the block's tile, for every channel, in s.carry[par] (whole block), and in `running` (threads
-// below CW: a channel each) that behind the cluster's tiles.  The warps' A, B are in s.wa, s.wb[par].
-template <int CW, bool REVERSE, bool PACKED>
-__device__ __forceinline__ void exchange(ScanShared<CW>& s, int par, float* running, int n, int rank) {
-  const int c = threadIdx.x;
-  if (n == 1) {
-    if (c < CW) s.carry[par][c] = *running;
-    __syncthreads();
-    if (c < CW) {
-      float h = *running;
+// What goes on from tile to tile, in a warp of its own: as it has no other stores, the release of the cluster's barrier
+// waits for none (with the state carried by warps of the tiles each round waited for their outputs to arrive in L2).  The
+// block's warps have A, B in s.wa, s.wb and wait for s.carry.
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 2, 288;" ::: "memory"); }
+__device__ __forceinline__ void block_arrive() { asm volatile("bar.arrive 2, 288;" ::: "memory"); }
+__device__ __forceinline__ void carry_sync() { asm volatile("bar.sync 3, 288;" ::: "memory"); }
+__device__ __forceinline__ void carry_arrive() { asm volatile("bar.arrive 3, 288;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+static_assert(kBlock == 288, "the barriers' counts");
+
+// The warps of the tiles, between s.wa, s.wb[par] written and s.carry[par] read.
+__device__ __forceinline__ void exchange_wait(bool clustered) {
+  if (!clustered) {
+    block_sync();  // (the carry of this tile was written before the carrying warp came here)
+    return;
+  }
+  block_arrive();
+  cluster_arrive_relaxed();
+  cluster_wait();
+  carry_sync();
+}
+// The carrying warp: all rounds of tiles.
+template <typename T, int LW, bool REVERSE, bool PACKED>
+__device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, int n, int rank) {
+  constexpr int CW = ScanShared<T, LW>::CW, MOST = ScanShared<T, LW>::MOST, K = (CW + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  float running[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) running[k] = 0.f;
+  for (int t = 0, par = 0; t < rounds; ++t, par ^= 1) {
+    if (n == 1) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (lane + 32 * k < CW) s.carry[par][lane + 32 * k] = running[k];
+    }
+    block_sync();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = lane + 32 * k;
+      if (CW % 32 != 0 && c >= CW) continue;
+      float A = 1.f, B = n == 1 ? running[k] : 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
         const int w = REVERSE ? kWarps - 1 - i : i;
-        h = carry_on<PACKED>(s.wa[par][w][c], s.wb[par][w][c], h);
+        const float fa = s.wa[par][w][c];
+        B = carry_on<PACKED>(fa, s.wb[par][w][c], B);
+        A = join<PACKED>(fa, A);
       }
-      *running = h;
-    }
-    return;
-  }
-  cg::cluster_group cl = cg::this_cluster();
-  __syncthreads();
-  if (c < CW) {
-    float A = 1.f, B = 0.f;
+      if (n == 1) {
+        running[k] = B;
+      } else {
+        cg::cluster_group cl = cg::this_cluster();
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const int w = REVERSE ? kWarps - 1 - i : i;
-      const float fa = s.wa[par][w][c];
-      B = carry_on<PACKED>(fa, s.wb[par][w][c], B);
-      A = join<PACKED>(fa, A);
-    }
-#pragma unroll
-    for (int i = 0; i < kMaxCluster; ++i)
-      if (i < n) {
-        cl.map_shared_rank(&s.ba[par][rank][0], i)[c] = A;
-        cl.map_shared_rank(&s.bb[par][rank][0], i)[c] = B;
+        for (int i = 0; i < MOST; ++i)
+          if (i < n) {
+            cl.map_shared_rank(&s.ba[par][rank][0], i)[c] = A;
+            cl.map_shared_rank(&s.bb[par][rank][0], i)[c] = B;
+          }
       }
-  }
-  cl.sync();
-  if (c < CW) {
-    float h = *running, mine = h;
-#pragma unroll
-    for (int i = 0; i < kMaxCluster; ++i) {
-      if (i == rank) mine = h;
-      if (i < n) h = carry_on<PACKED>(s.ba[par][i][c], s.bb[par][i][c], h);
     }
-    s.carry[par][c] = mine;
-    *running = h;
+    if (n == 1) continue;
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = lane + 32 * k;
+      if (CW % 32 != 0 && c >= CW) continue;
+      float h = running[k], mine = h;
+#pragma unroll
+      for (int i = 0; i < MOST; ++i) {
+        if (i == rank) mine = h;
+        if (i < n) h = carry_on<PACKED>(s.ba[par][i][c], s.bb[par][i][c], h);
+      }
+      s.carry[par][c] = mine;
+      running[k] = h;
+    }
+    __syncwarp();
+    carry_arrive();
   }
-  __syncthreads();
 }
 // The state before the warp: over the warps from `from` on (backwards: down to it).
 template <int CW, bool REVERSE, bool PACKED>
@@ -368,17 +447,30 @@ struct Stage {
   static __device__ __forceinline__ void fetch(T* to, const T* from, long long sn, long long row0, int lo, int hi, int c0,
                                                int D) {
     constexpr int N = ROWS * PIECES / kThreads, STEP = kThreads / PIECES;
+    static_assert(PAD == 0 || STEP % kR == 0, "the rows of a thread's copies lie evenly");
     const int piece = threadIdx.x % PIECES, r = threadIdx.x / PIECES;
     const int c = piece * (16 / (int)sizeof(T));
     const bool on = c0 + c < D;
     const T* src = from + (on ? c0 + c : 0);
+    unsigned dst = (unsigned)__cvta_generic_to_shared(to + at(r) + c);
+    if (on && row0 >= lo && row0 + ROWS <= hi) {
+      src += (row0 + r) * sn;
+      const long long step = STEP * sn;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        src += step;
+        dst += at(STEP) * (int)sizeof(T);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const long long row = row0 + r + i * STEP;
       const bool ok = on && row >= lo && row < hi;
-      const unsigned dst = (unsigned)__cvta_generic_to_shared(to + at(r + i * STEP) + c);
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src + (ok ? row * sn : 0)), "r"(ok ? 16 : 0)
                    : "memory");
+      dst += at(STEP) * (int)sizeof(T);
     }
   }
 };
@@ -387,12 +479,12 @@ __device__ __forceinline__ void copies_wait0() { asm volatile("cp.async.wait_gro
 
 // ---- forward
 template <typename T, int GATE, int LW, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
+__global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
   using Raw = typename Io<T, P>::Raw;
   using St = Stage<T, LW>;
   constexpr int kR = St::kR, CW = St::CW, ROWS = St::ROWS, GROUPS = 32 / LW;
-  __shared__ __align__(16) ScanShared<CW> s;
-  __shared__ MarkRows<PACKED ? ROWS : 1> marks;
+  __shared__ __align__(16) ScanShared<T, LW> s;
+  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % cluster), chain = (int)(blockIdx.x / cluster);
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
@@ -408,7 +500,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
     hi = min(max(p.cu[p.B], lo), p.N);
   }
   const int tiles = ret_pieces(p.N, ROWS), kept_rows = ret_pieces(p.N, kScanKept);
-  float running = 0.f;
+  if (tid >= kThreads) {
+    if (cluster > 1) cg::this_cluster().sync();  // every block runs: its shared memory may be written
+    carry_tiles<T, LW, false, PACKED>(s, ret_pieces(tiles, cluster), cluster, rank);
+    if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one writes its shared memory
+    return;
+  }
   extern __shared__ __align__(16) uint8_t raw[];
   T* stage = reinterpret_cast<T*>(raw);  // [2][x, g]
   const auto fetch = [&](int t, int buf) {
@@ -420,18 +517,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
     copies_commit();
   };
   fetch(rank, 0);
-  if (cluster > 1) cg::this_cluster().sync();  // every block runs: its shared memory may be written
+  if (cluster > 1) cg::this_cluster().sync();
   int par = 0;
   for (int t0 = 0; t0 < tiles; t0 += cluster, par ^= 1) {
     const int t = t0 + rank, row0 = (int)min((long long)t * ROWS, (long long)p.N);
     copies_wait0();
     if (PACKED)
-      mark_rows(p, row0, marks);
+      mark_rows<kR>(p, row0, marks);
     else
-      __syncthreads();  // (the tile is there, the other buffer has been read)
+      tile_sync();  // (the tile is there, the other buffer has been read)
     fetch(t + cluster, par ^ 1);
-    const Marks m = marks_of<kR>(p, PACKED ? &marks : nullptr, row0, r0, lo, hi);
-    const unsigned first = m.first & m.live;
+    const Marks m = PACKED ? packed_marks<kR>(marks, r0 / kR, row0 + r0, lo, hi) : dense_marks<kR>(row0 + r0, hi);
+    const unsigned first = m.first;
     const T *sx = stage + par * 2 * St::ELEMS + St::at(r0) + cl, *sg = sx + St::ELEMS;
     float2 a[kR][P], b[kR][P];
 #pragma unroll
@@ -441,9 +538,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
       unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        float2 rest;
-        gate_of<T, GATE>(gv[i], &a[r][i], &rest);
-        b[r][i] = input_of<GATE>(xv[i], rest);
+        const Gate k = gate_of<T, GATE>(gv[i]);
+        a[r][i] = k.a;
+        b[r][i] = input_of<GATE>(xv[i], k.rest);
       }
     }
     if (m.live != (1u << kR) - 1) {
@@ -458,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
 #pragma unroll
       for (int r = 0; r < kR; ++r)
         if (first >> r & 1) {
-          const int seq = PACKED ? marks.first[r0 + r] - 1 : batch;
+          const int seq = PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch;
           const int slot = p.load && on ? slot_of(p.slots, p.n_slots, seq) : -1;
           float2 h[P];
           if (slot >= 0) load_f(p.states + (long long)slot * p.D + c, h);
@@ -490,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
       store(&s.wa[par][warp][cl], wA);
       store(&s.wb[par][warp][cl], wB);
     }
-    exchange<CW, false, PACKED>(s, par, &running, cluster, rank);
+    exchange_wait(cluster > 1);
     float2 h[P];
     load_f(&s.carry[par][cl], h);
     over_warps<CW, false, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, h);
@@ -500,15 +597,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
     if (p.kept != nullptr && on && row < p.N && row % kScanKept == 0)
       store(p.kept + ((long long)batch * kept_rows + row / kScanKept) * p.D + c, h);
     T* py = y + row * p.y.sn;
-    const bool whole = on && m.live == (1u << kR) - 1;
+    const unsigned out = on ? m.live : 0, ends = p.states != nullptr && on ? m.last : 0;
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
 #pragma unroll
       for (int i = 0; i < P; ++i) h[i] = PACKED && (first >> r & 1) ? b[r][i] : fma2(a[r][i], h[i], b[r][i]);
-      if (whole || (on && m.live >> r & 1)) store(py, h);
+      if (out >> r & 1) store(py, h);
       py = next_row(py, p.y.sn);
-      if (p.states != nullptr && on && (m.last & m.live) >> r & 1) {
-        const int slot = slot_of(p.slots, p.n_slots, PACKED ? marks.last[r0 + r] - 1 : batch);
+      if (ends >> r & 1) {
+        const int slot = slot_of(p.slots, p.n_slots, PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch);
         if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
       }
     }
@@ -520,15 +617,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_forward_kernel(const _
 // A thread's rows three times: the runs of both directions; G from the last row on; h from the first row on, with what
 // goes out.  x, g and dy stay in registers as they came; the sigmoid is taken again in the third.
 template <typename T, int GATE, int LW, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
+__global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
   using Raw = typename Io<T, P>::Raw;
   using St = Stage<T, LW>;
   constexpr int kR = St::kR, CW = St::CW, ROWS = St::ROWS, GROUPS = 32 / LW;
   constexpr int PER = kScanKept / (GROUPS * kR) > 1 ? kScanKept / (GROUPS * kR) : 1;  // warps of a kept state
   static_assert((GROUPS * kR * PER) % kScanKept == 0 && kWarps % PER == 0, "a kept state at the first row of every PER warps");
-  __shared__ __align__(16) ScanShared<CW> s;
-  __shared__ __align__(16) float fwa[2][kWarps][CW], fwb[2][kWarps][CW];
-  __shared__ MarkRows<PACKED ? ROWS : 1> marks;
+  __shared__ __align__(16) ScanShared<T, LW> s;
+  __shared__ __align__(16) float fwa[kWarps][CW], fwb[kWarps][CW];
+  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % cluster), chain = (int)(blockIdx.x / cluster);
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
@@ -545,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
     lo = min(max(p.cu[0], 0), p.N);
     hi = min(max(p.cu[p.B], lo), p.N);
     // a sequence without tokens: its last state is its start
-    if (p.dh0 != nullptr && rank == 0)
+    if (p.dh0 != nullptr && rank == 0 && tid < kThreads)
       for (int i = tid / LW; i < p.B; i += kThreads / LW) {
         const int l = min(max(p.cu[i], 0), p.N);
         if (on && min(p.cu[i + 1], p.N) <= l) {
@@ -557,7 +654,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
       }
   }
   const int tiles = ret_pieces(p.N, ROWS), kept_rows = ret_pieces(p.N, kScanKept);
-  float running = 0.f;
+  if (tid >= kThreads) {
+    if (cluster > 1) cg::this_cluster().sync();  // every block runs: its shared memory may be written
+    carry_tiles<T, LW, true, PACKED>(s, ret_pieces(tiles, cluster), cluster, rank);
+    if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one writes its shared memory
+    return;
+  }
   extern __shared__ __align__(16) uint8_t raw[];
   T* stage = reinterpret_cast<T*>(raw);  // [2][x, g, dy]
   const auto fetch = [&](int t, int buf) {
@@ -582,21 +684,21 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
     if (on && krow < p.N) load_f(p.kept + ((long long)batch * kept_rows + krow / kScanKept) * p.D + c, h);
     copies_wait0();
     if (PACKED)
-      mark_rows(p, row0, marks);
+      mark_rows<kR>(p, row0, marks);
     else
-      __syncthreads();
+      tile_sync();
     fetch(t - cluster, par ^ 1);
     const T *sx = stage + par * 3 * St::ELEMS + St::at(r0) + cl, *sg = sx + St::ELEMS, *sd = sg + St::ELEMS;
-    const Marks m = marks_of<kR>(p, PACKED ? &marks : nullptr, row0, r0, lo, hi);
-    const unsigned first = m.first & m.live, last = m.last & m.live;
+    const Marks m = PACKED ? packed_marks<kR>(marks, r0 / kR, row0 + r0, lo, hi) : dense_marks<kR>(row0 + r0, hi);
+    const unsigned first = m.first, last = m.last;
     // the start of a sequence that begins in row r, the gradient behind one that ends there
     const auto start = [&](int r, float2 (&f)[P]) {
       fill(f, 0.f);
-      if (p.h0 != nullptr && on) load_f(p.h0 + (long long)(PACKED ? marks.first[r0 + r] - 1 : batch) * p.D + c, f);
+      if (p.h0 != nullptr && on) load_f(p.h0 + (long long)(PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch) * p.D + c, f);
     };
     const auto end = [&](int r, float2 (&f)[P]) {
       fill(f, 0.f);
-      if (p.dh_last != nullptr && on) load_f(p.dh_last + (long long)(PACKED ? marks.last[r0 + r] - 1 : batch) * p.D + c, f);
+      if (p.dh_last != nullptr && on) load_f(p.dh_last + (long long)(PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch) * p.D + c, f);
     };
     // the thread's rows: h -> fA h + fB forwards, c -> rA c + rB backwards
     float2 a[kR][P], fA[P], fB[P], rA[P], rB[P], wA[P], wB[P];
@@ -622,10 +724,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        float2 rest;
-        gate_of<T, GATE>(gv[i], &a[r][i], &rest);
+        const Gate gt = gate_of<T, GATE>(gv[i]);
+        a[r][i] = gt.a;
         if (!(m.live >> r & 1)) a[r][i] = both(1.f);
-        fB[i] = fma2(a[r][i], fB[i], input_of<GATE>(xv[i], rest));
+        fB[i] = fma2(a[r][i], fB[i], input_of<GATE>(xv[i], gt.rest));
         fA[i] = mul2(fA[i], a[r][i]);
         // backwards: row r acts before the rows so far, c -> rA (a (dy + c)) + rB
         rB[i] = carry_on<PACKED>(rA[i], rB[i], mul2(a[r][i], d[i]));
@@ -634,24 +736,25 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
     }
     scan_warp<LW, false, PACKED>(fA, fB, wA, wB, lane);
     if (PER > 1 && lane / LW == GROUPS - 1) {
-      store(&fwa[par][warp][cl], wA);
-      store(&fwb[par][warp][cl], wB);
+      store(&fwa[warp][cl], wA);
+      store(&fwb[warp][cl], wB);
     }
     scan_warp<LW, true, PACKED>(rA, rB, wA, wB, lane);
     if (lane / LW == 0) {
       store(&s.wa[par][warp][cl], wA);
       store(&s.wb[par][warp][cl], wB);
     }
-    exchange<CW, true, PACKED>(s, par, &running, cluster, rank);
+    exchange_wait(cluster > 1);
     float2 k[P];
     load_f(&s.carry[par][cl], k);
     over_warps<CW, true, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, k);
-    if (PER > 1) over_warps<CW, false, PACKED>(fwa[par], fwb[par], cl, warp, from, h);
+    if (PER > 1) over_warps<CW, false, PACKED>(fwa, fwb, cl, warp, from, h);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       k[i] = carry_on<PACKED>(rA[i], rB[i], k[i]);
       h[i] = carry_on<PACKED>(fA[i], fB[i], h[i]);
     }
+    const unsigned out = on ? m.live : 0, starts = p.dh0 != nullptr && on ? first : 0;
     float2 G[kR][P];
 #pragma unroll
     for (int r = kR - 1; r >= 0; --r) {
@@ -663,8 +766,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
         G[r][i] = add2(d[i], k[i]);
         k[i] = mul2(a[r][i], G[r][i]);
       }
-      if (p.dh0 != nullptr && on && first >> r & 1)
-        store(p.dh0 + (long long)(PACKED ? marks.first[r0 + r] - 1 : batch) * p.D + c, k);
+      if (starts >> r & 1) {
+        if (GATE == GATED_SCAN_SIGMOID) {  // (a small gate with all its digits)
+          float2 gv[P];
+          unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const float2 low = gate_of<T, GATE>(gv[i]).low;
+            k[i] = mul2(make_float2(gv[i].x > 0.f ? a[r][i].x : low.x, gv[i].y > 0.f ? a[r][i].y : low.y), G[r][i]);
+          }
+        }
+        store(p.dh0 + (long long)(PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch) * p.D + c, k);
+      }
     }
     const long long row = (long long)row0 + r0;
     T *px = dx + row * p.dx.sn, *pg = dg + row * p.dg.sn;
@@ -676,18 +789,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
       if (first >> r & 1) start(r, h);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        float2 at = a[r][i], rest;
-        if (GATE == GATED_SCAN_SIGMOID) gate_of<T, GATE>(gv[i], &at, &rest);
         if (GATE == GATED_SCAN_SIGMOID) {
-          ox[i] = mul2(rest, G[r][i]);
-          og[i] = mul2(mul2(at, ox[i]), fma2(xv[i], both(-1.f), h[i]));
+          const Gate gt = gate_of<T, GATE>(gv[i]);
+          ox[i] = mul2(gt.rest, G[r][i]);
+          og[i] = mul2(mul2(gt.low, ox[i]), fma2(xv[i], both(-1.f), h[i]));
+          h[i] = fma2(gt.a, h[i], mul2(gt.rest, xv[i]));
         } else {
           ox[i] = G[r][i];
-          og[i] = mul2(GATE == GATED_SCAN_LOG ? mul2(at, G[r][i]) : G[r][i], h[i]);
+          og[i] = mul2(GATE == GATED_SCAN_LOG ? mul2(a[r][i], G[r][i]) : G[r][i], h[i]);
+          h[i] = fma2(a[r][i], h[i], xv[i]);
         }
-        h[i] = fma2(at, h[i], input_of<GATE>(xv[i], rest));
       }
-      if (on && m.live >> r & 1) {
+      if (out >> r & 1) {
         store(px, ox);
         store(pg, og);
       }
@@ -721,9 +834,8 @@ __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_const
   unpack<T>(qg, gv);
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    float2 a, rest;
-    gate_of<T, GATE>(gv[i], &a, &rest);
-    h[i] = fma2(a, h[i], input_of<GATE>(xv[i], rest));
+    const Gate k = gate_of<T, GATE>(gv[i]);
+    h[i] = fma2(k.a, h[i], input_of<GATE>(xv[i], k.rest));
   }
   store(state, h);
   store(static_cast<T*>(const_cast<void*>(p.y.p)) + (long long)b * p.y.sb + c, h);
@@ -731,9 +843,9 @@ __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_const
 
 // ---- host
 // Blocks of a cluster: as many as the SMs need (two blocks each) and the tiles give, a power of two.
-int cluster_of(long long chains, int tiles) {
+int cluster_of(long long chains, int tiles, int most) {
   int n = 1;
-  while (n < kMaxCluster && chains * n < kRetSms && n < tiles) n *= 2;
+  while (n < most && chains * n < kRetSms && n < tiles) n *= 2;
   return n;
 }
 
@@ -743,14 +855,14 @@ cudaError_t launch_scan(const ScanArgs& a, bool backward, cudaStream_t st) {
   void (*kernel)(ScanArgs, int) =
       backward ? gated_scan_backward_kernel<T, GATE, LW, PACKED> : gated_scan_forward_kernel<T, GATE, LW, PACKED>;
   const long long chains = (PACKED ? 1ll : a.B) * ((a.D + CW - 1) / CW);
-  const int n = cluster_of(chains, ret_pieces(a.N, ROWS));
+  const int n = cluster_of(chains, ret_pieces(a.N, ROWS), ScanShared<T, LW>::MOST);
   if (chains * n > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim = {(unsigned)n, 1, 1};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(chains * n));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kBlock);
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = n > 1 ? 1 : 0;
@@ -764,13 +876,13 @@ cudaError_t launch_scan(const ScanArgs& a, bool backward, cudaStream_t st) {
   return e;
 }
 
-// The lanes of a row: the most (128 bytes of channels) with which the chains, in clusters of eight, fill the SMs.
+// The lanes of a row: the most (128 bytes of channels) with which the chains, in clusters, fill the SMs.
 template <typename T, int GATE>
 cudaError_t launch_gate(const ScanArgs& a, bool backward, cudaStream_t st) {
   constexpr int WIDE = Tile<T>::WIDE;
   const int cw = V * WIDE;
   const long long chains = (a.cu ? 1ll : a.B) * ((a.D + cw - 1) / cw);
-  const bool narrow = chains * std::min(kMaxCluster, ret_pieces(a.N, kThreads / WIDE * Tile<T>::R)) < kRetSms;
+  const bool narrow = chains * std::min(kWideCluster, ret_pieces(a.N, kThreads / WIDE * Tile<T>::R)) < kRetSms;
   if (a.cu != nullptr)
     return narrow ? launch_scan<T, GATE, WIDE / 4, true>(a, backward, st) : launch_scan<T, GATE, WIDE, true>(a, backward, st);
   return narrow ? launch_scan<T, GATE, WIDE / 4, false>(a, backward, st) : launch_scan<T, GATE, WIDE, false>(a, backward, st);
