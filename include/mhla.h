@@ -124,7 +124,7 @@ typedef enum {
   MHLA_PHI_ELU1 = 0, /* phi(x) = ELU(x) + 1 (the default everywhere)   [LA §二] */
   MHLA_PHI_RELU = 1, /* phi(x) = max(x, 0)                              [LA §二] */
   MHLA_PHI_EXP = 2,  /* phi(x) = exp(x)                                 [LA §二] */
-  MHLA_PHI_IDENTITY = 3 /* phi(x) = x: the retention_* entries only     [LA §七] */
+  MHLA_PHI_IDENTITY = 3 /* phi(x) = x: the retention_* and linattn_cross_* entries only [LA §七] */
 } mhla_feature;
 
 typedef struct {
@@ -454,6 +454,79 @@ mhla_status gated_scan_backward(const void* x, const mhla_strides* x_strides, co
 mhla_status gated_scan_step(const void* x, const mhla_strides* x_strides, const void* g, const mhla_strides* g_strides,
                             float* states, const int* slots, int n_slots, void* out, const mhla_strides* out_strides,
                             int B, int D, mhla_dtype dt, int gate, void* stream);
+
+/* ---------------------------------------------------- linear cross attention
+ * Queries of one sequence that read another one, an encoder's tokens, of another
+ * length ([LA] §三 with the keys and values of the encoder; its sums are the
+ * constant-size state of [LA] §八):
+ *   S = sum_j phi(k_j) v_j^T  (d x d, S[c][e]),  z = sum_j phi(k_j)
+ *   y_t = phi(q_t) S / (phi(q_t) . z + eps)       (normalise = 0: y_t = phi(q_t) S)
+ * The encoder is summed up once (linattn_cross_states) and read by any number of
+ * calls, of prompts and of single queries (linattn_cross_read).
+ * Conventions of the linattn_cross_* entries:
+ *   - Queries [B, H, Nq, d], keys and values [B, Hk, Nk, d], H a multiple of Hk:
+ *     query head h reads key head h / (H / Hk).  d = 16, 32, 64 or 128.  Strides as
+ *     in the retention_* entries.
+ *   - cu_seqlens as there (packed, one side or both), at most 2^31 - 128 tokens a
+ *     side.  lens: NULL, or device int32 [B], the tokens of each encoder row of a
+ *     padded batch (not with cu_seqlens of the keys), clamped to [0, Nk]: what lies
+ *     behind them is not read, not-a-number among it.
+ *   - An encoder without tokens gives S = 0, z = 0.  Where phi(q) . z + eps is 0
+ *     (eps = 0 and nothing summed) the output is 0, and so are the gradients through it.
+ *   - S: [n_slots, Hk, d, d] fp32, z: [n_slots, Hk, d] fp32.
+ *   - mhla_options: feature and normalise (gamma = 1); NULL: ELU + 1 with the
+ *     normaliser.  MHLA_PHI_IDENTITY goes without one (normalise = 0).
+ *   - Not-a-number or infinite values reach what is computed from their own
+ *     sequence only (a query's: its own outputs, and backward dk and dv of its sequence).
+ *   - Every sum has a fixed order: equal calls give equal bits.
+ *   - bf16 with d = 64 or 128 runs on the tensor cores, everything else on the FP32
+ *     units. */
+
+/* Workspace bytes of linattn_cross_states and linattn_cross_read (backward = 0) or
+ * of linattn_cross_backward (backward = 1; enough for the others too) for B
+ * sequences of tokens_q queries and tokens_k encoder tokens in all (dense: B Nq,
+ * B Nk); 0 if the sizes are invalid or more than a call takes.  Valid for both
+ * dtypes, dense and packed. */
+size_t linattn_cross_workspace_bytes(int B, int H, int Hk, int tokens_q, int tokens_k, int d, int backward);
+
+/* The sums of B encoder sequences.
+ *   slots : NULL (sequence i writes slot i), or device int32 [B]: a sequence whose
+ *           slot is outside [0, n_slots), or is the slot of a sequence before it, is
+ *           not kept.
+ *   S, z  : written (not accumulated), zeros for a sequence without tokens; slots
+ *           of no sequence stay as they are. */
+mhla_status linattn_cross_states(const void* k, const mhla_strides* k_strides, const void* v, const mhla_strides* v_strides,
+                                 float* S, float* z, int B, int Hk, int N, int d, const int* cu_seqlens, const int* lens,
+                                 const int* slots, int n_slots, mhla_dtype dt, const mhla_options* opt, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Queries of B sequences read their sums.  N = 1 without cu_seqlens is the step of
+ * a decoder: every key head's S is read once for its query heads, and the workspace
+ * may be NULL.
+ *   slots : NULL (sequence i reads slot i), or device int32 [B]; several sequences
+ *           may read one slot.  A sequence whose slot is outside [0, n_slots) is left
+ *           out: its rows of y are not written. */
+mhla_status linattn_cross_read(const void* q, const mhla_strides* q_strides, const float* S, const float* z, void* y,
+                               const mhla_strides* y_strides, int B, int H, int Hk, int N, int d, const int* cu_seqlens,
+                               const int* slots, int n_slots, mhla_dtype dt, const mhla_options* opt, float eps,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradients of q, k and v through both, with den_t = phi(q_t) . z + eps:
+ *   u_t = S dy_t,  dden_t = -(phi(q_t) . u_t) / den_t^2
+ *   dq_t = phi'(q_t) * (u_t / den_t + dden_t z)
+ *   dS = sum_t (phi(q_t) / den_t) dy_t^T,  dz = sum_t phi(q_t) dden_t   (over a key head's query heads)
+ *   dk_j = phi'(k_j) * (dS v_j + dz),  dv_j = dS^T phi(k_j)
+ * (normalise = 0: den = 1, dden = 0); phi' as in retention_backward.
+ *   S, z       : those of linattn_cross_states for these k and v: slot i is sequence i
+ *   dq, dk, dv : written (not accumulated); rows of a padded encoder batch behind
+ *                lens become zeros, rows of no packed sequence stay as they are. */
+mhla_status linattn_cross_backward(const void* q, const mhla_strides* q_strides, const void* k, const mhla_strides* k_strides,
+                                   const void* v, const mhla_strides* v_strides, const float* S, const float* z,
+                                   const void* dy, const mhla_strides* dy_strides, void* dq, const mhla_strides* dq_strides,
+                                   void* dk, const mhla_strides* dk_strides, void* dv, const mhla_strides* dv_strides, int B,
+                                   int H, int Hk, int Nq, int Nk, int d, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                                   const int* lens, mhla_dtype dt, const mhla_options* opt, float eps, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* Workspace bytes for rala_forward; 0 if the sizes are invalid. */
 size_t rala_workspace_bytes(int B, int H, int N, int d, int cx);

@@ -12,6 +12,10 @@ from .binding import (  # noqa: F401
     gated_scan_checkpoint_rows,
     gated_scan_forward,
     gated_scan_step,
+    linattn_cross_backward,
+    linattn_cross_read,
+    linattn_cross_states,
+    linattn_cross_workspace_bytes,
     linattn_decode_step,
     linattn_decode_steps,
     load,

@@ -57,6 +57,10 @@ _SIGNATURES = {
     "gated_scan_forward": (_i, [_vp] * 6 + [_i] * 3 + [_vp, _vp, _vp, _i, _i, _vp, _i, _i, _vp]),
     "gated_scan_backward": (_i, [_vp] * 11 + [_i] * 3 + [_vp] * 4 + [_i, _i, _vp]),
     "gated_scan_step": (_i, [_vp] * 6 + [_i, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "linattn_cross_workspace_bytes": (_sz, [_i] * 7),
+    "linattn_cross_states": (_i, [_vp] * 6 + [_i] * 4 + [_vp, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp]),
+    "linattn_cross_read": (_i, [_vp] * 6 + [_i] * 5 + [_vp, _vp, _i, _i, _vp, _f, _vp, _sz, _vp]),
+    "linattn_cross_backward": (_i, [_vp] * 16 + [_i] * 6 + [_vp, _vp, _vp, _i, _vp, _f, _vp, _sz, _vp]),
     "mhla_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
 }
 
@@ -723,6 +727,117 @@ def gated_scan_step(x, g, states, out, *, gate="sigmoid", slots=None, stream=Non
                     (*_scan_strided(x, "x"), *_scan_strided(g, "g"), states.data_ptr(), _address(slots), n_slots,
                      *_scan_strided(out, "out"), B, D, _dtype(x), _gate(gate)), stream)
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_options(feature, normalise):
+    if feature not in _RETENTION_FEATURES:
+        raise ValueError(f"feature: one of {sorted(_RETENTION_FEATURES)}, got {feature!r}")
+    return ctypes.byref(MhlaOptions(_RETENTION_FEATURES[feature], 1 if normalise else 0, 1.0))
+
+
+def _cross_sums(S, z, Hk, d):
+    """The slots of S [slots, Hk, d, d] and z [slots, Hk, d]."""
+    if S.dim() != 4:
+        raise ValueError(f"S: expected [slots, Hk, d, d], got shape {tuple(S.shape)}")
+    n = S.shape[0]
+    _expect_fast(S, "S", (n, Hk, d, d), torch.float32)
+    _expect_fast(z, "z", (n, Hk, d), torch.float32)
+    _fits_int(slots=n)
+    return n
+
+
+def _cross_heads(S, H, d):
+    if S.dim() != 4:
+        raise ValueError(f"S: expected [slots, Hk, d, d], got shape {tuple(S.shape)}")
+    Hk = S.shape[1]
+    if Hk == 0 or H % Hk != 0:
+        raise ValueError(f"S: {Hk} heads, {H} query heads are no multiple of them")
+    return Hk
+
+
+def linattn_cross_workspace_bytes(B: int, H: int, Hk: int, tokens_q: int, tokens_k: int, d: int,
+                                  backward: bool = False) -> int:
+    if max(B, H, Hk, tokens_q, tokens_k, d) > 0x7fffffff:
+        return 0
+    return int(load().linattn_cross_workspace_bytes(B, H, Hk, tokens_q, tokens_k, d, 1 if backward else 0))
+
+
+def _cross_workspace(workspace, sizes, backward, dev, stream):
+    if workspace is None:  # of the call's stream, as in _retention_workspace
+        with torch.cuda.stream(stream):
+            workspace = new_workspace(linattn_cross_workspace_bytes(*sizes, backward), dev)
+    return workspace
+
+
+def linattn_cross_states(k, v, S, z, *, cu_seqlens=None, lens=None, slots=None, feature="elu1", normalise=True,
+                         workspace=None, stream=None):
+    """The sums S = sum phi(k_j) v_j^T, z = sum phi(k_j) of encoder sequences: k/v [B, Hk, N, d] with any strides (rows
+    contiguous), S [slots, Hk, d, d] and z [slots, Hk, d] fp32, written.  Packed sequences: k/v [1, Hk, tokens, d] and
+    int32 ``cu_seqlens`` [sequences + 1]; a padded batch: int32 ``lens`` [B], the tokens of each row.  ``slots`` int32:
+    the slot of each sequence."""
+    B, Hk, N, d = _retention_sizes(k, cu_seqlens)
+    _expect_like(k, ("v", v))
+    if S is None or z is None:
+        raise ValueError("S, z: required")
+    n_slots = _cross_sums(S, z, Hk, d)
+    _expect_fast(lens, "lens", (B,), torch.int32)
+    _expect_fast(slots, "slots", (B,), torch.int32)
+    opt = _cross_options(feature, bool(normalise))
+    dev = _retention_device((k, v), (S, z, cu_seqlens, lens, slots, workspace))
+    ws = _cross_workspace(workspace, (B, Hk, Hk, 0, N if cu_seqlens is not None else B * N, d), False, dev, stream)
+    _retention_call("linattn_cross_states", dev,
+                    (*_strided(k, "k"), *_strided(v, "v"), S.data_ptr(), z.data_ptr(), B, Hk, N, d, _address(cu_seqlens),
+                     _address(lens), _address(slots), n_slots, _dtype(k), opt, ws.data_ptr(), ws.nbytes), stream)
+    return S, z
+
+
+def linattn_cross_read(q, S, z, y, *, cu_seqlens=None, slots=None, feature="elu1", normalise=True, eps=1e-6,
+                       workspace=None, stream=None):
+    """y_t = phi(q_t) S / (phi(q_t) . z + eps) from the sums of linattn_cross_states: q/y [B, H, N, d] with any strides
+    (rows contiguous), H a multiple of S's heads; packed queries: [1, H, tokens, d] and int32 ``cu_seqlens``.  ``slots``
+    int32: the slot that each sequence reads, an entry outside the pool leaves its rows out.  N = 1: a decoder's step."""
+    B, H, N, d = _retention_sizes(q, cu_seqlens)
+    _expect_like(q, ("y", y))
+    Hk = _cross_heads(S, H, d)
+    n_slots = _cross_sums(S, z, Hk, d)
+    _expect_fast(slots, "slots", (B,), torch.int32)
+    opt = _cross_options(feature, bool(normalise))
+    dev = _retention_device((q, y), (S, z, cu_seqlens, slots, workspace))
+    if workspace is None and (N != 1 or cu_seqlens is not None):
+        workspace = _cross_workspace(None, (B, H, Hk, N if cu_seqlens is not None else B * N, 0, d), False, dev, stream)
+    _retention_call("linattn_cross_read", dev,
+                    (*_strided(q, "q"), S.data_ptr(), z.data_ptr(), *_strided(y, "y"), B, H, Hk, N, d,
+                     _address(cu_seqlens), _address(slots), n_slots, _dtype(q), opt, eps, _address(workspace),
+                     0 if workspace is None else workspace.nbytes), stream)
+    return y
+
+
+def linattn_cross_backward(q, k, v, S, z, dy, dq, dk, dv, *, cu_seqlens_q=None, cu_seqlens_k=None, lens=None,
+                           feature="elu1", normalise=True, eps=1e-6, workspace=None, stream=None):
+    """Gradients of linattn_cross_read of linattn_cross_states (slot i is sequence i) from dy = dL/dY; dq, dk and dv are
+    written, rows of a padded encoder batch behind ``lens`` as zeros.  Shapes as there."""
+    B, H, Nq, d = _retention_sizes(q, cu_seqlens_q)
+    Bk, Hk, Nk, dk_ = _retention_sizes(k, cu_seqlens_k)
+    if Bk != B or dk_ != d or k.dtype != q.dtype:
+        raise ValueError(f"k: {Bk} sequences of width {dk_}, {k.dtype}; expected {B} of width {d}, {q.dtype}")
+    _expect_like(q, ("dy", dy), ("dq", dq))
+    _expect_like(k, ("v", v), ("dk", dk), ("dv", dv))
+    if _cross_heads(S, H, d) != Hk:
+        raise ValueError(f"S: {S.shape[1]} heads, k has {Hk}")
+    if _cross_sums(S, z, Hk, d) != B:
+        raise ValueError(f"S: {S.shape[0]} slots, expected one for each of {B} sequences")
+    _expect_fast(lens, "lens", (B,), torch.int32)
+    opt = _cross_options(feature, bool(normalise))
+    dev = _retention_device((q, k, v, dy, dq, dk, dv), (S, z, cu_seqlens_q, cu_seqlens_k, lens, workspace))
+    ws = _cross_workspace(workspace, (B, H, Hk, Nq if cu_seqlens_q is not None else B * Nq,
+                                      Nk if cu_seqlens_k is not None else B * Nk, d), True, dev, stream)
+    _retention_call("linattn_cross_backward", dev,
+                    (*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), S.data_ptr(), z.data_ptr(),
+                     *_strided(dy, "dy"), *_strided(dq, "dq"), *_strided(dk, "dk"), *_strided(dv, "dv"), B, H, Hk, Nq, Nk, d,
+                     _address(cu_seqlens_q), _address(cu_seqlens_k), _address(lens), _dtype(q), opt, eps, ws.data_ptr(),
+                     ws.nbytes), stream)
+    return dq, dk, dv
 
 
 def rala_forward(q, k, v, x, w, y, *, workspace=None, stream=None):

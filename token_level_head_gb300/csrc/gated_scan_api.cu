@@ -31,23 +31,6 @@ mhla_status sizes_of(Sizes* s, int B, int N, int D, const int* cu, mhla_dtype dt
   return MHLA_OK;
 }
 
-struct Region {
-  const void* p;
-  size_t n;
-  bool written;
-};
-// Does one of the regions from `first` on overlap one before it, one of the two written?  (The token tensors, before
-// `first`, may be interleaved slices of one tensor: disjoint() answers for them.)
-template <int n>
-bool clash(const Region (&r)[n], int first) {
-  for (int i = first; i < n; ++i)
-    for (int j = 0; j < i; ++j)
-      if ((r[i].written || r[j].written) && !apart(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
-  return false;
-}
-
-size_t span_bytes(const RetTensor& t, const Extent& e) { return (size_t)span(t, e) * e.es; }
-
 bool kept_bytes(size_t* n, const Extent& e) {
   const Wide w = (Wide)e.b * ret_pieces((int)e.n, kScanKept) * e.d * 4;
   *n = (size_t)w;

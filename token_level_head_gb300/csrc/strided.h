@@ -110,5 +110,22 @@ inline bool apart(const void* a, size_t an, const void* b, size_t bn) {
   return an == 0 || bn == 0 || a == nullptr || b == nullptr || x >= y + bn || y >= x + an;
 }
 
+struct Region {
+  const void* p;
+  size_t n;
+  bool written;
+};
+// Does one of the regions from `first` on overlap one before it, one of the two written?  (The token tensors, before
+// `first`, may be interleaved slices of one tensor: disjoint() answers for them.)
+template <int n>
+bool clash(const Region (&r)[n], int first) {
+  for (int i = first; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((r[i].written || r[j].written) && !apart(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+  return false;
+}
+
+inline size_t span_bytes(const RetTensor& t, const Extent& e) { return (size_t)span(t, e) * e.es; }
+
 }  // namespace
 }  // namespace mhla
