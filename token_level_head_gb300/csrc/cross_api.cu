@@ -7,6 +7,7 @@
 #include "cross.h"
 #include "internal.h"
 #include "strided.h"
+#include "tc_cross.h"
 
 namespace mhla {
 namespace {
@@ -133,8 +134,9 @@ mhla_status linattn_cross_states(const void* k, const mhla_strides* k_strides, c
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWorkspacePrefix);
   a.status = &static_cast<WorkspaceHeader*>(workspace)->status;
   cudaError_t err = cudaSuccess;
-  if (a.ks.segs > 0) err = simt_cross_states_launch(a, dt, static_cast<cudaStream_t>(stream));
-  if (err == cudaSuccess && cross_joined(a.ks)) err = cross_join_launch(a, false, false, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.ks.segs > 0) err = tc_cross_supported(d, dt) ? tc_cross_states_launch(a, s) : simt_cross_states_launch(a, dt, s);
+  if (err == cudaSuccess && cross_joined(a.ks)) err = cross_join_launch(a, false, a.ks.segs > 0, s);
   return from_cuda(err);
 }
 
@@ -175,7 +177,8 @@ mhla_status linattn_cross_read(const void* q, const mhla_strides* q_strides, con
     return from_cuda(cross_step_launch(a, dt, static_cast<cudaStream_t>(stream)));
   }
   a.status = &static_cast<WorkspaceHeader*>(workspace)->status;
-  return from_cuda(simt_cross_read_launch(a, dt, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(tc_cross_supported(d, dt) ? tc_cross_read_launch(a, s) : simt_cross_read_launch(a, dt, s));
 }
 
 mhla_status linattn_cross_backward(const void* q, const mhla_strides* q_strides, const void* k, const mhla_strides* k_strides,
@@ -244,7 +247,8 @@ mhla_status linattn_cross_backward(const void* q, const mhla_strides* q_strides,
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWorkspacePrefix);
   a.dS = a.part + (size_t)parts;
   a.status = &static_cast<WorkspaceHeader*>(workspace)->status;
-  return from_cuda(simt_cross_backward_launch(a, dt, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(tc_cross_supported(d, dt) ? tc_cross_backward_launch(a, s) : simt_cross_backward_launch(a, dt, s));
 }
 
 }  // extern "C"

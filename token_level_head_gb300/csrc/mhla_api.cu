@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "retention.h"
+#include "tc_cross.h"
 
 namespace mhla {
 
@@ -436,6 +437,7 @@ void mhla_debug_set_wait_limit_ns(unsigned long long ns) {
   tc_mhla_set_wait_limit(ns);
   tc_backward_set_wait_limit(ns);
   tc_retention_set_wait_limit(ns);
+  tc_cross_set_wait_limit(ns);
 }
 
 }  // extern "C"

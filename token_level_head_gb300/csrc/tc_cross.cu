@@ -1,0 +1,918 @@
+// Linear cross attention on the sm_103a tensor cores (bf16, d = 64 or 128): the same steps as the FP32 kernels'
+// (cross_simt.cu), a tile of 128 tokens at a time.
+//
+//   states  D[e][c] += sum_t v[t][e] phi(k)[t][c]   (A = v, B = phi(k) as a sum of three bf16 numbers: S is an fp32
+//           result), z in fp32 registers
+//   read    y[t][e] = (sum_c phi(q)[t][c] S[c][e]) / den_t
+//   query   u[t][c] = sum_e dy[t][e] S[c][e], dS^T[e][c] += sum_t dy[t][e] w[t][c] with w = phi(q) / den; S and w as sums of
+//           two bf16 numbers (dq is a difference of two nearly equal terms: u / den and dden z), dy as it is; dz in fp32
+//   key     dv[t][e] = sum_c phi(k)[t][c] dS[c][e], dphi(k)[t][c] = sum_e v[t][e] dS[c][e] (dS as a sum of two)
+//
+// Bound: memory (2, 2, 3 and 4 tensors), next to it the instructions that take the features and turn tiles.  A block has a
+// segment of a head and walks over its tiles: TMA brings the tile after next into the buffer that is free, D / 8 warps take
+// the features (a thread 32 columns of a row, in place in the 128-byte-swizzled tile), one thread issues the MMAs, the same
+// warps take the results from tensor memory, put them into the tile's buffer and store 64 bytes of a row together.  Two
+// blocks an SM for d = 64 (reads: three), one for d = 128, hide one another's waits.  Every wait is bounded (on time-out the
+// block stops, sets the status word and drains what it has in flight).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "cross.cuh"
+#include "tc_common.cuh"
+#include "tc_cross.h"
+
+namespace mhla {
+namespace {
+
+using namespace tc;
+
+constexpr int kT = 128;                       // tokens of a tile
+constexpr int kAtom = kT * 128;               // bytes of 64 columns of a tile
+constexpr uint64_t kWaitNs = 500000000ull;    // 0.5 s: a wait's default limit
+
+template <int D>
+struct Tc {
+  static constexpr int kTile = kT * D * 2;    // bytes of a tile of tokens
+  static constexpr int kMat = D * D * 2;      // of a d x d matrix
+  static constexpr int kThreads = 4 * D;      // a row 32 columns a thread
+  static constexpr int kCols = D / 32;        // threads of a row
+};
+
+struct Bars {
+  uint64_t full[2];  // a tile's tensors landed (tx)
+  uint64_t mma;      // MMA commits
+  uint64_t mma2;
+  unsigned long long wait_ns;
+  unsigned* status;
+  uint32_t tbase;
+  int abort;
+  int scratch;
+};
+
+struct TcArgs {
+  CrossArgs c;
+  CUtensorMap a, b;            // the tile's tensors: states, key: k, v; read: q; query: q, dy
+  int a_h, a_b, b_h, b_b;      // whether the tensors have heads and batch entries (stride not 0)
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ bool aborted(const int* ab) { return *reinterpret_cast<const volatile int*>(ab) != 0; }
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Bars* b) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait_ns(bar, parity, 256)) return true;
+    if (aborted(&b->abort)) return false;
+    if (globaltimer_ns() - t0 > b->wait_ns) break;
+  }
+  *reinterpret_cast<volatile int*>(&b->abort) = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b) {
+  return mbar_test(bar, parity) || wait_slow(bar, parity, b);
+}
+// Short wait (10 ms at most), only while winding down.
+__device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_ns(bar, parity, 1000))
+    if (globaltimer_ns() - t0 > 10000000ull) return;
+}
+
+// 16-byte piece j (columns 8 j ..) of row r of a tile of 64-column atoms of `rows` rows.
+__device__ __forceinline__ uint4* piece(uint8_t* tile, int rows, int r, int j) {
+  return reinterpret_cast<uint4*>(tile + (j >> 3) * (rows * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void unpack8(uint4 u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    f[2 * m] = __uint_as_float(w[m] << 16);
+    f[2 * m + 1] = __uint_as_float(w[m] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+// f - bf16(f) in place, given bf16(f) packed.
+__device__ __forceinline__ void remainder8(float* f, uint4 h) {
+  float g[8];
+  unpack8(h, g);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) f[x] -= g[x];
+}
+
+// phi and, from phi alone, phi'.
+template <int F>
+__device__ __forceinline__ float feature(float x) {
+  if (F == MHLA_PHI_ELU1) {  // as phi_f, but not-a-number stays
+    float m, e;
+    asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(m) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m * 1.4426950408889634f));
+    return e + fmaxf(x, 0.f);
+  }
+  if (F == MHLA_PHI_RELU) return x > 0.f ? x : (x == x ? 0.f : x);  // (not-a-number stays)
+  if (F == MHLA_PHI_EXP) return __expf(x);
+  return x;
+}
+template <int F>
+__device__ __forceinline__ float slope(float phi) {
+  if (F == MHLA_PHI_ELU1) return phi < 1.f ? phi : (phi == phi ? 1.f : phi);
+  if (F == MHLA_PHI_RELU) return phi > 0.f ? 1.f : 0.f;
+  if (F == MHLA_PHI_EXP) return phi;
+  return 1.f;
+}
+
+__device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
+  if (threadIdx.x == 0) {
+    mbar_init(&b->full[0], 1);
+    mbar_init(&b->full[1], 1);
+    mbar_init(&b->mma, 1);
+    mbar_init(&b->mma2, 1);
+    b->abort = 0;
+    b->wait_ns = p.wait_ns;
+    b->status = p.c.status;
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 32) {
+    tmem_alloc(&b->tbase, cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+// The end of a block: after an abort (one thread) short waits for the copies and MMAs in flight; then the columns are
+// freed.  issued: tiles whose copies were issued; mmas, mmas2: commits.
+__device__ __forceinline__ void finish(Bars* b, uint32_t cols, int issued, int mmas, int mmas2) {
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0 && aborted(&b->abort)) {
+    for (int j = max(issued - 2, 0); j < issued; ++j) drain(&b->full[j & 1], (j >> 1) & 1);
+    if (mmas > 0) drain(&b->mma, (mmas - 1) & 1);
+    if (mmas2 > 0) drain(&b->mma2, (mmas2 - 1) & 1);
+    atomicOr(b->status, 1u);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) tmem_dealloc(b->tbase, cols);
+}
+
+// One thread: a tile of one tensor (two atoms for d = 128).
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t* to, const CUtensorMap* m, int row, int h, int b, uint64_t* bar) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) tma_load_4d(to + i * kAtom, m, 64 * i, row, h, b, bar);
+}
+
+// A d x d fp32 matrix [r][c] as bf16 tiles of D rows, the high part and, where lo is given, the low part.
+template <int D>
+__device__ __forceinline__ void load_matrix(uint8_t* hi, uint8_t* lo, const float* from) {
+  for (int i = threadIdx.x; i < D * D / 8; i += Tc<D>::kThreads) {
+    const int r = i / (D / 8), j = i % (D / 8);
+    float f[8];
+    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(from + r * D + 8 * j);
+    *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(from + r * D + 8 * j + 4);
+    const uint4 u = pack8(f);
+    *piece(hi, D, r, j) = u;
+    if (lo != nullptr) {
+      remainder8(f, u);
+      *piece(lo, D, r, j) = pack8(f);
+    }
+  }
+}
+
+// The warp's 32 rows x 32 columns of a tile to memory: eight rows of 64 bytes at a time; n rows of the tile are written.
+__device__ __forceinline__ void store_rows(uint8_t* tile, __nv_bfloat16* out, long long sn, int n, int row0, int col0, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + i * 8 + lane / 4, j = col0 / 8 + lane % 4;
+    const uint4 u = *piece(tile, kT, r, j);
+    if (r < n) *reinterpret_cast<uint4*>(out + r * sn + 8 * j) = u;
+  }
+}
+
+// Descriptors.  Tokens' tile as A or B with the tokens along K ("MN-major"): K steps of 16 rows are 2048 bytes apart, 64
+// columns an atom; with the columns along K ("K-major"): steps of 32 bytes, 4 to an atom.
+__device__ __forceinline__ uint64_t along_rows(uint32_t tile, uint32_t atom) { return smem_desc(tile, atom, 1024); }
+template <int D>
+__device__ __forceinline__ uint64_t along_cols(uint32_t tile, uint32_t atom, int k) {
+  return smem_desc(tile + (k >> 2) * atom, 16, 1024) + (k & 3) * 2;
+}
+
+// ================================================================ states
+// K and V in two buffers (phi's high part is put over K), the middle and low parts in one more each.
+template <int D>
+struct SumSmem {
+  static constexpr int kK = 0, kV = 2 * Tc<D>::kTile, kMid = 4 * Tc<D>::kTile, kLo = 5 * Tc<D>::kTile, kBars = 6 * Tc<D>::kTile;
+  static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
+};
+template <int D, int F>
+__global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_states_kernel(const __grid_constant__ TcArgs p) {
+  using X = Tc<D>;
+  using M = SumSmem<D>;
+  constexpr bool kExact = F == MHLA_PHI_RELU || F == MHLA_PHI_IDENTITY;  // phi(k) is a bf16 number
+  constexpr uint32_t kColumns = 128;
+  extern __shared__ __align__(16) uint8_t smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
+  const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
+  if (g.seq < 0) return;
+  setup(p, b, kColumns);
+  const uint32_t tmem = b->tbase;
+  const int tiles = (g.len + kT - 1) / kT;
+  const int hh = h, bb = p.c.ks.cu == nullptr ? g.seq : 0;
+  int issued = 0, mmas = 0;
+  const auto fetch = [&](int j) {  // one thread
+    uint64_t* bar = &b->full[j & 1];
+    mbar_arrive_expect_tx(bar, 2 * X::kTile);
+    load_tile<D>(sm + M::kK + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? hh : 0, p.a_b ? bb : 0, bar);
+    load_tile<D>(sm + M::kV + (j & 1) * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? hh : 0, p.b_b ? bb : 0, bar);
+  };
+  if (tiles > 0) {
+    if (tid == 0) fetch(0);
+    issued = 1;
+  }
+  constexpr int P = D / 8, ROWS = X::kThreads / P;  // pieces of a row, rows at a time
+  const int pc = tid % P, r0 = tid / P;
+  float z[8] = {};
+  bool ok = true;
+  for (int j = 0; j < tiles; ++j) {
+    if (j > 0) ok = wait(&b->mma, (j - 1) & 1, b);  // the other buffer, mid and lo have been read
+    if (ok && j + 1 < tiles) {
+      if (tid == 0) fetch(j + 1);
+      ++issued;
+    }
+    ok = ok && wait(&b->full[j & 1], (j >> 1) & 1, b);
+    uint8_t *kt = sm + M::kK + (j & 1) * X::kTile, *vt = sm + M::kV + (j & 1) * X::kTile;
+    const int n = g.len - j * kT;
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < kT / ROWS; ++i) {
+        const int r = r0 + i * ROWS;
+        uint4* at = piece(kt, kT, r, pc);
+        float f[8];
+        unpack8(*at, f);
+        if (r >= n) {  // behind the sequence: nothing of what lies there counts
+#pragma unroll
+          for (int x = 0; x < 8; ++x) f[x] = 0.f;
+          *piece(vt, kT, r, pc) = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            f[x] = feature<F>(f[x]);
+            z[x] += f[x];
+          }
+        }
+        const uint4 hi = pack8(f);
+        *at = hi;
+        if (!kExact) {
+          remainder8(f, hi);
+          const uint4 mid = pack8(f);
+          *piece(sm + M::kMid, kT, r, pc) = mid;
+          remainder8(f, mid);
+          *piece(sm + M::kLo, kT, r, pc) = pack8(f);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t ka = smem_u32(kt), va = smem_u32(vt), mid = smem_u32(sm + M::kMid), lo = smem_u32(sm + M::kLo);
+      // d = 64: A's rows 64 .. 127 are another tile's columns, whose results are not read; B = the high and the middle part
+      // side by side (N = 128), then the low part onto the middle one's columns
+      const uint64_t da = along_rows(va, D == 64 ? mid - va : kAtom);
+      if (D == 64 && !kExact) {
+        const uint64_t d1 = along_rows(ka, mid - ka), d2 = along_rows(lo, kAtom);
+#pragma unroll
+        for (int s = 0; s < kT / 16; ++s) {
+          mma_bf16(tmem, da + s * 128, d1 + s * 128, idesc_bf16_f32(128, 128, 1, 1), j > 0 || s > 0);
+          mma_bf16(tmem + 64, da + s * 128, d2 + s * 128, idesc_bf16_f32(128, 64, 1, 1), true);
+        }
+      } else {
+#pragma unroll
+        for (int part = 0; part < (kExact ? 1 : 3); ++part) {
+          const uint64_t db = along_rows(part == 0 ? ka : part == 1 ? mid : lo, kAtom);
+#pragma unroll
+          for (int s = 0; s < kT / 16; ++s)
+            mma_bf16(tmem, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
+        }
+      }
+      mma_commit(&b->mma);
+    }
+    ++mmas;
+  }
+  float *so = nullptr, *zo = nullptr;
+  if (cross_joined(p.c.ks) && g.nseg != 1) {
+    so = p.c.part + ((size_t)k * p.c.Hk + h) * (D * D + D);
+    zo = so + D * D;
+  } else {
+    const int slot = ret_slot(p.c.slots, p.c.n_slots, g.seq);
+    if (slot >= 0) {
+      so = p.c.S + ((size_t)slot * p.c.Hk + h) * D * D;
+      zo = p.c.z + ((size_t)slot * p.c.Hk + h) * D;
+    }
+  }
+  if (ok && tiles > 0) ok = wait(&b->mma, (tiles - 1) & 1, b);
+  if (__syncthreads_and(ok)) {
+    tc_fence_after();
+    float* zp = reinterpret_cast<float*>(sm + M::kMid);  // [ROWS][D]
+#pragma unroll
+    for (int x = 0; x < 8; ++x) zp[r0 * D + 8 * pc + x] = z[x];
+    __syncthreads();
+    if (zo != nullptr) {
+      if (tid < D) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < ROWS; ++i) s += zp[i * D + tid];
+        zo[tid] = s;
+      }
+      const int e = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 32;
+      if ((warp & 3) * 32 < D) {
+        float v[32];
+        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
+        if (tiles > 0) {
+          tmem_ld16(at, v);
+          tmem_ld16(at + 16, v + 16);
+          if (D == 64 && !kExact) {
+            float w[32];
+            tmem_ld16(at + 64, w);
+            tmem_ld16(at + 80, w + 16);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] += w[x];
+          }
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) so[(c0 + x) * D + e] = tiles > 0 ? v[x] : 0.f;
+      }
+    }
+  }
+  finish(b, kColumns, issued, mmas, 0);
+}
+
+// ================================================================ read
+template <int D>
+struct ReadSmem {
+  static constexpr int kQ = 0, kS = 2 * Tc<D>::kTile, kZ = kS + Tc<D>::kMat, kDen = kZ + D * 4, kBars = kDen + Tc<D>::kCols * kT * 4;
+  static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
+};
+template <int D, int F>
+__global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_read_kernel(const __grid_constant__ TcArgs p) {
+  using X = Tc<D>;
+  using M = ReadSmem<D>;
+  constexpr uint32_t kColumns = D;
+  extern __shared__ __align__(16) uint8_t smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
+  float *z = reinterpret_cast<float*>(sm + M::kZ), *den = reinterpret_cast<float*>(sm + M::kDen);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % p.c.H, k = blockIdx.x / p.c.H;
+  const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
+  if (g.seq < 0 || g.len == 0) return;
+  const int slot = p.c.slots != nullptr ? p.c.slots[g.seq] : g.seq;
+  if (slot < 0 || slot >= p.c.n_slots) return;
+  setup(p, b, kColumns);
+  const uint32_t tmem = b->tbase;
+  const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
+  const auto fetch = [&](int j) {
+    uint64_t* bar = &b->full[j & 1];
+    mbar_arrive_expect_tx(bar, X::kTile);
+    load_tile<D>(sm + M::kQ + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+  };
+  int issued = min(tiles, 2), mmas = 0;
+  if (tid == 0)
+    for (int j = 0; j < issued; ++j) fetch(j);
+  const size_t unit = (size_t)slot * p.c.Hk + h / (p.c.H / p.c.Hk);
+  load_matrix<D>(sm + M::kS, nullptr, p.c.S + unit * D * D);
+  if (tid < D) z[tid] = p.c.z[unit * D + tid];
+  fence_proxy_async_smem();
+  __syncthreads();
+  const int row = (warp & 3) * 32 + lane, cg = warp >> 2;  // the thread's row, and its 32 columns
+  const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
+  const uint32_t sa = smem_u32(sm + M::kS);
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.y.p)) + cross_base(p.c.qs, p.c.y, g.seq, h) +
+                     (long long)g.row0 * p.c.y.sn;
+  bool ok = true;
+  for (int j = 0; j < tiles; ++j) {
+    uint8_t* qt = sm + M::kQ + (j & 1) * X::kTile;
+    ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
+    if (ok) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4* q = piece(qt, kT, row, cg * 4 + i);
+        float f[8], zz[8];
+        unpack8(*q, f);
+        *reinterpret_cast<float4*>(zz) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i);
+        *reinterpret_cast<float4*>(zz + 4) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i + 4);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          f[x] = feature<F>(f[x]);
+          d = fmaf(f[x], zz[x], d);
+        }
+        if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
+      }
+      den[cg * kT + row] = d;
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t qa = smem_u32(qt);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+        mma_bf16(tmem, along_cols<D>(qa, kAtom, s), along_rows(sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1), s > 0);
+      mma_commit(&b->mma);
+    }
+    ++mmas;
+    float inv = 1.f;
+    if (p.c.normalise) {
+      float d = p.c.eps;
+#pragma unroll
+      for (int i = 0; i < X::kCols; ++i) d += den[i * kT + row];
+      inv = cross_inverse(d);
+    }
+    ok = wait(&b->mma, j & 1, b);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      float v[32];
+      tmem_ld16(at, v);
+      tmem_ld16(at + 16, v + 16);
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 32; ++x) v[x] *= inv;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *piece(qt, kT, row, cg * 4 + i) = pack8(v + 8 * i);
+      __syncwarp();
+      store_rows(qt, y + (long long)j * kT * p.c.y.sn, p.c.y.sn, g.len - j * kT, (warp & 3) * 32, cg * 32, lane);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+    if (j + 2 < tiles) {
+      if (tid == 0) fetch(j + 2);
+      ++issued;
+    }
+  }
+  finish(b, kColumns, issued, mmas, 0);
+}
+
+// ================================================================ backward over the queries
+// The tiles of d = 128 leave 3 KB of a block's 227: what is small lies before them, up to the next 1024 bytes.
+template <int D>
+struct QuerySmem {
+  static constexpr int kQ = 0, kY = 2 * Tc<D>::kTile, kLo = 4 * Tc<D>::kTile, kS = 5 * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat,
+                       kEnd = kSLo + Tc<D>::kMat;
+  static constexpr int kZ = 0, kDen = kZ + D * 4, kBars = kDen + Tc<D>::kCols * kT * 4, kSmall = kBars + (int)sizeof(Bars);
+  static constexpr int kBytes = (kSmall + 1023) / 1024 * 1024 + kEnd;
+  static_assert(kBytes <= 232448 / (D == 64 ? 2 : 1), "two blocks of d = 64 an SM, one of d = 128");
+};
+// 32 values a lane: lane i ends with the warp's sum of value i.
+__device__ __forceinline__ float sum_turned(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+template <int D, int F>
+__global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_query_kernel(const __grid_constant__ TcArgs p) {
+  using X = Tc<D>;
+  using M = QuerySmem<D>;
+  constexpr uint32_t kColumns = 2 * D;  // u, dS^T
+  extern __shared__ __align__(16) uint8_t smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + M::kSmall + 1023) & ~uintptr_t(1023));
+  if (sm + M::kEnd > smraw + M::kBytes) {  // (shared memory starts at a multiple of 1024 bytes, or near enough)
+    if (threadIdx.x == 0) atomicOr(p.c.status, 1u);
+    return;
+  }
+  Bars* b = reinterpret_cast<Bars*>(smraw + M::kBars);
+  float *z = reinterpret_cast<float*>(smraw + M::kZ), *den = reinterpret_cast<float*>(smraw + M::kDen);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % p.c.H, k = blockIdx.x / p.c.H;
+  const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
+  if (g.seq < 0) return;
+  setup(p, b, kColumns);
+  const uint32_t tmem = b->tbase;
+  const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
+  const auto fetch = [&](int j) {
+    uint64_t* bar = &b->full[j & 1];
+    mbar_arrive_expect_tx(bar, 2 * X::kTile);
+    load_tile<D>(sm + M::kQ + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+    load_tile<D>(sm + M::kY + (j & 1) * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
+  };
+  int issued = min(tiles, 2), mmas = 0, mmas2 = 0;
+  if (tid == 0)
+    for (int j = 0; j < issued; ++j) fetch(j);
+  const size_t unit = (size_t)g.seq * p.c.Hk + h / (p.c.H / p.c.Hk);
+  load_matrix<D>(sm + M::kS, sm + M::kSLo, p.c.S + unit * D * D);
+  if (tid < D) z[tid] = p.c.z[unit * D + tid];
+  fence_proxy_async_smem();
+  __syncthreads();
+  const int row = (warp & 3) * 32 + lane, cg = warp >> 2;
+  const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
+  const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo), wl = smem_u32(sm + M::kLo);
+  __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dq.p)) + cross_base(p.c.qs, p.c.dq, g.seq, h) +
+                      (long long)g.row0 * p.c.dq.sn;
+  float dz = 0.f;  // of column cg * 32 + lane, over the warp's rows
+  bool ok = true;
+  for (int j = 0; j < tiles; ++j) {
+    uint8_t *qt = sm + M::kQ + (j & 1) * X::kTile, *yt = sm + M::kY + (j & 1) * X::kTile;
+    const int n = g.len - j * kT;
+    const bool live = row < n;
+    float f[32];
+    ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
+    if (ok) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        unpack8(*piece(qt, kT, row, cg * 4 + i), f + 8 * i);
+        if (!live) *piece(yt, kT, row, cg * 4 + i) = make_uint4(0, 0, 0, 0);
+        float zz[8];
+        *reinterpret_cast<float4*>(zz) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i);
+        *reinterpret_cast<float4*>(zz + 4) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i + 4);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          f[8 * i + x] = live ? feature<F>(f[8 * i + x]) : 0.f;
+          d = fmaf(f[8 * i + x], zz[x], d);
+        }
+      }
+      den[cg * kT + row] = d;
+    }
+    if (!live) fence_proxy_async_smem();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    float inv = 1.f;
+    if (p.c.normalise) {
+      float d = p.c.eps;
+#pragma unroll
+      for (int i = 0; i < X::kCols; ++i) d += den[i * kT + row];
+      inv = cross_inverse(d);
+    }
+    if (tid == 0) {  // u = dy S^T
+      tc_fence_after();
+      const uint32_t ya = smem_u32(yt);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          mma_bf16(tmem, along_cols<D>(ya, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s), idesc_bf16_f32(128, D, 0, 0),
+                   s > 0 || part > 0);
+      mma_commit(&b->mma);
+    }
+    ++mmas;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // w over phi's place
+      float w[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) w[x] = f[8 * i + x] * inv;
+      const uint4 hi = pack8(w);
+      *piece(qt, kT, row, cg * 4 + i) = hi;
+      remainder8(w, hi);
+      *piece(sm + M::kLo, kT, row, cg * 4 + i) = pack8(w);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {  // dS^T += dy^T w  (d = 64: A's rows 64 .. 127 are another tile's columns, whose results are not read)
+      tc_fence_after();
+      const uint32_t ya = smem_u32(yt), qa = smem_u32(qt);
+      const uint64_t da = along_rows(ya, D == 64 ? wl - ya : kAtom);
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const uint64_t db = along_rows(part ? wl : qa, kAtom);
+#pragma unroll
+        for (int s = 0; s < kT / 16; ++s)
+          mma_bf16(tmem + D, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
+      }
+      mma_commit(&b->mma2);
+    }
+    ++mmas2;
+    ok = __all_sync(0xffffffffu, wait(&b->mma, j & 1, b));
+    float u[32];
+    if (ok) {
+      tc_fence_after();
+      tmem_ld16(at, u);
+      tmem_ld16(at + 16, u + 16);
+      tmem_ld_wait();
+      float s = 0.f;
+#pragma unroll
+      for (int x = 0; x < 32; ++x) s = fmaf(f[x], u[x], s);
+      den[cg * kT + row] = s;
+    }
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+    float dd = 0.f;
+    if (p.c.normalise && live) {
+#pragma unroll
+      for (int i = 0; i < X::kCols; ++i) dd += den[i * kT + row];
+      dd *= -inv * inv;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float zz[4];
+      *reinterpret_cast<float4*>(zz) = *reinterpret_cast<const float4*>(z + cg * 32 + 4 * i);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        u[4 * i + x] = slope<F>(f[4 * i + x]) * fmaf(u[4 * i + x], inv, dd * zz[x]);
+        f[4 * i + x] *= dd;
+      }
+    }
+    if (p.c.normalise) dz += sum_turned(f, lane);
+    ok = __all_sync(0xffffffffu, wait(&b->mma2, j & 1, b));  // w has been read
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *piece(qt, kT, row, cg * 4 + i) = pack8(u + 8 * i);
+      __syncwarp();
+      store_rows(qt, dq + (long long)j * kT * p.c.dq.sn, p.c.dq.sn, n, (warp & 3) * 32, cg * 32, lane);
+    }
+    fence_proxy_async_smem();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    if (j + 2 < tiles) {
+      if (tid == 0) fetch(j + 2);
+      ++issued;
+    }
+  }
+  if (ok) {
+    tc_fence_after();
+    float* out = p.c.part + ((size_t)k * p.c.H + h) * (D * D + D);
+    den[(warp & 3) * D + cg * 32 + lane] = dz;  // (4 D floats are there: kCols * kT)
+    const int e = (warp & 3) * 32 + lane, c0 = cg * 32;
+    if ((warp & 3) * 32 < D) {
+      float v[32];
+      if (tiles > 0) {
+        tmem_ld16(at + D, v);
+        tmem_ld16(at + D + 16, v + 16);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) out[(c0 + x) * D + e] = tiles > 0 ? v[x] : 0.f;
+    }
+    __syncthreads();
+    if (tid < D) out[D * D + tid] = den[tid] + den[D + tid] + den[2 * D + tid] + den[3 * D + tid];
+  }
+  finish(b, kColumns, issued, mmas, mmas2);
+}
+
+// ================================================================ backward over the keys
+template <int D>
+struct KeySmem {
+  static constexpr int kK = 0, kV = 2 * Tc<D>::kTile, kS = 4 * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat, kZ = kSLo + Tc<D>::kMat,
+                       kBars = kZ + D * 4;
+  static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
+};
+template <int D, int F>
+__global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key_kernel(const __grid_constant__ TcArgs p) {
+  using X = Tc<D>;
+  using M = KeySmem<D>;
+  constexpr uint32_t kColumns = 2 * D;  // dv, dphi(k)
+  extern __shared__ __align__(16) uint8_t smraw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
+  float* z = reinterpret_cast<float*>(sm + M::kZ);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
+  const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
+  if (g.seq < 0) return;
+  const int rows = p.c.ks.cu != nullptr ? g.len : min(p.c.ks.L, p.c.ks.N - g.row0);  // dense: zeros behind the tokens
+  setup(p, b, kColumns);
+  const uint32_t tmem = b->tbase;
+  const int tiles = (rows + kT - 1) / kT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
+  const auto fetch = [&](int j) {
+    uint64_t* bar = &b->full[j & 1];
+    mbar_arrive_expect_tx(bar, 2 * X::kTile);
+    load_tile<D>(sm + M::kK + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+    load_tile<D>(sm + M::kV + (j & 1) * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
+  };
+  int issued = min(tiles, 2), mmas = 0;
+  if (tid == 0)
+    for (int j = 0; j < issued; ++j) fetch(j);
+  grid_dependency_wait();  // dS and dz
+  const float* from = p.c.dS + ((size_t)g.seq * p.c.Hk + h) * (D * D + D);
+  load_matrix<D>(sm + M::kS, sm + M::kSLo, from);
+  if (tid < D) z[tid] = from[D * D + tid];
+  fence_proxy_async_smem();
+  __syncthreads();
+  const int row = (warp & 3) * 32 + lane, cg = warp >> 2;
+  const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
+  const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo);
+  __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dk.p)) + cross_base(p.c.ks, p.c.dk, g.seq, h) +
+                      (long long)g.row0 * p.c.dk.sn;
+  __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dv.p)) + cross_base(p.c.ks, p.c.dv, g.seq, h) +
+                      (long long)g.row0 * p.c.dv.sn;
+  bool ok = true;
+  for (int j = 0; j < tiles; ++j) {
+    uint8_t *kt = sm + M::kK + (j & 1) * X::kTile, *vt = sm + M::kV + (j & 1) * X::kTile;
+    const bool live = row < g.len - j * kT;
+    float f[32];
+    ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4* at_k = piece(kt, kT, row, cg * 4 + i);
+        unpack8(*at_k, f + 8 * i);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) f[8 * i + x] = feature<F>(f[8 * i + x]);
+        if (F != MHLA_PHI_IDENTITY) *at_k = pack8(f + 8 * i);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t ka = smem_u32(kt), va = smem_u32(vt);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          mma_bf16(tmem, along_cols<D>(ka, kAtom, s), along_rows(part ? sl : sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1),
+                   s > 0 || part > 0);
+          mma_bf16(tmem + D, along_cols<D>(va, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s),
+                   idesc_bf16_f32(128, D, 0, 0), s > 0 || part > 0);
+        }
+      mma_commit(&b->mma);
+    }
+    ++mmas;
+    ok = __all_sync(0xffffffffu, wait(&b->mma, j & 1, b));
+    if (ok) {
+      tc_fence_after();
+      float v[32];
+      tmem_ld16(at + D, v);
+      tmem_ld16(at + D + 16, v + 16);
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 32; ++x) f[x] = live ? slope<F>(f[x]) * (v[x] + z[cg * 32 + x]) : 0.f;
+      tmem_ld16(at, v);
+      tmem_ld16(at + 16, v + 16);
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 32; ++x) v[x] = live ? v[x] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *piece(kt, kT, row, cg * 4 + i) = pack8(f + 8 * i);
+        *piece(vt, kT, row, cg * 4 + i) = pack8(v + 8 * i);
+      }
+      __syncwarp();
+      const int m = rows - j * kT;
+      store_rows(kt, dk + (long long)j * kT * p.c.dk.sn, p.c.dk.sn, m, (warp & 3) * 32, cg * 32, lane);
+      store_rows(vt, dv + (long long)j * kT * p.c.dv.sn, p.c.dv.sn, m, (warp & 3) * 32, cg * 32, lane);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+    if (j + 2 < tiles) {
+      if (tid == 0) fetch(j + 2);
+      ++issued;
+    }
+  }
+  finish(b, kColumns, issued, mmas, 0);
+}
+
+// ================================================================ host
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// A token tensor as [batch][head][row][d]; a dimension of stride 0 has one entry.  Rows behind the tensor read as zeros.
+bool make_map(CUtensorMap* m, const RetTensor& t, const CrossSide& s, int heads, int d) {
+  auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t row_bytes = t.sn ? (cuuint64_t)t.sn * 2 : (cuuint64_t)d * 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)s.N, t.sh ? (cuuint64_t)heads : 1,
+                              t.sb && s.cu == nullptr ? (cuuint64_t)s.B : 1};
+  const cuuint64_t strides[3] = {row_bytes, t.sh ? (cuuint64_t)t.sh * 2 : row_bytes, t.sb ? (cuuint64_t)t.sb * 2 : row_bytes};
+  const cuuint32_t box[4] = {64, (cuuint32_t)kT, 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+unsigned long long g_wait_ns = kWaitNs;
+
+// The launch's arguments, with the maps of the tile's one or two tensors.
+bool make_args(TcArgs* t, const CrossArgs& a, const CrossSide& s, int heads, const RetTensor& x, const RetTensor* y) {
+  t->c = a;
+  t->wait_ns = g_wait_ns;
+  t->a_h = x.sh != 0;
+  t->a_b = x.sb != 0 && s.cu == nullptr;
+  t->b_h = y != nullptr && y->sh != 0;
+  t->b_b = y != nullptr && y->sb != 0 && s.cu == nullptr;
+  return make_map(&t->a, x, s, heads, a.d) && (y == nullptr || make_map(&t->b, *y, s, heads, a.d));
+}
+
+cudaError_t launch(void (*kernel)(TcArgs), SmemOptIn& opt, long long blocks, int threads, int smem, bool dependent, const TcArgs& t,
+                   cudaStream_t st) {
+  const cudaError_t e = opt.ensure((const void*)kernel, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kernel, dim3((unsigned)blocks), (unsigned)threads, (size_t)smem, st, dependent, t);
+}
+
+template <int D, int F>
+cudaError_t states_t(const CrossArgs& a, cudaStream_t st) {
+  TcArgs t;
+  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v)) return cudaErrorInvalidValue;
+  static SmemOptIn opt;
+  return launch(tc_cross_states_kernel<D, F>, opt, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, SumSmem<D>::kBytes, false, t, st);
+}
+template <int D, int F>
+cudaError_t read_t(const CrossArgs& a, cudaStream_t st) {
+  TcArgs t;
+  if (!make_args(&t, a, a.qs, a.H, a.q, nullptr)) return cudaErrorInvalidValue;
+  static SmemOptIn opt;
+  return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, ReadSmem<D>::kBytes, false, t, st);
+}
+template <int D, int F>
+cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
+  TcArgs t;
+  static SmemOptIn opt_q, opt_k;
+  cudaError_t e = cudaSuccess;
+  if (a.qs.segs > 0) {
+    if (!make_args(&t, a, a.qs, a.H, a.q, &a.dy)) return cudaErrorInvalidValue;
+    e = launch(tc_cross_query_kernel<D, F>, opt_q, (long long)a.qs.segs * a.H, Tc<D>::kThreads, QuerySmem<D>::kBytes, false, t, st);
+  }
+  if (e != cudaSuccess || a.ks.segs == 0) return e;
+  e = cross_join_launch(a, true, a.qs.segs > 0, st);
+  if (e != cudaSuccess) return e;
+  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v)) return cudaErrorInvalidValue;
+  return launch(tc_cross_key_kernel<D, F>, opt_k, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, KeySmem<D>::kBytes, true, t, st);
+}
+
+#define CROSS_FEATURES(fn, D)                                                   \
+  switch (f) {                                                                  \
+    case MHLA_PHI_ELU1: return fn<D, MHLA_PHI_ELU1>(a, st);                     \
+    case MHLA_PHI_RELU: return fn<D, MHLA_PHI_RELU>(a, st);                     \
+    case MHLA_PHI_EXP: return fn<D, MHLA_PHI_EXP>(a, st);                       \
+    default: return fn<D, MHLA_PHI_IDENTITY>(a, st);                            \
+  }
+#define CROSS_WIDTHS(fn)          \
+  if (a.d == 64) {                \
+    CROSS_FEATURES(fn, 64)        \
+  }                               \
+  CROSS_FEATURES(fn, 128)
+
+}  // namespace
+
+void tc_cross_set_wait_limit(unsigned long long ns) { g_wait_ns = ns == 0 ? kWaitNs : ns; }
+bool tc_cross_supported(int d, mhla_dtype dt) { return dt == MHLA_BF16 && (d == 64 || d == 128); }
+cudaError_t tc_cross_states_launch(const CrossArgs& a, cudaStream_t st) {
+  const int f = a.k.feature;
+  CROSS_WIDTHS(states_t)
+}
+cudaError_t tc_cross_read_launch(const CrossArgs& a, cudaStream_t st) {
+  const int f = a.q.feature;
+  CROSS_WIDTHS(read_t)
+}
+cudaError_t tc_cross_backward_launch(const CrossArgs& a, cudaStream_t st) {
+  const int f = a.q.feature;
+  CROSS_WIDTHS(backward_t)
+}
+
+}  // namespace mhla
