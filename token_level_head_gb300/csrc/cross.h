@@ -9,7 +9,7 @@
 
 namespace mhla {
 
-// One side's tokens, queries or keys, as sequences cut into segments of L tokens (a multiple of 128).
+// One side's tokens, queries or keys, as sequences cut into segments of L tokens.
 struct CrossSide {
   int B, N, T;       // B sequences; dense: of N tokens each; packed: of T tokens in all (N = T)
   const int* cu;     // packed: [B + 1] offsets; dense: null

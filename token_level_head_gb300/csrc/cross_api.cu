@@ -12,22 +12,32 @@
 namespace mhla {
 namespace {
 
-// The length of a segment: so many tokens that the blocks (a segment of a head each) fill the SMs twice.
-int segment_length(const CrossSide& s, int heads) {
-  const long long slots = 2 * kRetSms, most = 1ll << 23;
+// The kernels that a call runs on, as far as the segments go: a segment's tokens are a multiple of `unit`, and `slots`
+// blocks (a segment of a head each) fill the SMs.
+struct Kind {
+  int unit, slots;
+};
+Kind kind_of(int d, bool tc) { return tc ? Kind{128, 2 * kRetSms} : Kind{64, (d == 128 ? 2 : 4) * kRetSms}; }
+
+// Reads (three blocks an SM on the tensor cores with d = 64) leave no parts, so their segments need no room.
+Kind read_kind(int d, bool tc) { return tc && d == 64 ? Kind{128, 3 * kRetSms} : kind_of(d, tc); }
+
+// The length of a segment: so many tokens that the blocks fill the SMs, and no fewer than a tile.
+int segment_length(const CrossSide& s, int heads, const Kind& k) {
+  const long long most = 1ll << 23;
   long long L;
   if (s.cu != nullptr) {
-    L = ((long long)s.T * heads + slots - 1) / slots;
+    L = ((long long)s.T * heads + k.slots - 1) / k.slots;
   } else {
-    const long long pieces = std::max(1ll, slots / std::max(1ll, (long long)s.B * heads));
+    const long long pieces = std::max(1ll, k.slots / std::max(1ll, (long long)s.B * heads));
     L = (s.N + pieces - 1) / pieces;
   }
-  return (int)std::max(128ll, std::min((L + 127) / 128 * 128, most));
+  return (int)std::max((long long)k.unit, std::min((L + k.unit - 1) / k.unit * k.unit, most));
 }
 // Cuts a side; false where the segments cannot be numbered.
-bool cut_side(CrossSide* s, int B, int N, const int* cu, const int* lens, int heads) {
+bool cut_side(CrossSide* s, int B, int N, const int* cu, const int* lens, int heads, const Kind& k) {
   *s = {B, N, cu ? N : 0, cu, lens, 0, 0};
-  s->L = segment_length(*s, heads);
+  s->L = segment_length(*s, heads, k);
   const long long segs = cu ? (long long)N / s->L + B : (long long)B * ret_pieces(N, s->L);
   s->segs = (int)std::min(segs, 0x7fffffffll);
   return segs * std::max(heads, 1) <= 0x7fffffffll;
@@ -83,14 +93,16 @@ size_t linattn_cross_workspace_bytes(int B, int H, int Hk, int tokens_q, int tok
   if (B == 0 || Hk == 0) return kWorkspacePrefix;
   Wide n = 0;
   static const int some = 0;  // (packed: an address that is not looked at)
-  for (bool packed : {false, true}) {
+  for (int i = 0; i < 4; ++i) {
+    const bool packed = i % 2 != 0;
+    const Kind kind = kind_of(d, i / 2 != 0);
     CrossSide s;
     if (packed || tokens_k % B == 0) {
-      if (!cut_side(&s, B, packed ? tokens_k : tokens_k / B, packed ? &some : nullptr, nullptr, Hk)) continue;
+      if (!cut_side(&s, B, packed ? tokens_k : tokens_k / B, packed ? &some : nullptr, nullptr, Hk, kind)) continue;
       n = std::max(n, part_floats(s, Hk, d));
     }
     if (backward && (packed || tokens_q % B == 0)) {
-      if (!cut_side(&s, B, packed ? tokens_q : tokens_q / B, packed ? &some : nullptr, nullptr, H)) continue;
+      if (!cut_side(&s, B, packed ? tokens_q : tokens_q / B, packed ? &some : nullptr, nullptr, H, kind)) continue;
       n = std::max(n, part_floats(s, H, d) + (Wide)B * Hk * entry(d));
     }
   }
@@ -108,7 +120,7 @@ mhla_status linattn_cross_states(const void* k, const mhla_strides* k_strides, c
   CrossArgs a{};
   Sums sb;
   if (!check_sums(&sb, S, z, n_slots, Hk, d) || !aligned(slots, 4)) return MHLA_ERR_INVALID_ARG;
-  if (!cut_side(&a.ks, B, N, cu_seqlens, lens, Hk) || (long long)B * Hk * (entry(d) / 256 + 1) > 0x7fffffffll)
+  if (!cut_side(&a.ks, B, N, cu_seqlens, lens, Hk, kind_of(d, tc_cross_supported(d, dt))) || (long long)B * Hk * (entry(d) / 128 + 1) > 0x7fffffffll)
     return MHLA_ERR_UNSUPPORTED;
   const size_t part = cross_joined(a.ks) ? (size_t)part_floats(a.ks, Hk, d) * 4 : 0;
   if (!workspace || !aligned(workspace, 256) || !fits(part_floats(a.ks, Hk, d) * 4) || workspace_bytes < kWorkspacePrefix + part)
@@ -151,7 +163,7 @@ mhla_status linattn_cross_read(const void* q, const mhla_strides* q_strides, con
   CrossArgs a{};
   Sums sb;
   if (!check_sums(&sb, S, z, n_slots, Hk, d) || !aligned(slots, 4)) return MHLA_ERR_INVALID_ARG;
-  if (!cut_side(&a.qs, B, N, cu_seqlens, nullptr, H)) return MHLA_ERR_UNSUPPORTED;
+  if (!cut_side(&a.qs, B, N, cu_seqlens, nullptr, H, read_kind(d, tc_cross_supported(d, dt)))) return MHLA_ERR_UNSUPPORTED;
   const bool step = N == 1 && cu_seqlens == nullptr;
   if (!(step && workspace == nullptr) && (!workspace || !aligned(workspace, 256) || workspace_bytes < kWorkspacePrefix)) return MHLA_ERR_INVALID_ARG;
   const Extent e{cu_seqlens ? 1 : B, H, N, d, dt == MHLA_F32 ? 4 : 2};
@@ -197,8 +209,9 @@ mhla_status linattn_cross_backward(const void* q, const mhla_strides* q_strides,
   CrossArgs a{};
   Sums sb;
   if (!check_sums(&sb, S, z, B, Hk, d)) return MHLA_ERR_INVALID_ARG;
-  if (!cut_side(&a.qs, B, Nq, cu_seqlens_q, nullptr, H) || !cut_side(&a.ks, B, Nk, cu_seqlens_k, lens, Hk) ||
-      (long long)B * Hk * (entry(d) / 256 + 1) > 0x7fffffffll)
+  const Kind kind = kind_of(d, tc_cross_supported(d, dt));
+  if (!cut_side(&a.qs, B, Nq, cu_seqlens_q, nullptr, H, kind) || !cut_side(&a.ks, B, Nk, cu_seqlens_k, lens, Hk, kind) ||
+      (long long)B * Hk * (entry(d) / 128 + 1) > 0x7fffffffll)
     return MHLA_ERR_UNSUPPORTED;
   const Wide parts = part_floats(a.qs, H, d), need = (parts + (Wide)B * Hk * entry(d)) * 4;
   if (!workspace || !aligned(workspace, 256) || !fits(need) || workspace_bytes < kWorkspacePrefix + (size_t)need)

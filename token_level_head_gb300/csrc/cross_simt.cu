@@ -55,6 +55,7 @@ template <int D>
 __device__ __forceinline__ void outer_sum(float (&acc)[Simt<D>::CN][Simt<D>::CN], const float* a, const float* b, int rows,
                                           int ty, int tx) {
   using S = Simt<D>;
+#pragma unroll 4
   for (int t = 0; t < rows; ++t) {
     float x[S::CN], w[S::CN];
 #pragma unroll
@@ -69,36 +70,59 @@ __device__ __forceinline__ void outer_sum(float (&acc)[Simt<D>::CN][Simt<D>::CN]
   }
 }
 
-// Rows row0 .. row0 + n - 1 of a tensor to shared memory (zeros up to `rows`), phi applied (feature) and, if raw is given,
-// as they are.
-template <typename T, int D>
-__device__ __forceinline__ void load_rows(float* to, const T* from, long long sn, int n, int rows, int feature,
-                                          float* raw = nullptr) {
-  constexpr int V = 16 / sizeof(T), PIECES = D / V;
-  for (int i = threadIdx.x; i < rows * PIECES; i += kThreads) {
-    const int r = i / PIECES, c = i % PIECES * V;
-    float* dst = to + r * Simt<D>::LD + c;
-    if (r < n) {
-      const uint4 u = *reinterpret_cast<const uint4*>(from + (long long)r * sn + c);
-      const T* e = reinterpret_cast<const T*>(&u);
+// n of ROWS rows of a tensor to shared memory (zeros behind them), phi applied (feature) and, if raw is given, as they are.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void load_rows(float* to, const T* from, long long sn, int n, int feature, float* raw = nullptr) {
+  constexpr int V = 16 / sizeof(T), PIECES = D / V, N = (ROWS * PIECES + kThreads - 1) / kThreads;
+  uint4 u[N];
 #pragma unroll
-      for (int x = 0; x < V; ++x) {
-        const float f = to_f(e[x]);
-        dst[x] = ret_phi(f, feature);
-        if (raw) raw[r * Simt<D>::LD + c + x] = f;
-      }
-    } else {
+  for (int i = 0; i < N; ++i) {  // (all loads in flight)
+    const int at = threadIdx.x + i * kThreads, r = at / PIECES, c = at % PIECES * V;
+    u[i] = r < n ? *reinterpret_cast<const uint4*>(from + (long long)r * sn + c) : make_uint4(0, 0, 0, 0);
+  }
 #pragma unroll
-      for (int x = 0; x < V; ++x) dst[x] = 0.f;
-    }
+  for (int i = 0; i < N; ++i) {
+    const int at = threadIdx.x + i * kThreads, r = at / PIECES, c = at % PIECES * V;
+    if (r >= ROWS) continue;
+    const T* e = reinterpret_cast<const T*>(&u[i]);
+    float f[V];
+#pragma unroll
+    for (int x = 0; x < V; ++x) f[x] = to_f(e[x]);
+    if (raw)
+#pragma unroll
+      for (int x = 0; x < V; x += 4)
+        *reinterpret_cast<float4*>(raw + r * Simt<D>::LD + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+#pragma unroll
+    for (int x = 0; x < V; ++x) f[x] = r < n ? ret_phi(f[x], feature) : 0.f;
+#pragma unroll
+    for (int x = 0; x < V; x += 4)
+      *reinterpret_cast<float4*>(to + r * Simt<D>::LD + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
   }
 }
-// A d x d fp32 matrix to shared memory, transposed or not.
-template <int D, bool TRANSPOSED>
-__device__ __forceinline__ void load_matrix(float* to, const float* from) {
-  for (int i = threadIdx.x; i < D * D; i += kThreads) {
-    const int r = i / D, c = i % D;
-    to[TRANSPOSED ? c * Simt<D>::LD + r : r * Simt<D>::LD + c] = from[i];
+// A d x d fp32 matrix to shared memory, as it is and transposed (either may be null).
+template <int D>
+__device__ __forceinline__ void load_matrix(float* to, float* turned, const float* from) {
+  constexpr int N = (D * D / 4 + kThreads - 1) / kThreads, BATCH = N < 4 ? N : 4;
+#pragma unroll 1
+  for (int b = 0; b < N; b += BATCH) {
+    float4 v[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int at = (threadIdx.x + (b + i) * kThreads) * 4;
+      if (at < D * D) v[i] = *reinterpret_cast<const float4*>(from + at);
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int at = (threadIdx.x + (b + i) * kThreads) * 4, r = at / D, c = at % D;
+      if (at >= D * D) continue;
+      if (to) *reinterpret_cast<float4*>(to + r * Simt<D>::LD + c) = v[i];
+      if (turned) {
+        turned[c * Simt<D>::LD + r] = v[i].x;
+        turned[(c + 1) * Simt<D>::LD + r] = v[i].y;
+        turned[(c + 2) * Simt<D>::LD + r] = v[i].z;
+        turned[(c + 3) * Simt<D>::LD + r] = v[i].w;
+      }
+    }
   }
 }
 template <int D, typename T>
@@ -124,8 +148,8 @@ __global__ void __launch_bounds__(kThreads) cross_states_kernel(const __grid_con
   for (int t = 0; t < g.len; t += kSumRows) {
     const int n = min(kSumRows, g.len - t);
     __syncthreads();
-    load_rows<T, D>(fk, kp + (long long)t * p.k.sn, p.k.sn, n, n, p.k.feature);
-    load_rows<T, D>(v, vp + (long long)t * p.v.sn, p.v.sn, n, n, kFeatIdentity);
+    load_rows<T, D, kSumRows>(fk, kp + (long long)t * p.k.sn, p.k.sn, n, p.k.feature);
+    load_rows<T, D, kSumRows>(v, vp + (long long)t * p.v.sn, p.v.sn, n, kFeatIdentity);
     __syncthreads();
     outer_sum<D>(acc, fk, v, n, ty, tx);
     if (tid < D)
@@ -146,12 +170,16 @@ __global__ void __launch_bounds__(kThreads) cross_states_kernel(const __grid_con
   if (tid < D) zo[tid] = zs;
 }
 
-// ---- sums over segments: element x of head h of a sequence a thread
-constexpr int kJoinThreads = 256;
+// ---- sums over segments: a block has 32 runs of four elements of a sequence's key head, and eight threads share a run's
+// parts, so that few sums of many segments (one long sequence) are read by enough threads at once (4 heads of 74 segments,
+// d = 128: 44 us with a thread an element).  The order is fixed: a thread's parts, then the eight.
+constexpr int kJoinRuns = 32, kJoinShare = 8, kJoinThreads = kJoinRuns * kJoinShare;
 __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_constant__ CrossArgs p, int backward) {
+  __shared__ float4 sums[kJoinShare][kJoinRuns];
   const CrossSide& s = backward ? p.qs : p.ks;
-  const int E = p.d * p.d + p.d, per = (E + kJoinThreads - 1) / kJoinThreads;
-  const int x = (int)(blockIdx.x % per) * kJoinThreads + threadIdx.x;
+  const int E = p.d * p.d + p.d, per = (E / 4 + kJoinRuns - 1) / kJoinRuns;
+  const int run = threadIdx.x % kJoinRuns, share = threadIdx.x / kJoinRuns;
+  const int x = ((int)(blockIdx.x % per) * kJoinRuns + run) * 4;
   const long long u = blockIdx.x / per;
   const int h = (int)(u % p.Hk), seq = (int)(u / p.Hk);
   int lo, hi;
@@ -159,17 +187,36 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_c
   const int first = cross_first(s, seq, lo), n = s.cu != nullptr ? ret_pieces(hi - lo, s.L) : ret_pieces(s.N, s.L);
   const int slot = backward ? seq : ret_slot(p.slots, p.n_slots, seq);
   grid_dependency_wait();
-  if (x >= E || slot < 0 || (!backward && n == 1)) return;
+  if (slot < 0 || (!backward && n == 1)) return;  // (the whole block)
   const int G = backward ? p.H / p.Hk : 1, heads = backward ? p.H : p.Hk;
-  float sum = 0.f;
-  for (int i = 0; i < n; ++i)
-    for (int m = 0; m < G; ++m) sum += p.part[((size_t)(first + i) * heads + h * G + m) * E + x];
-  if (backward)
-    p.dS[((size_t)seq * p.Hk + h) * E + x] = sum;
-  else if (x < p.d * p.d)
-    p.S[((size_t)slot * p.Hk + h) * p.d * p.d + x] = sum;
-  else
-    p.z[((size_t)slot * p.Hk + h) * p.d + x - p.d * p.d] = sum;
+  const float* part = p.part + ((size_t)first * heads + (size_t)h * G) * E + x;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int all = n * G;
+  if (x < E) {
+#pragma unroll 4
+    for (int i = share; i < all; i += kJoinShare) {
+      const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)(i / G) * heads + i % G) * E);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+  }
+  sums[share][run] = sum;
+  __syncthreads();
+  if (share != 0 || x >= E) return;
+#pragma unroll
+  for (int i = 1; i < kJoinShare; ++i) {
+    const float4 v = sums[i][run];
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  float* to = backward          ? p.dS + ((size_t)seq * p.Hk + h) * E + x
+              : x < p.d * p.d ? p.S + ((size_t)slot * p.Hk + h) * p.d * p.d + x
+                              : p.z + ((size_t)slot * p.Hk + h) * p.d + x - p.d * p.d;
+  *reinterpret_cast<float4*>(to) = sum;
 }
 
 // ---- read: a block reads the sums by a segment of a query head
@@ -188,14 +235,14 @@ __global__ void __launch_bounds__(kThreads) cross_read_kernel(const __grid_const
   const int slot = p.slots != nullptr ? p.slots[g.seq] : g.seq;
   if (slot < 0 || slot >= p.n_slots) return;
   const size_t unit = (size_t)slot * p.Hk + h / (p.H / p.Hk);
-  load_matrix<D, false>(mat, p.S + unit * D * D);
+  load_matrix<D>(mat, nullptr, p.S + unit * D * D);
   if (tid < D) z[tid] = p.z[unit * D + tid];
   const T* qp = static_cast<const T*>(p.q.p) + cross_base(p.qs, p.q, g.seq, h) + (long long)g.row0 * p.q.sn;
   T* yp = static_cast<T*>(const_cast<void*>(p.y.p)) + cross_base(p.qs, p.y, g.seq, h) + (long long)g.row0 * p.y.sn;
   for (int t = 0; t < g.len; t += kReadRows) {
     const int n = min(kReadRows, g.len - t);
     __syncthreads();
-    load_rows<T, D>(fq, qp + (long long)t * p.q.sn, p.q.sn, n, kReadRows, p.q.feature);
+    load_rows<T, D, kReadRows>(fq, qp + (long long)t * p.q.sn, p.q.sn, n, p.q.feature);
     __syncthreads();
     if (p.normalise) {  // four threads a row
       const int r = tid / 4;
@@ -234,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) cross_backward_query_kernel(const __
   const CrossSegment g = cross_segment(p.qs, k, &scratch);
   if (g.seq < 0) return;
   const size_t unit = (size_t)g.seq * p.Hk + h / (p.H / p.Hk);
-  load_matrix<D, true>(mat, p.S + unit * D * D);
+  load_matrix<D>(nullptr, mat, p.S + unit * D * D);
   if (tid < D) z[tid] = p.z[unit * D + tid];
   const T* qp = static_cast<const T*>(p.q.p) + cross_base(p.qs, p.q, g.seq, h) + (long long)g.row0 * p.q.sn;
   const T* dyp = static_cast<const T*>(p.dy.p) + cross_base(p.qs, p.dy, g.seq, h) + (long long)g.row0 * p.dy.sn;
@@ -243,8 +290,8 @@ __global__ void __launch_bounds__(kThreads) cross_backward_query_kernel(const __
   for (int t = 0; t < g.len; t += kBackRows) {
     const int n = min(kBackRows, g.len - t);
     __syncthreads();
-    load_rows<T, D>(fq, qp + (long long)t * p.q.sn, p.q.sn, n, kBackRows, p.q.feature, q);
-    load_rows<T, D>(dy, dyp + (long long)t * p.dy.sn, p.dy.sn, n, kBackRows, kFeatIdentity);
+    load_rows<T, D, kBackRows>(fq, qp + (long long)t * p.q.sn, p.q.sn, n, p.q.feature, q);
+    load_rows<T, D, kBackRows>(dy, dyp + (long long)t * p.dy.sn, p.dy.sn, n, kFeatIdentity);
     __syncthreads();
     float ur[RN][S::CN] = {};
     rows_times<D, RN>(ur, dy, mat, ty, tx);  // u[t][c] = sum_e dy[t][e] S[c][e]
@@ -315,14 +362,13 @@ __global__ void __launch_bounds__(kThreads) cross_backward_key_kernel(const __gr
   T* dvp = static_cast<T*>(const_cast<void*>(p.dv.p)) + cross_base(p.ks, p.dv, g.seq, h) + (long long)g.row0 * p.dv.sn;
   const int rows = p.ks.cu != nullptr ? g.len : min(p.ks.L, p.ks.N - g.row0);
   const float* from = p.dS + ((size_t)g.seq * p.Hk + h) * E;
-  load_matrix<D, false>(mat, from);
-  load_matrix<D, true>(mat_t, from);
+  load_matrix<D>(mat, mat_t, from);
   if (tid < D) dz[tid] = from[D * D + tid];
   for (int t = 0; t < rows; t += kBackRows) {
     const int n = min(kBackRows, max(g.len - t, 0)), m = min(kBackRows, rows - t);
     __syncthreads();
-    load_rows<T, D>(fk, kp + (long long)t * p.k.sn, p.k.sn, n, kBackRows, p.k.feature, kr);
-    load_rows<T, D>(v, vp + (long long)t * p.v.sn, p.v.sn, n, kBackRows, kFeatIdentity);
+    load_rows<T, D, kBackRows>(fk, kp + (long long)t * p.k.sn, p.k.sn, n, p.k.feature, kr);
+    load_rows<T, D, kBackRows>(v, vp + (long long)t * p.v.sn, p.v.sn, n, kFeatIdentity);
     __syncthreads();
     float gv[RN][S::CN] = {}, gk[RN][S::CN] = {};
     rows_times<D, RN>(gv, fk, mat, ty, tx);
@@ -462,7 +508,7 @@ cudaError_t step_t(const CrossArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t cross_join_launch(const CrossArgs& a, bool backward, bool dependent, cudaStream_t st) {
-  const int per = (a.d * a.d + a.d + kJoinThreads - 1) / kJoinThreads;
+  const int per = ((a.d * a.d + a.d) / 4 + kJoinRuns - 1) / kJoinRuns;
   const int B = backward ? a.qs.B : a.ks.B;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -41,9 +41,8 @@ struct Tc {
 };
 
 struct Bars {
-  uint64_t full[2];  // a tile's tensors landed (tx)
-  uint64_t mma;      // MMA commits
-  uint64_t mma2;
+  uint64_t full[3];  // a tile's tensors landed (tx), by its buffer
+  uint64_t mma[2];   // MMA commits
   unsigned long long wait_ns;
   unsigned* status;
   uint32_t tbase;
@@ -59,12 +58,18 @@ struct TcArgs {
 };
 
 __device__ __forceinline__ bool aborted(const int* ab) { return *reinterpret_cast<const volatile int*>(ab) != 0; }
+// (The global timer takes long to read, so the first tries, up to about 16 us, go without it; a diagnostic's short limit
+// counts from the start.)
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Bars* b) {
+  const unsigned long long limit = b->wait_ns;
+  if (limit > 1000000ull)
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait_ns(bar, parity, 1000)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     if (mbar_try_wait_ns(bar, parity, 256)) return true;
     if (aborted(&b->abort)) return false;
-    if (globaltimer_ns() - t0 > b->wait_ns) break;
+    if (globaltimer_ns() - t0 > limit) break;
   }
   *reinterpret_cast<volatile int*>(&b->abort) = 1;
   return false;
@@ -83,52 +88,83 @@ __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ uint4* piece(uint8_t* tile, int rows, int r, int j) {
   return reinterpret_cast<uint4*>(tile + (j >> 3) * (rows * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ void unpack8(uint4 u, float* f) {
+// Eight columns as pairs.
+__device__ __forceinline__ void unpack8(uint4 u, float2* f) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    f[2 * m] = __uint_as_float(w[m] << 16);
-    f[2 * m + 1] = __uint_as_float(w[m] & 0xffff0000u);
-  }
+  for (int m = 0; m < 4; ++m) f[m] = make_float2(__uint_as_float(w[m] << 16), __uint_as_float(w[m] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const float2* v) {
+  return make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
 }
 // f - bf16(f) in place, given bf16(f) packed.
-__device__ __forceinline__ void remainder8(float* f, uint4 h) {
-  float g[8];
+__device__ __forceinline__ void remainder8(float2* f, uint4 h) {
+  float2 g[4];
   unpack8(h, g);
 #pragma unroll
-  for (int x = 0; x < 8; ++x) f[x] -= g[x];
+  for (int x = 0; x < 4; ++x) f[x] = sub2(f[x], g[x]);
+}
+// 16 columns of the thread's lane of tensor memory.
+__device__ __forceinline__ void tmem_ld8(uint32_t at, float2* v) { tmem_ld16(at, reinterpret_cast<float*>(v)); }
+// Eight fp32 values of shared memory.
+__device__ __forceinline__ void load8(const float* p, float2* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(v + 2 * i) = *reinterpret_cast<const float4*>(p + 4 * i);
 }
 
 // phi and, from phi alone, phi'.
+__device__ __forceinline__ float exp2_of(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
+}
+// cross_inverse by the hardware's reciprocal (within a step of 2^-23).
+__device__ __forceinline__ float inverse(float den) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den));
+  return den == 0.f ? 0.f : r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {  // not-a-number stays
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 template <int F>
-__device__ __forceinline__ float feature(float x) {
-  if (F == MHLA_PHI_ELU1) {  // as phi_f, but not-a-number stays
-    float m, e;
-    asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(m) : "f"(x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m * 1.4426950408889634f));
-    return e + fmaxf(x, 0.f);
-  }
-  if (F == MHLA_PHI_RELU) return x > 0.f ? x : (x == x ? 0.f : x);  // (not-a-number stays)
-  if (F == MHLA_PHI_EXP) return __expf(x);
+__device__ __forceinline__ float2 feature(float2 x) {
+  if (F == MHLA_PHI_ELU1)  // exp(min(x, 0)) + max(x, 0)
+    return add2(make_float2(exp2_of(min_nan(x.x, 0.f) * kLog2e), exp2_of(min_nan(x.y, 0.f) * kLog2e)),
+                make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+  if (F == MHLA_PHI_RELU) return make_float2(x.x != x.x ? x.x : fmaxf(x.x, 0.f), x.y != x.y ? x.y : fmaxf(x.y, 0.f));
+  if (F == MHLA_PHI_EXP) return make_float2(exp2_of(x.x * kLog2e), exp2_of(x.y * kLog2e));
   return x;
 }
 template <int F>
-__device__ __forceinline__ float slope(float phi) {
-  if (F == MHLA_PHI_ELU1) return phi < 1.f ? phi : (phi == phi ? 1.f : phi);
-  if (F == MHLA_PHI_RELU) return phi > 0.f ? 1.f : 0.f;
-  if (F == MHLA_PHI_EXP) return phi;
-  return 1.f;
+__device__ __forceinline__ float2 slope(float2 phi) {
+  if (F == MHLA_PHI_ELU1) return make_float2(min_nan(phi.x, 1.f), min_nan(phi.y, 1.f));
+  if (F == MHLA_PHI_RELU) return make_float2(phi.x > 0.f ? 1.f : 0.f, phi.y > 0.f ? 1.f : 0.f);
+  return F == MHLA_PHI_EXP ? phi : both(1.f);
 }
 
 __device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
   if (threadIdx.x == 0) {
-    mbar_init(&b->full[0], 1);
-    mbar_init(&b->full[1], 1);
-    mbar_init(&b->mma, 1);
-    mbar_init(&b->mma2, 1);
+    for (uint64_t& f : b->full) mbar_init(&f, 1);
+    for (uint64_t& m : b->mma) mbar_init(&m, 1);
     b->abort = 0;
     b->wait_ns = p.wait_ns;
     b->status = p.c.status;
@@ -143,15 +179,16 @@ __device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
   tc_fence_after();
 }
 // The end of a block: after an abort (one thread) short waits for the copies and MMAs in flight; then the columns are
-// freed.  issued: tiles whose copies were issued; mmas, mmas2: commits.
+// freed.  issued: tiles whose copies were issued, into NB buffers in turn; mmas, mmas2: commits on the two barriers.
+template <int NB>
 __device__ __forceinline__ void finish(Bars* b, uint32_t cols, int issued, int mmas, int mmas2) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0 && aborted(&b->abort)) {
-    for (int j = max(issued - 2, 0); j < issued; ++j) drain(&b->full[j & 1], (j >> 1) & 1);
-    if (mmas > 0) drain(&b->mma, (mmas - 1) & 1);
-    if (mmas2 > 0) drain(&b->mma2, (mmas2 - 1) & 1);
+    for (int j = max(issued - NB, 0); j < issued; ++j) drain(&b->full[j % NB], (j / NB) & 1);
+    if (mmas > 0) drain(&b->mma[0], (mmas - 1) & 1);
+    if (mmas2 > 0) drain(&b->mma[1], (mmas2 - 1) & 1);
     atomicOr(b->status, 1u);
   }
   __syncthreads();
@@ -168,11 +205,11 @@ __device__ __forceinline__ void load_tile(uint8_t* to, const CUtensorMap* m, int
 // A d x d fp32 matrix [r][c] as bf16 tiles of D rows, the high part and, where lo is given, the low part.
 template <int D>
 __device__ __forceinline__ void load_matrix(uint8_t* hi, uint8_t* lo, const float* from) {
+#pragma unroll
   for (int i = threadIdx.x; i < D * D / 8; i += Tc<D>::kThreads) {
     const int r = i / (D / 8), j = i % (D / 8);
-    float f[8];
-    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(from + r * D + 8 * j);
-    *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(from + r * D + 8 * j + 4);
+    float2 f[4];
+    load8(from + r * D + 8 * j, f);
     const uint4 u = pack8(f);
     *piece(hi, D, r, j) = u;
     if (lo != nullptr) {
@@ -182,13 +219,34 @@ __device__ __forceinline__ void load_matrix(uint8_t* hi, uint8_t* lo, const floa
   }
 }
 
-// The warp's 32 rows x 32 columns of a tile to memory: eight rows of 64 bytes at a time; n rows of the tile are written.
-__device__ __forceinline__ void store_rows(uint8_t* tile, __nv_bfloat16* out, long long sn, int n, int row0, int col0, int lane) {
+// A thread's places in every tile: its row's four pieces of 32 columns, and what it stores, four times a piece of eight rows
+// of 64 bytes (a warp's 32 rows x 32 columns).
+struct Places {
+  uint32_t own[4], out[4];
+  int row, out_row, out_col;  // out_row: of the first of the four, eight apart
+};
+__device__ __forceinline__ Places places(int warp, int lane) {
+  Places p;
+  p.row = (warp & 3) * 32 + lane;
+  p.out_row = (warp & 3) * 32 + lane / 4;
+  const int j0 = (warp >> 2) * 4;
+  p.out_col = 8 * (j0 + lane % 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = row0 + i * 8 + lane / 4, j = col0 / 8 + lane % 4;
-    const uint4 u = *piece(tile, kT, r, j);
-    if (r < n) *reinterpret_cast<uint4*>(out + r * sn + 8 * j) = u;
+    const int j = j0 + i, o = j0 + lane % 4, r = p.out_row + 8 * i;
+    p.own[i] = (j >> 3) * kAtom + p.row * 128 + (((j & 7) ^ (p.row & 7)) << 4);
+    p.out[i] = (o >> 3) * kAtom + r * 128 + (((o & 7) ^ (r & 7)) << 4);
+  }
+  return p;
+}
+__device__ __forceinline__ uint4& at_byte(uint8_t* tile, uint32_t offset) { return *reinterpret_cast<uint4*>(tile + offset); }
+// The warp's part of a tile to memory; out: the tile's first row and the thread's columns; n rows of the tile are written.
+__device__ __forceinline__ void store_rows(uint8_t* tile, const Places& p, __nv_bfloat16* out, long long sn, int n) {
+  __nv_bfloat16* to = out + p.out_row * sn;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (p.out_row + 8 * i < n) *reinterpret_cast<uint4*>(to) = at_byte(tile, p.out[i]);
+    to += 8 * sn;
   }
 }
 
@@ -237,10 +295,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   }
   constexpr int P = D / 8, ROWS = X::kThreads / P;  // pieces of a row, rows at a time
   const int pc = tid % P, r0 = tid / P;
-  float z[8] = {};
+  float2 z[4] = {};
   bool ok = true;
   for (int j = 0; j < tiles; ++j) {
-    if (j > 0) ok = wait(&b->mma, (j - 1) & 1, b);  // the other buffer, mid and lo have been read
+    if (j > 0) ok = wait(&b->mma[0], (j - 1) & 1, b);  // the other buffer, mid and lo have been read
     if (ok && j + 1 < tiles) {
       if (tid == 0) fetch(j + 1);
       ++issued;
@@ -253,19 +311,17 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       for (int i = 0; i < kT / ROWS; ++i) {
         const int r = r0 + i * ROWS;
         uint4* at = piece(kt, kT, r, pc);
-        float f[8];
+        float2 f[4];
         unpack8(*at, f);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] = feature<F>(f[x]);
         if (r >= n) {  // behind the sequence: nothing of what lies there counts
 #pragma unroll
-          for (int x = 0; x < 8; ++x) f[x] = 0.f;
+          for (int x = 0; x < 4; ++x) f[x] = both(0.f);
           *piece(vt, kT, r, pc) = make_uint4(0, 0, 0, 0);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            f[x] = feature<F>(f[x]);
-            z[x] += f[x];
-          }
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) z[x] = add2(z[x], f[x]);
         const uint4 hi = pack8(f);
         *at = hi;
         if (!kExact) {
@@ -305,7 +361,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
             mma_bf16(tmem, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
         }
       }
-      mma_commit(&b->mma);
+      mma_commit(&b->mma[0]);
     }
     ++mmas;
   }
@@ -320,12 +376,12 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       zo = p.c.z + ((size_t)slot * p.c.Hk + h) * D;
     }
   }
-  if (ok && tiles > 0) ok = wait(&b->mma, (tiles - 1) & 1, b);
+  if (ok && tiles > 0) ok = wait(&b->mma[0], (tiles - 1) & 1, b);
   if (__syncthreads_and(ok)) {
     tc_fence_after();
     float* zp = reinterpret_cast<float*>(sm + M::kMid);  // [ROWS][D]
 #pragma unroll
-    for (int x = 0; x < 8; ++x) zp[r0 * D + 8 * pc + x] = z[x];
+    for (int x = 0; x < 4; ++x) *reinterpret_cast<float2*>(zp + r0 * D + 8 * pc + 2 * x) = z[x];
     __syncthreads();
     if (zo != nullptr) {
       if (tid < D) {
@@ -356,20 +412,22 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       }
     }
   }
-  finish(b, kColumns, issued, mmas, 0);
+  finish<2>(b, kColumns, issued, mmas, 0);
 }
 
 // ================================================================ read
+// Three buffers and two accumulators: while the MMA of a tile runs the warps store the tile before and take the next one's
+// features; one barrier of the block a tile, so what a tile leaves for the next turn lies in one of three places.
 template <int D>
 struct ReadSmem {
-  static constexpr int kQ = 0, kS = 2 * Tc<D>::kTile, kZ = kS + Tc<D>::kMat, kDen = kZ + D * 4, kBars = kDen + Tc<D>::kCols * kT * 4;
+  static constexpr int kQ = 0, kS = 3 * Tc<D>::kTile, kZ = kS + Tc<D>::kMat, kDen = kZ + D * 4, kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
   static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
 };
 template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_read_kernel(const __grid_constant__ TcArgs p) {
   using X = Tc<D>;
   using M = ReadSmem<D>;
-  constexpr uint32_t kColumns = D;
+  constexpr uint32_t kColumns = 2 * D;
   extern __shared__ __align__(16) uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
@@ -384,81 +442,45 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
   const auto fetch = [&](int j) {
-    uint64_t* bar = &b->full[j & 1];
+    uint64_t* bar = &b->full[j % 3];
     mbar_arrive_expect_tx(bar, X::kTile);
-    load_tile<D>(sm + M::kQ + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+    load_tile<D>(sm + M::kQ + j % 3 * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
   };
-  int issued = min(tiles, 2), mmas = 0;
+  int issued = min(tiles, 3), mmas = 0;
   if (tid == 0)
     for (int j = 0; j < issued; ++j) fetch(j);
   const size_t unit = (size_t)slot * p.c.Hk + h / (p.c.H / p.c.Hk);
   load_matrix<D>(sm + M::kS, nullptr, p.c.S + unit * D * D);
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
-  fence_proxy_async_smem();
   __syncthreads();
-  const int row = (warp & 3) * 32 + lane, cg = warp >> 2;  // the thread's row, and its 32 columns
+  const Places pl = places(warp, lane);
+  const int row = pl.row, cg = warp >> 2;  // the thread's row, and its 32 columns
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
   const uint32_t sa = smem_u32(sm + M::kS);
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.y.p)) + cross_base(p.c.qs, p.c.y, g.seq, h) +
-                     (long long)g.row0 * p.c.y.sn;
+                     (long long)g.row0 * p.c.y.sn + pl.out_col;
   bool ok = true;
-  for (int j = 0; j < tiles; ++j) {
-    uint8_t* qt = sm + M::kQ + (j & 1) * X::kTile;
-    ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
-    if (ok) {
-      float d = 0.f;
+  for (int j = 0; j <= tiles; ++j) {
+    if (j < tiles) {  // the features of tile j
+      uint8_t* qt = sm + M::kQ + j % 3 * X::kTile;
+      ok = wait(&b->full[j % 3], (j / 3) & 1, b);
+      if (ok) {
+        float2 d = both(0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4* q = piece(qt, kT, row, cg * 4 + i);
-        float f[8], zz[8];
-        unpack8(*q, f);
-        *reinterpret_cast<float4*>(zz) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i);
-        *reinterpret_cast<float4*>(zz + 4) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i + 4);
+        for (int i = 0; i < 4; ++i) {
+          uint4* q = &at_byte(qt, pl.own[i]);
+          float2 f[4], zz[4];
+          unpack8(*q, f);
+          load8(z + cg * 32 + 8 * i, zz);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          f[x] = feature<F>(f[x]);
-          d = fmaf(f[x], zz[x], d);
+          for (int x = 0; x < 4; ++x) {
+            f[x] = feature<F>(f[x]);
+            d = fma2(f[x], zz[x], d);
+          }
+          if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
         }
-        if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
+        den[(j % 3 * X::kCols + cg) * kT + row] = d.x + d.y;
       }
-      den[cg * kT + row] = d;
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (!__syncthreads_and(ok)) {
-      ok = false;
-      break;
-    }
-    if (tid == 0) {
-      tc_fence_after();
-      const uint32_t qa = smem_u32(qt);
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        mma_bf16(tmem, along_cols<D>(qa, kAtom, s), along_rows(sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1), s > 0);
-      mma_commit(&b->mma);
-    }
-    ++mmas;
-    float inv = 1.f;
-    if (p.c.normalise) {
-      float d = p.c.eps;
-#pragma unroll
-      for (int i = 0; i < X::kCols; ++i) d += den[i * kT + row];
-      inv = cross_inverse(d);
-    }
-    ok = wait(&b->mma, j & 1, b);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      float v[32];
-      tmem_ld16(at, v);
-      tmem_ld16(at + 16, v + 16);
-      tmem_ld_wait();
-#pragma unroll
-      for (int x = 0; x < 32; ++x) v[x] *= inv;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *piece(qt, kT, row, cg * 4 + i) = pack8(v + 8 * i);
-      __syncwarp();
-      store_rows(qt, y + (long long)j * kT * p.c.y.sn, p.c.y.sn, g.len - j * kT, (warp & 3) * 32, cg * 32, lane);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -467,12 +489,48 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
       break;
     }
     tc_fence_after();
-    if (j + 2 < tiles) {
-      if (tid == 0) fetch(j + 2);
+    if (j < tiles) {
+      if (tid == 0) {
+        const uint32_t qa = smem_u32(sm + M::kQ + j % 3 * X::kTile);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          mma_bf16(tmem + (j & 1) * D, along_cols<D>(qa, kAtom, s), along_rows(sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1),
+                   s > 0);
+        mma_commit(&b->mma[j & 1]);
+      }
+      ++mmas;
+    }
+    if (j >= 2 && j + 1 < tiles) {  // tile j - 2 has been stored: its buffer takes tile j + 1
+      if (tid == 0) fetch(j + 1);
       ++issued;
     }
+    if (j > 0) {  // tile j - 1 goes out
+      const int t = j - 1;
+      uint8_t* qt = sm + M::kQ + t % 3 * X::kTile;
+      float inv = 1.f;
+      if (p.c.normalise) {
+        float d = p.c.eps;
+#pragma unroll
+        for (int i = 0; i < X::kCols; ++i) d += den[(t % 3 * X::kCols + i) * kT + row];
+        inv = inverse(d);
+      }
+      ok = __all_sync(0xffffffffu, wait(&b->mma[t & 1], (t >> 1) & 1, b));
+      if (ok) {
+        tc_fence_after();
+        float2 v[16];
+        tmem_ld8(at + (t & 1) * D, v);
+        tmem_ld8(at + (t & 1) * D + 16, v + 8);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], both(inv));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at_byte(qt, pl.own[i]) = pack8(v + 4 * i);
+        __syncwarp();
+        store_rows(qt, pl, y + (long long)t * kT * p.c.y.sn, p.c.y.sn, g.len - t * kT);
+      }
+    }
   }
-  finish(b, kColumns, issued, mmas, 0);
+  finish<3>(b, kColumns, issued, (mmas + 1) / 2, mmas / 2);
 }
 
 // ================================================================ backward over the queries
@@ -485,7 +543,7 @@ struct QuerySmem {
   static constexpr int kBytes = (kSmall + 1023) / 1024 * 1024 + kEnd;
   static_assert(kBytes <= 232448 / (D == 64 ? 2 : 1), "two blocks of d = 64 an SM, one of d = 128");
 };
-// 32 values a lane: lane i ends with the warp's sum of value i.
+// 32 values a lane: the sum of value i over the warp, for lane i.
 __device__ __forceinline__ float sum_turned(float (&v)[32], int lane) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -532,69 +590,74 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
   fence_proxy_async_smem();
   __syncthreads();
-  const int row = (warp & 3) * 32 + lane, cg = warp >> 2;
+  const Places pl = places(warp, lane);
+  const int row = pl.row, cg = warp >> 2;
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
   const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo), wl = smem_u32(sm + M::kLo);
   __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dq.p)) + cross_base(p.c.qs, p.c.dq, g.seq, h) +
-                      (long long)g.row0 * p.c.dq.sn;
-  float dz = 0.f;  // of column cg * 32 + lane, over the warp's rows
+                      (long long)g.row0 * p.c.dq.sn + pl.out_col;
+  float2 dz[16] = {};  // of the thread's 32 columns, over its rows
+  const auto multiply_u = [&](const uint8_t* yt) {  // one thread: u = dy S^T
+    const uint32_t ya = smem_u32(yt);
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+        mma_bf16(tmem, along_cols<D>(ya, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s), idesc_bf16_f32(128, D, 0, 0),
+                 s > 0 || part > 0);
+    mma_commit(&b->mma[0]);
+  };
   bool ok = true;
   for (int j = 0; j < tiles; ++j) {
     uint8_t *qt = sm + M::kQ + (j & 1) * X::kTile, *yt = sm + M::kY + (j & 1) * X::kTile;
     const int n = g.len - j * kT;
-    const bool live = row < n;
-    float f[32];
+    const bool live = row < n, whole = n >= kT;
+    float2 f[16];
     ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
     if (ok) {
-      float d = 0.f;
+      if (whole && tid == 0) multiply_u(yt);
+      float2 d = both(0.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        unpack8(*piece(qt, kT, row, cg * 4 + i), f + 8 * i);
-        if (!live) *piece(yt, kT, row, cg * 4 + i) = make_uint4(0, 0, 0, 0);
-        float zz[8];
-        *reinterpret_cast<float4*>(zz) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i);
-        *reinterpret_cast<float4*>(zz + 4) = *reinterpret_cast<const float4*>(z + cg * 32 + 8 * i + 4);
+        unpack8(at_byte(qt, pl.own[i]), f + 4 * i);
+        if (!live) at_byte(yt, pl.own[i]) = make_uint4(0, 0, 0, 0);
+        float2 zz[4];
+        load8(z + cg * 32 + 8 * i, zz);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          f[8 * i + x] = live ? feature<F>(f[8 * i + x]) : 0.f;
-          d = fmaf(f[8 * i + x], zz[x], d);
+        for (int x = 0; x < 4; ++x) {
+          f[4 * i + x] = feature<F>(f[4 * i + x]);
+          if (!live) f[4 * i + x] = both(0.f);
+          d = fma2(f[4 * i + x], zz[x], d);
         }
       }
-      den[cg * kT + row] = d;
+      den[cg * kT + row] = d.x + d.y;
     }
-    if (!live) fence_proxy_async_smem();
+    if (!whole) fence_proxy_async_smem();
     if (!__syncthreads_and(ok)) {
       ok = false;
       break;
     }
+    if (!whole && tid == 0) {
+      tc_fence_after();
+      multiply_u(yt);
+    }
+    ++mmas;
     float inv = 1.f;
     if (p.c.normalise) {
       float d = p.c.eps;
 #pragma unroll
       for (int i = 0; i < X::kCols; ++i) d += den[i * kT + row];
-      inv = cross_inverse(d);
+      inv = inverse(d);
     }
-    if (tid == 0) {  // u = dy S^T
-      tc_fence_after();
-      const uint32_t ya = smem_u32(yt);
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+    for (int i = 0; i < 4; ++i) {  // w over q's place
+      float2 w[4];
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          mma_bf16(tmem, along_cols<D>(ya, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s), idesc_bf16_f32(128, D, 0, 0),
-                   s > 0 || part > 0);
-      mma_commit(&b->mma);
-    }
-    ++mmas;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // w over phi's place
-      float w[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) w[x] = f[8 * i + x] * inv;
+      for (int x = 0; x < 4; ++x) w[x] = mul2(f[4 * i + x], both(inv));
       const uint4 hi = pack8(w);
-      *piece(qt, kT, row, cg * 4 + i) = hi;
+      at_byte(qt, pl.own[i]) = hi;
       remainder8(w, hi);
-      *piece(sm + M::kLo, kT, row, cg * 4 + i) = pack8(w);
+      at_byte(sm + M::kLo, pl.own[i]) = pack8(w);
     }
     fence_proxy_async_smem();
     __syncthreads();
@@ -609,68 +672,80 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
         for (int s = 0; s < kT / 16; ++s)
           mma_bf16(tmem + D, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
       }
-      mma_commit(&b->mma2);
+      mma_commit(&b->mma[1]);
     }
     ++mmas2;
-    ok = __all_sync(0xffffffffu, wait(&b->mma, j & 1, b));
-    float u[32];
+    ok = __all_sync(0xffffffffu, wait(&b->mma[0], j & 1, b));
     if (ok) {
       tc_fence_after();
-      tmem_ld16(at, u);
-      tmem_ld16(at + 16, u + 16);
-      tmem_ld_wait();
-      float s = 0.f;
+      float2 s2 = both(0.f);
 #pragma unroll
-      for (int x = 0; x < 32; ++x) s = fmaf(f[x], u[x], s);
-      den[cg * kT + row] = s;
+      for (int c = 0; c < 2; ++c) {
+        float2 u[8];
+        tmem_ld8(at + 16 * c, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s2 = fma2(f[8 * c + x], u[x], s2);
+      }
+      den[cg * kT + row] = s2.x + s2.y;
     }
-    tc_fence_before();
     if (!__syncthreads_and(ok)) {
       ok = false;
       break;
     }
-    tc_fence_after();
     float dd = 0.f;
     if (p.c.normalise && live) {
 #pragma unroll
       for (int i = 0; i < X::kCols; ++i) dd += den[i * kT + row];
       dd *= -inv * inv;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float zz[4];
-      *reinterpret_cast<float4*>(zz) = *reinterpret_cast<const float4*>(z + cg * 32 + 4 * i);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        u[4 * i + x] = slope<F>(f[4 * i + x]) * fmaf(u[4 * i + x], inv, dd * zz[x]);
-        f[4 * i + x] *= dd;
-      }
-    }
-    if (p.c.normalise) dz += sum_turned(f, lane);
-    ok = __all_sync(0xffffffffu, wait(&b->mma2, j & 1, b));  // w has been read
+    ok = __all_sync(0xffffffffu, wait(&b->mma[1], j & 1, b));  // w has been read
     if (ok) {
+      tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *piece(qt, kT, row, cg * 4 + i) = pack8(u + 8 * i);
+      for (int c = 0; c < 2; ++c) {
+        float2 u[8];
+        tmem_ld8(at + 16 * c, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float2 zz[4];
+          load8(z + cg * 32 + 16 * c + 8 * i, zz);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int at_f = 8 * c + 4 * i + x;
+            dz[at_f] = fma2(f[at_f], both(dd), dz[at_f]);
+            u[4 * i + x] = mul2(slope<F>(f[at_f]), fma2(u[4 * i + x], both(inv), mul2(zz[x], both(dd))));
+          }
+          at_byte(qt, pl.own[2 * c + i]) = pack8(u + 4 * i);
+        }
+      }
       __syncwarp();
-      store_rows(qt, dq + (long long)j * kT * p.c.dq.sn, p.c.dq.sn, n, (warp & 3) * 32, cg * 32, lane);
+      store_rows(qt, pl, dq + (long long)j * kT * p.c.dq.sn, p.c.dq.sn, n);
     }
     fence_proxy_async_smem();
+    tc_fence_before();
     if (!__syncthreads_and(ok)) {
       ok = false;
       break;
     }
+    tc_fence_after();
     if (j + 2 < tiles) {
       if (tid == 0) fetch(j + 2);
       ++issued;
     }
   }
   if (ok) {
-    tc_fence_after();
     float* out = p.c.part + ((size_t)k * p.c.H + h) * (D * D + D);
-    den[(warp & 3) * D + cg * 32 + lane] = dz;  // (4 D floats are there: kCols * kT)
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[2 * i] = dz[i].x;
+      v[2 * i + 1] = dz[i].y;
+    }
+    den[(warp & 3) * D + cg * 32 + lane] = sum_turned(v, lane);  // (4 D floats are there: kCols * kT)
     const int e = (warp & 3) * 32 + lane, c0 = cg * 32;
     if ((warp & 3) * 32 < D) {
-      float v[32];
       if (tiles > 0) {
         tmem_ld16(at + D, v);
         tmem_ld16(at + D + 16, v + 16);
@@ -682,7 +757,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
     __syncthreads();
     if (tid < D) out[D * D + tid] = den[tid] + den[D + tid] + den[2 * D + tid] + den[3 * D + tid];
   }
-  finish(b, kColumns, issued, mmas, mmas2);
+  finish<2>(b, kColumns, issued, mmas, mmas2);
 }
 
 // ================================================================ backward over the keys
@@ -724,27 +799,28 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   if (tid < D) z[tid] = from[D * D + tid];
   fence_proxy_async_smem();
   __syncthreads();
-  const int row = (warp & 3) * 32 + lane, cg = warp >> 2;
+  const Places pl = places(warp, lane);
+  const int row = pl.row, cg = warp >> 2;
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
   const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo);
   __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dk.p)) + cross_base(p.c.ks, p.c.dk, g.seq, h) +
-                      (long long)g.row0 * p.c.dk.sn;
+                      (long long)g.row0 * p.c.dk.sn + pl.out_col;
   __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dv.p)) + cross_base(p.c.ks, p.c.dv, g.seq, h) +
-                      (long long)g.row0 * p.c.dv.sn;
+                      (long long)g.row0 * p.c.dv.sn + pl.out_col;
   bool ok = true;
   for (int j = 0; j < tiles; ++j) {
     uint8_t *kt = sm + M::kK + (j & 1) * X::kTile, *vt = sm + M::kV + (j & 1) * X::kTile;
     const bool live = row < g.len - j * kT;
-    float f[32];
+    float2 f[16];
     ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
     if (ok) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint4* at_k = piece(kt, kT, row, cg * 4 + i);
-        unpack8(*at_k, f + 8 * i);
+        uint4* at_k = &at_byte(kt, pl.own[i]);
+        unpack8(*at_k, f + 4 * i);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) f[8 * i + x] = feature<F>(f[8 * i + x]);
-        if (F != MHLA_PHI_IDENTITY) *at_k = pack8(f + 8 * i);
+        for (int x = 0; x < 4; ++x) f[4 * i + x] = feature<F>(f[4 * i + x]);
+        if (F != MHLA_PHI_IDENTITY) *at_k = pack8(f + 4 * i);
       }
     }
     fence_proxy_async_smem();
@@ -765,32 +841,35 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
           mma_bf16(tmem + D, along_cols<D>(va, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s),
                    idesc_bf16_f32(128, D, 0, 0), s > 0 || part > 0);
         }
-      mma_commit(&b->mma);
+      mma_commit(&b->mma[0]);
     }
     ++mmas;
-    ok = __all_sync(0xffffffffu, wait(&b->mma, j & 1, b));
+    ok = __all_sync(0xffffffffu, wait(&b->mma[0], j & 1, b));
     if (ok) {
       tc_fence_after();
-      float v[32];
-      tmem_ld16(at + D, v);
-      tmem_ld16(at + D + 16, v + 16);
-      tmem_ld_wait();
 #pragma unroll
-      for (int x = 0; x < 32; ++x) f[x] = live ? slope<F>(f[x]) * (v[x] + z[cg * 32 + x]) : 0.f;
-      tmem_ld16(at, v);
-      tmem_ld16(at + 16, v + 16);
-      tmem_ld_wait();
+      for (int c = 0; c < 2; ++c) {
+        float2 u[8], v[8];
+        tmem_ld8(at + D + 16 * c, u);
+        tmem_ld8(at + 16 * c, v);
+        tmem_ld_wait();
 #pragma unroll
-      for (int x = 0; x < 32; ++x) v[x] = live ? v[x] : 0.f;
+        for (int i = 0; i < 2; ++i) {
+          float2 zz[4];
+          load8(z + cg * 32 + 16 * c + 8 * i, zz);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        *piece(kt, kT, row, cg * 4 + i) = pack8(f + 8 * i);
-        *piece(vt, kT, row, cg * 4 + i) = pack8(v + 8 * i);
+          for (int x = 0; x < 4; ++x) {
+            u[4 * i + x] = mul2(slope<F>(f[8 * c + 4 * i + x]), add2(u[4 * i + x], zz[x]));
+            if (!live) u[4 * i + x] = v[4 * i + x] = both(0.f);
+          }
+          at_byte(kt, pl.own[2 * c + i]) = pack8(u + 4 * i);
+          at_byte(vt, pl.own[2 * c + i]) = pack8(v + 4 * i);
+        }
       }
       __syncwarp();
       const int m = rows - j * kT;
-      store_rows(kt, dk + (long long)j * kT * p.c.dk.sn, p.c.dk.sn, m, (warp & 3) * 32, cg * 32, lane);
-      store_rows(vt, dv + (long long)j * kT * p.c.dv.sn, p.c.dv.sn, m, (warp & 3) * 32, cg * 32, lane);
+      store_rows(kt, pl, dk + (long long)j * kT * p.c.dk.sn, p.c.dk.sn, m);
+      store_rows(vt, pl, dv + (long long)j * kT * p.c.dv.sn, p.c.dv.sn, m);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -804,7 +883,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
       ++issued;
     }
   }
-  finish(b, kColumns, issued, mmas, 0);
+  finish<2>(b, kColumns, issued, mmas, 0);
 }
 
 // ================================================================ host
