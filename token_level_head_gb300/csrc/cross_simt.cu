@@ -182,11 +182,12 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_c
   const int x = ((int)(blockIdx.x % per) * kJoinRuns + run) * 4;
   const long long u = blockIdx.x / per;
   const int h = (int)(u % p.Hk), seq = (int)(u / p.Hk);
+  launch_dependents();
+  grid_dependency_wait();
   int lo, hi;
   cross_range(s, seq, &lo, &hi);
   const int first = cross_first(s, seq, lo), n = s.cu != nullptr ? ret_pieces(hi - lo, s.L) : ret_pieces(s.N, s.L);
   const int slot = backward ? seq : ret_slot(p.slots, p.n_slots, seq);
-  grid_dependency_wait();
   if (slot < 0 || (!backward && n == 1)) return;  // (the whole block)
   const int G = backward ? p.H / p.Hk : 1, heads = backward ? p.H : p.Hk;
   const float* part = p.part + ((size_t)first * heads + (size_t)h * G) * E + x;

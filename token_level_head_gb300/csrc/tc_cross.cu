@@ -161,7 +161,10 @@ __device__ __forceinline__ float2 slope(float2 phi) {
   return F == MHLA_PHI_EXP ? phi : both(1.f);
 }
 
+// The start of a block: barriers, tensor memory, the maps; and then everything that the kernel before left.  Every kernel
+// here is launched while the one before it in the stream drains (whichever that is), so nothing is read before.
 __device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
+  launch_dependents();
   if (threadIdx.x == 0) {
     for (uint64_t& f : b->full) mbar_init(&f, 1);
     for (uint64_t& m : b->mma) mbar_init(&m, 1);
@@ -174,9 +177,11 @@ __device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
     tmem_alloc(&b->tbase, cols);
     tmem_relinquish();
   }
+  if (threadIdx.x == 32) prefetch_tmap(&p.a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();
 }
 // The end of a block: after an abort (one thread) short waits for the copies and MMAs in flight; then the columns are
 // freed.  issued: tiles whose copies were issued, into NB buffers in turn; mmas, mmas2: commits on the two barriers.
@@ -276,9 +281,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
-  const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
-  if (g.seq < 0) return;
   setup(p, b, kColumns);
+  const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
+  if (g.seq < 0) return finish<2>(b, kColumns, 0, 0, 0);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT;
   const int hh = h, bb = p.c.ks.cu == nullptr ? g.seq : 0;
@@ -434,11 +439,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   float *z = reinterpret_cast<float*>(sm + M::kZ), *den = reinterpret_cast<float*>(sm + M::kDen);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.c.H, k = blockIdx.x / p.c.H;
-  const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
-  if (g.seq < 0 || g.len == 0) return;
-  const int slot = p.c.slots != nullptr ? p.c.slots[g.seq] : g.seq;
-  if (slot < 0 || slot >= p.c.n_slots) return;
   setup(p, b, kColumns);
+  const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
+  const int slot = g.seq < 0 ? -1 : p.c.slots != nullptr ? p.c.slots[g.seq] : g.seq;
+  if (slot < 0 || slot >= p.c.n_slots) return finish<3>(b, kColumns, 0, 0, 0);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
   const auto fetch = [&](int j) {
@@ -571,9 +575,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
   float *z = reinterpret_cast<float*>(smraw + M::kZ), *den = reinterpret_cast<float*>(smraw + M::kDen);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.c.H, k = blockIdx.x / p.c.H;
-  const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
-  if (g.seq < 0) return;
   setup(p, b, kColumns);
+  const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
+  if (g.seq < 0) return finish<2>(b, kColumns, 0, 0, 0);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
   const auto fetch = [&](int j) {
@@ -778,10 +782,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   float* z = reinterpret_cast<float*>(sm + M::kZ);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
-  const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
-  if (g.seq < 0) return;
-  const int rows = p.c.ks.cu != nullptr ? g.len : min(p.c.ks.L, p.c.ks.N - g.row0);  // dense: zeros behind the tokens
   setup(p, b, kColumns);
+  const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
+  if (g.seq < 0) return finish<2>(b, kColumns, 0, 0, 0);
+  const int rows = p.c.ks.cu != nullptr ? g.len : min(p.c.ks.L, p.c.ks.N - g.row0);  // dense: zeros behind the tokens
   const uint32_t tmem = b->tbase;
   const int tiles = (rows + kT - 1) / kT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
   const auto fetch = [&](int j) {
@@ -793,7 +797,6 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   int issued = min(tiles, 2), mmas = 0;
   if (tid == 0)
     for (int j = 0; j < issued; ++j) fetch(j);
-  grid_dependency_wait();  // dS and dz
   const float* from = p.c.dS + ((size_t)g.seq * p.c.Hk + h) * (D * D + D);
   load_matrix<D>(sm + M::kS, sm + M::kSLo, from);
   if (tid < D) z[tid] = from[D * D + tid];
@@ -927,11 +930,11 @@ bool make_args(TcArgs* t, const CrossArgs& a, const CrossSide& s, int heads, con
   return make_map(&t->a, x, s, heads, a.d) && (y == nullptr || make_map(&t->b, *y, s, heads, a.d));
 }
 
-cudaError_t launch(void (*kernel)(TcArgs), SmemOptIn& opt, long long blocks, int threads, int smem, bool dependent, const TcArgs& t,
+cudaError_t launch(void (*kernel)(TcArgs), SmemOptIn& opt, long long blocks, int threads, int smem, const TcArgs& t,
                    cudaStream_t st) {
   const cudaError_t e = opt.ensure((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3((unsigned)blocks), (unsigned)threads, (size_t)smem, st, dependent, t);
+  return launch_dependent(kernel, dim3((unsigned)blocks), (unsigned)threads, (size_t)smem, st, true, t);
 }
 
 template <int D, int F>
@@ -939,14 +942,14 @@ cudaError_t states_t(const CrossArgs& a, cudaStream_t st) {
   TcArgs t;
   if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v)) return cudaErrorInvalidValue;
   static SmemOptIn opt;
-  return launch(tc_cross_states_kernel<D, F>, opt, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, SumSmem<D>::kBytes, false, t, st);
+  return launch(tc_cross_states_kernel<D, F>, opt, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, SumSmem<D>::kBytes, t, st);
 }
 template <int D, int F>
 cudaError_t read_t(const CrossArgs& a, cudaStream_t st) {
   TcArgs t;
   if (!make_args(&t, a, a.qs, a.H, a.q, nullptr)) return cudaErrorInvalidValue;
   static SmemOptIn opt;
-  return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, ReadSmem<D>::kBytes, false, t, st);
+  return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, ReadSmem<D>::kBytes, t, st);
 }
 template <int D, int F>
 cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
@@ -955,13 +958,13 @@ cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.qs.segs > 0) {
     if (!make_args(&t, a, a.qs, a.H, a.q, &a.dy)) return cudaErrorInvalidValue;
-    e = launch(tc_cross_query_kernel<D, F>, opt_q, (long long)a.qs.segs * a.H, Tc<D>::kThreads, QuerySmem<D>::kBytes, false, t, st);
+    e = launch(tc_cross_query_kernel<D, F>, opt_q, (long long)a.qs.segs * a.H, Tc<D>::kThreads, QuerySmem<D>::kBytes, t, st);
   }
   if (e != cudaSuccess || a.ks.segs == 0) return e;
   e = cross_join_launch(a, true, a.qs.segs > 0, st);
   if (e != cudaSuccess) return e;
   if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v)) return cudaErrorInvalidValue;
-  return launch(tc_cross_key_kernel<D, F>, opt_k, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, KeySmem<D>::kBytes, true, t, st);
+  return launch(tc_cross_key_kernel<D, F>, opt_k, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, KeySmem<D>::kBytes, t, st);
 }
 
 #define CROSS_FEATURES(fn, D)                                                   \
