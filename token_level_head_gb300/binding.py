@@ -607,56 +607,109 @@ def retention_copy_states(states, src, dst, *, stream=None):
     return states
 
 
+# The gated scan and the cross attention are called for single tokens too: what follows from shapes, strides, types and
+# options alone (their checks, and the C arguments) is kept for the values seen last.
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
+def _is_meta(m, name, shape, dtype):
+    """The same checks as _expect on (shape, stride, dtype), and contiguity."""
+    if m is None:
+        return
+    if tuple(m[0]) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(m[0])}, expected {tuple(shape)}")
+    if m[2] != dtype:
+        raise ValueError(f"{name}: dtype {m[2]}, expected {dtype}")
+    dense = 1
+    for n, s in zip(reversed(m[0]), reversed(m[1])):
+        if n > 1 and s != dense:
+            raise ValueError(f"{name}: must be contiguous, its strides are {tuple(m[1])}")
+        dense *= max(n, 1)
+
+
+def _token_metas(first, *named):
+    """Token tensors (name, meta) of the first one's shape and dtype with contiguous rows; their C dtype."""
+    name, m = first
+    if m[2] not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {m[2]}; use float32 or bfloat16")
+    for other, o in (first, *named):
+        if o[0] != m[0]:
+            raise ValueError(f"{other}: shape {tuple(o[0])}, expected {tuple(m[0])}")
+        if o[2] != m[2]:
+            raise ValueError(f"{other}: dtype {o[2]}, expected {m[2]}")
+        if o[1][-1] != 1 and o[0][-1] > 1:
+            raise ValueError(f"{other}: the last dimension must be contiguous, its stride is {o[1][-1]}")
+    return MHLA_BF16 if m[2] == torch.bfloat16 else MHLA_F32
+
+
+def _sequences(shape, cu, name, what, cu_name="cu_seqlens"):
+    """The sequences of tokens [B, ..]: B, or packed those of the offsets."""
+    _fits_int(**{f"{name}.shape[{i}]": n for i, n in enumerate(shape)})
+    if cu is None:
+        return shape[0]
+    if shape[0] != 1:
+        raise ValueError(f"{name}: expected [1, {what}] with {cu_name}, got shape {tuple(shape)}")
+    if len(cu[0]) != 1 or cu[0][0] < 1:
+        raise ValueError(f"{cu_name}: expected [sequences + 1], got shape {tuple(cu[0])}")
+    _is_meta(cu, cu_name, cu[0], torch.int32)
+    _fits_int(sequences=cu[0][0] - 1)
+    return cu[0][0] - 1
+
+
+def _one_device(*ts):
+    """The index of the one CUDA device of all tensors."""
+    index = ts[0].get_device()  # -1: not a CUDA tensor
+    for t in ts:
+        if t is not None and (t.get_device() != index or index < 0):
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA tensors")
+            raise ValueError(f"tensor on {t.device}, expected {ts[0].device}")
+    return index
+
+
+def _call_on(name, index, stream, *args):
+    """Calls entry ``name`` with device ``index`` current and the stream last."""
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:
+        handle = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    fn = getattr(_lib or load(), name)
+    if _current_device() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, handle)
+    if st != MHLA_OK:
+        raise MhlaError(name, st)
+
+
 GATES = {"sigmoid": 0, "log": 1, "decay": 2}
 
 
 def _gate(gate):
-    try:
-        return GATES[gate]
-    except (KeyError, TypeError):
-        raise ValueError(f"gate: {gate!r}, one of {', '.join(GATES)}") from None
+    if gate not in GATES:
+        raise ValueError(f"gate: {gate!r}, one of {', '.join(GATES)}")
+    return GATES[gate]
 
 
-@functools.lru_cache(maxsize=1024)
-def _c_scan_strides(st):
+def _scan_strides(m):
+    st = m[1]
     return ctypes.byref(_Strides(st[0], 0, st[1] if len(st) == 3 else 0))
 
 
-def _scan_strided(t, name):
-    """(pointer, strides) of a tensor [B, N, D] or [B, D] with contiguous rows."""
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous, its stride is {st[-1]}")
-    return t.data_ptr(), _c_scan_strides(st)
-
-
-def _scan_sizes(x, cu_seqlens):
-    """B (sequences), N (packed: all tokens), D of x [B, N, D]; packed: x [1, tokens, D]."""
-    if x.dim() != 3:
-        raise ValueError(f"x: expected [B, N, D], got shape {tuple(x.shape)}")
-    B, N, D = x.shape
-    if cu_seqlens is not None:
-        if B != 1:
-            raise ValueError(f"x: expected [1, tokens, D] with cu_seqlens, got shape {tuple(x.shape)}")
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError(f"cu_seqlens: expected [sequences + 1], got shape {tuple(cu_seqlens.shape)}")
-        _expect_fast(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
-        B = cu_seqlens.numel() - 1
-    _fits_int(B=B, N=N, D=D)
-    return B, N, D
-
-
-def _scan_states(states, slots, B, D):
+def _scan_pool(states, slots, B, D):
+    """The slots of a pool [slots, D]."""
     if states is None:
         if slots is not None:
             raise ValueError("slots: given without states")
         return 0
-    if states.dim() != 2:
-        raise ValueError(f"states: expected [slots, D], got shape {tuple(states.shape)}")
-    _expect_fast(states, "states", (states.shape[0], D), torch.float32)
-    _expect_fast(slots, "slots", (B,), torch.int32)
-    _fits_int(slots=states.shape[0])
-    return states.shape[0]
+    if len(states[0]) != 2:
+        raise ValueError(f"states: expected [slots, D], got shape {tuple(states[0])}")
+    _is_meta(states, "states", (states[0][0], D), torch.float32)
+    _is_meta(slots, "slots", (B,), torch.int32)
+    _fits_int(slots=states[0][0])
+    return states[0][0]
 
 
 def gated_scan_checkpoint_rows(B: int, N: int) -> int:
@@ -665,8 +718,23 @@ def gated_scan_checkpoint_rows(B: int, N: int) -> int:
     return 0 if max(B, N) > 0x7fffffff else int(load().gated_scan_checkpoint_rows(B, N))
 
 
-def _scan_checkpoints(checkpoints, x, D):
-    _expect_fast(checkpoints, "checkpoints", (gated_scan_checkpoint_rows(x.shape[0], x.shape[1]), D), torch.float32)
+def _scan_sizes(x, cu, kept):
+    if len(x[0]) != 3:
+        raise ValueError(f"x: expected [B, N, D], got shape {tuple(x[0])}")
+    B = _sequences(x[0], cu, "x", "tokens, D")
+    if kept is not None:
+        _is_meta(kept, "checkpoints", (gated_scan_checkpoint_rows(x[0][0], x[0][1]), x[0][2]), torch.float32)
+    return B, x[0][1], x[0][2]
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_forward_plan(x, g, y, cu, states, slots, load_state, kept, gate):
+    B, N, D = _scan_sizes(x, cu, kept)
+    dt = _token_metas(("x", x), ("g", g), ("y", y))
+    if load_state and states is None:
+        raise ValueError("load_state: needs states")
+    n_slots = _scan_pool(states, slots, B, D)
+    return B, N, D, dt, n_slots, _gate(gate), _scan_strides(x), _scan_strides(g), _scan_strides(y)
 
 
 def gated_scan_forward(x, g, y, *, gate="sigmoid", cu_seqlens=None, states=None, slots=None, load_state=False,
@@ -676,19 +744,24 @@ def gated_scan_forward(x, g, y, *, gate="sigmoid", cu_seqlens=None, states=None,
     strides (rows contiguous); packed sequences: [1, tokens, D] and int32 ``cu_seqlens`` [sequences + 1].  ``states``
     [slots, D] fp32 receives the final states (``slots``: the slot of each sequence, int32); with ``load_state`` the
     sequences start from them.  ``checkpoints`` (``gated_scan_checkpoint_rows``) is written for the backward pass."""
-    B, N, D = _scan_sizes(x, cu_seqlens)
-    _expect_like(x, ("g", g), ("y", y))
-    if load_state and states is None:
-        raise ValueError("load_state: needs states")
-    n_slots = _scan_states(states, slots, B, D)
-    if checkpoints is not None:
-        _scan_checkpoints(checkpoints, x, D)
-    dev = _retention_device((x, g, y), (cu_seqlens, states, slots, checkpoints))
-    _retention_call("gated_scan_forward", dev,
-                    (*_scan_strided(x, "x"), *_scan_strided(g, "g"), *_scan_strided(y, "y"), B, N, D,
-                     _address(cu_seqlens), _address(states), _address(slots), n_slots, 1 if load_state else 0,
-                     _address(checkpoints), _dtype(x), _gate(gate)), stream)
+    load_state = bool(load_state)
+    B, N, D, dt, n_slots, code, sx, sg, sy = _scan_forward_plan(
+        _meta(x), _meta(g), _meta(y), _meta(cu_seqlens), _meta(states), _meta(slots), load_state, _meta(checkpoints), gate)
+    _call_on("gated_scan_forward", _one_device(x, g, y, cu_seqlens, states, slots, checkpoints), stream,
+             x.data_ptr(), sx, g.data_ptr(), sg, y.data_ptr(), sy, B, N, D, _address(cu_seqlens), _address(states),
+             _address(slots), n_slots, 1 if load_state else 0, _address(checkpoints), dt, code)
     return y
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_backward_plan(x, g, dy, kept, dx, dg, cu, h0, dh_last, dh0, gate):
+    if kept is None:
+        raise ValueError("checkpoints: required")
+    B, N, D = _scan_sizes(x, cu, kept)
+    dt = _token_metas(("x", x), ("g", g), ("dy", dy), ("dx", dx), ("dg", dg))
+    for name, m in (("h0", h0), ("dh_last", dh_last), ("dh0", dh0)):
+        _is_meta(m, name, (B, D), torch.float32)
+    return B, N, D, dt, _gate(gate), *(_scan_strides(m) for m in (x, g, dy, dx, dg))
 
 
 def gated_scan_backward(x, g, dy, checkpoints, dx, dg, *, gate="sigmoid", cu_seqlens=None, h0=None, dh_last=None,
@@ -696,64 +769,66 @@ def gated_scan_backward(x, g, dy, checkpoints, dx, dg, *, gate="sigmoid", cu_seq
     """Gradients of gated_scan_forward from dy = dL/dy and, where given, ``dh_last`` = dL/d(last states): dx and dg are
     written, and ``dh0`` = dL/d(starts).  ``checkpoints``: of the forward call; ``h0``: the states that it started from
     (load_state; None: zero).  h0, dh_last, dh0: fp32 [sequences, D]."""
-    B, N, D = _scan_sizes(x, cu_seqlens)
-    _expect_like(x, ("g", g), ("dy", dy), ("dx", dx), ("dg", dg))
-    if checkpoints is None:
-        raise ValueError("checkpoints: required")
-    _scan_checkpoints(checkpoints, x, D)
-    for name, t in (("h0", h0), ("dh_last", dh_last), ("dh0", dh0)):
-        _expect_fast(t, name, (B, D), torch.float32)
-    dev = _retention_device((x, g, dy, dx, dg), (cu_seqlens, checkpoints, h0, dh_last, dh0))
-    _retention_call("gated_scan_backward", dev,
-                    (*_scan_strided(x, "x"), *_scan_strided(g, "g"), *_scan_strided(dy, "dy"), checkpoints.data_ptr(),
-                     *_scan_strided(dx, "dx"), *_scan_strided(dg, "dg"), B, N, D, _address(cu_seqlens), _address(h0),
-                     _address(dh_last), _address(dh0), _dtype(x), _gate(gate)), stream)
+    B, N, D, dt, code, sx, sg, sd, sdx, sdg = _scan_backward_plan(
+        _meta(x), _meta(g), _meta(dy), _meta(checkpoints), _meta(dx), _meta(dg), _meta(cu_seqlens), _meta(h0),
+        _meta(dh_last), _meta(dh0), gate)
+    _call_on("gated_scan_backward", _one_device(x, g, dy, checkpoints, dx, dg, cu_seqlens, h0, dh_last, dh0), stream,
+             x.data_ptr(), sx, g.data_ptr(), sg, dy.data_ptr(), sd, checkpoints.data_ptr(), dx.data_ptr(), sdx,
+             dg.data_ptr(), sdg, B, N, D, _address(cu_seqlens), _address(h0), _address(dh_last), _address(dh0), dt, code)
     return dx, dg
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_step_plan(x, g, states, out, slots, gate):
+    if len(x[0]) != 2:
+        raise ValueError(f"x: expected [B, D], got shape {tuple(x[0])}")
+    B, D = x[0]
+    _fits_int(B=B, D=D)
+    dt = _token_metas(("x", x), ("g", g), ("out", out))
+    if states is None:
+        raise ValueError("states: required")
+    return B, D, dt, _scan_pool(states, slots, B, D), _gate(gate), _scan_strides(x), _scan_strides(g), _scan_strides(out)
 
 
 def gated_scan_step(x, g, states, out, *, gate="sigmoid", slots=None, stream=None):
     """One token for every row: x/g/out [B, D] with any strides (rows contiguous), states [slots, D] fp32 (updated);
     ``slots`` int32 [B], an entry outside the pool leaves its row out."""
-    if x.dim() != 2:
-        raise ValueError(f"x: expected [B, D], got shape {tuple(x.shape)}")
-    B, D = x.shape
-    _fits_int(B=B, D=D)
-    _expect_like(x, ("g", g), ("out", out))
-    if states is None:
-        raise ValueError("states: required")
-    n_slots = _scan_states(states, slots, B, D)
-    dev = _retention_device((x, g, out), (states, slots))
-    _retention_call("gated_scan_step", dev,
-                    (*_scan_strided(x, "x"), *_scan_strided(g, "g"), states.data_ptr(), _address(slots), n_slots,
-                     *_scan_strided(out, "out"), B, D, _dtype(x), _gate(gate)), stream)
+    B, D, dt, n_slots, code, sx, sg, so = _scan_step_plan(_meta(x), _meta(g), _meta(states), _meta(out), _meta(slots), gate)
+    _call_on("gated_scan_step", _one_device(x, g, states, out, slots), stream, x.data_ptr(), sx, g.data_ptr(), sg,
+             states.data_ptr(), _address(slots), n_slots, out.data_ptr(), so, B, D, dt, code)
     return out
 
 
-@functools.lru_cache(maxsize=256)
 def _cross_options(feature, normalise):
     if feature not in _RETENTION_FEATURES:
         raise ValueError(f"feature: one of {sorted(_RETENTION_FEATURES)}, got {feature!r}")
     return ctypes.byref(MhlaOptions(_RETENTION_FEATURES[feature], 1 if normalise else 0, 1.0))
 
 
-def _cross_sums(S, z, Hk, d):
-    """The slots of S [slots, Hk, d, d] and z [slots, Hk, d]."""
-    if S.dim() != 4:
-        raise ValueError(f"S: expected [slots, Hk, d, d], got shape {tuple(S.shape)}")
-    n = S.shape[0]
-    _expect_fast(S, "S", (n, Hk, d, d), torch.float32)
-    _expect_fast(z, "z", (n, Hk, d), torch.float32)
-    _fits_int(slots=n)
-    return n
+def _cross_strides(m):
+    return ctypes.byref(_Strides(*m[1][:3]))
 
 
-def _cross_heads(S, H, d):
-    if S.dim() != 4:
-        raise ValueError(f"S: expected [slots, Hk, d, d], got shape {tuple(S.shape)}")
-    Hk = S.shape[1]
+def _cross_side(m, cu, name, cu_name="cu_seqlens"):
+    """B (sequences), heads, N (packed: all tokens), d of [B, heads, N, d]."""
+    if len(m[0]) != 4:
+        raise ValueError(f"{name}: expected [B, heads, N, d], got shape {tuple(m[0])}")
+    return _sequences(m[0], cu, name, "heads, tokens, d", cu_name), *m[0][1:]
+
+
+def _cross_sums(S, z, H, d):
+    """The slots and heads of S [slots, Hk, d, d] and z [slots, Hk, d], H a multiple of Hk."""
+    if S is None or z is None:
+        raise ValueError("S, z: required")
+    if len(S[0]) != 4:
+        raise ValueError(f"S: expected [slots, Hk, d, d], got shape {tuple(S[0])}")
+    n, Hk = S[0][:2]
     if Hk == 0 or H % Hk != 0:
         raise ValueError(f"S: {Hk} heads, {H} query heads are no multiple of them")
-    return Hk
+    _is_meta(S, "S", (n, Hk, d, d), torch.float32)
+    _is_meta(z, "z", (n, Hk, d), torch.float32)
+    _fits_int(slots=n)
+    return n, Hk
 
 
 def linattn_cross_workspace_bytes(B: int, H: int, Hk: int, tokens_q: int, tokens_k: int, d: int,
@@ -763,11 +838,25 @@ def linattn_cross_workspace_bytes(B: int, H: int, Hk: int, tokens_q: int, tokens
     return int(load().linattn_cross_workspace_bytes(B, H, Hk, tokens_q, tokens_k, d, 1 if backward else 0))
 
 
-def _cross_workspace(workspace, sizes, backward, dev, stream):
+def _cross_workspace(workspace, sizes, backward, device, stream):
     if workspace is None:  # of the call's stream, as in _retention_workspace
         with torch.cuda.stream(stream):
-            workspace = new_workspace(linattn_cross_workspace_bytes(*sizes, backward), dev)
+            workspace = new_workspace(linattn_cross_workspace_bytes(*sizes, backward), device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
     return workspace
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_states_plan(k, v, S, z, cu, lens, slots, feature, normalise):
+    B, Hk, N, d = _cross_side(k, cu, "k")
+    dt = _token_metas(("k", k), ("v", v))
+    n_slots, heads = _cross_sums(S, z, Hk, d)
+    if heads != Hk:
+        raise ValueError(f"S: {heads} heads, k has {Hk}")
+    _is_meta(lens, "lens", (B,), torch.int32)
+    _is_meta(slots, "slots", (B,), torch.int32)
+    return B, Hk, N, d, n_slots, dt, _cross_options(feature, normalise), _cross_strides(k), _cross_strides(v)
 
 
 def linattn_cross_states(k, v, S, z, *, cu_seqlens=None, lens=None, slots=None, feature="elu1", normalise=True,
@@ -776,20 +865,22 @@ def linattn_cross_states(k, v, S, z, *, cu_seqlens=None, lens=None, slots=None, 
     contiguous), S [slots, Hk, d, d] and z [slots, Hk, d] fp32, written.  Packed sequences: k/v [1, Hk, tokens, d] and
     int32 ``cu_seqlens`` [sequences + 1]; a padded batch: int32 ``lens`` [B], the tokens of each row.  ``slots`` int32:
     the slot of each sequence."""
-    B, Hk, N, d = _retention_sizes(k, cu_seqlens)
-    _expect_like(k, ("v", v))
-    if S is None or z is None:
-        raise ValueError("S, z: required")
-    n_slots = _cross_sums(S, z, Hk, d)
-    _expect_fast(lens, "lens", (B,), torch.int32)
-    _expect_fast(slots, "slots", (B,), torch.int32)
-    opt = _cross_options(feature, bool(normalise))
-    dev = _retention_device((k, v), (S, z, cu_seqlens, lens, slots, workspace))
-    ws = _cross_workspace(workspace, (B, Hk, Hk, 0, N if cu_seqlens is not None else B * N, d), False, dev, stream)
-    _retention_call("linattn_cross_states", dev,
-                    (*_strided(k, "k"), *_strided(v, "v"), S.data_ptr(), z.data_ptr(), B, Hk, N, d, _address(cu_seqlens),
-                     _address(lens), _address(slots), n_slots, _dtype(k), opt, ws.data_ptr(), ws.nbytes), stream)
+    B, Hk, N, d, n_slots, dt, opt, sk, sv = _cross_states_plan(
+        _meta(k), _meta(v), _meta(S), _meta(z), _meta(cu_seqlens), _meta(lens), _meta(slots), feature, bool(normalise))
+    index = _one_device(k, v, S, z, cu_seqlens, lens, slots, workspace)
+    ws = _cross_workspace(workspace, (B, Hk, Hk, 0, N if cu_seqlens is not None else B * N, d), False, k.device, stream)
+    _call_on("linattn_cross_states", index, stream, k.data_ptr(), sk, v.data_ptr(), sv, S.data_ptr(), z.data_ptr(), B, Hk, N,
+             d, _address(cu_seqlens), _address(lens), _address(slots), n_slots, dt, opt, ws.data_ptr(), ws.nbytes)
     return S, z
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_read_plan(q, S, z, y, cu, slots, feature, normalise):
+    B, H, N, d = _cross_side(q, cu, "q")
+    dt = _token_metas(("q", q), ("y", y))
+    n_slots, Hk = _cross_sums(S, z, H, d)
+    _is_meta(slots, "slots", (B,), torch.int32)
+    return B, H, Hk, N, d, n_slots, dt, _cross_options(feature, normalise), _cross_strides(q), _cross_strides(y)
 
 
 def linattn_cross_read(q, S, z, y, *, cu_seqlens=None, slots=None, feature="elu1", normalise=True, eps=1e-6,
@@ -797,46 +888,47 @@ def linattn_cross_read(q, S, z, y, *, cu_seqlens=None, slots=None, feature="elu1
     """y_t = phi(q_t) S / (phi(q_t) . z + eps) from the sums of linattn_cross_states: q/y [B, H, N, d] with any strides
     (rows contiguous), H a multiple of S's heads; packed queries: [1, H, tokens, d] and int32 ``cu_seqlens``.  ``slots``
     int32: the slot that each sequence reads, an entry outside the pool leaves its rows out.  N = 1: a decoder's step."""
-    B, H, N, d = _retention_sizes(q, cu_seqlens)
-    _expect_like(q, ("y", y))
-    Hk = _cross_heads(S, H, d)
-    n_slots = _cross_sums(S, z, Hk, d)
-    _expect_fast(slots, "slots", (B,), torch.int32)
-    opt = _cross_options(feature, bool(normalise))
-    dev = _retention_device((q, y), (S, z, cu_seqlens, slots, workspace))
-    if workspace is None and (N != 1 or cu_seqlens is not None):
-        workspace = _cross_workspace(None, (B, H, Hk, N if cu_seqlens is not None else B * N, 0, d), False, dev, stream)
-    _retention_call("linattn_cross_read", dev,
-                    (*_strided(q, "q"), S.data_ptr(), z.data_ptr(), *_strided(y, "y"), B, H, Hk, N, d,
-                     _address(cu_seqlens), _address(slots), n_slots, _dtype(q), opt, eps, _address(workspace),
-                     0 if workspace is None else workspace.nbytes), stream)
+    B, H, Hk, N, d, n_slots, dt, opt, sq, sy = _cross_read_plan(
+        _meta(q), _meta(S), _meta(z), _meta(y), _meta(cu_seqlens), _meta(slots), feature, bool(normalise))
+    index = _one_device(q, y, S, z, cu_seqlens, slots, workspace)
+    if workspace is not None or N != 1 or cu_seqlens is not None:
+        workspace = _cross_workspace(workspace, (B, H, Hk, N if cu_seqlens is not None else B * N, 0, d), False, q.device, stream)
+    _call_on("linattn_cross_read", index, stream, q.data_ptr(), sq, S.data_ptr(), z.data_ptr(), y.data_ptr(), sy, B, H, Hk, N,
+             d, _address(cu_seqlens), _address(slots), n_slots, dt, opt, eps, _address(workspace),
+             0 if workspace is None else workspace.nbytes)
     return y
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_backward_plan(q, k, v, S, z, dy, dq, dk, dv, cu_q, cu_k, lens, feature, normalise):
+    B, H, Nq, d = _cross_side(q, cu_q, "q", "cu_seqlens_q")
+    Bk, Hk, Nk, d_k = _cross_side(k, cu_k, "k", "cu_seqlens_k")
+    if Bk != B or d_k != d or k[2] != q[2]:
+        raise ValueError(f"k: {Bk} sequences of width {d_k}, {k[2]}; expected {B} of width {d}, {q[2]}")
+    dt = _token_metas(("q", q), ("dy", dy), ("dq", dq))
+    _token_metas(("k", k), ("v", v), ("dk", dk), ("dv", dv))
+    slots, heads = _cross_sums(S, z, H, d)
+    if heads != Hk:
+        raise ValueError(f"S: {heads} heads, k has {Hk}")
+    if slots != B:
+        raise ValueError(f"S: {slots} slots, expected one for each of {B} sequences")
+    _is_meta(lens, "lens", (B,), torch.int32)
+    return B, H, Hk, Nq, Nk, d, dt, _cross_options(feature, normalise), *(_cross_strides(m) for m in (q, k, v, dy, dq, dk, dv))
 
 
 def linattn_cross_backward(q, k, v, S, z, dy, dq, dk, dv, *, cu_seqlens_q=None, cu_seqlens_k=None, lens=None,
                            feature="elu1", normalise=True, eps=1e-6, workspace=None, stream=None):
     """Gradients of linattn_cross_read of linattn_cross_states (slot i is sequence i) from dy = dL/dY; dq, dk and dv are
     written, rows of a padded encoder batch behind ``lens`` as zeros.  Shapes as there."""
-    B, H, Nq, d = _retention_sizes(q, cu_seqlens_q)
-    Bk, Hk, Nk, dk_ = _retention_sizes(k, cu_seqlens_k)
-    if Bk != B or dk_ != d or k.dtype != q.dtype:
-        raise ValueError(f"k: {Bk} sequences of width {dk_}, {k.dtype}; expected {B} of width {d}, {q.dtype}")
-    _expect_like(q, ("dy", dy), ("dq", dq))
-    _expect_like(k, ("v", v), ("dk", dk), ("dv", dv))
-    if _cross_heads(S, H, d) != Hk:
-        raise ValueError(f"S: {S.shape[1]} heads, k has {Hk}")
-    if _cross_sums(S, z, Hk, d) != B:
-        raise ValueError(f"S: {S.shape[0]} slots, expected one for each of {B} sequences")
-    _expect_fast(lens, "lens", (B,), torch.int32)
-    opt = _cross_options(feature, bool(normalise))
-    dev = _retention_device((q, k, v, dy, dq, dk, dv), (S, z, cu_seqlens_q, cu_seqlens_k, lens, workspace))
+    B, H, Hk, Nq, Nk, d, dt, opt, sq, sk, sv, sdy, sdq, sdk, sdv = _cross_backward_plan(
+        _meta(q), _meta(k), _meta(v), _meta(S), _meta(z), _meta(dy), _meta(dq), _meta(dk), _meta(dv), _meta(cu_seqlens_q),
+        _meta(cu_seqlens_k), _meta(lens), feature, bool(normalise))
+    index = _one_device(q, k, v, S, z, dy, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, lens, workspace)
     ws = _cross_workspace(workspace, (B, H, Hk, Nq if cu_seqlens_q is not None else B * Nq,
-                                      Nk if cu_seqlens_k is not None else B * Nk, d), True, dev, stream)
-    _retention_call("linattn_cross_backward", dev,
-                    (*_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"), S.data_ptr(), z.data_ptr(),
-                     *_strided(dy, "dy"), *_strided(dq, "dq"), *_strided(dk, "dk"), *_strided(dv, "dv"), B, H, Hk, Nq, Nk, d,
-                     _address(cu_seqlens_q), _address(cu_seqlens_k), _address(lens), _dtype(q), opt, eps, ws.data_ptr(),
-                     ws.nbytes), stream)
+                                      Nk if cu_seqlens_k is not None else B * Nk, d), True, q.device, stream)
+    _call_on("linattn_cross_backward", index, stream, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, S.data_ptr(),
+             z.data_ptr(), dy.data_ptr(), sdy, dq.data_ptr(), sdq, dk.data_ptr(), sdk, dv.data_ptr(), sdv, B, H, Hk, Nq, Nk, d,
+             _address(cu_seqlens_q), _address(cu_seqlens_k), _address(lens), dt, opt, eps, ws.data_ptr(), ws.nbytes)
     return dq, dk, dv
 
 
