@@ -40,7 +40,7 @@ cudaError_t simt_cross_backward_launch(const CrossArgs& a, mhla_dtype dt, cudaSt
 // one query a row (N = 1, dense)
 cudaError_t cross_step_launch(const CrossArgs& a, mhla_dtype dt, cudaStream_t st);
 // The sums over segments (and, backward, over the query heads of a key head): what the segments' kernels left in part.
-cudaError_t cross_join_launch(const CrossArgs& a, bool backward, bool dependent, cudaStream_t st);
+cudaError_t cross_join_launch(const CrossArgs& a, bool backward, cudaStream_t st);
 
 // Whether the segments' kernel of the states has to be joined: not where every sequence is one segment.
 __host__ __device__ inline bool cross_joined(const CrossSide& s) { return s.cu != nullptr || s.N == 0 || s.N > s.L; }

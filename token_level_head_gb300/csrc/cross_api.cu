@@ -17,10 +17,10 @@ namespace {
 struct Kind {
   int unit, slots;
 };
-Kind kind_of(int d, bool tc) { return tc ? Kind{128, 2 * kRetSms} : Kind{64, (d == 128 ? 2 : 4) * kRetSms}; }
+Kind kind_of(int d, bool tc) { return tc ? Kind{128, 2 * kRetSms} : Kind{32, (d == 128 ? 2 : 6) * kRetSms}; }
 
 // Reads (three blocks an SM on the tensor cores with d = 64) leave no parts, so their segments need no room.
-Kind read_kind(int d, bool tc) { return tc && d == 64 ? Kind{128, 3 * kRetSms} : kind_of(d, tc); }
+Kind read_kind(int d, bool tc) { return tc ? Kind{128, (d == 64 ? 3 : 2) * kRetSms} : Kind{64, (d == 128 ? 2 : 4) * kRetSms}; }
 
 // The length of a segment: so many tokens that the blocks fill the SMs, and no fewer than a tile.
 int segment_length(const CrossSide& s, int heads, const Kind& k) {
@@ -148,7 +148,7 @@ mhla_status linattn_cross_states(const void* k, const mhla_strides* k_strides, c
   cudaError_t err = cudaSuccess;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.ks.segs > 0) err = tc_cross_supported(d, dt) ? tc_cross_states_launch(a, s) : simt_cross_states_launch(a, dt, s);
-  if (err == cudaSuccess && cross_joined(a.ks)) err = cross_join_launch(a, false, a.ks.segs > 0, s);
+  if (err == cudaSuccess && cross_joined(a.ks)) err = cross_join_launch(a, false, s);
   return from_cuda(err);
 }
 

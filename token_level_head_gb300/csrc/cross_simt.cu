@@ -135,6 +135,8 @@ __device__ __forceinline__ void store_cols(T* row, int tx, const float (&f)[Simt
 constexpr int kSumRows = 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cross_states_kernel(const __grid_constant__ CrossArgs p) {
+  launch_dependents();
+  grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   using S = Simt<D>;
   extern __shared__ float sm[];
   __shared__ int scratch;
@@ -224,6 +226,8 @@ __global__ void __launch_bounds__(kJoinThreads) cross_join_kernel(const __grid_c
 constexpr int kReadRows = 64;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cross_read_kernel(const __grid_constant__ CrossArgs p) {
+  launch_dependents();
+  grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   using S = Simt<D>;
   constexpr int RN = kReadRows / 16;
   extern __shared__ float sm[];
@@ -272,6 +276,8 @@ __global__ void __launch_bounds__(kThreads) cross_read_kernel(const __grid_const
 constexpr int kBackRows = 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cross_backward_query_kernel(const __grid_constant__ CrossArgs p) {
+  launch_dependents();
+  grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   using S = Simt<D>;
   constexpr int RN = kBackRows / 16, E = D * D + D;
   extern __shared__ float sm[];
@@ -348,6 +354,8 @@ __global__ void __launch_bounds__(kThreads) cross_backward_query_kernel(const __
 // ---- backward over the keys: dk and dv; dense rows behind a sequence's tokens become zeros
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cross_backward_key_kernel(const __grid_constant__ CrossArgs p) {
+  launch_dependents();
+  grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   using S = Simt<D>;
   constexpr int RN = kBackRows / 16, E = D * D + D;
   extern __shared__ float sm[];
@@ -397,6 +405,8 @@ struct Step {
 };
 template <typename T, int D>
 __global__ void __launch_bounds__(Step<D>::kThreads) cross_step_kernel(const __grid_constant__ CrossArgs p) {
+  launch_dependents();
+  grid_dependency_wait();
   constexpr int THREADS = Step<D>::kThreads, LANES = D / 4, ROWS = THREADS / LANES;  // threads of a row of S, rows at a time
   __shared__ float fq[D];
   __shared__ float red[THREADS / 32][D + 1];
@@ -461,13 +471,10 @@ __global__ void __launch_bounds__(Step<D>::kThreads) cross_step_kernel(const __g
 }
 
 // ---- host
-template <typename K>
-cudaError_t launch(K kernel, SmemOptIn& opt, long long blocks, int smem, const CrossArgs& a, cudaStream_t st) {
+cudaError_t launch(void (*kernel)(CrossArgs), SmemOptIn& opt, long long blocks, int smem, const CrossArgs& a, cudaStream_t st) {
   const cudaError_t e = opt.ensure((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)blocks, kThreads, smem, st>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(kernel, dim3((unsigned)blocks), kThreads, (size_t)smem, st, true, a);
 }
 
 template <typename T, int D>
@@ -487,15 +494,13 @@ cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
   if (a.qs.segs > 0)
     e = launch(cross_backward_query_kernel<T, D>, opt_q, (long long)a.qs.segs * a.H, (D + 4 * kBackRows) * Simt<D>::LD * 4, a, st);
   if (e != cudaSuccess || a.ks.segs == 0) return e;
-  e = cross_join_launch(a, true, false, st);
+  e = cross_join_launch(a, true, st);
   if (e != cudaSuccess) return e;
   return launch(cross_backward_key_kernel<T, D>, opt_k, (long long)a.ks.segs * a.Hk, (2 * D + 3 * kBackRows) * Simt<D>::LD * 4, a, st);
 }
 template <typename T, int D>
 cudaError_t step_t(const CrossArgs& a, cudaStream_t st) {
-  cross_step_kernel<T, D><<<(unsigned)((long long)a.qs.B * a.Hk), Step<D>::kThreads, 0, st>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(cross_step_kernel<T, D>, dim3((unsigned)((long long)a.qs.B * a.Hk)), Step<D>::kThreads, 0, st, true, a);
 }
 
 #define CROSS_DISPATCH(fn)                                                                        \
@@ -508,7 +513,7 @@ cudaError_t step_t(const CrossArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t cross_join_launch(const CrossArgs& a, bool backward, bool dependent, cudaStream_t st) {
+cudaError_t cross_join_launch(const CrossArgs& a, bool backward, cudaStream_t st) {
   const int per = ((a.d * a.d + a.d) / 4 + kJoinRuns - 1) / kJoinRuns;
   const int B = backward ? a.qs.B : a.ks.B;
   cudaLaunchAttribute at;
@@ -519,7 +524,7 @@ cudaError_t cross_join_launch(const CrossArgs& a, bool backward, bool dependent,
   c.blockDim = dim3(kJoinThreads);
   c.stream = st;
   c.attrs = &at;
-  c.numAttrs = dependent ? 1 : 0;
+  c.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&c, cross_join_kernel, a, (int)backward);
   note_launch();
   return e;

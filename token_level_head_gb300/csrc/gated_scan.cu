@@ -24,7 +24,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the tiles,
 constexpr int kBlock = kThreads + 32;                  // and a warp that carries the state over the tiles (exchange)
-constexpr int kWideCluster = 4, kNarrowCluster = 8;    // blocks of a cluster at most, with 128 bytes of channels and with 32
+constexpr int kWideCluster = 4, kNarrowCluster = 8;    // blocks of a cluster at most, with 128 bytes of channels and with 64
 constexpr int P = 1, V = 2 * P;  // channels of a thread: a pair, so that a warp of bf16 has a row of 128 bytes to itself
 
 // A thread's rows of a tile (32 values each of a and b in registers) and the lanes of 128 bytes of channels.
@@ -183,17 +183,20 @@ struct Marks {
 __device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // the kThreads of the tiles
 static_assert(kThreads == 256, "the barrier's count");
 
-// Packed sequences: bits of the tile's rows row0 .. (the tiles' threads), a word for the kR rows of a thread.  Offsets
-// outside [0, N] are clamped; out of order they mark rows of the tile all the same and nothing else.
+// Packed sequences: bits of the tile's rows row0 .., a word for the kR rows of a thread; two sets, by the tile's parity, as
+// the next tile's are made while the state that enters this one is on its way.  Offsets outside [0, N] are clamped; out of
+// order they mark rows of the tile all the same and nothing else.
 template <int GROUPS>
 struct MarkRows {
   unsigned first[GROUPS], last[GROUPS];
 };
-template <int kR, int GROUPS>
-__device__ __forceinline__ void mark_rows(const ScanArgs& p, int row0, MarkRows<GROUPS>& m) {
-  tile_sync();  // (the marks of the tile before have been read)
+// (the tiles' threads, between two of their barriers each: cleared, then set)
+template <int GROUPS>
+__device__ __forceinline__ void clear_marks(MarkRows<GROUPS>& m) {
   for (int i = threadIdx.x; i < GROUPS; i += kThreads) m.first[i] = m.last[i] = 0;
-  tile_sync();
+}
+template <int kR, int GROUPS>
+__device__ __forceinline__ void set_marks(const ScanArgs& p, int row0, MarkRows<GROUPS>& m) {
   for (int i = threadIdx.x; i < p.B; i += kThreads) {
     const int lo = min(max(p.cu[i], 0), p.N), hi = min(max(p.cu[i + 1], lo), p.N);
     if (lo == hi) continue;
@@ -201,7 +204,6 @@ __device__ __forceinline__ void mark_rows(const ScanArgs& p, int row0, MarkRows<
     if (f >= 0 && f < GROUPS * kR) atomicOr(&m.first[f / kR], 1u << f % kR);
     if (l >= 0 && l < GROUPS * kR) atomicOr(&m.last[l / kR], 1u << l % kR);
   }
-  tile_sync();
 }
 // The sequence that a marked row is in: the last one whose offset is not behind the row.
 __device__ __noinline__ int sequence_of(const int* cu, int B, int row) {
@@ -336,25 +338,23 @@ struct ScanShared {
 // What goes on from tile to tile, in a warp of its own: as it has no other stores, the release of the cluster's barrier
 // waits for none (with the state carried by warps of the tiles each round waited for their outputs to arrive in L2).  The
 // block's warps have A, B in s.wa, s.wb and wait for s.carry.
-__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 2, 288;" ::: "memory"); }
-__device__ __forceinline__ void block_arrive() { asm volatile("bar.arrive 2, 288;" ::: "memory"); }
-__device__ __forceinline__ void carry_sync() { asm volatile("bar.sync 3, 288;" ::: "memory"); }
-__device__ __forceinline__ void carry_arrive() { asm volatile("bar.arrive 3, 288;" ::: "memory"); }
+// (Two barriers each, by the tile's parity: one side may be a tile ahead of the other.)
+__device__ __forceinline__ void block_sync(int par) { asm volatile("bar.sync %0, 288;" ::"r"(2 + par) : "memory"); }
+__device__ __forceinline__ void block_arrive(int par) { asm volatile("bar.arrive %0, 288;" ::"r"(2 + par) : "memory"); }
+__device__ __forceinline__ void carry_sync(int par) { asm volatile("bar.sync %0, 288;" ::"r"(4 + par) : "memory"); }
+__device__ __forceinline__ void carry_arrive(int par) { asm volatile("bar.arrive %0, 288;" ::"r"(4 + par) : "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 static_assert(kBlock == 288, "the barriers' counts");
 
-// The warps of the tiles, between s.wa, s.wb[par] written and s.carry[par] read.
-__device__ __forceinline__ void exchange_wait(bool clustered) {
-  if (!clustered) {
-    block_sync();  // (the carry of this tile was written before the carrying warp came here)
-    return;
-  }
-  block_arrive();
-  cluster_arrive_relaxed();
-  cluster_wait();
-  carry_sync();
+// The warps of the tiles: s.wa, s.wb[par] of a tile are written.  The tile before must have passed give_wait.
+__device__ __forceinline__ void give(int par, bool clustered) {
+  block_arrive(par);
+  if (clustered) cluster_arrive_relaxed();
+}
+__device__ __forceinline__ void give_wait(bool clustered) {
+  if (clustered) cluster_wait();
 }
 // The carrying warp: all rounds of tiles.
 template <typename T, int LW, bool REVERSE, bool PACKED>
@@ -365,12 +365,14 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
 #pragma unroll
   for (int k = 0; k < K; ++k) running[k] = 0.f;
   for (int t = 0, par = 0; t < rounds; ++t, par ^= 1) {
+    block_sync(par);
     if (n == 1) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
         if (lane + 32 * k < CW) s.carry[par][lane + 32 * k] = running[k];
+      __syncwarp();
+      carry_arrive(par);
     }
-    block_sync();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = lane + 32 * k;
@@ -413,7 +415,7 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
       running[k] = h;
     }
     __syncwarp();
-    carry_arrive();
+    carry_arrive(par);
   }
 }
 // The state before the warp: over the warps from `from` on (backwards: down to it).
@@ -475,6 +477,7 @@ struct Stage {
   }
 };
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // ---- forward
@@ -484,7 +487,9 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   using St = Stage<T, LW>;
   constexpr int kR = St::kR, CW = St::CW, ROWS = St::ROWS, GROUPS = 32 / LW;
   __shared__ __align__(16) ScanShared<T, LW> s;
-  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks;
+  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks[2];
+  launch_dependents();
+  grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % cluster), chain = (int)(blockIdx.x / cluster);
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
@@ -507,105 +512,144 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     return;
   }
   extern __shared__ __align__(16) uint8_t raw[];
-  T* stage = reinterpret_cast<T*>(raw);  // [2][x, g]
-  const auto fetch = [&](int t, int buf) {
-    T* to = stage + buf * 2 * St::ELEMS;
-    if (t < tiles) {
+  T* stage = reinterpret_cast<T*>(raw);  // [3][x, g]
+  const int rounds = ret_pieces(tiles, cluster);
+  const auto fetch = [&](int i) {  // the block's tile of round i
+    const int t = i * cluster + rank;
+    T* to = stage + i % 3 * 2 * St::ELEMS;
+    if (i < rounds && t < tiles) {
       St::fetch(to, x, p.x.sn, (long long)t * ROWS, lo, hi, c0, p.D);
       St::fetch(to + St::ELEMS, g, p.g.sn, (long long)t * ROWS, lo, hi, c0, p.D);
     }
     copies_commit();
   };
-  fetch(rank, 0);
-  if (cluster > 1) cg::this_cluster().sync();
-  int par = 0;
-  for (int t0 = 0; t0 < tiles; t0 += cluster, par ^= 1) {
-    const int t = t0 + rank, row0 = (int)min((long long)t * ROWS, (long long)p.N);
-    copies_wait0();
-    if (PACKED)
-      mark_rows<kR>(p, row0, marks);
-    else
-      tile_sync();  // (the tile is there, the other buffer has been read)
-    fetch(t + cluster, par ^ 1);
-    const Marks m = PACKED ? packed_marks<kR>(marks, r0 / kR, row0 + r0, lo, hi) : dense_marks<kR>(row0 + r0, hi);
-    const unsigned first = m.first;
-    const T *sx = stage + par * 2 * St::ELEMS + St::at(r0) + cl, *sg = sx + St::ELEMS;
-    float2 a[kR][P], b[kR][P];
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      float2 gv[P], xv[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
-      unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const Gate k = gate_of<T, GATE>(gv[i]);
-        a[r][i] = k.a;
-        b[r][i] = input_of<GATE>(xv[i], k.rest);
-      }
-    }
-    if (m.live != (1u << kR) - 1) {
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-        if (!(m.live >> r & 1)) {
-          fill(a[r], 1.f);
-          fill(b[r], 0.f);
-        }
-    }
-    if (first != 0) {
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-        if (first >> r & 1) {
-          const int seq = PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch;
-          const int slot = p.load && on ? slot_of(p.slots, p.n_slots, seq) : -1;
-          float2 h[P];
-          if (slot >= 0) load_f(p.states + (long long)slot * p.D + c, h);
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            if (slot >= 0) b[r][i] = fma2(a[r][i], h[i], b[r][i]);
-            if (PACKED) a[r][i] = both(kCut);  // (dense: nothing comes before)
-          }
-        }
-    }
-    float2 A[P], B[P], wA[P], wB[P];
+  // a and b of the thread's row r
+  const auto row_of = [&](const T* sx, int r, float2 (&a)[P], float2 (&b)[P]) {
+    float2 gv[P], xv[P];
+    unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
+    unpack<T>(*reinterpret_cast<const Raw*>(sx + St::ELEMS + r * CW), gv);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      A[i] = a[0][i];
-      B[i] = b[0][i];
+      const Gate k = gate_of<T, GATE>(gv[i]);
+      a[i] = k.a;
+      b[i] = input_of<GATE>(xv[i], k.rest);
+    }
+  };
+  // The start of the sequence whose first token is row `row`.
+  const auto start_of = [&](int row, float2 (&h)[P]) {
+    fill(h, 0.f);
+    const int slot = slot_of(p.slots, p.n_slots, PACKED ? sequence_of(p.cu, p.B, row) : batch);
+    if (slot >= 0) load_f(p.states + (long long)slot * p.D + c, h);
+  };
+  // What is known of a tile before the state that enters it.
+  struct Ahead {
+    Marks m;
+    int row;                 // the thread's first
+    float2 A[P], B[P];       // of the row groups of the warp before the thread's
+    float2 h0[P];            // the start of the last sequence that begins in the thread's rows: its slot may be written (by
+  };                         // the thread with its last token) before the rows are run once more; the others' are not
+  // (whole block; the tile of round i has landed for every thread)
+  const auto look = [&](int i, Ahead& n) {
+    const int par = i & 1, row0 = (int)min(((long long)i * cluster + rank) * ROWS, (long long)p.N);
+    n.row = row0 + r0;
+    n.m = PACKED ? packed_marks<kR>(marks[par], r0 / kR, n.row, lo, hi) : dense_marks<kR>(n.row, hi);
+    const T* sx = stage + i % 3 * 2 * St::ELEMS + St::at(r0) + cl;
+    float2 wA[P], wB[P];
+    fill(n.A, 1.f);
+    fill(n.B, 0.f);
+    const bool whole = n.m.live == (1u << kR) - 1;
 #pragma unroll
-      for (int r = 1; r < kR; ++r) {
-        if (PACKED && (first >> r & 1)) {
-          B[i] = b[r][i];
-          A[i] = both(kCut);
+    for (int r = 0; r < kR; ++r) {
+      float2 a[P], b[P];
+      row_of(sx, r, a, b);
+      if (p.load && on && n.m.first >> r & 1) {
+        start_of(n.row + r, n.h0);
+#pragma unroll
+        for (int k = 0; k < P; ++k) b[k] = fma2(a[k], n.h0[k], b[k]);
+      }
+      if (!whole && !(n.m.live >> r & 1)) continue;
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        if (PACKED && (n.m.first >> r & 1)) {
+          n.B[k] = b[k];
+          n.A[k] = both(kCut);
         } else {
-          B[i] = fma2(a[r][i], B[i], b[r][i]);
-          A[i] = mul2(A[i], a[r][i]);
+          n.B[k] = fma2(a[k], n.B[k], b[k]);
+          n.A[k] = mul2(n.A[k], a[k]);
         }
       }
     }
-    scan_warp<LW, false, PACKED>(A, B, wA, wB, lane);
+    scan_warp<LW, false, PACKED>(n.A, n.B, wA, wB, lane);
     if (lane / LW == GROUPS - 1) {
       store(&s.wa[par][warp][cl], wA);
       store(&s.wb[par][warp][cl], wB);
     }
-    exchange_wait(cluster > 1);
+  };
+  const auto row0_of = [&](int i) { return (int)min(((long long)i * cluster + rank) * ROWS, (long long)p.N); };
+  fetch(0);
+  fetch(1);
+  if (cluster > 1) cg::this_cluster().sync();
+  Ahead next;
+  if (PACKED) {
+    clear_marks(marks[0]);
+    clear_marks(marks[1]);
+    tile_sync();
+    set_marks<kR>(p, row0_of(0), marks[0]);
+    set_marks<kR>(p, row0_of(1), marks[1]);
+  }
+  copies_wait1();
+  tile_sync();
+  look(0, next);
+  give(0, cluster > 1);
+  for (int i = 0; i < rounds; ++i) {
+    const int par = i & 1;
+    const Ahead now = next;
+    if (i + 1 < rounds) {  // while the state that enters this tile is on its way, the next one
+      copies_wait0();
+      tile_sync();  // every thread's part of it is there, the buffer after it and this tile's marks have been read
+      fetch(i + 2);
+      if (PACKED) clear_marks(marks[par]);
+      look(i + 1, next);
+    }
+    give_wait(cluster > 1);
+    if (i + 1 < rounds) give(par ^ 1, cluster > 1);
+    if (PACKED && i + 2 < rounds) {
+      tile_sync();
+      set_marks<kR>(p, row0_of(i + 2), marks[par]);
+    }
+    carry_sync(par);
     float2 h[P];
     load_f(&s.carry[par][cl], h);
     over_warps<CW, false, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, h);
 #pragma unroll
-    for (int i = 0; i < P; ++i) h[i] = carry_on<PACKED>(A[i], B[i], h[i]);
-    const int row = row0 + r0;
+    for (int k = 0; k < P; ++k) h[k] = carry_on<PACKED>(now.A[k], now.B[k], h[k]);
+    const int row = now.row;
     if (p.kept != nullptr && on && row < p.N && row % kScanKept == 0)
       store(p.kept + ((long long)batch * kept_rows + row / kScanKept) * p.D + c, h);
+    const T* sx = stage + i % 3 * 2 * St::ELEMS + St::at(r0) + cl;
     T* py = y + row * p.y.sn;
-    const unsigned out = on ? m.live : 0, ends = p.states != nullptr && on ? m.last : 0;
+    const unsigned out = on ? now.m.live : 0, ends = p.states != nullptr && on ? now.m.last : 0;
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
+      float2 a[P], b[P];
+      row_of(sx, r, a, b);
+      if (p.load && on && now.m.first >> r & 1) {
+        float2 h0[P];
+        if (now.m.first >> r == 1) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) h[i] = PACKED && (first >> r & 1) ? b[r][i] : fma2(a[r][i], h[i], b[r][i]);
+          for (int k = 0; k < P; ++k) h0[k] = now.h0[k];
+        } else {
+          start_of(row + r, h0);
+        }
+#pragma unroll
+        for (int k = 0; k < P; ++k) b[k] = fma2(a[k], h0[k], b[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < P; ++k) h[k] = PACKED && (now.m.first >> r & 1) ? b[k] : fma2(a[k], h[k], b[k]);
       if (out >> r & 1) store(py, h);
       py = next_row(py, p.y.sn);
       if (ends >> r & 1) {
-        const int slot = slot_of(p.slots, p.n_slots, PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch);
+        const int slot = slot_of(p.slots, p.n_slots, PACKED ? sequence_of(p.cu, p.B, row + r) : batch);
         if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
       }
     }
@@ -625,7 +669,9 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
   static_assert((GROUPS * kR * PER) % kScanKept == 0 && kWarps % PER == 0, "a kept state at the first row of every PER warps");
   __shared__ __align__(16) ScanShared<T, LW> s;
   __shared__ __align__(16) float fwa[kWarps][CW], fwb[kWarps][CW];
-  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks;
+  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks[2];
+  launch_dependents();
+  grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)(blockIdx.x % cluster), chain = (int)(blockIdx.x / cluster);
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
@@ -672,6 +718,11 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     copies_commit();
   };
   fetch(tiles - 1 - rank, 0);
+  if (PACKED) {
+    clear_marks(marks[0]);
+    tile_sync();
+    set_marks<kR>(p, tiles - 1 - rank >= 0 ? (tiles - 1 - rank) * ROWS : p.N, marks[0]);
+  }
   if (cluster > 1) cg::this_cluster().sync();
   int par = 0;
   for (int t0 = 0; t0 < tiles; t0 += cluster, par ^= 1) {
@@ -683,13 +734,11 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     const int from = warp / PER * PER, krow = row0 + from * GROUPS * kR;
     if (on && krow < p.N) load_f(p.kept + ((long long)batch * kept_rows + krow / kScanKept) * p.D + c, h);
     copies_wait0();
-    if (PACKED)
-      mark_rows<kR>(p, row0, marks);
-    else
-      tile_sync();
+    tile_sync();
     fetch(t - cluster, par ^ 1);
+    if (PACKED) clear_marks(marks[par ^ 1]);
     const T *sx = stage + par * 3 * St::ELEMS + St::at(r0) + cl, *sg = sx + St::ELEMS, *sd = sg + St::ELEMS;
-    const Marks m = PACKED ? packed_marks<kR>(marks, r0 / kR, row0 + r0, lo, hi) : dense_marks<kR>(row0 + r0, hi);
+    const Marks m = PACKED ? packed_marks<kR>(marks[par], r0 / kR, row0 + r0, lo, hi) : dense_marks<kR>(row0 + r0, hi);
     const unsigned first = m.first, last = m.last;
     // the start of a sequence that begins in row r, the gradient behind one that ends there
     const auto start = [&](int r, float2 (&f)[P]) {
@@ -744,7 +793,13 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
       store(&s.wa[par][warp][cl], wA);
       store(&s.wb[par][warp][cl], wB);
     }
-    exchange_wait(cluster > 1);
+    give(par, cluster > 1);
+    if (PACKED && t0 + cluster < tiles) {
+      tile_sync();
+      set_marks<kR>(p, t - cluster >= 0 ? (t - cluster) * ROWS : p.N, marks[par ^ 1]);
+    }
+    give_wait(cluster > 1);
+    carry_sync(par);
     float2 k[P];
     load_f(&s.carry[par][cl], k);
     over_warps<CW, true, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, k);
@@ -817,6 +872,8 @@ template <typename T, int GATE>
 __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_constant__ ScanArgs p) {
   using Raw = typename Io<T, kStepPairs>::Raw;
   constexpr int P = kStepPairs, V = 2 * P;
+  launch_dependents();
+  grid_dependency_wait();
   const int runs = (p.D + 128 * V - 1) / (128 * V);
   const int b = (int)(blockIdx.x / runs), c = ((int)(blockIdx.x % runs) * 128 + threadIdx.x) * V;
   const bool on = c < p.D;
@@ -857,17 +914,19 @@ cudaError_t launch_scan(const ScanArgs& a, bool backward, cudaStream_t st) {
   const long long chains = (PACKED ? 1ll : a.B) * ((a.D + CW - 1) / CW);
   const int n = cluster_of(chains, ret_pieces(a.N, ROWS), ScanShared<T, LW>::MOST);
   if (chains * n > 0x7fffffffll) return cudaErrorInvalidValue;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim = {(unsigned)n, 1, 1};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)n, 1, 1};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(chains * n));
   cfg.blockDim = dim3(kBlock);
   cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = n > 1 ? 1 : 0;
+  cfg.attrs = at;
+  cfg.numAttrs = n > 1 ? 2 : 1;
   static SmemOptIn opt[2];
-  const int smem = 2 * (backward ? 3 : 2) * Stage<T, LW>::ELEMS * (int)sizeof(T);
+  const int smem = 6 * Stage<T, LW>::ELEMS * (int)sizeof(T);  // forward three tiles of two tensors, backward two of three
   cudaError_t e = opt[backward].ensure((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   cfg.dynamicSmemBytes = smem;
@@ -884,8 +943,8 @@ cudaError_t launch_gate(const ScanArgs& a, bool backward, cudaStream_t st) {
   const long long chains = (a.cu ? 1ll : a.B) * ((a.D + cw - 1) / cw);
   const bool narrow = chains * std::min(kWideCluster, ret_pieces(a.N, kThreads / WIDE * Tile<T>::R)) < kRetSms;
   if (a.cu != nullptr)
-    return narrow ? launch_scan<T, GATE, WIDE / 4, true>(a, backward, st) : launch_scan<T, GATE, WIDE, true>(a, backward, st);
-  return narrow ? launch_scan<T, GATE, WIDE / 4, false>(a, backward, st) : launch_scan<T, GATE, WIDE, false>(a, backward, st);
+    return narrow ? launch_scan<T, GATE, WIDE / 2, true>(a, backward, st) : launch_scan<T, GATE, WIDE, true>(a, backward, st);
+  return narrow ? launch_scan<T, GATE, WIDE / 2, false>(a, backward, st) : launch_scan<T, GATE, WIDE, false>(a, backward, st);
 }
 
 template <typename T>
@@ -900,9 +959,7 @@ cudaError_t launch_type(const ScanArgs& a, bool backward, cudaStream_t st) {
 template <typename T, int GATE>
 cudaError_t launch_step(const ScanArgs& a, cudaStream_t st) {
   const int run = 128 * 2 * kStepPairs;
-  gated_scan_step_kernel<T, GATE><<<(unsigned)((long long)a.B * ((a.D + run - 1) / run)), 128, 0, st>>>(a);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(gated_scan_step_kernel<T, GATE>, dim3((unsigned)((long long)a.B * ((a.D + run - 1) / run))), 128, 0, st, true, a);
 }
 
 template <typename T>

@@ -961,7 +961,7 @@ cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
     e = launch(tc_cross_query_kernel<D, F>, opt_q, (long long)a.qs.segs * a.H, Tc<D>::kThreads, QuerySmem<D>::kBytes, t, st);
   }
   if (e != cudaSuccess || a.ks.segs == 0) return e;
-  e = cross_join_launch(a, true, a.qs.segs > 0, st);
+  e = cross_join_launch(a, true, st);
   if (e != cudaSuccess) return e;
   if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v)) return cudaErrorInvalidValue;
   return launch(tc_cross_key_kernel<D, F>, opt_k, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, KeySmem<D>::kBytes, t, st);
