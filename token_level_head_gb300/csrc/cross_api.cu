@@ -17,10 +17,10 @@ namespace {
 struct Kind {
   int unit, slots;
 };
-Kind kind_of(int d, bool tc) { return tc ? Kind{128, 2 * kRetSms} : Kind{32, (d == 128 ? 2 : 6) * kRetSms}; }
+Kind kind_of(int d, bool tc) { return tc ? Kind{128, (d == 64 ? 2 : 1) * kRetSms} : Kind{32, (d == 128 ? 2 : 6) * kRetSms}; }
 
 // Reads (three blocks an SM on the tensor cores with d = 64) leave no parts, so their segments need no room.
-Kind read_kind(int d, bool tc) { return tc ? Kind{128, (d == 64 ? 3 : 2) * kRetSms} : Kind{64, (d == 128 ? 2 : 4) * kRetSms}; }
+Kind read_kind(int d, bool tc) { return tc ? Kind{128, (d == 64 ? 3 : 1) * kRetSms} : Kind{64, (d == 128 ? 2 : 4) * kRetSms}; }
 
 // The length of a segment: so many tokens that the blocks fill the SMs, and no fewer than a tile.
 int segment_length(const CrossSide& s, int heads, const Kind& k) {

@@ -42,7 +42,7 @@ struct Tc {
 
 struct Bars {
   uint64_t full[3];  // a tile's tensors landed (tx), by its buffer
-  uint64_t mma[2];   // MMA commits
+  uint64_t mma[3];   // MMA commits
   unsigned long long wait_ns;
   unsigned* status;
   uint32_t tbase;
@@ -264,10 +264,15 @@ __device__ __forceinline__ uint64_t along_cols(uint32_t tile, uint32_t atom, int
 }
 
 // ================================================================ states
-// K and V in two buffers (phi's high part is put over K), the middle and low parts in one more each.
+// Three stages of 64 tokens: K (phi's high part is put over it), its middle and low parts, V.  While the MMAs of a tile run
+// the warps take the next one's features and TMA brings the one after; one barrier of the block a tile.  (With tiles of 128
+// tokens, and room for one of them in parts, the features waited for the MMAs: 65,536 tokens of 4 heads, d = 128, 44 us.)
+constexpr int kSumT = 64;
 template <int D>
 struct SumSmem {
-  static constexpr int kK = 0, kV = 2 * Tc<D>::kTile, kMid = 4 * Tc<D>::kTile, kLo = 5 * Tc<D>::kTile, kBars = 6 * Tc<D>::kTile;
+  static constexpr int kPart = kSumT * D * 2;                                    // bytes of a tile of one tensor
+  static constexpr int kV = 0, kK = kPart, kMid = 2 * kPart, kLo = 3 * kPart, kStage = 4 * kPart;
+  static constexpr int kBars = 3 * kStage;
   static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
 };
 template <int D, int F>
@@ -276,6 +281,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   using M = SumSmem<D>;
   constexpr bool kExact = F == MHLA_PHI_RELU || F == MHLA_PHI_IDENTITY;  // phi(k) is a bf16 number
   constexpr uint32_t kColumns = 128;
+  constexpr int kSumAtom = kSumT * 128;
   extern __shared__ __align__(16) uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
@@ -283,39 +289,35 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
-  if (g.seq < 0) return finish<2>(b, kColumns, 0, 0, 0);
+  if (g.seq < 0) return finish<3>(b, kColumns, 0, 0, 0);
   const uint32_t tmem = b->tbase;
-  const int tiles = (g.len + kT - 1) / kT;
-  const int hh = h, bb = p.c.ks.cu == nullptr ? g.seq : 0;
-  int issued = 0, mmas = 0;
+  const int tiles = (g.len + kSumT - 1) / kSumT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
   const auto fetch = [&](int j) {  // one thread
-    uint64_t* bar = &b->full[j & 1];
-    mbar_arrive_expect_tx(bar, 2 * X::kTile);
-    load_tile<D>(sm + M::kK + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? hh : 0, p.a_b ? bb : 0, bar);
-    load_tile<D>(sm + M::kV + (j & 1) * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? hh : 0, p.b_b ? bb : 0, bar);
+    uint64_t* bar = &b->full[j % 3];
+    uint8_t* to = sm + j % 3 * M::kStage;
+    mbar_arrive_expect_tx(bar, 2 * M::kPart);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      tma_load_4d(to + M::kK + i * kSumAtom, &p.a, 64 * i, g.row0 + j * kSumT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+      tma_load_4d(to + M::kV + i * kSumAtom, &p.b, 64 * i, g.row0 + j * kSumT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
+    }
   };
-  if (tiles > 0) {
-    if (tid == 0) fetch(0);
-    issued = 1;
-  }
+  int issued = min(tiles, 2), mmas = 0;
+  if (tid == 0)
+    for (int j = 0; j < issued; ++j) fetch(j);
   constexpr int P = D / 8, ROWS = X::kThreads / P;  // pieces of a row, rows at a time
   const int pc = tid % P, r0 = tid / P;
   float2 z[4] = {};
   bool ok = true;
   for (int j = 0; j < tiles; ++j) {
-    if (j > 0) ok = wait(&b->mma[0], (j - 1) & 1, b);  // the other buffer, mid and lo have been read
-    if (ok && j + 1 < tiles) {
-      if (tid == 0) fetch(j + 1);
-      ++issued;
-    }
-    ok = ok && wait(&b->full[j & 1], (j >> 1) & 1, b);
-    uint8_t *kt = sm + M::kK + (j & 1) * X::kTile, *vt = sm + M::kV + (j & 1) * X::kTile;
-    const int n = g.len - j * kT;
+    uint8_t* st = sm + j % 3 * M::kStage;
+    ok = wait(&b->full[j % 3], (j / 3) & 1, b);
+    const int n = g.len - j * kSumT;
     if (ok) {
 #pragma unroll
-      for (int i = 0; i < kT / ROWS; ++i) {
+      for (int i = 0; i < kSumT / ROWS; ++i) {
         const int r = r0 + i * ROWS;
-        uint4* at = piece(kt, kT, r, pc);
+        uint4* at = piece(st + M::kK, kSumT, r, pc);
         float2 f[4];
         unpack8(*at, f);
 #pragma unroll
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
         if (r >= n) {  // behind the sequence: nothing of what lies there counts
 #pragma unroll
           for (int x = 0; x < 4; ++x) f[x] = both(0.f);
-          *piece(vt, kT, r, pc) = make_uint4(0, 0, 0, 0);
+          *piece(st + M::kV, kSumT, r, pc) = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) z[x] = add2(z[x], f[x]);
@@ -332,43 +334,48 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
         if (!kExact) {
           remainder8(f, hi);
           const uint4 mid = pack8(f);
-          *piece(sm + M::kMid, kT, r, pc) = mid;
+          *piece(st + M::kMid, kSumT, r, pc) = mid;
           remainder8(f, mid);
-          *piece(sm + M::kLo, kT, r, pc) = pack8(f);
+          *piece(st + M::kLo, kSumT, r, pc) = pack8(f);
         }
       }
     }
     fence_proxy_async_smem();
-    tc_fence_before();
     if (!__syncthreads_and(ok)) {
       ok = false;
       break;
     }
     if (tid == 0) {
       tc_fence_after();
-      const uint32_t ka = smem_u32(kt), va = smem_u32(vt), mid = smem_u32(sm + M::kMid), lo = smem_u32(sm + M::kLo);
-      // d = 64: A's rows 64 .. 127 are another tile's columns, whose results are not read; B = the high and the middle part
-      // side by side (N = 128), then the low part onto the middle one's columns
-      const uint64_t da = along_rows(va, D == 64 ? mid - va : kAtom);
+      const uint32_t va = smem_u32(st), ka = va + M::kK;
+      // d = 64: A's rows 64 .. 127 are another tile's columns (phi's, behind V), whose results are not read; B = the high and
+      // the middle part side by side (N = 128), then the low part onto the middle one's columns
+      static_assert(M::kK == M::kV + (D == 64 ? kSumAtom : 2 * kSumAtom), "what lies behind V");
+      const uint64_t da = along_rows(va, kSumAtom);
       if (D == 64 && !kExact) {
-        const uint64_t d1 = along_rows(ka, mid - ka), d2 = along_rows(lo, kAtom);
+        const uint64_t d1 = along_rows(ka, M::kPart), d2 = along_rows(va + M::kLo, kSumAtom);
 #pragma unroll
-        for (int s = 0; s < kT / 16; ++s) {
+        for (int s = 0; s < kSumT / 16; ++s) {
           mma_bf16(tmem, da + s * 128, d1 + s * 128, idesc_bf16_f32(128, 128, 1, 1), j > 0 || s > 0);
           mma_bf16(tmem + 64, da + s * 128, d2 + s * 128, idesc_bf16_f32(128, 64, 1, 1), true);
         }
       } else {
 #pragma unroll
         for (int part = 0; part < (kExact ? 1 : 3); ++part) {
-          const uint64_t db = along_rows(part == 0 ? ka : part == 1 ? mid : lo, kAtom);
+          const uint64_t db = along_rows(ka + part * M::kPart, kSumAtom);
 #pragma unroll
-          for (int s = 0; s < kT / 16; ++s)
+          for (int s = 0; s < kSumT / 16; ++s)
             mma_bf16(tmem, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
         }
       }
-      mma_commit(&b->mma[0]);
+      mma_commit(&b->mma[j % 3]);
+      ++mmas;
+      // the stage of tile j - 1 takes tile j + 2
+      if (j + 2 < tiles && (j == 0 || wait(&b->mma[(j - 1) % 3], ((j - 1) / 3) & 1, b))) {
+        fetch(j + 2);
+        ++issued;
+      }
     }
-    ++mmas;
   }
   float *so = nullptr, *zo = nullptr;
   if (cross_joined(p.c.ks) && g.nseg != 1) {
@@ -381,10 +388,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       zo = p.c.z + ((size_t)slot * p.c.Hk + h) * D;
     }
   }
-  if (ok && tiles > 0) ok = wait(&b->mma[0], (tiles - 1) & 1, b);
+  for (int j = max(tiles - 3, 0); ok && j < tiles; ++j) ok = wait(&b->mma[j % 3], (j / 3) & 1, b);
   if (__syncthreads_and(ok)) {
     tc_fence_after();
-    float* zp = reinterpret_cast<float*>(sm + M::kMid);  // [ROWS][D]
+    float* zp = reinterpret_cast<float*>(sm);  // [ROWS][D]: the stages have been read
 #pragma unroll
     for (int x = 0; x < 4; ++x) *reinterpret_cast<float2*>(zp + r0 * D + 8 * pc + 2 * x) = z[x];
     __syncthreads();
@@ -417,7 +424,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       }
     }
   }
-  finish<2>(b, kColumns, issued, mmas, 0);
+  if (tid == 0 && aborted(&b->abort))
+    for (int j = max(mmas - 3, 0); j < mmas; ++j) drain(&b->mma[j % 3], (j / 3) & 1);
+  finish<3>(b, kColumns, issued, 0, 0);
 }
 
 // ================================================================ read
@@ -904,14 +913,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // A token tensor as [batch][head][row][d]; a dimension of stride 0 has one entry.  Rows behind the tensor read as zeros.
-bool make_map(CUtensorMap* m, const RetTensor& t, const CrossSide& s, int heads, int d) {
+bool make_map(CUtensorMap* m, const RetTensor& t, const CrossSide& s, int heads, int d, int box_rows) {
   auto enc = encoder();
   if (!enc) return false;
   const cuuint64_t row_bytes = t.sn ? (cuuint64_t)t.sn * 2 : (cuuint64_t)d * 2;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)s.N, t.sh ? (cuuint64_t)heads : 1,
                               t.sb && s.cu == nullptr ? (cuuint64_t)s.B : 1};
   const cuuint64_t strides[3] = {row_bytes, t.sh ? (cuuint64_t)t.sh * 2 : row_bytes, t.sb ? (cuuint64_t)t.sb * 2 : row_bytes};
-  const cuuint32_t box[4] = {64, (cuuint32_t)kT, 1, 1}, es[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, es[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.p), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -920,14 +929,15 @@ bool make_map(CUtensorMap* m, const RetTensor& t, const CrossSide& s, int heads,
 unsigned long long g_wait_ns = kWaitNs;
 
 // The launch's arguments, with the maps of the tile's one or two tensors.
-bool make_args(TcArgs* t, const CrossArgs& a, const CrossSide& s, int heads, const RetTensor& x, const RetTensor* y) {
+bool make_args(TcArgs* t, const CrossArgs& a, const CrossSide& s, int heads, const RetTensor& x, const RetTensor* y,
+               int box_rows = kT) {
   t->c = a;
   t->wait_ns = g_wait_ns;
   t->a_h = x.sh != 0;
   t->a_b = x.sb != 0 && s.cu == nullptr;
   t->b_h = y != nullptr && y->sh != 0;
   t->b_b = y != nullptr && y->sb != 0 && s.cu == nullptr;
-  return make_map(&t->a, x, s, heads, a.d) && (y == nullptr || make_map(&t->b, *y, s, heads, a.d));
+  return make_map(&t->a, x, s, heads, a.d, box_rows) && (y == nullptr || make_map(&t->b, *y, s, heads, a.d, box_rows));
 }
 
 cudaError_t launch(void (*kernel)(TcArgs), SmemOptIn& opt, long long blocks, int threads, int smem, const TcArgs& t,
@@ -940,7 +950,7 @@ cudaError_t launch(void (*kernel)(TcArgs), SmemOptIn& opt, long long blocks, int
 template <int D, int F>
 cudaError_t states_t(const CrossArgs& a, cudaStream_t st) {
   TcArgs t;
-  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v)) return cudaErrorInvalidValue;
+  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v, kSumT)) return cudaErrorInvalidValue;
   static SmemOptIn opt;
   return launch(tc_cross_states_kernel<D, F>, opt, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, SumSmem<D>::kBytes, t, st);
 }
