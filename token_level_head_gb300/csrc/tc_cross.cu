@@ -36,18 +36,22 @@ template <int D>
 struct Tc {
   static constexpr int kTile = kT * D * 2;    // bytes of a tile of tokens
   static constexpr int kMat = D * D * 2;      // of a d x d matrix
-  static constexpr int kThreads = 4 * D;      // a row 32 columns a thread
+  static constexpr int kWork = 4 * D;         // threads that take features and results: a row 32 columns a thread
+  static constexpr int kThreads = kWork + 32; // and a warp that issues the copies and the MMAs
   static constexpr int kCols = D / 32;        // threads of a row
 };
 
 struct Bars {
-  uint64_t full[3];  // a tile's tensors landed (tx), by its buffer
-  uint64_t mma[3];   // MMA commits
+  uint64_t full[3];   // a tile's tensors landed (tx), by its buffer
+  uint64_t ready[3];  // a tile's operands are written (the working warps)
+  uint64_t mma[3];    // MMA commits
+  uint64_t ready2, mma2;
   unsigned long long wait_ns;
   unsigned* status;
   uint32_t tbase;
   int abort;
   int scratch;
+  int issued, mmas, mmas2;  // by the issuing thread: tiles copied, commits (for the wind-down)
 };
 
 struct TcArgs {
@@ -168,6 +172,10 @@ __device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
   if (threadIdx.x == 0) {
     for (uint64_t& f : b->full) mbar_init(&f, 1);
     for (uint64_t& m : b->mma) mbar_init(&m, 1);
+    for (uint64_t& r : b->ready) mbar_init(&r, blockDim.x / 32 - 1);
+    mbar_init(&b->ready2, blockDim.x / 32 - 1);
+    mbar_init(&b->mma2, 1);
+    b->issued = b->mmas = b->mmas2 = 0;
     b->abort = 0;
     b->wait_ns = p.wait_ns;
     b->status = p.c.status;
@@ -183,35 +191,44 @@ __device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
   tc_fence_after();
   grid_dependency_wait();
 }
+// A working warp has written its part of a tile's operands (and read what the next MMAs overwrite).
+__device__ __forceinline__ void arrive(uint64_t* bar, int lane) {
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
 // The end of a block: after an abort (one thread) short waits for the copies and MMAs in flight; then the columns are
-// freed.  issued: tiles whose copies were issued, into NB buffers in turn; mmas, mmas2: commits on the two barriers.
-template <int NB>
-__device__ __forceinline__ void finish(Bars* b, uint32_t cols, int issued, int mmas, int mmas2) {
+// freed.  NB: buffers that the copies went to in turn, NM: barriers that the commits did.
+template <int NB, int NM>
+__device__ __forceinline__ void finish(Bars* b, uint32_t cols) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0 && aborted(&b->abort)) {
-    for (int j = max(issued - NB, 0); j < issued; ++j) drain(&b->full[j % NB], (j / NB) & 1);
-    if (mmas > 0) drain(&b->mma[0], (mmas - 1) & 1);
-    if (mmas2 > 0) drain(&b->mma[1], (mmas2 - 1) & 1);
+    for (int j = max(b->issued - NB, 0); j < b->issued; ++j) drain(&b->full[j % NB], (j / NB) & 1);
+    for (int j = max(b->mmas - NM, 0); j < b->mmas; ++j) drain(&b->mma[j % NM], (j / NM) & 1);
+    if (b->mmas2 > 0) drain(&b->mma2, (b->mmas2 - 1) & 1);
     atomicOr(b->status, 1u);
   }
   __syncthreads();
   if (threadIdx.x < 32) tmem_dealloc(b->tbase, cols);
 }
 
-// One thread: a tile of one tensor (two atoms for d = 128).
-template <int D>
+// One thread: a tile of one tensor (its atoms of 64 columns one behind the other).
 __device__ __forceinline__ void load_tile(uint8_t* to, const CUtensorMap* m, int row, int h, int b, uint64_t* bar) {
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) tma_load_4d(to + i * kAtom, m, 64 * i, row, h, b, bar);
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(smem_u32(to)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(row), "r"(h), "r"(b), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // A d x d fp32 matrix [r][c] as bf16 tiles of D rows, the high part and, where lo is given, the low part.
 template <int D>
 __device__ __forceinline__ void load_matrix(uint8_t* hi, uint8_t* lo, const float* from) {
 #pragma unroll
-  for (int i = threadIdx.x; i < D * D / 8; i += Tc<D>::kThreads) {
+  for (int i = threadIdx.x; i < D * D / 8; i += Tc<D>::kWork) {
     const int r = i / (D / 8), j = i % (D / 8);
     float2 f[4];
     load8(from + r * D + 8 * j, f);
@@ -280,7 +297,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   using X = Tc<D>;
   using M = SumSmem<D>;
   constexpr bool kExact = F == MHLA_PHI_RELU || F == MHLA_PHI_IDENTITY;  // phi(k) is a bf16 number
-  constexpr uint32_t kColumns = 128;
+  constexpr uint32_t kColumns = 2 * D;
   constexpr int kSumAtom = kSumT * 128;
   extern __shared__ __align__(16) uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
@@ -289,31 +306,52 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
-  if (g.seq < 0) return finish<3>(b, kColumns, 0, 0, 0);
+  if (g.seq < 0) return finish<3, 3>(b, kColumns);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kSumT - 1) / kSumT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
-  const auto fetch = [&](int j) {  // one thread
-    uint64_t* bar = &b->full[j % 3];
-    uint8_t* to = sm + j % 3 * M::kStage;
-    mbar_arrive_expect_tx(bar, 2 * M::kPart);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      tma_load_4d(to + M::kK + i * kSumAtom, &p.a, 64 * i, g.row0 + j * kSumT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
-      tma_load_4d(to + M::kV + i * kSumAtom, &p.b, 64 * i, g.row0 + j * kSumT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
-    }
-  };
-  int issued = min(tiles, 2), mmas = 0;
-  if (tid == 0)
-    for (int j = 0; j < issued; ++j) fetch(j);
-  constexpr int P = D / 8, ROWS = X::kThreads / P;  // pieces of a row, rows at a time
+  constexpr int P = D / 8, ROWS = X::kWork / P;  // pieces of a row, rows at a time
   const int pc = tid % P, r0 = tid / P;
   float2 z[4] = {};
   bool ok = true;
-  for (int j = 0; j < tiles; ++j) {
-    uint8_t* st = sm + j % 3 * M::kStage;
-    ok = wait(&b->full[j % 3], (j / 3) & 1, b);
-    const int n = g.len - j * kSumT;
-    if (ok) {
+  if (tid >= X::kWork) {
+    if (lane == 0) {
+      const auto fetch = [&](int j) {
+        uint64_t* bar = &b->full[j % 3];
+        uint8_t* to = sm + j % 3 * M::kStage;
+        mbar_arrive_expect_tx(bar, 2 * M::kPart);
+        load_tile(to + M::kK, &p.a, g.row0 + j * kSumT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+        load_tile(to + M::kV, &p.b, g.row0 + j * kSumT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
+        b->issued = j + 1;
+      };
+      for (int j = 0; j < min(tiles, 3); ++j) fetch(j);
+      for (int j = 0; j < tiles; ++j) {
+        if (!wait(&b->ready[j % 3], (j / 3) & 1, b)) break;
+        tc_fence_after();
+        const uint32_t va = smem_u32(sm + j % 3 * M::kStage), ka = va + M::kK;
+        // A = v.  d = 64: its rows 64 .. 127 are another tile's columns (phi's, behind V), whose results are not read.
+        // B = the high and the middle part side by side, then the low part onto the middle one's columns.
+        static_assert(M::kK == M::kV + D / 64 * kSumAtom, "what lies behind V");
+        const uint64_t da = along_rows(va, kSumAtom), d1 = along_rows(ka, kSumAtom), d2 = along_rows(va + M::kLo, kSumAtom);
+#pragma unroll
+        for (int s = 0; s < kSumT / 16; ++s) {
+          mma_bf16(tmem, da + s * 128, d1 + s * 128, idesc_bf16_f32(128, kExact ? D : 2 * D, 1, 1), j > 0 || s > 0);
+          if (!kExact) mma_bf16(tmem + D, da + s * 128, d2 + s * 128, idesc_bf16_f32(128, D, 1, 1), true);
+        }
+        mma_commit(&b->mma[j % 3]);
+        b->mmas = j + 1;
+        if (j > 0 && j + 2 < tiles) {  // the stage of tile j - 1 takes tile j + 2
+          if (!wait(&b->mma[(j - 1) % 3], ((j - 1) / 3) & 1, b)) break;
+          fetch(j + 2);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    for (int j = 0; ok && j < tiles; ++j) {
+      uint8_t* st = sm + j % 3 * M::kStage;
+      ok = __all_sync(0xffffffffu, wait(&b->full[j % 3], (j / 3) & 1, b));
+      if (!ok) break;
+      const int n = g.len - j * kSumT;
 #pragma unroll
       for (int i = 0; i < kSumT / ROWS; ++i) {
         const int r = r0 + i * ROWS;
@@ -339,43 +377,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
           *piece(st + M::kLo, kSumT, r, pc) = pack8(f);
         }
       }
+      arrive(&b->ready[j % 3], lane);
     }
-    fence_proxy_async_smem();
-    if (!__syncthreads_and(ok)) {
-      ok = false;
-      break;
-    }
-    if (tid == 0) {
-      tc_fence_after();
-      const uint32_t va = smem_u32(st), ka = va + M::kK;
-      // d = 64: A's rows 64 .. 127 are another tile's columns (phi's, behind V), whose results are not read; B = the high and
-      // the middle part side by side (N = 128), then the low part onto the middle one's columns
-      static_assert(M::kK == M::kV + (D == 64 ? kSumAtom : 2 * kSumAtom), "what lies behind V");
-      const uint64_t da = along_rows(va, kSumAtom);
-      if (D == 64 && !kExact) {
-        const uint64_t d1 = along_rows(ka, M::kPart), d2 = along_rows(va + M::kLo, kSumAtom);
-#pragma unroll
-        for (int s = 0; s < kSumT / 16; ++s) {
-          mma_bf16(tmem, da + s * 128, d1 + s * 128, idesc_bf16_f32(128, 128, 1, 1), j > 0 || s > 0);
-          mma_bf16(tmem + 64, da + s * 128, d2 + s * 128, idesc_bf16_f32(128, 64, 1, 1), true);
-        }
-      } else {
-#pragma unroll
-        for (int part = 0; part < (kExact ? 1 : 3); ++part) {
-          const uint64_t db = along_rows(ka + part * M::kPart, kSumAtom);
-#pragma unroll
-          for (int s = 0; s < kSumT / 16; ++s)
-            mma_bf16(tmem, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
-        }
-      }
-      mma_commit(&b->mma[j % 3]);
-      ++mmas;
-      // the stage of tile j - 1 takes tile j + 2
-      if (j + 2 < tiles && (j == 0 || wait(&b->mma[(j - 1) % 3], ((j - 1) / 3) & 1, b))) {
-        fetch(j + 2);
-        ++issued;
-      }
-    }
+    if (ok && tiles > 0) ok = wait(&b->mma[(tiles - 1) % 3], ((tiles - 1) / 3) & 1, b);  // (and all MMAs before it)
   }
   float *so = nullptr, *zo = nullptr;
   if (cross_joined(p.c.ks) && g.nseg != 1) {
@@ -388,14 +392,14 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       zo = p.c.z + ((size_t)slot * p.c.Hk + h) * D;
     }
   }
-  for (int j = max(tiles - 3, 0); ok && j < tiles; ++j) ok = wait(&b->mma[j % 3], (j / 3) & 1, b);
-  if (__syncthreads_and(ok)) {
+  if (__syncthreads_and(ok && !aborted(&b->abort))) {
     tc_fence_after();
     float* zp = reinterpret_cast<float*>(sm);  // [ROWS][D]: the stages have been read
+    if (tid < X::kWork)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) *reinterpret_cast<float2*>(zp + r0 * D + 8 * pc + 2 * x) = z[x];
+      for (int x = 0; x < 4; ++x) *reinterpret_cast<float2*>(zp + r0 * D + 8 * pc + 2 * x) = z[x];
     __syncthreads();
-    if (zo != nullptr) {
+    if (zo != nullptr && tid < X::kWork) {
       if (tid < D) {
         float s = 0.f;
 #pragma unroll 8
@@ -409,10 +413,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
         if (tiles > 0) {
           tmem_ld16(at, v);
           tmem_ld16(at + 16, v + 16);
-          if (D == 64 && !kExact) {
+          if (!kExact) {
             float w[32];
-            tmem_ld16(at + 64, w);
-            tmem_ld16(at + 80, w + 16);
+            tmem_ld16(at + D, w);
+            tmem_ld16(at + D + 16, w + 16);
             tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] += w[x];
@@ -424,9 +428,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       }
     }
   }
-  if (tid == 0 && aborted(&b->abort))
-    for (int j = max(mmas - 3, 0); j < mmas; ++j) drain(&b->mma[j % 3], (j / 3) & 1);
-  finish<3>(b, kColumns, issued, 0, 0);
+  finish<3, 3>(b, kColumns);
 }
 
 // ================================================================ read
@@ -451,75 +453,79 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
   const int slot = g.seq < 0 ? -1 : p.c.slots != nullptr ? p.c.slots[g.seq] : g.seq;
-  if (slot < 0 || slot >= p.c.n_slots) return finish<3>(b, kColumns, 0, 0, 0);
+  if (slot < 0 || slot >= p.c.n_slots) return finish<3, 2>(b, kColumns);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
-  const auto fetch = [&](int j) {
-    uint64_t* bar = &b->full[j % 3];
-    mbar_arrive_expect_tx(bar, X::kTile);
-    load_tile<D>(sm + M::kQ + j % 3 * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
-  };
-  int issued = min(tiles, 3), mmas = 0;
-  if (tid == 0)
-    for (int j = 0; j < issued; ++j) fetch(j);
   const size_t unit = (size_t)slot * p.c.Hk + h / (p.c.H / p.c.Hk);
-  load_matrix<D>(sm + M::kS, nullptr, p.c.S + unit * D * D);
+  if (tid < X::kWork) load_matrix<D>(sm + M::kS, nullptr, p.c.S + unit * D * D);
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
-  __syncthreads();
-  const Places pl = places(warp, lane);
-  const int row = pl.row, cg = warp >> 2;  // the thread's row, and its 32 columns
-  const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
-  const uint32_t sa = smem_u32(sm + M::kS);
-  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.y.p)) + cross_base(p.c.qs, p.c.y, g.seq, h) +
-                     (long long)g.row0 * p.c.y.sn + pl.out_col;
-  bool ok = true;
-  for (int j = 0; j <= tiles; ++j) {
-    if (j < tiles) {  // the features of tile j
-      uint8_t* qt = sm + M::kQ + j % 3 * X::kTile;
-      ok = wait(&b->full[j % 3], (j / 3) & 1, b);
-      if (ok) {
-        float2 d = both(0.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4* q = &at_byte(qt, pl.own[i]);
-          float2 f[4], zz[4];
-          unpack8(*q, f);
-          load8(z + cg * 32 + 8 * i, zz);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            f[x] = feature<F>(f[x]);
-            d = fma2(f[x], zz[x], d);
-          }
-          if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
-        }
-        den[(j % 3 * X::kCols + cg) * kT + row] = d.x + d.y;
-      }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (!__syncthreads_and(ok)) {
-      ok = false;
-      break;
-    }
-    tc_fence_after();
-    if (j < tiles) {
-      if (tid == 0) {
+  if (tid >= X::kWork) {
+    if (lane == 0) {
+      const auto fetch = [&](int j) {
+        uint64_t* bar = &b->full[j % 3];
+        mbar_arrive_expect_tx(bar, X::kTile);
+        load_tile(sm + M::kQ + j % 3 * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+        b->issued = j + 1;
+      };
+      const uint32_t sa = smem_u32(sm + M::kS);
+      for (int j = 0; j < min(tiles, 3); ++j) fetch(j);
+      for (int j = 0; j < tiles; ++j) {
+        // every warp has the features of tile j (the first time: S) written, and tile j - 2 stored
+        if (!wait(&b->ready[j % 3], (j / 3) & 1, b)) break;
+        tc_fence_after();
         const uint32_t qa = smem_u32(sm + M::kQ + j % 3 * X::kTile);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
           mma_bf16(tmem + (j & 1) * D, along_cols<D>(qa, kAtom, s), along_rows(sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1),
                    s > 0);
         mma_commit(&b->mma[j & 1]);
+        b->mmas = j + 1;
+        if (j >= 2 && j + 1 < tiles) fetch(j + 1);
       }
-      ++mmas;
     }
-    if (j >= 2 && j + 1 < tiles) {  // tile j - 2 has been stored: its buffer takes tile j + 1
-      if (tid == 0) fetch(j + 1);
-      ++issued;
+    __syncwarp();
+    __syncthreads();
+    return finish<3, 2>(b, kColumns);
+  }
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(X::kWork) : "memory");  // z
+  const Places pl = places(warp, lane);
+  const int row = pl.row, cg = warp >> 2;  // the thread's row, and its 32 columns
+  const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.y.p)) + cross_base(p.c.qs, p.c.y, g.seq, h) +
+                     (long long)g.row0 * p.c.y.sn + pl.out_col;
+  bool ok = true;
+  for (int j = 0; ok && j <= tiles; ++j) {
+    if (j < tiles) {  // the features of tile j
+      uint8_t* qt = sm + M::kQ + j % 3 * X::kTile;
+      ok = __all_sync(0xffffffffu, wait(&b->full[j % 3], (j / 3) & 1, b));
+      if (!ok) break;
+      float2 d = both(0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4* q = &at_byte(qt, pl.own[i]);
+        float2 f[4], zz[4];
+        unpack8(*q, f);
+        load8(z + cg * 32 + 8 * i, zz);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          f[x] = feature<F>(f[x]);
+          d = fma2(f[x], zz[x], d);
+        }
+        if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
+      }
+      den[(j % 3 * X::kCols + cg) * kT + row] = d.x + d.y;
+      arrive(&b->ready[j % 3], lane);
     }
     if (j > 0) {  // tile j - 1 goes out
       const int t = j - 1;
       uint8_t* qt = sm + M::kQ + t % 3 * X::kTile;
+      ok = __all_sync(0xffffffffu, wait(&b->mma[t & 1], (t >> 1) & 1, b));
+      if (!ok) break;
+      tc_fence_after();
+      float2 v[16];
+      tmem_ld8(at + (t & 1) * D, v);
+      tmem_ld8(at + (t & 1) * D + 16, v + 8);
       float inv = 1.f;
       if (p.c.normalise) {
         float d = p.c.eps;
@@ -527,23 +533,17 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
         for (int i = 0; i < X::kCols; ++i) d += den[(t % 3 * X::kCols + i) * kT + row];
         inv = inverse(d);
       }
-      ok = __all_sync(0xffffffffu, wait(&b->mma[t & 1], (t >> 1) & 1, b));
-      if (ok) {
-        tc_fence_after();
-        float2 v[16];
-        tmem_ld8(at + (t & 1) * D, v);
-        tmem_ld8(at + (t & 1) * D + 16, v + 8);
-        tmem_ld_wait();
+      tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], both(inv));
+      for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], both(inv));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) at_byte(qt, pl.own[i]) = pack8(v + 4 * i);
-        __syncwarp();
-        store_rows(qt, pl, y + (long long)t * kT * p.c.y.sn, p.c.y.sn, g.len - t * kT);
-      }
+      for (int i = 0; i < 4; ++i) at_byte(qt, pl.own[i]) = pack8(v + 4 * i);
+      __syncwarp();
+      store_rows(qt, pl, y + (long long)t * kT * p.c.y.sn, p.c.y.sn, g.len - t * kT);
     }
   }
-  finish<3>(b, kColumns, issued, (mmas + 1) / 2, mmas / 2);
+  __syncthreads();
+  finish<3, 2>(b, kColumns);
 }
 
 // ================================================================ backward over the queries
@@ -556,6 +556,8 @@ struct QuerySmem {
   static constexpr int kBytes = (kSmall + 1023) / 1024 * 1024 + kEnd;
   static_assert(kBytes <= 232448 / (D == 64 ? 2 : 1), "two blocks of d = 64 an SM, one of d = 128");
 };
+// All of the n threads of the warps that share 32 rows, or none; what they wrote before is there.
+__device__ __forceinline__ bool row_and(bool ok, int warp, int n) { return group_and(1 + (warp & 3), n, ok); }
 // 32 values a lane: the sum of value i over the warp, for lane i.
 __device__ __forceinline__ float sum_turned(float (&v)[32], int lane) {
 #pragma unroll
@@ -586,84 +588,105 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
   const int h = blockIdx.x % p.c.H, k = blockIdx.x / p.c.H;
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
-  if (g.seq < 0) return finish<2>(b, kColumns, 0, 0, 0);
+  if (g.seq < 0) return finish<2, 1>(b, kColumns);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
-  const auto fetch = [&](int j) {
-    uint64_t* bar = &b->full[j & 1];
-    mbar_arrive_expect_tx(bar, 2 * X::kTile);
-    load_tile<D>(sm + M::kQ + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
-    load_tile<D>(sm + M::kY + (j & 1) * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
-  };
-  int issued = min(tiles, 2), mmas = 0, mmas2 = 0;
-  if (tid == 0)
-    for (int j = 0; j < issued; ++j) fetch(j);
   const size_t unit = (size_t)g.seq * p.c.Hk + h / (p.c.H / p.c.Hk);
-  load_matrix<D>(sm + M::kS, sm + M::kSLo, p.c.S + unit * D * D);
+  if (tid < X::kWork) load_matrix<D>(sm + M::kS, sm + M::kSLo, p.c.S + unit * D * D);
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
-  fence_proxy_async_smem();
-  __syncthreads();
+  if (tid >= X::kWork) {
+    if (lane == 0) {
+      const auto fetch = [&](int j) {
+        uint64_t* bar = &b->full[j & 1];
+        mbar_arrive_expect_tx(bar, 2 * X::kTile);
+        load_tile(sm + M::kQ + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+        load_tile(sm + M::kY + (j & 1) * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
+        b->issued = j + 1;
+      };
+      const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo), wl = smem_u32(sm + M::kLo);
+      if (tiles > 0) fetch(0);
+      for (int j = 0; j < tiles; ++j) {
+        const uint32_t qa = smem_u32(sm + M::kQ + (j & 1) * X::kTile), ya = smem_u32(sm + M::kY + (j & 1) * X::kTile);
+        // every warp has the tile before stored (the first time: S written), and rows without a token cleared
+        if (!wait(&b->ready[0], j & 1, b)) break;
+        tc_fence_after();
+        // u = dy S^T
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_bf16(tmem, along_cols<D>(ya, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s), idesc_bf16_f32(128, D, 0, 0),
+                     s > 0 || part > 0);
+        mma_commit(&b->mma[0]);
+        b->mmas = j + 1;
+        if (j + 1 < tiles) fetch(j + 1);
+        if (!wait(&b->ready2, j & 1, b)) break;
+        tc_fence_after();
+        // dS^T += dy^T w  (d = 64: A's rows 64 .. 127 are another tile's columns, whose results are not read)
+        const uint64_t da = along_rows(ya, D == 64 ? wl - ya : kAtom);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint64_t db = along_rows(part ? wl : qa, kAtom);
+#pragma unroll
+          for (int s = 0; s < kT / 16; ++s)
+            mma_bf16(tmem + D, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
+        }
+        mma_commit(&b->mma2);
+        b->mmas2 = j + 1;
+      }
+    }
+    __syncwarp();
+    __syncthreads_and(true);  // (the two barriers of the other warps' end)
+    __syncthreads();
+    return finish<2, 1>(b, kColumns);
+  }
+  __syncwarp();
+  asm volatile("bar.sync 5, %0;" ::"n"(X::kWork) : "memory");  // z
   const Places pl = places(warp, lane);
   const int row = pl.row, cg = warp >> 2;
+  const auto row_sync = [&] { named_bar(1 + (warp & 3), X::kWork / 4); };  // the warps that share 32 rows
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
-  const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo), wl = smem_u32(sm + M::kLo);
   __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dq.p)) + cross_base(p.c.qs, p.c.dq, g.seq, h) +
                       (long long)g.row0 * p.c.dq.sn + pl.out_col;
   float2 dz[16] = {};  // of the thread's 32 columns, over its rows
-  const auto multiply_u = [&](const uint8_t* yt) {  // one thread: u = dy S^T
-    const uint32_t ya = smem_u32(yt);
-#pragma unroll
-    for (int part = 0; part < 2; ++part)
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        mma_bf16(tmem, along_cols<D>(ya, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s), idesc_bf16_f32(128, D, 0, 0),
-                 s > 0 || part > 0);
-    mma_commit(&b->mma[0]);
-  };
   bool ok = true;
   for (int j = 0; j < tiles; ++j) {
     uint8_t *qt = sm + M::kQ + (j & 1) * X::kTile, *yt = sm + M::kY + (j & 1) * X::kTile;
     const int n = g.len - j * kT;
-    const bool live = row < n, whole = n >= kT;
-    float2 f[16];
+    const bool live = row < n;
     ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
-    if (ok) {
-      if (whole && tid == 0) multiply_u(yt);
-      float2 d = both(0.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        unpack8(at_byte(qt, pl.own[i]), f + 4 * i);
-        if (!live) at_byte(yt, pl.own[i]) = make_uint4(0, 0, 0, 0);
-        float2 zz[4];
-        load8(z + cg * 32 + 8 * i, zz);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          f[4 * i + x] = feature<F>(f[4 * i + x]);
-          if (!live) f[4 * i + x] = both(0.f);
-          d = fma2(f[4 * i + x], zz[x], d);
-        }
-      }
-      den[cg * kT + row] = d.x + d.y;
-    }
-    if (!whole) fence_proxy_async_smem();
-    if (!__syncthreads_and(ok)) {
+    if (!row_and(ok, warp, X::kWork / 4)) {
       ok = false;
       break;
     }
-    if (!whole && tid == 0) {
-      tc_fence_after();
-      multiply_u(yt);
+    if (!live)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at_byte(yt, pl.own[i]) = make_uint4(0, 0, 0, 0);
+    arrive(&b->ready[0], lane);
+    float2 f[16], d = both(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack8(at_byte(qt, pl.own[i]), f + 4 * i);
+      float2 zz[4];
+      load8(z + cg * 32 + 8 * i, zz);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        f[4 * i + x] = feature<F>(f[4 * i + x]);
+        if (!live) f[4 * i + x] = both(0.f);
+        d = fma2(f[4 * i + x], zz[x], d);
+      }
     }
-    ++mmas;
+    den[cg * kT + row] = d.x + d.y;
+    row_sync();
     float inv = 1.f;
     if (p.c.normalise) {
-      float d = p.c.eps;
+      float dd = p.c.eps;
 #pragma unroll
-      for (int i = 0; i < X::kCols; ++i) d += den[i * kT + row];
-      inv = inverse(d);
+      for (int i = 0; i < X::kCols; ++i) dd += den[i * kT + row];
+      inv = inverse(dd);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // w over q's place
+    for (int i = 0; i < 4; ++i) {  // w over q's place (the low part's has been read: the tile before is stored)
       float2 w[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) w[x] = mul2(f[4 * i + x], both(inv));
@@ -672,23 +695,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
       remainder8(w, hi);
       at_byte(sm + M::kLo, pl.own[i]) = pack8(w);
     }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {  // dS^T += dy^T w  (d = 64: A's rows 64 .. 127 are another tile's columns, whose results are not read)
-      tc_fence_after();
-      const uint32_t ya = smem_u32(yt), qa = smem_u32(qt);
-      const uint64_t da = along_rows(ya, D == 64 ? wl - ya : kAtom);
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const uint64_t db = along_rows(part ? wl : qa, kAtom);
-#pragma unroll
-        for (int s = 0; s < kT / 16; ++s)
-          mma_bf16(tmem + D, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
-      }
-      mma_commit(&b->mma[1]);
-    }
-    ++mmas2;
-    ok = __all_sync(0xffffffffu, wait(&b->mma[0], j & 1, b));
+    arrive(&b->ready2, lane);
+    ok = wait(&b->mma[0], j & 1, b);
+    ok = __all_sync(0xffffffffu, ok);
+    float s = 0.f;
     if (ok) {
       tc_fence_after();
       float2 s2 = both(0.f);
@@ -700,9 +710,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
 #pragma unroll
         for (int x = 0; x < 8; ++x) s2 = fma2(f[8 * c + x], u[x], s2);
       }
-      den[cg * kT + row] = s2.x + s2.y;
+      s = s2.x + s2.y;
     }
-    if (!__syncthreads_and(ok)) {
+    row_sync();  // den has been read
+    den[cg * kT + row] = s;
+    if (!row_and(ok, warp, X::kWork / 4)) {
       ok = false;
       break;
     }
@@ -712,43 +724,32 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
       for (int i = 0; i < X::kCols; ++i) dd += den[i * kT + row];
       dd *= -inv * inv;
     }
-    ok = __all_sync(0xffffffffu, wait(&b->mma[1], j & 1, b));  // w has been read
-    if (ok) {
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float2 u[8];
-        tmem_ld8(at + 16 * c, u);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float2 zz[4];
-          load8(z + cg * 32 + 16 * c + 8 * i, zz);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int at_f = 8 * c + 4 * i + x;
-            dz[at_f] = fma2(f[at_f], both(dd), dz[at_f]);
-            u[4 * i + x] = mul2(slope<F>(f[at_f]), fma2(u[4 * i + x], both(inv), mul2(zz[x], both(dd))));
-          }
-          at_byte(qt, pl.own[2 * c + i]) = pack8(u + 4 * i);
-        }
-      }
-      __syncwarp();
-      store_rows(qt, pl, dq + (long long)j * kT * p.c.dq.sn, p.c.dq.sn, n);
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (!__syncthreads_and(ok)) {
-      ok = false;
-      break;
-    }
+    ok = row_and(wait(&b->mma2, j & 1, b), warp, X::kWork / 4);  // w has been read; and the row's sums
+    if (!ok) break;
     tc_fence_after();
-    if (j + 2 < tiles) {
-      if (tid == 0) fetch(j + 2);
-      ++issued;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float2 u[8];
+      tmem_ld8(at + 16 * c, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 zz[4];
+        load8(z + cg * 32 + 16 * c + 8 * i, zz);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int at_f = 8 * c + 4 * i + x;
+          dz[at_f] = fma2(f[at_f], both(dd), dz[at_f]);
+          u[4 * i + x] = mul2(slope<F>(f[at_f]), fma2(u[4 * i + x], both(inv), mul2(zz[x], both(dd))));
+        }
+        at_byte(qt, pl.own[2 * c + i]) = pack8(u + 4 * i);
+      }
     }
+    __syncwarp();
+    store_rows(qt, pl, dq + (long long)j * kT * p.c.dq.sn, p.c.dq.sn, n);
   }
-  if (ok) {
+  if (__syncthreads_and(ok && !aborted(&b->abort))) {
+    tc_fence_after();
     float* out = p.c.part + ((size_t)k * p.c.H + h) * (D * D + D);
     float v[32];
 #pragma unroll
@@ -769,133 +770,148 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
     }
     __syncthreads();
     if (tid < D) out[D * D + tid] = den[tid] + den[D + tid] + den[2 * D + tid] + den[3 * D + tid];
+  } else {
+    __syncthreads();
   }
-  finish<2>(b, kColumns, issued, mmas, mmas2);
+  finish<2, 1>(b, kColumns);
 }
 
 // ================================================================ backward over the keys
+// d = 64: three buffers and two accumulators, as the read; d = 128: two buffers and one accumulator.
 template <int D>
 struct KeySmem {
-  static constexpr int kK = 0, kV = 2 * Tc<D>::kTile, kS = 4 * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat, kZ = kSLo + Tc<D>::kMat,
-                       kBars = kZ + D * 4;
-  static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
+  static constexpr int kBuffers = D == 64 ? 3 : 2, kAcc = D == 64 ? 2 : 1;
+  static constexpr int kK = 0, kV = kBuffers * Tc<D>::kTile, kS = 2 * kBuffers * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat,
+                       kEnd = kSLo + Tc<D>::kMat;
+  static constexpr int kZ = 0, kBars = kZ + D * 4, kSmall = kBars + (int)sizeof(Bars);
+  static constexpr int kBytes = (kSmall + 1023) / 1024 * 1024 + kEnd;
+  static_assert(kBytes <= (D == 64 ? 115712 : 232448), "two blocks of d = 64 an SM, one of d = 128");
 };
 template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key_kernel(const __grid_constant__ TcArgs p) {
   using X = Tc<D>;
   using M = KeySmem<D>;
-  constexpr uint32_t kColumns = 2 * D;  // dv, dphi(k)
+  constexpr int NB = M::kBuffers, NA = M::kAcc;
+  constexpr uint32_t kColumns = 2 * D * NA;  // dv, dphi(k), an accumulator each
   extern __shared__ __align__(16) uint8_t smraw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
-  Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
-  float* z = reinterpret_cast<float*>(sm + M::kZ);
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + M::kSmall + 1023) & ~uintptr_t(1023));
+  if (sm + M::kEnd > smraw + M::kBytes) {  // (shared memory starts at a multiple of 1024 bytes, or near enough)
+    if (threadIdx.x == 0) atomicOr(p.c.status, 1u);
+    return;
+  }
+  Bars* b = reinterpret_cast<Bars*>(smraw + M::kBars);
+  float* z = reinterpret_cast<float*>(smraw + M::kZ);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
-  if (g.seq < 0) return finish<2>(b, kColumns, 0, 0, 0);
+  if (g.seq < 0) return finish<NB, NA>(b, kColumns);
   const int rows = p.c.ks.cu != nullptr ? g.len : min(p.c.ks.L, p.c.ks.N - g.row0);  // dense: zeros behind the tokens
   const uint32_t tmem = b->tbase;
   const int tiles = (rows + kT - 1) / kT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
-  const auto fetch = [&](int j) {
-    uint64_t* bar = &b->full[j & 1];
-    mbar_arrive_expect_tx(bar, 2 * X::kTile);
-    load_tile<D>(sm + M::kK + (j & 1) * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
-    load_tile<D>(sm + M::kV + (j & 1) * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
-  };
-  int issued = min(tiles, 2), mmas = 0;
-  if (tid == 0)
-    for (int j = 0; j < issued; ++j) fetch(j);
   const float* from = p.c.dS + ((size_t)g.seq * p.c.Hk + h) * (D * D + D);
-  load_matrix<D>(sm + M::kS, sm + M::kSLo, from);
+  if (tid < X::kWork) load_matrix<D>(sm + M::kS, sm + M::kSLo, from);
   if (tid < D) z[tid] = from[D * D + tid];
-  fence_proxy_async_smem();
-  __syncthreads();
+  if (tid >= X::kWork) {
+    if (lane == 0) {
+      const auto fetch = [&](int j) {
+        uint64_t* bar = &b->full[j % NB];
+        mbar_arrive_expect_tx(bar, 2 * X::kTile);
+        load_tile(sm + M::kK + j % NB * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+        load_tile(sm + M::kV + j % NB * X::kTile, &p.b, g.row0 + j * kT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
+        b->issued = j + 1;
+      };
+      const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo);
+      // so many tiles that the warps may be at: tile j's features wait for the tile j - LAG stored
+      constexpr int LAG = NA;
+      for (int j = 0; j < min(tiles, NB == 3 ? 3 : 1); ++j) fetch(j);
+      for (int j = 0; j < tiles; ++j) {
+        // every warp has the features of tile j (the first time: dS) written, and tile j - LAG stored
+        if (!wait(&b->ready[j % NB], (j / NB) & 1, b)) break;
+        tc_fence_after();
+        const uint32_t ka = smem_u32(sm + M::kK + j % NB * X::kTile), va = smem_u32(sm + M::kV + j % NB * X::kTile);
+        const uint32_t acc = tmem + j % NA * 2 * D;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            mma_bf16(acc, along_cols<D>(ka, kAtom, s), along_rows(part ? sl : sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1),
+                     s > 0 || part > 0);
+            mma_bf16(acc + D, along_cols<D>(va, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s),
+                     idesc_bf16_f32(128, D, 0, 0), s > 0 || part > 0);
+          }
+        mma_commit(&b->mma[j % NA]);
+        b->mmas = j + 1;
+        if (j >= LAG && j + 1 < tiles && NB == 3) fetch(j + 1);
+        if (NB == 2 && j + 1 < tiles) fetch(j + 1);
+      }
+    }
+    __syncwarp();
+    __syncthreads();
+    return finish<NB, NA>(b, kColumns);
+  }
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(X::kWork) : "memory");  // z
   const Places pl = places(warp, lane);
   const int row = pl.row, cg = warp >> 2;
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
-  const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo);
   __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dk.p)) + cross_base(p.c.ks, p.c.dk, g.seq, h) +
                       (long long)g.row0 * p.c.dk.sn + pl.out_col;
   __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dv.p)) + cross_base(p.c.ks, p.c.dv, g.seq, h) +
                       (long long)g.row0 * p.c.dv.sn + pl.out_col;
-  bool ok = true;
-  for (int j = 0; j < tiles; ++j) {
-    uint8_t *kt = sm + M::kK + (j & 1) * X::kTile, *vt = sm + M::kV + (j & 1) * X::kTile;
-    const bool live = row < g.len - j * kT;
-    float2 f[16];
-    ok = wait(&b->full[j & 1], (j >> 1) & 1, b);
-    if (ok) {
+  // phi(k) of tile j over its keys
+  const auto features = [&](int j) {
+    uint8_t* kt = sm + M::kK + j % NB * X::kTile;
+    if (!__all_sync(0xffffffffu, wait(&b->full[j % NB], (j / NB) & 1, b))) return false;
+    if (F != MHLA_PHI_IDENTITY)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint4* at_k = &at_byte(kt, pl.own[i]);
-        unpack8(*at_k, f + 4 * i);
+        float2 f[4];
+        unpack8(at_byte(kt, pl.own[i]), f);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) f[4 * i + x] = feature<F>(f[4 * i + x]);
-        if (F != MHLA_PHI_IDENTITY) *at_k = pack8(f + 4 * i);
+        for (int x = 0; x < 4; ++x) f[x] = feature<F>(f[x]);
+        at_byte(kt, pl.own[i]) = pack8(f);
       }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (!__syncthreads_and(ok)) {
-      ok = false;
-      break;
-    }
-    if (tid == 0) {
-      tc_fence_after();
-      const uint32_t ka = smem_u32(kt), va = smem_u32(vt);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          mma_bf16(tmem, along_cols<D>(ka, kAtom, s), along_rows(part ? sl : sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1),
-                   s > 0 || part > 0);
-          mma_bf16(tmem + D, along_cols<D>(va, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s),
-                   idesc_bf16_f32(128, D, 0, 0), s > 0 || part > 0);
-        }
-      mma_commit(&b->mma[0]);
-    }
-    ++mmas;
-    ok = __all_sync(0xffffffffu, wait(&b->mma[0], j & 1, b));
-    if (ok) {
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float2 u[8], v[8];
-        tmem_ld8(at + D + 16 * c, u);
-        tmem_ld8(at + 16 * c, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float2 zz[4];
-          load8(z + cg * 32 + 16 * c + 8 * i, zz);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            u[4 * i + x] = mul2(slope<F>(f[8 * c + 4 * i + x]), add2(u[4 * i + x], zz[x]));
-            if (!live) u[4 * i + x] = v[4 * i + x] = both(0.f);
-          }
-          at_byte(kt, pl.own[2 * c + i]) = pack8(u + 4 * i);
-          at_byte(vt, pl.own[2 * c + i]) = pack8(v + 4 * i);
-        }
-      }
-      __syncwarp();
-      const int m = rows - j * kT;
-      store_rows(kt, pl, dk + (long long)j * kT * p.c.dk.sn, p.c.dk.sn, m);
-      store_rows(vt, pl, dv + (long long)j * kT * p.c.dv.sn, p.c.dv.sn, m);
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (!__syncthreads_and(ok)) {
-      ok = false;
-      break;
-    }
+    arrive(&b->ready[j % NB], lane);
+    return true;
+  };
+  bool ok = tiles == 0 || features(0);
+  for (int j = 0; ok && j < tiles; ++j) {
+    uint8_t *kt = sm + M::kK + j % NB * X::kTile, *vt = sm + M::kV + j % NB * X::kTile;
+    if (NA == 2 && j + 1 < tiles && !features(j + 1)) break;
+    ok = __all_sync(0xffffffffu, wait(&b->mma[j % NA], (j / NA) & 1, b));
+    if (!ok) break;
     tc_fence_after();
-    if (j + 2 < tiles) {
-      if (tid == 0) fetch(j + 2);
-      ++issued;
+    const bool live = row < g.len - j * kT;
+    const uint32_t acc = at + j % NA * 2 * D;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float2 u[8], v[8];
+      tmem_ld8(acc + D + 16 * c, u);
+      tmem_ld8(acc + 16 * c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 f[4], zz[4];
+        unpack8(at_byte(kt, pl.own[2 * c + i]), f);  // (phi rounded to bf16: phi' goes by it, and its rounding by dk's)
+        load8(z + cg * 32 + 16 * c + 8 * i, zz);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          u[4 * i + x] = mul2(slope<F>(f[x]), add2(u[4 * i + x], zz[x]));
+          if (!live) u[4 * i + x] = v[4 * i + x] = both(0.f);
+        }
+        at_byte(kt, pl.own[2 * c + i]) = pack8(u + 4 * i);
+        at_byte(vt, pl.own[2 * c + i]) = pack8(v + 4 * i);
+      }
     }
+    __syncwarp();
+    const int m = rows - j * kT;
+    store_rows(kt, pl, dk + (long long)j * kT * p.c.dk.sn, p.c.dk.sn, m);
+    store_rows(vt, pl, dv + (long long)j * kT * p.c.dv.sn, p.c.dv.sn, m);
+    if (NA == 1 && j + 1 < tiles) ok = features(j + 1);
   }
-  finish<2>(b, kColumns, issued, mmas, 0);
+  __syncthreads();
+  finish<NB, NA>(b, kColumns);
 }
 
 // ================================================================ host
@@ -912,16 +928,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// A token tensor as [batch][head][row][d]; a dimension of stride 0 has one entry.  Rows behind the tensor read as zeros.
+// A token tensor as [batch][head][64 columns][row][column]; a dimension of stride 0 has one entry.  Rows behind the tensor read as zeros.
 bool make_map(CUtensorMap* m, const RetTensor& t, const CrossSide& s, int heads, int d, int box_rows) {
   auto enc = encoder();
   if (!enc) return false;
   const cuuint64_t row_bytes = t.sn ? (cuuint64_t)t.sn * 2 : (cuuint64_t)d * 2;
-  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)s.N, t.sh ? (cuuint64_t)heads : 1,
+  const cuuint64_t dims[5] = {64, (cuuint64_t)s.N, (cuuint64_t)d / 64, t.sh ? (cuuint64_t)heads : 1,
                               t.sb && s.cu == nullptr ? (cuuint64_t)s.B : 1};
-  const cuuint64_t strides[3] = {row_bytes, t.sh ? (cuuint64_t)t.sh * 2 : row_bytes, t.sb ? (cuuint64_t)t.sb * 2 : row_bytes};
-  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.p), dims, strides, box, es,
+  const cuuint64_t strides[4] = {row_bytes, 128, t.sh ? (cuuint64_t)t.sh * 2 : row_bytes, t.sb ? (cuuint64_t)t.sb * 2 : row_bytes};
+  const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, (cuuint32_t)d / 64, 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(t.p), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
