@@ -42,7 +42,7 @@ struct Tc {
 };
 
 struct Bars {
-  uint64_t full[3];   // a tile's tensors landed (tx), by its buffer
+  uint64_t full[4];   // a tile's tensors landed (tx), by its buffer
   uint64_t ready[3];  // a tile's operands are written (the working warps)
   uint64_t mma[3];    // MMA commits
   uint64_t ready2, mma2;
@@ -281,16 +281,17 @@ __device__ __forceinline__ uint64_t along_cols(uint32_t tile, uint32_t atom, int
 }
 
 // ================================================================ states
-// Three stages of 64 tokens: K (phi's high part is put over it), its middle and low parts, V.  While the MMAs of a tile run
-// the warps take the next one's features and TMA brings the one after; one barrier of the block a tile.  (With tiles of 128
-// tokens, and room for one of them in parts, the features waited for the MMAs: 65,536 tokens of 4 heads, d = 128, 44 us.)
-constexpr int kSumT = 64;
+// Tiles of 64 tokens: four buffers of K and V, so that three tiles are on their way at a time, and two of phi(k)'s three
+// parts, so that the features of a tile are taken while the MMAs of the one before run.  (65,536 tokens of 4 heads, d = 128:
+// with 128 tokens and one set of parts 44 us, with three buffers of 64 tokens that hold K, V and the parts together 40 us.)
+constexpr int kSumT = 64, kSumBuffers = 4;
 template <int D>
 struct SumSmem {
-  static constexpr int kPart = kSumT * D * 2;                                    // bytes of a tile of one tensor
-  static constexpr int kV = 0, kK = kPart, kMid = 2 * kPart, kLo = 3 * kPart, kStage = 4 * kPart;
-  static constexpr int kBars = 3 * kStage;
-  static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
+  static constexpr int kPart = kSumT * D * 2;  // bytes of a tile of one tensor
+  static constexpr int kV = 0, kK = kSumBuffers * kPart, kParts = 2 * kSumBuffers * kPart, kEnd = kParts + 6 * kPart;
+  static constexpr int kSmall = (int)sizeof(Bars);
+  static constexpr int kBytes = (kSmall + 1023) / 1024 * 1024 + kEnd;
+  static_assert(kBytes <= (D == 64 ? 115712 : 232448), "two blocks of d = 64 an SM, one of d = 128");
 };
 template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_states_kernel(const __grid_constant__ TcArgs p) {
@@ -300,13 +301,17 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   constexpr uint32_t kColumns = 2 * D;
   constexpr int kSumAtom = kSumT * 128;
   extern __shared__ __align__(16) uint8_t smraw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
-  Bars* b = reinterpret_cast<Bars*>(sm + M::kBars);
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + M::kSmall + 1023) & ~uintptr_t(1023));
+  if (sm + M::kEnd > smraw + M::kBytes) {  // (shared memory starts at a multiple of 1024 bytes, or near enough)
+    if (threadIdx.x == 0) atomicOr(p.c.status, 1u);
+    return;
+  }
+  Bars* b = reinterpret_cast<Bars*>(smraw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
-  if (g.seq < 0) return finish<3, 3>(b, kColumns);
+  if (g.seq < 0) return finish<kSumBuffers, 2>(b, kColumns);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kSumT - 1) / kSumT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
   constexpr int P = D / 8, ROWS = X::kWork / P;  // pieces of a row, rows at a time
@@ -316,70 +321,71 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   if (tid >= X::kWork) {
     if (lane == 0) {
       const auto fetch = [&](int j) {
-        uint64_t* bar = &b->full[j % 3];
-        uint8_t* to = sm + j % 3 * M::kStage;
+        uint64_t* bar = &b->full[j % kSumBuffers];
+        uint8_t* to = sm + j % kSumBuffers * M::kPart;
         mbar_arrive_expect_tx(bar, 2 * M::kPart);
         load_tile(to + M::kK, &p.a, g.row0 + j * kSumT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
         load_tile(to + M::kV, &p.b, g.row0 + j * kSumT, p.b_h ? h : 0, p.b_b ? bb : 0, bar);
         b->issued = j + 1;
       };
-      for (int j = 0; j < min(tiles, 3); ++j) fetch(j);
+      for (int j = 0; j < min(tiles, kSumBuffers); ++j) fetch(j);
       for (int j = 0; j < tiles; ++j) {
-        if (!wait(&b->ready[j % 3], (j / 3) & 1, b)) break;
+        if (!wait(&b->ready[j & 1], (j >> 1) & 1, b)) break;
         tc_fence_after();
-        const uint32_t va = smem_u32(sm + j % 3 * M::kStage), ka = va + M::kK;
-        // A = v.  d = 64: its rows 64 .. 127 are another tile's columns (phi's, behind V), whose results are not read.
-        // B = the high and the middle part side by side, then the low part onto the middle one's columns.
-        static_assert(M::kK == M::kV + D / 64 * kSumAtom, "what lies behind V");
-        const uint64_t da = along_rows(va, kSumAtom), d1 = along_rows(ka, kSumAtom), d2 = along_rows(va + M::kLo, kSumAtom);
+        const uint32_t va = smem_u32(sm + M::kV + j % kSumBuffers * M::kPart), pa = smem_u32(sm + M::kParts + (j & 1) * 3 * M::kPart);
+        // A = v.  d = 64: its rows 64 .. 127 are what lies behind the tile (another tile's columns), whose results are not
+        // read.  B = the high and the middle part side by side, then the low part onto the middle one's columns.
+        const uint64_t da = along_rows(va, kSumAtom), d1 = along_rows(pa, kSumAtom), d2 = along_rows(pa + 2 * M::kPart, kSumAtom);
 #pragma unroll
         for (int s = 0; s < kSumT / 16; ++s) {
           mma_bf16(tmem, da + s * 128, d1 + s * 128, idesc_bf16_f32(128, kExact ? D : 2 * D, 1, 1), j > 0 || s > 0);
           if (!kExact) mma_bf16(tmem + D, da + s * 128, d2 + s * 128, idesc_bf16_f32(128, D, 1, 1), true);
         }
-        mma_commit(&b->mma[j % 3]);
+        mma_commit(&b->mma[j & 1]);
         b->mmas = j + 1;
-        if (j > 0 && j + 2 < tiles) {  // the stage of tile j - 1 takes tile j + 2
-          if (!wait(&b->mma[(j - 1) % 3], ((j - 1) / 3) & 1, b)) break;
-          fetch(j + 2);
+        if (j > 0 && j + kSumBuffers - 1 < tiles) {  // the buffer of tile j - 1 takes the next one
+          if (!wait(&b->mma[(j - 1) & 1], ((j - 1) >> 1) & 1, b)) break;
+          fetch(j + kSumBuffers - 1);
         }
       }
     }
     __syncwarp();
   } else {
     for (int j = 0; ok && j < tiles; ++j) {
-      uint8_t* st = sm + j % 3 * M::kStage;
-      ok = __all_sync(0xffffffffu, wait(&b->full[j % 3], (j / 3) & 1, b));
+      uint8_t *kt = sm + M::kK + j % kSumBuffers * M::kPart, *vt = sm + M::kV + j % kSumBuffers * M::kPart;
+      uint8_t* part = sm + M::kParts + (j & 1) * 3 * M::kPart;
+      ok = wait(&b->full[j % kSumBuffers], (j / kSumBuffers) & 1, b);
+      if (ok && j >= 2) ok = wait(&b->mma[j & 1], ((j - 2) >> 1) & 1, b);  // the parts have been read
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int n = g.len - j * kSumT;
 #pragma unroll
       for (int i = 0; i < kSumT / ROWS; ++i) {
         const int r = r0 + i * ROWS;
-        uint4* at = piece(st + M::kK, kSumT, r, pc);
         float2 f[4];
-        unpack8(*at, f);
+        unpack8(*piece(kt, kSumT, r, pc), f);
 #pragma unroll
         for (int x = 0; x < 4; ++x) f[x] = feature<F>(f[x]);
         if (r >= n) {  // behind the sequence: nothing of what lies there counts
 #pragma unroll
           for (int x = 0; x < 4; ++x) f[x] = both(0.f);
-          *piece(st + M::kV, kSumT, r, pc) = make_uint4(0, 0, 0, 0);
+          *piece(vt, kSumT, r, pc) = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) z[x] = add2(z[x], f[x]);
         const uint4 hi = pack8(f);
-        *at = hi;
+        *piece(part, kSumT, r, pc) = hi;
         if (!kExact) {
           remainder8(f, hi);
           const uint4 mid = pack8(f);
-          *piece(st + M::kMid, kSumT, r, pc) = mid;
+          *piece(part + M::kPart, kSumT, r, pc) = mid;
           remainder8(f, mid);
-          *piece(st + M::kLo, kSumT, r, pc) = pack8(f);
+          *piece(part + 2 * M::kPart, kSumT, r, pc) = pack8(f);
         }
       }
-      arrive(&b->ready[j % 3], lane);
+      arrive(&b->ready[j & 1], lane);
     }
-    if (ok && tiles > 0) ok = wait(&b->mma[(tiles - 1) % 3], ((tiles - 1) / 3) & 1, b);  // (and all MMAs before it)
+    if (ok && tiles > 0) ok = wait(&b->mma[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, b);  // (and all MMAs before it)
   }
   float *so = nullptr, *zo = nullptr;
   if (cross_joined(p.c.ks) && g.nseg != 1) {
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   }
   if (__syncthreads_and(ok && !aborted(&b->abort))) {
     tc_fence_after();
-    float* zp = reinterpret_cast<float*>(sm);  // [ROWS][D]: the stages have been read
+    float* zp = reinterpret_cast<float*>(sm);  // [ROWS][D]: the buffers have been read
     if (tid < X::kWork)
 #pragma unroll
       for (int x = 0; x < 4; ++x) *reinterpret_cast<float2*>(zp + r0 * D + 8 * pc + 2 * x) = z[x];
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
       }
     }
   }
-  finish<3, 3>(b, kColumns);
+  finish<kSumBuffers, 2>(b, kColumns);
 }
 
 // ================================================================ read
