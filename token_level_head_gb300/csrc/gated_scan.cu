@@ -749,22 +749,15 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
       fill(f, 0.f);
       if (p.dh_last != nullptr && on) load_f(p.dh_last + (long long)(PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch) * p.D + c, f);
     };
-    // the thread's rows: h -> fA h + fB forwards, c -> rA c + rB backwards
-    float2 a[kR][P], fA[P], fB[P], rA[P], rB[P], wA[P], wB[P];
-    fill(fA, 1.f);
+    // the thread's rows backwards, c -> rA c + rB
+    float2 a[kR][P], rA[P], rB[P], wA[P], wB[P];
     fill(rA, 1.f);
-    fill(fB, 0.f);
     fill(rB, 0.f);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      float2 gv[P], xv[P], d[P];
+      float2 gv[P], d[P];
       unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
-      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
       unpack<T>(*reinterpret_cast<const Raw*>(sd + r * CW), d);
-      if (first >> r & 1) {
-        start(r, fB);
-        if (PACKED) fill(fA, kCut);  // (dense: the state before the first row is zero)
-      }
       if (last >> r & 1) {
         float2 e[P];
         end(r, e);
@@ -773,20 +766,12 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        const Gate gt = gate_of<T, GATE>(gv[i]);
-        a[r][i] = gt.a;
+        a[r][i] = gate_of<T, GATE>(gv[i]).a;
         if (!(m.live >> r & 1)) a[r][i] = both(1.f);
-        fB[i] = fma2(a[r][i], fB[i], input_of<GATE>(xv[i], gt.rest));
-        fA[i] = mul2(fA[i], a[r][i]);
-        // backwards: row r acts before the rows so far, c -> rA (a (dy + c)) + rB
+        // row r acts before the rows so far, c -> rA (a (dy + c)) + rB
         rB[i] = carry_on<PACKED>(rA[i], rB[i], mul2(a[r][i], d[i]));
         rA[i] = join<PACKED>(rA[i], PACKED && (last >> r & 1) ? both(kCut) : a[r][i]);
       }
-    }
-    scan_warp<LW, false, PACKED>(fA, fB, wA, wB, lane);
-    if (PER > 1 && lane / LW == GROUPS - 1) {
-      store(&fwa[warp][cl], wA);
-      store(&fwb[warp][cl], wB);
     }
     scan_warp<LW, true, PACKED>(rA, rB, wA, wB, lane);
     if (lane / LW == 0) {
@@ -794,21 +779,48 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
       store(&s.wb[par][warp][cl], wB);
     }
     give(par, cluster > 1);
+    // and forwards, h -> fA h + fB, while the gradient that enters the tile is on its way.  b = x - a x here: off by 2^-24 of x,
+    // as h is anyway
     if (PACKED && t0 + cluster < tiles) {
       tile_sync();
       set_marks<kR>(p, t - cluster >= 0 ? (t - cluster) * ROWS : p.N, marks[par ^ 1]);
     }
+    float2 fA[P], fB[P];
+    fill(fA, 1.f);
+    fill(fB, 0.f);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      float2 xv[P];
+      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
+      if (first >> r & 1) {
+        start(r, fB);
+        if (PACKED) fill(fA, kCut);  // (dense: the state before the first row is zero)
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 b = GATE == GATED_SCAN_SIGMOID ? fma2(a[r][i], make_float2(-xv[i].x, -xv[i].y), xv[i]) : xv[i];
+        fB[i] = fma2(a[r][i], fB[i], b);
+        fA[i] = mul2(fA[i], a[r][i]);
+      }
+    }
+    scan_warp<LW, false, PACKED>(fA, fB, wA, wB, lane);
+    if (PER > 1) {
+      if (lane / LW == GROUPS - 1) {
+        store(&fwa[warp][cl], wA);
+        store(&fwb[warp][cl], wB);
+      }
+      tile_sync();
+      over_warps<CW, false, PACKED>(fwa, fwb, cl, warp, from, h);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) h[i] = carry_on<PACKED>(fA[i], fB[i], h[i]);
     give_wait(cluster > 1);
     carry_sync(par);
     float2 k[P];
     load_f(&s.carry[par][cl], k);
     over_warps<CW, true, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, k);
-    if (PER > 1) over_warps<CW, false, PACKED>(fwa, fwb, cl, warp, from, h);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      k[i] = carry_on<PACKED>(rA[i], rB[i], k[i]);
-      h[i] = carry_on<PACKED>(fA[i], fB[i], h[i]);
-    }
+    for (int i = 0; i < P; ++i) k[i] = carry_on<PACKED>(rA[i], rB[i], k[i]);
     const unsigned out = on ? m.live : 0, starts = p.dh0 != nullptr && on ? first : 0;
     float2 G[kR][P];
 #pragma unroll

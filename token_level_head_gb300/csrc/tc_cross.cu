@@ -581,7 +581,7 @@ template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_query_kernel(const __grid_constant__ TcArgs p) {
   using X = Tc<D>;
   using M = QuerySmem<D>;
-  constexpr uint32_t kColumns = 2 * D;  // u, dS^T
+  constexpr uint32_t kColumns = 256;  // u, dS^T (d = 64: in two parts)
   extern __shared__ __align__(16) uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + M::kSmall + 1023) & ~uintptr_t(1023));
   if (sm + M::kEnd > smraw + M::kBytes) {  // (shared memory starts at a multiple of 1024 bytes, or near enough)
@@ -629,13 +629,14 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
         if (!wait(&b->ready2, j & 1, b)) break;
         tc_fence_after();
         // dS^T += dy^T w  (d = 64: A's rows 64 .. 127 are another tile's columns, whose results are not read)
+        // d = 64: the high and the low part of w side by side, in columns of their own
         const uint64_t da = along_rows(ya, D == 64 ? wl - ya : kAtom);
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const uint64_t db = along_rows(part ? wl : qa, kAtom);
+        for (int part = 0; part < (D == 64 ? 1 : 2); ++part) {
+          const uint64_t db = along_rows(part ? wl : qa, D == 64 ? wl - qa : kAtom);
 #pragma unroll
           for (int s = 0; s < kT / 16; ++s)
-            mma_bf16(tmem + D, da + s * 128, db + s * 128, idesc_bf16_f32(128, D, 1, 1), j > 0 || s > 0 || part > 0);
+            mma_bf16(tmem + D, da + s * 128, db + s * 128, idesc_bf16_f32(128, 128, 1, 1), j > 0 || s > 0 || part > 0);
         }
         mma_commit(&b->mma2);
         b->mmas2 = j + 1;
@@ -770,6 +771,14 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
         tmem_ld16(at + D, v);
         tmem_ld16(at + D + 16, v + 16);
         tmem_ld_wait();
+        if (D == 64) {
+          float w[32];
+          tmem_ld16(at + 2 * D, w);
+          tmem_ld16(at + 2 * D + 16, w + 16);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] += w[x];
+        }
       }
 #pragma unroll
       for (int x = 0; x < 32; ++x) out[(c0 + x) * D + e] = tiles > 0 ? v[x] : 0.f;
