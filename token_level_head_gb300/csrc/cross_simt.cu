@@ -125,10 +125,21 @@ __device__ __forceinline__ void load_matrix(float* to, float* turned, const floa
     }
   }
 }
+// The thread's columns of a row.
 template <int D, typename T>
 __device__ __forceinline__ void store_cols(T* row, int tx, const float (&f)[Simt<D>::CN]) {
+  using S = Simt<D>;
 #pragma unroll
-  for (int j = 0; j < Simt<D>::CN; ++j) row[Simt<D>::col(tx, j)] = from_f<T>(f[j]);
+  for (int j = 0; j < S::CN; j += S::VEC) {
+    T v[S::VEC];
+#pragma unroll
+    for (int x = 0; x < S::VEC; ++x) v[x] = from_f<T>(f[j + x]);
+    T* to = row + S::col(tx, j);
+    if (sizeof(v) == 16) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(v);
+    if (sizeof(v) == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(v);
+    if (sizeof(v) == 4) *reinterpret_cast<unsigned*>(to) = *reinterpret_cast<const unsigned*>(v);
+    if (sizeof(v) == 2) *to = v[0];
+  }
 }
 
 // ---- states: a block sums up a segment of a key head
@@ -303,9 +314,7 @@ __global__ void __launch_bounds__(kThreads) cross_backward_query_kernel(const __
     float ur[RN][S::CN] = {};
     rows_times<D, RN>(ur, dy, mat, ty, tx);  // u[t][c] = sum_e dy[t][e] S[c][e]
 #pragma unroll
-    for (int i = 0; i < RN; ++i)
-#pragma unroll
-      for (int j = 0; j < S::CN; ++j) u[(ty + 16 * i) * S::LD + S::col(tx, j)] = ur[i][j];
+    for (int i = 0; i < RN; ++i) store_cols<D>(u + (ty + 16 * i) * S::LD, tx, ur[i]);
     __syncthreads();
     {  // eight threads a row: den and phi(q) . u
       const int r = tid / 8;

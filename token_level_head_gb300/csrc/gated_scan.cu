@@ -183,43 +183,40 @@ struct Marks {
 __device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // the kThreads of the tiles
 static_assert(kThreads == 256, "the barrier's count");
 
-// Packed sequences: bits of the tile's rows row0 .., a word for the kR rows of a thread; two sets, by the tile's parity, as
-// the next tile's are made while the state that enters this one is on its way.  Offsets outside [0, N] are clamped; out of
-// order they mark rows of the tile all the same and nothing else.
-template <int GROUPS>
+// Packed sequences: bits of the tile's rows row0 .., a word for the kR rows of a thread, and the sequences of the rows that
+// have one (a row that begins one and ends one is the same's).  Sets by the tile, as a later tile's are made while the state
+// that enters this one is on its way.  Offsets outside [0, N] are clamped; out of order they mark rows of the tile all the
+// same and nothing else.
+template <int GROUPS, int ROWS>
 struct MarkRows {
   unsigned first[GROUPS], last[GROUPS];
+  int seq[ROWS];
 };
+template <>
+struct MarkRows<0, 0> {};  // dense
 // (the tiles' threads, between two of their barriers each: cleared, then set)
-template <int GROUPS>
-__device__ __forceinline__ void clear_marks(MarkRows<GROUPS>& m) {
+template <int GROUPS, int ROWS>
+__device__ __forceinline__ void clear_marks(MarkRows<GROUPS, ROWS>& m) {
   for (int i = threadIdx.x; i < GROUPS; i += kThreads) m.first[i] = m.last[i] = 0;
+  for (int i = threadIdx.x; i < ROWS; i += kThreads) m.seq[i] = 0;
 }
-template <int kR, int GROUPS>
-__device__ __forceinline__ void set_marks(const ScanArgs& p, int row0, MarkRows<GROUPS>& m) {
+template <int GROUPS, int ROWS>
+__device__ __forceinline__ void set_marks(const ScanArgs& p, int row0, MarkRows<GROUPS, ROWS>& m) {
+  constexpr int kR = ROWS / GROUPS;
   for (int i = threadIdx.x; i < p.B; i += kThreads) {
     const int lo = min(max(p.cu[i], 0), p.N), hi = min(max(p.cu[i + 1], lo), p.N);
     if (lo == hi) continue;
     const int f = lo - row0, l = hi - 1 - row0;
-    if (f >= 0 && f < GROUPS * kR) atomicOr(&m.first[f / kR], 1u << f % kR);
-    if (l >= 0 && l < GROUPS * kR) atomicOr(&m.last[l / kR], 1u << l % kR);
-  }
-}
-// The sequence that a marked row is in: the last one whose offset is not behind the row.
-__device__ __noinline__ int sequence_of(const int* cu, int B, int row) {
-  int lo = 0, n = B;  // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int half = n / 2;
-    if (cu[lo + half] <= row) {
-      lo += half;
-      n -= half;
-    } else {
-      n = half;
+    if (f >= 0 && f < ROWS) {
+      atomicOr(&m.first[f / kR], 1u << f % kR);
+      atomicMax(&m.seq[f], i);
+    }
+    if (l >= 0 && l < ROWS) {
+      atomicOr(&m.last[l / kR], 1u << l % kR);
+      atomicMax(&m.seq[l], i);
     }
   }
-  return lo;
 }
-
 // The thread's kR rows from `row` on; rows in [lo, hi) are tokens.
 template <int kR>
 __device__ __forceinline__ unsigned live_rows(int row, int lo, int hi) {
@@ -235,8 +232,8 @@ __device__ __forceinline__ Marks dense_marks(int row, int hi) {
   k.last = hi > row && hi - row <= kR ? 1u << (hi - 1 - row) : 0u;
   return k;
 }
-template <int kR, int GROUPS>
-__device__ __forceinline__ Marks packed_marks(const MarkRows<GROUPS>& m, int group, int row, int lo, int hi) {
+template <int kR, int GROUPS, int ROWS>
+__device__ __forceinline__ Marks packed_marks(const MarkRows<GROUPS, ROWS>& m, int group, int row, int lo, int hi) {
   Marks k;
   k.live = live_rows<kR>(row, lo, hi);
   k.first = m.first[group] & k.live;
@@ -436,20 +433,20 @@ __device__ __forceinline__ void over_warps(const float (&wa)[kWarps][CW], const 
 }
 
 // ---- tiles in shared memory
-// A tile's ROWS rows of CW channels of one tensor; row groups are 32 bytes further apart where several of them are read at
-// once, so that they lie in banks of their own.
+// A tile's ROWS rows of CW channels of one tensor.  Rows of 64 bytes are read two row groups at a time: in every other group
+// neighbouring rows change places, so that the two lie in banks of their own.
 template <typename T, int LW>
 struct Stage {
   static constexpr int CW = V * LW, kR = Tile<T>::R, ROWS = kThreads / LW * kR, PIECES = CW * (int)sizeof(T) / 16;
-  static constexpr int PAD = LW < Tile<T>::WIDE ? 32 / (int)sizeof(T) : 0;      // elements
-  static constexpr int ELEMS = ROWS * CW + ROWS / kR * PAD;
-  static __device__ __forceinline__ int at(int row) { return row * CW + row / kR * PAD; }
+  static constexpr bool SWAP = LW < Tile<T>::WIDE;
+  static constexpr int ELEMS = ROWS * CW;
+  static __device__ __forceinline__ int at(int row) { return (SWAP ? row ^ (row / kR & 1) : row) * CW; }
   // The copy of rows [row0, row0 + ROWS) and channels from c0 on (D - c0 at most), asynchronously; zeros for rows outside
   // [lo, hi) and channels behind D.
   static __device__ __forceinline__ void fetch(T* to, const T* from, long long sn, long long row0, int lo, int hi, int c0,
                                                int D) {
     constexpr int N = ROWS * PIECES / kThreads, STEP = kThreads / PIECES;
-    static_assert(PAD == 0 || STEP % kR == 0, "the rows of a thread's copies lie evenly");
+    static_assert(!SWAP || STEP % (2 * kR) == 0, "the rows of a thread's copies change places alike");
     const int piece = threadIdx.x % PIECES, r = threadIdx.x / PIECES;
     const int c = piece * (16 / (int)sizeof(T));
     const bool on = c0 + c < D;
@@ -462,7 +459,7 @@ struct Stage {
       for (int i = 0; i < N; ++i) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
         src += step;
-        dst += at(STEP) * (int)sizeof(T);
+        dst += STEP * CW * (int)sizeof(T);
       }
       return;
     }
@@ -472,10 +469,15 @@ struct Stage {
       const bool ok = on && row >= lo && row < hi;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src + (ok ? row * sn : 0)), "r"(ok ? 16 : 0)
                    : "memory");
-      dst += at(STEP) * (int)sizeof(T);
+      dst += STEP * CW * (int)sizeof(T);
     }
   }
 };
+// Row r of a thread's rows, from its first row's place; delta: the way to the neighbour where rows have changed places.
+template <int CW, typename T>
+__device__ __forceinline__ const T* row_at(const T* first, int r, int delta) {
+  return first + r * CW + (r & 1 ? -delta : delta);
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   using St = Stage<T, LW>;
   constexpr int kR = St::kR, CW = St::CW, ROWS = St::ROWS, GROUPS = 32 / LW;
   __shared__ __align__(16) ScanShared<T, LW> s;
-  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks[2];
+  __shared__ MarkRows<PACKED ? ROWS / kR : 0, PACKED ? ROWS : 0> marks[3];
   launch_dependents();
   grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -495,6 +497,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
   const int cl = (tid % LW) * V, c = c0 + cl;         // the thread's channels
   const int r0 = (warp * GROUPS + lane / LW) * kR;    // and rows of the tile
+  const int delta = St::SWAP && (r0 / kR & 1) ? CW : 0;
   const bool on = c < p.D;
   const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb;
   const T* g = static_cast<const T*>(p.g.p) + (long long)batch * p.g.sb;
@@ -526,8 +529,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   // a and b of the thread's row r
   const auto row_of = [&](const T* sx, int r, float2 (&a)[P], float2 (&b)[P]) {
     float2 gv[P], xv[P];
-    unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
-    unpack<T>(*reinterpret_cast<const Raw*>(sx + St::ELEMS + r * CW), gv);
+    unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sx, r, delta)), xv);
+    unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sx, r, delta) + St::ELEMS), gv);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const Gate k = gate_of<T, GATE>(gv[i]);
@@ -535,10 +538,14 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
       b[i] = input_of<GATE>(xv[i], k.rest);
     }
   };
-  // The start of the sequence whose first token is row `row`.
-  const auto start_of = [&](int row, float2 (&h)[P]) {
+  // The sequence that row r of the thread's in the tile of round i begins or ends, and the start of it.
+  const auto sequence_of = [&](int i, int r) {
+    if constexpr (PACKED) return marks[i % 3].seq[r0 + r];
+    return batch;
+  };
+  const auto start_of = [&](int i, int r, float2 (&h)[P]) {
     fill(h, 0.f);
-    const int slot = slot_of(p.slots, p.n_slots, PACKED ? sequence_of(p.cu, p.B, row) : batch);
+    const int slot = slot_of(p.slots, p.n_slots, sequence_of(i, r));
     if (slot >= 0) load_f(p.states + (long long)slot * p.D + c, h);
   };
   // What is known of a tile before the state that enters it.
@@ -552,8 +559,11 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   const auto look = [&](int i, Ahead& n) {
     const int par = i & 1, row0 = (int)min(((long long)i * cluster + rank) * ROWS, (long long)p.N);
     n.row = row0 + r0;
-    n.m = PACKED ? packed_marks<kR>(marks[par], r0 / kR, n.row, lo, hi) : dense_marks<kR>(n.row, hi);
-    const T* sx = stage + i % 3 * 2 * St::ELEMS + St::at(r0) + cl;
+    if constexpr (PACKED)
+      n.m = packed_marks<kR>(marks[i % 3], r0 / kR, n.row, lo, hi);
+    else
+      n.m = dense_marks<kR>(n.row, hi);
+    const T* sx = stage + i % 3 * 2 * St::ELEMS + r0 * CW + cl;
     float2 wA[P], wB[P];
     fill(n.A, 1.f);
     fill(n.B, 0.f);
@@ -563,7 +573,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
       float2 a[P], b[P];
       row_of(sx, r, a, b);
       if (p.load && on && n.m.first >> r & 1) {
-        start_of(n.row + r, n.h0);
+        start_of(i, r, n.h0);
 #pragma unroll
         for (int k = 0; k < P; ++k) b[k] = fma2(a[k], n.h0[k], b[k]);
       }
@@ -590,12 +600,12 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   fetch(1);
   if (cluster > 1) cg::this_cluster().sync();
   Ahead next;
-  if (PACKED) {
+  if constexpr (PACKED) {
     clear_marks(marks[0]);
     clear_marks(marks[1]);
     tile_sync();
-    set_marks<kR>(p, row0_of(0), marks[0]);
-    set_marks<kR>(p, row0_of(1), marks[1]);
+    set_marks(p, row0_of(0), marks[0]);
+    set_marks(p, row0_of(1), marks[1]);
   }
   copies_wait1();
   tile_sync();
@@ -606,16 +616,18 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     const Ahead now = next;
     if (i + 1 < rounds) {  // while the state that enters this tile is on its way, the next one
       copies_wait0();
-      tile_sync();  // every thread's part of it is there, the buffer after it and this tile's marks have been read
+      tile_sync();  // every thread's part of it is there, the buffer after it has been read
       fetch(i + 2);
-      if (PACKED) clear_marks(marks[par]);
+      if constexpr (PACKED) clear_marks(marks[(i + 2) % 3]);
       look(i + 1, next);
     }
     give_wait(cluster > 1);
     if (i + 1 < rounds) give(par ^ 1, cluster > 1);
-    if (PACKED && i + 2 < rounds) {
-      tile_sync();
-      set_marks<kR>(p, row0_of(i + 2), marks[par]);
+    if constexpr (PACKED) {
+      if (i + 2 < rounds) {
+        tile_sync();
+        set_marks(p, row0_of(i + 2), marks[(i + 2) % 3]);
+      }
     }
     carry_sync(par);
     float2 h[P];
@@ -626,7 +638,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     const int row = now.row;
     if (p.kept != nullptr && on && row < p.N && row % kScanKept == 0)
       store(p.kept + ((long long)batch * kept_rows + row / kScanKept) * p.D + c, h);
-    const T* sx = stage + i % 3 * 2 * St::ELEMS + St::at(r0) + cl;
+    const T* sx = stage + i % 3 * 2 * St::ELEMS + r0 * CW + cl;
     T* py = y + row * p.y.sn;
     const unsigned out = on ? now.m.live : 0, ends = p.states != nullptr && on ? now.m.last : 0;
 #pragma unroll
@@ -639,7 +651,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
 #pragma unroll
           for (int k = 0; k < P; ++k) h0[k] = now.h0[k];
         } else {
-          start_of(row + r, h0);
+          start_of(i, r, h0);
         }
 #pragma unroll
         for (int k = 0; k < P; ++k) b[k] = fma2(a[k], h0[k], b[k]);
@@ -649,7 +661,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
       if (out >> r & 1) store(py, h);
       py = next_row(py, p.y.sn);
       if (ends >> r & 1) {
-        const int slot = slot_of(p.slots, p.n_slots, PACKED ? sequence_of(p.cu, p.B, row + r) : batch);
+        const int slot = slot_of(p.slots, p.n_slots, sequence_of(i, r));
         if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
       }
     }
@@ -668,8 +680,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
   constexpr int PER = kScanKept / (GROUPS * kR) > 1 ? kScanKept / (GROUPS * kR) : 1;  // warps of a kept state
   static_assert((GROUPS * kR * PER) % kScanKept == 0 && kWarps % PER == 0, "a kept state at the first row of every PER warps");
   __shared__ __align__(16) ScanShared<T, LW> s;
-  __shared__ __align__(16) float fwa[kWarps][CW], fwb[kWarps][CW];
-  __shared__ MarkRows<PACKED ? ROWS / kR : 1> marks[2];
+  __shared__ MarkRows<PACKED ? ROWS / kR : 0, PACKED ? ROWS : 0> marks[2];
   launch_dependents();
   grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -677,6 +688,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
   const int cl = (tid % LW) * V, c = c0 + cl;
   const int r0 = (warp * GROUPS + lane / LW) * kR;
+  const int delta = St::SWAP && (r0 / kR & 1) ? CW : 0;
   const bool on = c < p.D;
   const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb;
   const T* g = static_cast<const T*>(p.g.p) + (long long)batch * p.g.sb;
@@ -718,10 +730,10 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     copies_commit();
   };
   fetch(tiles - 1 - rank, 0);
-  if (PACKED) {
+  if constexpr (PACKED) {
     clear_marks(marks[0]);
     tile_sync();
-    set_marks<kR>(p, tiles - 1 - rank >= 0 ? (tiles - 1 - rank) * ROWS : p.N, marks[0]);
+    set_marks(p, tiles - 1 - rank >= 0 ? (tiles - 1 - rank) * ROWS : p.N, marks[0]);
   }
   if (cluster > 1) cg::this_cluster().sync();
   int par = 0;
@@ -736,18 +748,26 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     copies_wait0();
     tile_sync();
     fetch(t - cluster, par ^ 1);
-    if (PACKED) clear_marks(marks[par ^ 1]);
-    const T *sx = stage + par * 3 * St::ELEMS + St::at(r0) + cl, *sg = sx + St::ELEMS, *sd = sg + St::ELEMS;
-    const Marks m = PACKED ? packed_marks<kR>(marks[par], r0 / kR, row0 + r0, lo, hi) : dense_marks<kR>(row0 + r0, hi);
+    if constexpr (PACKED) clear_marks(marks[par ^ 1]);
+    const T *sx = stage + par * 3 * St::ELEMS + r0 * CW + cl, *sg = sx + St::ELEMS, *sd = sg + St::ELEMS;
+    Marks m;
+    if constexpr (PACKED)
+      m = packed_marks<kR>(marks[par], r0 / kR, row0 + r0, lo, hi);
+    else
+      m = dense_marks<kR>(row0 + r0, hi);
+    const auto sequence_of = [&](int r) {
+      if constexpr (PACKED) return marks[par].seq[r0 + r];
+      return batch;
+    };
     const unsigned first = m.first, last = m.last;
     // the start of a sequence that begins in row r, the gradient behind one that ends there
     const auto start = [&](int r, float2 (&f)[P]) {
       fill(f, 0.f);
-      if (p.h0 != nullptr && on) load_f(p.h0 + (long long)(PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch) * p.D + c, f);
+      if (p.h0 != nullptr && on) load_f(p.h0 + (long long)sequence_of(r) * p.D + c, f);
     };
     const auto end = [&](int r, float2 (&f)[P]) {
       fill(f, 0.f);
-      if (p.dh_last != nullptr && on) load_f(p.dh_last + (long long)(PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch) * p.D + c, f);
+      if (p.dh_last != nullptr && on) load_f(p.dh_last + (long long)sequence_of(r) * p.D + c, f);
     };
     // the thread's rows backwards, c -> rA c + rB
     float2 a[kR][P], rA[P], rB[P], wA[P], wB[P];
@@ -756,8 +776,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       float2 gv[P], d[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
-      unpack<T>(*reinterpret_cast<const Raw*>(sd + r * CW), d);
+      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
+      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sd, r, delta)), d);
       if (last >> r & 1) {
         float2 e[P];
         end(r, e);
@@ -781,9 +801,11 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     give(par, cluster > 1);
     // and forwards, h -> fA h + fB, while the gradient that enters the tile is on its way.  b = x - a x here: off by 2^-24 of x,
     // as h is anyway
-    if (PACKED && t0 + cluster < tiles) {
-      tile_sync();
-      set_marks<kR>(p, t - cluster >= 0 ? (t - cluster) * ROWS : p.N, marks[par ^ 1]);
+    if constexpr (PACKED) {
+      if (t0 + cluster < tiles) {
+        tile_sync();
+        set_marks(p, t - cluster >= 0 ? (t - cluster) * ROWS : p.N, marks[par ^ 1]);
+      }
     }
     float2 fA[P], fB[P];
     fill(fA, 1.f);
@@ -791,7 +813,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       float2 xv[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
+      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sx, r, delta)), xv);
       if (first >> r & 1) {
         start(r, fB);
         if (PACKED) fill(fA, kCut);  // (dense: the state before the first row is zero)
@@ -806,11 +828,11 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     scan_warp<LW, false, PACKED>(fA, fB, wA, wB, lane);
     if (PER > 1) {
       if (lane / LW == GROUPS - 1) {
-        store(&fwa[warp][cl], wA);
-        store(&fwb[warp][cl], wB);
+        store(&s.wa[par ^ 1][warp][cl], wA);  // (the tile before's have been read)
+        store(&s.wb[par ^ 1][warp][cl], wB);
       }
       tile_sync();
-      over_warps<CW, false, PACKED>(fwa, fwb, cl, warp, from, h);
+      over_warps<CW, false, PACKED>(s.wa[par ^ 1], s.wb[par ^ 1], cl, warp, from, h);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) h[i] = carry_on<PACKED>(fA[i], fB[i], h[i]);
@@ -826,7 +848,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
 #pragma unroll
     for (int r = kR - 1; r >= 0; --r) {
       float2 d[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(sd + r * CW), d);
+      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sd, r, delta)), d);
       if (last >> r & 1) end(r, k);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
@@ -836,14 +858,14 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
       if (starts >> r & 1) {
         if (GATE == GATED_SCAN_SIGMOID) {  // (a small gate with all its digits)
           float2 gv[P];
-          unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
+          unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
             const float2 low = gate_of<T, GATE>(gv[i]).low;
             k[i] = mul2(make_float2(gv[i].x > 0.f ? a[r][i].x : low.x, gv[i].y > 0.f ? a[r][i].y : low.y), G[r][i]);
           }
         }
-        store(p.dh0 + (long long)(PACKED ? sequence_of(p.cu, p.B, row0 + r0 + r) : batch) * p.D + c, k);
+        store(p.dh0 + (long long)sequence_of(r) * p.D + c, k);
       }
     }
     const long long row = (long long)row0 + r0;
@@ -851,8 +873,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       float2 gv[P], xv[P], ox[P], og[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(sg + r * CW), gv);
-      unpack<T>(*reinterpret_cast<const Raw*>(sx + r * CW), xv);
+      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
+      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sx, r, delta)), xv);
       if (first >> r & 1) start(r, h);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
