@@ -149,11 +149,15 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // not-a-number st
   return r;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+// exp(x), and x + 1 in its place where x > 0: a comparison and an addition under it.
+__device__ __forceinline__ float elu1(float x) {
+  float e = exp2_of(x * kLog2e);
+  asm("{\n\t.reg .pred p;\n\tsetp.gt.f32 p, %1, 0f00000000;\n\t@p add.f32 %0, %1, 0f3F800000;\n\t}" : "+f"(e) : "f"(x));
+  return e;
+}
 template <int F>
 __device__ __forceinline__ float2 feature(float2 x) {
-  if (F == MHLA_PHI_ELU1)  // exp(min(x, 0)) + max(x, 0)
-    return add2(make_float2(exp2_of(min_nan(x.x, 0.f) * kLog2e), exp2_of(min_nan(x.y, 0.f) * kLog2e)),
-                make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+  if (F == MHLA_PHI_ELU1) return make_float2(elu1(x.x), elu1(x.y));
   if (F == MHLA_PHI_RELU) return make_float2(x.x != x.x ? x.x : fmaxf(x.x, 0.f), x.y != x.y ? x.y : fmaxf(x.y, 0.f));
   if (F == MHLA_PHI_EXP) return make_float2(exp2_of(x.x * kLog2e), exp2_of(x.y * kLog2e));
   return x;
@@ -501,10 +505,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.y.p)) + cross_base(p.c.qs, p.c.y, g.seq, h) +
                      (long long)g.row0 * p.c.y.sn + pl.out_col;
   bool ok = true;
+  int buf = 0, before = 2, phase = 0;  // j % 3, (j - 1) % 3, j / 3 & 1
   for (int j = 0; ok && j <= tiles; ++j) {
     if (j < tiles) {  // the features of tile j
-      uint8_t* qt = sm + M::kQ + j % 3 * X::kTile;
-      ok = __all_sync(0xffffffffu, wait(&b->full[j % 3], (j / 3) & 1, b));
+      uint8_t* qt = sm + M::kQ + buf * X::kTile;
+      ok = __all_sync(0xffffffffu, wait(&b->full[buf], phase, b));
       if (!ok) break;
       float2 d = both(0.f);
 #pragma unroll
@@ -520,12 +525,12 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
         }
         if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
       }
-      den[(j % 3 * X::kCols + cg) * kT + row] = d.x + d.y;
-      arrive(&b->ready[j % 3], lane);
+      den[(buf * X::kCols + cg) * kT + row] = d.x + d.y;
+      arrive(&b->ready[buf], lane);
     }
     if (j > 0) {  // tile j - 1 goes out
       const int t = j - 1;
-      uint8_t* qt = sm + M::kQ + t % 3 * X::kTile;
+      uint8_t* qt = sm + M::kQ + before * X::kTile;
       ok = __all_sync(0xffffffffu, wait(&b->mma[t & 1], (t >> 1) & 1, b));
       if (!ok) break;
       tc_fence_after();
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
       if (p.c.normalise) {
         float d = p.c.eps;
 #pragma unroll
-        for (int i = 0; i < X::kCols; ++i) d += den[(t % 3 * X::kCols + i) * kT + row];
+        for (int i = 0; i < X::kCols; ++i) d += den[(before * X::kCols + i) * kT + row];
         inv = inverse(d);
       }
       tmem_ld_wait();
@@ -547,6 +552,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
       __syncwarp();
       store_rows(qt, pl, y + (long long)t * kT * p.c.y.sn, p.c.y.sn, g.len - t * kT);
     }
+    before = buf;
+    buf = buf == 2 ? 0 : buf + 1;
+    phase ^= buf == 0;
   }
   __syncthreads();
   finish<3, 2>(b, kColumns);
