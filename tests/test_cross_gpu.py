@@ -339,3 +339,30 @@ def test_a_decoder_layer_step_by_step():
     # two orders of the same fp32 sums, of 170 terms at most; the outputs are means of |v| < 6
     assert (h - whole).abs().max() <= 2.0 ** -18 * whole.abs().max()
     assert (out - y).abs().max() <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("feature,normalise", [("elu1", True), ("exp", True), ("identity", False)])
+def test_gradients_are_the_differences(feature, normalise):
+    """fp32 calls against central differences of the calls themselves: sum(dy y) for small moves of q, k and v."""
+    c = Call(2, 4, 2, 40, 33, 16, F32, feature, normalise, cu_q=[0, 25, 40], scale=0.5).run()
+    grads, x = [t.double() for t in (c.dq, c.dk, c.dv)], [c.q, c.k, c.v]
+
+    def value(q, k, v):
+        c.q, c.k, c.v = q, k, v
+        c.run(backward=False)
+        return (c.dy.double() * c.y.double()).sum(), (c.dy.double() * c.y.double()).abs().sum()
+
+    for n in range(3):
+        for seed in range(3):
+            m = rand(x[n].shape, F32, 10 + seed)
+            step = 2.0 ** -8
+            lo, hi = list(x), list(x)
+            lo[n], hi[n] = lo[n] - step * m, hi[n] + step * m
+            (a, size), (b, _) = value(*hi), value(*lo)
+            grad = (grads[n] * m.double()).sum()
+            terms = (grads[n] * m.double()).abs().sum()
+            # what a difference leaves out: step^2 / 6 of the third derivative, whose terms are the first's times at most
+            # 8 |m|^2 (|m| < 5) through phi and the quotient; where ELU + 1 changes its form the second derivative jumps by
+            # at most 1, for the 2 x 5 step of the values that a move takes there: step / 4 of the terms.  fp32 values of y:
+            # 2^-18 of their sum over the 2 steps
+            assert abs((a - b) / (2 * step) - grad) <= terms * (step ** 2 * 40 + step / 4 * (feature == "elu1")) + size * 2.0 ** -18 / step

@@ -129,3 +129,59 @@ def test_binding_refusals():
         a.update(bad)
         with pytest.raises(ValueError):
             binding.gated_scan_step(**a)
+
+
+def test_a_call_runs_on_its_tensors_device(monkeypatch):
+    """With another device current the binding makes that of the tensors current around the call, takes its stream,
+    and goes back also when the call fails."""
+    log = []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            log.append(("enter", self.index))
+
+        def __exit__(self, *_):
+            log.append(("exit", self.index))
+
+    class Entries:
+        status = OK
+
+        def gated_scan_step(self, *args):
+            log.append(("call", args))
+            return self.status
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(binding, "_lib", Entries())
+    binding._call_on("gated_scan_step", 1, None, 7)
+    assert log == [("enter", 1), ("call", (7, 1001)), ("exit", 1)]
+    log.clear()
+    binding._call_on("gated_scan_step", 0, Stream(), 7)
+    assert log == [("call", (7, 77))]
+    log.clear()
+    monkeypatch.setattr(binding, "status_string", lambda status: "refused")
+    binding._lib.status = INVALID
+    with pytest.raises(binding.MhlaError):
+        binding._call_on("gated_scan_step", 1, None, 7)
+    assert [e[0] for e in log] == ["enter", "call", "exit"]
+
+
+def test_tensors_of_two_devices_are_refused():
+    class Tensor:
+        def __init__(self, index):
+            self.index, self.is_cuda, self.device = index, index >= 0, f"cuda:{index}" if index >= 0 else "cpu"
+
+        def get_device(self):
+            return self.index
+
+    assert binding._one_device(Tensor(1), None, Tensor(1)) == 1
+    for other in (0, -1):
+        with pytest.raises(ValueError):
+            binding._one_device(Tensor(1), Tensor(other))

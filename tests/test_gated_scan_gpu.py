@@ -165,6 +165,26 @@ def test_clusters(B, N, D, dtype):
             assert (a - b).abs().max() <= tol * b.abs().max()
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("B", [1, 5, 8, 10, 14, 15, 16, 19, 23, 29, 37, 48, 80])
+def test_clusters_of_every_size(B, packed):
+    """64 channels of B rows of 4500 tokens (packed: 64 B channels): chains whose clusters have from sixteen blocks down to
+    one, powers of two or not, the last round of tiles short."""
+    N, D = 4500, 64
+    gate = GATES[B % 3]
+    shape = (1, N, 64 * B) if packed else (B, N, D)
+    cu = [0, 1000, 1001, 4099, N] if packed else None
+    x, dy, g = rand(*shape, seed=1, dtype=BF), rand(*shape, seed=2, dtype=BF), gate_values(shape, gate, BF, 3)
+    y, dx, dg = (torch.empty_like(x) for _ in range(3))
+    ck, kw = kept(x), dict(gate=gate, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda") if packed else None)
+    lib.gated_scan_forward(x, g, y, checkpoints=ck, **kw)
+    lib.gated_scan_backward(x, g, dy, ck, dx, dg, **kw)
+    for s in (slice(0, 8), slice(shape[2] - 8, shape[2])):
+        part = [t[-1:, :, s] for t in (x, g, y, dy, dx, dg)]
+        check_forward(*part[:3], gate, cu)
+        check_backward(part[0], part[1], *part[3:], gate, cu)
+
+
 def test_equal_calls_give_equal_bits():
     x, g, dy = rand(1, 7000, 512, seed=1, dtype=BF), gate_values((1, 7000, 512), "sigmoid", BF, 2), rand(1, 7000, 512, seed=3, dtype=BF)
     out = []

@@ -19,10 +19,13 @@ class SmemOptIn {
   cudaError_t ensure(const void* fn, int bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+    return e == cudaSuccess ? ensure(fn, bytes, dev) : e;
+  }
+  // (dev: the current device)
+  cudaError_t ensure(const void* fn, int bytes, int dev) {
     std::lock_guard<std::mutex> lk(mu_);
     if (dev < 64 && ((done_ >> dev) & 1ull)) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && dev < 64) done_ |= 1ull << dev;
     return e;
   }

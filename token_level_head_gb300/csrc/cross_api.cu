@@ -13,7 +13,8 @@ namespace mhla {
 namespace {
 
 // The kernels that a call runs on, as far as the segments go: a segment's tokens are a multiple of `unit`, and `slots`
-// blocks (a segment of a head each) fill the SMs.
+// blocks (a segment of a head each) fill the SMs.  The FP32 kernels' unit is half of a tile of theirs: forward and gradients
+// of 2003 queries and 1501 keys of 6 heads, d = 64, with segments of 128 tokens 99 us, of 64 72, of 32 64.
 struct Kind {
   int unit, slots;
 };

@@ -6,13 +6,18 @@
 // through shared memory; then every thread knows the state before its rows and runs them once more.  The gradient
 // runs the same way from the end: c_t = a_t (dy_t + c_{t+1}), G_t = dy_t + c_{t+1}.
 //
-// Bound: memory (forward 3 tensors, backward 5), next to it the instructions (at the memory's rate an SM has 32 a bf16
-// value and lane forwards, 53 backwards).  A block takes a tile of rows and LW lanes of channels; tiles behind one another
-// are taken by the blocks of a cluster, which exchange their (A, B) through distributed shared memory, and a cluster walks
-// along the sequence.  So x and g are read once and no memory, flag or wait is shared between clusters.
+// Bound: memory (forward 3 tensors, backward 5), next to it the instructions of the gates and of two passes over a tile (an
+// SM that two blocks fill issues in half of its cycles; the rest are the waits of a tile for the one before).  A block takes a
+// tile of rows and LW lanes of channels; tiles behind one another are taken by the blocks of a cluster, which exchange their
+// (A, B) through distributed shared memory, and a cluster walks along the sequence.  So x and g are read once and no memory,
+// flag or wait is shared between clusters.
+// Measured, whole calls: 65,536 x 1024 bf16, log, 91 us (4.5 TB/s); 77 x 1024 bf16 8.3; forward and backward of 4 x 8192 x 1024
+// bf16, sigmoid, 139 (3.9 TB/s), of 20,011 packed x 384 fp32, decay, 78 (3.1 TB/s); the step of 256 x 8192 bf16 8.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "gated_scan.h"
 #include "retention.cuh"
@@ -24,10 +29,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the tiles,
 constexpr int kBlock = kThreads + 32;                  // and a warp that carries the state over the tiles (exchange)
-constexpr int kWideCluster = 4, kNarrowCluster = 8;    // blocks of a cluster at most, with 128 bytes of channels and with 64
+constexpr int kWideCluster = 6, kNarrowCluster = 16;   // blocks of a cluster at most, with 128 bytes of channels and with 64
 constexpr int P = 1, V = 2 * P;  // channels of a thread: a pair, so that a warp of bf16 has a row of 128 bytes to itself
 
-// A thread's rows of a tile (32 values each of a and b in registers) and the lanes of 128 bytes of channels.
+// A thread's rows of a tile and the lanes of 128 bytes of channels.  Half of the values for fp32, whose tiles are as many bytes.
 template <typename T>
 struct Tile;
 template <>
@@ -387,11 +392,15 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
       } else {
         cg::cluster_group cl = cg::this_cluster();
 #pragma unroll
-        for (int i = 0; i < MOST; ++i)
-          if (i < n) {
-            cl.map_shared_rank(&s.ba[par][rank][0], i)[c] = A;
-            cl.map_shared_rank(&s.bb[par][rank][0], i)[c] = B;
-          }
+        for (int j = 0; j < MOST; j += 8) {
+          if (j >= n) break;
+#pragma unroll
+          for (int i = j; i < MOST && i < j + 8; ++i)
+            if (i < n) {
+              cl.map_shared_rank(&s.ba[par][rank][0], i)[c] = A;
+              cl.map_shared_rank(&s.bb[par][rank][0], i)[c] = B;
+            }
+        }
       }
     }
     if (n == 1) continue;
@@ -404,9 +413,13 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
       if (CW % 32 != 0 && c >= CW) continue;
       float h = running[k], mine = h;
 #pragma unroll
-      for (int i = 0; i < MOST; ++i) {
-        if (i == rank) mine = h;
-        if (i < n) h = carry_on<PACKED>(s.ba[par][i][c], s.bb[par][i][c], h);
+      for (int j = 0; j < MOST; j += 8) {
+        if (j >= n) break;
+#pragma unroll
+        for (int i = j; i < MOST && i < j + 8; ++i) {
+          if (i == rank) mine = h;
+          if (i < n) h = carry_on<PACKED>(s.ba[par][i][c], s.bb[par][i][c], h);
+        }
       }
       s.carry[par][c] = mine;
       running[k] = h;
@@ -483,6 +496,11 @@ __device__ __forceinline__ void copies_wait1() { asm volatile("cp.async.wait_gro
 __device__ __forceinline__ void copies_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // ---- forward
+// A tile's rows twice, from shared memory: folded into (A, B) while the state that enters the tile before is on its way, and
+// run with that state.  The gates are taken both times: kept in registers they would cost the second block of an SM (one
+// block an SM: 212 us and more for the forward and backward of 4 x 8192 x 1024, two 139).
+// The look ahead: log gates of 65,536 x 1024 109 us against 125 without it; sigmoid gates of 4 x 8192 x 1024 58 against 53,
+// the one case that it costs (its clusters fill the SMs, so the waits are another block's to fill).
 template <typename T, int GATE, int LW, bool PACKED>
 __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
   using Raw = typename Io<T, P>::Raw;
@@ -671,7 +689,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
 
 // ---- backward
 // A thread's rows three times: the runs of both directions; G from the last row on; h from the first row on, with what
-// goes out.  x, g and dy stay in registers as they came; the sigmoid is taken again in the third.
+// goes out.  The gates of the first two stay in registers, the third takes them again.
 template <typename T, int GATE, int LW, bool PACKED>
 __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
   using Raw = typename Io<T, P>::Raw;
@@ -878,15 +896,15 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
       if (first >> r & 1) start(r, h);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
+        const Gate gt = gate_of<T, GATE>(gv[i]);
         if (GATE == GATED_SCAN_SIGMOID) {
-          const Gate gt = gate_of<T, GATE>(gv[i]);
           ox[i] = mul2(gt.rest, G[r][i]);
           og[i] = mul2(mul2(gt.low, ox[i]), fma2(xv[i], both(-1.f), h[i]));
           h[i] = fma2(gt.a, h[i], mul2(gt.rest, xv[i]));
         } else {
           ox[i] = G[r][i];
-          og[i] = mul2(GATE == GATED_SCAN_LOG ? mul2(a[r][i], G[r][i]) : G[r][i], h[i]);
-          h[i] = fma2(a[r][i], h[i], xv[i]);
+          og[i] = mul2(GATE == GATED_SCAN_LOG ? mul2(gt.a, G[r][i]) : G[r][i], h[i]);
+          h[i] = fma2(gt.a, h[i], xv[i]);
         }
       }
       if (out >> r & 1) {
@@ -901,6 +919,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
 }
 
 // ---- one token for every row: a block a row and a run of channels
+// Bound by the call (launch 2 to 3 us, the binding 4): 256 x 8192 bf16 8 us, of it 4.3 the floor of its 29 MB.
 constexpr int kStepPairs = 2;
 template <typename T, int GATE>
 __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_constant__ ScanArgs p) {
@@ -933,61 +952,125 @@ __global__ void __launch_bounds__(128) gated_scan_step_kernel(const __grid_const
 }
 
 // ---- host
-// Blocks of a cluster: as many as the SMs need (two blocks each) and the tiles give, a power of two.
-int cluster_of(long long chains, int tiles, int most) {
-  int n = 1;
-  while (n < most && chains * n < kRetSms && n < tiles) n *= 2;
-  return n;
-}
+// Blocks of a cluster: as many as there are places for with all clusters running at once, which the SMs of the processing
+// clusters decide (a cluster has to lie within one), so the driver is asked, once a kernel and device.  Forward and backward
+// of 20,011 packed x 384 fp32 (24 chains): 6 blocks 115 us, 8 blocks 88, 10 blocks 77, 11, of which one cluster has to wait for
+// the others, 125; 4 x 8192 x 1024 bf16 (64 chains): 4 blocks 140, 8, in two turns, 157.
+class ClusterFit {
+ public:
+  // The most blocks, up to `most`, of which `chains` clusters run at once; 1 if none do.
+  int blocks(int dev, const void* kernel, int smem, long long chains, int most) {
+    if (most <= 1 || dev >= kDevices) return 1;
+    if (!known_[dev].load(std::memory_order_acquire)) ask(dev, kernel, smem);
+    int n = most;
+    while (n > 1 && fit_[dev][n] < chains) --n;
+    return n;
+  }
 
+ private:
+  void ask(int dev, const void* kernel, int smem) {
+    std::lock_guard<std::mutex> lk(mu_);
+    if (!known_[dev].load(std::memory_order_relaxed)) {
+      // (more than 8 blocks are not portable; every cluster of a kernel here may have them)
+      const bool large = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      for (int n = 2; n <= kNarrowCluster; ++n) {
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim = {(unsigned)n, 1, 1};
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)n);
+        cfg.blockDim = dim3(kBlock);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        int k = 0;
+        if ((n > 8 && !large) || cudaOccupancyMaxActiveClusters(&k, kernel, &cfg) != cudaSuccess) k = 0;
+        fit_[dev][n] = (unsigned short)std::min(k, 65535);
+      }
+      (void)cudaGetLastError();  // (a size that is refused has no clusters)
+      known_[dev].store(true, std::memory_order_release);
+    }
+  }
+
+  static constexpr int kDevices = 16;
+  std::mutex mu_;
+  std::atomic<bool> known_[kDevices] = {};
+  unsigned short fit_[kDevices][kNarrowCluster + 1] = {};
+};
+
+struct Plan {
+  long long chains;
+  int cluster;
+  long long turns;  // tiles that a place on an SM takes, one behind the other
+};
 template <typename T, int GATE, int LW, bool PACKED>
-cudaError_t launch_scan(const ScanArgs& a, bool backward, cudaStream_t st) {
-  constexpr int CW = V * LW, ROWS = kThreads / LW * Tile<T>::R;
-  void (*kernel)(ScanArgs, int) =
-      backward ? gated_scan_backward_kernel<T, GATE, LW, PACKED> : gated_scan_forward_kernel<T, GATE, LW, PACKED>;
-  const long long chains = (PACKED ? 1ll : a.B) * ((a.D + CW - 1) / CW);
-  const int n = cluster_of(chains, ret_pieces(a.N, ROWS), ScanShared<T, LW>::MOST);
-  if (chains * n > 0x7fffffffll) return cudaErrorInvalidValue;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim = {(unsigned)n, 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(chains * n));
-  cfg.blockDim = dim3(kBlock);
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = n > 1 ? 2 : 1;
-  static SmemOptIn opt[2];
-  const int smem = 6 * Stage<T, LW>::ELEMS * (int)sizeof(T);  // forward three tiles of two tensors, backward two of three
-  cudaError_t e = opt[backward].ensure((const void*)kernel, smem);
+struct Scan {
+  static constexpr int CW = V * LW, ROWS = kThreads / LW * Tile<T>::R;
+  static constexpr int kSmem = 6 * Stage<T, LW>::ELEMS * (int)sizeof(T);  // forward three tiles of two tensors, backward two of three
+  using Kernel = void (*)(ScanArgs, int);
+  static Kernel kernel(bool backward) {
+    return backward ? gated_scan_backward_kernel<T, GATE, LW, PACKED> : gated_scan_forward_kernel<T, GATE, LW, PACKED>;
+  }
+  static cudaError_t plan(const ScanArgs& a, bool backward, int dev, Plan* p) {
+    static SmemOptIn opt[2];
+    static ClusterFit fit[2];
+    const int tiles = ret_pieces(a.N, ROWS);
+    p->chains = (PACKED ? 1ll : a.B) * ((a.D + CW - 1) / CW);
+    const cudaError_t e = opt[backward].ensure((const void*)kernel(backward), kSmem, dev);
+    if (e != cudaSuccess) return e;
+    p->cluster = fit[backward].blocks(dev, (const void*)kernel(backward), kSmem, p->chains, std::min(ScanShared<T, LW>::MOST, tiles));
+    const long long places = 2ll * kRetSms;
+    p->turns = (p->cluster > 1 ? 1 : (p->chains + places - 1) / places) * ret_pieces(tiles, p->cluster);
+    return p->chains * p->cluster > 0x7fffffffll ? cudaErrorInvalidValue : cudaSuccess;
+  }
+  static cudaError_t launch(const ScanArgs& a, bool backward, const Plan& p, cudaStream_t st) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim = {(unsigned)p.cluster, 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.chains * p.cluster));
+    cfg.blockDim = dim3(kBlock);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel(backward), a, p.cluster);
+    note_launch();
+    return e;
+  }
+};
+
+// The lanes of a row, 128 bytes of channels or 64: those with which a place on an SM takes fewer tiles, and 128 where it is the
+// same (a tile has as many bytes either way).  128 bytes against 64: 4 x 8192 x 1024 bf16 (64 chains of 128 bytes, 16 tiles
+// each way) 140 us against 147; 65,536 x 1024 bf16 (16 chains) 160 against 91; 20,011 x 384 fp32 (12 chains) 132 against 88.
+// 32 bytes, where 64 fill the SMs too: 111 against 100.
+template <typename T, int GATE, bool PACKED>
+cudaError_t launch_gate(const ScanArgs& a, bool backward, cudaStream_t st) {
+  using Wide = Scan<T, GATE, Tile<T>::WIDE, PACKED>;
+  using Narrow = Scan<T, GATE, Tile<T>::WIDE / 2, PACKED>;
+  Plan w, n{};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = Wide::plan(a, backward, dev, &w);
+  if (e == cudaSuccess && w.turns > 1) e = Narrow::plan(a, backward, dev, &n);
   if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = smem;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, n);
-  note_launch();
-  return e;
+  return w.turns > 1 && n.turns < w.turns ? Narrow::launch(a, backward, n, st) : Wide::launch(a, backward, w, st);
 }
 
-// The lanes of a row: the most (128 bytes of channels) with which the chains, in clusters, fill the SMs.
-template <typename T, int GATE>
-cudaError_t launch_gate(const ScanArgs& a, bool backward, cudaStream_t st) {
-  constexpr int WIDE = Tile<T>::WIDE;
-  const int cw = V * WIDE;
-  const long long chains = (a.cu ? 1ll : a.B) * ((a.D + cw - 1) / cw);
-  const bool narrow = chains * std::min(kWideCluster, ret_pieces(a.N, kThreads / WIDE * Tile<T>::R)) < kRetSms;
-  if (a.cu != nullptr)
-    return narrow ? launch_scan<T, GATE, WIDE / 2, true>(a, backward, st) : launch_scan<T, GATE, WIDE, true>(a, backward, st);
-  return narrow ? launch_scan<T, GATE, WIDE / 2, false>(a, backward, st) : launch_scan<T, GATE, WIDE, false>(a, backward, st);
+template <typename T, bool PACKED>
+cudaError_t launch_gated(const ScanArgs& a, bool backward, cudaStream_t st) {
+  switch (a.gate) {
+    case GATED_SCAN_DECAY: return launch_gate<T, GATED_SCAN_DECAY, PACKED>(a, backward, st);
+    case GATED_SCAN_LOG: return launch_gate<T, GATED_SCAN_LOG, PACKED>(a, backward, st);
+    default: return launch_gate<T, GATED_SCAN_SIGMOID, PACKED>(a, backward, st);
+  }
 }
 
 template <typename T>
 cudaError_t launch_type(const ScanArgs& a, bool backward, cudaStream_t st) {
-  switch (a.gate) {
-    case GATED_SCAN_DECAY: return launch_gate<T, GATED_SCAN_DECAY>(a, backward, st);
-    case GATED_SCAN_LOG: return launch_gate<T, GATED_SCAN_LOG>(a, backward, st);
-    default: return launch_gate<T, GATED_SCAN_SIGMOID>(a, backward, st);
-  }
+  return a.cu != nullptr ? launch_gated<T, true>(a, backward, st) : launch_gated<T, false>(a, backward, st);
 }
 
 template <typename T, int GATE>
