@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "gated_scan.h"
 #include "retention.cuh"
@@ -132,13 +133,10 @@ __device__ __forceinline__ float exp2_of(float x) {
 // exp(x).  bf16 tensors: the hardware's base-2 exponential of x log2 e (log2 e = 1.4426950408889634), off by
 // |x| 2^-24 + 2^-22 at most, far below what a bf16 gate says; fp32: expf.  Not-a-number stays.
 template <typename T>
-__device__ __forceinline__ float exp_of(float x) {
-  return sizeof(T) == 4 ? expf(x) : exp2_of(x * 1.4426950408889634f);
-}
-__device__ __forceinline__ float min_nan(float a, float b) {  // not-a-number stays
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+__device__ __forceinline__ float2 exp_of(float2 x) {
+  if (sizeof(T) == 4) return make_float2(expf(x.x), expf(x.y));
+  const float2 t = mul2(x, both(1.4426950408889634f));
+  return make_float2(exp2_of(t.x), exp2_of(t.y));
 }
 __device__ __forceinline__ float rcp_of(float x) {
   float r;
@@ -151,28 +149,22 @@ struct Gate {
   float2 rest;  // sigmoid: 1 - a, the factor of x
   float2 low;   // sigmoid: a once more, with all its digits also where it is small
 };
-// sigmoid, with e = exp(-g): 1 - a = e / (1 + e); a = 1 - (1 - a), so that gates near 1 are rounded once (a long memory
-// multiplies thousands of them, and their errors) and all are within 2^-24; low = 1 / (1 + e).  e stops at 2^126, where
-// e / (1 + e) is still a number.  Not-a-number stays.
+// sigmoid, with e = exp(g): 1 - a = 1 / (1 + e), which needs no case for either end; a = 1 - (1 - a), so that gates near 1 are
+// rounded once (a long memory multiplies thousands of them, and their errors) and all are within 2^-24; low = e / (1 + e) where
+// that is below 2/3.  Not-a-number stays.
 template <typename T, int GATE>
 __device__ __forceinline__ Gate gate_of(float2 g) {
   Gate k;
   if (GATE == GATED_SCAN_DECAY) {
     k.a = g;
   } else if (GATE == GATED_SCAN_LOG) {
-    k.a = make_float2(exp_of<T>(g.x), exp_of<T>(g.y));
+    k.a = exp_of<T>(g);
   } else {
-    float2 e;
-    if (sizeof(T) == 4) {
-      e = make_float2(expf(min_nan(-g.x, 87.f)), expf(min_nan(-g.y, 87.f)));
-    } else {
-      const float2 t = mul2(g, both(-1.4426950408889634f));
-      e = make_float2(exp2_of(min_nan(t.x, 126.f)), exp2_of(min_nan(t.y, 126.f)));
-    }
-    const float2 d = add2(e, both(1.f));
-    k.low = make_float2(rcp_of(d.x), rcp_of(d.y));
-    k.rest = mul2(e, k.low);
+    const float2 e = exp_of<T>(g), d = add2(e, both(1.f));
+    k.rest = make_float2(rcp_of(d.x), rcp_of(d.y));
     k.a = fma2(k.rest, both(-1.f), both(1.f));
+    const float2 low = mul2(e, k.rest);
+    k.low = make_float2(e.x < 2.f ? low.x : k.a.x, e.y < 2.f ? low.y : k.a.y);
   }
   return k;
 }
@@ -515,6 +507,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
   const int cl = (tid % LW) * V, c = c0 + cl;         // the thread's channels
   const int r0 = (warp * GROUPS + lane / LW) * kR;    // and rows of the tile
+  constexpr unsigned kAll = (1u << kR) - 1;           // (plain: a thread's rows that are all tokens, of one sequence's middle)
   const int delta = St::SWAP && (r0 / kR & 1) ? CW : 0;
   const bool on = c < p.D;
   const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb;
@@ -585,28 +578,38 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     float2 wA[P], wB[P];
     fill(n.A, 1.f);
     fill(n.B, 0.f);
-    const bool whole = n.m.live == (1u << kR) - 1;
+    const auto fold = [&](auto plain) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      float2 a[P], b[P];
-      row_of(sx, r, a, b);
-      if (p.load && on && n.m.first >> r & 1) {
-        start_of(i, r, n.h0);
+      for (int r = 0; r < kR; ++r) {
+        float2 a[P], b[P];
+        row_of(sx, r, a, b);
+        if constexpr (!plain) {
+          if (p.load && on && n.m.first >> r & 1) {
+            start_of(i, r, n.h0);
 #pragma unroll
-        for (int k = 0; k < P; ++k) b[k] = fma2(a[k], n.h0[k], b[k]);
-      }
-      if (!whole && !(n.m.live >> r & 1)) continue;
+            for (int k = 0; k < P; ++k) b[k] = fma2(a[k], n.h0[k], b[k]);
+          }
+          if (!(n.m.live >> r & 1)) continue;
+          if (PACKED && (n.m.first >> r & 1)) {
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        if (PACKED && (n.m.first >> r & 1)) {
-          n.B[k] = b[k];
-          n.A[k] = both(kCut);
-        } else {
+            for (int k = 0; k < P; ++k) {
+              n.B[k] = b[k];
+              n.A[k] = both(kCut);
+            }
+            continue;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
           n.B[k] = fma2(a[k], n.B[k], b[k]);
           n.A[k] = mul2(n.A[k], a[k]);
         }
       }
-    }
+    };
+    if (n.m.live == kAll && n.m.first == 0)
+      fold(std::true_type());
+    else
+      fold(std::false_type());
     scan_warp<LW, false, PACKED>(n.A, n.B, wA, wB, lane);
     if (lane / LW == GROUPS - 1) {
       store(&s.wa[par][warp][cl], wA);
@@ -659,30 +662,42 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     const T* sx = stage + i % 3 * 2 * St::ELEMS + r0 * CW + cl;
     T* py = y + row * p.y.sn;
     const unsigned out = on ? now.m.live : 0, ends = p.states != nullptr && on ? now.m.last : 0;
+    const auto run = [&](auto plain) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      float2 a[P], b[P];
-      row_of(sx, r, a, b);
-      if (p.load && on && now.m.first >> r & 1) {
-        float2 h0[P];
-        if (now.m.first >> r == 1) {
+      for (int r = 0; r < kR; ++r) {
+        float2 a[P], b[P];
+        row_of(sx, r, a, b);
+        bool cut = false;
+        if constexpr (!plain) {
+          if (p.load && on && now.m.first >> r & 1) {
+            float2 h0[P];
+            if (now.m.first >> r == 1) {
 #pragma unroll
-          for (int k = 0; k < P; ++k) h0[k] = now.h0[k];
-        } else {
-          start_of(i, r, h0);
+              for (int k = 0; k < P; ++k) h0[k] = now.h0[k];
+            } else {
+              start_of(i, r, h0);
+            }
+#pragma unroll
+            for (int k = 0; k < P; ++k) b[k] = fma2(a[k], h0[k], b[k]);
+          }
+          cut = PACKED && (now.m.first >> r & 1);
         }
 #pragma unroll
-        for (int k = 0; k < P; ++k) b[k] = fma2(a[k], h0[k], b[k]);
+        for (int k = 0; k < P; ++k) h[k] = cut ? b[k] : fma2(a[k], h[k], b[k]);
+        if (plain || out >> r & 1) store(py, h);
+        py = next_row(py, p.y.sn);
+        if constexpr (!plain) {
+          if (ends >> r & 1) {
+            const int slot = slot_of(p.slots, p.n_slots, sequence_of(i, r));
+            if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
+          }
+        }
       }
-#pragma unroll
-      for (int k = 0; k < P; ++k) h[k] = PACKED && (now.m.first >> r & 1) ? b[k] : fma2(a[k], h[k], b[k]);
-      if (out >> r & 1) store(py, h);
-      py = next_row(py, p.y.sn);
-      if (ends >> r & 1) {
-        const int slot = slot_of(p.slots, p.n_slots, sequence_of(i, r));
-        if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
-      }
-    }
+    };
+    if (out == kAll && now.m.first == 0 && ends == 0)
+      run(std::true_type());
+    else
+      run(std::false_type());
   }
   if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one writes its shared memory
 }
@@ -706,6 +721,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
   const int cols = (p.D + CW - 1) / CW, batch = chain / cols, c0 = (chain % cols) * CW;
   const int cl = (tid % LW) * V, c = c0 + cl;
   const int r0 = (warp * GROUPS + lane / LW) * kR;
+  constexpr unsigned kAll = (1u << kR) - 1;  // (plain: as in the forward)
   const int delta = St::SWAP && (r0 / kR & 1) ? CW : 0;
   const bool on = c < p.D;
   const T* x = static_cast<const T*>(p.x.p) + (long long)batch * p.x.sb;
@@ -791,26 +807,42 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     float2 a[kR][P], rA[P], rB[P], wA[P], wB[P];
     fill(rA, 1.f);
     fill(rB, 0.f);
+    const bool is_plain = m.live == kAll && on && (first | last) == 0;
+    const auto fold = [&](auto plain) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      float2 gv[P], d[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
-      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sd, r, delta)), d);
-      if (last >> r & 1) {
-        float2 e[P];
-        end(r, e);
+      for (int r = 0; r < kR; ++r) {
+        float2 gv[P], d[P];
+        unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
+        unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sd, r, delta)), d);
 #pragma unroll
-        for (int i = 0; i < P; ++i) d[i] = add2(d[i], e[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        a[r][i] = gate_of<T, GATE>(gv[i]).a;
-        if (!(m.live >> r & 1)) a[r][i] = both(1.f);
+        for (int i = 0; i < P; ++i) a[r][i] = gate_of<T, GATE>(gv[i]).a;
         // row r acts before the rows so far, c -> rA (a (dy + c)) + rB
-        rB[i] = carry_on<PACKED>(rA[i], rB[i], mul2(a[r][i], d[i]));
-        rA[i] = join<PACKED>(rA[i], PACKED && (last >> r & 1) ? both(kCut) : a[r][i]);
+        if constexpr (plain) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            rB[i] = fma2(rA[i], mul2(a[r][i], d[i]), rB[i]);
+            rA[i] = mul2(rA[i], a[r][i]);
+          }
+        } else {
+          if (last >> r & 1) {
+            float2 e[P];
+            end(r, e);
+#pragma unroll
+            for (int i = 0; i < P; ++i) d[i] = add2(d[i], e[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            if (!(m.live >> r & 1)) a[r][i] = both(1.f);
+            rB[i] = carry_on<PACKED>(rA[i], rB[i], mul2(a[r][i], d[i]));
+            rA[i] = join<PACKED>(rA[i], PACKED && (last >> r & 1) ? both(kCut) : a[r][i]);
+          }
+        }
       }
-    }
+    };
+    if (is_plain)
+      fold(std::true_type());
+    else
+      fold(std::false_type());
     scan_warp<LW, true, PACKED>(rA, rB, wA, wB, lane);
     if (lane / LW == 0) {
       store(&s.wa[par][warp][cl], wA);
@@ -832,7 +864,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     for (int r = 0; r < kR; ++r) {
       float2 xv[P];
       unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sx, r, delta)), xv);
-      if (first >> r & 1) {
+      if (!is_plain && first >> r & 1) {
         start(r, fB);
         if (PACKED) fill(fA, kCut);  // (dense: the state before the first row is zero)
       }
@@ -862,58 +894,67 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
 #pragma unroll
     for (int i = 0; i < P; ++i) k[i] = carry_on<PACKED>(rA[i], rB[i], k[i]);
     const unsigned out = on ? m.live : 0, starts = p.dh0 != nullptr && on ? first : 0;
-    float2 G[kR][P];
-#pragma unroll
-    for (int r = kR - 1; r >= 0; --r) {
-      float2 d[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sd, r, delta)), d);
-      if (last >> r & 1) end(r, k);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        G[r][i] = add2(d[i], k[i]);
-        k[i] = mul2(a[r][i], G[r][i]);
-      }
-      if (starts >> r & 1) {
-        if (GATE == GATED_SCAN_SIGMOID) {  // (a small gate with all its digits)
-          float2 gv[P];
-          unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float2 low = gate_of<T, GATE>(gv[i]).low;
-            k[i] = mul2(make_float2(gv[i].x > 0.f ? a[r][i].x : low.x, gv[i].y > 0.f ? a[r][i].y : low.y), G[r][i]);
-          }
-        }
-        store(p.dh0 + (long long)sequence_of(r) * p.D + c, k);
-      }
-    }
     const long long row = (long long)row0 + r0;
     T *px = dx + row * p.dx.sn, *pg = dg + row * p.dg.sn;
+    const auto run = [&](auto plain) {
+      float2 G[kR][P];
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      float2 gv[P], xv[P], ox[P], og[P];
-      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
-      unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sx, r, delta)), xv);
-      if (first >> r & 1) start(r, h);
+      for (int r = kR - 1; r >= 0; --r) {
+        float2 d[P];
+        unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sd, r, delta)), d);
+        if constexpr (!plain) {
+          if (last >> r & 1) end(r, k);
+        }
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const Gate gt = gate_of<T, GATE>(gv[i]);
-        if (GATE == GATED_SCAN_SIGMOID) {
-          ox[i] = mul2(gt.rest, G[r][i]);
-          og[i] = mul2(mul2(gt.low, ox[i]), fma2(xv[i], both(-1.f), h[i]));
-          h[i] = fma2(gt.a, h[i], mul2(gt.rest, xv[i]));
-        } else {
-          ox[i] = G[r][i];
-          og[i] = mul2(GATE == GATED_SCAN_LOG ? mul2(gt.a, G[r][i]) : G[r][i], h[i]);
-          h[i] = fma2(gt.a, h[i], xv[i]);
+        for (int i = 0; i < P; ++i) {
+          G[r][i] = add2(d[i], k[i]);
+          k[i] = mul2(a[r][i], G[r][i]);
+        }
+        if constexpr (!plain) {
+          if (starts >> r & 1) {
+            if (GATE == GATED_SCAN_SIGMOID) {  // (a small gate with all its digits)
+              float2 gv[P];
+              unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
+#pragma unroll
+              for (int i = 0; i < P; ++i) k[i] = mul2(gate_of<T, GATE>(gv[i]).low, G[r][i]);
+            }
+            store(p.dh0 + (long long)sequence_of(r) * p.D + c, k);
+          }
         }
       }
-      if (out >> r & 1) {
-        store(px, ox);
-        store(pg, og);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        float2 gv[P], xv[P], ox[P], og[P];
+        unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
+        unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sx, r, delta)), xv);
+        if constexpr (!plain) {
+          if (first >> r & 1) start(r, h);
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const Gate gt = gate_of<T, GATE>(gv[i]);
+          if (GATE == GATED_SCAN_SIGMOID) {
+            ox[i] = mul2(gt.rest, G[r][i]);
+            og[i] = mul2(mul2(gt.low, ox[i]), fma2(xv[i], both(-1.f), h[i]));
+            h[i] = fma2(gt.a, h[i], mul2(gt.rest, xv[i]));
+          } else {
+            ox[i] = G[r][i];
+            og[i] = mul2(GATE == GATED_SCAN_LOG ? mul2(gt.a, G[r][i]) : G[r][i], h[i]);
+            h[i] = fma2(gt.a, h[i], xv[i]);
+          }
+        }
+        if (plain || out >> r & 1) {
+          store(px, ox);
+          store(pg, og);
+        }
+        px = next_row(px, p.dx.sn);
+        pg = next_row(pg, p.dg.sn);
       }
-      px = next_row(px, p.dx.sn);
-      pg = next_row(pg, p.dg.sn);
-    }
+    };
+    if (is_plain)
+      run(std::true_type());
+    else
+      run(std::false_type());
   }
   if (cluster > 1) cg::this_cluster().sync();
 }
