@@ -11,8 +11,8 @@
 // tile of rows and LW lanes of channels; tiles behind one another are taken by the blocks of a cluster, which exchange their
 // (A, B) through distributed shared memory, and a cluster walks along the sequence.  So x and g are read once and no memory,
 // flag or wait is shared between clusters.
-// Measured, whole calls: 65,536 x 1024 bf16, log, 91 us (4.5 TB/s); 77 x 1024 bf16 8.3; forward and backward of 4 x 8192 x 1024
-// bf16, sigmoid, 139 (3.9 TB/s), of 20,011 packed x 384 fp32, decay, 78 (3.1 TB/s); the step of 256 x 8192 bf16 8.
+// Measured, whole calls: 65,536 x 1024 bf16, log, 81 us (4.9 TB/s); 77 x 1024 bf16 8; forward and backward of 4 x 8192 x 1024
+// bf16, sigmoid, 125 (4.3 TB/s), of 20,011 packed x 384 fp32, decay, 77 (3.2 TB/s); the step of 256 x 8192 bf16 8.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -324,14 +324,15 @@ __device__ __forceinline__ void scan_warp(float2 (&A)[P], float2 (&B)[P], float2
 template <typename T, int LW>
 struct ScanShared {
   static constexpr int CW = V * LW, MOST = LW == Tile<T>::WIDE ? kWideCluster : kNarrowCluster;
-  float wa[2][kWarps][CW], wb[2][kWarps][CW];  // A, B of the warps, by the tile's parity
+  float wa[2][kWarps][CW], wb[2][kWarps][CW];  // A, B of the warps, by the tile's parity; then of what lies before them
   float ba[2][MOST][CW], bb[2][MOST][CW];      // of the cluster's blocks, which write them here
   float carry[2][CW];                          // the state entering the block's tile
 };
 
 // What goes on from tile to tile, in a warp of its own: as it has no other stores, the release of the cluster's barrier
 // waits for none (with the state carried by warps of the tiles each round waited for their outputs to arrive in L2).  The
-// block's warps have A, B in s.wa, s.wb and wait for s.carry.
+// block's warps have A, B in s.wa, s.wb and wait for s.carry.  It also leaves what lies before each warp in s.wa, s.wb (every
+// warp for itself over up to seven others: 65,536 x 1024 85 us against 81).
 // (Two barriers each, by the tile's parity: one side may be a tile ahead of the other.)
 __device__ __forceinline__ void block_sync(int par) { asm volatile("bar.sync %0, 288;" ::"r"(2 + par) : "memory"); }
 __device__ __forceinline__ void block_arrive(int par) { asm volatile("bar.arrive %0, 288;" ::"r"(2 + par) : "memory"); }
@@ -360,27 +361,27 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
   for (int k = 0; k < K; ++k) running[k] = 0.f;
   for (int t = 0, par = 0; t < rounds; ++t, par ^= 1) {
     block_sync(par);
-    if (n == 1) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (lane + 32 * k < CW) s.carry[par][lane + 32 * k] = running[k];
-      __syncwarp();
-      carry_arrive(par);
-    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = lane + 32 * k;
       if (CW % 32 != 0 && c >= CW) continue;
-      float A = 1.f, B = n == 1 ? running[k] : 0.f;
+      float A = 1.f, B = 0.f, fa[kWarps], fb[kWarps];
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
+      for (int w = 0; w < kWarps; ++w) {
+        fa[w] = s.wa[par][w][c];
+        fb[w] = s.wb[par][w][c];
+      }
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {  // what a warp had becomes what lies before it in the block
         const int w = REVERSE ? kWarps - 1 - i : i;
-        const float fa = s.wa[par][w][c];
-        B = carry_on<PACKED>(fa, s.wb[par][w][c], B);
-        A = join<PACKED>(fa, A);
+        s.wa[par][w][c] = A;
+        s.wb[par][w][c] = B;
+        B = carry_on<PACKED>(fa[w], fb[w], B);
+        A = join<PACKED>(fa[w], A);
       }
       if (n == 1) {
-        running[k] = B;
+        s.carry[par][c] = running[k];
+        running[k] = carry_on<PACKED>(A, B, running[k]);
       } else {
         cg::cluster_group cl = cg::this_cluster();
 #pragma unroll
@@ -395,7 +396,11 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
         }
       }
     }
-    if (n == 1) continue;
+    if (n == 1) {
+      __syncwarp();
+      carry_arrive(par);
+      continue;
+    }
     __syncwarp();
     cluster_arrive();
     cluster_wait();
@@ -420,14 +425,23 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
     carry_arrive(par);
   }
 }
-// The state before the warp: over the warps from `from` on (backwards: down to it).
-template <int CW, bool REVERSE, bool PACKED>
+// The state before the warp, once the carrying warp has been there.
+template <typename T, int LW, bool PACKED>
+__device__ __forceinline__ void state_before(const ScanShared<T, LW>& s, int par, int cl, int warp, float2 (&h)[P]) {
+  float2 A[P], B[P];
+  load_f(&s.carry[par][cl], h);
+  load_f(&s.wa[par][warp][cl], A);
+  load_f(&s.wb[par][warp][cl], B);
+#pragma unroll
+  for (int j = 0; j < P; ++j) h[j] = carry_on<PACKED>(A[j], B[j], h[j]);
+}
+// h over the warps from `from` on, up to the warp.
+template <int CW, bool PACKED>
 __device__ __forceinline__ void over_warps(const float (&wa)[kWarps][CW], const float (&wb)[kWarps][CW], int cl, int warp,
                                            int from, float2 (&h)[P]) {
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const int w = REVERSE ? kWarps - 1 - i : i;
-    if (REVERSE ? w > warp : w >= from && w < warp) {
+  for (int w = 0; w < kWarps; ++w) {
+    if (w >= from && w < warp) {
       float2 A[P], B[P];
       load_f(&wa[w][cl], A);
       load_f(&wb[w][cl], B);
@@ -490,9 +504,11 @@ __device__ __forceinline__ void copies_wait0() { asm volatile("cp.async.wait_gro
 // ---- forward
 // A tile's rows twice, from shared memory: folded into (A, B) while the state that enters the tile before is on its way, and
 // run with that state.  The gates are taken both times: kept in registers they would cost the second block of an SM (one
-// block an SM: 212 us and more for the forward and backward of 4 x 8192 x 1024, two 139).
-// The look ahead: log gates of 65,536 x 1024 109 us against 125 without it; sigmoid gates of 4 x 8192 x 1024 58 against 53,
-// the one case that it costs (its clusters fill the SMs, so the waits are another block's to fill).
+// block an SM: 212 us and more for the forward and backward of 4 x 8192 x 1024, where two took 139; four of half the threads 145).
+// The look ahead, when it came: log gates of 65,536 x 1024 109 us against 125 without it; sigmoid gates of 4 x 8192 x 1024 58
+// against 53, as its clusters fill the SMs and the waits are another block's to fill.
+// Plain rows, without a look at their marks: with the sigmoid below 139 us to 127 for the forward and backward of 4 x 8192 x
+// 1024.  Four channels a thread and half of the rows (fewer addresses, one more shuffle): 134 against 127.
 template <typename T, int GATE, int LW, bool PACKED>
 __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __grid_constant__ ScanArgs p, int cluster) {
   using Raw = typename Io<T, P>::Raw;
@@ -652,8 +668,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     }
     carry_sync(par);
     float2 h[P];
-    load_f(&s.carry[par][cl], h);
-    over_warps<CW, false, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, h);
+    state_before<T, LW, PACKED>(s, par, cl, warp, h);
 #pragma unroll
     for (int k = 0; k < P; ++k) h[k] = carry_on<PACKED>(now.A[k], now.B[k], h[k]);
     const int row = now.row;
@@ -882,15 +897,14 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
         store(&s.wb[par ^ 1][warp][cl], wB);
       }
       tile_sync();
-      over_warps<CW, false, PACKED>(s.wa[par ^ 1], s.wb[par ^ 1], cl, warp, from, h);
+      over_warps<CW, PACKED>(s.wa[par ^ 1], s.wb[par ^ 1], cl, warp, from, h);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) h[i] = carry_on<PACKED>(fA[i], fB[i], h[i]);
     give_wait(cluster > 1);
     carry_sync(par);
     float2 k[P];
-    load_f(&s.carry[par][cl], k);
-    over_warps<CW, true, PACKED>(s.wa[par], s.wb[par], cl, warp, 0, k);
+    state_before<T, LW, PACKED>(s, par, cl, warp, k);
 #pragma unroll
     for (int i = 0; i < P; ++i) k[i] = carry_on<PACKED>(rA[i], rB[i], k[i]);
     const unsigned out = on ? m.live : 0, starts = p.dh0 != nullptr && on ? first : 0;
