@@ -11,12 +11,12 @@
 // Bound: memory (2, 2, 3 and 4 tensors), next to it the instructions that take the features and turn tiles.  A block has a
 // segment of a head and walks over its tiles: a warp of its own issues the copies (TMA, into the buffer that is free) and the
 // MMAs, D / 8 warps take the features (a thread 32 columns of a row, in place in the 128-byte-swizzled tile), take the results
-// from tensor memory, put them into the tile's buffer and store 64 bytes of a row together.  Two blocks an SM for d = 64
-// (reads: three), one for d = 128, hide one another's waits.  Every wait is bounded (on time-out the block stops, sets the
-// status word and drains what it has in flight).
-// Measured, whole calls: 8 x 6 heads, 4096 queries, 77 keys, d 64: 22 us; 4 key heads of 65,536 keys, d 128, and 777 queries
-// of 16 heads: 41 (3.5 TB/s); forward and gradients of 8 x 6 heads, 4096 queries, 2048 keys, d 64: 80 (2.5 TB/s).  Next to
-// them the start of a kernel (barriers, tensor memory, S: 2 us) and, of the small ones, the launches.
+// from tensor memory and put them into the tile's buffer, whence TMA copies them out (a packed sequence's last tile: the warps,
+// as its rows end within it).  Two blocks an SM for d = 64 (reads: three), one for d = 128, hide one another's waits.  Every
+// wait is bounded (on time-out the block stops, sets the status word and drains what it has in flight).
+// Measured in a graph: states and read of 8 x 6 heads, 4096 queries, 77 keys, d 64: 17 us; of 4 key heads of 65,536 keys, d 128,
+// and 777 queries of 16 heads: 45 (3.1 TB/s); forward and gradients of 8 x 6 heads, 4096 queries, 2048 keys, d 64: 71 (2.8
+// TB/s), of 8 x 8 heads, d 128: 208 (2.6 TB/s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -48,6 +48,7 @@ struct Bars {
   uint64_t full[4];   // a tile's tensors landed (tx), by its buffer
   uint64_t ready[3];  // a tile's operands are written (the working warps)
   uint64_t mma[3];    // MMA commits
+  uint64_t out[2];    // a tile's results lie in its place
   uint64_t ready2, mma2;
   unsigned long long wait_ns;
   unsigned* status;
@@ -60,7 +61,9 @@ struct Bars {
 struct TcArgs {
   CrossArgs c;
   CUtensorMap a, b;            // the tile's tensors: states, key: k, v; read: q; query: q, dy
+  CUtensorMap c_map, d_map;    // what is written: read: y; query: dq; key: dk, dv
   int a_h, a_b, b_h, b_b;      // whether the tensors have heads and batch entries (stride not 0)
+  int c_h, c_b, d_h, d_b;
   unsigned long long wait_ns;
 };
 
@@ -180,6 +183,7 @@ __device__ __forceinline__ void setup(const TcArgs& p, Bars* b, uint32_t cols) {
     for (uint64_t& f : b->full) mbar_init(&f, 1);
     for (uint64_t& m : b->mma) mbar_init(&m, 1);
     for (uint64_t& r : b->ready) mbar_init(&r, blockDim.x / 32 - 1);
+    for (uint64_t& r : b->out) mbar_init(&r, blockDim.x / 32 - 1);
     mbar_init(&b->ready2, blockDim.x / 32 - 1);
     mbar_init(&b->mma2, 1);
     b->issued = b->mmas = b->mmas2 = 0;
@@ -231,52 +235,60 @@ __device__ __forceinline__ void load_tile(uint8_t* to, const CUtensorMap* m, int
       : "memory");
 }
 
+// One thread: a tile's rows to memory (rows behind the tensor are not), and the wait until its place may be written again.
+__device__ __forceinline__ void store_tile(const CUtensorMap* m, uint8_t* from, int row, int h, int b) {
+  asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %1, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(0), "r"(row), "r"(h), "r"(b), "r"(smem_u32(from))
+               : "memory");
+}
+__device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // A d x d fp32 matrix [r][c] as bf16 tiles of D rows, the high part and, where lo is given, the low part.
 template <int D>
 __device__ __forceinline__ void load_matrix(uint8_t* hi, uint8_t* lo, const float* from) {
+  constexpr int N = D * D / 8 / Tc<D>::kWork;
+  float2 f[N][4];
 #pragma unroll
-  for (int i = threadIdx.x; i < D * D / 8; i += Tc<D>::kWork) {
-    const int r = i / (D / 8), j = i % (D / 8);
-    float2 f[4];
-    load8(from + r * D + 8 * j, f);
-    const uint4 u = pack8(f);
+  for (int n = 0; n < N; ++n) {  // (all loads in flight)
+    const int i = threadIdx.x + n * Tc<D>::kWork;
+    load8(from + i * 8, f[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int i = threadIdx.x + n * Tc<D>::kWork, r = i / (D / 8), j = i % (D / 8);
+    const uint4 u = pack8(f[n]);
     *piece(hi, D, r, j) = u;
     if (lo != nullptr) {
-      remainder8(f, u);
-      *piece(lo, D, r, j) = pack8(f);
+      remainder8(f[n], u);
+      *piece(lo, D, r, j) = pack8(f[n]);
     }
   }
 }
 
-// A thread's places in every tile: its row's four pieces of 32 columns, and what it stores, four times a piece of eight rows
-// of 64 bytes (a warp's 32 rows x 32 columns).
+// A thread's places in every tile: its row's four pieces of 32 columns.
 struct Places {
-  uint32_t own[4], out[4];
-  int row, out_row, out_col;  // out_row: of the first of the four, eight apart
+  uint32_t own[4];
+  int row, col;
 };
 __device__ __forceinline__ Places places(int warp, int lane) {
   Places p;
   p.row = (warp & 3) * 32 + lane;
-  p.out_row = (warp & 3) * 32 + lane / 4;
-  const int j0 = (warp >> 2) * 4;
-  p.out_col = 8 * (j0 + lane % 4);
+  p.col = (warp >> 2) * 32;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int j = j0 + i, o = j0 + lane % 4, r = p.out_row + 8 * i;
+    const int j = p.col / 8 + i;
     p.own[i] = (j >> 3) * kAtom + p.row * 128 + (((j & 7) ^ (p.row & 7)) << 4);
-    p.out[i] = (o >> 3) * kAtom + r * 128 + (((o & 7) ^ (r & 7)) << 4);
   }
   return p;
 }
 __device__ __forceinline__ uint4& at_byte(uint8_t* tile, uint32_t offset) { return *reinterpret_cast<uint4*>(tile + offset); }
-// The warp's part of a tile to memory; out: the tile's first row and the thread's columns; n rows of the tile are written.
-__device__ __forceinline__ void store_rows(uint8_t* tile, const Places& p, __nv_bfloat16* out, long long sn, int n) {
-  __nv_bfloat16* to = out + p.out_row * sn;
+// The last tile of a packed sequence, whose rows end in it: the thread's 32 columns from their place to its row.
+__device__ __forceinline__ void store_own(uint8_t* tile, const Places& p, __nv_bfloat16* to) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (p.out_row + 8 * i < n) *reinterpret_cast<uint4*>(to) = at_byte(tile, p.out[i]);
-    to += 8 * sn;
-  }
+  for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(to)[i] = at_byte(tile, p.own[i]);
 }
 
 // Descriptors.  Tokens' tile as A or B with the tokens along K ("MN-major"): K steps of 16 rows are 2048 bytes apart, 64
@@ -447,19 +459,23 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
 }
 
 // ================================================================ read
-// 8 x 6 heads of 4096 queries, d = 64: 19 us from a cold cache (50 MB); issue slots 40 %, the rest the start and the chain of a
-// tile (copy, features, MMA, results) that three blocks an SM share.
-// Three buffers and two accumulators: while the MMA of a tile runs the warps store the tile before and take the next one's
-// features; one barrier of the block a tile, so what a tile leaves for the next turn lies in one of three places.
+// 8 x 6 heads of 4096 queries, d = 64: 12 us (50 MB, 4.3 TB/s), 8 x 8 heads, d = 128: 32 (134 MB, 4.2 TB/s); issue slots 40 %,
+// the rest the start and the chain of a tile (copy, features, MMA, results) that three blocks an SM share.  With the warps
+// storing rows of 64 bytes, which occupies the shared memory's data path, and three buffers throughout: 13 and 50.
+// Three buffers (d = 128: four) and two accumulators: while the MMA of a tile runs the warps put the results of the one before
+// into its place, whence they are copied out, and take the next one's features.
 template <int D>
 struct ReadSmem {
-  static constexpr int kQ = 0, kS = 3 * Tc<D>::kTile, kZ = kS + Tc<D>::kMat, kDen = kZ + D * 4, kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
+  static constexpr int kBuffers = D == 64 ? 3 : 4;
+  static constexpr int kQ = 0, kS = kBuffers * Tc<D>::kTile, kZ = kS + Tc<D>::kMat, kDen = kZ + D * 4,
+                       kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
   static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
 };
 template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_read_kernel(const __grid_constant__ TcArgs p) {
   using X = Tc<D>;
   using M = ReadSmem<D>;
+  constexpr int NB = M::kBuffers;
   constexpr uint32_t kColumns = 2 * D;
   extern __shared__ __align__(16) uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
@@ -470,39 +486,55 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.qs, k, &b->scratch);
   const int slot = g.seq < 0 ? -1 : p.c.slots != nullptr ? p.c.slots[g.seq] : g.seq;
-  if (slot < 0 || slot >= p.c.n_slots) return finish<3, 2>(b, kColumns);
+  if (slot < 0 || slot >= p.c.n_slots) return finish<NB, 2>(b, kColumns);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
+  const auto whole = [&](int j) { return p.c.qs.cu == nullptr || (j + 1) * kT <= g.len; };  // (dense: the tensor ends there too)
   const size_t unit = (size_t)slot * p.c.Hk + h / (p.c.H / p.c.Hk);
   if (tid < X::kWork) load_matrix<D>(sm + M::kS, nullptr, p.c.S + unit * D * D);
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
   if (tid >= X::kWork) {
     if (lane == 0) {
       const auto fetch = [&](int j) {
-        uint64_t* bar = &b->full[j % 3];
+        uint64_t* bar = &b->full[j % NB];
         mbar_arrive_expect_tx(bar, X::kTile);
-        load_tile(sm + M::kQ + j % 3 * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
+        load_tile(sm + M::kQ + j % NB * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
         b->issued = j + 1;
       };
       const uint32_t sa = smem_u32(sm + M::kS);
-      for (int j = 0; j < min(tiles, 3); ++j) fetch(j);
+      // the results of tile j, and another tile into its place
+      const auto out = [&](int j) {
+        if (!wait(&b->out[j & 1], (j >> 1) & 1, b)) return false;
+        if (whole(j)) {
+          store_tile(&p.c_map, sm + M::kQ + j % NB * X::kTile, g.row0 + j * kT, p.c_h ? h : 0, p.c_b ? bb : 0);
+          stores_commit();
+        }
+        if (j + NB < tiles) {
+          stores_read();
+          fetch(j + NB);
+        }
+        return true;
+      };
+      for (int j = 0; j < min(tiles, NB); ++j) fetch(j);
       for (int j = 0; j < tiles; ++j) {
-        // every warp has the features of tile j (the first time: S) written, and tile j - 2 stored
+        // every warp has the features of tile j (the first time: S) written, and the results of tile j - 2 taken
         if (!wait(&b->ready[j % 3], (j / 3) & 1, b)) break;
         tc_fence_after();
-        const uint32_t qa = smem_u32(sm + M::kQ + j % 3 * X::kTile);
+        const uint32_t qa = smem_u32(sm + M::kQ + j % NB * X::kTile);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
           mma_bf16(tmem + (j & 1) * D, along_cols<D>(qa, kAtom, s), along_rows(sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1),
                    s > 0);
         mma_commit(&b->mma[j & 1]);
         b->mmas = j + 1;
-        if (j >= 2 && j + 1 < tiles) fetch(j + 1);
+        if (j > 0 && !out(j - 1)) break;
+        if (j == tiles - 1) out(j);
       }
+      stores_done();
     }
     __syncwarp();
     __syncthreads();
-    return finish<3, 2>(b, kColumns);
+    return finish<NB, 2>(b, kColumns);
   }
   __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"(X::kWork) : "memory");  // z
@@ -510,9 +542,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   const int row = pl.row, cg = warp >> 2;  // the thread's row, and its 32 columns
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.y.p)) + cross_base(p.c.qs, p.c.y, g.seq, h) +
-                     (long long)g.row0 * p.c.y.sn + pl.out_col;
+                     ((long long)g.row0 + row) * p.c.y.sn + pl.col;
   bool ok = true;
-  int buf = 0, before = 2, phase = 0;  // j % 3, (j - 1) % 3, j / 3 & 1
+  int buf = 0, before = 0, phase = 0, slot3 = 0, before3 = 0;  // of tiles j and j - 1: their buffers (and phase), j % 3
   for (int j = 0; ok && j <= tiles; ++j) {
     if (j < tiles) {  // the features of tile j
       uint8_t* qt = sm + M::kQ + buf * X::kTile;
@@ -532,12 +564,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
         }
         if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
       }
-      den[(buf * X::kCols + cg) * kT + row] = d.x + d.y;
-      arrive(&b->ready[buf], lane);
+      den[(slot3 * X::kCols + cg) * kT + row] = d.x + d.y;
+      arrive(&b->ready[slot3], lane);
     }
     if (j > 0) {  // tile j - 1 goes out
       const int t = j - 1;
-      uint8_t* qt = sm + M::kQ + before * X::kTile;
       ok = __all_sync(0xffffffffu, wait(&b->mma[t & 1], (t >> 1) & 1, b));
       if (!ok) break;
       tc_fence_after();
@@ -548,28 +579,32 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
       if (p.c.normalise) {
         float d = p.c.eps;
 #pragma unroll
-        for (int i = 0; i < X::kCols; ++i) d += den[(before * X::kCols + i) * kT + row];
+        for (int i = 0; i < X::kCols; ++i) d += den[(before3 * X::kCols + i) * kT + row];
         inv = inverse(d);
       }
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], both(inv));
+      uint8_t* qt = sm + M::kQ + before * X::kTile;
 #pragma unroll
       for (int i = 0; i < 4; ++i) at_byte(qt, pl.own[i]) = pack8(v + 4 * i);
-      __syncwarp();
-      store_rows(qt, pl, y + (long long)t * kT * p.c.y.sn, p.c.y.sn, g.len - t * kT);
+      if (!whole(t) && row < g.len - t * kT) store_own(qt, pl, y + (long long)t * kT * p.c.y.sn);
+      arrive(&b->out[t & 1], lane);
     }
     before = buf;
-    buf = buf == 2 ? 0 : buf + 1;
+    before3 = slot3;
+    buf = buf == NB - 1 ? 0 : buf + 1;
     phase ^= buf == 0;
+    slot3 = slot3 == 2 ? 0 : slot3 + 1;
   }
   __syncthreads();
-  finish<3, 2>(b, kColumns);
+  finish<NB, 2>(b, kColumns);
 }
 
 // ================================================================ backward over the queries
-// 8 x 6 heads of 4096 queries, d = 64: 30 us from a cold cache (75 MB); issue slots 42 %, tensor pipe 17 %.  Bound by the chain
-// of a tile: u, its row sums, dq and the stores; dS from w runs next to the sums.
+// 8 x 6 heads of 4096 queries, d = 64: about 26 us (75 MB), 8 x 8 heads, d = 128: about 85 (201 MB); issue slots 40 %, tensor
+// pipe 20 %.  Bound by the chain of a tile: u, its row sums, dq and the copy out; dS from w runs next to the sums.  With the next
+// tile's u taken ahead, in a second place of tensor memory: 1 and 9 us more, as the tile after comes in later.
 // The tiles of d = 128 leave 3 KB of a block's 227: what is small lies before them, up to the next 1024 bytes.
 template <int D>
 struct QuerySmem {
@@ -614,6 +649,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
   if (g.seq < 0) return finish<2, 1>(b, kColumns);
   const uint32_t tmem = b->tbase;
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
+  const auto whole = [&](int j) { return p.c.qs.cu == nullptr || (j + 1) * kT <= g.len; };  // (dense: the tensor ends there too)
   const size_t unit = (size_t)g.seq * p.c.Hk + h / (p.c.H / p.c.Hk);
   if (tid < X::kWork) load_matrix<D>(sm + M::kS, sm + M::kSLo, p.c.S + unit * D * D);
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
@@ -627,6 +663,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
         b->issued = j + 1;
       };
       const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo), wl = smem_u32(sm + M::kLo);
+      const auto store = [&](int j) {  // dq of tile j, where the warps' arrival for the next turn has been seen
+        if (!whole(j)) return;
+        store_tile(&p.c_map, sm + M::kQ + (j & 1) * X::kTile, g.row0 + j * kT, p.c_h ? h : 0, p.c_b ? bb : 0);
+        stores_commit();
+      };
       if (tiles > 0) fetch(0);
       for (int j = 0; j < tiles; ++j) {
         const uint32_t qa = smem_u32(sm + M::kQ + (j & 1) * X::kTile), ya = smem_u32(sm + M::kY + (j & 1) * X::kTile);
@@ -642,7 +683,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
                      s > 0 || part > 0);
         mma_commit(&b->mma[0]);
         b->mmas = j + 1;
-        if (j + 1 < tiles) fetch(j + 1);
+        if (j > 0) store(j - 1);
+        if (j + 1 < tiles) {
+          stores_read();
+          fetch(j + 1);
+        }
         if (!wait(&b->ready2, j & 1, b)) break;
         tc_fence_after();
         // dS^T += dy^T w  (d = 64: A's rows 64 .. 127 are another tile's columns, whose results are not read)
@@ -657,7 +702,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
         }
         mma_commit(&b->mma2);
         b->mmas2 = j + 1;
+        if (j == tiles - 1 && wait(&b->out[0], 0, b)) store(j);
       }
+      stores_done();
     }
     __syncwarp();
     __syncthreads_and(true);  // (the two barriers of the other warps' end)
@@ -671,7 +718,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
   const auto row_sync = [&] { named_bar(1 + (warp & 3), X::kWork / 4); };  // the warps that share 32 rows
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
   __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dq.p)) + cross_base(p.c.qs, p.c.dq, g.seq, h) +
-                      (long long)g.row0 * p.c.dq.sn + pl.out_col;
+                      ((long long)g.row0 + row) * p.c.dq.sn + pl.col;
   float2 dz[16] = {};  // of the thread's 32 columns, over its rows
   bool ok = true;
   for (int j = 0; j < tiles; ++j) {
@@ -769,8 +816,8 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
         at_byte(qt, pl.own[2 * c + i]) = pack8(u + 4 * i);
       }
     }
-    __syncwarp();
-    store_rows(qt, pl, dq + (long long)j * kT * p.c.dq.sn, p.c.dq.sn, n);
+    if (!whole(j) && live) store_own(qt, pl, dq + (long long)j * kT * p.c.dq.sn);
+    if (j == tiles - 1) arrive(&b->out[0], lane);
   }
   if (__syncthreads_and(ok && !aborted(&b->abort))) {
     tc_fence_after();
@@ -809,11 +856,13 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
 }
 
 // ================================================================ backward over the keys
-// 8 x 6 heads of 2048 keys, d = 64: 19 us from a cold cache (50 MB), the matrices' parts and the chain of a tile.
-// d = 64: three buffers and two accumulators, as the read; d = 128: two buffers and one accumulator.
+// 8 x 6 heads of 2048 keys, d = 64: about 11 us (50 MB); 8 x 8 heads, d = 128: about 36 (134 MB), where two buffers wait for
+// one another's copies in and out.
+// Two accumulators: while the MMAs of a tile run the warps put the results of the one before into its place, whence they are
+// copied out; three buffers, two for d = 128.
 template <int D>
 struct KeySmem {
-  static constexpr int kBuffers = D == 64 ? 3 : 2, kAcc = D == 64 ? 2 : 1;
+  static constexpr int kBuffers = D == 64 ? 3 : 2;
   static constexpr int kK = 0, kV = kBuffers * Tc<D>::kTile, kS = 2 * kBuffers * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat,
                        kEnd = kSLo + Tc<D>::kMat;
   static constexpr int kZ = 0, kBars = kZ + D * 4, kSmall = kBars + (int)sizeof(Bars);
@@ -824,8 +873,8 @@ template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key_kernel(const __grid_constant__ TcArgs p) {
   using X = Tc<D>;
   using M = KeySmem<D>;
-  constexpr int NB = M::kBuffers, NA = M::kAcc;
-  constexpr uint32_t kColumns = 2 * D * NA;  // dv, dphi(k), an accumulator each
+  constexpr int NB = M::kBuffers;
+  constexpr uint32_t kColumns = 4 * D;  // dv and dphi(k), twice
   extern __shared__ __align__(16) uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + M::kSmall + 1023) & ~uintptr_t(1023));
   if (sm + M::kEnd > smraw + M::kBytes) {  // (shared memory starts at a multiple of 1024 bytes, or near enough)
@@ -838,10 +887,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   const int h = blockIdx.x % p.c.Hk, k = blockIdx.x / p.c.Hk;
   setup(p, b, kColumns);
   const CrossSegment g = cross_segment(p.c.ks, k, &b->scratch);
-  if (g.seq < 0) return finish<NB, NA>(b, kColumns);
+  if (g.seq < 0) return finish<NB, 2>(b, kColumns);
   const int rows = p.c.ks.cu != nullptr ? g.len : min(p.c.ks.L, p.c.ks.N - g.row0);  // dense: zeros behind the tokens
   const uint32_t tmem = b->tbase;
   const int tiles = (rows + kT - 1) / kT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
+  const auto whole = [&](int j) { return p.c.ks.cu == nullptr || (j + 1) * kT <= g.len; };  // (dense: the tensor ends there too)
   const float* from = p.c.dS + ((size_t)g.seq * p.c.Hk + h) * (D * D + D);
   if (tid < X::kWork) load_matrix<D>(sm + M::kS, sm + M::kSLo, from);
   if (tid < D) z[tid] = from[D * D + tid];
@@ -855,15 +905,27 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
         b->issued = j + 1;
       };
       const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo);
-      // so many tiles that the warps may be at: tile j's features wait for the tile j - LAG stored
-      constexpr int LAG = NA;
-      for (int j = 0; j < min(tiles, NB == 3 ? 3 : 1); ++j) fetch(j);
+      // the results of tile j, and another tile into its place
+      const auto out = [&](int j) {
+        if (!wait(&b->out[j & 1], (j >> 1) & 1, b)) return false;
+        if (whole(j)) {
+          store_tile(&p.c_map, sm + M::kK + j % NB * X::kTile, g.row0 + j * kT, p.c_h ? h : 0, p.c_b ? bb : 0);
+          store_tile(&p.d_map, sm + M::kV + j % NB * X::kTile, g.row0 + j * kT, p.d_h ? h : 0, p.d_b ? bb : 0);
+          stores_commit();
+        }
+        if (j + NB < tiles) {
+          stores_read();
+          fetch(j + NB);
+        }
+        return true;
+      };
+      for (int j = 0; j < min(tiles, NB); ++j) fetch(j);
       for (int j = 0; j < tiles; ++j) {
-        // every warp has the features of tile j (the first time: dS) written, and tile j - LAG stored
-        if (!wait(&b->ready[j % NB], (j / NB) & 1, b)) break;
+        // every warp has the features of tile j (the first time: dS) written, and the results of tile j - 2 taken
+        if (!wait(&b->ready[j % 3], (j / 3) & 1, b)) break;
         tc_fence_after();
         const uint32_t ka = smem_u32(sm + M::kK + j % NB * X::kTile), va = smem_u32(sm + M::kV + j % NB * X::kTile);
-        const uint32_t acc = tmem + j % NA * 2 * D;
+        const uint32_t acc = tmem + (j & 1) * 2 * D;
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -873,15 +935,16 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
             mma_bf16(acc + D, along_cols<D>(va, kAtom, s), along_cols<D>(part ? sl : sa, D * 128, s),
                      idesc_bf16_f32(128, D, 0, 0), s > 0 || part > 0);
           }
-        mma_commit(&b->mma[j % NA]);
+        mma_commit(&b->mma[j & 1]);
         b->mmas = j + 1;
-        if (j >= LAG && j + 1 < tiles && NB == 3) fetch(j + 1);
-        if (NB == 2 && j + 1 < tiles) fetch(j + 1);
+        if (j > 0 && !out(j - 1)) break;
+        if (j == tiles - 1) out(j);
       }
+      stores_done();
     }
     __syncwarp();
     __syncthreads();
-    return finish<NB, NA>(b, kColumns);
+    return finish<NB, 2>(b, kColumns);
   }
   __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"(X::kWork) : "memory");  // z
@@ -889,9 +952,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   const int row = pl.row, cg = warp >> 2;
   const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + cg * 32;
   __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dk.p)) + cross_base(p.c.ks, p.c.dk, g.seq, h) +
-                      (long long)g.row0 * p.c.dk.sn + pl.out_col;
+                      ((long long)g.row0 + row) * p.c.dk.sn + pl.col;
   __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dv.p)) + cross_base(p.c.ks, p.c.dv, g.seq, h) +
-                      (long long)g.row0 * p.c.dv.sn + pl.out_col;
+                      ((long long)g.row0 + row) * p.c.dv.sn + pl.col;
   // phi(k) of tile j over its keys
   const auto features = [&](int j) {
     uint8_t* kt = sm + M::kK + j % NB * X::kTile;
@@ -905,18 +968,18 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
         for (int x = 0; x < 4; ++x) f[x] = feature<F>(f[x]);
         at_byte(kt, pl.own[i]) = pack8(f);
       }
-    arrive(&b->ready[j % NB], lane);
+    arrive(&b->ready[j % 3], lane);
     return true;
   };
   bool ok = tiles == 0 || features(0);
   for (int j = 0; ok && j < tiles; ++j) {
-    uint8_t *kt = sm + M::kK + j % NB * X::kTile, *vt = sm + M::kV + j % NB * X::kTile;
-    if (NA == 2 && j + 1 < tiles && !features(j + 1)) break;
-    ok = __all_sync(0xffffffffu, wait(&b->mma[j % NA], (j / NA) & 1, b));
+    if (j + 1 < tiles && !features(j + 1)) break;
+    ok = __all_sync(0xffffffffu, wait(&b->mma[j & 1], (j >> 1) & 1, b));
     if (!ok) break;
     tc_fence_after();
-    const bool live = row < g.len - j * kT;
-    const uint32_t acc = at + j % NA * 2 * D;
+    uint8_t *kt = sm + M::kK + j % NB * X::kTile, *vt = sm + M::kV + j % NB * X::kTile;
+    const bool live = row < g.len - j * kT;  // (dense: zeros behind the tokens)
+    const uint32_t acc = at + (j & 1) * 2 * D;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float2 u[8], v[8];
@@ -926,25 +989,26 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float2 f[4], zz[4];
-        unpack8(at_byte(kt, pl.own[2 * c + i]), f);  // (phi rounded to bf16: phi' goes by it, and its rounding by dk's)
+        if (F != MHLA_PHI_IDENTITY) unpack8(at_byte(kt, pl.own[2 * c + i]), f);  // (phi rounded to bf16: phi' goes by it, and its rounding by dk's)
         load8(z + cg * 32 + 16 * c + 8 * i, zz);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          u[4 * i + x] = mul2(slope<F>(f[x]), add2(u[4 * i + x], zz[x]));
+          u[4 * i + x] = add2(u[4 * i + x], zz[x]);
+          if (F != MHLA_PHI_IDENTITY) u[4 * i + x] = mul2(slope<F>(f[x]), u[4 * i + x]);
           if (!live) u[4 * i + x] = v[4 * i + x] = both(0.f);
         }
         at_byte(kt, pl.own[2 * c + i]) = pack8(u + 4 * i);
         at_byte(vt, pl.own[2 * c + i]) = pack8(v + 4 * i);
       }
     }
-    __syncwarp();
-    const int m = rows - j * kT;
-    store_rows(kt, pl, dk + (long long)j * kT * p.c.dk.sn, p.c.dk.sn, m);
-    store_rows(vt, pl, dv + (long long)j * kT * p.c.dv.sn, p.c.dv.sn, m);
-    if (NA == 1 && j + 1 < tiles) ok = features(j + 1);
+    if (!whole(j) && live) {
+      store_own(kt, pl, dk + (long long)j * kT * p.c.dk.sn);
+      store_own(vt, pl, dv + (long long)j * kT * p.c.dv.sn);
+    }
+    arrive(&b->out[j & 1], lane);
   }
   __syncthreads();
-  finish<NB, NA>(b, kColumns);
+  finish<NB, 2>(b, kColumns);
 }
 
 // ================================================================ host
@@ -977,16 +1041,19 @@ bool make_map(CUtensorMap* m, const RetTensor& t, const CrossSide& s, int heads,
 
 unsigned long long g_wait_ns = kWaitNs;
 
-// The launch's arguments, with the maps of the tile's one or two tensors.
+// The launch's arguments, with the maps of the tile's one or two tensors and of what is written.
 bool make_args(TcArgs* t, const CrossArgs& a, const CrossSide& s, int heads, const RetTensor& x, const RetTensor* y,
-               int box_rows = kT) {
+               const RetTensor* out, const RetTensor* out2, int box_rows = kT) {
   t->c = a;
   t->wait_ns = g_wait_ns;
-  t->a_h = x.sh != 0;
-  t->a_b = x.sb != 0 && s.cu == nullptr;
-  t->b_h = y != nullptr && y->sh != 0;
-  t->b_b = y != nullptr && y->sb != 0 && s.cu == nullptr;
-  return make_map(&t->a, x, s, heads, a.d, box_rows) && (y == nullptr || make_map(&t->b, *y, s, heads, a.d, box_rows));
+  const auto map = [&](CUtensorMap* m, int* has_h, int* has_b, const RetTensor* x) {
+    if (x == nullptr) return true;
+    *has_h = x->sh != 0;
+    *has_b = x->sb != 0 && s.cu == nullptr;
+    return make_map(m, *x, s, heads, a.d, box_rows);
+  };
+  return map(&t->a, &t->a_h, &t->a_b, &x) && map(&t->b, &t->b_h, &t->b_b, y) && map(&t->c_map, &t->c_h, &t->c_b, out) &&
+         map(&t->d_map, &t->d_h, &t->d_b, out2);
 }
 
 cudaError_t launch(void (*kernel)(TcArgs), SmemOptIn& opt, long long blocks, int threads, int smem, const TcArgs& t,
@@ -999,14 +1066,14 @@ cudaError_t launch(void (*kernel)(TcArgs), SmemOptIn& opt, long long blocks, int
 template <int D, int F>
 cudaError_t states_t(const CrossArgs& a, cudaStream_t st) {
   TcArgs t;
-  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v, kSumT)) return cudaErrorInvalidValue;
+  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v, nullptr, nullptr, kSumT)) return cudaErrorInvalidValue;
   static SmemOptIn opt;
   return launch(tc_cross_states_kernel<D, F>, opt, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, SumSmem<D>::kBytes, t, st);
 }
 template <int D, int F>
 cudaError_t read_t(const CrossArgs& a, cudaStream_t st) {
   TcArgs t;
-  if (!make_args(&t, a, a.qs, a.H, a.q, nullptr)) return cudaErrorInvalidValue;
+  if (!make_args(&t, a, a.qs, a.H, a.q, nullptr, &a.y, nullptr)) return cudaErrorInvalidValue;
   static SmemOptIn opt;
   return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, ReadSmem<D>::kBytes, t, st);
 }
@@ -1016,13 +1083,13 @@ cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
   static SmemOptIn opt_q, opt_k;
   cudaError_t e = cudaSuccess;
   if (a.qs.segs > 0) {
-    if (!make_args(&t, a, a.qs, a.H, a.q, &a.dy)) return cudaErrorInvalidValue;
+    if (!make_args(&t, a, a.qs, a.H, a.q, &a.dy, &a.dq, nullptr)) return cudaErrorInvalidValue;
     e = launch(tc_cross_query_kernel<D, F>, opt_q, (long long)a.qs.segs * a.H, Tc<D>::kThreads, QuerySmem<D>::kBytes, t, st);
   }
   if (e != cudaSuccess || a.ks.segs == 0) return e;
   e = cross_join_launch(a, true, st);
   if (e != cudaSuccess) return e;
-  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v)) return cudaErrorInvalidValue;
+  if (!make_args(&t, a, a.ks, a.Hk, a.k, &a.v, &a.dk, &a.dv)) return cudaErrorInvalidValue;
   return launch(tc_cross_key_kernel<D, F>, opt_k, (long long)a.ks.segs * a.Hk, Tc<D>::kThreads, KeySmem<D>::kBytes, t, st);
 }
 
