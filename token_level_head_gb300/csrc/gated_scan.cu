@@ -94,14 +94,6 @@ __device__ __forceinline__ void unpack(const uint4& u, float2 (&f)[2]) {
   f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
   f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-// The next row's pointer, taken row by row: sixteen rows' pointers in registers would be spilled.
-template <typename T>
-__device__ __forceinline__ T* next_row(T* p, long long sn) {
-  p += sn;
-  asm volatile("" : "+l"(p));
-  return p;
-}
-
 __device__ __forceinline__ void store(float* p, const float2 (&f)[1]) { *reinterpret_cast<float2*>(p) = f[0]; }
 __device__ __forceinline__ void store(float* p, const float2 (&f)[2]) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
@@ -700,7 +692,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
 #pragma unroll
         for (int k = 0; k < P; ++k) h[k] = cut ? b[k] : fma2(a[k], h[k], b[k]);
         if (plain || out >> r & 1) store(py, h);
-        py = next_row(py, p.y.sn);
+        py += p.y.sn;
         if constexpr (!plain) {
           if (ends >> r & 1) {
             const int slot = slot_of(p.slots, p.n_slots, sequence_of(i, r));
@@ -961,8 +953,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
           store(px, ox);
           store(pg, og);
         }
-        px = next_row(px, p.dx.sn);
-        pg = next_row(pg, p.dg.sn);
+        px += p.dx.sn;
+        pg += p.dg.sn;
       }
     };
     if (is_plain)
