@@ -11,8 +11,8 @@
 // tile of rows and LW lanes of channels; tiles behind one another are taken by the blocks of a cluster, which exchange their
 // (A, B) through distributed shared memory, and a cluster walks along the sequence.  So x and g are read once and no memory,
 // flag or wait is shared between clusters.
-// Measured, whole calls: 65,536 x 1024 bf16, log, 81 us (4.9 TB/s); 77 x 1024 bf16 8; forward and backward of 4 x 8192 x 1024
-// bf16, sigmoid, 125 (4.3 TB/s), of 20,011 packed x 384 fp32, decay, 77 (3.2 TB/s); the step of 256 x 8192 bf16 8.
+// Measured, whole calls: 65,536 x 1024 bf16, log, 79 us (5.1 TB/s); 77 x 1024 bf16 8; forward and backward of 4 x 8192 x 1024
+// bf16, sigmoid, 121 (4.4 TB/s), of 20,011 packed x 384 fp32, decay, 73 (3.4 TB/s); the step of 256 x 8192 bf16 8.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -30,7 +30,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the tiles,
 constexpr int kBlock = kThreads + 32;                  // and a warp that carries the state over the tiles (exchange)
-constexpr int kWideCluster = 6, kNarrowCluster = 16;   // blocks of a cluster at most, with 128 bytes of channels and with 64
+constexpr int kMostBlocks = 16;                        // of a cluster
 constexpr int P = 1, V = 2 * P;  // channels of a thread: a pair, so that a warp of bf16 has a row of 128 bytes to itself
 
 // A thread's rows of a tile and the lanes of 128 bytes of channels.  Half of the values for fp32, whose tiles are as many bytes.
@@ -315,15 +315,16 @@ __device__ __forceinline__ void scan_warp(float2 (&A)[P], float2 (&B)[P], float2
 
 template <typename T, int LW>
 struct ScanShared {
-  static constexpr int CW = V * LW, MOST = LW == Tile<T>::WIDE ? kWideCluster : kNarrowCluster;
+  static constexpr int CW = V * LW;
   float wa[2][kWarps][CW], wb[2][kWarps][CW];  // A, B of the warps, by the tile's parity; then of what lies before them
-  float ba[2][MOST][CW], bb[2][MOST][CW];      // of the cluster's blocks, which write them here
+  float ba[2][CW], bb[2][CW];                  // of the block, which the cluster's others read
   float carry[2][CW];                          // the state entering the block's tile
 };
 
 // What goes on from tile to tile, in a warp of its own: as it has no other stores, the release of the cluster's barrier
-// waits for none (with the state carried by warps of the tiles each round waited for their outputs to arrive in L2).  The
-// block's warps have A, B in s.wa, s.wb and wait for s.carry.  It also leaves what lies before each warp in s.wa, s.wb (every
+// waits for none (with the state carried by warps of the tiles each round waited for their outputs to arrive in L2).  Blocks
+// read one another's A, B behind that barrier (each writing them to all: 65,536 x 1024 80 us against 79, 20,011 packed x 384 76
+// against 73); a place is written again two tiles later, behind another one.  The block's warps have A, B in s.wa, s.wb and wait for s.carry.  It also leaves what lies before each warp in s.wa, s.wb (every
 // warp for itself over up to seven others: 65,536 x 1024 85 us against 81).
 // (Two barriers each, by the tile's parity: one side may be a tile ahead of the other.)
 __device__ __forceinline__ void block_sync(int par) { asm volatile("bar.sync %0, 288;" ::"r"(2 + par) : "memory"); }
@@ -346,7 +347,7 @@ __device__ __forceinline__ void give_wait(bool clustered) {
 // The carrying warp: all rounds of tiles.
 template <typename T, int LW, bool REVERSE, bool PACKED>
 __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, int n, int rank) {
-  constexpr int CW = ScanShared<T, LW>::CW, MOST = ScanShared<T, LW>::MOST, K = (CW + 31) / 32;
+  constexpr int CW = ScanShared<T, LW>::CW, K = (CW + 31) / 32;
   const int lane = threadIdx.x & 31;
   float running[K];
 #pragma unroll
@@ -375,17 +376,8 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
         s.carry[par][c] = running[k];
         running[k] = carry_on<PACKED>(A, B, running[k]);
       } else {
-        cg::cluster_group cl = cg::this_cluster();
-#pragma unroll
-        for (int j = 0; j < MOST; j += 8) {
-          if (j >= n) break;
-#pragma unroll
-          for (int i = j; i < MOST && i < j + 8; ++i)
-            if (i < n) {
-              cl.map_shared_rank(&s.ba[par][rank][0], i)[c] = A;
-              cl.map_shared_rank(&s.bb[par][rank][0], i)[c] = B;
-            }
-        }
+        s.ba[par][c] = A;
+        s.bb[par][c] = B;
       }
     }
     if (n == 1) {
@@ -401,13 +393,21 @@ __device__ __forceinline__ void carry_tiles(ScanShared<T, LW>& s, int rounds, in
       const int c = lane + 32 * k;
       if (CW % 32 != 0 && c >= CW) continue;
       float h = running[k], mine = h;
+      cg::cluster_group cl = cg::this_cluster();
 #pragma unroll
-      for (int j = 0; j < MOST; j += 8) {
+      for (int j = 0; j < kMostBlocks; j += 8) {
         if (j >= n) break;
+        float A[8], B[8];
 #pragma unroll
-        for (int i = j; i < MOST && i < j + 8; ++i) {
-          if (i == rank) mine = h;
-          if (i < n) h = carry_on<PACKED>(s.ba[par][i][c], s.bb[par][i][c], h);
+        for (int i = 0; i < 8; ++i) {
+          if (j + i >= n) continue;
+          A[i] = cl.map_shared_rank(&s.ba[par][0], j + i)[c];
+          B[i] = cl.map_shared_rank(&s.bb[par][0], j + i)[c];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (j + i == rank) mine = h;
+          if (j + i < n) h = carry_on<PACKED>(A[i], B[i], h);
         }
       }
       s.carry[par][c] = mine;
@@ -528,9 +528,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   }
   const int tiles = ret_pieces(p.N, ROWS), kept_rows = ret_pieces(p.N, kScanKept);
   if (tid >= kThreads) {
-    if (cluster > 1) cg::this_cluster().sync();  // every block runs: its shared memory may be written
     carry_tiles<T, LW, false, PACKED>(s, ret_pieces(tiles, cluster), cluster, rank);
-    if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one writes its shared memory
+    if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one reads its shared memory
     return;
   }
   extern __shared__ __align__(16) uint8_t raw[];
@@ -627,7 +626,6 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   const auto row0_of = [&](int i) { return (int)min(((long long)i * cluster + rank) * ROWS, (long long)p.N); };
   fetch(0);
   fetch(1);
-  if (cluster > 1) cg::this_cluster().sync();
   Ahead next;
   if constexpr (PACKED) {
     clear_marks(marks[0]);
@@ -706,7 +704,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     else
       run(std::false_type());
   }
-  if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one writes its shared memory
+  if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one reads its shared memory
 }
 
 // ---- backward
@@ -754,9 +752,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
   }
   const int tiles = ret_pieces(p.N, ROWS), kept_rows = ret_pieces(p.N, kScanKept);
   if (tid >= kThreads) {
-    if (cluster > 1) cg::this_cluster().sync();  // every block runs: its shared memory may be written
     carry_tiles<T, LW, true, PACKED>(s, ret_pieces(tiles, cluster), cluster, rank);
-    if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one writes its shared memory
+    if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one reads its shared memory
     return;
   }
   extern __shared__ __align__(16) uint8_t raw[];
@@ -776,7 +773,6 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     tile_sync();
     set_marks(p, tiles - 1 - rank >= 0 ? (tiles - 1 - rank) * ROWS : p.N, marks[0]);
   }
-  if (cluster > 1) cg::this_cluster().sync();
   int par = 0;
   for (int t0 = 0; t0 < tiles; t0 += cluster, par ^= 1) {
     // tiles from the last one on; a cluster's last round may hold tiles before the first: without rows
@@ -1020,7 +1016,7 @@ class ClusterFit {
     if (!known_[dev].load(std::memory_order_relaxed)) {
       // (more than 8 blocks are not portable; every cluster of a kernel here may have them)
       const bool large = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-      for (int n = 2; n <= kNarrowCluster; ++n) {
+      for (int n = 2; n <= kMostBlocks; ++n) {
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeClusterDimension;
         at.val.clusterDim = {(unsigned)n, 1, 1};
@@ -1042,7 +1038,7 @@ class ClusterFit {
   static constexpr int kDevices = 16;
   std::mutex mu_;
   std::atomic<bool> known_[kDevices] = {};
-  unsigned short fit_[kDevices][kNarrowCluster + 1] = {};
+  unsigned short fit_[kDevices][kMostBlocks + 1] = {};
 };
 
 struct Plan {
@@ -1065,7 +1061,7 @@ struct Scan {
     p->chains = (PACKED ? 1ll : a.B) * ((a.D + CW - 1) / CW);
     const cudaError_t e = opt[backward].ensure((const void*)kernel(backward), kSmem, dev);
     if (e != cudaSuccess) return e;
-    p->cluster = fit[backward].blocks(dev, (const void*)kernel(backward), kSmem, p->chains, std::min(ScanShared<T, LW>::MOST, tiles));
+    p->cluster = fit[backward].blocks(dev, (const void*)kernel(backward), kSmem, p->chains, std::min(kMostBlocks, tiles));
     const long long places = 2ll * kRetSms;
     p->turns = (p->cluster > 1 ? 1 : (p->chains + places - 1) / places) * ret_pieces(tiles, p->cluster);
     return p->chains * p->cluster > 0x7fffffffll ? cudaErrorInvalidValue : cudaSuccess;
