@@ -324,8 +324,9 @@ struct ScanShared {
 // What goes on from tile to tile, in a warp of its own: as it has no other stores, the release of the cluster's barrier
 // waits for none (with the state carried by warps of the tiles each round waited for their outputs to arrive in L2).  Blocks
 // read one another's A, B behind that barrier (each writing them to all: 65,536 x 1024 80 us against 79, 20,011 packed x 384 76
-// against 73); a place is written again two tiles later, behind another one.  The block's warps have A, B in s.wa, s.wb and wait for s.carry.  It also leaves what lies before each warp in s.wa, s.wb (every
-// warp for itself over up to seven others: 65,536 x 1024 85 us against 81).
+// against 73); a place is written again two tiles later, behind another one.  The block's warps have A, B in s.wa, s.wb and wait
+// for s.carry.  The warp also leaves what lies before each of them in s.wa, s.wb (every warp for itself over up to seven
+// others: 65,536 x 1024 85 us against 81).
 // (Two barriers each, by the tile's parity: one side may be a tile ahead of the other.)
 __device__ __forceinline__ void block_sync(int par) { asm volatile("bar.sync %0, 288;" ::"r"(2 + par) : "memory"); }
 __device__ __forceinline__ void block_arrive(int par) { asm volatile("bar.arrive %0, 288;" ::"r"(2 + par) : "memory"); }
