@@ -19,13 +19,10 @@ class SmemOptIn {
   cudaError_t ensure(const void* fn, int bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    return e == cudaSuccess ? ensure(fn, bytes, dev) : e;
-  }
-  // (dev: the current device)
-  cudaError_t ensure(const void* fn, int bytes, int dev) {
+    if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lk(mu_);
     if (dev < 64 && ((done_ >> dev) & 1ull)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && dev < 64) done_ |= 1ull << dev;
     return e;
   }

@@ -1060,7 +1060,7 @@ struct Scan {
     static ClusterFit fit[2];
     const int tiles = ret_pieces(a.N, ROWS);
     p->chains = (PACKED ? 1ll : a.B) * ((a.D + CW - 1) / CW);
-    const cudaError_t e = opt[backward].ensure((const void*)kernel(backward), kSmem, dev);
+    const cudaError_t e = opt[backward].ensure((const void*)kernel(backward), kSmem);
     if (e != cudaSuccess) return e;
     p->cluster = fit[backward].blocks(dev, (const void*)kernel(backward), kSmem, p->chains, std::min(kMostBlocks, tiles));
     const long long places = 2ll * kRetSms;
