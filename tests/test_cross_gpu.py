@@ -341,6 +341,62 @@ def test_a_decoder_layer_step_by_step():
     assert (out - y).abs().max() <= 2.0 ** -14
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("feature", ["elu1", "exp"])
+@pytest.mark.parametrize("nk,eps", [(1, 1e-6), (2, 1e-6), (1, 0.5), (2, 40.0)])
+def test_gradients_where_a_sequence_s_values_are_equal(nk, eps, feature, d):
+    """One value in all of a sequence's keys: without eps dq and dk vanish, as differences of equal terms, so the bf16 calls must
+    not leave the roundings of S there.  dq, relative to its terms: S takes 3 nk products, each cut by at most 2^-23, and S - z m^T
+    one more rounding; that comes in with u and with phi(q) . u, each at most its share of the terms: (3 nk + 2) 2^-22, and 16 more
+    steps of 2^-24 for what eps leaves (sums of d values of m . dy, split in eight, and products).  dk: its sum over 2 d products of dS
+    and the same of dS m, (2 d + 40) 2^-23, and the above.  Each with half a step of the value."""
+    B, nq = 3, 200
+    c = Call(B, 4, 2, nq, B * nk, d, BF, feature, eps=eps, cu_k=[i * nk for i in range(B + 1)])
+    for i in range(B):
+        c.v[0, :, i * nk:(i + 1) * nk] = c.v[0, :, i * nk:i * nk + 1]
+    c.run()
+    for i in range(B):
+        (bq, rq), (bk, rk) = c.rows(i)
+        q, dy, k, v = (to_f64(t) for t in (c.q[bq, :, rq], c.dy[bq, :, rq], c.k[bk, :, rk], c.v[bk, :, rk]))
+        args = (feature, True, eps)
+        _, _, _, mdq, mdk, _ = co.magnitudes(q, k, v, dy, *args)
+        dq, dk, _ = co.backward(q, k, v, dy, *args)
+        near = (3 * nk + 2) * 2.0 ** -22 + 16 * 2.0 ** -24
+        # eps itself gives terms of the size of eps / den of the others; they are rounded as the rest of a bf16 call
+        share = eps / (eps + co.states(k, v, feature)[1].min())
+        for got, ref, mag, tol in ((c.dq[bq, :, rq], dq, mdq, near), (c.dk[bk, :, rk], dk, mdk, near + (2 * d + 40) * 2.0 ** -23)):
+            bad = np.abs(to_f64(got) - ref) > 2.0 ** -8 * np.abs(ref) + (tol + 3 * 2.0 ** -8 * share) * mag + 1e-37
+            assert not bad.any(), (i, bad.sum(), np.max(np.abs(to_f64(got) - ref) / mag) / tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("feature", ["elu1", "exp"])
+def test_vanishing_gradients_are_as_small_as_in_32_bits(feature, d):
+    """Sequences of one key, whose dq and dk are what eps leaves of differences of equal terms: a bf16 call's are off by no more,
+    in the mean, than the formulas evaluated in 32 bits: twice that for dq; for dk, which sums 2 d products in the accumulators of
+    the tensor cores (each step cut by 2^-23, not rounded by 2^-24) where the formula sums d, eight times."""
+    B, nq = 8, 100
+    c = Call(B, 4, 2, nq, 1, d, BF, feature).run()
+    off = {"dq": 0.0, "dk": 0.0, "dq32": 0.0, "dk32": 0.0}
+    phi = lambda x: np.exp(x) if feature == "exp" else np.where(x > 0, x + 1, np.exp(np.minimum(x, 0)))  # noqa: E731
+    slope = lambda x: np.exp(x) if feature == "exp" else np.exp(np.minimum(x, 0))  # noqa: E731
+    for i in range(B):
+        q, dy, k, v = (to_f64(t[i]) for t in (c.q, c.dy, c.k, c.v))
+        dq, dk, _ = co.backward(q, k, v, dy, feature, True, c.eps)
+        q, dy, k, v = (t.astype(np.float32) for t in (q, dy, k, v))
+        fq, fk = phi(q), np.repeat(phi(k), 2, 0)
+        S, z = np.swapaxes(fk, 1, 2) @ np.repeat(v, 2, 0), fk.sum(1)[:, None]
+        den = (fq * z).sum(-1, keepdims=True) + np.float32(c.eps)
+        u = dy @ np.swapaxes(S, 1, 2)
+        dden = -(fq * u).sum(-1, keepdims=True) / (den * den)
+        dS, dz = np.swapaxes(fq / den, 1, 2) @ dy, (fq * dden).sum(1)
+        dS, dz = (t.reshape(2, 2, *t.shape[1:]).sum(1) for t in (dS, dz))
+        dq32, dk32 = slope(q) * (u / den + dden * z), slope(k) * (v @ np.swapaxes(dS, 1, 2) + dz[:, None])
+        for name, got, ref in (("dq", to_f64(c.dq[i]), dq), ("dk", to_f64(c.dk[i]), dk), ("dq32", dq32, dq), ("dk32", dk32, dk)):
+            off[name] += ((got - ref) ** 2).sum()
+    assert off["dq"] <= 2 ** 2 * off["dq32"] and off["dk"] <= 8 ** 2 * off["dk32"], off
+
+
 @pytest.mark.parametrize("feature,normalise", [("elu1", True), ("exp", True), ("identity", False)])
 def test_gradients_are_the_differences(feature, normalise):
     """fp32 calls against central differences of the calls themselves: sum(dy y) for small moves of q, k and v."""

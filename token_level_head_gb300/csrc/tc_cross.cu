@@ -4,8 +4,8 @@
 //   states  D[e][c] += sum_t v[t][e] phi(k)[t][c]   (A = v, B = phi(k) as a sum of three bf16 numbers: S is an fp32
 //           result), z in fp32 registers
 //   read    y[t][e] = (sum_c phi(q)[t][c] S[c][e]) / den_t
-//   query   u[t][c] = sum_e dy[t][e] S[c][e], dS^T[e][c] += sum_t dy[t][e] w[t][c] with w = phi(q) / den; S and w as sums of
-//           two bf16 numbers (dq is a difference of two nearly equal terms: u / den and dden z), dy as it is; dz in fp32
+//   query   u[t][c] = sum_e dy[t][e] S[c][e], dS^T[e][c] += sum_t dy[t][e] w[t][c] with w = phi(q) / den; S (less a middle of
+//           the values, `middle`) and w as sums of two bf16 numbers, as dq is a difference, dy as it is; dz in fp32
 //   key     dv[t][e] = sum_c phi(k)[t][c] dS[c][e], dphi(k)[t][c] = sum_e v[t][e] dS[c][e] (dS as a sum of two)
 //
 // Bound: memory (2, 2, 3 and 4 tensors), next to it the instructions that take the features and turn tiles.  A block has a
@@ -246,26 +246,71 @@ __device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.co
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// A d x d fp32 matrix [r][c] as bf16 tiles of D rows, the high part and, where lo is given, the low part.
+// A d x d fp32 matrix [r][c] as the working threads hold it: eight columns of a row, the same columns in every row of a thread.
 template <int D>
-__device__ __forceinline__ void load_matrix(uint8_t* hi, uint8_t* lo, const float* from) {
-  constexpr int N = D * D / 8 / Tc<D>::kWork;
+struct Matrix {
+  static constexpr int N = D * D / 8 / Tc<D>::kWork, P = D / 8;  // pieces of a thread, of a row
   float2 f[N][4];
+  static __device__ __forceinline__ int row(int n) { return ((int)threadIdx.x + n * Tc<D>::kWork) / P; }
+  static __device__ __forceinline__ int piece_of_row() { return (int)threadIdx.x % P; }
+  __device__ __forceinline__ void load(const float* from) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {  // (all loads in flight)
-    const int i = threadIdx.x + n * Tc<D>::kWork;
-    load8(from + i * 8, f[n]);
+    for (int n = 0; n < N; ++n) load8(from + ((int)threadIdx.x + n * Tc<D>::kWork) * 8, f[n]);
   }
+  // as bf16 tiles of D rows, the high part and, where lo is given, the low part
+  __device__ __forceinline__ void put(uint8_t* hi, uint8_t* lo) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int i = threadIdx.x + n * Tc<D>::kWork, r = i / (D / 8), j = i % (D / 8);
-    const uint4 u = pack8(f[n]);
-    *piece(hi, D, r, j) = u;
-    if (lo != nullptr) {
-      remainder8(f[n], u);
-      *piece(lo, D, r, j) = pack8(f[n]);
+    for (int n = 0; n < N; ++n) {
+      const uint4 u = pack8(f[n]);
+      *piece(hi, D, row(n), piece_of_row()) = u;
+      if (lo != nullptr) {
+        remainder8(f[n], u);
+        *piece(lo, D, row(n), piece_of_row()) = pack8(f[n]);
+      }
     }
   }
+};
+// A vector m near the values (backward): the mean of v under the features' sums, m[e] = sum_c S[c][e] / sum_c z[c], rounded to
+// bf16.  The gradients of q and k are small differences where the values of a sequence are alike (of one token they vanish), so
+// they are taken of v - m:  u' = (S - z m^T) dy,  dden' = -(phi(q) . u') / den^2 + (m . dy) eps / den^2,
+//   dq = phi'(q) (u' / den + dden' z),  dz' = sum phi(q) dden',  dk = phi'(k) (dS v + (dz' - dS m))
+// where the roundings of S - z m^T and dS then meet v - m.  Any m is right; without a normaliser, and where it is no number, 0.
+// (Working threads; id: a barrier of theirs; scratch: kWork / 32 rows of D floats; z is there after it.)
+template <int D>
+__device__ __forceinline__ void middle(const Matrix<D>& S, const float* z_from, bool on, float* z, float* scratch,
+                                       __nv_bfloat16* m, int id) {
+  constexpr int kWork = Tc<D>::kWork, P = Matrix<D>::P;
+  const int tid = threadIdx.x, lane = tid & 31;
+  float2 s[4] = {};
+#pragma unroll
+  for (int n = 0; n < Matrix<D>::N; ++n)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s[x] = add2(s[x], S.f[n][x]);
+#pragma unroll
+  for (int o = P; o < 32; o <<= 1)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      s[x].x += __shfl_xor_sync(0xffffffffu, s[x].x, o);
+      s[x].y += __shfl_xor_sync(0xffffffffu, s[x].y, o);
+    }
+  if (lane < P)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) *reinterpret_cast<float2*>(scratch + (tid >> 5) * D + lane * 8 + 2 * x) = s[x];
+  if (tid < D) z[tid] = z_from[tid];
+  named_bar(id, kWork);
+  if (tid < D) {
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWork / 32; ++w) a += scratch[w * D + tid];
+#pragma unroll 4
+    for (int i = 0; i < D; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(z + i);
+      b += (v.x + v.y) + (v.z + v.w);
+    }
+    const float mean = a / b;
+    m[tid] = __float2bfloat16_rn(on && fabsf(mean) < 1e38f ? mean : 0.f);
+  }
+  named_bar(id, kWork);
 }
 
 // A thread's places in every tile: its row's four pieces of 32 columns.
@@ -491,7 +536,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
   const auto whole = [&](int j) { return p.c.qs.cu == nullptr || (j + 1) * kT <= g.len; };  // (dense: the tensor ends there too)
   const size_t unit = (size_t)slot * p.c.Hk + h / (p.c.H / p.c.Hk);
-  if (tid < X::kWork) load_matrix<D>(sm + M::kS, nullptr, p.c.S + unit * D * D);
+  if (tid < X::kWork) {
+    Matrix<D> S;
+    S.load(p.c.S + unit * D * D);
+    S.put(sm + M::kS, nullptr);
+  }
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
   if (tid >= X::kWork) {
     if (lane == 0) {
@@ -610,7 +659,8 @@ template <int D>
 struct QuerySmem {
   static constexpr int kQ = 0, kY = 2 * Tc<D>::kTile, kLo = 4 * Tc<D>::kTile, kS = 5 * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat,
                        kEnd = kSLo + Tc<D>::kMat;
-  static constexpr int kZ = 0, kDen = kZ + D * 4, kBars = kDen + Tc<D>::kCols * kT * 4, kSmall = kBars + (int)sizeof(Bars);
+  static constexpr int kZ = 0, kM = kZ + D * 4, kDen = kM + D * 2, kBars = kDen + Tc<D>::kCols * kT * 4,
+                       kSmall = kBars + (int)sizeof(Bars);
   static constexpr int kBytes = (kSmall + 1023) / 1024 * 1024 + kEnd;
   static_assert(kBytes <= 232448 / (D == 64 ? 2 : 1), "two blocks of d = 64 an SM, one of d = 128");
 };
@@ -651,8 +701,21 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
   const int tiles = (g.len + kT - 1) / kT, bb = p.c.qs.cu == nullptr ? g.seq : 0;
   const auto whole = [&](int j) { return p.c.qs.cu == nullptr || (j + 1) * kT <= g.len; };  // (dense: the tensor ends there too)
   const size_t unit = (size_t)g.seq * p.c.Hk + h / (p.c.H / p.c.Hk);
-  if (tid < X::kWork) load_matrix<D>(sm + M::kS, sm + M::kSLo, p.c.S + unit * D * D);
-  if (tid < D) z[tid] = p.c.z[unit * D + tid];
+  __nv_bfloat16* mid = reinterpret_cast<__nv_bfloat16*>(smraw + M::kM);
+  if (tid < X::kWork) {  // S - z m^T
+    Matrix<D> S;
+    S.load(p.c.S + unit * D * D);
+    middle<D>(S, p.c.z + unit * D, p.c.normalise, z, reinterpret_cast<float*>(sm + M::kLo), mid, 5);
+    float2 m[4];
+    unpack8(*reinterpret_cast<const uint4*>(mid + 8 * S.piece_of_row()), m);
+#pragma unroll
+    for (int n = 0; n < S.N; ++n) {
+      const float minus = -z[S.row(n)];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) S.f[n][x] = fma2(both(minus), m[x], S.f[n][x]);
+    }
+    S.put(sm + M::kS, sm + M::kSLo);
+  }
   if (tid >= X::kWork) {
     if (lane == 0) {
       const auto fetch = [&](int j) {
@@ -794,6 +857,17 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
 #pragma unroll
       for (int i = 0; i < X::kCols; ++i) dd += den[i * kT + row];
       dd *= -inv * inv;
+      if (p.c.eps * inv > 0x1p-26f) {  // (m . dy) eps / den^2, no less than a rounding of u' / den
+        float s1 = 0.f;
+        for (int i = 0; i < D / 8; ++i) {
+          float2 a[4], e[4];
+          unpack8(*piece(yt, kT, row, i), a);
+          unpack8(*reinterpret_cast<const uint4*>(mid + 8 * i), e);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s1 = fmaf(a[x].x, e[x].x, fmaf(a[x].y, e[x].y, s1));
+        }
+        dd = fmaf(s1, p.c.eps * inv * inv, dd);
+      }
     }
     ok = row_and(wait(&b->mma2, j & 1, b), warp, X::kWork / 4);  // w has been read; and the row's sums
     if (!ok) break;
@@ -865,7 +939,7 @@ struct KeySmem {
   static constexpr int kBuffers = D == 64 ? 3 : 2;
   static constexpr int kK = 0, kV = kBuffers * Tc<D>::kTile, kS = 2 * kBuffers * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat,
                        kEnd = kSLo + Tc<D>::kMat;
-  static constexpr int kZ = 0, kBars = kZ + D * 4, kSmall = kBars + (int)sizeof(Bars);
+  static constexpr int kZ = 0, kM = kZ + D * 4, kBars = kM + D * 2, kSmall = kBars + (int)sizeof(Bars);
   static constexpr int kBytes = (kSmall + 1023) / 1024 * 1024 + kEnd;
   static_assert(kBytes <= (D == 64 ? 115712 : 232448), "two blocks of d = 64 an SM, one of d = 128");
 };
@@ -893,8 +967,31 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   const int tiles = (rows + kT - 1) / kT, bb = p.c.ks.cu == nullptr ? g.seq : 0;
   const auto whole = [&](int j) { return p.c.ks.cu == nullptr || (j + 1) * kT <= g.len; };  // (dense: the tensor ends there too)
   const float* from = p.c.dS + ((size_t)g.seq * p.c.Hk + h) * (D * D + D);
-  if (tid < X::kWork) load_matrix<D>(sm + M::kS, sm + M::kSLo, from);
-  if (tid < D) z[tid] = from[D * D + tid];
+  if (tid < X::kWork) {
+    const size_t unit = (size_t)g.seq * p.c.Hk + h;
+    __nv_bfloat16* mid = reinterpret_cast<__nv_bfloat16*>(smraw + M::kM);
+    Matrix<D> S, dS;
+    S.load(p.c.S + unit * D * D);
+    dS.load(from);
+    middle<D>(S, p.c.z + unit * D, p.c.normalise, z, reinterpret_cast<float*>(sm + M::kS), mid, 1);
+    float2 m[4];
+    unpack8(*reinterpret_cast<const uint4*>(mid + 8 * S.piece_of_row()), m);
+    dS.put(sm + M::kS, sm + M::kSLo);
+    // z: dz' - dS m, of dS as it lies there
+#pragma unroll
+    for (int n = 0; n < S.N; ++n) {
+      const int r = S.row(n);
+      float2 a[4], e[4], s2 = both(0.f);
+      unpack8(*piece(sm + M::kS, D, r, S.piece_of_row()), a);
+      unpack8(*piece(sm + M::kSLo, D, r, S.piece_of_row()), e);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s2 = fma2(add2(a[x], e[x]), m[x], s2);
+      float s1 = s2.x + s2.y;
+#pragma unroll
+      for (int o = 1; o < S.P; o <<= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      if (S.piece_of_row() == 0) z[r] = from[D * D + r] - s1;
+    }
+  }
   if (tid >= X::kWork) {
     if (lane == 0) {
       const auto fetch = [&](int j) {
