@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
   using X = Tc<D>;
   using M = SumSmem<D>;
   constexpr bool kExact = F == MHLA_PHI_RELU || F == MHLA_PHI_IDENTITY;  // phi(k) is a bf16 number
-  constexpr uint32_t kColumns = 2 * D;
+  constexpr uint32_t kColumns = 4 * D;  // the tiles in turn into two sets: half as many additions, which are cut, one behind the other
   constexpr int kSumAtom = kSumT * 128;
   extern __shared__ __align__(16) uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + M::kSmall + 1023) & ~uintptr_t(1023));
@@ -404,8 +404,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
         const uint64_t da = along_rows(va, kSumAtom), d1 = along_rows(pa, kSumAtom), d2 = along_rows(pa + 2 * M::kPart, kSumAtom);
 #pragma unroll
         for (int s = 0; s < kSumT / 16; ++s) {
-          mma_bf16(tmem, da + s * 128, d1 + s * 128, idesc_bf16_f32(128, kExact ? D : 2 * D, 1, 1), j > 0 || s > 0);
-          if (!kExact) mma_bf16(tmem + D, da + s * 128, d2 + s * 128, idesc_bf16_f32(128, D, 1, 1), true);
+          const uint32_t acc = tmem + (j & 1) * 2 * D;
+          mma_bf16(acc, da + s * 128, d1 + s * 128, idesc_bf16_f32(128, kExact ? D : 2 * D, 1, 1), j > 1 || s > 0);
+          if (!kExact) mma_bf16(acc + D, da + s * 128, d2 + s * 128, idesc_bf16_f32(128, D, 1, 1), true);
         }
         mma_commit(&b->mma[j & 1]);
         b->mmas = j + 1;
@@ -485,15 +486,20 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
         if (tiles > 0) {
           tmem_ld16(at, v);
           tmem_ld16(at + 16, v + 16);
-          if (!kExact) {
+          tmem_ld_wait();
+          const auto add = [&](uint32_t at) {
             float w[32];
-            tmem_ld16(at + D, w);
-            tmem_ld16(at + D + 16, w + 16);
+            tmem_ld16(at, w);
+            tmem_ld16(at + 16, w + 16);
             tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] += w[x];
+          };
+          if (!kExact) add(at + D);
+          if (tiles > 1) {
+            add(at + 2 * D);
+            if (!kExact) add(at + 3 * D);
           }
-          tmem_ld_wait();
         }
 #pragma unroll
         for (int x = 0; x < 32; ++x) so[(c0 + x) * D + e] = tiles > 0 ? v[x] : 0.f;
@@ -509,17 +515,20 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
 // storing rows of 64 bytes, which occupies the shared memory's data path, and three buffers throughout: 13 and 50.
 // Three buffers (d = 128: four) and two accumulators: while the MMA of a tile runs the warps put the results of the one before
 // into its place, whence they are copied out, and take the next one's features.
-template <int D>
+// S as one bf16 number, whose rounding is that of phi(q); where phi(q) is a bf16 number itself as two, so that y is rounded once.
+template <int D, int F>
 struct ReadSmem {
+  static constexpr bool kTwo = F == MHLA_PHI_RELU || F == MHLA_PHI_IDENTITY;
   static constexpr int kBuffers = D == 64 ? 3 : 4;
-  static constexpr int kQ = 0, kS = kBuffers * Tc<D>::kTile, kZ = kS + Tc<D>::kMat, kDen = kZ + D * 4,
-                       kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
+  static constexpr int kQ = 0, kS = kBuffers * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat, kZ = kSLo + (kTwo ? Tc<D>::kMat : 0),
+                       kDen = kZ + D * 4, kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
   static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
+  static_assert(kBytes <= (D == 64 ? 76800 : 232448), "three blocks of d = 64 an SM, one of d = 128");
 };
 template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_read_kernel(const __grid_constant__ TcArgs p) {
   using X = Tc<D>;
-  using M = ReadSmem<D>;
+  using M = ReadSmem<D, F>;
   constexpr int NB = M::kBuffers;
   constexpr uint32_t kColumns = 2 * D;
   extern __shared__ __align__(16) uint8_t smraw[];
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   if (tid < X::kWork) {
     Matrix<D> S;
     S.load(p.c.S + unit * D * D);
-    S.put(sm + M::kS, nullptr);
+    S.put(sm + M::kS, M::kTwo ? sm + M::kSLo : nullptr);
   }
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
   if (tid >= X::kWork) {
@@ -550,7 +559,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
         load_tile(sm + M::kQ + j % NB * X::kTile, &p.a, g.row0 + j * kT, p.a_h ? h : 0, p.a_b ? bb : 0, bar);
         b->issued = j + 1;
       };
-      const uint32_t sa = smem_u32(sm + M::kS);
+      const uint32_t sa = smem_u32(sm + M::kS), sl = smem_u32(sm + M::kSLo);
       // the results of tile j, and another tile into its place
       const auto out = [&](int j) {
         if (!wait(&b->out[j & 1], (j >> 1) & 1, b)) return false;
@@ -571,9 +580,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
         tc_fence_after();
         const uint32_t qa = smem_u32(sm + M::kQ + j % NB * X::kTile);
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          mma_bf16(tmem + (j & 1) * D, along_cols<D>(qa, kAtom, s), along_rows(sa, D * 128) + s * 128, idesc_bf16_f32(128, D, 0, 1),
-                   s > 0);
+        for (int part = 0; part < (M::kTwo ? 2 : 1); ++part)
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_bf16(tmem + (j & 1) * D, along_cols<D>(qa, kAtom, s), along_rows(part ? sl : sa, D * 128) + s * 128,
+                     idesc_bf16_f32(128, D, 0, 1), s > 0 || part > 0);
         mma_commit(&b->mma[j & 1]);
         b->mmas = j + 1;
         if (j > 0 && !out(j - 1)) break;
@@ -1052,6 +1063,8 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
                       ((long long)g.row0 + row) * p.c.dk.sn + pl.col;
   __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.dv.p)) + cross_base(p.c.ks, p.c.dv, g.seq, h) +
                       ((long long)g.row0 + row) * p.c.dv.sn + pl.col;
+  const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(p.c.k.p) + cross_base(p.c.ks, p.c.k, g.seq, h) +
+                              ((long long)g.row0 + row) * p.c.k.sn + pl.col;
   // phi(k) of tile j over its keys
   const auto features = [&](int j) {
     uint8_t* kt = sm + M::kK + j % NB * X::kTile;
@@ -1071,11 +1084,15 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   bool ok = tiles == 0 || features(0);
   for (int j = 0; ok && j < tiles; ++j) {
     if (j + 1 < tiles && !features(j + 1)) break;
+    const bool live = row < g.len - j * kT;  // (dense: zeros behind the tokens)
+    uint4 own[4];  // k once more, where phi' is all of phi (elsewhere it goes by phi as it lies there, rounded to bf16)
+    if (F == MHLA_PHI_EXP && live)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own[i] = reinterpret_cast<const uint4*>(keys + (long long)j * kT * p.c.k.sn)[i];
     ok = __all_sync(0xffffffffu, wait(&b->mma[j & 1], (j >> 1) & 1, b));
     if (!ok) break;
     tc_fence_after();
     uint8_t *kt = sm + M::kK + j % NB * X::kTile, *vt = sm + M::kV + j % NB * X::kTile;
-    const bool live = row < g.len - j * kT;  // (dense: zeros behind the tokens)
     const uint32_t acc = at + (j & 1) * 2 * D;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -1086,7 +1103,13 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float2 f[4], zz[4];
-        if (F != MHLA_PHI_IDENTITY) unpack8(at_byte(kt, pl.own[2 * c + i]), f);  // (phi rounded to bf16: phi' goes by it, and its rounding by dk's)
+        if (F == MHLA_PHI_EXP) {
+          unpack8(own[2 * c + i], f);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) f[x] = feature<F>(f[x]);
+        } else if (F != MHLA_PHI_IDENTITY) {
+          unpack8(at_byte(kt, pl.own[2 * c + i]), f);
+        }
         load8(z + cg * 32 + 16 * c + 8 * i, zz);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -1172,7 +1195,7 @@ cudaError_t read_t(const CrossArgs& a, cudaStream_t st) {
   TcArgs t;
   if (!make_args(&t, a, a.qs, a.H, a.q, nullptr, &a.y, nullptr)) return cudaErrorInvalidValue;
   static SmemOptIn opt;
-  return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, ReadSmem<D>::kBytes, t, st);
+  return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, (ReadSmem<D, F>::kBytes), t, st);
 }
 template <int D, int F>
 cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
