@@ -3,7 +3,7 @@
 //
 //   states  D[e][c] += sum_t v[t][e] phi(k)[t][c]   (A = v, B = phi(k) as a sum of three bf16 numbers: S is an fp32
 //           result), z in fp32 registers
-//   read    y[t][e] = (sum_c phi(q)[t][c] S[c][e]) / den_t
+//   read    y[t][e] = (sum_c phi(q)[t][c] S[c][e]) / den_t   (S as a sum of two bf16 numbers)
 //   query   u[t][c] = sum_e dy[t][e] S[c][e], dS^T[e][c] += sum_t dy[t][e] w[t][c] with w = phi(q) / den; S (less a middle of
 //           the values, `middle`) and w as sums of two bf16 numbers, as dq is a difference, dy as it is; dz in fp32
 //   key     dv[t][e] = sum_c phi(k)[t][c] dS[c][e], dphi(k)[t][c] = sum_e v[t][e] dS[c][e] (dS as a sum of two)
@@ -14,9 +14,9 @@
 // from tensor memory and put them into the tile's buffer, whence TMA copies them out (a packed sequence's last tile: the warps,
 // as its rows end within it).  Two blocks an SM for d = 64 (reads: three), one for d = 128, hide one another's waits.  Every
 // wait is bounded (on time-out the block stops, sets the status word and drains what it has in flight).
-// Measured in a graph: states and read of 8 x 6 heads, 4096 queries, 77 keys, d 64: 17 us; of 4 key heads of 65,536 keys, d 128,
-// and 777 queries of 16 heads: 45 (3.1 TB/s); forward and gradients of 8 x 6 heads, 4096 queries, 2048 keys, d 64: 71 (2.8
-// TB/s), of 8 x 8 heads, d 128: 208 (2.6 TB/s).
+// Measured in a graph: states and read of 8 x 6 heads, 4096 queries, 77 keys, d 64: 18 us; of 4 key heads of 65,536 keys, d 128,
+// and 777 queries of 16 heads: 45 (3.1 TB/s); forward and gradients of 8 x 6 heads, 4096 queries, 2048 keys, d 64: 73 (2.8
+// TB/s), of 8 x 8 heads, d 128: 216 (2.5 TB/s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -510,25 +510,26 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
 }
 
 // ================================================================ read
-// 8 x 6 heads of 4096 queries, d = 64: 12 us (50 MB, 4.3 TB/s), 8 x 8 heads, d = 128: 32 (134 MB, 4.2 TB/s); issue slots 40 %,
-// the rest the start and the chain of a tile (copy, features, MMA, results) that three blocks an SM share.  With the warps
-// storing rows of 64 bytes, which occupies the shared memory's data path, and three buffers throughout: 13 and 50.
+// 8 x 6 heads of 4096 queries, d = 64: 13 us (50 MB, 3.9 TB/s), 8 x 8 heads, d = 128: 36 (134 MB, 3.7 TB/s); issue slots 40 %,
+// the rest the start and the chain of a tile (copy, features, MMA, results) that three blocks an SM share.  With S as one bf16
+// number and den of the unrounded phi(q) 12 and 32, but y of one key off by up to 2e-4 of it; the same with the warps storing
+// rows of 64 bytes, which occupies the shared memory's data path, and three buffers throughout: 13 and 50.
 // Three buffers (d = 128: four) and two accumulators: while the MMA of a tile runs the warps put the results of the one before
 // into its place, whence they are copied out, and take the next one's features.
-// S as one bf16 number, whose rounding is that of phi(q); where phi(q) is a bf16 number itself as two, so that y is rounded once.
-template <int D, int F>
+// phi(q) is rounded to bf16 for den as for the product, so that the weights of the values add up to one whatever the rounding; with S
+// as two bf16 numbers y is then as exact as its own rounding where the values are alike (one key: y is its value).
+template <int D>
 struct ReadSmem {
-  static constexpr bool kTwo = F == MHLA_PHI_RELU || F == MHLA_PHI_IDENTITY;
   static constexpr int kBuffers = D == 64 ? 3 : 4;
-  static constexpr int kQ = 0, kS = kBuffers * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat, kZ = kSLo + (kTwo ? Tc<D>::kMat : 0),
-                       kDen = kZ + D * 4, kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
+  static constexpr int kQ = 0, kS = kBuffers * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat, kZ = kSLo + Tc<D>::kMat, kDen = kZ + D * 4,
+                       kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
   static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
   static_assert(kBytes <= (D == 64 ? 76800 : 232448), "three blocks of d = 64 an SM, one of d = 128");
 };
 template <int D, int F>
 __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_read_kernel(const __grid_constant__ TcArgs p) {
   using X = Tc<D>;
-  using M = ReadSmem<D, F>;
+  using M = ReadSmem<D>;
   constexpr int NB = M::kBuffers;
   constexpr uint32_t kColumns = 2 * D;
   extern __shared__ __align__(16) uint8_t smraw[];
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   if (tid < X::kWork) {
     Matrix<D> S;
     S.load(p.c.S + unit * D * D);
-    S.put(sm + M::kS, M::kTwo ? sm + M::kSLo : nullptr);
+    S.put(sm + M::kS, sm + M::kSLo);
   }
   if (tid < D) z[tid] = p.c.z[unit * D + tid];
   if (tid >= X::kWork) {
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
         tc_fence_after();
         const uint32_t qa = smem_u32(sm + M::kQ + j % NB * X::kTile);
 #pragma unroll
-        for (int part = 0; part < (M::kTwo ? 2 : 1); ++part)
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
             mma_bf16(tmem + (j & 1) * D, along_cols<D>(qa, kAtom, s), along_rows(part ? sl : sa, D * 128) + s * 128,
@@ -618,11 +619,14 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
         unpack8(*q, f);
         load8(z + cg * 32 + 8 * i, zz);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          f[x] = feature<F>(f[x]);
-          d = fma2(f[x], zz[x], d);
+        for (int x = 0; x < 4; ++x) f[x] = feature<F>(f[x]);
+        if (F != MHLA_PHI_IDENTITY) {
+          const uint4 u = pack8(f);
+          *q = u;
+          unpack8(u, f);
         }
-        if (F != MHLA_PHI_IDENTITY) *q = pack8(f);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) d = fma2(f[x], zz[x], d);
       }
       den[(slot3 * X::kCols + cg) * kT + row] = d.x + d.y;
       arrive(&b->ready[slot3], lane);
@@ -1195,7 +1199,7 @@ cudaError_t read_t(const CrossArgs& a, cudaStream_t st) {
   TcArgs t;
   if (!make_args(&t, a, a.qs, a.H, a.q, nullptr, &a.y, nullptr)) return cudaErrorInvalidValue;
   static SmemOptIn opt;
-  return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, (ReadSmem<D, F>::kBytes), t, st);
+  return launch(tc_cross_read_kernel<D, F>, opt, (long long)a.qs.segs * a.H, Tc<D>::kThreads, ReadSmem<D>::kBytes, t, st);
 }
 template <int D, int F>
 cudaError_t backward_t(const CrossArgs& a, cudaStream_t st) {
