@@ -23,6 +23,7 @@
 #include <mutex>
 
 #include "cross.cuh"
+#include "cross_ring.h"
 #include "tc_common.cuh"
 #include "tc_cross.h"
 
@@ -520,9 +521,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_sta
 // as two bf16 numbers y is then as exact as its own rounding where the values are alike (one key: y is its value).
 template <int D>
 struct ReadSmem {
-  static constexpr int kBuffers = D == 64 ? 3 : 4;
+  static constexpr int kBuffers = read_buffers(D), kSums = read_sums(D);
   static constexpr int kQ = 0, kS = kBuffers * Tc<D>::kTile, kSLo = kS + Tc<D>::kMat, kZ = kSLo + Tc<D>::kMat, kDen = kZ + D * 4,
-                       kBars = kDen + 3 * Tc<D>::kCols * kT * 4;
+                       kBars = kDen + kSums * Tc<D>::kCols * kT * 4;
+  static_assert(kSums == kBuffers, "a tile's sums lie beside its buffer");
   static constexpr int kBytes = 1024 + kBars + (int)sizeof(Bars);
   static_assert(kBytes <= (D == 64 ? 76800 : 232448), "three blocks of d = 64 an SM, one of d = 128");
 };
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(const_cast<void*>(p.c.y.p)) + cross_base(p.c.qs, p.c.y, g.seq, h) +
                      ((long long)g.row0 + row) * p.c.y.sn + pl.col;
   bool ok = true;
-  int buf = 0, before = 0, phase = 0, slot3 = 0, before3 = 0;  // of tiles j and j - 1: their buffers (and phase), j % 3
+  int buf = 0, before = 0, phase = 0, slot3 = 0;  // of tiles j and j - 1: their buffers, with their sums (and phase); j % 3
   for (int j = 0; ok && j <= tiles; ++j) {
     if (j < tiles) {  // the features of tile j
       uint8_t* qt = sm + M::kQ + buf * X::kTile;
@@ -628,7 +630,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
 #pragma unroll
         for (int x = 0; x < 4; ++x) d = fma2(f[x], zz[x], d);
       }
-      den[(slot3 * X::kCols + cg) * kT + row] = d.x + d.y;
+      den[(buf * X::kCols + cg) * kT + row] = d.x + d.y;
       arrive(&b->ready[slot3], lane);
     }
     if (j > 0) {  // tile j - 1 goes out
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
       if (p.c.normalise) {
         float d = p.c.eps;
 #pragma unroll
-        for (int i = 0; i < X::kCols; ++i) d += den[(before3 * X::kCols + i) * kT + row];
+        for (int i = 0; i < X::kCols; ++i) d += den[(before * X::kCols + i) * kT + row];
         inv = inverse(d);
       }
       tmem_ld_wait();
@@ -656,7 +658,6 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 3 : 1) tc_cross_rea
       arrive(&b->out[t & 1], lane);
     }
     before = buf;
-    before3 = slot3;
     buf = buf == NB - 1 ? 0 : buf + 1;
     phase ^= buf == 0;
     slot3 = slot3 == 2 ? 0 : slot3 + 1;
