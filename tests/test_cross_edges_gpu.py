@@ -33,3 +33,25 @@ def test_reads_of_many_tiles(d, H, n):
         c.y.fill_(7.0)
         c.run(backward=False)
         assert torch.equal(c.y, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_packed_sides_without_a_token(d, dtype):
+    """Tensors of no rows at all: S and z become zeros (in their slots, others stay), dq is zero, dk and dv of no queries are."""
+    B, H, Hk, n = 3, 4, 2, 150
+    c = Call(B, H, Hk, n, 0, d, dtype, cu_q=[0, 100, 100, n], cu_k=[0, 0, 0, 0]).run()
+    assert not c.S.any() and not c.z.any() and not c.y.any() and not c.dq.any()
+    pool, zp = torch.full((5, Hk, d, d), 5.0, device="cuda"), torch.full((5, Hk, d), 5.0, device="cuda")
+    slots = torch.tensor([4, -1, 1], dtype=torch.int32, device="cuda")
+    lib.linattn_cross_states(c.k, c.v, pool, zp, cu_seqlens=c.dev(c.cu_k), slots=slots)
+    assert not pool[[1, 4]].any() and not zp[[1, 4]].any() and (pool[[0, 2, 3]] == 5).all() and (zp[[0, 2, 3]] == 5).all()
+    c = Call(B, H, Hk, 0, n, d, dtype, cu_q=[0, 0, 0, 0], cu_k=[0, 100, 100, n]).run()
+    for i in range(B):
+        k, v = (to_f64(t[0, :, c.cu_k[i]:c.cu_k[i + 1]]) for t in (c.k, c.v))
+        (S, z), (mS, mz) = co.states(k, v), co.states(k, np.abs(v))
+        check(c.S[i], S, mS, F32, n, 0, f"S of {i}")
+        check(c.z[i], z, mz, F32, n, 0, f"z of {i}")
+    assert not c.dk.any() and not c.dv.any()
+    c = Call(B, H, Hk, 0, 0, d, dtype, cu_q=[0, 0, 0, 0], cu_k=[0, 0, 0, 0]).run()
+    assert not c.S.any() and not c.z.any()

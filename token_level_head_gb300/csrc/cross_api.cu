@@ -35,11 +35,12 @@ int segment_length(const CrossSide& s, int heads, const Kind& k) {
   }
   return (int)std::max((long long)k.unit, std::min((L + k.unit - 1) / k.unit * k.unit, most));
 }
-// Cuts a side; false where the segments cannot be numbered.
+// Cuts a side; false where the segments cannot be numbered.  A side without a token has none (packed too): its tensors may
+// have no address, and the joins of no parts give the zeros.
 bool cut_side(CrossSide* s, int B, int N, const int* cu, const int* lens, int heads, const Kind& k) {
   *s = {B, N, cu ? N : 0, cu, lens, 0, 0};
   s->L = segment_length(*s, heads, k);
-  const long long segs = cu ? (long long)N / s->L + B : (long long)B * ret_pieces(N, s->L);
+  const long long segs = N == 0 ? 0 : cu ? (long long)N / s->L + B : (long long)B * ret_pieces(N, s->L);
   s->segs = (int)std::min(segs, 0x7fffffffll);
   return segs * std::max(heads, 1) <= 0x7fffffffll;
 }
