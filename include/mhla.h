@@ -519,7 +519,8 @@ mhla_status linattn_cross_read(const void* q, const mhla_strides* q_strides, con
  * (normalise = 0: den = 1, dden = 0); phi' as in retention_backward.
  *   S, z       : those of linattn_cross_states for these k and v: slot i is sequence i
  *   dq, dk, dv : written (not accumulated); rows of a padded encoder batch behind
- *                lens become zeros, rows of no packed sequence stay as they are. */
+ *                lens become zeros, rows of no packed sequence stay as they are;
+ *                without a query (H or Nq = 0) dk and dv are zeros. */
 mhla_status linattn_cross_backward(const void* q, const mhla_strides* q_strides, const void* k, const mhla_strides* k_strides,
                                    const void* v, const mhla_strides* v_strides, const float* S, const float* z,
                                    const void* dy, const mhla_strides* dy_strides, void* dq, const mhla_strides* dq_strides,

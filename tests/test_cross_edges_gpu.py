@@ -55,3 +55,13 @@ def test_packed_sides_without_a_token(d, dtype):
     assert not c.dk.any() and not c.dv.any()
     c = Call(B, H, Hk, 0, 0, d, dtype, cu_q=[0, 0, 0, 0], cu_k=[0, 0, 0, 0]).run()
     assert not c.S.any() and not c.z.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_no_query_head(d, dtype):
+    """No head of queries on two of keys: the gradients of keys and values are zeros."""
+    for cu in (None, [0, 100, 150]):
+        c = Call(2, 0, 2, 150, 150, d, dtype, cu_q=cu, cu_k=cu)
+        c.run()
+        assert not c.dk.any() and not c.dv.any() and c.S.any()

@@ -85,6 +85,18 @@ def test_gradients_of_a_side_without_a_token_have_no_segments_there(host, packed
 
 
 @pytest.mark.parametrize("d,dt", WIDTHS)
+@pytest.mark.parametrize("packed", [False, True])
+def test_gradients_without_a_query_head(host, packed, d, dt):
+    """No query head on two of keys: no segments of queries, dk and dv are zeros."""
+    cu = dict(cq=20 * P, ck=21 * P) if packed else {}
+    calls(host)
+    assert backward(host, H=0, d=d, dt=dt, **cu) == OK
+    assert plan(host, True)[0] == 0 and plan(host, True)[1] > 0
+    assert backward(host, H=0, Nk=0, d=d, dt=dt, **cu) == OK
+    assert calls(host) == [0, 0, 1, 0]
+
+
+@pytest.mark.parametrize("d,dt", WIDTHS)
 @pytest.mark.parametrize("B,H,Hk,nq,nk", [(3, 6, 2, 1000, 70), (1, 4, 4, 129, 9000), (7, 2, 1, 4096, 33), (600, 1, 1, 1, 1),
                                           (1, 16, 4, 777, 65536), (2, 2, 2, 0, 500), (2, 2, 2, 500, 0)])
 def test_the_workspace_query_is_enough_and_less_than_a_calls_need_is_refused(host, B, H, Hk, nq, nk, d, dt):

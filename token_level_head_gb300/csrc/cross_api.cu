@@ -204,6 +204,7 @@ mhla_status linattn_cross_backward(const void* q, const mhla_strides* q_strides,
                                    size_t workspace_bytes, void* stream) {
   if (!sizes_ok(B, H, Hk, Nq, d) || Nk < 0 || (dt != MHLA_F32 && dt != MHLA_BF16) || !options_ok(opt, eps))
     return MHLA_ERR_INVALID_ARG;
+  if (H == 0) Nq = 0;  // no query head is no query: dk and dv become zeros
   if (B == 0 || Hk == 0 || (Nq == 0 && Nk == 0)) return MHLA_OK;
   mhla_status st = check_side(B, Nq, cu_seqlens_q != nullptr, cu_seqlens_q, nullptr);
   if (st == MHLA_OK) st = check_side(B, Nk, cu_seqlens_k != nullptr, cu_seqlens_k, lens);
