@@ -1,0 +1,70 @@
+"""The gated scan on the GPU at its edges, against the float64 oracle; tolerances as in ``test_gated_scan_gpu`` where no
+other is derived."""
+
+import numpy as np
+import pytest
+import torch
+
+import token_level_head_gb300 as lib
+from gpu_util import to_f64
+from oracle import gated_scan_oracle as go
+from test_gated_scan_gpu import BF, F32, GATES, check, check_backward, check_forward, gate_values, kept, rand
+from token_level_head_gb300.build import build_library
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    build_library()
+
+
+def gates_by_the_step(g, gate):
+    """The gates a that the library takes for g [n]: the state of a step on h = 1, x = 0."""
+    n = -(-g.numel() // 8) * 8
+    wide = torch.zeros(1, n, dtype=g.dtype, device="cuda")
+    wide[0, :g.numel()] = g
+    states, out = torch.ones(1, n, device="cuda"), torch.empty_like(wide)
+    lib.gated_scan_step(torch.zeros_like(wide), wide, states, out, gate=gate)
+    return to_f64(states[0, :g.numel()])
+
+
+def all_bf16(lo, hi):
+    """Every bf16 number of [lo, hi]."""
+    v = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(BF)
+    v = v[torch.isfinite(v.float())]
+    return v[(v.float() >= lo) & (v.float() <= hi)].cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_small_sigmoid_gates_keep_their_digits(dtype):
+    """e / (1 + e), e = exp(g), relative to itself: e is within 2 steps of 2^-23 (fp32: expf), or within 2^-22 and a product of
+    half a step of |g| log2 e (bf16); 1 + e half a step and the share of e's; its reciprocal and the product 1.5 steps more;
+    the product with h none (h = 1).  Gates below 2^-126 may be zero."""
+    g = torch.linspace(-87.0, 20.0, 60000, device="cuda") if dtype == F32 else all_bf16(-87.0, 20.0)
+    a, ref = gates_by_the_step(g, "sigmoid"), 1 / (1 + np.exp(-to_f64(g)))
+    exp_off = 2 * 2.0 ** -23 if dtype == F32 else 2.0 ** -22 + np.abs(to_f64(g)) * 2.0 ** -24
+    assert (np.abs(a - ref) <= ref * (2 * exp_off + 2 * 2.0 ** -23) * 1.001 + 2.0 ** -126).all(), np.max(np.abs(a - ref) / ref)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("packed", [False, True])
+def test_states_through_small_sigmoid_gates(packed, dtype):
+    """Tokens without an input (x = 0, padding) and gates from 1/4 to e^-30 (bf16: e^-12): y and the state are the start times the
+    gates, with their digits.  bf16: a gate is off by |g| 2^-24 + 2^-22 + 4 2^-23 < 2^-19 for |g| <= 12."""
+    B, N, D = 3, 6, 64
+    x = torch.zeros(B, N, D, dtype=dtype, device="cuda")
+    g = -(1 + torch.rand(B, N, D, generator=torch.Generator().manual_seed(1)) * (29 if dtype == F32 else 11)).to(dtype).cuda()
+    g[:, 3:] = 8.0                                     # and then kept
+    h0, dl, dy = rand(B, D, seed=2), rand(B, D, seed=3), torch.zeros_like(x)
+    y, dx, dg, st, dh0, kw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), h0.clone(), torch.empty_like(h0), {}
+    t = [x, g, y, dy, dx, dg]
+    if packed:
+        t, kw = [a.view(1, -1, D) for a in t], dict(cu_seqlens=torch.arange(B + 1, dtype=torch.int32, device="cuda") * N)
+    ck = kept(t[0])
+    lib.gated_scan_forward(*t[:3], states=st, load_state=True, checkpoints=ck, **kw)
+    check_forward(x, g, y, "sigmoid", start=h0, final=st)
+    lib.gated_scan_backward(t[0], t[1], t[3], ck, *t[4:], h0=h0, dh_last=dl, dh0=dh0, **kw)
+    check_backward(x, g, dy, dx, dg, "sigmoid", h0=h0, dl=dl, dh0=dh0)

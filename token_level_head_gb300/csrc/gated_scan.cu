@@ -12,7 +12,7 @@
 // (A, B) through distributed shared memory, and a cluster walks along the sequence.  So x and g are read once and no memory,
 // flag or wait is shared between clusters.
 // Measured, whole calls: 65,536 x 1024 bf16, log, 79 us (5.1 TB/s); 77 x 1024 bf16 8; forward and backward of 4 x 8192 x 1024
-// bf16, sigmoid, 121 (4.4 TB/s), of 20,011 packed x 384 fp32, decay, 73 (3.4 TB/s); the step of 256 x 8192 bf16 8.
+// bf16, sigmoid, 126 (4.3 TB/s), of 20,011 packed x 384 fp32, decay, 73 (3.4 TB/s); the step of 256 x 8192 bf16 8.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -136,14 +136,20 @@ __device__ __forceinline__ float rcp_of(float x) {
   return r;
 }
 
+// a = e rest where e < 2: a comparison and a product under it (both forms and a selection: 129 us instead of 126 for the forward
+// and backward of 4 x 8192 x 1024).
+__device__ __forceinline__ void small_gate(float& a, float e, float rest) {
+  asm("{\n\t.reg .pred p;\n\tsetp.lt.f32 p, %1, 0f40000000;\n\t@p mul.f32 %0, %1, %2;\n\t}" : "+f"(a) : "f"(e), "f"(rest));
+}
+
 struct Gate {
   float2 a;     // the gate
   float2 rest;  // sigmoid: 1 - a, the factor of x
-  float2 low;   // sigmoid: a once more, with all its digits also where it is small
 };
-// sigmoid, with e = exp(g): 1 - a = 1 / (1 + e), which needs no case for either end; a = 1 - (1 - a), so that gates near 1 are
-// rounded once (a long memory multiplies thousands of them, and their errors) and all are within 2^-24; low = e / (1 + e) where
-// that is below 2/3.  Not-a-number stays.
+// sigmoid, with e = exp(g): 1 - a = 1 / (1 + e), which needs no case for either end.  a = e / (1 + e) below 2/3, so that a small
+// gate has all its digits (what fades is off by 2^-21 of itself, not of x; a = 1 - (1 - a) throughout had 5e-4 at g = -10 and
+// zero from -17 on); from there 1 - (1 - a), so that gates near 1 are rounded once (a long memory multiplies thousands of them,
+// and their errors).  Not-a-number stays.
 template <typename T, int GATE>
 __device__ __forceinline__ Gate gate_of(float2 g) {
   Gate k;
@@ -155,8 +161,8 @@ __device__ __forceinline__ Gate gate_of(float2 g) {
     const float2 e = exp_of<T>(g), d = add2(e, both(1.f));
     k.rest = make_float2(rcp_of(d.x), rcp_of(d.y));
     k.a = fma2(k.rest, both(-1.f), both(1.f));
-    const float2 low = mul2(e, k.rest);
-    k.low = make_float2(e.x < 2.f ? low.x : k.a.x, e.y < 2.f ? low.y : k.a.y);
+    small_gate(k.a.x, e.x, k.rest.x);
+    small_gate(k.a.y, e.y, k.rest.y);
   }
   return k;
 }
@@ -914,15 +920,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
           k[i] = mul2(a[r][i], G[r][i]);
         }
         if constexpr (!plain) {
-          if (starts >> r & 1) {
-            if (GATE == GATED_SCAN_SIGMOID) {  // (a small gate with all its digits)
-              float2 gv[P];
-              unpack<T>(*reinterpret_cast<const Raw*>(row_at<CW>(sg, r, delta)), gv);
-#pragma unroll
-              for (int i = 0; i < P; ++i) k[i] = mul2(gate_of<T, GATE>(gv[i]).low, G[r][i]);
-            }
+          if (starts >> r & 1)
             store(p.dh0 + (long long)sequence_of(r) * p.D + c, k);
-          }
         }
       }
 #pragma unroll
@@ -938,7 +937,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
           const Gate gt = gate_of<T, GATE>(gv[i]);
           if (GATE == GATED_SCAN_SIGMOID) {
             ox[i] = mul2(gt.rest, G[r][i]);
-            og[i] = mul2(mul2(gt.low, ox[i]), fma2(xv[i], both(-1.f), h[i]));
+            og[i] = mul2(mul2(gt.a, ox[i]), fma2(xv[i], both(-1.f), h[i]));
             h[i] = fma2(gt.a, h[i], mul2(gt.rest, xv[i]));
           } else {
             ox[i] = G[r][i];
