@@ -40,12 +40,12 @@ def all_bf16(lo, hi):
 
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_small_sigmoid_gates_keep_their_digits(dtype):
-    """e / (1 + e), e = exp(g), relative to itself: e is within 2 steps of 2^-23 (fp32: expf), or within 2^-22 and a product of
-    half a step of |g| log2 e (bf16); 1 + e half a step and the share of e's; its reciprocal and the product 1.5 steps more;
+    """e / (1 + e), e = exp(g), relative to itself: e is within 2 steps of 2^-23 (fp32: expf), or within 2^-22, half a step of
+    |g| log2 e and the rounding of log2 e, 2^-26 of itself (bf16); 1 + e half a step and the share of e's; its reciprocal and the product 1.5 steps more;
     the product with h none (h = 1).  Gates below 2^-126 may be zero."""
     g = torch.linspace(-87.0, 20.0, 60000, device="cuda") if dtype == F32 else all_bf16(-87.0, 20.0)
     a, ref = gates_by_the_step(g, "sigmoid"), 1 / (1 + np.exp(-to_f64(g)))
-    exp_off = 2 * 2.0 ** -23 if dtype == F32 else 2.0 ** -22 + np.abs(to_f64(g)) * 2.0 ** -24
+    exp_off = 2 * 2.0 ** -23 if dtype == F32 else 2.0 ** -22 + np.abs(to_f64(g)) * (2.0 ** -24 + 2.0 ** -26)
     assert (np.abs(a - ref) <= ref * (2 * exp_off + 2 * 2.0 ** -23) * 1.001 + 2.0 ** -126).all(), np.max(np.abs(a - ref) / ref)
 
 
@@ -68,3 +68,26 @@ def test_states_through_small_sigmoid_gates(packed, dtype):
     check_forward(x, g, y, "sigmoid", start=h0, final=st)
     lib.gated_scan_backward(t[0], t[1], t[3], ck, *t[4:], h0=h0, dh_last=dl, dh0=dh0, **kw)
     check_backward(x, g, dy, dx, dg, "sigmoid", h0=h0, dl=dl, dh0=dh0)
+
+
+def test_bf16_log_gates():
+    """exp(g), relative to itself: the hardware's base-2 exponential is within 2^-22; half a step of |g| log2 e, and the rounding of
+    log2 e (1.44269502 for 1.44269504, 0.9 2^-26 of itself).  Half a bf16 step of g is |g| 2^-9."""
+    g = all_bf16(-87.0, 0.0)
+    a, ref, size = gates_by_the_step(g, "log"), np.exp(to_f64(g)), np.abs(to_f64(g))
+    tol = 2.0 ** -22 + size * (2.0 ** -24 + 2.0 ** -26)
+    off = np.abs(a - ref) / ref
+    assert (off <= tol * 1.001 + 2.0 ** -126 / ref).all(), (off / tol).max()
+
+
+@pytest.mark.parametrize("rate", [-2.0 ** -10, -1e-4, -1e-5])
+def test_long_memories_of_constant_log_gates(rate):
+    """65,536 tokens of one bf16 gate near 1: the last state in 32 bits.  A token costs the state the gate's rounding (2^-25) and a
+    product's or sum's (2^-24), and an eighth of those where runs of sixteen tokens are joined: below the oracle's 2 x 2^-24."""
+    N, D = 65536, 64
+    g = torch.full((1, N, D), rate, device="cuda").to(BF)
+    x, y, st = rand(1, N, D, seed=1, dtype=BF) + 1, torch.empty(1, N, D, dtype=BF, device="cuda"), torch.empty(1, D, device="cuda")
+    lib.gated_scan_forward(x, g, y, gate="log", states=st)
+    s = slice(0, 64, 9)
+    ref, e = go.scan(to_f64(x[0, :, s]), to_f64(g[0, :, s]), "log", None, 2.0 ** -24)
+    check(st[0, s], ref[-1], e[-1], F32, "last state")
