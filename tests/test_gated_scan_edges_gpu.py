@@ -91,3 +91,28 @@ def test_long_memories_of_constant_log_gates(rate):
     s = slice(0, 64, 9)
     ref, e = go.scan(to_f64(x[0, :, s]), to_f64(g[0, :, s]), "log", None, 2.0 ** -24)
     check(st[0, s], ref[-1], e[-1], F32, "last state")
+
+
+def test_no_gate_undoes_the_cut_between_sequences():
+    """Decays of 0 and -0 behind a sequence's first token; not-a-number in the sequence before stays there."""
+    T, D, cu = 300, 16, [0, 100, 300]
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    for zeros in ([0.0], [-0.0], [-0.0, -0.0], [-0.0, 0.0, -0.0], [-0.0] * 3 + [0.5]):
+        for dtype in (F32, BF):
+            x, dy = rand(1, T, D, seed=1, dtype=dtype), rand(1, T, D, seed=2, dtype=dtype)
+            g = gate_values((1, T, D), "decay", dtype, 3)
+            g[0, 101:101 + len(zeros)] = torch.tensor(zeros, device="cuda")[:, None].to(dtype)
+            g[0, 199:199 + len(zeros)] = torch.tensor(zeros, device="cuda")[:, None].to(dtype)
+            x[0, 5], dy[0, 295] = float("nan"), 0.0
+            y, dx, dg, ck = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), kept(x)
+            lib.gated_scan_forward(x, g, y, gate="decay", cu_seqlens=c, checkpoints=ck)
+            lib.gated_scan_backward(x, g, dy, ck, dx, dg, gate="decay", cu_seqlens=c)
+            assert torch.isnan(y[0, 5:100]).all() and torch.isfinite(y[0, 100:]).all() and torch.isfinite(dg[0, 100:]).all()
+            check_forward(x[:, 100:], g[:, 100:], y[:, 100:], "decay")
+            check_backward(x[:, 100:], g[:, 100:], dy[:, 100:], dx[:, 100:], dg[:, 100:], "decay")
+            # and backwards: not-a-number in the later sequence's gradients
+            x[0, 5], dy[0, 200] = 0.0, float("nan")
+            g[0, 95:95 + len(zeros)] = torch.tensor(zeros, device="cuda")[:, None].to(dtype)[:5]
+            lib.gated_scan_forward(x, g, y, gate="decay", cu_seqlens=c, checkpoints=ck)
+            lib.gated_scan_backward(x, g, dy, ck, dx, dg, gate="decay", cu_seqlens=c)
+            check_backward(x[:, :100], g[:, :100], dy[:, :100], dx[:, :100], dg[:, :100], "decay")

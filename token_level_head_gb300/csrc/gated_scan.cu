@@ -157,7 +157,7 @@ template <typename T, int GATE>
 __device__ __forceinline__ Gate gate_of(float2 g) {
   Gate k;
   if (GATE == GATED_SCAN_DECAY) {
-    k.a = g;
+    k.a = add2(g, both(0.f));  // (-0, which stands for a cut, see kCut, becomes 0)
   } else if (GATE == GATED_SCAN_LOG) {
     k.a = exp_of<T>(g);
   } else {
@@ -251,7 +251,8 @@ __device__ __noinline__ int slot_of(const int* slots, int n_slots, int i) {
 
 // ---- runs of rows, h -> A h + B
 // Packed rows: where a sequence starts (backwards: ends) within a run, nothing of h goes on, not even not-a-number.  Such
-// a run has A = -0, which no product of gates >= 0 gives.
+// a run has A = -0, which no product of gates >= 0 gives, and which any such gate behind it leaves as it is (gates of -0 are
+// taken as 0).
 constexpr float kCut = -0.f;
 template <bool PACKED>
 __device__ __forceinline__ bool is_cut(float A) {
