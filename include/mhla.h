@@ -472,7 +472,8 @@ mhla_status gated_scan_step(const void* x, const mhla_strides* x_strides, const 
  *     padded batch (not with cu_seqlens of the keys), clamped to [0, Nk]: what lies
  *     behind them is not read, not-a-number among it.
  *   - An encoder without tokens gives S = 0, z = 0.  Where phi(q) . z + eps is 0
- *     (eps = 0 and nothing summed) the output is 0, and so are the gradients through it.
+ *     (eps = 0 and nothing summed) or below 2^-120 the output is 0, and so are the
+ *     gradients through it.
  *   - S: [n_slots, Hk, d, d] fp32, z: [n_slots, Hk, d] fp32.
  *   - mhla_options: feature and normalise (gamma = 1); NULL: ELU + 1 with the
  *     normaliser.  MHLA_PHI_IDENTITY goes without one (normalise = 0).

@@ -65,3 +65,22 @@ def test_no_query_head(d, dtype):
         c = Call(2, 0, 2, 150, 150, d, dtype, cu_q=cu, cu_k=cu)
         c.run()
         assert not c.dk.any() and not c.dv.any() and c.S.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_denominators_near_the_least_numbers(d, dtype):
+    """An eps of 1e-40 beside nothing summed, and sums of d e^-91.5 (2.3e-38 for d = 128): a denominator below 2^-120 (7.5e-37)
+    counts as 0; prompts, single queries and gradients have no infinity and no not-a-number."""
+    c = Call(2, 2, 2, 70, 90, d, dtype, eps=1e-40, lens=[0, 90]).run().check()
+    assert not c.y[0].any() and not c.dq[0].any() and not c.dk[0].any()
+    one = torch.full_like(c.y[:, :, :1], 7.0)
+    lib.linattn_cross_read(c.q[:, :, :1], c.S, c.z, one, eps=1e-40)
+    assert not one[0].any() and torch.isfinite(one).all()
+    c = Call(2, 2, 2, 70, 1, d, dtype, "exp", eps=0.0)
+    c.q.fill_(-45.5)
+    c.k.fill_(-46.0)
+    c.run()
+    lib.linattn_cross_read(c.q[:, :, :1], c.S, c.z, one, feature="exp", eps=0.0)
+    for t in (c.y, one, c.dq, c.dk, c.dv):
+        assert not t.any()

@@ -65,7 +65,10 @@ __device__ __forceinline__ long long cross_base(const CrossSide& s, const RetTen
   return (s.cu == nullptr ? (long long)seq * t.sb : 0ll) + (long long)h * t.sh;
 }
 
-// 1 / den: 0 where no token counts (den = 0 with eps = 0 and nothing summed), so that such rows are zeros.
-__device__ __forceinline__ float cross_inverse(float den) { return den == 0.f ? 0.f : 1.f / den; }
+// 1 / den: 0 where no token counts (den = 0 with eps = 0 and nothing summed), so that such rows are zeros.  A den below 2^-120
+// counts as 0 too: the reciprocal of one below 2^-128 is infinite, and zeros times it not a number; and y . dy / den, which the
+// gradients go through, passes the largest number for |y . dy| = 2^8 at 2^-120.
+constexpr float kLeastDen = 0x1p-120f;
+__device__ __forceinline__ float cross_inverse(float den) { return fabsf(den) < kLeastDen ? 0.f : 1.f / den; }
 
 }  // namespace mhla

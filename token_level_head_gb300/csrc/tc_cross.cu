@@ -148,7 +148,7 @@ __device__ __forceinline__ float exp2_of(float x) {
 __device__ __forceinline__ float inverse(float den) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den));
-  return den == 0.f ? 0.f : r;
+  return fabsf(den) < kLeastDen ? 0.f : r;
 }
 __device__ __forceinline__ float min_nan(float a, float b) {  // not-a-number stays
   float r;
