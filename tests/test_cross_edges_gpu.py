@@ -84,3 +84,23 @@ def test_denominators_near_the_least_numbers(d, dtype):
     lib.linattn_cross_read(c.q[:, :, :1], c.S, c.z, one, feature="exp", eps=0.0)
     for t in (c.y, one, c.dq, c.dk, c.dv):
         assert not t.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_large_denominators(d, dtype):
+    """exp features whose denominators are about 10^20, 10^33 and just below the largest number, 1 / den among the numbers below the
+    normal ones: one key, so that y is its value (up to the rounding of phi(q) in numerator and denominator alike, and 2^-20
+    for the steps of 1 / den, 2^-149 wide at 2^-127)."""
+    for shift in (22.0, 37.0, 41.5 + 0.5 * (d == 64) + 0.75 * (d == 16)):
+        c = Call(2, 2, 2, 150, 1, d, dtype, "exp")
+        c.q.fill_(shift)
+        c.k.fill_(41.5 if shift > 40 else shift)
+        c.v.uniform_(-1.0, 1.0, generator=torch.Generator(device="cuda").manual_seed(5))
+        c.run()
+        want = c.v.float().expand_as(c.y)
+        assert ((c.y.float() - want).abs() <= (2.0 ** -7 if dtype == BF else 2.0 ** -18) * want.abs()).all(), shift
+    c = Call(1, 2, 2, 150, 200, d, dtype, "exp")
+    c.q += 22
+    c.k += 22
+    c.run().check()

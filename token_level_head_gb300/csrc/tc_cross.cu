@@ -144,10 +144,11 @@ __device__ __forceinline__ float exp2_of(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
   return e;
 }
-// cross_inverse by the hardware's reciprocal (within a step of 2^-23).
+// cross_inverse by the hardware's reciprocal (within a step of 2^-23; not flushed: that of a den from 2^126 on is below the normal
+// numbers, and y is not 0 there).
 __device__ __forceinline__ float inverse(float den) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(den));
   return fabsf(den) < kLeastDen ? 0.f : r;
 }
 __device__ __forceinline__ float min_nan(float a, float b) {  // not-a-number stays
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
     if (p.c.normalise && live) {
 #pragma unroll
       for (int i = 0; i < X::kCols; ++i) dd += den[i * kT + row];
-      dd *= -inv * inv;
+      dd = -(dd * inv) * inv;  // (inv^2 alone is 0 for a den of 2^75 and above, inf for one of 2^-64)
       if (p.c.eps * inv > 0x1p-26f) {  // (m . dy) eps / den^2, no less than a rounding of u' / den
         float s1 = 0.f;
         for (int i = 0; i < D / 8; ++i) {
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
 #pragma unroll
           for (int x = 0; x < 4; ++x) s1 = fmaf(a[x].x, e[x].x, fmaf(a[x].y, e[x].y, s1));
         }
-        dd = fmaf(s1, p.c.eps * inv * inv, dd);
+        dd = fmaf(s1 * (p.c.eps * inv), inv, dd);
       }
     }
     ok = row_and(wait(&b->mma2, j & 1, b), warp, X::kWork / 4);  // w has been read; and the row's sums
