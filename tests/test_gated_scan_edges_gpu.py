@@ -116,3 +116,74 @@ def test_no_gate_undoes_the_cut_between_sequences():
             lib.gated_scan_forward(x, g, y, gate="decay", cu_seqlens=c, checkpoints=ck)
             lib.gated_scan_backward(x, g, dy, ck, dx, dg, gate="decay", cu_seqlens=c)
             check_backward(x[:, :100], g[:, :100], dy[:, :100], dx[:, :100], dg[:, :100], "decay")
+
+
+def owners(slots, n):
+    """For each sequence its slot, -1 where that is out of the pool or a sequence before it has it."""
+    seen, out = set(), []
+    for s in slots:
+        out.append(s if 0 <= s < n and s not in seen else -1)
+        seen.add(s)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("length,D", [(1, 64), (5, 192), (16, 1024), (1, 16)])
+def test_thousands_of_packed_sequences_on_a_pool(length, D, dtype):
+    """Slots of 3000 short sequences, some twice, some out of the pool, some with no token: states in and out."""
+    B, pool_rows = 3000, 3500
+    gen = torch.Generator().manual_seed(1)
+    slots = torch.randperm(pool_rows + 200, generator=gen)[:B] - 100
+    again = torch.randint(0, B, (300,), generator=gen)
+    slots[again] = slots[torch.randint(0, B, (300,), generator=gen)]
+    lens = torch.full((B,), length)
+    lens[::7] = torch.randint(0, 2 * length + 1, (len(lens[::7]),), generator=gen)
+    cu = torch.nn.functional.pad(torch.cumsum(lens, 0), (1, 0))
+    T = int(cu[-1])
+    x, g = rand(1, T, D, seed=1, dtype=dtype), gate_values((1, T, D), "sigmoid", dtype, 2)
+    pool = rand(pool_rows, D, seed=3)
+    was, y = pool.clone(), torch.empty_like(x)
+    lib.gated_scan_forward(x, g, y, cu_seqlens=cu.int().cuda(), states=pool, slots=slots.int().cuda(), load_state=True)
+    own = owners(slots.tolist(), pool_rows)
+    start = torch.zeros(B, D, device="cuda")
+    has = torch.tensor([s >= 0 for s in own]).cuda()
+    start[has] = was[torch.tensor([s for s in own if s >= 0]).cuda()]
+    alone, y2 = start.clone(), torch.empty_like(x)
+    lib.gated_scan_forward(x, g, y2, cu_seqlens=cu.int().cuda(), states=alone, load_state=True)   # sequence i on slot i
+    assert torch.equal(y, y2)
+    want = was.clone()
+    want[torch.tensor([s for s in own if s >= 0]).cuda()] = alone[has]
+    assert torch.equal(pool, want)
+    some = slice(0, 200)
+    check_forward(x[:, :int(cu[200])], g[:, :int(cu[200])], y[:, :int(cu[200])], "sigmoid", cu[:201].tolist(), start=start[some],
+                  final=alone[some], channels=8)
+
+
+def us(fn, n=20):
+    for _ in range(3):
+        fn()
+    best = 1e9
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(n):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / n)
+    return best
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_the_search_for_slots_costs_little(packed):
+    """Slots given or not: 4096 packed sequences of 16 tokens, and a dense batch of 1024 rows."""
+    B, N, D = (1, 65536, 256) if packed else (1024, 64, 256)
+    n = 4096 if packed else B
+    x, g = rand(B, N, D, seed=1, dtype=BF), gate_values((B, N, D), "sigmoid", BF, 2)
+    y, pool = torch.empty_like(x), rand(n, D, seed=3)
+    kw = dict(cu_seqlens=torch.arange(0, N + 1, 16, dtype=torch.int32, device="cuda")) if packed else {}
+    slots = torch.randperm(n, generator=torch.Generator().manual_seed(4)).int().cuda()
+    without = us(lambda: lib.gated_scan_forward(x, g, y, states=pool, load_state=True, **kw))
+    given = us(lambda: lib.gated_scan_forward(x, g, y, states=pool, slots=slots, load_state=True, **kw))
+    print(f"{'packed' if packed else 'dense'}: {without:.1f} us without slots, {given:.1f} with")
+    assert given <= 2 * without + 10, (given, without)

@@ -179,10 +179,19 @@ struct Marks {
   unsigned live, first, last;  // bit r: row r of the thread
 };
 __device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // the kThreads of the tiles
+__device__ __forceinline__ bool tile_sync_or(bool any) {  // and whether one of them has `any`
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((unsigned)any)
+      : "memory");
+  return r != 0;
+}
 static_assert(kThreads == 256, "the barrier's count");
 
 // Packed sequences: bits of the tile's rows row0 .., a word for the kR rows of a thread, and the sequences of the rows that
-// have one (a row that begins one and ends one is the same's).  Sets by the tile, as a later tile's are made while the state
+// have one (a row that begins one and ends one is the same's; find_slots makes slots of them).  Sets by the tile, as a later tile's are made while the state
 // that enters this one is on its way.  Offsets outside [0, N] are clamped; out of order they mark rows of the tile all the
 // same and nothing else.
 template <int GROUPS, int ROWS>
@@ -198,9 +207,11 @@ __device__ __forceinline__ void clear_marks(MarkRows<GROUPS, ROWS>& m) {
   for (int i = threadIdx.x; i < GROUPS; i += kThreads) m.first[i] = m.last[i] = 0;
   for (int i = threadIdx.x; i < ROWS; i += kThreads) m.seq[i] = 0;
 }
+// (Whether the thread has set one.)
 template <int GROUPS, int ROWS>
-__device__ __forceinline__ void set_marks(const ScanArgs& p, int row0, MarkRows<GROUPS, ROWS>& m) {
+__device__ __forceinline__ bool set_marks(const ScanArgs& p, int row0, MarkRows<GROUPS, ROWS>& m) {
   constexpr int kR = ROWS / GROUPS;
+  bool any = false;
   for (int i = threadIdx.x; i < p.B; i += kThreads) {
     const int lo = min(max(p.cu[i], 0), p.N), hi = min(max(p.cu[i + 1], lo), p.N);
     if (lo == hi) continue;
@@ -208,12 +219,89 @@ __device__ __forceinline__ void set_marks(const ScanArgs& p, int row0, MarkRows<
     if (f >= 0 && f < ROWS) {
       atomicOr(&m.first[f / kR], 1u << f % kR);
       atomicMax(&m.seq[f], i);
+      any = true;
     }
     if (l >= 0 && l < ROWS) {
       atomicOr(&m.last[l / kR], 1u << l % kR);
       atomicMax(&m.seq[l], i);
+      any = true;
     }
   }
+  return any;
+}
+
+// The slots of packed sequences, -1 for none: out of range, or the slot of a sequence before.  The slots of the sequences that
+// begin or end in the tile go into a table (open addressing, half full at most); one pass over the slots up to the tile's last
+// sequence, shared by the tiles' threads as set_marks's pass over the offsets is, then finds the first sequence with each.  (With every thread looking through
+// the slots before its own sequences': 65,536 x 256 bf16 as 4096 sequences 4239 us, so 175, without slots 143; a dense
+// batch of 1024 x 64 rows, where a block looks once, 793, so 68.)
+template <int ROWS>
+struct SlotTable {
+  int key[2 * ROWS], first[2 * ROWS];  // a slot (-1: free), the first sequence with it
+  int end;                             // behind the last sequence of the tile
+};
+template <>
+struct SlotTable<0> {};  // dense
+// m.seq becomes the slots.  (The tiles' threads, behind set_marks, with a barrier of theirs since the call before; `any`: what
+// set_marks gave.)
+template <int GROUPS, int ROWS>
+__device__ __noinline__ void find_slots(const int* slots, int n_slots, bool any, MarkRows<GROUPS, ROWS>& m,
+                                        SlotTable<ROWS>& t) {
+  constexpr int kR = ROWS / GROUPS, SIZE = 2 * ROWS;
+  static_assert(ROWS <= kThreads && (SIZE & (SIZE - 1)) == 0, "a thread a row, a table of a power of two");
+  const auto place = [](int s) { return (int)((unsigned)s * 2654435769u >> 16) % SIZE; };  // (2^32 over the golden ratio)
+  for (int i = threadIdx.x; i < SIZE; i += kThreads) {
+    t.key[i] = -1;
+    t.first[i] = 0x7fffffff;
+  }
+  if (threadIdx.x == 0) t.end = 0;
+  if (!tile_sync_or(any)) return;
+  const int r = threadIdx.x;
+  int seq = -1, slot = -1, at = 0;
+  if (r < ROWS && ((m.first[r / kR] | m.last[r / kR]) >> r % kR & 1u)) {
+    seq = m.seq[r];
+    slot = slots[seq];
+    atomicMax(&t.end, seq + 1);
+    if (slot >= n_slots || slot < 0) slot = -1;
+    if (slot >= 0)
+      for (at = place(slot);; at = (at + 1) % SIZE) {
+        const int was = atomicCAS(&t.key[at], -1, slot);
+        if (was == -1 || was == slot) break;
+      }
+  }
+  tile_sync();
+  constexpr int U = 4;  // loads in flight
+  const int end = t.end;
+  for (int i0 = threadIdx.x; i0 < end; i0 += U * kThreads) {
+    int s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] = i0 + u * kThreads < end ? slots[i0 + u * kThreads] : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s[u] < 0) continue;
+      for (int a = place(s[u]); t.key[a] != -1; a = (a + 1) % SIZE)
+        if (t.key[a] == s[u]) {
+          atomicMin(&t.first[a], i0 + u * kThreads);
+          break;
+        }
+    }
+  }
+  tile_sync();
+  if (seq >= 0) m.seq[r] = slot >= 0 && t.first[at] == seq ? slot : -1;
+}
+// (A call, as it is rare: in the rows' loops its code would stand sixteen times over.)
+__device__ __noinline__ int slot_at(const int* place, bool given, int n_slots) {
+  const int s = *place;
+  return given || s < n_slots ? s : -1;
+}
+// The slot of dense sequence i, as above (all of the tiles' threads).
+__device__ __forceinline__ int find_slot(const int* slots, int n_slots, int i) {
+  if (slots == nullptr) return i < n_slots ? i : -1;
+  const int s = slots[i];
+  bool taken = false;
+#pragma unroll 4
+  for (int j = threadIdx.x; j < i; j += kThreads) taken |= slots[j] == s;
+  return tile_sync_or(taken) || s < 0 || s >= n_slots ? -1 : s;
 }
 // The thread's kR rows from `row` on; rows in [lo, hi) are tokens.
 template <int kR>
@@ -237,16 +325,6 @@ __device__ __forceinline__ Marks packed_marks(const MarkRows<GROUPS, ROWS>& m, i
   k.first = m.first[group] & k.live;
   k.last = m.last[group] & k.live;
   return k;
-}
-
-// The slot of sequence i, -1 for none: out of range, or the slot of a sequence before it (one thread).
-__device__ __noinline__ int slot_of(const int* slots, int n_slots, int i) {
-  if (slots == nullptr) return i < n_slots ? i : -1;
-  const int s = slots[i];
-  if (s < 0 || s >= n_slots) return -1;
-  for (int j = 0; j < i; ++j)
-    if (slots[j] == s) return -1;
-  return s;
 }
 
 // ---- runs of rows, h -> A h + B
@@ -519,6 +597,8 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   constexpr int kR = St::kR, CW = St::CW, ROWS = St::ROWS, GROUPS = 32 / LW;
   __shared__ __align__(16) ScanShared<T, LW> s;
   __shared__ MarkRows<PACKED ? ROWS / kR : 0, PACKED ? ROWS : 0> marks[3];
+  __shared__ SlotTable<PACKED ? ROWS : 0> table;
+  __shared__ int dense_slot;
   launch_dependents();
   grid_dependency_wait();  // (every kernel here is launched while the one before it in the stream drains)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -543,7 +623,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one reads its shared memory
     return;
   }
-  extern __shared__ __align__(16) uint8_t raw[];
+  extern __shared__ __align__(128) uint8_t raw[];  // (16 bytes off a multiple of 128: 65,536 x 1024 105 us instead of 79)
   T* stage = reinterpret_cast<T*>(raw);  // [3][x, g]
   const int rounds = ret_pieces(tiles, cluster);
   const auto fetch = [&](int i) {  // the block's tile of round i
@@ -567,14 +647,14 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
       b[i] = input_of<GATE>(xv[i], k.rest);
     }
   };
-  // The sequence that row r of the thread's in the tile of round i begins or ends, and the start of it.
-  const auto sequence_of = [&](int i, int r) {
-    if constexpr (PACKED) return marks[i % 3].seq[r0 + r];
-    return batch;
+  // The slot of the sequence that row r of the thread's in the tile of round i begins or ends, and the start of it.
+  const auto slot_of = [&](int i, int r) {
+    if constexpr (PACKED) return slot_at(&marks[i % 3].seq[r0 + r], p.slots != nullptr, p.n_slots);
+    return slot_at(&dense_slot, true, 0);
   };
   const auto start_of = [&](int i, int r, float2 (&h)[P]) {
     fill(h, 0.f);
-    const int slot = slot_of(p.slots, p.n_slots, sequence_of(i, r));
+    const int slot = slot_of(i, r);
     if (slot >= 0) load_f(p.states + (long long)slot * p.D + c, h);
   };
   // What is known of a tile before the state that enters it.
@@ -638,12 +718,22 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
   fetch(0);
   fetch(1);
   Ahead next;
+  const auto mark = [&](int i) {
+    if constexpr (PACKED) {
+      const bool any = set_marks(p, row0_of(i), marks[i % 3]);
+      if (p.slots != nullptr) find_slots(p.slots, p.n_slots, any, marks[i % 3], table);
+    }
+  };
   if constexpr (PACKED) {
     clear_marks(marks[0]);
     clear_marks(marks[1]);
     tile_sync();
-    set_marks(p, row0_of(0), marks[0]);
-    set_marks(p, row0_of(1), marks[1]);
+    mark(0);
+    tile_sync();
+    mark(1);
+  } else if (p.states != nullptr && (rank == 0 || rank == (tiles - 1) % cluster)) {  // the sequence begins or ends here
+    const int slot = find_slot(p.slots, p.n_slots, batch);
+    if (tid == 0) dense_slot = slot;
   }
   copies_wait1();
   tile_sync();
@@ -664,7 +754,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
     if constexpr (PACKED) {
       if (i + 2 < rounds) {
         tile_sync();
-        set_marks(p, row0_of(i + 2), marks[(i + 2) % 3]);
+        mark(i + 2);
       }
     }
     carry_sync(par);
@@ -704,7 +794,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_forward_kernel(const __g
         py += p.y.sn;
         if constexpr (!plain) {
           if (ends >> r & 1) {
-            const int slot = slot_of(p.slots, p.n_slots, sequence_of(i, r));
+            const int slot = slot_of(i, r);
             if (slot >= 0) store(p.states + (long long)slot * p.D + c, h);
           }
         }
@@ -767,7 +857,7 @@ __global__ void __launch_bounds__(kBlock, 2) gated_scan_backward_kernel(const __
     if (cluster > 1) cg::this_cluster().sync();  // no block ends while another one reads its shared memory
     return;
   }
-  extern __shared__ __align__(16) uint8_t raw[];
+  extern __shared__ __align__(128) uint8_t raw[];
   T* stage = reinterpret_cast<T*>(raw);  // [2][x, g, dy]
   const auto fetch = [&](int t, int buf) {
     T* to = stage + buf * 3 * St::ELEMS;
