@@ -118,6 +118,39 @@ def test_no_gate_undoes_the_cut_between_sequences():
             check_backward(x[:, :100], g[:, :100], dy[:, :100], dx[:, :100], dg[:, :100], "decay")
 
 
+def long_gates(shape, gate, dtype, seed):
+    """Memories of some thousands of tokens: logits from 8 to 11, and every eighth channel 20 (a sequence's start stays to its end)."""
+    t = 8 + 3 * torch.rand(*shape, generator=torch.Generator().manual_seed(seed))
+    t[..., ::8] = 20.0
+    t = {"sigmoid": t, "log": -torch.exp(-t), "decay": torch.exp(-torch.exp(-t))}[gate]
+    return t.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("B,D,cu", [(1, 64, None), (2, 640, None), (15, 64, None), (23, 64, None), (80, 64, None),
+                                    (1, 64, [0, 2000, 9001]), (1, 1024, [0, 1, 4500, 9001]), (1, 2048, [3, 8000, 8000, 9001])], ids=str)
+def test_long_memories_across_tiles_and_clusters(B, D, cu, gate, dtype):
+    """States and gradients that reach over tiles, warps, the blocks of a cluster and its rounds, from starts and ends that are not
+    zero: they make up a visible part of the last state, of dh0 and of every row between."""
+    N = 9001 if cu else 4500
+    n = len(cu) - 1 if cu else B
+    x, dy, g = rand(B, N, D, seed=1, dtype=dtype), rand(B, N, D, seed=2, dtype=dtype), long_gates((B, N, D), gate, dtype, 3)
+    h0, dl = 100 * rand(n, D, seed=4), 100 * rand(n, D, seed=5)
+    if gate == "sigmoid":
+        x = x * 3 + 2
+    y, dx, dg, st, dh0, ck = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), h0.clone(), torch.empty_like(h0), kept(x)
+    kw = dict(gate=gate, cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    lib.gated_scan_forward(x, g, y, states=st, load_state=True, checkpoints=ck, **kw)
+    lib.gated_scan_backward(x, g, dy, ck, dx, dg, h0=h0, dh_last=dl, dh0=dh0, **kw)
+    for s in (slice(0, 10), slice(D - 6, D)):
+        rows = slice(max(0, B - 2), B)
+        part = [t[rows, :, s] for t in (x, g, y, dy, dx, dg)]
+        ends = [t[slice(max(0, n - 2), n) if cu is None else slice(None), s] for t in (h0, st, dl, dh0)]
+        check_forward(*part[:3], gate, cu, start=ends[0], final=ends[1])
+        check_backward(part[0], part[1], *part[3:], gate, cu, ends[0], ends[2], ends[3])
+
+
 def owners(slots, n):
     """For each sequence its slot, -1 where that is out of the pool or a sequence before it has it."""
     seen, out = set(), []
