@@ -404,7 +404,8 @@ mhla_status retention_copy_states(float* states, int n_slots, int H, int d, cons
  *     0 in b.  Outputs overlap neither inputs nor each other nor themselves.
  *   - cu_seqlens as there: NULL, or device int32 [B + 1] with tensors [1, N, D].
  *     Rows of no sequence are not written.
- *   - At most 2^31 - 1024 tokens a sequence (packed: a call): MHLA_ERR_UNSUPPORTED.
+ *   - At most 2^31 - 1024 tokens a sequence (packed: a call) and as many channels:
+ *     MHLA_ERR_UNSUPPORTED.
  *   - states: [n_slots, D] fp32, slots as there: a sequence whose slot is outside
  *     [0, n_slots), or is the slot of a sequence before it, has none.
  *   - h, the gradients and every sum are fp32.  Sums have a fixed order: equal

@@ -14,6 +14,8 @@ constexpr int kScanKept = 64;
 
 // Tokens of a sequence (packed: of a call) at most: a row of a tile that ends behind them has an int of its own.
 constexpr long long kScanMaxTokens = (1ll << 31) - 1024;
+// Channels at most: a block's last channel, in the row or behind it, has an int of its own.
+constexpr int kScanMaxChannels = (int)((1ll << 31) - 1024);
 
 struct ScanArgs {
   RetTensor x, g, y;            // [B, 1, N, D] (sh unused)

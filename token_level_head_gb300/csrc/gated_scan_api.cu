@@ -21,7 +21,7 @@ mhla_status sizes_of(Sizes* s, int B, int N, int D, const int* cu, mhla_dtype dt
   const int es = dt == MHLA_F32 ? 4 : 2;
   if (D % (16 / es) != 0 || !aligned(cu, 4)) return MHLA_ERR_INVALID_ARG;
   *empty = B == 0 || N == 0 || D == 0;
-  if (N > kScanMaxTokens) return MHLA_ERR_UNSUPPORTED;
+  if (N > kScanMaxTokens || D > kScanMaxChannels) return MHLA_ERR_UNSUPPORTED;
   if ((Wide)B * D * 4 > kNoMemory) return MHLA_ERR_INVALID_ARG;
   if ((long long)B * ((D + 31) / 32) > 0x7fffffffll / 16) return MHLA_ERR_UNSUPPORTED;  // the blocks are numbered
   s->e = {cu ? 1 : B, 1, N, D, es};
