@@ -104,3 +104,20 @@ def test_large_denominators(d, dtype):
     c.q += 22
     c.k += 22
     c.run().check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("feature,normalise", [("elu1", True), ("exp", True), ("elu1", False)])
+def test_dk_is_off_by_its_own_rounding(feature, normalise, d):
+    """bf16 calls: dk = phi'(k) (dS v + dz) takes k and v as they are; dS, the w that it is summed from and S less z m^T, which dz
+    goes through, are sums of two bf16 numbers, each off by 2^-17 of its terms.  Where those are some ten times dk, that adds
+    (10 x 3 x 2^-17 / 2^-9)^2 < 1.5 % to the mean square of dk's own rounding; a phi' that is rounded itself would add half of it
+    (ELU + 1, whose phi' is 1 for half of the keys: a fifth)."""
+    c = Call(2, 4, 2, 700, 900, d, BF, feature, normalise).run()
+    off = own = 0.0
+    for i in range(2):
+        q, dy, k, v = (to_f64(t[i]) for t in (c.q, c.dy, c.k, c.v))
+        dk = co.backward(q, k, v, dy, feature, normalise, c.eps)[1]
+        off += ((to_f64(c.dk[i]) - dk) ** 2).sum()
+        own += ((to_f64(torch.from_numpy(dk).to(BF)) - dk) ** 2).sum()
+    assert off <= 1.03 * own, off / own
