@@ -220,3 +220,17 @@ def test_the_search_for_slots_costs_little(packed):
     given = us(lambda: lib.gated_scan_forward(x, g, y, states=pool, slots=slots, load_state=True, **kw))
     print(f"{'packed' if packed else 'dense'}: {without:.1f} us without slots, {given:.1f} with")
     assert given <= 2 * without + 10, (given, without)
+
+
+def test_offsets_that_break_their_contract_on_a_pool():
+    """Out of range and out of order, with slots, some twice and some out of the pool: nothing beside the tensors and the pool is touched."""
+    T, D = 600, 64
+    big, pools = torch.full((T + 200, D), 7.0, device="cuda"), torch.full((20, D), 5.0, device="cuda")
+    x, g = rand(1, T, D, seed=1), gate_values((1, T, D), "sigmoid", F32, 2)
+    for cu in ([-5, 100, 900, 250, 10 ** 9], [500, 200, 100, 50, 400, 0], [10 ** 9, 10 ** 9 + 5, 3], [-(10 ** 9), -5, 5, 4, 3, 599]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        slots = torch.tensor([2, 3, 2, -(1 << 31), (1 << 31) - 1][:len(cu) - 1], dtype=torch.int32, device="cuda")
+        lib.gated_scan_forward(x, g, big[100:100 + T][None], cu_seqlens=c, states=pools[8:12], slots=slots, load_state=True)
+        assert (big[:100] == 7).all() and (big[100 + T:] == 7).all() and (pools[:8] == 5).all() and (pools[12:] == 5).all()
+        big.fill_(7.0)
+        pools.fill_(5.0)
