@@ -409,7 +409,9 @@ mhla_status retention_copy_states(float* states, int n_slots, int H, int d, cons
  *   - states: [n_slots, D] fp32, slots as there: a sequence whose slot is outside
  *     [0, n_slots), or is the slot of a sequence before it, has none.
  *   - h, the gradients and every sum are fp32.  Sums have a fixed order: equal
- *     calls give equal bits.  No workspace and no device-side wait.
+ *     calls give equal bits.  No workspace and no device-side wait.  Gates are fp32
+ *     numbers; sigmoid(g), 1 - sigmoid(g) and exp(g) are each within 2^-21 of themselves
+ *     (bf16 tensors: and 2^-23 |g|).
  *   - Not-a-number or infinite values of a token reach later tokens (backward:
  *     earlier ones too) of its own sequence and channel only. */
 typedef enum { GATED_SCAN_SIGMOID = 0, GATED_SCAN_LOG = 1, GATED_SCAN_DECAY = 2 } gated_scan_gate;
@@ -482,7 +484,13 @@ mhla_status gated_scan_step(const void* x, const mhla_strides* x_strides, const 
  *     sequence only (a query's: its own outputs, and backward dk and dv of its sequence).
  *   - Every sum has a fixed order: equal calls give equal bits.
  *   - bf16 with d = 64 or 128 runs on the tensor cores, everything else on the FP32
- *     units. */
+ *     units.  There bf16 operands stand for 32-bit ones: phi(q) of a read (numerator
+ *     and denominator alike) and phi(k) of dv are rounded once (2^-8 at most; ReLU
+ *     and the identity not at all), S, dS and phi(q) / den are sums of two bf16
+ *     numbers (2^-17), phi(k) of S one of three (2^-24); exponentials and 1 / den are
+ *     within 2^-22.  All sums are fp32, of which the tensor cores cut each by at most
+ *     2^-23 (S of 65,536 tokens is off by 8e-7 of its terms).  Everything else is fp32
+ *     arithmetic. */
 
 /* Workspace bytes of linattn_cross_states and linattn_cross_read (backward = 0) or
  * of linattn_cross_backward (backward = 1; enough for the others too) for B

@@ -12,7 +12,7 @@
 // (A, B) through distributed shared memory, and a cluster walks along the sequence.  So x and g are read once and no memory,
 // flag or wait is shared between clusters.
 // Measured, whole calls: 65,536 x 1024 bf16, log, 79 us (5.1 TB/s); 77 x 1024 bf16 8; forward and backward of 4 x 8192 x 1024
-// bf16, sigmoid, 126 (4.3 TB/s), of 20,011 packed x 384 fp32, decay, 73 (3.4 TB/s); the step of 256 x 8192 bf16 8.
+// bf16, sigmoid, 126 (4.3 TB/s), of 20,011 packed x 384 fp32, decay, 74 (3.3 TB/s); the step of 256 x 8192 bf16 8.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -150,9 +150,9 @@ struct Gate {
   float2 rest;  // sigmoid: 1 - a, the factor of x
 };
 // sigmoid, with e = exp(g): 1 - a = 1 / (1 + e), which needs no case for either end.  a = e / (1 + e) below 2/3, so that a small
-// gate has all its digits (what fades is off by 2^-21 of itself, bf16 and by |g| 2^-23, not of x; a = 1 - (1 - a) throughout had 5e-4 at g = -10 and
-// zero from -17 on); from there 1 - (1 - a), so that gates near 1 are rounded once (a long memory multiplies thousands of them,
-// and their errors).  Not-a-number stays.
+// gate has all its digits (what fades is off by 2^-21 of itself, bf16 and by |g| 2^-23; a = 1 - (1 - a) throughout was off by
+// 5e-4 at g = -10 and zero from -17 on); from there 1 - (1 - a), so that gates near 1 are rounded once (a long memory
+// multiplies thousands of them, and their errors).  Not-a-number stays.
 template <typename T, int GATE>
 __device__ __forceinline__ Gate gate_of(float2 g) {
   Gate k;
@@ -232,9 +232,9 @@ __device__ __forceinline__ bool set_marks(const ScanArgs& p, int row0, MarkRows<
 
 // The slots of packed sequences, -1 for none: out of range, or the slot of a sequence before.  The slots of the sequences that
 // begin or end in the tile go into a table (open addressing, half full at most); one pass over the slots up to the tile's last
-// sequence, shared by the tiles' threads as set_marks's pass over the offsets is, then finds the first sequence with each.  (With every thread looking through
-// the slots before its own sequences': 65,536 x 256 bf16 as 4096 sequences 4239 us, so 175, without slots 143; a dense
-// batch of 1024 x 64 rows, where a block looks once, 793, so 68.)
+// sequence, shared by the tiles' threads as set_marks's pass over the offsets is, then finds the first sequence with each.
+// (With every thread looking through the slots before its own sequences': 65,536 x 256 bf16 as 4096 sequences 4239 us, so 175,
+// without slots 143; a dense batch of 1024 x 64 rows, where a block looks once, 793, so 68.)
 template <int ROWS>
 struct SlotTable {
   int key[2 * ROWS], first[2 * ROWS];  // a slot (-1: free), the first sequence with it

@@ -15,8 +15,8 @@
 // as its rows end within it).  Two blocks an SM for d = 64 (reads: three), one for d = 128, hide one another's waits.  Every
 // wait is bounded (on time-out the block stops, sets the status word and drains what it has in flight).
 // Measured in a graph: states and read of 8 x 6 heads, 4096 queries, 77 keys, d 64: 18 us; of 4 key heads of 65,536 keys, d 128,
-// and 777 queries of 16 heads: 45 (3.1 TB/s); forward and gradients of 8 x 6 heads, 4096 queries, 2048 keys, d 64: 73 (2.8
-// TB/s), of 8 x 8 heads, d 128: 216 (2.5 TB/s).
+// and 777 queries of 16 heads: 45 (3.1 TB/s); forward and gradients of 8 x 6 heads, 4096 queries, 2048 keys, d 64: 76 (2.7
+// TB/s), of 8 x 8 heads, d 128: 227 (2.4 TB/s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -947,8 +947,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_que
 }
 
 // ================================================================ backward over the keys
-// 8 x 6 heads of 2048 keys, d = 64: about 11 us (50 MB); 8 x 8 heads, d = 128: about 36 (134 MB), where two buffers wait for
-// one another's copies in and out.
+// 8 x 6 heads of 2048 keys, d = 64: about 14 us (50 MB); 8 x 8 heads, d = 128: about 48 (134 MB), where two buffers wait for
+// one another's copies in and out.  phi(k) is one bf16 number for dv (off by 2^-9 of each term in the mean, of 64 or 128 of them;
+// dv by 1.69e-3 where its own rounding makes 1.66e-3), as a second part would take the third buffer's room; dS is two.
 // Two accumulators: while the MMAs of a tile run the warps put the results of the one before into its place, whence they are
 // copied out; three buffers, two for d = 128.
 template <int D>
@@ -1092,8 +1093,9 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, D == 64 ? 2 : 1) tc_cross_key
   for (int j = 0; ok && j < tiles; ++j) {
     if (j + 1 < tiles && !features(j + 1)) break;
     const bool live = row < g.len - j * kT;  // (dense: zeros behind the tokens)
-    uint4 own[4];  // k once more, where phi' is an exponential: by phi as it lies there, rounded to bf16, dk would be off by twice
-                   // its own rounding (ELU + 1, 8 x 6 heads of 2048 keys: by 1.83e-3 in the mean instead of 1.66e-3; the gradients 2.5 us less)
+    // k once more, where phi' is an exponential: by phi as it lies there, rounded to bf16, dk would be off by a second rounding
+    // (ELU + 1, 8 x 6 heads of 2048 keys: by 1.83e-3 in the mean, so by 1.66e-3, its own; 3 us, 8 x 8 heads of d 128 12 us)
+    uint4 own[4];
     if (kExpSlope && live)
 #pragma unroll
       for (int i = 0; i < 4; ++i) own[i] = reinterpret_cast<const uint4*>(keys + (long long)j * kT * p.c.k.sn)[i];
